@@ -580,10 +580,10 @@ class _Cache:
             a, b = -(-old // self.page), -(-(old + add) // self.page)
             if old % self.page and self.refs[self.table[seq, a - 1]] > 1:
                 need += 1
+                p = self.table[seq, a - 1]
+                self.refs[p] -= 1
                 if at < len(spare):
-                    p = self.table[seq, a - 1]
                     copies.append([p, spare[at], old % self.page, 0])
-                    self.refs[p] -= 1
                     self.refs[spare[at]] = 1
                     self.table[seq, a - 1] = spare[at]
                 at += 1
