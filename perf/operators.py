@@ -295,7 +295,7 @@ def prepare(case, seed):
         s["tables"] = db.PageTables(s["table"], s["length"], s["refs"], s["free"], s["page"])
         s["ws"] = db.workspace(db.page_workspace_size(s["table"].shape[0], s["refs"].shape[0]))
         if s["op"] == "compact":
-            s["tables_out"] = db.PageTables(s["table_out"], s["length"], s["refs_out"], s["free_out"], s["page"])
+            s["after"] = db.PageTables(s["table_out"], s["length"], s["refs_out"], s["free_out"], s["page"])
     return s
 
 
@@ -483,7 +483,7 @@ def run(s):
                 db.page_fork(t, s["fork"], ws, status=s["fork_status"], ctr=s["fork_ctr"])
             db.page_extend(t, s["grow"], s["list"], s["count"], ws, status=s["grow_status"], ctr=s["grow_ctr"])
         elif op == "compact":
-            db.page_compact(s["tables"], s["tables_out"], s["list"], s["count"], s["ws"], ctr=s["move_ctr"])
+            db.page_compact(s["tables"], s["after"], s["list"], s["count"], s["ws"], ctr=s["move_ctr"])
         if "dst" in s:
             db.page_copy(s["list"], s["count"], s["src"], s["dst"], s["token_dim"])
         return _answer(s)
