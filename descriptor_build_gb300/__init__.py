@@ -14,6 +14,11 @@ Record layouts (all tensors contiguous, on the GPU):
   put          16 B  {u64 off; u32 bytes; u16 pe; u16 qp} -> int64 [n, 2]
   WQE          64 B                                    -> uint8 [rings, depth, 64]
   counters     32 B  {total, n_invalid, n_overflow, err} -> int64 [4]
+Records of the paged cache (include/pagecache.h), u32 fields as int32 bits:
+  cut           8 B  {seq, keep}                       -> int32 [n, 2]
+  grow          8 B  {seq, tokens}                     -> int32 [n, 2]
+  fork         16 B  {parent, child, tokens, rsvd}     -> int32 [n, 4]
+  move         16 B  {src, dst, tokens, rsvd}          -> int32 [n, 4]
 """
 
 from __future__ import annotations
@@ -41,6 +46,9 @@ __all__ = [
     "PRP_OK", "PRP_INVALID", "PRP_OVERFLOW", "MR_MISS", "MR_EXACT", "MR_CONTAINED",
     "MR_INVALID", "ERR_TIMEOUT", "ERR_RING_OVERFLOW", "ERR_TABLE_ORDER", "PRP_ZERO_TAIL",
     "PRP_SCHED_SINGLE", "PRP_SCHED_SPLIT",
+    "PageTables", "page_workspace_size", "page_extend", "page_fork", "page_free", "page_compact",
+    "page_copy", "PAGE_NONE", "PAGE_ALL", "PAGE_OK", "PAGE_INVALID", "PAGE_SHORT",
+    "ERR_PAGE_TABLE",
 ]
 
 PRP_OK, PRP_INVALID, PRP_OVERFLOW = 0, 1, 2
@@ -49,6 +57,9 @@ ERR_TIMEOUT, ERR_RING_OVERFLOW, ERR_TABLE_ORDER = 1, 2, 4
 PRP_ZERO_TAIL = 1
 PRP_SCHED_SINGLE, PRP_SCHED_SPLIT = 2, 4
 XPORT_RDMA, XPORT_P2P, XPORT_SDMA = 0, 1, 2
+PAGE_NONE, PAGE_ALL = -1, -1  # a table entry without a page; "every token" of a move (0xFFFFFFFF)
+PAGE_OK, PAGE_INVALID, PAGE_SHORT = 0, 1, 2
+ERR_PAGE_TABLE = 8
 
 lib_path = _build.LIB
 
@@ -113,6 +124,15 @@ def _load():
     lib.db_cq_request_stop.restype = None
     for name in ("db_cq_mirror", "db_cq_attach", "db_cq_detach", "db_cq_wait_ack",
                  "db_cq_host_reap"):
+        getattr(lib, name).restype = i32
+    lib.db_page_workspace_size.argtypes = [u32, u32, psz]
+    lib.db_page_extend.argtypes = [vp, vp, u32, vp, vp, vp, vp, vp, sz, vp]
+    lib.db_page_fork.argtypes = [vp, vp, u32, vp, vp, vp, sz, vp]
+    lib.db_page_free.argtypes = lib.db_page_fork.argtypes
+    lib.db_page_compact.argtypes = [vp, vp, vp, u32, vp, vp, vp, sz, vp]
+    lib.db_page_copy.argtypes = [vp, u32, vp, vp, vp, vp, vp, vp]
+    for name in ("db_page_workspace_size", "db_page_extend", "db_page_fork", "db_page_free",
+                 "db_page_compact", "db_page_copy"):
         getattr(lib, name).restype = i32
     lib.db_strerror.argtypes = [i32]
     lib.db_strerror.restype = ctypes.c_char_p
@@ -410,3 +430,151 @@ def cq_host_reap(host_cq: torch.Tensor, head: int, phase: int, max_entries: int 
 
 def cq_request_stop(stop: torch.Tensor) -> None:
     _lib.db_cq_request_stop(_host(stop))
+
+
+# ---------------------------------------------------------------- paged cache
+class _Tables(ctypes.Structure):  # db_page_tables
+    _fields_ = [("table", ctypes.c_void_p), ("length", ctypes.c_void_p),
+                ("refs", ctypes.c_void_p), ("free", ctypes.c_void_p), ("n_seqs", ctypes.c_uint32),
+                ("columns", ctypes.c_uint32), ("n_pages", ctypes.c_uint32),
+                ("page_tokens", ctypes.c_uint32)]
+
+
+class _Pool(ctypes.Structure):  # db_page_pool
+    _fields_ = [("base", ctypes.c_void_p), ("n_pages", ctypes.c_uint64),
+                ("plane_stride", ctypes.c_uint64), ("page_stride", ctypes.c_uint64)]
+
+
+class _Shape(ctypes.Structure):  # db_page_shape
+    _fields_ = [("planes", ctypes.c_uint32), ("segments", ctypes.c_uint32),
+                ("page_tokens", ctypes.c_uint32), ("token_bytes", ctypes.c_uint32)]
+
+
+class PageTables:
+    """The state of a paged cache: int32 CUDA tensors table [n_seqs, columns],
+    length [n_seqs], refs [n_pages] and free [ceil(n_pages / 32)], which the
+    calls below update in place (their bits are the header's u32)."""
+
+    def __init__(self, table: torch.Tensor, length: torch.Tensor, refs: torch.Tensor,
+                 free: torch.Tensor, page_tokens: int):
+        if table.dim() != 2:
+            raise ValueError("table must be [n_seqs, columns]")
+        n_seqs, columns = table.shape
+        n_pages = refs.numel()
+        for name, t, n in (("table", table, n_seqs * columns), ("length", length, n_seqs),
+                           ("refs", refs, n_pages), ("free", free, (n_pages + 31) // 32)):
+            if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != n:
+                raise ValueError(f"{name} must be a contiguous int32 tensor of {n} elements")
+        self.table, self.length, self.refs, self.free = table, length, refs, free
+        self.page_tokens = int(page_tokens)
+        self._c = _Tables(table.data_ptr(), length.data_ptr(), refs.data_ptr(), free.data_ptr(),
+                          n_seqs, columns, n_pages, self.page_tokens)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, n_seqs: int, columns: int, n_pages: int, page_tokens: int,
+              device=None) -> "PageTables":
+        """An empty cache: no sequence holds a token and every page is free."""
+        device = device or "cuda"
+        free = torch.full(((n_pages + 31) // 32,), -1, dtype=torch.int32, device=device)
+        if n_pages % 32:
+            free[-1] = (1 << (n_pages % 32)) - 1
+        return cls(torch.full((n_seqs, columns), PAGE_NONE, dtype=torch.int32, device=device),
+                   torch.zeros(n_seqs, dtype=torch.int32, device=device),
+                   torch.zeros(n_pages, dtype=torch.int32, device=device), free, page_tokens)
+
+
+def page_workspace_size(n_seqs: int, n_pages: int) -> int:
+    return _size(_lib.db_page_workspace_size, n_seqs, n_pages)
+
+
+def _status(status: torch.Tensor | None, n: int) -> int | None:
+    if status is not None and status.numel() * status.element_size() < n:
+        raise ValueError(f"status holds fewer than {n} bytes")
+    return _ptr(status)
+
+
+def page_extend(tables: PageTables, req: torch.Tensor, moves: torch.Tensor,
+                n_moves: torch.Tensor, ws: torch.Tensor, status: torch.Tensor | None = None,
+                ctr: torch.Tensor | None = None, stream=None) -> None:
+    """db_page_extend: sequences grow by tokens (req [n, 2] {seq, tokens});
+    moves [>= n, 4] and n_moves [1] get the copies page_copy has to make."""
+    n = _records(req, 8)
+    if _records(moves, 16) < n:
+        raise ValueError(f"moves holds fewer than {n} records")
+    _check("db_page_extend", _lib.db_page_extend(
+        tables._ref, _ptr(req), n, _ptr(moves), _ptr(n_moves), _status(status, n), _ptr(ctr),
+        _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def page_fork(tables: PageTables, req: torch.Tensor, ws: torch.Tensor,
+              status: torch.Tensor | None = None, ctr: torch.Tensor | None = None,
+              stream=None) -> None:
+    """db_page_fork: children share their parents' first tokens (req [n, 4]
+    {parent, child, tokens, ignored})."""
+    n = _records(req, 16)
+    _check("db_page_fork", _lib.db_page_fork(
+        tables._ref, _ptr(req), n, _status(status, n), _ptr(ctr), _ptr(ws),
+        ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def page_free(tables: PageTables, req: torch.Tensor, ws: torch.Tensor,
+              status: torch.Tensor | None = None, ctr: torch.Tensor | None = None,
+              stream=None) -> None:
+    """db_page_free: sequences cut back to their first tokens (req [n, 2]
+    {seq, keep}) give their other pages back."""
+    n = _records(req, 8)
+    _check("db_page_free", _lib.db_page_free(
+        tables._ref, _ptr(req), n, _status(status, n), _ptr(ctr), _ptr(ws),
+        ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def page_compact(tables: PageTables, out: PageTables, moves: torch.Tensor, n_moves: torch.Tensor,
+                 ws: torch.Tensor, ctr: torch.Tensor | None = None, stream=None) -> None:
+    """db_page_compact: live pages move down to the lowest indices. The cache
+    after the moves goes to ``out`` (``tables`` itself, or other tensors of the
+    same sizes); moves [cap, 4] and n_moves [1] get what page_copy has to
+    move."""
+    _check("db_page_compact", _lib.db_page_compact(
+        tables._ref, out._ref, _ptr(moves), _records(moves, 16), _ptr(n_moves), _ptr(ctr),
+        _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def _pool(t: torch.Tensor) -> _Pool:
+    """A pool tensor [planes, pages, ...], strided in its first two axes."""
+    if t.dim() < 3:
+        raise ValueError("a pool is [planes, pages, ...]")
+    want = 1
+    for size, stride in zip(reversed(t.shape[2:]), reversed(t.stride()[2:])):
+        if size != 1 and stride != want:
+            raise ValueError("a pool's pages must be contiguous")
+        want *= size
+    es = t.element_size()
+    return _Pool(t.data_ptr(), t.shape[1], t.stride(0) * es, t.stride(1) * es)
+
+
+def page_copy(moves: torch.Tensor, n_moves: torch.Tensor, src: torch.Tensor, dst: torch.Tensor,
+              token_dim: int | None = None, ctr: torch.Tensor | None = None,
+              stream=None) -> None:
+    """db_page_copy: the bytes of ``moves`` ({src, dst, tokens, ignored}, of
+    which n_moves [1] counts), from pages of ``src`` to pages of ``dst`` (the
+    same tensor, or another of the same page shape). Pools are [planes, pages,
+    ...], on the GPU or in pinned host memory, strided in the first two axes;
+    ``token_dim`` is the axis of a page's tokens, None when it has none (then
+    every move takes whole pages)."""
+    if src.dtype != dst.dtype or src.shape[0] != dst.shape[0] or src.shape[2:] != dst.shape[2:]:
+        raise ValueError("source and destination pools differ in type, planes or page shape")
+    a = _pool(src)
+    b = a if dst is src else _pool(dst)
+    page = src.shape[2:]
+    if token_dim is None:
+        segments, page_tokens, k = 1, 1, 0
+    else:
+        if not 2 <= token_dim < src.dim():
+            raise ValueError("token_dim must be one of a page's axes (2 and up)")
+        k = token_dim - 1
+        segments, page_tokens = page[:k - 1].numel(), page[k - 1]
+    shape = _Shape(src.shape[0], segments, page_tokens, page[k:].numel() * src.element_size())
+    _check("db_page_copy", _lib.db_page_copy(
+        _ptr(moves), _records(moves, 16), _ptr(n_moves), ctypes.byref(a), ctypes.byref(b),
+        ctypes.byref(shape), _ptr(ctr), _stream(stream)))
