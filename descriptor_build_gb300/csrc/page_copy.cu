@@ -1,16 +1,23 @@
 // Copies of cache pages (include/pagecache.h: db_page_copy).
 //
-// A record's work in one plane is a fixed number of slots, each a vector of
-// kVec bytes: `runs` runs of `len` bytes, every run rounded up to whole
-// vectors. Slots are numbered through records and planes, a warp takes 256 of
-// them at a time, 8 loads in flight a lane, and stores them.
+// A record is `planes` copies of either the whole page, one run of bytes, or
+// its first tokens, a run in each of `segments`. Two kernels share the rest:
+//
+//  - page_copy_wide_kernel, for pages (or segments, where there are several)
+//    of kWideBytes and more: a warp takes a chunk of 4 KiB of one run, finds
+//    record, plane and segment once, and moves 8 vectors of 16 bytes a lane,
+//    all loads in flight before the first store;
+//  - page_copy_fine_kernel, for smaller ones and for addresses that are not
+//    multiples of 16: the vectors of all records and planes are numbered in
+//    one sequence, so that short runs share a warp, and each lane finds its
+//    own vectors.
 #include "common.cuh"
 #include "pagecache.h"
 
 namespace db {
 namespace {
 
-constexpr uint32_t kThreads = 256;
+constexpr uint32_t kThreads = 128;
 constexpr uint32_t kBatch = 8;                   // vectors a lane has in flight
 constexpr uint32_t kWarpSlots = 32 * kBatch;     // slots a warp takes at a time
 
@@ -21,9 +28,39 @@ struct CopyParams {
   db_page_pool src, dst;
   uint32_t planes, segments, page_tokens, token_bytes;
   uint64_t seg_bytes, page_bytes;
-  uint64_t slots;  // of a record in one plane: a multiple of kWarpSlots, or a power of two below it
+  uint64_t slots;  // of a record in one plane; fine: vectors, a multiple of kWarpSlots or a power
+                   // of two below it; wide: chunks
+  uint32_t seg_chunks;  // wide: chunks of a segment
   db_counters* ctr;
 };
+
+// The counters, by one CTA.
+__device__ __forceinline__ void count_records(const CopyParams& p, uint32_t n) {
+  if (p.ctr && blockIdx.x == 0) {
+    __shared__ unsigned int s_bad;
+    if (threadIdx.x == 0) s_bad = 0;
+    __syncthreads();
+    uint32_t bad = 0;
+    for (uint32_t r = threadIdx.x; r < n; r += kThreads) {
+      const uint4 m = *(reinterpret_cast<const uint4*>(p.moves) + r);
+      bad += m.x >= p.src.n_pages || m.y >= p.dst.n_pages;
+    }
+    if (bad) atomicAdd(&s_bad, bad);
+    __syncthreads();
+    if (threadIdx.x == 0) *p.ctr = db_counters{(uint64_t)n - s_bad, s_bad, 0, 0};
+  }
+}
+
+// A load of page data: L1 holds none of it. (Not the read-only path: source
+// and destination may be one pool.)
+__device__ __forceinline__ ulonglong2 ld_page16(const void* p, uint64_t pol) {
+  ulonglong2 v;
+  asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v2.u64 {%0, %1}, [%2], %3;"
+               : "=l"(v.x), "=l"(v.y)
+               : "l"(p), "l"(pol)
+               : "memory");
+  return v;
+}
 
 template <int kVec>
 struct Vec;
@@ -80,7 +117,7 @@ __device__ __forceinline__ Piece piece(const CopyParams& p, uint32_t tokens, uin
 }
 
 template <int kVec>
-__global__ void __launch_bounds__(kThreads) page_copy_kernel(const CopyParams p) {
+__global__ void __launch_bounds__(kThreads) page_copy_fine_kernel(const CopyParams p) {
   typedef typename Vec<kVec>::type V;
   wait_for_prerequisites();
   dependents_may_launch();
@@ -121,19 +158,75 @@ __global__ void __launch_bounds__(kThreads) page_copy_kernel(const CopyParams p)
     for (uint32_t j = 0; j < kBatch; ++j)
       if (bytes[j] == kVec) *(V*)to[j] = v[j];
   }
-  if (p.ctr && blockIdx.x == 0) {
-    __shared__ unsigned int s_bad;
-    if (threadIdx.x == 0) s_bad = 0;
-    __syncthreads();
-    uint32_t bad = 0;
-    for (uint32_t r = threadIdx.x; r < n; r += kThreads) {
-      const uint4 m = *(reinterpret_cast<const uint4*>(p.moves) + r);
-      bad += m.x >= p.src.n_pages || m.y >= p.dst.n_pages;
+  count_records(p, n);
+}
+
+// ---------------------------------------------------------------------- wide
+constexpr uint32_t kChunk = kWarpSlots * 16;  // bytes a warp moves at a time
+constexpr uint64_t kWideBytes = 2048;
+// CTAs an SM of the largest grid. How many records there are is on the device,
+// so the grid is bounded and loops; 8 CTAs are resident, and several times as
+// many even out what the loops leave at the end. 3,500 pages of 16 planes of
+// 32 KiB (3.67 GB read and written), us: 580 with one grid of residents, 557
+// twice, 544 four times, 538 eight times (6.8 TB/s, the rate of a plain copy),
+// 535 sixteen times; six pages alone take 0.3 us less in CTAs of 128 threads
+// than of 256. The same pages through shared memory by bulk copies (4 to 16 KiB,
+// 3 to 12 CTAs an SM, 2 or 4 stages ahead) took 570 to 607 us, and 2.8 KB
+// runs 75 us and more where these loads and stores take 44.
+constexpr uint32_t kWideCtas = 64;
+
+__device__ __forceinline__ uint64_t div64(uint64_t a, uint32_t b) {
+  return (a >> 32) ? a / b : (uint32_t)a / b;
+}
+
+__global__ void __launch_bounds__(kThreads) page_copy_wide_kernel(const CopyParams p) {
+  wait_for_prerequisites();
+  dependents_may_launch();
+  const uint32_t n = min(__ldcg(p.n_moves), p.max_moves);
+  const uint32_t lane = threadIdx.x & 31;
+  const uint32_t chunks = (uint32_t)p.slots;  // of a record in one plane
+  const uint64_t all = (uint64_t)n * p.planes * chunks;
+  const uint64_t stride = (uint64_t)gridDim.x * (kThreads / 32);
+  for (uint64_t x = (uint64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; x < all; x += stride) {
+    const uint64_t rp = div64(x, chunks), r = div64(rp, p.planes);
+    const uint32_t plane = (uint32_t)(rp - r * p.planes);
+    uint32_t k = (uint32_t)(x - rp * chunks);
+    const uint4 m = *(reinterpret_cast<const uint4*>(p.moves) + r);
+    if (m.x >= p.src.n_pages || m.y >= p.dst.n_pages) continue;
+    uint64_t len = p.page_bytes, at = 0;
+    if (m.z < p.page_tokens) {
+      len = (uint64_t)m.z * p.token_bytes;
+      if (p.segments > 1) {
+        const uint32_t s = k / p.seg_chunks;
+        k -= s * p.seg_chunks;
+        at = s * p.seg_bytes;
+      }
     }
-    if (bad) atomicAdd(&s_bad, bad);
-    __syncthreads();
-    if (threadIdx.x == 0) *p.ctr = db_counters{(uint64_t)n - s_bad, s_bad, 0, 0};
+    const uint64_t off = (uint64_t)k * kChunk;
+    if (off >= len) continue;
+    at += off;
+    const uint32_t left = (uint32_t)min(len - off, (uint64_t)kChunk);
+    const char* from = (const char*)p.src.base + plane * p.src.plane_stride + m.x * p.src.page_stride + at;
+    char* to = (char*)p.dst.base + plane * p.dst.plane_stride + m.y * p.dst.page_stride + at;
+    const uint64_t pol = policy_evict_first();
+    ulonglong2 v[kBatch];
+    if (left == kChunk) {
+#pragma unroll
+      for (uint32_t j = 0; j < kBatch; ++j) v[j] = ld_page16(from + 16 * (32 * j + lane), pol);
+#pragma unroll
+      for (uint32_t j = 0; j < kBatch; ++j) st_stream16(to + 16 * (32 * j + lane), v[j].x, v[j].y, pol);
+    } else {
+      const uint32_t whole = left / 16;
+#pragma unroll
+      for (uint32_t j = 0; j < kBatch; ++j)
+        if (32 * j + lane < whole) v[j] = ld_page16(from + 16 * (32 * j + lane), pol);
+#pragma unroll
+      for (uint32_t j = 0; j < kBatch; ++j)
+        if (32 * j + lane < whole) st_stream16(to + 16 * (32 * j + lane), v[j].x, v[j].y, pol);
+      if (lane < left % 16) to[16 * whole + lane] = from[16 * whole + lane];
+    }
   }
+  count_records(p, n);
 }
 
 bool pool_ok(const db_page_pool* q, const db_page_shape* f, uint64_t page_bytes) {
@@ -153,8 +246,8 @@ int launch_copy(CopyParams& p, cudaStream_t s) {
     while (p.slots < per) p.slots *= 2;
   }
   const uint64_t warps = ((uint64_t)p.max_moves * p.planes * p.slots + kWarpSlots - 1) / kWarpSlots;
-  const uint64_t want = (warps + kThreads / 32 - 1) / (kThreads / 32), most = 8ull * num_sms();
-  return launch_dependent(page_copy_kernel<kVec>, (unsigned)(want < most ? want : most), kThreads,
+  const uint64_t want = (warps + kThreads / 32 - 1) / (kThreads / 32), most = 16ull * num_sms();
+  return launch_dependent(page_copy_fine_kernel<kVec>, (unsigned)(want < most ? want : most), kThreads,
                           0, s, p);
 }
 
@@ -168,11 +261,11 @@ extern "C" int db_page_copy(const db_page_move* moves, uint32_t max_moves, const
                             const db_page_shape* shape, db_counters* ctr, void* stream) {
   if (!shape || !shape->planes || !shape->segments || !shape->page_tokens || !shape->token_bytes)
     return -EINVAL;
-  // A page stays below 2^32 bytes, a record below 2^40 in all its planes.
-  const uint64_t rows = (uint64_t)shape->segments * shape->page_tokens;
-  if (rows > 0xFFFFFFFFull || rows * shape->token_bytes > 0xFFFFFFFFull || shape->planes > 65536)
-    return -EINVAL;
+  // A page's bytes in all planes are at most 2^31: what is numbered below stays within 64 bits.
+  const uint64_t limit = 1ull << 31, rows = (uint64_t)shape->segments * shape->page_tokens;
+  if (shape->planes > 65536 || rows > limit) return -EINVAL;
   const uint64_t page_bytes = rows * shape->token_bytes;
+  if (page_bytes > limit || page_bytes * shape->planes > limit) return -EINVAL;
   if (!pool_ok(src, shape, page_bytes) || !pool_ok(dst, shape, page_bytes)) return -EINVAL;
   if (!n_moves || !aligned(n_moves, 4) || !aligned(ctr, 8)) return -EINVAL;
   if (max_moves && (!moves || !aligned(moves, 16))) return -EINVAL;
@@ -201,6 +294,13 @@ extern "C" int db_page_copy(const db_page_move* moves, uint32_t max_moves, const
   if (src->n_pages > 1) all |= src->page_stride;
   if (dst->n_pages > 1) all |= dst->page_stride;
   if (p.segments > 1) all |= p.seg_bytes;
+  if (!(all & 15) && (p.segments > 1 ? p.seg_bytes : page_bytes) >= kWideBytes) {
+    p.seg_chunks = (uint32_t)((p.seg_bytes + kChunk - 1) / kChunk);
+    p.slots = (uint64_t)p.seg_chunks * p.segments;
+    const uint64_t warps = p.max_moves * (p.planes * p.slots);
+    const uint64_t want = (warps + kThreads / 32 - 1) / (kThreads / 32), most = (uint64_t)kWideCtas * num_sms();
+    return launch_dependent(page_copy_wide_kernel, (unsigned)(want < most ? want : most), kThreads, 0, s, p);
+  }
   if (!(all & 15)) return launch_copy<16>(p, s);
   if (!(all & 7)) return launch_copy<8>(p, s);
   if (!(all & 3)) return launch_copy<4>(p, s);

@@ -183,7 +183,8 @@ typedef struct db_page_shape {
  * another (in one pool): its bytes are then undefined. A record naming a page
  * outside its pool is skipped; ctr (NULL or counters): total = records
  * copied, n_invalid = records skipped. Strides must keep pages of one pool
- * apart; they and the bases need no alignment, but 16 bytes copy fastest. */
+ * apart; they and the bases need no alignment, but 16 bytes copy fastest. A
+ * page's bytes in all planes are at most 2^31, planes at most 65536. */
 int db_page_copy(const db_page_move* moves, uint32_t max_moves, const uint32_t* n_moves,
                  const db_page_pool* src, const db_page_pool* dst, const db_page_shape* shape,
                  db_counters* ctr, void* stream);
