@@ -24,6 +24,8 @@ Records of the paged cache (include/pagecache.h), u32 fields as int32 bits:
 from __future__ import annotations
 
 import ctypes
+import functools
+import math
 import os
 
 import numpy as np
@@ -163,9 +165,17 @@ def _records(t: torch.Tensor, size: int) -> int:
     return nbytes // size
 
 
+# The current device's current stream as a number. torch.cuda.current_stream()
+# builds a Stream object for it (2.9 us a call on the GPU's host, these 0.2 us).
+_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None or _device is None or not torch.cuda.is_initialized():
+            return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -461,6 +471,8 @@ class PageTables:
             raise ValueError("table must be [n_seqs, columns]")
         n_seqs, columns = table.shape
         n_pages = refs.numel()
+        if max(n_seqs, columns, n_pages, int(page_tokens)) > 0xFFFFFFFF:
+            raise ValueError("sizes of a cache are below 2^32")
         for name, t, n in (("table", table, n_seqs * columns), ("length", length, n_seqs),
                            ("refs", refs, n_pages), ("free", free, (n_pages + 31) // 32)):
             if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != n:
@@ -488,6 +500,13 @@ def page_workspace_size(n_seqs: int, n_pages: int) -> int:
     return _size(_lib.db_page_workspace_size, n_seqs, n_pages)
 
 
+def _requests(t: torch.Tensor, size: int) -> int:
+    n = _records(t, size)
+    if n > 0xFFFFFFFF:
+        raise ValueError("a batch has fewer than 2^32 records")
+    return n
+
+
 def _status(status: torch.Tensor | None, n: int) -> int | None:
     if status is not None and status.numel() * status.element_size() < n:
         raise ValueError(f"status holds fewer than {n} bytes")
@@ -499,8 +518,8 @@ def page_extend(tables: PageTables, req: torch.Tensor, moves: torch.Tensor,
                 ctr: torch.Tensor | None = None, stream=None) -> None:
     """db_page_extend: sequences grow by tokens (req [n, 2] {seq, tokens});
     moves [>= n, 4] and n_moves [1] get the copies page_copy has to make."""
-    n = _records(req, 8)
-    if _records(moves, 16) < n:
+    n = _requests(req, 8)
+    if _requests(moves, 16) < n:
         raise ValueError(f"moves holds fewer than {n} records")
     _check("db_page_extend", _lib.db_page_extend(
         tables._ref, _ptr(req), n, _ptr(moves), _ptr(n_moves), _status(status, n), _ptr(ctr),
@@ -512,7 +531,7 @@ def page_fork(tables: PageTables, req: torch.Tensor, ws: torch.Tensor,
               stream=None) -> None:
     """db_page_fork: children share their parents' first tokens (req [n, 4]
     {parent, child, tokens, ignored})."""
-    n = _records(req, 16)
+    n = _requests(req, 16)
     _check("db_page_fork", _lib.db_page_fork(
         tables._ref, _ptr(req), n, _status(status, n), _ptr(ctr), _ptr(ws),
         ws.numel() * ws.element_size(), _stream(stream)))
@@ -523,7 +542,7 @@ def page_free(tables: PageTables, req: torch.Tensor, ws: torch.Tensor,
               stream=None) -> None:
     """db_page_free: sequences cut back to their first tokens (req [n, 2]
     {seq, keep}) give their other pages back."""
-    n = _records(req, 8)
+    n = _requests(req, 8)
     _check("db_page_free", _lib.db_page_free(
         tables._ref, _ptr(req), n, _status(status, n), _ptr(ctr), _ptr(ws),
         ws.numel() * ws.element_size(), _stream(stream)))
@@ -536,21 +555,40 @@ def page_compact(tables: PageTables, out: PageTables, moves: torch.Tensor, n_mov
     same sizes); moves [cap, 4] and n_moves [1] get what page_copy has to
     move."""
     _check("db_page_compact", _lib.db_page_compact(
-        tables._ref, out._ref, _ptr(moves), _records(moves, 16), _ptr(n_moves), _ptr(ctr),
+        tables._ref, out._ref, _ptr(moves), _requests(moves, 16), _ptr(n_moves), _ptr(ctr),
         _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
 
 
-def _pool(t: torch.Tensor) -> _Pool:
-    """A pool tensor [planes, pages, ...], strided in its first two axes."""
-    if t.dim() < 3:
+def _strides(shape, stride, item: int) -> tuple[int, int]:
+    """Bytes between the planes and the pages of a pool [planes, pages, ...]."""
+    if len(shape) < 3:
         raise ValueError("a pool is [planes, pages, ...]")
     want = 1
-    for size, stride in zip(reversed(t.shape[2:]), reversed(t.stride()[2:])):
-        if size != 1 and stride != want:
+    for size, step in zip(reversed(shape[2:]), reversed(stride[2:])):
+        if size != 1 and step != want:
             raise ValueError("a pool's pages must be contiguous")
         want *= size
-    es = t.element_size()
-    return _Pool(t.data_ptr(), t.shape[1], t.stride(0) * es, t.stride(1) * es)
+    return stride[0] * item, stride[1] * item
+
+
+@functools.lru_cache(maxsize=1024)
+def _copy_plan(src_shape, src_stride, dst_shape, dst_stride, item: int, token_dim):
+    """What a copy's pools have in common and their strides, from their shapes alone."""
+    if src_shape[0] != dst_shape[0] or src_shape[2:] != dst_shape[2:]:
+        raise ValueError("source and destination pools differ in planes or page shape")
+    a, b = _strides(src_shape, src_stride, item), _strides(dst_shape, dst_stride, item)
+    page = src_shape[2:]
+    if token_dim is None:
+        segments, page_tokens, k = 1, 1, 0
+    else:
+        if not 2 <= token_dim < len(src_shape):
+            raise ValueError("token_dim must be one of a page's axes (2 and up)")
+        k = token_dim - 1
+        segments, page_tokens = math.prod(page[:k - 1]), page[k - 1]
+    if math.prod(page) * item * src_shape[0] > 1 << 31:
+        raise ValueError("a page has at most 2^31 bytes in all planes")
+    shape = _Shape(src_shape[0], segments, page_tokens, math.prod(page[k:]) * item)
+    return shape, ctypes.byref(shape), a, b
 
 
 def page_copy(moves: torch.Tensor, n_moves: torch.Tensor, src: torch.Tensor, dst: torch.Tensor,
@@ -562,19 +600,11 @@ def page_copy(moves: torch.Tensor, n_moves: torch.Tensor, src: torch.Tensor, dst
     ...], on the GPU or in pinned host memory, strided in the first two axes;
     ``token_dim`` is the axis of a page's tokens, None when it has none (then
     every move takes whole pages)."""
-    if src.dtype != dst.dtype or src.shape[0] != dst.shape[0] or src.shape[2:] != dst.shape[2:]:
-        raise ValueError("source and destination pools differ in type, planes or page shape")
-    a = _pool(src)
-    b = a if dst is src else _pool(dst)
-    page = src.shape[2:]
-    if token_dim is None:
-        segments, page_tokens, k = 1, 1, 0
-    else:
-        if not 2 <= token_dim < src.dim():
-            raise ValueError("token_dim must be one of a page's axes (2 and up)")
-        k = token_dim - 1
-        segments, page_tokens = page[:k - 1].numel(), page[k - 1]
-    shape = _Shape(src.shape[0], segments, page_tokens, page[k:].numel() * src.element_size())
+    if src.dtype != dst.dtype:
+        raise ValueError("source and destination pools differ in type")
+    shape, ref, a, b = _copy_plan(src.shape, src.stride(), dst.shape, dst.stride(),
+                                  src.element_size(), token_dim)
     _check("db_page_copy", _lib.db_page_copy(
-        _ptr(moves), _records(moves, 16), _ptr(n_moves), ctypes.byref(a), ctypes.byref(b),
-        ctypes.byref(shape), _ptr(ctr), _stream(stream)))
+        _ptr(moves), _requests(moves, 16), _ptr(n_moves),
+        ctypes.byref(_Pool(src.data_ptr(), src.shape[1], *a)),
+        ctypes.byref(_Pool(dst.data_ptr(), dst.shape[1], *b)), ref, _ptr(ctr), _stream(stream)))

@@ -3,9 +3,11 @@
 //
 // A call's requests are planned by one team: a single CTA or one cluster of
 // CTAs, whose barriers are the hardware's, so no kernel here waits on memory.
-// The plan is a prefix sum over the requests (how many table entries or pages
-// each of them has), and what follows is work on single entries found again
-// in that prefix by a search in shared memory.
+// The plan is a prefix sum over what the requests ask for, and what follows
+// is work on pieces of it, found again by a search in shared memory. The team
+// does that work itself when it is little; otherwise a second kernel does it
+// on the whole GPU, launched as a dependent of the first when the sizes of
+// the call allow for so much (how much there is, only the device knows).
 //
 // Nothing depends on the order in which atomics land: a request's claim on
 // its sequence and the holders of a shared page are a maximum and a count,
@@ -19,22 +21,30 @@ namespace {
 
 constexpr uint32_t kTeamThreads = 1024;
 constexpr uint32_t kTeamWarps = kTeamThreads / 32;
+#ifndef DB_PAGE_TEAM
+#define DB_PAGE_TEAM 8
+#endif
+constexpr uint32_t kMaxTeam = DB_PAGE_TEAM;  // CTAs of the largest team
 constexpr uint32_t kSearch = 4096;     // prefix entries kept in shared memory
+constexpr uint32_t kRows = 8;          // requests of a group (see free_units)
 constexpr uint32_t kNoMove = 0xFFFFFFFFu;
+constexpr uint32_t kNoEntry = 0xFFFFFFFEu;   // a row without an entry in the column
+constexpr uint32_t kBadEntry = 0xFFFFFFFFu;  // no page
+#ifndef DB_PAGE_OWN
+#define DB_PAGE_OWN 4
+#endif
+constexpr uint32_t kOwn = DB_PAGE_OWN;  // what a warp (unit) or thread (page) of the team does itself
 
 // One request's place in the plan.
 struct __align__(16) Plan {
-  uint32_t start;  // entries (or pages) of the requests before it
-  uint32_t seq;    // row that is written
-  uint32_t col;    // its first entry's column
-  uint32_t aux;    // extend: index of its move or kNoMove; fork: the parent's row
+  uint32_t row;   // row that is written
+  uint32_t from;  // free, fork: first column; extend: the column of its first page
+  uint32_t end;   // free, fork: past the last column; extend: pages of the requests before it
+  uint32_t aux;   // extend: index of its move or kNoMove; fork: the parent's row
 };
 
-// Workspace: header, then one claim a sequence, the holders of each page in
-// the batch (count, latest), the plan, the free pages before each 128.
 struct Head {
-  unsigned long long total;  // entries of the plan
-  uint32_t n_live;
+  uint32_t units;      // left for the second kernel
   uint32_t moved;      // compact: moves made
   uint32_t dst_last;   // compact: the last page moved to (with moved > 0)
   uint32_t src_first;  // compact: the lowest page moved from, or n_pages
@@ -46,8 +56,9 @@ struct Work {
   uint32_t* holders;  // [n_pages], zero between calls
   uint32_t* latest;   // [n_pages], zero between calls
   Plan* plan;         // [n_seqs]
-  uint32_t* before;   // [n_quads] free pages before each quad of words
-  uint32_t* renamed;  // [n_pages] compact: where a moved page went
+  uint2* group;       // [n_seqs / kRows] {units before it, its first column}
+  uint32_t* before;   // [n_words] free pages before each word
+  uint32_t* pages;    // [n_pages] extend: the pages taken, by rank; compact: where a moved page went
 };
 
 inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -65,8 +76,9 @@ size_t carve(char* ws, uint32_t n_seqs, uint32_t n_pages, Work* w) {
   x.holders = (uint32_t*)take(4 * (size_t)n_pages);
   x.latest = (uint32_t*)take(4 * (size_t)n_pages);
   x.plan = (Plan*)take(16 * (size_t)n_seqs);
-  x.before = (uint32_t*)take(4 * (((size_t)n_pages + 127) / 128));
-  x.renamed = (uint32_t*)take(4 * (size_t)n_pages);
+  x.group = (uint2*)take(8 * (((size_t)n_seqs + kRows - 1) / kRows));
+  x.before = (uint32_t*)take(4 * (((size_t)n_pages + 31) / 32));
+  x.pages = (uint32_t*)take(4 * (size_t)n_pages);
   if (w) *w = x;
   return at;
 }
@@ -197,15 +209,14 @@ struct Team {
 // sync of a kernel's team comes after its last scan in every kernel below, so
 // no CTA leaves before its peers have read it.
 
-// --------------------------------------------------------- finding an entry
-// The request that entry e belongs to: the last i with start[i] <= e, among
-// requests whose starts are in shared memory, every `step`-th of them when
-// there are more than kSearch.
+// ---------------------------------------------------------- finding a piece
+// The last i with start(i) <= e, where start is not decreasing: every
+// `step`-th start is in shared memory, all of them up to kSearch.
 struct Finder {
   const uint32_t* s_start;
-  const Plan* plan;
   uint32_t n, kept, step;
-  __device__ __forceinline__ uint32_t find(uint32_t e) const {
+  template <typename Start>
+  __device__ __forceinline__ uint32_t find(uint32_t e, Start start) const {
     uint32_t lo = 0, hi = kept;  // s_start[lo] <= e < s_start[hi]
     while (hi - lo > 1) {
       const uint32_t mid = (lo + hi) >> 1;
@@ -216,23 +227,22 @@ struct Finder {
       hi = min(n, lo + step);
       while (hi - lo > 1) {
         const uint32_t mid = (lo + hi) >> 1;
-        if (__ldcg(&plan[mid].start) <= e) lo = mid; else hi = mid;
+        if (start(mid) <= e) lo = mid; else hi = mid;
       }
     }
     return lo;
   }
 };
 
-// Load the plan's starts (every thread of a CTA; ends past a barrier).
-__device__ __forceinline__ Finder load_finder(uint32_t* s_start, const Plan* plan, uint32_t n) {
+// Load the starts (every thread of a CTA; ends past a barrier).
+template <typename Start>
+__device__ __forceinline__ Finder load_finder(uint32_t* s_start, uint32_t n, Start start) {
   Finder f;
   f.s_start = s_start;
-  f.plan = plan;
   f.n = n;
   f.step = (n + kSearch - 1) / kSearch;
   f.kept = (n + f.step - 1) / f.step;
-  for (uint32_t k = threadIdx.x; k < f.kept; k += blockDim.x)
-    s_start[k] = __ldcg(&plan[k * f.step].start);
+  for (uint32_t k = threadIdx.x; k < f.kept; k += blockDim.x) s_start[k] = start(k * f.step);
   __syncthreads();
   return f;
 }
@@ -240,6 +250,9 @@ __device__ __forceinline__ Finder load_finder(uint32_t* s_start, const Plan* pla
 __device__ __forceinline__ Plan ld_plan(const Plan* p) {
   const uint4 v = __ldcg(reinterpret_cast<const uint4*>(p));
   return Plan{v.x, v.y, v.z, v.w};
+}
+__device__ __forceinline__ void st_plan(Plan* p, const Plan& v) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(v.row, v.from, v.end, v.aux);
 }
 
 // First come, first served: of the requests naming a sequence the first has
@@ -252,232 +265,320 @@ __device__ __forceinline__ bool claimed(const uint32_t* c, uint32_t seq, uint32_
 }
 
 __device__ __forceinline__ uint32_t pages_of(uint64_t tokens, uint32_t page_tokens) {
-  return (uint32_t)((tokens + page_tokens - 1) / page_tokens);
+  return (tokens >> 32) || tokens + page_tokens > 0xFFFFFFFFull
+             ? (uint32_t)((tokens + page_tokens - 1) / page_tokens)
+             : ((uint32_t)tokens + page_tokens - 1) / page_tokens;
 }
 
-// The four free words of quad q, with the bits past n_pages cleared.
-__device__ __forceinline__ uint4 ld_quad(const uint32_t* bits, uint32_t q, uint32_t n_pages) {
-  uint4 v = make_uint4(0, 0, 0, 0);
-  const uint32_t words = (n_pages + 31) / 32, w = 4 * q;
-  if (w + 3 < words) {
-    v = __ldcg(reinterpret_cast<const uint4*>(bits) + q);
-  } else {
-    if (w < words) v.x = __ldcg(&bits[w]);
-    if (w + 1 < words) v.y = __ldcg(&bits[w + 1]);
-    if (w + 2 < words) v.z = __ldcg(&bits[w + 2]);
-    if (w + 3 < words) v.w = __ldcg(&bits[w + 3]);
-  }
-  const uint32_t tail = n_pages & 31;
-  if (tail && w + 4 >= words) {
-    const uint32_t mask = (1u << tail) - 1, last = (words - 1) & 3;
-    if (words > w) {
-      if (last == 0) v.x &= mask;
-      if (last == 1) v.y &= mask;
-      if (last == 2) v.z &= mask;
-      if (last == 3) v.w &= mask;
-    }
-  }
+// Word w of the free bits, without bits past n_pages.
+__device__ __forceinline__ uint32_t ld_word(const uint32_t* bits, uint32_t w, uint32_t n_pages) {
+  uint32_t v = __ldcg(&bits[w]);
+  if (n_pages - 32 * w < 32) v &= (1u << (n_pages & 31)) - 1;
   return v;
 }
-__device__ __forceinline__ uint32_t popc4(const uint4& v) {
-  return __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w);
-}
 
-// Free pages before each quad into `before`; returns their number.
+// Free pages before each word into `before`; returns their number.
 __device__ __forceinline__ uint32_t scan_free(Team& team, const uint32_t* bits, uint32_t n_pages,
                                               uint32_t* before) {
-  const uint32_t quads = (n_pages + 127) / 128;
+  const uint32_t words = (n_pages + 31) / 32;
   uint32_t carry = 0;
-  for (uint32_t q0 = 0; q0 < quads; q0 += team.threads()) {
-    const uint32_t q = q0 + team.id();
-    const uint32_t c = q < quads ? popc4(ld_quad(bits, q, n_pages)) : 0;
+  for (uint32_t w0 = 0; w0 < words; w0 += team.threads()) {
+    const uint32_t w = w0 + team.id();
+    const uint32_t c = w < words ? __popc(ld_word(bits, w, n_pages)) : 0;
     Sum total;
     const Sum x = team.scan(Sum{c, 0}, &total);
-    if (q < quads) before[q] = carry + (uint32_t)x.a;
+    if (w < words) before[w] = carry + (uint32_t)x.a;
     carry += (uint32_t)total.a;
   }
   return carry;
 }
 
-__device__ __forceinline__ uint32_t word_of(const uint4& v, uint32_t k) {
-  return k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w;
+// A count and an error, one warp's at a time, into the counters.
+__device__ __forceinline__ void add_count(uint64_t* to, uint32_t count) {
+  const uint32_t c = warp_sum32(count);
+  if ((threadIdx.x & 31) == 0 && c) atomicAdd((unsigned long long*)to, (unsigned long long)c);
+}
+__device__ __forceinline__ void add_error(db_counters* ctr, bool bad) {
+  if (__any_sync(kFull, bad) && (threadIdx.x & 31) == 0)
+    atomicOr((unsigned long long*)&ctr->err, (unsigned long long)DB_ERR_PAGE_TABLE);
 }
 
-// Add a CTA's per-thread count and error bits to the counters.
-__device__ __forceinline__ void add_counts(uint64_t* total, uint64_t* err, uint32_t count,
-                                           uint32_t bad) {
-  const uint32_t c = warp_sum32(count);
-  const uint32_t e = __any_sync(kFull, bad != 0);
-  if ((threadIdx.x & 31) == 0) {
-    if (c) atomicAdd((unsigned long long*)total, (unsigned long long)c);
-    if (e) atomicOr((unsigned long long*)err, (unsigned long long)DB_ERR_PAGE_TABLE);
+// --------------------------------------------------------------- row units
+// Free and fork work on columns [from, end) of each request's row. kRows
+// requests in order are a group; the columns from the first to the last that
+// any of them has, from a multiple of 32 on, are cut into units of 32, and a
+// warp takes a unit: one column a lane, kRows rows in flight. Rows of one
+// group often name the same page in one column (a common prefix, the
+// children of one parent); its references then change by one atomic.
+struct Rows {
+  db_page_tables t;
+  db_counters* ctr;
+  uint8_t* status;
+  uint32_t n;
+  Work w;
+};
+
+// Each thread's columns into the groups; ends with every group of these
+// requests written (not yet visible to other CTAs). `carry`: units before.
+__device__ __forceinline__ void plan_rows(Team& team, const Rows& p, uint32_t i, const Plan& pl,
+                                          uint32_t* carry) {
+  uint32_t lo = pl.from < pl.end ? pl.from : 0xFFFFFFFFu, hi = pl.from < pl.end ? pl.end : 0;
+#pragma unroll
+  for (uint32_t o = 1; o < kRows; o <<= 1) {
+    lo = min(lo, __shfl_xor_sync(kFull, lo, o));
+    hi = max(hi, __shfl_xor_sync(kFull, hi, o));
   }
+  lo &= ~31u;
+  const uint32_t units = hi > lo ? (hi - lo + 31) / 32 : 0;
+  const bool first = i % kRows == 0;
+  Sum total;
+  const Sum x = team.scan(Sum{first ? units : 0, 0}, &total);
+  if (i < p.n) {
+    st_plan(&p.w.plan[i], pl);
+    if (first) p.w.group[i / kRows] = make_uint2(*carry + (uint32_t)x.a, lo);
+  }
+  *carry += (uint32_t)total.a;
+}
+
+struct GroupStart {
+  const uint2* group;
+  __device__ __forceinline__ uint32_t operator()(uint32_t g) const { return __ldcg(&group[g].x); }
+};
+
+// The rows of unit u: lane j < kRows holds the j-th plan (empty if there is
+// none); returns this lane's column.
+__device__ __forceinline__ uint32_t load_unit(const Rows& p, const Finder& f, uint32_t u,
+                                              uint32_t lane, Plan* pl) {
+  const uint32_t g = f.find(u, GroupStart{p.w.group});
+  const uint2 at = __ldcg(&p.w.group[g]);
+  const uint32_t i = g * kRows + lane;
+  *pl = Plan{0, 0, 0, 0};
+  if (lane < kRows && i < p.n) *pl = ld_plan(&p.w.plan[i]);
+  return at.y + (u - at.x) * 32 + lane;
 }
 
 // ---------------------------------------------------------------------- free
 struct FreeParams {
-  db_page_tables t;
+  Rows r;
   const db_page_cut* req;
-  uint32_t n;
-  uint8_t* status;
-  db_counters* ctr;
-  Work w;
 };
 
-// Entry e: its page loses a reference, and is free when that was the last.
-__device__ __forceinline__ void free_entries(const FreeParams& p, const Finder& f, uint64_t total,
-                                             uint64_t first, uint64_t stride) {
-  uint32_t released = 0, bad = 0;
-  for (uint64_t e = first; e < total; e += stride) {
-    const Plan pl = ld_plan(&p.w.plan[f.find((uint32_t)e)]);
-    int32_t* at = &p.t.table[(uint64_t)pl.seq * p.t.columns + pl.col + ((uint32_t)e - pl.start)];
-    const uint32_t page = (uint32_t)*at;
-    *at = DB_PAGE_NONE;
-    if (page >= p.t.n_pages) {
-      bad = 1;
-      continue;
+__device__ __forceinline__ void free_units(const Rows& p, const Finder& f, uint32_t first,
+                                           uint32_t stride, uint32_t units) {
+  const uint32_t lane = threadIdx.x & 31;
+  uint32_t released = 0;
+  bool bad = false;
+  for (uint32_t u = first; u < units; u += stride) {
+    Plan pl;
+    const uint32_t c = load_unit(p, f, u, lane, &pl);
+    uint32_t page[kRows];
+    bool clear[kRows];
+#pragma unroll
+    for (uint32_t j = 0; j < kRows; ++j) {
+      const uint32_t row = __shfl_sync(kFull, pl.row, j), from = __shfl_sync(kFull, pl.from, j);
+      const uint32_t end = __shfl_sync(kFull, pl.end, j);
+      page[j] = kNoEntry;
+      if (c >= from && c < end) page[j] = (uint32_t)p.t.table[(uint64_t)row * p.t.columns + c];
+      clear[j] = c >= from && c < end;
     }
-    const uint32_t old = atomicSub(&p.t.refs[page], 1u);
-    if (old == 1) {
-      atomicOr(&p.t.free[page >> 5], 1u << (page & 31));
-      ++released;
-    } else if (old == 0) {  // a free page: leave it so
-      atomicAdd(&p.t.refs[page], 1u);
-      bad = 1;
+#pragma unroll
+    for (uint32_t j = 0; j < kRows; ++j) {
+      const uint32_t row = __shfl_sync(kFull, pl.row, j);
+      if (!clear[j]) continue;
+      p.t.table[(uint64_t)row * p.t.columns + c] = DB_PAGE_NONE;
+      if (page[j] == kNoEntry) page[j] = kBadEntry;
+    }
+    uint32_t old[kRows], times[kRows];
+#pragma unroll
+    for (uint32_t j = 0; j < kRows; ++j) {
+      times[j] = 0;
+      if (page[j] == kNoEntry || (j && page[j] == page[j - 1])) continue;
+      if (page[j] >= p.t.n_pages) {
+        bad = true;
+        continue;
+      }
+      uint32_t run = 1;
+#pragma unroll
+      for (uint32_t k = j + 1; k < kRows; ++k)
+        if (run == k - j && page[k] == page[j]) ++run;
+      times[j] = run;
+      old[j] = atomicSub(&p.t.refs[page[j]], run);
+    }
+#pragma unroll
+    for (uint32_t j = 0; j < kRows; ++j) {
+      if (!times[j]) continue;
+      if (old[j] == times[j]) {
+        atomicOr(&p.t.free[page[j] >> 5], 1u << (page[j] & 31));
+        ++released;
+      } else if (old[j] < times[j]) {  // more rows than references: leave them as they were
+        atomicAdd(&p.t.refs[page[j]], times[j]);
+        bad = true;
+      }
     }
   }
-  if (p.ctr) add_counts(&p.ctr->total, &p.ctr->err, released, bad);
+  if (p.ctr) {
+    add_count(&p.ctr->total, released);
+    add_error(p.ctr, bad);
+  }
 }
 
-__global__ void __launch_bounds__(kTeamThreads) page_free_plan_kernel(const FreeParams p) {
+__global__ void __launch_bounds__(kTeamThreads) page_free_kernel(const FreeParams q) {
   __shared__ TeamShared s_team;
+  __shared__ uint32_t s_start[kSearch];
+  const Rows& p = q.r;
   wait_for_prerequisites();
   dependents_may_launch();
   Team team(&s_team);
+  if (p.ctr && team.id() == 0) *p.ctr = db_counters{0, 0, 0, 0};
   for (uint32_t i = team.id(); i < p.n; i += team.threads()) {
-    const uint32_t seq = p.req[i].seq;
+    const uint32_t seq = q.req[i].seq;
     if (seq < p.t.n_seqs) claim(p.w.claim, seq, i);
   }
   team.sync();
-  uint64_t carry = 0, invalid = 0;
+  uint32_t units = 0, invalid = 0;
   for (uint32_t i0 = 0; i0 < p.n; i0 += team.threads()) {
     const uint32_t i = i0 + team.id();
-    uint32_t from = 0, count = 0, seq = 0;
-    bool ok = false;
+    Plan pl = {0, 0, 0, 0};
     if (i < p.n) {
-      const db_page_cut r = p.req[i];
-      seq = r.seq;
-      ok = seq < p.t.n_seqs && claimed(p.w.claim, seq, i);
+      const db_page_cut r = q.req[i];
+      const uint32_t len = r.seq < p.t.n_seqs ? p.t.length[r.seq] : 0;
+      const bool ok = r.seq < p.t.n_seqs && claimed(p.w.claim, r.seq, i);
       if (ok) {
-        p.w.claim[seq] = 0;
-        const uint32_t len = p.t.length[seq];
+        p.w.claim[r.seq] = 0;
         if (r.keep < len) {
-          from = pages_of(r.keep, p.t.page_tokens);
-          count = min(pages_of(len, p.t.page_tokens), p.t.columns);
-          count = count > from ? count - from : 0;
-          p.t.length[seq] = r.keep;
+          pl = Plan{r.seq, pages_of(r.keep, p.t.page_tokens),
+                    min(pages_of(len, p.t.page_tokens), p.t.columns), 0};
+          p.t.length[r.seq] = r.keep;
         }
       }
+      invalid += !ok;
       if (p.status) p.status[i] = ok ? DB_PAGE_OK : DB_PAGE_INVALID;
     }
-    Sum total;
-    const Sum x = team.scan(Sum{count, (uint32_t)(i < p.n && !ok)}, &total);
-    if (i < p.n) p.w.plan[i] = Plan{(uint32_t)(carry + x.a), seq, from, 0};
-    carry += total.a;
-    invalid += total.b;
+    plan_rows(team, p, i, pl, &units);
   }
-  if (team.id() == 0) {
-    p.w.head->total = carry;
-    if (p.ctr) *p.ctr = db_counters{0, invalid, 0, 0};
-  }
+  if (p.ctr) add_count(&p.ctr->n_invalid, invalid);
+  const bool own = units <= kOwn * (team.threads() / 32);
+  if (team.id() == 0) p.w.head->units = own ? 0 : units;
   team.sync();
+  if (!own || !units) return;
+  const Finder f = load_finder(s_start, (p.n + kRows - 1) / kRows, GroupStart{p.w.group});
+  free_units(p, f, team.id() / 32, team.threads() / 32, units);
 }
 
-__global__ void __launch_bounds__(256) page_free_entries_kernel(const FreeParams p) {
+__global__ void __launch_bounds__(256) page_free_units_kernel(const FreeParams q) {
   __shared__ uint32_t s_start[kSearch];
+  const Rows& p = q.r;
   wait_for_prerequisites();
   dependents_may_launch();
-  const uint64_t total = __ldcg(&p.w.head->total), first = (uint64_t)blockIdx.x * 256;
-  if (first >= total) return;
-  const Finder f = load_finder(s_start, p.w.plan, p.n);
-  free_entries(p, f, total, first + threadIdx.x, (uint64_t)gridDim.x * 256);
+  const uint32_t units = __ldcg(&p.w.head->units);
+  if (blockIdx.x * 8 >= units) return;
+  const Finder f = load_finder(s_start, (p.n + kRows - 1) / kRows, GroupStart{p.w.group});
+  free_units(p, f, blockIdx.x * 8 + threadIdx.x / 32, gridDim.x * 8, units);
 }
 
 // ---------------------------------------------------------------------- fork
 struct ForkParams {
-  db_page_tables t;
+  Rows r;
   const db_page_fork_req* req;
-  uint32_t n;
-  uint8_t* status;
-  db_counters* ctr;
-  Work w;
 };
 
-__device__ __forceinline__ void fork_entries(const ForkParams& p, const Finder& f, uint64_t total,
-                                             uint64_t first, uint64_t stride) {
-  uint32_t bad = 0;
-  for (uint64_t e = first; e < total; e += stride) {
-    const Plan pl = ld_plan(&p.w.plan[f.find((uint32_t)e)]);
-    const uint32_t col = (uint32_t)e - pl.start;
-    const int32_t page = p.t.table[(uint64_t)pl.aux * p.t.columns + col];
-    p.t.table[(uint64_t)pl.seq * p.t.columns + col] = page;
-    if ((uint32_t)page < p.t.n_pages)
-      atomicAdd(&p.t.refs[page], 1u);
-    else
-      bad = 1;
+__device__ __forceinline__ void fork_units(const Rows& p, const Finder& f, uint32_t first,
+                                           uint32_t stride, uint32_t units) {
+  const uint32_t lane = threadIdx.x & 31;
+  bool bad = false;
+  for (uint32_t u = first; u < units; u += stride) {
+    Plan pl;
+    const uint32_t c = load_unit(p, f, u, lane, &pl);
+    uint32_t page[kRows];
+#pragma unroll
+    for (uint32_t j = 0; j < kRows; ++j) {
+      const uint32_t from = __shfl_sync(kFull, pl.aux, j), end = __shfl_sync(kFull, pl.end, j);
+      page[j] = kNoEntry;
+      if (c < end) page[j] = (uint32_t)p.t.table[(uint64_t)from * p.t.columns + c];
+    }
+#pragma unroll
+    for (uint32_t j = 0; j < kRows; ++j) {
+      const uint32_t row = __shfl_sync(kFull, pl.row, j), end = __shfl_sync(kFull, pl.end, j);
+      if (c >= end) continue;
+      p.t.table[(uint64_t)row * p.t.columns + c] = (int32_t)page[j];
+      if (page[j] >= p.t.n_pages) {
+        bad = true;
+        page[j] = kNoEntry;
+        continue;
+      }
+      if (j && page[j] == page[j - 1]) continue;
+      uint32_t run = 1;
+#pragma unroll
+      for (uint32_t k = j + 1; k < kRows; ++k)
+        if (run == k - j && page[k] == page[j]) ++run;
+      atomicAdd(&p.t.refs[page[j]], run);
+    }
   }
-  if (p.ctr) add_counts(&p.ctr->total, &p.ctr->err, 0, bad);
+  if (p.ctr) add_error(p.ctr, bad);
 }
 
-__global__ void __launch_bounds__(kTeamThreads) page_fork_plan_kernel(const ForkParams p) {
+__global__ void __launch_bounds__(kTeamThreads) page_fork_kernel(const ForkParams q) {
   __shared__ TeamShared s_team;
+  __shared__ uint32_t s_start[kSearch];
+  const Rows& p = q.r;
   wait_for_prerequisites();
   dependents_may_launch();
   Team team(&s_team);
+  if (p.ctr && team.id() == 0) *p.ctr = db_counters{0, 0, 0, 0};
   for (uint32_t i = team.id(); i < p.n; i += team.threads()) {
-    const uint32_t child = p.req[i].child;
+    const uint32_t child = q.req[i].child;
     if (child < p.t.n_seqs) claim(p.w.claim, child, i);
   }
   team.sync();
-  uint64_t carry = 0, invalid = 0;
+  uint32_t units = 0, invalid = 0;
+  uint64_t taken = 0;
   for (uint32_t i0 = 0; i0 < p.n; i0 += team.threads()) {
     const uint32_t i = i0 + team.id();
-    db_page_fork_req r = {0, 0, 0, 0};
-    uint32_t count = 0;
-    bool ok = false;
+    Plan pl = {kNoMove, 0, 0, 0};
     if (i < p.n) {
-      r = p.req[i];
+      const db_page_fork_req r = q.req[i];
+      bool ok = false;
       if (r.child < p.t.n_seqs && claimed(p.w.claim, r.child, i)) {
         p.w.claim[r.child] = 0;
-        ok = r.parent < p.t.n_seqs && r.parent != r.child && p.t.length[r.child] == 0 &&
-             r.tokens <= p.t.length[r.parent];
+        ok = r.parent < p.t.n_seqs && r.parent != r.child && __ldcg(&p.t.length[r.child]) == 0 &&
+             r.tokens <= __ldcg(&p.t.length[r.parent]);
       }
-      if (ok) count = min(pages_of(r.tokens, p.t.page_tokens), p.t.columns);
+      if (ok) {
+        pl = Plan{r.child, 0, min(pages_of(r.tokens, p.t.page_tokens), p.t.columns), r.parent};
+        taken += pl.end;
+      }
+      invalid += !ok;
       if (p.status) p.status[i] = ok ? DB_PAGE_OK : DB_PAGE_INVALID;
     }
-    Sum total;
-    const Sum x = team.scan(Sum{count, (uint32_t)(i < p.n && !ok)}, &total);
-    if (i < p.n) p.w.plan[i] = Plan{(uint32_t)(carry + x.a), r.child, ok ? 1u : 0u, r.parent};
-    carry += total.a;
-    invalid += total.b;
+    plan_rows(team, p, i, pl, &units);
   }
-  if (team.id() == 0) {
-    p.w.head->total = carry;
-    if (p.ctr) *p.ctr = db_counters{carry, invalid, 0, 0};
+  if (p.ctr) {
+    add_count(&p.ctr->n_invalid, invalid);
+    const uint64_t c = warp_sum64(taken);
+    if ((threadIdx.x & 31) == 0 && c)
+      atomicAdd((unsigned long long*)&p.ctr->total, (unsigned long long)c);
   }
+  const bool own = units <= kOwn * (team.threads() / 32);
+  if (team.id() == 0) p.w.head->units = own ? 0 : units;
   team.sync();  // every length is read
-  for (uint32_t i = team.id(); i < p.n; i += team.threads())
-    if (p.w.plan[i].col) p.t.length[p.req[i].child] = p.req[i].tokens;
+  for (uint32_t i = team.id(); i < p.n; i += team.threads()) {
+    const uint32_t row = p.w.plan[i].row;
+    if (row != kNoMove) p.t.length[row] = q.req[i].tokens;
+  }
+  if (!own || !units) return;
+  const Finder f = load_finder(s_start, (p.n + kRows - 1) / kRows, GroupStart{p.w.group});
+  fork_units(p, f, team.id() / 32, team.threads() / 32, units);
 }
 
-__global__ void __launch_bounds__(256) page_fork_entries_kernel(const ForkParams p) {
+__global__ void __launch_bounds__(256) page_fork_units_kernel(const ForkParams q) {
   __shared__ uint32_t s_start[kSearch];
+  const Rows& p = q.r;
   wait_for_prerequisites();
   dependents_may_launch();
-  const uint64_t total = __ldcg(&p.w.head->total), first = (uint64_t)blockIdx.x * 256;
-  if (first >= total) return;
-  const Finder f = load_finder(s_start, p.w.plan, p.n);
-  fork_entries(p, f, total, first + threadIdx.x, (uint64_t)gridDim.x * 256);
+  const uint32_t units = __ldcg(&p.w.head->units);
+  if (blockIdx.x * 8 >= units) return;
+  const Finder f = load_finder(s_start, (p.n + kRows - 1) / kRows, GroupStart{p.w.group});
+  fork_units(p, f, blockIdx.x * 8 + threadIdx.x / 32, gridDim.x * 8, units);
 }
 
 // -------------------------------------------------------------------- extend
@@ -492,37 +593,63 @@ struct ExtendParams {
   Work w;
 };
 
-// What request i asks for, from the state before the call.
+// What a request asks for, from the state before the call.
 struct Ask {
-  bool ok;
-  bool corrupt;     // its last page does not exist
-  uint32_t had;     // pages before
-  uint32_t grow;    // pages after - before
-  uint32_t last;    // its last page, when `shared`
-  uint32_t refs;    // of that page
-  bool shared;      // it adds to a partly filled page with other holders
+  uint32_t seq, now;  // its row, and its length after
+  uint32_t had;       // pages before
+  uint32_t grow;      // pages after - before
+  uint32_t part;      // tokens in a partly filled last page that it adds to, or 0
+  uint32_t last;      // that page
+  uint32_t refs;      // its references
+  bool mine, ok, corrupt;
+  __device__ __forceinline__ bool shares() const { return part && refs > 1; }
 };
 
-__device__ __forceinline__ Ask ask(const ExtendParams& p, uint32_t i, const db_page_grow& r) {
-  Ask a = {false, false, 0, 0, 0, 0, false};
-  if (r.seq >= p.t.n_seqs || !claimed(p.w.claim, r.seq, i)) return a;
-  const uint64_t len = p.t.length[r.seq], now = len + r.tokens;
-  if (now > (uint64_t)p.t.columns * p.t.page_tokens || now > 0xFFFFFFFFull) return a;
+__device__ __forceinline__ Ask ask(const ExtendParams& p, uint32_t i) {
+  Ask a = {0, 0, 0, 0, 0, 0, 0, false, false, false};
+  if (i >= p.n) return a;
+  const db_page_grow r = p.req[i];
+  a.seq = r.seq;
+  if (r.seq >= p.t.n_seqs) return a;
+  const uint32_t len = p.t.length[r.seq];
+  a.mine = claimed(p.w.claim, r.seq, i);
+  const uint64_t now = (uint64_t)len + r.tokens;
+  if (!a.mine || now > (uint64_t)p.t.columns * p.t.page_tokens || now > 0xFFFFFFFFull) return a;
   a.ok = true;
+  a.now = (uint32_t)now;
   a.had = pages_of(len, p.t.page_tokens);
   a.grow = pages_of(now, p.t.page_tokens) - a.had;
-  if (r.tokens && len % p.t.page_tokens) {
+  const uint32_t part = len % p.t.page_tokens;
+  if (r.tokens && part) {
     a.last = (uint32_t)p.t.table[(uint64_t)r.seq * p.t.columns + a.had - 1];
     if (a.last >= p.t.n_pages) {
       a.ok = false;
       a.corrupt = true;
       a.grow = 0;
-      return a;
+    } else {
+      a.refs = __ldcg(&p.t.refs[a.last]);
+      a.part = part;
     }
-    a.refs = __ldcg(&p.t.refs[a.last]);
-    a.shared = a.refs > 1;
   }
   return a;
+}
+
+struct PlanStart {
+  const Plan* plan;
+  __device__ __forceinline__ uint32_t operator()(uint32_t i) const { return __ldcg(&plan[i].end); }
+};
+
+// Page e of the batch into its row.
+__device__ __forceinline__ void place_pages(const ExtendParams& p, const Finder& f, uint32_t first,
+                                            uint32_t stride, uint32_t total) {
+  for (uint32_t e = first; e < total; e += stride) {
+    const uint32_t page = __ldcg(&p.w.pages[e]);
+    const Plan pl = ld_plan(&p.w.plan[f.find(e, PlanStart{p.w.plan})]);
+    const uint32_t j = e - pl.end;
+    p.t.table[(uint64_t)pl.row * p.t.columns + pl.from + j] = (int32_t)page;
+    p.t.refs[page] = 1;
+    if (j == 0 && pl.aux != kNoMove) p.moves[pl.aux].dst = page;
+  }
 }
 
 __global__ void __launch_bounds__(kTeamThreads) page_extend_kernel(const ExtendParams p) {
@@ -531,117 +658,110 @@ __global__ void __launch_bounds__(kTeamThreads) page_extend_kernel(const ExtendP
   wait_for_prerequisites();
   dependents_may_launch();
   Team team(&s_team);
-  for (uint32_t i = team.id(); i < p.n; i += team.threads()) {
+  const uint32_t id = team.id(), threads = team.threads();
+  const bool one = p.n <= threads;  // every request has a thread: asked once, kept in registers
+  if (p.ctr && id == 0) *p.ctr = db_counters{0, 0, 0, 0};
+  for (uint32_t i = id; i < p.n; i += threads) {
     const uint32_t seq = p.req[i].seq;
     if (seq < p.t.n_seqs) claim(p.w.claim, seq, i);
   }
   const uint32_t avail = scan_free(team, p.t.free, p.t.n_pages, p.w.before);
   team.sync();
   // How many of the batch's requests hold each shared page, and the last of them.
-  for (uint32_t i = team.id(); i < p.n; i += team.threads()) {
-    const Ask a = ask(p, i, p.req[i]);
-    if (a.shared) {
+  Ask a = {0, 0, 0, 0, 0, 0, 0, false, false, false};
+  for (uint32_t i = id; i < p.n; i += threads) {
+    a = ask(p, i);
+    if (a.shares()) {
       atomicAdd(&p.w.holders[a.last], 1u);
       atomicMax(&p.w.latest[a.last], i);
     }
   }
   team.sync();
-  uint64_t total_need = 0, n_moves = 0, n_bad = 0, n_corrupt = 0;
-  for (uint32_t i0 = 0; i0 < p.n; i0 += team.threads()) {
-    const uint32_t i = i0 + team.id();
-    Ask a = {false, false, 0, 0, 0, 0, false};
-    db_page_grow r = {0, 0};
-    uint32_t cow = 0;
-    if (i < p.n) {
-      r = p.req[i];
-      a = ask(p, i, r);
-      if (a.shared)
-        cow = !(__ldcg(&p.w.holders[a.last]) == a.refs && __ldcg(&p.w.latest[a.last]) == i);
-    }
+  uint64_t need = 0;
+  uint32_t n_moves = 0;
+  for (uint32_t i0 = 0; i0 < p.n; i0 += threads) {
+    const uint32_t i = i0 + id;
+    if (!one) a = ask(p, i);
+    const uint32_t cow = a.shares() && !(__ldcg(&p.w.holders[a.last]) == a.refs &&
+                                     __ldcg(&p.w.latest[a.last]) == i);
     Sum total;
     const Sum x = team.scan(Sum{(uint64_t)a.grow + cow, cow}, &total);
     if (i < p.n)
-      p.w.plan[i] = Plan{(uint32_t)min(total_need + x.a, (uint64_t)0xFFFFFFFFu), r.seq, a.had - cow,
-                         cow ? (uint32_t)n_moves + x.b : kNoMove};
-    total_need += total.a;
+      st_plan(&p.w.plan[i], Plan{a.seq, a.had - cow, (uint32_t)min(need + x.a, (uint64_t)0xFFFFFFFFu),
+                                 cow ? n_moves + x.b : kNoMove});
+    need += total.a;
     n_moves += total.b;
-    Sum bad;
-    team.scan(Sum{(uint64_t)(i < p.n && !a.ok), (uint32_t)a.corrupt}, &bad);
-    n_bad += bad.a;
-    n_corrupt += bad.b;
   }
-  const bool go = total_need <= avail;
-  if (team.id() == 0) {
-    *p.n_moves = go ? (uint32_t)n_moves : 0;
-    if (p.ctr)
-      *p.ctr = db_counters{total_need, n_bad, go ? 0 : p.n - n_bad,
-                           n_corrupt ? (uint64_t)DB_ERR_PAGE_TABLE : 0};
+  const bool go = need <= avail;
+  const bool own = need <= (uint64_t)kOwn * threads;
+  if (id == 0) {
+    *p.n_moves = go ? n_moves : 0;
+    p.w.head->units = go && !own ? (uint32_t)need : 0;
+    if (p.ctr) p.ctr->total = need;
   }
   team.sync();
   // Lengths, moves and status, and the workspace as the next call wants it.
-  for (uint32_t i = team.id(); i < p.n; i += team.threads()) {
-    const db_page_grow r = p.req[i];
-    const bool mine = r.seq < p.t.n_seqs && claimed(p.w.claim, r.seq, i);
-    bool ok = false;
-    if (mine) {
-      const uint32_t len = p.t.length[r.seq];
-      const uint64_t now = (uint64_t)len + r.tokens;
-      ok = now <= (uint64_t)p.t.columns * p.t.page_tokens && now <= 0xFFFFFFFFull;
-      if (ok && r.tokens && len % p.t.page_tokens) {
-        const uint32_t had = pages_of(len, p.t.page_tokens);
-        const uint32_t last = (uint32_t)p.t.table[(uint64_t)r.seq * p.t.columns + had - 1];
-        if (last >= p.t.n_pages) {
-          ok = false;
-        } else {
-          p.w.holders[last] = 0;
-          p.w.latest[last] = 0;
-          const uint32_t m = p.w.plan[i].aux;
-          if (go && m != kNoMove) {
-            atomicSub(&p.t.refs[last], 1u);
-            p.moves[m].src = last;
-            p.moves[m].tokens = len % p.t.page_tokens;
-            p.moves[m].rsvd = 0;
-          }
-        }
+  uint32_t invalid = 0, refused = 0;
+  bool corrupt = false;
+  for (uint32_t i = id; i < p.n; i += threads) {
+    if (!one) a = ask(p, i);
+    const uint32_t m = p.w.plan[i].aux;
+    if (m != kNoMove) {  // at least one holder of every shared page copies, and clears for all
+      p.w.holders[a.last] = 0;
+      p.w.latest[a.last] = 0;
+      if (go) {
+        atomicSub(&p.t.refs[a.last], 1u);
+        p.moves[m].src = a.last;
+        *reinterpret_cast<uint2*>(&p.moves[m].tokens) = make_uint2(a.part, 0);
       }
-      p.w.claim[r.seq] = 0;
-      if (ok && go) p.t.length[r.seq] = (uint32_t)now;
     }
-    if (p.status) p.status[i] = !ok ? DB_PAGE_INVALID : go ? DB_PAGE_OK : DB_PAGE_SHORT;
+    if (a.mine) p.w.claim[a.seq] = 0;
+    if (a.ok && go) p.t.length[a.seq] = a.now;
+    invalid += !a.ok;
+    refused += a.ok && !go;
+    corrupt |= a.corrupt;
+    if (p.status) p.status[i] = !a.ok ? DB_PAGE_INVALID : go ? DB_PAGE_OK : DB_PAGE_SHORT;
   }
-  team.sync();  // the replaced entries have been read
-  if (!go || total_need == 0) return;
-  // The pages, by rank among the free ones: a warp takes 32 words, one word at
-  // a time with a page per lane, so that neighbours write neighbours.
-  const Finder f = load_finder(s_start, p.w.plan, p.n);
+  if (p.ctr) {
+    add_count(&p.ctr->n_invalid, invalid);
+    add_count(&p.ctr->n_overflow, refused);
+    add_error(p.ctr, corrupt);
+  }
+  if (!go || need == 0) return;
+  // The pages taken, by rank: a word at a time, a page per lane.
   const uint32_t lane = threadIdx.x & 31, words = (p.t.n_pages + 31) / 32;
-  const uint32_t groups = (words + 31) / 32, warps = team.threads() / 32;
-  for (uint32_t g = team.id() / 32; g < groups; g += warps) {
-    uint32_t rank = __ldcg(&p.w.before[8 * g]);
-    if (rank >= total_need) break;  // ranks grow with g
-    const uint32_t w = 32 * g + lane;
-    uint32_t bits = w < words ? __ldcg(&p.t.free[w]) : 0;
-    if (w == words - 1 && (p.t.n_pages & 31)) bits &= (1u << (p.t.n_pages & 31)) - 1;
+  for (uint32_t w0 = id - lane; w0 < words; w0 += threads) {
+    const uint32_t w = w0 + lane;
+    const uint32_t rank = w < words ? __ldcg(&p.w.before[w]) : 0xFFFFFFFFu;
+    const uint32_t bits = w < words ? ld_word(p.t.free, w, p.t.n_pages) : 0;
+    uint32_t active = __ballot_sync(kFull, bits && rank < need);
     uint32_t left = bits;
-    for (uint32_t k = 0; k < 32; ++k) {
+    while (active) {
+      const uint32_t k = __ffs(active) - 1;
+      active &= active - 1;
       const uint32_t v = __shfl_sync(kFull, bits, k);
-      const uint32_t e = rank + __popc(v & lanemask_lt());
-      const bool mine = (v >> lane & 1) && e < total_need;
+      const uint32_t e = __shfl_sync(kFull, rank, k) + __popc(v & lanemask_lt());
+      const bool mine = (v >> lane & 1) && e < need;
       const uint32_t taken = __ballot_sync(kFull, mine);
+      if (mine) p.w.pages[e] = (w0 + k) * 32 + lane;
       if (lane == k) left &= ~taken;
-      if (mine) {
-        const uint32_t page = (32 * g + k) * 32 + lane;
-        const Plan pl = ld_plan(&p.w.plan[f.find(e)]);
-        const uint32_t j = e - pl.start;
-        p.t.table[(uint64_t)pl.seq * p.t.columns + pl.col + j] = (int32_t)page;
-        p.t.refs[page] = 1;
-        if (j == 0 && pl.aux != kNoMove) p.moves[pl.aux].dst = page;
-      }
-      rank += __popc(v);
-      if (rank >= total_need) break;
     }
     if (left != bits) p.t.free[w] = left;
   }
+  team.sync();  // the pages are known, and the replaced entries have been read
+  if (!own) return;
+  const Finder f = load_finder(s_start, p.n, PlanStart{p.w.plan});
+  place_pages(p, f, id, threads, (uint32_t)need);
+}
+
+__global__ void __launch_bounds__(256) page_place_kernel(const ExtendParams p) {
+  __shared__ uint32_t s_start[kSearch];
+  wait_for_prerequisites();
+  dependents_may_launch();
+  const uint32_t total = __ldcg(&p.w.head->units);
+  if (blockIdx.x * 256 >= total) return;
+  const Finder f = load_finder(s_start, p.n, PlanStart{p.w.plan});
+  place_pages(p, f, blockIdx.x * 256 + threadIdx.x, gridDim.x * 256, total);
 }
 
 // ------------------------------------------------------------------- compact
@@ -659,52 +779,50 @@ __global__ void __launch_bounds__(kTeamThreads) page_compact_plan_kernel(const C
   wait_for_prerequisites();
   dependents_may_launch();
   Team team(&s_team);
-  const uint32_t n_pages = p.t.n_pages;
+  const uint32_t id = team.id(), threads = team.threads();
+  const uint32_t n_pages = p.t.n_pages, words = (n_pages + 31) / 32;
   const uint32_t n_live = n_pages - scan_free(team, p.t.free, n_pages, p.w.before);
   team.sync();
   // M: the free pages below n_live.
-  uint32_t holes;
-  if (n_live == n_pages) {
-    holes = 0;
-  } else {
-    const uint32_t q = n_live / 128;
-    const uint4 v = ld_quad(p.t.free, q, n_pages);
-    holes = __ldcg(&p.w.before[q]);
-    for (uint32_t k = 0; k < 4; ++k) {
-      const uint32_t at = q * 128 + k * 32, x = word_of(v, k);
-      if (n_live >= at + 32)
-        holes += __popc(x);
-      else if (n_live > at)
-        holes += __popc(x & ((1u << (n_live - at)) - 1));
-    }
+  uint32_t holes = 0;
+  if (n_live < n_pages) {
+    const uint32_t w = n_live / 32;
+    holes = __ldcg(&p.w.before[w]) +
+            __popc(ld_word(p.t.free, w, n_pages) & ((1u << (n_live & 31)) - 1));
   }
   const uint32_t moved = min(holes, p.cap);
-  if (team.id() == 0) {
+  if (id == 0) {
     *p.n_moves = moved;
     p.w.head->moved = moved;
-    p.w.head->n_live = n_live;
     if (moved == 0) {
       p.w.head->src_first = n_pages;
       p.w.head->dst_last = 0;
     }
     if (p.ctr) *p.ctr = db_counters{holes, 0, (uint64_t)holes - moved, 0};
   }
-  const uint32_t lane = threadIdx.x & 31, words = (n_pages + 31) / 32;
-  const uint32_t groups = (words + 31) / 32, warps = team.threads() / 32;
-  for (uint32_t g = team.id() / 32; g < groups && moved; g += warps) {
-    uint32_t before = __ldcg(&p.w.before[8 * g]);
-    const uint32_t w = 32 * g + lane;
-    const uint32_t bits = w < words ? __ldcg(&p.t.free[w]) : 0;
-    for (uint32_t k = 0; k < 32; ++k) {
+  const uint32_t lane = threadIdx.x & 31;
+  for (uint32_t w0 = id - lane; w0 < words && moved; w0 += threads) {
+    const uint32_t w = w0 + lane, first = 32 * w;
+    const uint32_t bits = w < words ? ld_word(p.t.free, w, n_pages) : 0;
+    const uint32_t before = w < words ? __ldcg(&p.w.before[w]) : 0;
+    // free pages below n_live to move to, or live pages from n_live on to move from
+    bool use = false;
+    if (w < words) {
+      if (first < n_live) use = bits && before < moved;
+      if (first + 31 >= n_live) use |= bits != kFull;
+    }
+    uint32_t active = __ballot_sync(kFull, use);
+    while (active) {
+      const uint32_t k = __ffs(active) - 1;
+      active &= active - 1;
       const uint32_t v = __shfl_sync(kFull, bits, k);
-      const uint32_t page = (32 * g + k) * 32 + lane;
-      const uint32_t rank = before + __popc(v & lanemask_lt());  // free pages before it
+      const uint32_t page = (w0 + k) * 32 + lane;
+      const uint32_t rank = __shfl_sync(kFull, before, k) + __popc(v & lanemask_lt());
       if (page < n_pages) {
         if (v >> lane & 1) {
           if (page < n_live && rank < moved) {
             p.moves[rank].dst = page;
-            p.moves[rank].tokens = DB_PAGE_ALL;
-            p.moves[rank].rsvd = 0;
+            *reinterpret_cast<uint2*>(&p.moves[rank].tokens) = make_uint2(DB_PAGE_ALL, 0);
             if (rank == moved - 1) p.w.head->dst_last = page;
           }
         } else if (page >= n_live) {
@@ -715,15 +833,14 @@ __global__ void __launch_bounds__(kTeamThreads) page_compact_plan_kernel(const C
           }
         }
       }
-      before += __popc(v);
     }
   }
   team.sync();
-  for (uint32_t k = team.id(); k < moved; k += team.threads()) {
-    const uint32_t src = __ldcg(&p.moves[k].src), dst = __ldcg(&p.moves[k].dst);
-    p.w.renamed[src] = dst;
-    p.out.refs[dst] = p.t.refs[src];
-    p.out.refs[src] = 0;
+  for (uint32_t k = id; k < moved; k += threads) {
+    const uint2 m = __ldcg(reinterpret_cast<const uint2*>(&p.moves[k]));
+    p.w.pages[m.x] = m.y;
+    p.out.refs[m.y] = p.t.refs[m.x];
+    p.out.refs[m.x] = 0;
   }
 }
 
@@ -735,16 +852,16 @@ __global__ void __launch_bounds__(256) page_compact_apply_kernel(const CompactPa
   const uint32_t moved = __ldcg(&p.w.head->moved), src_first = __ldcg(&p.w.head->src_first);
   const uint32_t dst_last = __ldcg(&p.w.head->dst_last);
   const uint64_t entries = (uint64_t)p.t.n_seqs * p.t.columns;
-  uint32_t bad = 0;
+  bool bad = false;
   for (uint64_t e = id; e < entries; e += step) {
     const uint32_t was = (uint32_t)p.t.table[e];
     uint32_t is = was;
     if (was >= src_first && was != (uint32_t)DB_PAGE_NONE) {
-      if (was < n_pages) is = __ldcg(&p.w.renamed[was]); else bad = 1;
+      if (was < n_pages) is = __ldcg(&p.w.pages[was]); else bad = true;
     }
     if (p.out.table != p.t.table || is != was) p.out.table[e] = (int32_t)is;
   }
-  if (p.ctr) add_counts(&p.ctr->total, &p.ctr->err, 0, bad);
+  if (p.ctr) add_error(p.ctr, bad);
   if (p.out.refs != p.t.refs)
     for (uint64_t q = id; q < n_pages; q += step) {
       const uint32_t v = p.t.refs[q];
@@ -790,6 +907,7 @@ int launch_team(void (*kernel)(P), uint32_t ctas, cudaStream_t s, const P& param
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
+  if (ctas > 8) cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, params);
   if (e != cudaSuccess) return cuda_failure(e);
   return launch_result();
@@ -830,12 +948,31 @@ int nothing(db_counters* ctr, uint32_t* n_moves, cudaStream_t s) {
   return 0;
 }
 
-uint32_t team_size() { return 1; }
+// CTAs of the team for `n` requests, `words` of free bits and at most `units`
+// pieces of a warp's work.
+uint32_t team_size(uint64_t n, uint64_t words, uint64_t units) {
+  uint64_t want = n > words ? n : words;
+  if (units * 32 / kOwn > want) want = units * 32 / kOwn;
+  uint32_t c = 1;
+  while (c < kMaxTeam && (uint64_t)c * kTeamThreads < want) c *= 2;
+  return c;
+}
 
-// CTAs of an entries kernel over at most `entries`.
-unsigned entry_grid(uint64_t entries) {
-  const uint64_t want = (entries + 255) / 256, most = 8ull * num_sms();
+// CTAs of 256 threads for at most `threads`.
+unsigned whole_grid(uint64_t threads) {
+  const uint64_t want = (threads + 255) / 256, most = 8ull * num_sms();
   return (unsigned)(want < 1 ? 1 : want < most ? want : most);
+}
+
+// Free and fork: the team, and the whole GPU where there may be more than the
+// team does itself.
+template <typename P>
+int launch_rows(void (*team)(P), void (*rest)(P), cudaStream_t s, const P& p) {
+  const uint64_t units = ((uint64_t)p.r.n + kRows - 1) / kRows * (((uint64_t)p.r.t.columns + 31) / 32);
+  const uint32_t ctas = team_size(p.r.n, 0, units);
+  const int e = launch_team(team, ctas, s, p);
+  if (e || units <= (uint64_t)kOwn * ctas * kTeamWarps) return e;
+  return launch_dependent(rest, whole_grid(units * 32), 256, 0, s, p);
 }
 
 }  // namespace
@@ -853,40 +990,34 @@ extern "C" int db_page_free(const db_page_tables* t, const db_page_cut* req, uin
                             uint8_t* status, db_counters* ctr, void* ws, size_t ws_bytes,
                             void* stream) {
   FreeParams p = {};
-  const int rc = check_call(t, req, 8, n, ctr, ws, ws_bytes, &p.w);
+  const int rc = check_call(t, req, sizeof(*req), n, ctr, ws, ws_bytes, &p.r.w);
   if (rc) return rc;
   const cudaStream_t s = (cudaStream_t)stream;
   if (!n) return nothing(ctr, nullptr, s);
   if ((uint64_t)n * t->columns > 0xFFFFFFFFull) return -EINVAL;  // entries are numbered in 32 bits
-  p.t = *t;
+  p.r.t = *t;
+  p.r.n = n;
+  p.r.status = status;
+  p.r.ctr = ctr;
   p.req = req;
-  p.n = n;
-  p.status = status;
-  p.ctr = ctr;
-  const int e = launch_team(page_free_plan_kernel, team_size(), s, p);
-  if (e) return e;
-  return launch_dependent(page_free_entries_kernel, entry_grid((uint64_t)n * t->columns), 256, 0,
-                          s, p);
+  return launch_rows(page_free_kernel, page_free_units_kernel, s, p);
 }
 
 extern "C" int db_page_fork(const db_page_tables* t, const db_page_fork_req* req, uint32_t n,
                             uint8_t* status, db_counters* ctr, void* ws, size_t ws_bytes,
                             void* stream) {
   ForkParams p = {};
-  const int rc = check_call(t, req, 16, n, ctr, ws, ws_bytes, &p.w);
+  const int rc = check_call(t, req, sizeof(*req), n, ctr, ws, ws_bytes, &p.r.w);
   if (rc) return rc;
   const cudaStream_t s = (cudaStream_t)stream;
   if (!n) return nothing(ctr, nullptr, s);
   if ((uint64_t)n * t->columns > 0xFFFFFFFFull) return -EINVAL;  // entries are numbered in 32 bits
-  p.t = *t;
+  p.r.t = *t;
+  p.r.n = n;
+  p.r.status = status;
+  p.r.ctr = ctr;
   p.req = req;
-  p.n = n;
-  p.status = status;
-  p.ctr = ctr;
-  const int e = launch_team(page_fork_plan_kernel, team_size(), s, p);
-  if (e) return e;
-  return launch_dependent(page_fork_entries_kernel, entry_grid((uint64_t)n * t->columns), 256, 0,
-                          s, p);
+  return launch_rows(page_fork_kernel, page_fork_units_kernel, s, p);
 }
 
 extern "C" int db_page_extend(const db_page_tables* t, const db_page_grow* req, uint32_t n,
@@ -905,7 +1036,11 @@ extern "C" int db_page_extend(const db_page_tables* t, const db_page_grow* req, 
   p.n_moves = n_moves;
   p.status = status;
   p.ctr = ctr;
-  return launch_team(page_extend_kernel, team_size(), s, p);
+  const uint64_t pages = (uint64_t)n * t->columns < t->n_pages ? (uint64_t)n * t->columns : t->n_pages;
+  const uint32_t ctas = team_size(n, (t->n_pages + 31) / 32, 0);
+  const int e = launch_team(page_extend_kernel, ctas, s, p);
+  if (e || pages <= (uint64_t)kOwn * ctas * kTeamThreads) return e;
+  return launch_dependent(page_place_kernel, whole_grid(pages), 256, 0, s, p);
 }
 
 extern "C" int db_page_compact(const db_page_tables* t, const db_page_tables* out,
@@ -927,9 +1062,9 @@ extern "C" int db_page_compact(const db_page_tables* t, const db_page_tables* ou
   p.n_moves = n_moves;
   p.ctr = ctr;
   const cudaStream_t s = (cudaStream_t)stream;
-  const int e = launch_team(page_compact_plan_kernel, team_size(), s, p);
+  const int e = launch_team(page_compact_plan_kernel, team_size(0, (t->n_pages + 31) / 32, 0), s, p);
   if (e) return e;
   const uint64_t entries = (uint64_t)t->n_seqs * t->columns;
   return launch_dependent(page_compact_apply_kernel,
-                          entry_grid(entries > t->n_pages ? entries : t->n_pages), 256, 0, s, p);
+                          whole_grid(entries > t->n_pages ? entries : t->n_pages), 256, 0, s, p);
 }
