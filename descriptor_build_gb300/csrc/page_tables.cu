@@ -21,19 +21,18 @@ namespace {
 
 constexpr uint32_t kTeamThreads = 1024;
 constexpr uint32_t kTeamWarps = kTeamThreads / 32;
-#ifndef DB_PAGE_TEAM
-#define DB_PAGE_TEAM 8
-#endif
-constexpr uint32_t kMaxTeam = DB_PAGE_TEAM;  // CTAs of the largest team
-constexpr uint32_t kSearch = 4096;     // prefix entries kept in shared memory
-constexpr uint32_t kRows = 8;          // requests of a group (see free_units)
+constexpr uint32_t kMaxTeam = 8;       // CTAs of the largest team
+constexpr uint32_t kSearch = 1024;     // starts kept in shared memory, the others are near one
+constexpr uint32_t kRows = 8;          // requests of a group (see "row units")
+constexpr uint32_t kSoloWords = 2048;  // free words of a team of one CTA
+// What a team does itself when a second kernel is there for the rest: units of
+// rows for each of its CTAs, pages for each of its threads. The second kernel
+// is launched when the sizes of the call allow for more than kRest of them.
+constexpr uint32_t kOwnUnits = 8, kOwnPages = 4;
+constexpr uint32_t kRestUnits = 64, kRestPages = 16384;
 constexpr uint32_t kNoMove = 0xFFFFFFFFu;
 constexpr uint32_t kNoEntry = 0xFFFFFFFEu;   // a row without an entry in the column
 constexpr uint32_t kBadEntry = 0xFFFFFFFFu;  // no page
-#ifndef DB_PAGE_OWN
-#define DB_PAGE_OWN 4
-#endif
-constexpr uint32_t kOwn = DB_PAGE_OWN;  // what a warp (unit) or thread (page) of the team does itself
 
 // One request's place in the plan.
 struct __align__(16) Plan {
@@ -48,6 +47,7 @@ struct Head {
   uint32_t moved;      // compact: moves made
   uint32_t dst_last;   // compact: the last page moved to (with moved > 0)
   uint32_t src_first;  // compact: the lowest page moved from, or n_pages
+  uint32_t holes;      // compact: free pages below the number of live ones
 };
 
 struct Work {
@@ -58,7 +58,8 @@ struct Work {
   Plan* plan;         // [n_seqs]
   uint2* group;       // [n_seqs / kRows] {units before it, its first column}
   uint32_t* before;   // [n_words] free pages before each word
-  uint32_t* pages;    // [n_pages] extend: the pages taken, by rank; compact: where a moved page went
+  uint32_t* bits;     // [n_words] extend: the free words before the call
+  uint32_t* renamed;  // [n_pages] compact: where a moved page went
 };
 
 inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -77,8 +78,10 @@ size_t carve(char* ws, uint32_t n_seqs, uint32_t n_pages, Work* w) {
   x.latest = (uint32_t*)take(4 * (size_t)n_pages);
   x.plan = (Plan*)take(16 * (size_t)n_seqs);
   x.group = (uint2*)take(8 * (((size_t)n_seqs + kRows - 1) / kRows));
-  x.before = (uint32_t*)take(4 * (((size_t)n_pages + 31) / 32));
-  x.pages = (uint32_t*)take(4 * (size_t)n_pages);
+  const size_t words = ((size_t)n_pages + 31) / 32;
+  x.before = (uint32_t*)take(4 * words);
+  x.bits = (uint32_t*)take(4 * words);
+  x.renamed = (uint32_t*)take(4 * (size_t)n_pages);
   if (w) *w = x;
   return at;
 }
@@ -109,16 +112,18 @@ struct TeamShared {
   uint32_t base_b, total_b;
 };
 
+// kSolo: the team is one CTA.
+template <bool kSolo>
 struct Team {
   uint32_t rank, size, round;
   TeamShared* s;
   __device__ __forceinline__ explicit Team(TeamShared* sh)
-      : rank(cluster_rank()), size(cluster_size()), round(0), s(sh) {}
+      : rank(kSolo ? 0 : cluster_rank()), size(kSolo ? 1 : cluster_size()), round(0), s(sh) {}
   __device__ __forceinline__ uint32_t id() const { return rank * kTeamThreads + threadIdx.x; }
   __device__ __forceinline__ uint32_t threads() const { return size * kTeamThreads; }
   // Barrier of the team; global and shared writes before it are seen after it.
   __device__ __forceinline__ void sync() const {
-    if (size == 1) {
+    if (kSolo) {
       __syncthreads();
     } else {
       asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
@@ -172,7 +177,7 @@ struct Team {
       }
     }
     sync();
-    if (size > 1) {
+    if (!kSolo) {
       if (warp == 0) {
         uint64_t pa = 0;
         uint32_t pb = 0;
@@ -210,8 +215,9 @@ struct Team {
 // no CTA leaves before its peers have read it.
 
 // ---------------------------------------------------------- finding a piece
-// The last i with start(i) <= e, where start is not decreasing: every
-// `step`-th start is in shared memory, all of them up to kSearch.
+// The last i < n with start(i) <= e, where start does not decrease: every
+// `step`-th start is in shared memory (all of them up to kSearch), and those
+// between two of them lie in a line or two of memory.
 struct Finder {
   const uint32_t* s_start;
   uint32_t n, kept, step;
@@ -234,21 +240,29 @@ struct Finder {
   }
 };
 
-// Load the starts (every thread of a CTA; ends past a barrier).
+__device__ __forceinline__ Finder finder_of(const uint32_t* s_start, uint32_t n) {
+  const uint32_t step = (n + kSearch - 1) / kSearch;
+  return Finder{s_start, n, (n + step - 1) / step, step};
+}
+
+// Load the starts (every thread of a CTA; a barrier has to follow).
 template <typename Start>
 __device__ __forceinline__ Finder load_finder(uint32_t* s_start, uint32_t n, Start start) {
-  Finder f;
-  f.s_start = s_start;
-  f.n = n;
-  f.step = (n + kSearch - 1) / kSearch;
-  f.kept = (n + f.step - 1) / f.step;
+  const Finder f = finder_of(s_start, n);
   for (uint32_t k = threadIdx.x; k < f.kept; k += blockDim.x) s_start[k] = start(k * f.step);
-  __syncthreads();
   return f;
 }
 
+// What a team of one CTA keeps of its plan on chip instead of in the workspace.
+struct SoloPlan {
+  Plan plan[kTeamThreads];
+  uint2 group[kTeamThreads / kRows];
+};
+
+// The plan, in shared memory or in the workspace. (A team's barrier and the
+// wait for the kernel before order these after the stores of other CTAs.)
 __device__ __forceinline__ Plan ld_plan(const Plan* p) {
-  const uint4 v = __ldcg(reinterpret_cast<const uint4*>(p));
+  const uint4 v = *reinterpret_cast<const uint4*>(p);
   return Plan{v.x, v.y, v.z, v.w};
 }
 __device__ __forceinline__ void st_plan(Plan* p, const Plan& v) {
@@ -277,20 +291,64 @@ __device__ __forceinline__ uint32_t ld_word(const uint32_t* bits, uint32_t w, ui
   return v;
 }
 
-// Free pages before each word into `before`; returns their number.
-__device__ __forceinline__ uint32_t scan_free(Team& team, const uint32_t* bits, uint32_t n_pages,
-                                              uint32_t* before) {
-  const uint32_t words = (n_pages + 31) / 32;
-  uint32_t carry = 0;
-  for (uint32_t w0 = 0; w0 < words; w0 += team.threads()) {
-    const uint32_t w = w0 + team.id();
-    const uint32_t c = w < words ? __popc(ld_word(bits, w, n_pages)) : 0;
-    Sum total;
-    const Sum x = team.scan(Sum{c, 0}, &total);
-    if (w < words) before[w] = carry + (uint32_t)x.a;
-    carry += (uint32_t)total.a;
+// A thread's share of the free bits: `words` consecutive words from `first` on,
+// one where the team has a thread for each, else a multiple of four, of which
+// the first four stay in registers.
+struct Bits {
+  uint32_t first, words;
+  uint32_t before;  // free pages before them
+  uint32_t total;   // free pages of the cache
+  uint4 v;
+};
+
+template <bool kSolo>
+__device__ __forceinline__ Bits scan_free(Team<kSolo>& team, const uint32_t* bits,
+                                          uint32_t n_pages) {
+  const uint32_t all = (n_pages + 31) / 32, threads = team.threads();
+  Bits b;
+  b.words = all <= threads ? 1 : 4 * ((all + 4 * threads - 1) / (4 * threads));
+  b.first = team.id() * b.words;
+  b.v = make_uint4(0, 0, 0, 0);
+  uint32_t c = 0;
+  if (b.words == 1) {
+    if (b.first < all) b.v.x = ld_word(bits, b.first, n_pages);
+    c = __popc(b.v.x);
+  } else {
+    for (uint32_t s = 0; s < b.words && b.first + s < all; s += 4) {
+      const uint32_t w = b.first + s;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (w + 4 < all) {
+        v = __ldcg(reinterpret_cast<const uint4*>(bits + w));
+      } else {
+        v.x = ld_word(bits, w, n_pages);
+        if (w + 1 < all) v.y = ld_word(bits, w + 1, n_pages);
+        if (w + 2 < all) v.z = ld_word(bits, w + 2, n_pages);
+        if (w + 3 < all) v.w = ld_word(bits, w + 3, n_pages);
+      }
+      c += __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w);
+      if (s == 0) b.v = v;
+    }
   }
-  return carry;
+  Sum total;
+  b.before = (uint32_t)team.scan(Sum{c, 0}, &total).a;
+  b.total = (uint32_t)total.a;
+  return b;
+}
+
+// f(word's index, its free bits, free pages before it) for every word, by whole
+// warps (a lane without a word has no free bits and an index past the words).
+template <typename F>
+__device__ __forceinline__ void each_word(const Bits& b, const uint32_t* bits, uint32_t n_pages,
+                                          F f) {
+  const uint32_t all = (n_pages + 31) / 32;
+  uint32_t before = b.before;
+  for (uint32_t s = 0; s < b.words; ++s) {
+    const uint32_t w = b.first + s;
+    uint32_t v = s == 0 ? b.v.x : s == 1 ? b.v.y : s == 2 ? b.v.z : b.v.w;
+    if (s >= 4) v = w < all ? ld_word(bits, w, n_pages) : 0;
+    f(w, v, before);
+    before += __popc(v);
+  }
 }
 
 // A count and an error, one warp's at a time, into the counters.
@@ -315,13 +373,15 @@ struct Rows {
   db_counters* ctr;
   uint8_t* status;
   uint32_t n;
+  bool rest;  // a second kernel follows
   Work w;
 };
 
 // Each thread's columns into the groups; ends with every group of these
 // requests written (not yet visible to other CTAs). `carry`: units before.
-__device__ __forceinline__ void plan_rows(Team& team, const Rows& p, uint32_t i, const Plan& pl,
-                                          uint32_t* carry) {
+template <bool kSolo>
+__device__ __forceinline__ void plan_rows(Team<kSolo>& team, const Rows& p, SoloPlan* solo,
+                                          uint32_t i, const Plan& pl, uint32_t* carry) {
   uint32_t lo = pl.from < pl.end ? pl.from : 0xFFFFFFFFu, hi = pl.from < pl.end ? pl.end : 0;
 #pragma unroll
   for (uint32_t o = 1; o < kRows; o <<= 1) {
@@ -334,27 +394,49 @@ __device__ __forceinline__ void plan_rows(Team& team, const Rows& p, uint32_t i,
   Sum total;
   const Sum x = team.scan(Sum{first ? units : 0, 0}, &total);
   if (i < p.n) {
-    st_plan(&p.w.plan[i], pl);
-    if (first) p.w.group[i / kRows] = make_uint2(*carry + (uint32_t)x.a, lo);
+    const uint2 g = make_uint2(*carry + (uint32_t)x.a, lo);
+    st_plan(&p.w.plan[i], pl);  // for the second kernel, when there is one
+    if (first) p.w.group[i / kRows] = g;
+    if (kSolo) {
+      st_plan(&solo->plan[i], pl);
+      if (first) solo->group[i / kRows] = g;
+    }
   }
   *carry += (uint32_t)total.a;
 }
 
 struct GroupStart {
   const uint2* group;
-  __device__ __forceinline__ uint32_t operator()(uint32_t g) const { return __ldcg(&group[g].x); }
+  __device__ __forceinline__ uint32_t operator()(uint32_t g) const { return group[g].x; }
 };
 
-// The rows of unit u: lane j < kRows holds the j-th plan (empty if there is
-// none); returns this lane's column.
-__device__ __forceinline__ uint32_t load_unit(const Rows& p, const Finder& f, uint32_t u,
-                                              uint32_t lane, Plan* pl) {
-  const uint32_t g = f.find(u, GroupStart{p.w.group});
-  const uint2 at = __ldcg(&p.w.group[g]);
-  const uint32_t i = g * kRows + lane;
-  *pl = Plan{0, 0, 0, 0};
-  if (lane < kRows && i < p.n) *pl = ld_plan(&p.w.plan[i]);
-  return at.y + (u - at.x) * 32 + lane;
+// Where the units of a call are found.
+struct Units {
+  Finder f;
+  const Plan* plan;
+  const uint2* group;
+  uint32_t n;
+  // The rows of unit u: lane j < kRows holds the j-th plan (empty if there is
+  // none); returns this lane's column.
+  __device__ __forceinline__ uint32_t load(uint32_t u, uint32_t lane, Plan* pl) const {
+    const uint32_t g = f.find(u, GroupStart{group});
+    const uint2 at = group[g];
+    const uint32_t i = g * kRows + lane;
+    *pl = Plan{0, 0, 0, 0};
+    if (lane < kRows && i < n) *pl = ld_plan(&plan[i]);
+    return at.y + (u - at.x) * 32 + lane;
+  }
+};
+
+__device__ __forceinline__ Units find_units(const Rows& p, const Plan* plan, const uint2* group,
+                                            uint32_t* s_start) {
+  Units x;
+  x.plan = plan;
+  x.group = group;
+  x.n = p.n;
+  x.f = load_finder(s_start, (p.n + kRows - 1) / kRows, GroupStart{group});
+  __syncthreads();
+  return x;
 }
 
 // ---------------------------------------------------------------------- free
@@ -363,14 +445,14 @@ struct FreeParams {
   const db_page_cut* req;
 };
 
-__device__ __forceinline__ void free_units(const Rows& p, const Finder& f, uint32_t first,
+__device__ __forceinline__ void free_units(const Rows& p, const Units& x, uint32_t first,
                                            uint32_t stride, uint32_t units) {
   const uint32_t lane = threadIdx.x & 31;
   uint32_t released = 0;
   bool bad = false;
   for (uint32_t u = first; u < units; u += stride) {
     Plan pl;
-    const uint32_t c = load_unit(p, f, u, lane, &pl);
+    const uint32_t c = x.load(u, lane, &pl);
     uint32_t page[kRows];
     bool clear[kRows];
 #pragma unroll
@@ -388,10 +470,10 @@ __device__ __forceinline__ void free_units(const Rows& p, const Finder& f, uint3
       p.t.table[(uint64_t)row * p.t.columns + c] = DB_PAGE_NONE;
       if (page[j] == kNoEntry) page[j] = kBadEntry;
     }
-    uint32_t old[kRows], times[kRows];
+    uint32_t refs[kRows], times[kRows];
 #pragma unroll
     for (uint32_t j = 0; j < kRows; ++j) {
-      times[j] = 0;
+      times[j] = refs[j] = 0;
       if (page[j] == kNoEntry || (j && page[j] == page[j - 1])) continue;
       if (page[j] >= p.t.n_pages) {
         bad = true;
@@ -402,17 +484,24 @@ __device__ __forceinline__ void free_units(const Rows& p, const Finder& f, uint3
       for (uint32_t k = j + 1; k < kRows; ++k)
         if (run == k - j && page[k] == page[j]) ++run;
       times[j] = run;
-      old[j] = atomicSub(&p.t.refs[page[j]], run);
+      refs[j] = __ldcg(&p.t.refs[page[j]]);
     }
+    // References that are down to these rows' are nobody else's to drop, in
+    // this call or before: a store does, and most pages have one reference.
 #pragma unroll
     for (uint32_t j = 0; j < kRows; ++j) {
       if (!times[j]) continue;
-      if (old[j] == times[j]) {
+      bool last = refs[j] == times[j];
+      if (last) {
+        p.t.refs[page[j]] = 0;
+      } else if (refs[j] > times[j]) {
+        last = atomicSub(&p.t.refs[page[j]], times[j]) == times[j];
+      } else {  // more rows than references
+        bad = true;
+      }
+      if (last) {
         atomicOr(&p.t.free[page[j] >> 5], 1u << (page[j] & 31));
         ++released;
-      } else if (old[j] < times[j]) {  // more rows than references: leave them as they were
-        atomicAdd(&p.t.refs[page[j]], times[j]);
-        bad = true;
       }
     }
   }
@@ -422,13 +511,15 @@ __device__ __forceinline__ void free_units(const Rows& p, const Finder& f, uint3
   }
 }
 
+template <bool kSolo>
 __global__ void __launch_bounds__(kTeamThreads) page_free_kernel(const FreeParams q) {
   __shared__ TeamShared s_team;
-  __shared__ uint32_t s_start[kSearch];
+  __shared__ SoloPlan s_plan;
+  __shared__ uint32_t s_start[kSolo ? kTeamThreads / kRows : kSearch];
   const Rows& p = q.r;
   wait_for_prerequisites();
   dependents_may_launch();
-  Team team(&s_team);
+  Team<kSolo> team(&s_team);
   if (p.ctr && team.id() == 0) *p.ctr = db_counters{0, 0, 0, 0};
   for (uint32_t i = team.id(); i < p.n; i += team.threads()) {
     const uint32_t seq = q.req[i].seq;
@@ -454,15 +545,16 @@ __global__ void __launch_bounds__(kTeamThreads) page_free_kernel(const FreeParam
       invalid += !ok;
       if (p.status) p.status[i] = ok ? DB_PAGE_OK : DB_PAGE_INVALID;
     }
-    plan_rows(team, p, i, pl, &units);
+    plan_rows(team, p, &s_plan, i, pl, &units);
   }
   if (p.ctr) add_count(&p.ctr->n_invalid, invalid);
-  const bool own = units <= kOwn * (team.threads() / 32);
+  const bool own = !p.rest || units <= kOwnUnits * team.size;
   if (team.id() == 0) p.w.head->units = own ? 0 : units;
   team.sync();
   if (!own || !units) return;
-  const Finder f = load_finder(s_start, (p.n + kRows - 1) / kRows, GroupStart{p.w.group});
-  free_units(p, f, team.id() / 32, team.threads() / 32, units);
+  const Units x = find_units(p, kSolo ? s_plan.plan : p.w.plan, kSolo ? s_plan.group : p.w.group,
+                             s_start);
+  free_units(p, x, team.id() / 32, team.threads() / 32, units);
 }
 
 __global__ void __launch_bounds__(256) page_free_units_kernel(const FreeParams q) {
@@ -472,8 +564,8 @@ __global__ void __launch_bounds__(256) page_free_units_kernel(const FreeParams q
   dependents_may_launch();
   const uint32_t units = __ldcg(&p.w.head->units);
   if (blockIdx.x * 8 >= units) return;
-  const Finder f = load_finder(s_start, (p.n + kRows - 1) / kRows, GroupStart{p.w.group});
-  free_units(p, f, blockIdx.x * 8 + threadIdx.x / 32, gridDim.x * 8, units);
+  const Units x = find_units(p, p.w.plan, p.w.group, s_start);
+  free_units(p, x, blockIdx.x * 8 + threadIdx.x / 32, gridDim.x * 8, units);
 }
 
 // ---------------------------------------------------------------------- fork
@@ -482,13 +574,13 @@ struct ForkParams {
   const db_page_fork_req* req;
 };
 
-__device__ __forceinline__ void fork_units(const Rows& p, const Finder& f, uint32_t first,
+__device__ __forceinline__ void fork_units(const Rows& p, const Units& x, uint32_t first,
                                            uint32_t stride, uint32_t units) {
   const uint32_t lane = threadIdx.x & 31;
   bool bad = false;
   for (uint32_t u = first; u < units; u += stride) {
     Plan pl;
-    const uint32_t c = load_unit(p, f, u, lane, &pl);
+    const uint32_t c = x.load(u, lane, &pl);
     uint32_t page[kRows];
 #pragma unroll
     for (uint32_t j = 0; j < kRows; ++j) {
@@ -517,13 +609,15 @@ __device__ __forceinline__ void fork_units(const Rows& p, const Finder& f, uint3
   if (p.ctr) add_error(p.ctr, bad);
 }
 
+template <bool kSolo>
 __global__ void __launch_bounds__(kTeamThreads) page_fork_kernel(const ForkParams q) {
   __shared__ TeamShared s_team;
-  __shared__ uint32_t s_start[kSearch];
+  __shared__ SoloPlan s_plan;
+  __shared__ uint32_t s_start[kSolo ? kTeamThreads / kRows : kSearch];
   const Rows& p = q.r;
   wait_for_prerequisites();
   dependents_may_launch();
-  Team team(&s_team);
+  Team<kSolo> team(&s_team);
   if (p.ctr && team.id() == 0) *p.ctr = db_counters{0, 0, 0, 0};
   for (uint32_t i = team.id(); i < p.n; i += team.threads()) {
     const uint32_t child = q.req[i].child;
@@ -550,7 +644,7 @@ __global__ void __launch_bounds__(kTeamThreads) page_fork_kernel(const ForkParam
       invalid += !ok;
       if (p.status) p.status[i] = ok ? DB_PAGE_OK : DB_PAGE_INVALID;
     }
-    plan_rows(team, p, i, pl, &units);
+    plan_rows(team, p, &s_plan, i, pl, &units);
   }
   if (p.ctr) {
     add_count(&p.ctr->n_invalid, invalid);
@@ -558,16 +652,18 @@ __global__ void __launch_bounds__(kTeamThreads) page_fork_kernel(const ForkParam
     if ((threadIdx.x & 31) == 0 && c)
       atomicAdd((unsigned long long*)&p.ctr->total, (unsigned long long)c);
   }
-  const bool own = units <= kOwn * (team.threads() / 32);
+  const bool own = !p.rest || units <= kOwnUnits * team.size;
   if (team.id() == 0) p.w.head->units = own ? 0 : units;
-  team.sync();  // every length is read
+  // every length was read before the last scan
   for (uint32_t i = team.id(); i < p.n; i += team.threads()) {
-    const uint32_t row = p.w.plan[i].row;
+    const uint32_t row = kSolo ? s_plan.plan[i].row : p.w.plan[i].row;
     if (row != kNoMove) p.t.length[row] = q.req[i].tokens;
   }
+  team.sync();
   if (!own || !units) return;
-  const Finder f = load_finder(s_start, (p.n + kRows - 1) / kRows, GroupStart{p.w.group});
-  fork_units(p, f, team.id() / 32, team.threads() / 32, units);
+  const Units x = find_units(p, kSolo ? s_plan.plan : p.w.plan, kSolo ? s_plan.group : p.w.group,
+                             s_start);
+  fork_units(p, x, team.id() / 32, team.threads() / 32, units);
 }
 
 __global__ void __launch_bounds__(256) page_fork_units_kernel(const ForkParams q) {
@@ -577,8 +673,8 @@ __global__ void __launch_bounds__(256) page_fork_units_kernel(const ForkParams q
   dependents_may_launch();
   const uint32_t units = __ldcg(&p.w.head->units);
   if (blockIdx.x * 8 >= units) return;
-  const Finder f = load_finder(s_start, (p.n + kRows - 1) / kRows, GroupStart{p.w.group});
-  fork_units(p, f, blockIdx.x * 8 + threadIdx.x / 32, gridDim.x * 8, units);
+  const Units x = find_units(p, p.w.plan, p.w.group, s_start);
+  fork_units(p, x, blockIdx.x * 8 + threadIdx.x / 32, gridDim.x * 8, units);
 }
 
 // -------------------------------------------------------------------- extend
@@ -590,6 +686,7 @@ struct ExtendParams {
   uint32_t* n_moves;
   uint8_t* status;
   db_counters* ctr;
+  bool rest;  // a second kernel follows
   Work w;
 };
 
@@ -611,40 +708,63 @@ __device__ __forceinline__ Ask ask(const ExtendParams& p, uint32_t i) {
   const db_page_grow r = p.req[i];
   a.seq = r.seq;
   if (r.seq >= p.t.n_seqs) return a;
-  const uint32_t len = p.t.length[r.seq];
-  a.mine = claimed(p.w.claim, r.seq, i);
+  const uint32_t len = p.t.length[r.seq], of = __ldcg(&p.w.claim[r.seq]);
   const uint64_t now = (uint64_t)len + r.tokens;
-  if (!a.mine || now > (uint64_t)p.t.columns * p.t.page_tokens || now > 0xFFFFFFFFull) return a;
-  a.ok = true;
-  a.now = (uint32_t)now;
-  a.had = pages_of(len, p.t.page_tokens);
-  a.grow = pages_of(now, p.t.page_tokens) - a.had;
-  const uint32_t part = len % p.t.page_tokens;
-  if (r.tokens && part) {
-    a.last = (uint32_t)p.t.table[(uint64_t)r.seq * p.t.columns + a.had - 1];
-    if (a.last >= p.t.n_pages) {
-      a.ok = false;
-      a.corrupt = true;
-      a.grow = 0;
-    } else {
-      a.refs = __ldcg(&p.t.refs[a.last]);
-      a.part = part;
-    }
+  const bool fits = now <= (uint64_t)p.t.columns * p.t.page_tokens && now <= 0xFFFFFFFFull;
+  const uint32_t had = pages_of(len, p.t.page_tokens), part = len % p.t.page_tokens;
+  // its page is looked up before it is known whose sequence it is
+  uint32_t last = 0, refs = 0;
+  if (fits && r.tokens && part) {
+    last = (uint32_t)p.t.table[(uint64_t)r.seq * p.t.columns + had - 1];
+    if (last < p.t.n_pages) refs = __ldcg(&p.t.refs[last]);
   }
+  a.mine = of == 0xFFFFFFFFu - i;
+  if (!a.mine || !fits) return a;
+  a.corrupt = last >= p.t.n_pages;
+  a.ok = !a.corrupt;
+  if (!a.ok) return a;
+  a.now = (uint32_t)now;
+  a.had = had;
+  a.grow = pages_of(now, p.t.page_tokens) - had;
+  if (r.tokens) a.part = part;
+  a.last = last;
+  a.refs = refs;
   return a;
 }
 
 struct PlanStart {
   const Plan* plan;
-  __device__ __forceinline__ uint32_t operator()(uint32_t i) const { return __ldcg(&plan[i].end); }
+  __device__ __forceinline__ uint32_t operator()(uint32_t i) const { return plan[i].end; }
+};
+struct WordStart {
+  const uint32_t* before;
+  __device__ __forceinline__ uint32_t operator()(uint32_t w) const { return before[w]; }
 };
 
-// Page e of the batch into its row.
-__device__ __forceinline__ void place_pages(const ExtendParams& p, const Finder& f, uint32_t first,
-                                            uint32_t stride, uint32_t total) {
+// The j-th set bit (from 0) of v.
+__device__ __forceinline__ uint32_t nth_bit(uint32_t v, uint32_t j) {
+  uint32_t at = 0;
+#pragma unroll
+  for (uint32_t half = 16; half; half >>= 1) {
+    const uint32_t c = __popc(v & ((1u << half) - 1));
+    if (j >= c) {
+      j -= c;
+      at += half;
+      v >>= half;
+    }
+  }
+  return at;
+}
+
+// Page e of the batch: the e-th free one, into the row it is for.
+__device__ __forceinline__ void place_pages(const ExtendParams& p, const Finder& request,
+                                            const Plan* plan, const Finder& word,
+                                            const uint32_t* before, const uint32_t* bits,
+                                            uint32_t first, uint32_t stride, uint32_t total) {
   for (uint32_t e = first; e < total; e += stride) {
-    const uint32_t page = __ldcg(&p.w.pages[e]);
-    const Plan pl = ld_plan(&p.w.plan[f.find(e, PlanStart{p.w.plan})]);
+    const uint32_t w = word.find(e, WordStart{before});
+    const uint32_t page = 32 * w + nth_bit(bits[w], e - before[w]);
+    const Plan pl = ld_plan(&plan[request.find(e, PlanStart{plan})]);
     const uint32_t j = e - pl.end;
     p.t.table[(uint64_t)pl.row * p.t.columns + pl.from + j] = (int32_t)page;
     p.t.refs[page] = 1;
@@ -652,65 +772,107 @@ __device__ __forceinline__ void place_pages(const ExtendParams& p, const Finder&
   }
 }
 
+template <bool kSolo>
 __global__ void __launch_bounds__(kTeamThreads) page_extend_kernel(const ExtendParams p) {
   __shared__ TeamShared s_team;
-  __shared__ uint32_t s_start[kSearch];
+  __shared__ uint32_t s_start[kSolo ? kTeamThreads : kSearch], s_word[kSearch];
+  __shared__ Plan s_plan[kSolo ? kTeamThreads : 1];
+  __shared__ uint32_t s_before[kSolo ? kSoloWords : 1], s_bits[kSolo ? kSoloWords : 1];
   wait_for_prerequisites();
   dependents_may_launch();
-  Team team(&s_team);
+  Team<kSolo> team(&s_team);
   const uint32_t id = team.id(), threads = team.threads();
-  const bool one = p.n <= threads;  // every request has a thread: asked once, kept in registers
+  const uint32_t words = (p.t.n_pages + 31) / 32;
+  const bool one = kSolo || p.n <= threads;  // a thread for every request, which asks once
   if (p.ctr && id == 0) *p.ctr = db_counters{0, 0, 0, 0};
   for (uint32_t i = id; i < p.n; i += threads) {
     const uint32_t seq = p.req[i].seq;
     if (seq < p.t.n_seqs) claim(p.w.claim, seq, i);
   }
-  const uint32_t avail = scan_free(team, p.t.free, p.t.n_pages, p.w.before);
-  team.sync();
-  // How many of the batch's requests hold each shared page, and the last of them.
+  const Bits bits = scan_free(team, p.t.free, p.t.n_pages);  // its barrier is the claims'
+  // How many of the batch's requests hold each shared page, and the last of
+  // them; requests of a warp that hold the same one (samples of one prompt)
+  // count together.
   Ask a = {0, 0, 0, 0, 0, 0, 0, false, false, false};
-  for (uint32_t i = id; i < p.n; i += threads) {
+  bool shares = false;
+  for (uint32_t i0 = 0; i0 < p.n; i0 += threads) {
+    const uint32_t i = i0 + id;
     a = ask(p, i);
     if (a.shares()) {
-      atomicAdd(&p.w.holders[a.last], 1u);
-      atomicMax(&p.w.latest[a.last], i);
+      shares = true;
+      const uint32_t same = __match_any_sync(__activemask(), a.last);
+      if ((same & lanemask_lt()) == 0) {
+        atomicAdd(&p.w.holders[a.last], (uint32_t)__popc(same));
+        atomicMax(&p.w.latest[a.last], i + (31 - __clz(same)) - (threadIdx.x & 31));
+      }
     }
   }
-  team.sync();
+  if (kSolo) shares = __syncthreads_or(shares); else team.sync();
   uint64_t need = 0;
   uint32_t n_moves = 0;
   for (uint32_t i0 = 0; i0 < p.n; i0 += threads) {
     const uint32_t i = i0 + id;
     if (!one) a = ask(p, i);
-    const uint32_t cow = a.shares() && !(__ldcg(&p.w.holders[a.last]) == a.refs &&
-                                     __ldcg(&p.w.latest[a.last]) == i);
+    uint32_t cow = 0;
+    if ((!kSolo || shares) && a.shares())
+      cow = !(__ldcg(&p.w.holders[a.last]) == a.refs && __ldcg(&p.w.latest[a.last]) == i);
     Sum total;
     const Sum x = team.scan(Sum{(uint64_t)a.grow + cow, cow}, &total);
-    if (i < p.n)
-      st_plan(&p.w.plan[i], Plan{a.seq, a.had - cow, (uint32_t)min(need + x.a, (uint64_t)0xFFFFFFFFu),
-                                 cow ? n_moves + x.b : kNoMove});
+    if (i < p.n) {
+      const Plan pl = {a.seq, a.had - cow, (uint32_t)min(need + x.a, (uint64_t)0xFFFFFFFFu),
+                       cow ? n_moves + x.b : kNoMove};
+      st_plan(&p.w.plan[i], pl);
+      if (kSolo) {
+        st_plan(&s_plan[i], pl);
+        s_start[i] = pl.end;
+      }
+    }
     need += total.a;
     n_moves += total.b;
   }
-  const bool go = need <= avail;
-  const bool own = need <= (uint64_t)kOwn * threads;
+  const bool go = need <= bits.total;
+  const bool own = !p.rest || need <= (uint64_t)kOwnPages * threads;
   if (id == 0) {
     *p.n_moves = go ? n_moves : 0;
     p.w.head->units = go && !own ? (uint32_t)need : 0;
     if (p.ctr) p.ctr->total = need;
   }
-  team.sync();
-  // Lengths, moves and status, and the workspace as the next call wants it.
+  // The words as they were, to find the pages in, and without those taken.
+  if (go && need) {
+    const uint32_t stop = (uint32_t)need;
+    const Finder f = finder_of(s_word, words);
+    each_word(bits, p.t.free, p.t.n_pages, [&](uint32_t w, uint32_t free, uint32_t before) {
+      if (w >= words) return;
+      if (kSolo) {
+        s_before[w] = before;
+        s_bits[w] = free;
+        if (w % f.step == 0) s_word[w / f.step] = before;
+      }
+      if (!kSolo || !own) {
+        p.w.before[w] = before;
+        p.w.bits[w] = free;
+      }
+      if (free && before < stop) {
+        uint32_t left = 0;
+        if (before + __popc(free) > stop)
+          left = free & ~((2u << nth_bit(free, stop - before - 1)) - 1);
+        p.t.free[w] = left;
+      }
+    });
+  }
+  // Every request has been asked before the last scan. Lengths, moves and
+  // status, and the workspace as the next call wants it.
   uint32_t invalid = 0, refused = 0;
   bool corrupt = false;
   for (uint32_t i = id; i < p.n; i += threads) {
     if (!one) a = ask(p, i);
-    const uint32_t m = p.w.plan[i].aux;
+    const uint32_t m = kSolo ? s_plan[i].aux : p.w.plan[i].aux;
     if (m != kNoMove) {  // at least one holder of every shared page copies, and clears for all
       p.w.holders[a.last] = 0;
       p.w.latest[a.last] = 0;
       if (go) {
-        atomicSub(&p.t.refs[a.last], 1u);
+        const uint32_t same = __match_any_sync(__activemask(), a.last);
+        if ((same & lanemask_lt()) == 0) atomicSub(&p.t.refs[a.last], (uint32_t)__popc(same));
         p.moves[m].src = a.last;
         *reinterpret_cast<uint2*>(&p.moves[m].tokens) = make_uint2(a.part, 0);
       }
@@ -727,41 +889,30 @@ __global__ void __launch_bounds__(kTeamThreads) page_extend_kernel(const ExtendP
     add_count(&p.ctr->n_overflow, refused);
     add_error(p.ctr, corrupt);
   }
-  if (!go || need == 0) return;
-  // The pages taken, by rank: a word at a time, a page per lane.
-  const uint32_t lane = threadIdx.x & 31, words = (p.t.n_pages + 31) / 32;
-  for (uint32_t w0 = id - lane; w0 < words; w0 += threads) {
-    const uint32_t w = w0 + lane;
-    const uint32_t rank = w < words ? __ldcg(&p.w.before[w]) : 0xFFFFFFFFu;
-    const uint32_t bits = w < words ? ld_word(p.t.free, w, p.t.n_pages) : 0;
-    uint32_t active = __ballot_sync(kFull, bits && rank < need);
-    uint32_t left = bits;
-    while (active) {
-      const uint32_t k = __ffs(active) - 1;
-      active &= active - 1;
-      const uint32_t v = __shfl_sync(kFull, bits, k);
-      const uint32_t e = __shfl_sync(kFull, rank, k) + __popc(v & lanemask_lt());
-      const bool mine = (v >> lane & 1) && e < need;
-      const uint32_t taken = __ballot_sync(kFull, mine);
-      if (mine) p.w.pages[e] = (w0 + k) * 32 + lane;
-      if (lane == k) left &= ~taken;
-    }
-    if (left != bits) p.t.free[w] = left;
+  team.sync();  // plan and words are known, and the replaced entries have been read
+  if (!go || !need || !own) return;
+  if (kSolo) {
+    place_pages(p, Finder{s_start, p.n, p.n, 1}, s_plan, finder_of(s_word, words), s_before, s_bits,
+                id, threads, (uint32_t)need);
+  } else {
+    const Finder r = load_finder(s_start, p.n, PlanStart{p.w.plan});
+    const Finder f = load_finder(s_word, words, WordStart{p.w.before});
+    __syncthreads();
+    place_pages(p, r, p.w.plan, f, p.w.before, p.w.bits, id, threads, (uint32_t)need);
   }
-  team.sync();  // the pages are known, and the replaced entries have been read
-  if (!own) return;
-  const Finder f = load_finder(s_start, p.n, PlanStart{p.w.plan});
-  place_pages(p, f, id, threads, (uint32_t)need);
 }
 
 __global__ void __launch_bounds__(256) page_place_kernel(const ExtendParams p) {
-  __shared__ uint32_t s_start[kSearch];
+  __shared__ uint32_t s_start[kSearch], s_word[kSearch];
   wait_for_prerequisites();
   dependents_may_launch();
-  const uint32_t total = __ldcg(&p.w.head->units);
+  const uint32_t total = p.w.head->units;
   if (blockIdx.x * 256 >= total) return;
-  const Finder f = load_finder(s_start, p.n, PlanStart{p.w.plan});
-  place_pages(p, f, blockIdx.x * 256 + threadIdx.x, gridDim.x * 256, total);
+  const Finder r = load_finder(s_start, p.n, PlanStart{p.w.plan});
+  const Finder f = load_finder(s_word, (p.t.n_pages + 31) / 32, WordStart{p.w.before});
+  __syncthreads();
+  place_pages(p, r, p.w.plan, f, p.w.before, p.w.bits, blockIdx.x * 256 + threadIdx.x,
+              gridDim.x * 256, total);
 }
 
 // ------------------------------------------------------------------- compact
@@ -774,23 +925,33 @@ struct CompactParams {
   Work w;
 };
 
+// Live pages before a word.
+struct LiveStart {
+  const uint32_t* before;
+  __device__ __forceinline__ uint32_t operator()(uint32_t w) const { return 32 * w - before[w]; }
+};
+
+template <bool kSolo>
 __global__ void __launch_bounds__(kTeamThreads) page_compact_plan_kernel(const CompactParams p) {
   __shared__ TeamShared s_team;
+  __shared__ uint32_t s_word[kSearch], s_live[kSearch];
   wait_for_prerequisites();
   dependents_may_launch();
-  Team team(&s_team);
+  Team<kSolo> team(&s_team);
   const uint32_t id = team.id(), threads = team.threads();
   const uint32_t n_pages = p.t.n_pages, words = (n_pages + 31) / 32;
-  const uint32_t n_live = n_pages - scan_free(team, p.t.free, n_pages, p.w.before);
+  const Bits bits = scan_free(team, p.t.free, n_pages);
+  const uint32_t n_live = n_pages - bits.total;
+  // M, the free pages below n_live: known to the thread that has the word.
+  each_word(bits, p.t.free, n_pages, [&](uint32_t w, uint32_t free, uint32_t before) {
+    if (w >= words) return;
+    p.w.before[w] = before;
+    if (w == n_live / 32)
+      p.w.head->holes = before + __popc(free & ((1u << (n_live & 31)) - 1));
+  });
+  if (n_live == n_pages && id == 0) p.w.head->holes = 0;
   team.sync();
-  // M: the free pages below n_live.
-  uint32_t holes = 0;
-  if (n_live < n_pages) {
-    const uint32_t w = n_live / 32;
-    holes = __ldcg(&p.w.before[w]) +
-            __popc(ld_word(p.t.free, w, n_pages) & ((1u << (n_live & 31)) - 1));
-  }
-  const uint32_t moved = min(holes, p.cap);
+  const uint32_t holes = __ldcg(&p.w.head->holes), moved = min(holes, p.cap);
   if (id == 0) {
     *p.n_moves = moved;
     p.w.head->moved = moved;
@@ -800,47 +961,24 @@ __global__ void __launch_bounds__(kTeamThreads) page_compact_plan_kernel(const C
     }
     if (p.ctr) *p.ctr = db_counters{holes, 0, (uint64_t)holes - moved, 0};
   }
-  const uint32_t lane = threadIdx.x & 31;
-  for (uint32_t w0 = id - lane; w0 < words && moved; w0 += threads) {
-    const uint32_t w = w0 + lane, first = 32 * w;
-    const uint32_t bits = w < words ? ld_word(p.t.free, w, n_pages) : 0;
-    const uint32_t before = w < words ? __ldcg(&p.w.before[w]) : 0;
-    // free pages below n_live to move to, or live pages from n_live on to move from
-    bool use = false;
-    if (w < words) {
-      if (first < n_live) use = bits && before < moved;
-      if (first + 31 >= n_live) use |= bits != kFull;
-    }
-    uint32_t active = __ballot_sync(kFull, use);
-    while (active) {
-      const uint32_t k = __ffs(active) - 1;
-      active &= active - 1;
-      const uint32_t v = __shfl_sync(kFull, bits, k);
-      const uint32_t page = (w0 + k) * 32 + lane;
-      const uint32_t rank = __shfl_sync(kFull, before, k) + __popc(v & lanemask_lt());
-      if (page < n_pages) {
-        if (v >> lane & 1) {
-          if (page < n_live && rank < moved) {
-            p.moves[rank].dst = page;
-            *reinterpret_cast<uint2*>(&p.moves[rank].tokens) = make_uint2(DB_PAGE_ALL, 0);
-            if (rank == moved - 1) p.w.head->dst_last = page;
-          }
-        } else if (page >= n_live) {
-          const uint32_t top = n_live - 1 - (page - rank);  // live pages above it
-          if (top < moved) {
-            p.moves[top].src = page;
-            if (top == moved - 1) p.w.head->src_first = page;
-          }
-        }
-      }
-    }
-  }
-  team.sync();
+  if (!moved) return;
+  const Finder f = load_finder(s_word, words, WordStart{p.w.before});
+  const Finder g = load_finder(s_live, words, LiveStart{p.w.before});
+  __syncthreads();
   for (uint32_t k = id; k < moved; k += threads) {
-    const uint2 m = __ldcg(reinterpret_cast<const uint2*>(&p.moves[k]));
-    p.w.pages[m.x] = m.y;
-    p.out.refs[m.y] = p.t.refs[m.x];
-    p.out.refs[m.x] = 0;
+    // the k-th free page, and the k-th live one from above
+    const uint32_t v = f.find(k, WordStart{p.w.before});
+    const uint32_t dst = 32 * v + nth_bit(ld_word(p.t.free, v, n_pages), k - p.w.before[v]);
+    const uint32_t e = n_live - 1 - k, w = g.find(e, LiveStart{p.w.before});
+    const uint32_t src = 32 * w + nth_bit(~ld_word(p.t.free, w, n_pages), e - (32 * w - p.w.before[w]));
+    *reinterpret_cast<uint4*>(&p.moves[k]) = make_uint4(src, dst, DB_PAGE_ALL, 0);
+    p.w.renamed[src] = dst;
+    p.out.refs[dst] = p.t.refs[src];
+    p.out.refs[src] = 0;
+    if (k == moved - 1) {
+      p.w.head->dst_last = dst;
+      p.w.head->src_first = src;
+    }
   }
 }
 
@@ -857,7 +995,7 @@ __global__ void __launch_bounds__(256) page_compact_apply_kernel(const CompactPa
     const uint32_t was = (uint32_t)p.t.table[e];
     uint32_t is = was;
     if (was >= src_first && was != (uint32_t)DB_PAGE_NONE) {
-      if (was < n_pages) is = __ldcg(&p.w.pages[was]); else bad = true;
+      if (was < n_pages) is = __ldcg(&p.w.renamed[was]); else bad = true;
     }
     if (p.out.table != p.t.table || is != was) p.out.table[e] = (int32_t)is;
   }
@@ -948,30 +1086,28 @@ int nothing(db_counters* ctr, uint32_t* n_moves, cudaStream_t s) {
   return 0;
 }
 
-// CTAs of the team for `n` requests, `words` of free bits and at most `units`
-// pieces of a warp's work.
-uint32_t team_size(uint64_t n, uint64_t words, uint64_t units) {
-  uint64_t want = n > words ? n : words;
-  if (units * 32 / kOwn > want) want = units * 32 / kOwn;
+// CTAs of a team that wants `threads`.
+uint32_t team_size(uint64_t threads) {
   uint32_t c = 1;
-  while (c < kMaxTeam && (uint64_t)c * kTeamThreads < want) c *= 2;
+  while (c < kMaxTeam && (uint64_t)c * kTeamThreads < threads) c *= 2;
   return c;
 }
+inline uint64_t most_of(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
 // CTAs of 256 threads for at most `threads`.
 unsigned whole_grid(uint64_t threads) {
-  const uint64_t want = (threads + 255) / 256, most = 8ull * num_sms();
+  const uint64_t want = (threads + 255) / 256, most = 4ull * num_sms();
   return (unsigned)(want < 1 ? 1 : want < most ? want : most);
 }
 
-// Free and fork: the team, and the whole GPU where there may be more than the
-// team does itself.
+// Free and fork: the team, and the whole GPU where there may be much to do.
 template <typename P>
-int launch_rows(void (*team)(P), void (*rest)(P), cudaStream_t s, const P& p) {
+int launch_rows(void (*solo)(P), void (*team)(P), void (*rest)(P), cudaStream_t s, P& p) {
   const uint64_t units = ((uint64_t)p.r.n + kRows - 1) / kRows * (((uint64_t)p.r.t.columns + 31) / 32);
-  const uint32_t ctas = team_size(p.r.n, 0, units);
-  const int e = launch_team(team, ctas, s, p);
-  if (e || units <= (uint64_t)kOwn * ctas * kTeamWarps) return e;
+  const uint32_t ctas = team_size(p.r.n);
+  p.r.rest = units > kRestUnits;
+  const int e = launch_team(ctas == 1 ? solo : team, ctas, s, p);
+  if (e || !p.r.rest) return e;
   return launch_dependent(rest, whole_grid(units * 32), 256, 0, s, p);
 }
 
@@ -1000,7 +1136,7 @@ extern "C" int db_page_free(const db_page_tables* t, const db_page_cut* req, uin
   p.r.status = status;
   p.r.ctr = ctr;
   p.req = req;
-  return launch_rows(page_free_kernel, page_free_units_kernel, s, p);
+  return launch_rows(page_free_kernel<true>, page_free_kernel<false>, page_free_units_kernel, s, p);
 }
 
 extern "C" int db_page_fork(const db_page_tables* t, const db_page_fork_req* req, uint32_t n,
@@ -1017,7 +1153,7 @@ extern "C" int db_page_fork(const db_page_tables* t, const db_page_fork_req* req
   p.r.status = status;
   p.r.ctr = ctr;
   p.req = req;
-  return launch_rows(page_fork_kernel, page_fork_units_kernel, s, p);
+  return launch_rows(page_fork_kernel<true>, page_fork_kernel<false>, page_fork_units_kernel, s, p);
 }
 
 extern "C" int db_page_extend(const db_page_tables* t, const db_page_grow* req, uint32_t n,
@@ -1037,9 +1173,11 @@ extern "C" int db_page_extend(const db_page_tables* t, const db_page_grow* req, 
   p.status = status;
   p.ctr = ctr;
   const uint64_t pages = (uint64_t)n * t->columns < t->n_pages ? (uint64_t)n * t->columns : t->n_pages;
-  const uint32_t ctas = team_size(n, (t->n_pages + 31) / 32, 0);
-  const int e = launch_team(page_extend_kernel, ctas, s, p);
-  if (e || pages <= (uint64_t)kOwn * ctas * kTeamThreads) return e;
+  const uint32_t words = (t->n_pages + 31) / 32;
+  const uint32_t ctas = team_size(words > kSoloWords ? most_of(n, words / 4) + kTeamThreads : n);
+  p.rest = pages > kRestPages;
+  const int e = launch_team(ctas == 1 ? page_extend_kernel<true> : page_extend_kernel<false>, ctas, s, p);
+  if (e || !p.rest) return e;
   return launch_dependent(page_place_kernel, whole_grid(pages), 256, 0, s, p);
 }
 
@@ -1062,7 +1200,9 @@ extern "C" int db_page_compact(const db_page_tables* t, const db_page_tables* ou
   p.n_moves = n_moves;
   p.ctr = ctr;
   const cudaStream_t s = (cudaStream_t)stream;
-  const int e = launch_team(page_compact_plan_kernel, team_size(0, (t->n_pages + 31) / 32, 0), s, p);
+  const uint32_t ctas = team_size(((uint64_t)t->n_pages + 31) / 32);
+  const int e = launch_team(ctas == 1 ? page_compact_plan_kernel<true> : page_compact_plan_kernel<false>,
+                            ctas, s, p);
   if (e) return e;
   const uint64_t entries = (uint64_t)t->n_seqs * t->columns;
   return launch_dependent(page_compact_apply_kernel,
