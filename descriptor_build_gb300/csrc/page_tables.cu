@@ -1,7 +1,7 @@
 // Page tables of a cache in the device heap: extend, fork, free, compact
 // (include/pagecache.h has the definitions).
 //
-// A call's requests are planned by one team: a single CTA or one cluster of
+// A call's requests are planned by one team: a single CTA, or one cluster of
 // CTAs, whose barriers are the hardware's, so no kernel here waits on memory.
 // The plan is a prefix sum over what the requests ask for, and what follows
 // is work on pieces of it, found again by a search in shared memory. The team
@@ -19,20 +19,25 @@
 namespace db {
 namespace {
 
-constexpr uint32_t kTeamThreads = 1024;
-constexpr uint32_t kTeamWarps = kTeamThreads / 32;
-constexpr uint32_t kMaxTeam = 8;       // CTAs of the largest team
-constexpr uint32_t kSearch = 1024;     // starts kept in shared memory, the others are near one
-constexpr uint32_t kRows = 8;          // requests of a group (see "row units")
-constexpr uint32_t kSoloWords = 2048;  // free words of a team of one CTA
-// What a team does itself when a second kernel is there for the rest: units of
-// rows for each of its CTAs, pages for each of its threads. The second kernel
-// is launched when the sizes of the call allow for more than kRest of them.
-constexpr uint32_t kOwnUnits = 8, kOwnPages = 4;
-constexpr uint32_t kRestUnits = 64, kRestPages = 16384;
+constexpr uint32_t kMaxTeam = 8;        // CTAs of the largest team
+constexpr uint32_t kTeamThreads = 1024; // threads of a CTA of a cluster
+constexpr uint32_t kSmallThreads = 256; // threads of the smallest team
+constexpr uint32_t kRows = 8;           // requests of a group (see "row units")
+constexpr uint32_t kSearch = 1024;      // starts that a second kernel keeps in shared memory
+constexpr uint32_t kTeamSearch = 4096;  // starts that a CTA of a cluster keeps
+constexpr uint32_t kOwnUnits = 8;       // units that a team does itself, for each of its CTAs,
+constexpr uint32_t kOwnPages = 4;       // and pages, for each of its threads, when a second
+constexpr uint32_t kRestUnits = 64;     // kernel is there: where the sizes of the call allow for
+constexpr uint32_t kRestPages = 16384;  // more than kRestUnits, kRestPages or kRestMoves
+constexpr uint32_t kRestMoves = 8192;
+constexpr uint32_t kSoloEntries = 32768;  // table entries that a compaction's one CTA renames itself
 constexpr uint32_t kNoMove = 0xFFFFFFFFu;
 constexpr uint32_t kNoEntry = 0xFFFFFFFEu;   // a row without an entry in the column
 constexpr uint32_t kBadEntry = 0xFFFFFFFFu;  // no page
+
+// Free words that a team of one CTA keeps in shared memory.
+template <uint32_t kThreads>
+constexpr uint32_t kSoloWords = kThreads == kSmallThreads ? 1024 : 2048;
 
 // One request's place in the plan.
 struct __align__(16) Plan {
@@ -43,11 +48,13 @@ struct __align__(16) Plan {
 };
 
 struct Head {
-  uint32_t units;      // left for the second kernel
+  uint32_t units;      // left for the second kernel: units, pages or moves
+  uint32_t used;       // extend: free words up to the last one used
+  uint32_t n_live;     // compact: live pages
+  uint32_t holes;      // compact: free pages below n_live
   uint32_t moved;      // compact: moves made
   uint32_t dst_last;   // compact: the last page moved to (with moved > 0)
   uint32_t src_first;  // compact: the lowest page moved from, or n_pages
-  uint32_t holes;      // compact: free pages below the number of live ones
 };
 
 struct Work {
@@ -87,40 +94,37 @@ size_t carve(char* ws, uint32_t n_seqs, uint32_t n_pages, Work* w) {
 }
 
 // ------------------------------------------------------------------ the team
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-
-struct Sum {
-  uint64_t a;
-  uint32_t b;
-};
-
 struct TeamShared {
-  uint64_t warp_a[kTeamWarps];
-  uint32_t warp_b[kTeamWarps];
-  uint64_t cta_a[2];  // this CTA's sums, read by its peers; two rounds apart
-  uint32_t cta_b[2];
-  uint64_t base_a, total_a;
-  uint32_t base_b, total_b;
+  uint32_t warp_a[2][32], warp_b[2][32];            // each warp's sums, two scans apart
+  uint32_t cta_a[2][kMaxTeam], cta_b[2][kMaxTeam];  // each CTA's, written by it
 };
 
-// kSolo: the team is one CTA.
-template <bool kSolo>
+// kSolo: the team is one CTA of kThreads.
+template <uint32_t kThreads, bool kSolo>
 struct Team {
+  static constexpr uint32_t kWarps = kThreads / 32;
   uint32_t rank, size, round;
   TeamShared* s;
-  __device__ __forceinline__ explicit Team(TeamShared* sh)
-      : rank(kSolo ? 0 : cluster_rank()), size(kSolo ? 1 : cluster_size()), round(0), s(sh) {}
-  __device__ __forceinline__ uint32_t id() const { return rank * kTeamThreads + threadIdx.x; }
-  __device__ __forceinline__ uint32_t threads() const { return size * kTeamThreads; }
+
+  __device__ __forceinline__ explicit Team(TeamShared* sh) : rank(0), size(1), round(0), s(sh) {
+    if (!kSolo) {
+      asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+      asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
+      asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    }
+  }
+  // Every CTA of the cluster has started: its shared memory may be written.
+  // Comes once, before the first sync or scan.
+  __device__ __forceinline__ void started() const {
+    if (!kSolo) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  }
+  __device__ __forceinline__ uint32_t id() const { return rank * kThreads + threadIdx.x; }
+  __device__ __forceinline__ uint32_t threads() const { return size * kThreads; }
+  // Requests are dealt evenly to the CTAs: a round takes per(n) * size of
+  // them, thread t of CTA r the (r * per(n) + t)-th when t < per(n).
+  __device__ __forceinline__ uint32_t per(uint32_t n) const {
+    return kSolo ? kThreads : min(kThreads, ((n + size - 1) / size + 31) & ~31u);
+  }
   // Barrier of the team; global and shared writes before it are seen after it.
   __device__ __forceinline__ void sync() const {
     if (kSolo) {
@@ -130,94 +134,67 @@ struct Team {
                        : "memory");
     }
   }
-  // Exclusive prefix of one pair per thread in id() order, and the team's sum.
-  __device__ __forceinline__ Sum scan(Sum v, Sum* total) {
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint64_t a = v.a;
-    uint32_t b = v.b;
+  // Exclusive prefix of v in the order of CTAs and threads, and the sum; with
+  // kFlags also of a flag. Also a barrier of the team. The arrays of one scan
+  // are written again two scans later, past the barrier of the one between.
+  template <bool kFlags>
+  __device__ __forceinline__ uint32_t scan(uint32_t v, uint32_t* total, bool flag = false,
+                                           uint32_t* flag_rank = nullptr,
+                                           uint32_t* flag_total = nullptr) {
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = round++ & 1;
+    uint32_t x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t x = __shfl_up_sync(kFull, a, o);
-      const uint32_t y = __shfl_up_sync(kFull, b, o);
-      if (lane >= (uint32_t)o) {
-        a += x;
-        b += y;
-      }
+      const uint32_t y = __shfl_up_sync(kFull, x, o);
+      if (lane >= (uint32_t)o) x += y;
     }
-    __syncthreads();  // the last round's readers are done
+    const uint32_t vote = kFlags ? __ballot_sync(kFull, flag) : 0;
     if (lane == 31) {
-      s->warp_a[warp] = a;
-      s->warp_b[warp] = b;
+      s->warp_a[k][warp] = x;
+      if (kFlags) s->warp_b[k][warp] = __popc(vote);
     }
     __syncthreads();
-    const uint32_t k = round++ & 1;
-    if (warp == 0) {
-      const uint64_t wa = s->warp_a[lane];
-      const uint32_t wb = s->warp_b[lane];
-      uint64_t xa = wa;
-      uint32_t xb = wb;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t x = __shfl_up_sync(kFull, xa, o);
-        const uint32_t y = __shfl_up_sync(kFull, xb, o);
-        if (lane >= (uint32_t)o) {
-          xa += x;
-          xb += y;
-        }
-      }
-      s->warp_a[lane] = xa - wa;
-      s->warp_b[lane] = xb - wb;
-      if (lane == 31) {
-        s->cta_a[k] = xa;
-        s->cta_b[k] = xb;
-        s->base_a = 0;
-        s->base_b = 0;
-        s->total_a = xa;
-        s->total_b = xb;
-      }
-    }
-    sync();
-    if (!kSolo) {
+    const uint32_t a = lane < kWarps ? s->warp_a[k][lane] : 0;
+    const uint32_t b = kFlags && lane < kWarps ? s->warp_b[k][lane] : 0;
+    uint32_t base_a = __reduce_add_sync(kFull, lane < warp ? a : 0), base_b = 0;
+    if (kFlags) base_b = __reduce_add_sync(kFull, lane < warp ? b : 0);
+    if (kSolo) {
+      *total = __reduce_add_sync(kFull, a);
+      if (kFlags) *flag_total = __reduce_add_sync(kFull, b);
+    } else {
       if (warp == 0) {
-        uint64_t pa = 0;
-        uint32_t pb = 0;
+        const uint32_t sum_a = __reduce_add_sync(kFull, a);
+        const uint32_t sum_b = kFlags ? __reduce_add_sync(kFull, b) : 0;
         if (lane < size) {
-          uint32_t at, bt;
-          asm("mapa.shared::cluster.u32 %0, %1, %2;"
-              : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(&s->cta_a[k])), "r"(lane));
-          asm("mapa.shared::cluster.u32 %0, %1, %2;"
-              : "=r"(bt) : "r"((uint32_t)__cvta_generic_to_shared(&s->cta_b[k])), "r"(lane));
-          asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(pa) : "r"(at) : "memory");
-          asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(pb) : "r"(bt) : "memory");
-        }
-        const uint64_t ta = warp_sum64(pa), ba = warp_sum64(lane < rank ? pa : 0);
-        const uint32_t tb = warp_sum32(pb), bb = warp_sum32(lane < rank ? pb : 0);
-        if (lane == 0) {
-          s->base_a = ba;
-          s->base_b = bb;
-          s->total_a = ta;
-          s->total_b = tb;
+          to_peer(&s->cta_a[k][rank], lane, sum_a);
+          if (kFlags) to_peer(&s->cta_b[k][rank], lane, sum_b);
         }
       }
-      __syncthreads();
+      sync();
+      const uint32_t c = lane < size ? s->cta_a[k][lane] : 0;
+      base_a += __reduce_add_sync(kFull, lane < rank ? c : 0);
+      *total = __reduce_add_sync(kFull, c);
+      if (kFlags) {
+        const uint32_t d = lane < size ? s->cta_b[k][lane] : 0;
+        base_b += __reduce_add_sync(kFull, lane < rank ? d : 0);
+        *flag_total = __reduce_add_sync(kFull, d);
+      }
     }
-    total->a = s->total_a;
-    total->b = s->total_b;
-    Sum out;
-    out.a = s->base_a + s->warp_a[warp] + a - v.a;
-    out.b = s->base_b + s->warp_b[warp] + b - v.b;
-    return out;
+    if (kFlags) *flag_rank = base_b + __popc(vote & lanemask_lt());
+    return base_a + x - v;
+  }
+  __device__ __forceinline__ static void to_peer(uint32_t* mine, uint32_t peer, uint32_t v) {
+    uint32_t at;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;"
+        : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(mine)), "r"(peer));
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
   }
 };
 
-// A scan may end with a peer still reading this CTA's shared memory: the last
-// sync of a kernel's team comes after its last scan in every kernel below, so
-// no CTA leaves before its peers have read it.
-
 // ---------------------------------------------------------- finding a piece
 // The last i < n with start(i) <= e, where start does not decrease: every
-// `step`-th start is in shared memory (all of them up to kSearch), and those
-// between two of them lie in a line or two of memory.
+// `step`-th start is in shared memory, and those between two of them lie in a
+// line or two of memory.
 struct Finder {
   const uint32_t* s_start;
   uint32_t n, kept, step;
@@ -240,24 +217,14 @@ struct Finder {
   }
 };
 
-__device__ __forceinline__ Finder finder_of(const uint32_t* s_start, uint32_t n) {
-  const uint32_t step = (n + kSearch - 1) / kSearch;
-  return Finder{s_start, n, (n + step - 1) / step, step};
-}
-
-// Load the starts (every thread of a CTA; a barrier has to follow).
+// Load the starts, at most `most` (every thread of a CTA; a barrier follows).
 template <typename Start>
-__device__ __forceinline__ Finder load_finder(uint32_t* s_start, uint32_t n, Start start) {
-  const Finder f = finder_of(s_start, n);
-  for (uint32_t k = threadIdx.x; k < f.kept; k += blockDim.x) s_start[k] = start(k * f.step);
-  return f;
+__device__ __forceinline__ Finder load_finder(uint32_t* s_start, uint32_t most, uint32_t n,
+                                              Start start) {
+  const uint32_t step = (n + most - 1) / most, kept = (n + step - 1) / step;
+  for (uint32_t k = threadIdx.x; k < kept; k += blockDim.x) s_start[k] = start(k * step);
+  return Finder{s_start, n, kept, step};
 }
-
-// What a team of one CTA keeps of its plan on chip instead of in the workspace.
-struct SoloPlan {
-  Plan plan[kTeamThreads];
-  uint2 group[kTeamThreads / kRows];
-};
 
 // The plan, in shared memory or in the workspace. (A team's barrier and the
 // wait for the kernel before order these after the stores of other CTAs.)
@@ -279,87 +246,120 @@ __device__ __forceinline__ bool claimed(const uint32_t* c, uint32_t seq, uint32_
 }
 
 __device__ __forceinline__ uint32_t pages_of(uint64_t tokens, uint32_t page_tokens) {
-  return (tokens >> 32) || tokens + page_tokens > 0xFFFFFFFFull
+  return tokens + page_tokens > 0xFFFFFFFFull
              ? (uint32_t)((tokens + page_tokens - 1) / page_tokens)
              : ((uint32_t)tokens + page_tokens - 1) / page_tokens;
 }
 
-// Word w of the free bits, without bits past n_pages.
-__device__ __forceinline__ uint32_t ld_word(const uint32_t* bits, uint32_t w, uint32_t n_pages) {
-  uint32_t v = __ldcg(&bits[w]);
-  if (n_pages - 32 * w < 32) v &= (1u << (n_pages & 31)) - 1;
-  return v;
-}
-
-// A thread's share of the free bits: `words` consecutive words from `first` on,
-// one where the team has a thread for each, else a multiple of four, of which
-// the first four stay in registers.
-struct Bits {
-  uint32_t first, words;
-  uint32_t before;  // free pages before them
-  uint32_t total;   // free pages of the cache
-  uint4 v;
-};
-
-template <bool kSolo>
-__device__ __forceinline__ Bits scan_free(Team<kSolo>& team, const uint32_t* bits,
-                                          uint32_t n_pages) {
-  const uint32_t all = (n_pages + 31) / 32, threads = team.threads();
-  Bits b;
-  b.words = all <= threads ? 1 : 4 * ((all + 4 * threads - 1) / (4 * threads));
-  b.first = team.id() * b.words;
-  b.v = make_uint4(0, 0, 0, 0);
-  uint32_t c = 0;
-  if (b.words == 1) {
-    if (b.first < all) b.v.x = ld_word(bits, b.first, n_pages);
-    c = __popc(b.v.x);
-  } else {
-    for (uint32_t s = 0; s < b.words && b.first + s < all; s += 4) {
-      const uint32_t w = b.first + s;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (w + 4 < all) {
-        v = __ldcg(reinterpret_cast<const uint4*>(bits + w));
-      } else {
-        v.x = ld_word(bits, w, n_pages);
-        if (w + 1 < all) v.y = ld_word(bits, w + 1, n_pages);
-        if (w + 2 < all) v.z = ld_word(bits, w + 2, n_pages);
-        if (w + 3 < all) v.w = ld_word(bits, w + 3, n_pages);
-      }
-      c += __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w);
-      if (s == 0) b.v = v;
+// The j-th set bit (from 0) of v.
+__device__ __forceinline__ uint32_t nth_bit(uint32_t v, uint32_t j) {
+  uint32_t at = 0;
+#pragma unroll
+  for (uint32_t half = 16; half; half >>= 1) {
+    const uint32_t c = __popc(v & ((1u << half) - 1));
+    if (j >= c) {
+      j -= c;
+      at += half;
+      v >>= half;
     }
   }
-  Sum total;
-  b.before = (uint32_t)team.scan(Sum{c, 0}, &total).a;
-  b.total = (uint32_t)total.a;
-  return b;
-}
-
-// f(word's index, its free bits, free pages before it) for every word, by whole
-// warps (a lane without a word has no free bits and an index past the words).
-template <typename F>
-__device__ __forceinline__ void each_word(const Bits& b, const uint32_t* bits, uint32_t n_pages,
-                                          F f) {
-  const uint32_t all = (n_pages + 31) / 32;
-  uint32_t before = b.before;
-  for (uint32_t s = 0; s < b.words; ++s) {
-    const uint32_t w = b.first + s;
-    uint32_t v = s == 0 ? b.v.x : s == 1 ? b.v.y : s == 2 ? b.v.z : b.v.w;
-    if (s >= 4) v = w < all ? ld_word(bits, w, n_pages) : 0;
-    f(w, v, before);
-    before += __popc(v);
-  }
+  return at;
 }
 
 // A count and an error, one warp's at a time, into the counters.
 __device__ __forceinline__ void add_count(uint64_t* to, uint32_t count) {
-  const uint32_t c = warp_sum32(count);
+  const uint32_t c = __reduce_add_sync(kFull, count);
   if ((threadIdx.x & 31) == 0 && c) atomicAdd((unsigned long long*)to, (unsigned long long)c);
 }
 __device__ __forceinline__ void add_error(db_counters* ctr, bool bad) {
   if (__any_sync(kFull, bad) && (threadIdx.x & 31) == 0)
     atomicOr((unsigned long long*)&ctr->err, (unsigned long long)DB_ERR_PAGE_TABLE);
 }
+
+// ---------------------------------------------------------------- free words
+// Word w of the free bits, without bits past n_pages.
+__device__ __forceinline__ uint32_t ld_word(const uint32_t* bits, uint32_t w, uint32_t n_pages) {
+  uint32_t v = __ldcg(&bits[w]);
+  if (n_pages - 32 * w < 32) v &= (1u << (n_pages & 31)) - 1;
+  return v;
+}
+// Words w to w + 3 of `all` (0 past them).
+__device__ __forceinline__ uint4 ld_quad(const uint32_t* bits, uint32_t w, uint32_t all,
+                                         uint32_t n_pages) {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (w + 4 < all) {
+    v = __ldcg(reinterpret_cast<const uint4*>(bits + w));
+  } else {
+    if (w < all) v.x = ld_word(bits, w, n_pages);
+    if (w + 1 < all) v.y = ld_word(bits, w + 1, n_pages);
+    if (w + 2 < all) v.z = ld_word(bits, w + 2, n_pages);
+    if (w + 3 < all) v.w = ld_word(bits, w + 3, n_pages);
+  }
+  return v;
+}
+
+// A thread's share of the free bits: `quads` quads of consecutive words from
+// `first` on, the first of which stays in registers.
+struct Bits {
+  uint32_t first, quads;
+  uint32_t before;  // free pages before them
+  uint32_t total;   // free pages of the cache
+  uint4 v;
+};
+
+template <uint32_t kThreads, bool kSolo>
+__device__ __forceinline__ Bits scan_free(Team<kThreads, kSolo>& team, const uint32_t* bits,
+                                          uint32_t n_pages) {
+  const uint32_t all = (n_pages + 31) / 32, threads = team.threads();
+  Bits b;
+  b.quads = (all + 4 * threads - 1) / (4 * threads);
+  b.first = team.id() * b.quads * 4;
+  b.v = ld_quad(bits, b.first, all, n_pages);
+  uint32_t c = __popc(b.v.x) + __popc(b.v.y) + __popc(b.v.z) + __popc(b.v.w);
+  for (uint32_t s = 1; s < b.quads; ++s) {
+    const uint4 v = ld_quad(bits, b.first + 4 * s, all, n_pages);
+    c += __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w);
+  }
+  b.before = team.template scan<false>(c, &b.total);
+  return b;
+}
+
+// f(first word, its quad, free pages before each of the four) for a thread's
+// quads, in order, until f returns false.
+template <typename F>
+__device__ __forceinline__ void each_quad(const Bits& b, const uint32_t* bits, uint32_t n_pages,
+                                          F f) {
+  const uint32_t all = (n_pages + 31) / 32;
+  uint32_t before = b.before;
+  for (uint32_t s = 0; s < b.quads; ++s) {
+    const uint32_t w = b.first + 4 * s;
+    if (w >= all) return;
+    const uint4 v = s ? ld_quad(bits, w, all, n_pages) : b.v;
+    uint4 at;
+    at.x = before;
+    at.y = at.x + __popc(v.x);
+    at.z = at.y + __popc(v.y);
+    at.w = at.z + __popc(v.z);
+    if (!f(w, v, at)) return;
+    before = at.w + __popc(v.w);
+  }
+}
+
+// A quad of words into an array of `all` words, 16-byte aligned.
+__device__ __forceinline__ void st_quad(uint32_t* to, uint32_t w, uint32_t all, const uint4& v) {
+  if (w + 4 <= all) {
+    *reinterpret_cast<uint4*>(to + w) = v;
+  } else {
+    to[w] = v.x;
+    if (w + 1 < all) to[w + 1] = v.y;
+    if (w + 2 < all) to[w + 2] = v.z;
+  }
+}
+
+struct WordStart {
+  const uint32_t* before;
+  __device__ __forceinline__ uint32_t operator()(uint32_t w) const { return before[w]; }
+};
 
 // --------------------------------------------------------------- row units
 // Free and fork work on columns [from, end) of each request's row. kRows
@@ -377,11 +377,20 @@ struct Rows {
   Work w;
 };
 
-// Each thread's columns into the groups; ends with every group of these
-// requests written (not yet visible to other CTAs). `carry`: units before.
-template <bool kSolo>
-__device__ __forceinline__ void plan_rows(Team<kSolo>& team, const Rows& p, SoloPlan* solo,
-                                          uint32_t i, const Plan& pl, uint32_t* carry) {
+// What a team of one CTA keeps of its plan on chip.
+template <uint32_t kThreads, bool kSolo>
+struct RowPlan {
+  Plan plan[kSolo ? kThreads : 1];
+  uint32_t col[kSolo ? kThreads / kRows : 1];
+  uint32_t start[kSolo ? kThreads / kRows : kTeamSearch];
+};
+
+// Each thread's columns into the groups (visible past the next barrier).
+// `carry`: units before.
+template <uint32_t kThreads, bool kSolo>
+__device__ __forceinline__ void plan_rows(Team<kThreads, kSolo>& team, const Rows& p,
+                                          RowPlan<kThreads, kSolo>* s, uint32_t i, bool mine,
+                                          const Plan& pl, uint32_t* carry) {
   uint32_t lo = pl.from < pl.end ? pl.from : 0xFFFFFFFFu, hi = pl.from < pl.end ? pl.end : 0;
 #pragma unroll
   for (uint32_t o = 1; o < kRows; o <<= 1) {
@@ -389,20 +398,23 @@ __device__ __forceinline__ void plan_rows(Team<kSolo>& team, const Rows& p, Solo
     hi = max(hi, __shfl_xor_sync(kFull, hi, o));
   }
   lo &= ~31u;
-  const uint32_t units = hi > lo ? (hi - lo + 31) / 32 : 0;
-  const bool first = i % kRows == 0;
-  Sum total;
-  const Sum x = team.scan(Sum{first ? units : 0, 0}, &total);
-  if (i < p.n) {
-    const uint2 g = make_uint2(*carry + (uint32_t)x.a, lo);
-    st_plan(&p.w.plan[i], pl);  // for the second kernel, when there is one
-    if (first) p.w.group[i / kRows] = g;
+  const bool first = mine && i % kRows == 0;
+  uint32_t total;
+  const uint32_t x = team.template scan<false>(first && hi > lo ? (hi - lo + 31) / 32 : 0, &total);
+  if (mine) {
     if (kSolo) {
-      st_plan(&solo->plan[i], pl);
-      if (first) solo->group[i / kRows] = g;
+      s->plan[i] = pl;
+      if (first) {
+        s->start[i / kRows] = x;
+        s->col[i / kRows] = lo;
+      }
+    }
+    if (!kSolo || p.rest) {
+      st_plan(&p.w.plan[i], pl);
+      if (first) p.w.group[i / kRows] = make_uint2(*carry + x, lo);
     }
   }
-  *carry += (uint32_t)total.a;
+  *carry += total;
 }
 
 struct GroupStart {
@@ -410,33 +422,54 @@ struct GroupStart {
   __device__ __forceinline__ uint32_t operator()(uint32_t g) const { return group[g].x; }
 };
 
-// Where the units of a call are found.
+// Where the units of a call are found: in the workspace, or in a RowPlan.
 struct Units {
   Finder f;
   const Plan* plan;
-  const uint2* group;
+  const uint2* group;   // in the workspace, or null:
+  const uint32_t* col;  // a RowPlan's columns
   uint32_t n;
   // The rows of unit u: lane j < kRows holds the j-th plan (empty if there is
   // none); returns this lane's column.
   __device__ __forceinline__ uint32_t load(uint32_t u, uint32_t lane, Plan* pl) const {
     const uint32_t g = f.find(u, GroupStart{group});
-    const uint2 at = group[g];
     const uint32_t i = g * kRows + lane;
     *pl = Plan{0, 0, 0, 0};
     if (lane < kRows && i < n) *pl = ld_plan(&plan[i]);
+    const uint2 at = group ? group[g] : make_uint2(f.s_start[g], col[g]);
     return at.y + (u - at.x) * 32 + lane;
   }
 };
 
-__device__ __forceinline__ Units find_units(const Rows& p, const Plan* plan, const uint2* group,
-                                            uint32_t* s_start) {
+// The units of a plan in the workspace (a barrier follows).
+__device__ __forceinline__ Units find_units(const Rows& p, uint32_t* s_start, uint32_t most) {
   Units x;
-  x.plan = plan;
-  x.group = group;
+  x.plan = p.w.plan;
+  x.group = p.w.group;
+  x.col = nullptr;
   x.n = p.n;
-  x.f = load_finder(s_start, (p.n + kRows - 1) / kRows, GroupStart{group});
-  __syncthreads();
+  x.f = load_finder(s_start, most, (p.n + kRows - 1) / kRows, GroupStart{p.w.group});
   return x;
+}
+
+// The end of a planning team: its own units, or their number for the second
+// kernel.
+template <uint32_t kThreads, bool kSolo, typename F>
+__device__ __forceinline__ void own_units(Team<kThreads, kSolo>& team, const Rows& p,
+                                          RowPlan<kThreads, kSolo>* s, uint32_t units, F work) {
+  const bool own = !p.rest || units <= kOwnUnits * team.size;
+  if (team.id() == 0 && p.rest) p.w.head->units = own ? 0 : units;
+  if (!own || !units) return;
+  team.sync();
+  Units x;
+  if (kSolo) {
+    const uint32_t groups = (p.n + kRows - 1) / kRows;
+    x = Units{Finder{s->start, groups, groups, 1}, s->plan, nullptr, s->col, p.n};
+  } else {
+    x = find_units(p, s->start, kTeamSearch);
+    __syncthreads();
+  }
+  work(x, team.id() / 32, team.threads() / 32, units);
 }
 
 // ---------------------------------------------------------------------- free
@@ -460,8 +493,8 @@ __device__ __forceinline__ void free_units(const Rows& p, const Units& x, uint32
       const uint32_t row = __shfl_sync(kFull, pl.row, j), from = __shfl_sync(kFull, pl.from, j);
       const uint32_t end = __shfl_sync(kFull, pl.end, j);
       page[j] = kNoEntry;
-      if (c >= from && c < end) page[j] = (uint32_t)p.t.table[(uint64_t)row * p.t.columns + c];
       clear[j] = c >= from && c < end;
+      if (clear[j]) page[j] = (uint32_t)p.t.table[(uint64_t)row * p.t.columns + c];
     }
 #pragma unroll
     for (uint32_t j = 0; j < kRows; ++j) {
@@ -511,26 +544,28 @@ __device__ __forceinline__ void free_units(const Rows& p, const Units& x, uint32
   }
 }
 
-template <bool kSolo>
-__global__ void __launch_bounds__(kTeamThreads) page_free_kernel(const FreeParams q) {
+template <uint32_t kThreads, bool kSolo>
+__global__ void __launch_bounds__(kThreads) page_free_kernel(const FreeParams q) {
   __shared__ TeamShared s_team;
-  __shared__ SoloPlan s_plan;
-  __shared__ uint32_t s_start[kSolo ? kTeamThreads / kRows : kSearch];
+  __shared__ RowPlan<kThreads, kSolo> s_plan;
   const Rows& p = q.r;
+  Team<kThreads, kSolo> team(&s_team);
   wait_for_prerequisites();
   dependents_may_launch();
-  Team<kSolo> team(&s_team);
+  const uint32_t per = team.per(p.n), at = team.rank * per + threadIdx.x;
   if (p.ctr && team.id() == 0) *p.ctr = db_counters{0, 0, 0, 0};
-  for (uint32_t i = team.id(); i < p.n; i += team.threads()) {
+  for (uint32_t i = at; threadIdx.x < per && i < p.n; i += per * team.size) {
     const uint32_t seq = q.req[i].seq;
     if (seq < p.t.n_seqs) claim(p.w.claim, seq, i);
   }
+  team.started();
   team.sync();
   uint32_t units = 0, invalid = 0;
-  for (uint32_t i0 = 0; i0 < p.n; i0 += team.threads()) {
-    const uint32_t i = i0 + team.id();
+  for (uint32_t i0 = 0; i0 < p.n; i0 += per * team.size) {
+    const uint32_t i = i0 + at;
+    const bool mine = threadIdx.x < per && i < p.n;
     Plan pl = {0, 0, 0, 0};
-    if (i < p.n) {
+    if (mine) {
       const db_page_cut r = q.req[i];
       const uint32_t len = r.seq < p.t.n_seqs ? p.t.length[r.seq] : 0;
       const bool ok = r.seq < p.t.n_seqs && claimed(p.w.claim, r.seq, i);
@@ -545,27 +580,26 @@ __global__ void __launch_bounds__(kTeamThreads) page_free_kernel(const FreeParam
       invalid += !ok;
       if (p.status) p.status[i] = ok ? DB_PAGE_OK : DB_PAGE_INVALID;
     }
-    plan_rows(team, p, &s_plan, i, pl, &units);
+    plan_rows(team, p, &s_plan, i, mine, pl, &units);
   }
   if (p.ctr) add_count(&p.ctr->n_invalid, invalid);
-  const bool own = !p.rest || units <= kOwnUnits * team.size;
-  if (team.id() == 0) p.w.head->units = own ? 0 : units;
-  team.sync();
-  if (!own || !units) return;
-  const Units x = find_units(p, kSolo ? s_plan.plan : p.w.plan, kSolo ? s_plan.group : p.w.group,
-                             s_start);
-  free_units(p, x, team.id() / 32, team.threads() / 32, units);
+  own_units(team, p, &s_plan, units, [&](const Units& x, uint32_t first, uint32_t stride, uint32_t n) {
+    free_units(p, x, first, stride, n);
+  });
 }
 
-__global__ void __launch_bounds__(256) page_free_units_kernel(const FreeParams q) {
+constexpr uint32_t kUnitThreads = 128;
+
+__global__ void __launch_bounds__(kUnitThreads) page_free_units_kernel(const FreeParams q) {
   __shared__ uint32_t s_start[kSearch];
   const Rows& p = q.r;
   wait_for_prerequisites();
   dependents_may_launch();
-  const uint32_t units = __ldcg(&p.w.head->units);
-  if (blockIdx.x * 8 >= units) return;
-  const Units x = find_units(p, p.w.plan, p.w.group, s_start);
-  free_units(p, x, blockIdx.x * 8 + threadIdx.x / 32, gridDim.x * 8, units);
+  const uint32_t units = p.w.head->units, first = (blockIdx.x * kUnitThreads + threadIdx.x) / 32;
+  if (blockIdx.x * (kUnitThreads / 32) >= units) return;
+  const Units x = find_units(p, s_start, kSearch);
+  __syncthreads();
+  free_units(p, x, first, gridDim.x * (kUnitThreads / 32), units);
 }
 
 // ---------------------------------------------------------------------- fork
@@ -609,33 +643,40 @@ __device__ __forceinline__ void fork_units(const Rows& p, const Units& x, uint32
   if (p.ctr) add_error(p.ctr, bad);
 }
 
-template <bool kSolo>
-__global__ void __launch_bounds__(kTeamThreads) page_fork_kernel(const ForkParams q) {
+template <uint32_t kThreads, bool kSolo>
+__global__ void __launch_bounds__(kThreads) page_fork_kernel(const ForkParams q) {
   __shared__ TeamShared s_team;
-  __shared__ SoloPlan s_plan;
-  __shared__ uint32_t s_start[kSolo ? kTeamThreads / kRows : kSearch];
+  __shared__ RowPlan<kThreads, kSolo> s_plan;
   const Rows& p = q.r;
+  Team<kThreads, kSolo> team(&s_team);
   wait_for_prerequisites();
   dependents_may_launch();
-  Team<kSolo> team(&s_team);
+  const uint32_t per = team.per(p.n), at = team.rank * per + threadIdx.x;
   if (p.ctr && team.id() == 0) *p.ctr = db_counters{0, 0, 0, 0};
-  for (uint32_t i = team.id(); i < p.n; i += team.threads()) {
+  for (uint32_t i = at; threadIdx.x < per && i < p.n; i += per * team.size) {
     const uint32_t child = q.req[i].child;
     if (child < p.t.n_seqs) claim(p.w.claim, child, i);
   }
+  team.started();
   team.sync();
+  const bool one = kSolo || p.n <= per * team.size;
   uint32_t units = 0, invalid = 0;
   uint64_t taken = 0;
-  for (uint32_t i0 = 0; i0 < p.n; i0 += team.threads()) {
-    const uint32_t i = i0 + team.id();
-    Plan pl = {kNoMove, 0, 0, 0};
-    if (i < p.n) {
+  Plan pl;
+  for (uint32_t i0 = 0; i0 < p.n; i0 += per * team.size) {
+    const uint32_t i = i0 + at;
+    const bool mine = threadIdx.x < per && i < p.n;
+    pl = Plan{kNoMove, 0, 0, 0};
+    if (mine) {
       const db_page_fork_req r = q.req[i];
       bool ok = false;
-      if (r.child < p.t.n_seqs && claimed(p.w.claim, r.child, i)) {
-        p.w.claim[r.child] = 0;
-        ok = r.parent < p.t.n_seqs && r.parent != r.child && __ldcg(&p.t.length[r.child]) == 0 &&
-             r.tokens <= __ldcg(&p.t.length[r.parent]);
+      if (r.child < p.t.n_seqs) {
+        const uint32_t held = __ldcg(&p.t.length[r.child]);
+        const uint32_t of = r.parent < p.t.n_seqs ? __ldcg(&p.t.length[r.parent]) : 0;
+        if (claimed(p.w.claim, r.child, i)) {
+          p.w.claim[r.child] = 0;
+          ok = r.parent < p.t.n_seqs && r.parent != r.child && held == 0 && r.tokens <= of;
+        }
       }
       if (ok) {
         pl = Plan{r.child, 0, min(pages_of(r.tokens, p.t.page_tokens), p.t.columns), r.parent};
@@ -644,7 +685,7 @@ __global__ void __launch_bounds__(kTeamThreads) page_fork_kernel(const ForkParam
       invalid += !ok;
       if (p.status) p.status[i] = ok ? DB_PAGE_OK : DB_PAGE_INVALID;
     }
-    plan_rows(team, p, &s_plan, i, pl, &units);
+    plan_rows(team, p, &s_plan, i, mine, pl, &units);
   }
   if (p.ctr) {
     add_count(&p.ctr->n_invalid, invalid);
@@ -652,29 +693,26 @@ __global__ void __launch_bounds__(kTeamThreads) page_fork_kernel(const ForkParam
     if ((threadIdx.x & 31) == 0 && c)
       atomicAdd((unsigned long long*)&p.ctr->total, (unsigned long long)c);
   }
-  const bool own = !p.rest || units <= kOwnUnits * team.size;
-  if (team.id() == 0) p.w.head->units = own ? 0 : units;
-  // every length was read before the last scan
-  for (uint32_t i = team.id(); i < p.n; i += team.threads()) {
-    const uint32_t row = kSolo ? s_plan.plan[i].row : p.w.plan[i].row;
+  // Every length was read before the last scan's barrier.
+  for (uint32_t i = at; threadIdx.x < per && i < p.n; i += per * team.size) {
+    const uint32_t row = one ? pl.row : p.w.plan[i].row;
     if (row != kNoMove) p.t.length[row] = q.req[i].tokens;
   }
-  team.sync();
-  if (!own || !units) return;
-  const Units x = find_units(p, kSolo ? s_plan.plan : p.w.plan, kSolo ? s_plan.group : p.w.group,
-                             s_start);
-  fork_units(p, x, team.id() / 32, team.threads() / 32, units);
+  own_units(team, p, &s_plan, units, [&](const Units& x, uint32_t first, uint32_t stride, uint32_t n) {
+    fork_units(p, x, first, stride, n);
+  });
 }
 
-__global__ void __launch_bounds__(256) page_fork_units_kernel(const ForkParams q) {
+__global__ void __launch_bounds__(kUnitThreads) page_fork_units_kernel(const ForkParams q) {
   __shared__ uint32_t s_start[kSearch];
   const Rows& p = q.r;
   wait_for_prerequisites();
   dependents_may_launch();
-  const uint32_t units = __ldcg(&p.w.head->units);
-  if (blockIdx.x * 8 >= units) return;
-  const Units x = find_units(p, p.w.plan, p.w.group, s_start);
-  fork_units(p, x, blockIdx.x * 8 + threadIdx.x / 32, gridDim.x * 8, units);
+  const uint32_t units = p.w.head->units, first = (blockIdx.x * kUnitThreads + threadIdx.x) / 32;
+  if (blockIdx.x * (kUnitThreads / 32) >= units) return;
+  const Units x = find_units(p, s_start, kSearch);
+  __syncthreads();
+  fork_units(p, x, first, gridDim.x * (kUnitThreads / 32), units);
 }
 
 // -------------------------------------------------------------------- extend
@@ -702,9 +740,9 @@ struct Ask {
   __device__ __forceinline__ bool shares() const { return part && refs > 1; }
 };
 
-__device__ __forceinline__ Ask ask(const ExtendParams& p, uint32_t i) {
+__device__ __forceinline__ Ask ask(const ExtendParams& p, uint32_t i, bool any) {
   Ask a = {0, 0, 0, 0, 0, 0, 0, false, false, false};
-  if (i >= p.n) return a;
+  if (!any) return a;
   const db_page_grow r = p.req[i];
   a.seq = r.seq;
   if (r.seq >= p.t.n_seqs) return a;
@@ -736,25 +774,6 @@ struct PlanStart {
   const Plan* plan;
   __device__ __forceinline__ uint32_t operator()(uint32_t i) const { return plan[i].end; }
 };
-struct WordStart {
-  const uint32_t* before;
-  __device__ __forceinline__ uint32_t operator()(uint32_t w) const { return before[w]; }
-};
-
-// The j-th set bit (from 0) of v.
-__device__ __forceinline__ uint32_t nth_bit(uint32_t v, uint32_t j) {
-  uint32_t at = 0;
-#pragma unroll
-  for (uint32_t half = 16; half; half >>= 1) {
-    const uint32_t c = __popc(v & ((1u << half) - 1));
-    if (j >= c) {
-      j -= c;
-      at += half;
-      v >>= half;
-    }
-  }
-  return at;
-}
 
 // Page e of the batch: the e-th free one, into the row it is for.
 __device__ __forceinline__ void place_pages(const ExtendParams& p, const Finder& request,
@@ -772,32 +791,36 @@ __device__ __forceinline__ void place_pages(const ExtendParams& p, const Finder&
   }
 }
 
-template <bool kSolo>
-__global__ void __launch_bounds__(kTeamThreads) page_extend_kernel(const ExtendParams p) {
+template <uint32_t kThreads, bool kSolo>
+__global__ void __launch_bounds__(kThreads) page_extend_kernel(const ExtendParams p) {
+  constexpr uint32_t kWords = kSolo ? kSoloWords<kThreads> : kSearch;
   __shared__ TeamShared s_team;
-  __shared__ uint32_t s_start[kSolo ? kTeamThreads : kSearch], s_word[kSearch];
-  __shared__ Plan s_plan[kSolo ? kTeamThreads : 1];
-  __shared__ uint32_t s_before[kSolo ? kSoloWords : 1], s_bits[kSolo ? kSoloWords : 1];
+  __shared__ uint32_t s_start[kSolo ? kThreads : kTeamSearch];
+  __shared__ Plan s_plan[kSolo ? kThreads : 1];
+  __shared__ __align__(16) uint32_t s_before[kWords], s_bits[kSolo ? kWords : 4];
+  __shared__ uint32_t s_used;
+  Team<kThreads, kSolo> team(&s_team);
   wait_for_prerequisites();
   dependents_may_launch();
-  Team<kSolo> team(&s_team);
-  const uint32_t id = team.id(), threads = team.threads();
-  const uint32_t words = (p.t.n_pages + 31) / 32;
-  const bool one = kSolo || p.n <= threads;  // a thread for every request, which asks once
+  const uint32_t id = team.id(), words = (p.t.n_pages + 31) / 32;
+  const uint32_t per = team.per(p.n), at = team.rank * per + threadIdx.x;
+  const uint32_t step = per * team.size;
+  const bool one = kSolo || p.n <= step;  // a thread for every request, which asks once
   if (p.ctr && id == 0) *p.ctr = db_counters{0, 0, 0, 0};
-  for (uint32_t i = id; i < p.n; i += threads) {
+  for (uint32_t i = at; threadIdx.x < per && i < p.n; i += step) {
     const uint32_t seq = p.req[i].seq;
     if (seq < p.t.n_seqs) claim(p.w.claim, seq, i);
   }
+  team.started();
   const Bits bits = scan_free(team, p.t.free, p.t.n_pages);  // its barrier is the claims'
   // How many of the batch's requests hold each shared page, and the last of
   // them; requests of a warp that hold the same one (samples of one prompt)
   // count together.
-  Ask a = {0, 0, 0, 0, 0, 0, 0, false, false, false};
+  Ask a;
   bool shares = false;
-  for (uint32_t i0 = 0; i0 < p.n; i0 += threads) {
-    const uint32_t i = i0 + id;
-    a = ask(p, i);
+  for (uint32_t i0 = 0; i0 < p.n; i0 += step) {
+    const uint32_t i = i0 + at;
+    a = ask(p, i, threadIdx.x < per && i < p.n);
     if (a.shares()) {
       shares = true;
       const uint32_t same = __match_any_sync(__activemask(), a.last);
@@ -808,73 +831,89 @@ __global__ void __launch_bounds__(kTeamThreads) page_extend_kernel(const ExtendP
     }
   }
   if (kSolo) shares = __syncthreads_or(shares); else team.sync();
-  uint64_t need = 0;
-  uint32_t n_moves = 0;
-  for (uint32_t i0 = 0; i0 < p.n; i0 += threads) {
-    const uint32_t i = i0 + id;
-    if (!one) a = ask(p, i);
-    uint32_t cow = 0;
+  uint32_t need = 0, n_moves = 0, move = kNoMove;
+  for (uint32_t i0 = 0; i0 < p.n; i0 += step) {
+    const uint32_t i = i0 + at;
+    const bool mine = threadIdx.x < per && i < p.n;
+    if (!one) a = ask(p, i, mine);
+    bool cow = false;
     if ((!kSolo || shares) && a.shares())
       cow = !(__ldcg(&p.w.holders[a.last]) == a.refs && __ldcg(&p.w.latest[a.last]) == i);
-    Sum total;
-    const Sum x = team.scan(Sum{(uint64_t)a.grow + cow, cow}, &total);
-    if (i < p.n) {
-      const Plan pl = {a.seq, a.had - cow, (uint32_t)min(need + x.a, (uint64_t)0xFFFFFFFFu),
-                       cow ? n_moves + x.b : kNoMove};
-      st_plan(&p.w.plan[i], pl);
+    uint32_t total, copies = 0, rank = 0, x;
+    if (!kSolo || shares)
+      x = team.template scan<true>(a.grow + cow, &total, cow, &rank, &copies);
+    else
+      x = team.template scan<false>(a.grow, &total);
+    move = cow ? n_moves + rank : kNoMove;
+    if (mine) {
+      const Plan pl = {a.seq, a.had - cow, need + x, move};
       if (kSolo) {
-        st_plan(&s_plan[i], pl);
+        s_plan[i] = pl;
         s_start[i] = pl.end;
       }
+      if (!kSolo || p.rest) st_plan(&p.w.plan[i], pl);
     }
-    need += total.a;
-    n_moves += total.b;
+    need += total;
+    n_moves += copies;
   }
   const bool go = need <= bits.total;
-  const bool own = !p.rest || need <= (uint64_t)kOwnPages * threads;
+  const bool own = !p.rest || need <= kOwnPages * team.threads();
   if (id == 0) {
     *p.n_moves = go ? n_moves : 0;
-    p.w.head->units = go && !own ? (uint32_t)need : 0;
+    if (p.rest) p.w.head->units = go && !own ? need : 0;
     if (p.ctr) p.ctr->total = need;
   }
-  // The words as they were, to find the pages in, and without those taken.
-  if (go && need) {
-    const uint32_t stop = (uint32_t)need;
-    const Finder f = finder_of(s_word, words);
-    each_word(bits, p.t.free, p.t.n_pages, [&](uint32_t w, uint32_t free, uint32_t before) {
-      if (w >= words) return;
+  // The words up to the last one used as they were, to find the pages in, and
+  // without those taken.
+  if (go && need && bits.before < need)
+    each_quad(bits, p.t.free, p.t.n_pages, [&](uint32_t w, const uint4& v, const uint4& before) {
+      if (before.x >= need) return false;
       if (kSolo) {
-        s_before[w] = before;
-        s_bits[w] = free;
-        if (w % f.step == 0) s_word[w / f.step] = before;
+        st_quad(s_before, w, words, before);
+        st_quad(s_bits, w, words, v);
       }
       if (!kSolo || !own) {
-        p.w.before[w] = before;
-        p.w.bits[w] = free;
+        st_quad(p.w.before, w, words, before);
+        st_quad(p.w.bits, w, words, v);
       }
-      if (free && before < stop) {
-        uint32_t left = 0;
-        if (before + __popc(free) > stop)
-          left = free & ~((2u << nth_bit(free, stop - before - 1)) - 1);
-        p.t.free[w] = left;
+      const uint32_t end = before.w + __popc(v.w);
+      uint4 left = make_uint4(0, 0, 0, 0);
+      if (end >= need) {  // the last quad used
+        const uint32_t vs[4] = {v.x, v.y, v.z, v.w}, bs[4] = {before.x, before.y, before.z, before.w};
+        uint32_t ls[4];
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k) {
+          ls[k] = 0;
+          if (bs[k] >= need) {
+            ls[k] = vs[k];
+          } else if (bs[k] + __popc(vs[k]) >= need) {
+            ls[k] = vs[k] & ~((2u << nth_bit(vs[k], need - bs[k] - 1)) - 1);
+            (kSolo ? s_used : p.w.head->used) = w + k + 1;
+            if (kSolo && !own) p.w.head->used = w + k + 1;
+          }
+        }
+        left = make_uint4(ls[0], ls[1], ls[2], ls[3]);
       }
+      st_quad(p.t.free, w, words, left);
+      return true;
     });
-  }
   // Every request has been asked before the last scan. Lengths, moves and
   // status, and the workspace as the next call wants it.
   uint32_t invalid = 0, refused = 0;
   bool corrupt = false;
-  for (uint32_t i = id; i < p.n; i += threads) {
-    if (!one) a = ask(p, i);
-    const uint32_t m = kSolo ? s_plan[i].aux : p.w.plan[i].aux;
-    if (m != kNoMove) {  // at least one holder of every shared page copies, and clears for all
+  for (uint32_t i = at; threadIdx.x < per && i < p.n; i += step) {
+    if (!one) {
+      a = ask(p, i, true);
+      move = p.w.plan[i].aux;
+    }
+    if (move != kNoMove) {  // at least one holder of every shared page copies, and clears for all
       p.w.holders[a.last] = 0;
       p.w.latest[a.last] = 0;
       if (go) {
         const uint32_t same = __match_any_sync(__activemask(), a.last);
         if ((same & lanemask_lt()) == 0) atomicSub(&p.t.refs[a.last], (uint32_t)__popc(same));
-        p.moves[m].src = a.last;
-        *reinterpret_cast<uint2*>(&p.moves[m].tokens) = make_uint2(a.part, 0);
+        p.moves[move].src = a.last;
+        *reinterpret_cast<uint2*>(&p.moves[move].tokens) = make_uint2(a.part, 0);
       }
     }
     if (a.mine) p.w.claim[a.seq] = 0;
@@ -892,27 +931,30 @@ __global__ void __launch_bounds__(kTeamThreads) page_extend_kernel(const ExtendP
   team.sync();  // plan and words are known, and the replaced entries have been read
   if (!go || !need || !own) return;
   if (kSolo) {
-    place_pages(p, Finder{s_start, p.n, p.n, 1}, s_plan, finder_of(s_word, words), s_before, s_bits,
-                id, threads, (uint32_t)need);
+    const uint32_t used = s_used;
+    place_pages(p, Finder{s_start, p.n, p.n, 1}, s_plan, Finder{s_before, used, used, 1}, s_before,
+                s_bits, id, kThreads, need);
   } else {
-    const Finder r = load_finder(s_start, p.n, PlanStart{p.w.plan});
-    const Finder f = load_finder(s_word, words, WordStart{p.w.before});
+    const Finder r = load_finder(s_start, kTeamSearch, p.n, PlanStart{p.w.plan});
+    const Finder f = load_finder(s_before, kWords, __ldcg(&p.w.head->used), WordStart{p.w.before});
     __syncthreads();
-    place_pages(p, r, p.w.plan, f, p.w.before, p.w.bits, id, threads, (uint32_t)need);
+    place_pages(p, r, p.w.plan, f, p.w.before, p.w.bits, id, team.threads(), need);
   }
 }
 
-__global__ void __launch_bounds__(256) page_place_kernel(const ExtendParams p) {
+constexpr uint32_t kPlaceThreads = 256;
+
+__global__ void __launch_bounds__(kPlaceThreads) page_place_kernel(const ExtendParams p) {
   __shared__ uint32_t s_start[kSearch], s_word[kSearch];
   wait_for_prerequisites();
   dependents_may_launch();
   const uint32_t total = p.w.head->units;
-  if (blockIdx.x * 256 >= total) return;
-  const Finder r = load_finder(s_start, p.n, PlanStart{p.w.plan});
-  const Finder f = load_finder(s_word, (p.t.n_pages + 31) / 32, WordStart{p.w.before});
+  if (blockIdx.x * kPlaceThreads >= total) return;
+  const Finder r = load_finder(s_start, kSearch, p.n, PlanStart{p.w.plan});
+  const Finder f = load_finder(s_word, kSearch, p.w.head->used, WordStart{p.w.before});
   __syncthreads();
-  place_pages(p, r, p.w.plan, f, p.w.before, p.w.bits, blockIdx.x * 256 + threadIdx.x,
-              gridDim.x * 256, total);
+  place_pages(p, r, p.w.plan, f, p.w.before, p.w.bits, blockIdx.x * kPlaceThreads + threadIdx.x,
+              gridDim.x * kPlaceThreads, total);
 }
 
 // ------------------------------------------------------------------- compact
@@ -922,6 +964,8 @@ struct CompactParams {
   uint32_t cap;
   uint32_t* n_moves;
   db_counters* ctr;
+  bool rest;   // moves are left to a second kernel
+  bool whole;  // the planning CTA does everything
   Work w;
 };
 
@@ -931,46 +975,20 @@ struct LiveStart {
   __device__ __forceinline__ uint32_t operator()(uint32_t w) const { return 32 * w - before[w]; }
 };
 
-template <bool kSolo>
-__global__ void __launch_bounds__(kTeamThreads) page_compact_plan_kernel(const CompactParams p) {
-  __shared__ TeamShared s_team;
-  __shared__ uint32_t s_word[kSearch], s_live[kSearch];
-  wait_for_prerequisites();
-  dependents_may_launch();
-  Team<kSolo> team(&s_team);
-  const uint32_t id = team.id(), threads = team.threads();
-  const uint32_t n_pages = p.t.n_pages, words = (n_pages + 31) / 32;
-  const Bits bits = scan_free(team, p.t.free, n_pages);
-  const uint32_t n_live = n_pages - bits.total;
-  // M, the free pages below n_live: known to the thread that has the word.
-  each_word(bits, p.t.free, n_pages, [&](uint32_t w, uint32_t free, uint32_t before) {
-    if (w >= words) return;
-    p.w.before[w] = before;
-    if (w == n_live / 32)
-      p.w.head->holes = before + __popc(free & ((1u << (n_live & 31)) - 1));
-  });
-  if (n_live == n_pages && id == 0) p.w.head->holes = 0;
-  team.sync();
-  const uint32_t holes = __ldcg(&p.w.head->holes), moved = min(holes, p.cap);
-  if (id == 0) {
-    *p.n_moves = moved;
-    p.w.head->moved = moved;
-    if (moved == 0) {
-      p.w.head->src_first = n_pages;
-      p.w.head->dst_last = 0;
-    }
-    if (p.ctr) *p.ctr = db_counters{holes, 0, (uint64_t)holes - moved, 0};
-  }
-  if (!moved) return;
-  const Finder f = load_finder(s_word, words, WordStart{p.w.before});
-  const Finder g = load_finder(s_live, words, LiveStart{p.w.before});
+// Move k: the k-th free page gets the k-th live one from above.
+__device__ __forceinline__ void make_moves(const CompactParams& p, uint32_t* s_word,
+                                           uint32_t* s_live, uint32_t n_live, uint32_t moved,
+                                           uint32_t first, uint32_t stride) {
+  const uint32_t words = (p.t.n_pages + 31) / 32;
+  const Finder f = load_finder(s_word, kSearch, words, WordStart{p.w.before});
+  const Finder g = load_finder(s_live, kSearch, words, LiveStart{p.w.before});
   __syncthreads();
-  for (uint32_t k = id; k < moved; k += threads) {
-    // the k-th free page, and the k-th live one from above
+  for (uint32_t k = first; k < moved; k += stride) {
     const uint32_t v = f.find(k, WordStart{p.w.before});
-    const uint32_t dst = 32 * v + nth_bit(ld_word(p.t.free, v, n_pages), k - p.w.before[v]);
+    const uint32_t dst = 32 * v + nth_bit(ld_word(p.t.free, v, p.t.n_pages), k - p.w.before[v]);
     const uint32_t e = n_live - 1 - k, w = g.find(e, LiveStart{p.w.before});
-    const uint32_t src = 32 * w + nth_bit(~ld_word(p.t.free, w, n_pages), e - (32 * w - p.w.before[w]));
+    const uint32_t src =
+        32 * w + nth_bit(~ld_word(p.t.free, w, p.t.n_pages), e - (32 * w - p.w.before[w]));
     *reinterpret_cast<uint4*>(&p.moves[k]) = make_uint4(src, dst, DB_PAGE_ALL, 0);
     p.w.renamed[src] = dst;
     p.out.refs[dst] = p.t.refs[src];
@@ -982,33 +1000,63 @@ __global__ void __launch_bounds__(kTeamThreads) page_compact_plan_kernel(const C
   }
 }
 
-__global__ void __launch_bounds__(256) page_compact_apply_kernel(const CompactParams p) {
-  wait_for_prerequisites();
-  dependents_may_launch();
-  const uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x, step = (uint64_t)gridDim.x * 256;
-  const uint32_t n_pages = p.t.n_pages;
-  const uint32_t moved = __ldcg(&p.w.head->moved), src_first = __ldcg(&p.w.head->src_first);
-  const uint32_t dst_last = __ldcg(&p.w.head->dst_last);
-  const uint64_t entries = (uint64_t)p.t.n_seqs * p.t.columns;
-  bool bad = false;
-  for (uint64_t e = id; e < entries; e += step) {
-    const uint32_t was = (uint32_t)p.t.table[e];
-    uint32_t is = was;
-    if (was >= src_first && was != (uint32_t)DB_PAGE_NONE) {
-      if (was < n_pages) is = __ldcg(&p.w.renamed[was]); else bad = true;
+// An array of n words from `in` to `out` through f, four at a time where both
+// are aligned. f(index, word) may have out's word left as it is by `keep`.
+template <typename F>
+__device__ __forceinline__ void rewrite(const uint32_t* in, uint32_t* out, uint64_t n, uint64_t id,
+                                        uint64_t step, F f) {
+  uint64_t done = 0;
+  if ((((uintptr_t)in | (uintptr_t)out) & 15) == 0) {
+    done = n & ~3ull;
+    for (uint64_t q = 4 * id; q < done; q += 4 * step) {
+      const uint4 was = *reinterpret_cast<const uint4*>(in + q);
+      uint4 is = was;
+      bool skip = false;
+      f(q, &is.x, &skip);
+      f(q + 1, &is.y, &skip);
+      f(q + 2, &is.z, &skip);
+      f(q + 3, &is.w, &skip);
+      if (skip) {  // words that are written elsewhere: each for itself
+        for (uint32_t k = 0; k < 4; ++k) {
+          uint32_t v = k == 0 ? was.x : k == 1 ? was.y : k == 2 ? was.z : was.w;
+          bool leave = false;
+          f(q + k, &v, &leave);
+          if (!leave) out[q + k] = v;
+        }
+      } else if (in != out || is.x != was.x || is.y != was.y || is.z != was.z || is.w != was.w) {
+        *reinterpret_cast<uint4*>(out + q) = is;
+      }
     }
-    if (p.out.table != p.t.table || is != was) p.out.table[e] = (int32_t)is;
   }
+  for (uint64_t q = done + id; q < n; q += step) {
+    const uint32_t was = in[q];
+    uint32_t is = was;
+    bool skip = false;
+    f(q, &is, &skip);
+    if (!skip && (in != out || is != was)) out[q] = is;
+  }
+}
+
+// Tables, references, free bits and lengths after the moves.
+__device__ __forceinline__ void apply_moves(const CompactParams& p, uint32_t moved,
+                                            uint32_t src_first, uint32_t dst_last, uint64_t id,
+                                            uint64_t step) {
+  const uint32_t n_pages = p.t.n_pages, words = (n_pages + 31) / 32;
+  bool bad = false;
+  rewrite((const uint32_t*)p.t.table, (uint32_t*)p.out.table, (uint64_t)p.t.n_seqs * p.t.columns,
+          id, step, [&](uint64_t, uint32_t* v, bool*) {
+            if (*v >= src_first && *v != (uint32_t)DB_PAGE_NONE) {
+              if (*v < n_pages) *v = p.w.renamed[*v]; else bad = true;
+            }
+          });
   if (p.ctr) add_error(p.ctr, bad);
   if (p.out.refs != p.t.refs)
-    for (uint64_t q = id; q < n_pages; q += step) {
-      const uint32_t v = p.t.refs[q];
+    rewrite(p.t.refs, p.out.refs, n_pages, id, step, [&](uint64_t q, uint32_t* v, bool* skip) {
       if (q >= src_first)
-        p.out.refs[q] = 0;
-      else if (v || !moved || q > dst_last)  // the plan wrote the pages moved to
-        p.out.refs[q] = v;
-    }
-  const uint32_t words = (n_pages + 31) / 32;
+        *v = 0;
+      else if (!*v && moved && q <= dst_last)
+        *skip = true;  // moved to: written with the move
+    });
   for (uint64_t w = id; w < words; w += step) {
     uint32_t v = p.t.free[w];
     const uint64_t at = 32 * w;
@@ -1029,12 +1077,72 @@ __global__ void __launch_bounds__(256) page_compact_apply_kernel(const CompactPa
     for (uint64_t s = id; s < p.t.n_seqs; s += step) p.out.length[s] = p.t.length[s];
 }
 
+template <uint32_t kThreads, bool kSolo>
+__global__ void __launch_bounds__(kThreads) page_compact_plan_kernel(const CompactParams p) {
+  __shared__ TeamShared s_team;
+  __shared__ uint32_t s_word[kSearch], s_live[kSearch];
+  Team<kThreads, kSolo> team(&s_team);
+  wait_for_prerequisites();
+  dependents_may_launch();
+  const uint32_t id = team.id(), n_pages = p.t.n_pages, words = (n_pages + 31) / 32;
+  team.started();
+  const Bits bits = scan_free(team, p.t.free, n_pages);
+  const uint32_t n_live = n_pages - bits.total;
+  // M, the free pages below n_live: known to the thread that has the word.
+  each_quad(bits, p.t.free, n_pages, [&](uint32_t w, const uint4& v, const uint4& before) {
+    st_quad(p.w.before, w, words, before);
+    if (n_live / 32 >= w && n_live / 32 < w + 4) {
+      const uint32_t k = n_live / 32 - w, x = k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w;
+      p.w.head->holes = (k == 0 ? before.x : k == 1 ? before.y : k == 2 ? before.z : before.w) +
+                        __popc(x & ((1u << (n_live & 31)) - 1));
+    }
+    return true;
+  });
+  team.sync();
+  const uint32_t holes = n_live == n_pages ? 0 : __ldcg(&p.w.head->holes);
+  const uint32_t moved = min(holes, p.cap);
+  if (id == 0) {
+    *p.n_moves = moved;
+    p.w.head->moved = moved;
+    p.w.head->n_live = n_live;
+    if (moved == 0) {
+      p.w.head->src_first = n_pages;
+      p.w.head->dst_last = 0;
+    }
+    if (p.ctr) *p.ctr = db_counters{holes, 0, (uint64_t)holes - moved, 0};
+  }
+  if (p.rest) return;
+  if (moved) make_moves(p, s_word, s_live, n_live, moved, id, team.threads());
+  if (!kSolo || !p.whole) return;
+  __syncthreads();
+  apply_moves(p, moved, p.w.head->src_first, p.w.head->dst_last, id, kThreads);
+}
+
+__global__ void __launch_bounds__(256) page_compact_moves_kernel(const CompactParams p) {
+  __shared__ uint32_t s_word[kSearch], s_live[kSearch];
+  wait_for_prerequisites();
+  dependents_may_launch();
+  const uint32_t moved = p.w.head->moved;
+  if (blockIdx.x * 256 >= moved) return;
+  make_moves(p, s_word, s_live, p.w.head->n_live, moved, blockIdx.x * 256 + threadIdx.x,
+             gridDim.x * 256);
+}
+
+__global__ void __launch_bounds__(256) page_compact_apply_kernel(const CompactParams p) {
+  wait_for_prerequisites();
+  dependents_may_launch();
+  apply_moves(p, p.w.head->moved, p.w.head->src_first, p.w.head->dst_last,
+              (uint64_t)blockIdx.x * 256 + threadIdx.x, (uint64_t)gridDim.x * 256);
+}
+
 // ---------------------------------------------------------------- host side
 template <typename P>
-int launch_team(void (*kernel)(P), uint32_t ctas, cudaStream_t s, const P& params) {
+int launch_team(void (*kernel)(P), uint32_t ctas, uint32_t threads, cudaStream_t s,
+                const P& params) {
+  if (ctas == 1) return launch_dependent(kernel, 1, threads, 0, s, params);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kTeamThreads);
+  cfg.blockDim = dim3(threads);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1045,7 +1153,6 @@ int launch_team(void (*kernel)(P), uint32_t ctas, cudaStream_t s, const P& param
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (ctas > 8) cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, params);
   if (e != cudaSuccess) return cuda_failure(e);
   return launch_result();
@@ -1068,6 +1175,7 @@ int check_call(const db_page_tables* t, const void* req, uintptr_t req_align, ui
   if (!ws || !aligned(ws, 256) || !aligned(ctr, 8)) return -EINVAL;
   if (n && (!req || !aligned(req, req_align))) return -EINVAL;
   if (n > t->n_seqs) return -EINVAL;
+  if ((uint64_t)n * t->columns > 0xFFFFFFFFull) return -EINVAL;  // entries are counted in 32 bits
   if (ws_bytes < carve(nullptr, t->n_seqs, t->n_pages, nullptr)) return -ENOSPC;
   carve((char*)ws, t->n_seqs, t->n_pages, w);
   return 0;
@@ -1092,23 +1200,24 @@ uint32_t team_size(uint64_t threads) {
   while (c < kMaxTeam && (uint64_t)c * kTeamThreads < threads) c *= 2;
   return c;
 }
-inline uint64_t most_of(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
-// CTAs of 256 threads for at most `threads`.
-unsigned whole_grid(uint64_t threads) {
-  const uint64_t want = (threads + 255) / 256, most = 4ull * num_sms();
+// CTAs of `block` threads for at most `threads`, at most `each` an SM.
+unsigned whole_grid(uint64_t threads, uint32_t block, uint32_t each) {
+  const uint64_t want = (threads + block - 1) / block, most = (uint64_t)each * num_sms();
   return (unsigned)(want < 1 ? 1 : want < most ? want : most);
 }
 
 // Free and fork: the team, and the whole GPU where there may be much to do.
 template <typename P>
-int launch_rows(void (*solo)(P), void (*team)(P), void (*rest)(P), cudaStream_t s, P& p) {
+int launch_rows(void (*small)(P), void (*solo)(P), void (*team)(P), void (*rest)(P),
+                cudaStream_t s, P& p) {
   const uint64_t units = ((uint64_t)p.r.n + kRows - 1) / kRows * (((uint64_t)p.r.t.columns + 31) / 32);
   const uint32_t ctas = team_size(p.r.n);
   p.r.rest = units > kRestUnits;
-  const int e = launch_team(ctas == 1 ? solo : team, ctas, s, p);
+  const int e = p.r.n <= kSmallThreads ? launch_team(small, 1, kSmallThreads, s, p)
+                                       : launch_team(ctas == 1 ? solo : team, ctas, kTeamThreads, s, p);
   if (e || !p.r.rest) return e;
-  return launch_dependent(rest, whole_grid(units * 32), 256, 0, s, p);
+  return launch_dependent(rest, whole_grid(units * 32, kUnitThreads, 8), kUnitThreads, 0, s, p);
 }
 
 }  // namespace
@@ -1130,13 +1239,13 @@ extern "C" int db_page_free(const db_page_tables* t, const db_page_cut* req, uin
   if (rc) return rc;
   const cudaStream_t s = (cudaStream_t)stream;
   if (!n) return nothing(ctr, nullptr, s);
-  if ((uint64_t)n * t->columns > 0xFFFFFFFFull) return -EINVAL;  // entries are numbered in 32 bits
   p.r.t = *t;
   p.r.n = n;
   p.r.status = status;
   p.r.ctr = ctr;
   p.req = req;
-  return launch_rows(page_free_kernel<true>, page_free_kernel<false>, page_free_units_kernel, s, p);
+  return launch_rows(page_free_kernel<kSmallThreads, true>, page_free_kernel<kTeamThreads, true>,
+                     page_free_kernel<kTeamThreads, false>, page_free_units_kernel, s, p);
 }
 
 extern "C" int db_page_fork(const db_page_tables* t, const db_page_fork_req* req, uint32_t n,
@@ -1147,20 +1256,20 @@ extern "C" int db_page_fork(const db_page_tables* t, const db_page_fork_req* req
   if (rc) return rc;
   const cudaStream_t s = (cudaStream_t)stream;
   if (!n) return nothing(ctr, nullptr, s);
-  if ((uint64_t)n * t->columns > 0xFFFFFFFFull) return -EINVAL;  // entries are numbered in 32 bits
   p.r.t = *t;
   p.r.n = n;
   p.r.status = status;
   p.r.ctr = ctr;
   p.req = req;
-  return launch_rows(page_fork_kernel<true>, page_fork_kernel<false>, page_fork_units_kernel, s, p);
+  return launch_rows(page_fork_kernel<kSmallThreads, true>, page_fork_kernel<kTeamThreads, true>,
+                     page_fork_kernel<kTeamThreads, false>, page_fork_units_kernel, s, p);
 }
 
 extern "C" int db_page_extend(const db_page_tables* t, const db_page_grow* req, uint32_t n,
                               db_page_move* moves, uint32_t* n_moves, uint8_t* status,
                               db_counters* ctr, void* ws, size_t ws_bytes, void* stream) {
   ExtendParams p = {};
-  const int rc = check_call(t, req, 8, n, ctr, ws, ws_bytes, &p.w);
+  const int rc = check_call(t, req, sizeof(*req), n, ctr, ws, ws_bytes, &p.w);
   if (rc) return rc;
   if (!n_moves || !aligned(n_moves, 4) || (n && (!moves || !aligned(moves, 16)))) return -EINVAL;
   const cudaStream_t s = (cudaStream_t)stream;
@@ -1174,11 +1283,20 @@ extern "C" int db_page_extend(const db_page_tables* t, const db_page_grow* req, 
   p.ctr = ctr;
   const uint64_t pages = (uint64_t)n * t->columns < t->n_pages ? (uint64_t)n * t->columns : t->n_pages;
   const uint32_t words = (t->n_pages + 31) / 32;
-  const uint32_t ctas = team_size(words > kSoloWords ? most_of(n, words / 4) + kTeamThreads : n);
   p.rest = pages > kRestPages;
-  const int e = launch_team(ctas == 1 ? page_extend_kernel<true> : page_extend_kernel<false>, ctas, s, p);
+  int e;
+  if (n <= kSmallThreads && words <= kSoloWords<kSmallThreads>) {
+    e = launch_team(page_extend_kernel<kSmallThreads, true>, 1, kSmallThreads, s, p);
+  } else if (n <= kTeamThreads && words <= kSoloWords<kTeamThreads>) {
+    e = launch_team(page_extend_kernel<kTeamThreads, true>, 1, kTeamThreads, s, p);
+  } else {
+    uint32_t ctas = team_size(n > words / 4 ? n : words / 4);
+    if (ctas == 1) ctas = 2;
+    e = launch_team(page_extend_kernel<kTeamThreads, false>, ctas, kTeamThreads, s, p);
+  }
   if (e || !p.rest) return e;
-  return launch_dependent(page_place_kernel, whole_grid(pages), 256, 0, s, p);
+  return launch_dependent(page_place_kernel, whole_grid(pages, kPlaceThreads, 8), kPlaceThreads, 0,
+                          s, p);
 }
 
 extern "C" int db_page_compact(const db_page_tables* t, const db_page_tables* out,
@@ -1200,11 +1318,16 @@ extern "C" int db_page_compact(const db_page_tables* t, const db_page_tables* ou
   p.n_moves = n_moves;
   p.ctr = ctr;
   const cudaStream_t s = (cudaStream_t)stream;
-  const uint32_t ctas = team_size(((uint64_t)t->n_pages + 31) / 32);
-  const int e = launch_team(ctas == 1 ? page_compact_plan_kernel<true> : page_compact_plan_kernel<false>,
-                            ctas, s, p);
-  if (e) return e;
   const uint64_t entries = (uint64_t)t->n_seqs * t->columns;
-  return launch_dependent(page_compact_apply_kernel,
-                          whole_grid(entries > t->n_pages ? entries : t->n_pages), 256, 0, s, p);
+  const uint32_t most = cap < t->n_pages / 2 ? cap : t->n_pages / 2;
+  const uint32_t ctas = team_size(((uint64_t)t->n_pages + 127) / 128);
+  p.rest = most > kRestMoves;
+  p.whole = ctas == 1 && !p.rest && entries <= kSoloEntries;
+  int e = ctas == 1 ? launch_team(page_compact_plan_kernel<kTeamThreads, true>, 1, kTeamThreads, s, p)
+                    : launch_team(page_compact_plan_kernel<kTeamThreads, false>, ctas, kTeamThreads, s, p);
+  if (e || p.whole) return e;
+  if (p.rest) e = launch_dependent(page_compact_moves_kernel, whole_grid(most, 256, 8), 256, 0, s, p);
+  if (e) return e;
+  const uint64_t work = entries > t->n_pages ? entries : t->n_pages;
+  return launch_dependent(page_compact_apply_kernel, whole_grid((work + 3) / 4, 256, 8), 256, 0, s, p);
 }

@@ -116,7 +116,7 @@ int db_page_workspace_size(uint32_t n_seqs, uint32_t n_pages, size_t* bytes);
  *   ctr     NULL or counters: total = pages the valid requests need. With
  *           fewer free pages than that the batch changes nothing: n_overflow
  *           = the valid requests, their status DB_PAGE_SHORT, *n_moves = 0.
- * n <= n_seqs. */
+ * n <= n_seqs, n * columns < 2^32. */
 int db_page_extend(const db_page_tables* t, const db_page_grow* req, uint32_t n,
                    db_page_move* moves, uint32_t* n_moves, uint8_t* status, db_counters* ctr,
                    void* ws, size_t ws_bytes, void* stream);
