@@ -572,23 +572,26 @@ def _strides(shape, stride, item: int) -> tuple[int, int]:
 
 
 @functools.lru_cache(maxsize=1024)
-def _copy_plan(src_shape, src_stride, dst_shape, dst_stride, item: int, token_dim):
-    """What a copy's pools have in common and their strides, from their shapes alone."""
-    if src_shape[0] != dst_shape[0] or src_shape[2:] != dst_shape[2:]:
-        raise ValueError("source and destination pools differ in planes or page shape")
-    a, b = _strides(src_shape, src_stride, item), _strides(dst_shape, dst_stride, item)
-    page = src_shape[2:]
+def _copy_plan(shape, stride, item: int, token_dim, dst_shape=None, dst_stride=None):
+    """What a copy's pools have in common and their strides, from their shapes
+    alone (without dst_shape they are one pool)."""
+    a = b = _strides(shape, stride, item)
+    if dst_shape is not None:
+        if shape[0] != dst_shape[0] or shape[2:] != dst_shape[2:]:
+            raise ValueError("source and destination pools differ in planes or page shape")
+        b = _strides(dst_shape, dst_stride, item)
+    page = shape[2:]
     if token_dim is None:
         segments, page_tokens, k = 1, 1, 0
     else:
-        if not 2 <= token_dim < len(src_shape):
+        if not 2 <= token_dim < len(shape):
             raise ValueError("token_dim must be one of a page's axes (2 and up)")
         k = token_dim - 1
         segments, page_tokens = math.prod(page[:k - 1]), page[k - 1]
-    if math.prod(page) * item * src_shape[0] > 1 << 31:
+    if math.prod(page) * item * shape[0] > 1 << 31:
         raise ValueError("a page has at most 2^31 bytes in all planes")
-    shape = _Shape(src_shape[0], segments, page_tokens, math.prod(page[k:]) * item)
-    return shape, ctypes.byref(shape), a, b
+    form = _Shape(shape[0], segments, page_tokens, math.prod(page[k:]) * item)
+    return form, ctypes.byref(form), a, b
 
 
 def page_copy(moves: torch.Tensor, n_moves: torch.Tensor, src: torch.Tensor, dst: torch.Tensor,
@@ -600,11 +603,17 @@ def page_copy(moves: torch.Tensor, n_moves: torch.Tensor, src: torch.Tensor, dst
     ...], on the GPU or in pinned host memory, strided in the first two axes;
     ``token_dim`` is the axis of a page's tokens, None when it has none (then
     every move takes whole pages)."""
-    if src.dtype != dst.dtype:
-        raise ValueError("source and destination pools differ in type")
-    shape, ref, a, b = _copy_plan(src.shape, src.stride(), dst.shape, dst.stride(),
-                                  src.element_size(), token_dim)
+    shape = src.shape
+    if dst is src:
+        _, form, a, _ = _copy_plan(shape, src.stride(), src.element_size(), token_dim)
+        here = there = ctypes.byref(_Pool(src.data_ptr(), shape[1], *a))
+    else:
+        if src.dtype != dst.dtype:
+            raise ValueError("source and destination pools differ in type")
+        _, form, a, b = _copy_plan(shape, src.stride(), src.element_size(), token_dim, dst.shape,
+                                   dst.stride())
+        here = ctypes.byref(_Pool(src.data_ptr(), shape[1], *a))
+        there = ctypes.byref(_Pool(dst.data_ptr(), dst.shape[1], *b))
     _check("db_page_copy", _lib.db_page_copy(
-        _ptr(moves), _requests(moves, 16), _ptr(n_moves),
-        ctypes.byref(_Pool(src.data_ptr(), src.shape[1], *a)),
-        ctypes.byref(_Pool(dst.data_ptr(), dst.shape[1], *b)), ref, _ptr(ctr), _stream(stream)))
+        _ptr(moves), _requests(moves, 16), _ptr(n_moves), here, there, form, _ptr(ctr),
+        _stream(stream)))

@@ -24,20 +24,19 @@ constexpr uint32_t kTeamThreads = 1024; // threads of a CTA of a cluster
 constexpr uint32_t kSmallThreads = 256; // threads of the smallest team
 constexpr uint32_t kRows = 8;           // requests of a group (see "row units")
 constexpr uint32_t kSearch = 1024;      // starts that a second kernel keeps in shared memory
-constexpr uint32_t kTeamSearch = 4096;  // starts that a CTA of a cluster keeps
-constexpr uint32_t kOwnUnits = 8;       // units that a team does itself, for each of its CTAs,
-constexpr uint32_t kOwnPages = 4;       // and pages, for each of its threads, when a second
-constexpr uint32_t kRestUnits = 64;     // kernel is there: where the sizes of the call allow for
-constexpr uint32_t kRestPages = 16384;  // more than kRestUnits, kRestPages or kRestMoves
+constexpr uint32_t kOwnEntries = 1024;  // entries that a team does itself, for each of its CTAs, and
+constexpr uint32_t kOwnPages = 4096;    // pages, when a second kernel is there: where the sizes of
+constexpr uint32_t kRestUnits = 64;     // the call allow for more than kRestUnits, kRestPages or
+constexpr uint32_t kRestPages = 16384;  // kRestMoves
 constexpr uint32_t kRestMoves = 8192;
 constexpr uint32_t kSoloEntries = 32768;  // table entries that a compaction's one CTA renames itself
 constexpr uint32_t kNoMove = 0xFFFFFFFFu;
 constexpr uint32_t kNoEntry = 0xFFFFFFFEu;   // a row without an entry in the column
 constexpr uint32_t kBadEntry = 0xFFFFFFFFu;  // no page
 
-// Free words that a team of one CTA keeps in shared memory.
+// Free words that a CTA of a team keeps in shared memory.
 template <uint32_t kThreads>
-constexpr uint32_t kSoloWords = kThreads == kSmallThreads ? 1024 : 2048;
+constexpr uint32_t kTeamWords = kThreads == kSmallThreads ? 1024 : 2048;
 
 // One request's place in the plan.
 struct __align__(16) Plan {
@@ -134,13 +133,13 @@ struct Team {
                        : "memory");
     }
   }
-  // Exclusive prefix of v in the order of CTAs and threads, and the sum; with
-  // kFlags also of a flag. Also a barrier of the team. The arrays of one scan
-  // are written again two scans later, past the barrier of the one between.
-  template <bool kFlags>
-  __device__ __forceinline__ uint32_t scan(uint32_t v, uint32_t* total, bool flag = false,
-                                           uint32_t* flag_rank = nullptr,
-                                           uint32_t* flag_total = nullptr) {
+  // Exclusive prefix of v in the order of CTAs and threads, and the sum; also
+  // the sum of w, and the number of threads before with w != 0, when kPair.
+  // Also a barrier of the team. The arrays of one scan are written again two
+  // scans later, past the barrier of the one between.
+  template <bool kPair>
+  __device__ __forceinline__ uint32_t scan(uint32_t v, uint32_t* total, uint32_t w = 0,
+                                           uint32_t* sum_w = nullptr, uint32_t* rank_w = nullptr) {
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = round++ & 1;
     uint32_t x = v;
 #pragma unroll
@@ -148,46 +147,56 @@ struct Team {
       const uint32_t y = __shfl_up_sync(kFull, x, o);
       if (lane >= (uint32_t)o) x += y;
     }
-    const uint32_t vote = kFlags ? __ballot_sync(kFull, flag) : 0;
+    const uint32_t ws = kPair ? __reduce_add_sync(kFull, w) : 0;
     if (lane == 31) {
       s->warp_a[k][warp] = x;
-      if (kFlags) s->warp_b[k][warp] = __popc(vote);
+      if (kPair) s->warp_b[k][warp] = ws;
     }
     __syncthreads();
     const uint32_t a = lane < kWarps ? s->warp_a[k][lane] : 0;
-    const uint32_t b = kFlags && lane < kWarps ? s->warp_b[k][lane] : 0;
+    const uint32_t b = kPair && lane < kWarps ? s->warp_b[k][lane] : 0;
     uint32_t base_a = __reduce_add_sync(kFull, lane < warp ? a : 0), base_b = 0;
-    if (kFlags) base_b = __reduce_add_sync(kFull, lane < warp ? b : 0);
+    if (rank_w) base_b = __reduce_add_sync(kFull, lane < warp ? b : 0);
     if (kSolo) {
       *total = __reduce_add_sync(kFull, a);
-      if (kFlags) *flag_total = __reduce_add_sync(kFull, b);
+      if (kPair) *sum_w = __reduce_add_sync(kFull, b);
     } else {
       if (warp == 0) {
         const uint32_t sum_a = __reduce_add_sync(kFull, a);
-        const uint32_t sum_b = kFlags ? __reduce_add_sync(kFull, b) : 0;
+        const uint32_t sum_b = kPair ? __reduce_add_sync(kFull, b) : 0;
         if (lane < size) {
           to_peer(&s->cta_a[k][rank], lane, sum_a);
-          if (kFlags) to_peer(&s->cta_b[k][rank], lane, sum_b);
+          if (kPair) to_peer(&s->cta_b[k][rank], lane, sum_b);
         }
       }
       sync();
       const uint32_t c = lane < size ? s->cta_a[k][lane] : 0;
       base_a += __reduce_add_sync(kFull, lane < rank ? c : 0);
       *total = __reduce_add_sync(kFull, c);
-      if (kFlags) {
+      if (kPair) {
         const uint32_t d = lane < size ? s->cta_b[k][lane] : 0;
-        base_b += __reduce_add_sync(kFull, lane < rank ? d : 0);
-        *flag_total = __reduce_add_sync(kFull, d);
+        if (rank_w) base_b += __reduce_add_sync(kFull, lane < rank ? d : 0);
+        *sum_w = __reduce_add_sync(kFull, d);
       }
     }
-    if (kFlags) *flag_rank = base_b + __popc(vote & lanemask_lt());
+    if (rank_w) *rank_w = base_b + __popc(__ballot_sync(kFull, w != 0) & lanemask_lt());
     return base_a + x - v;
   }
-  __device__ __forceinline__ static void to_peer(uint32_t* mine, uint32_t peer, uint32_t v) {
+  __device__ __forceinline__ static uint32_t peer_address(void* mine, uint32_t peer) {
     uint32_t at;
     asm("mapa.shared::cluster.u32 %0, %1, %2;"
         : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(mine)), "r"(peer));
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+    return at;
+  }
+  __device__ __forceinline__ static void to_peer(uint32_t* mine, uint32_t peer, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_address(mine, peer)), "r"(v) : "memory");
+  }
+  // A quad to the same place in every CTA.
+  __device__ __forceinline__ void to_all(uint32_t* mine, const uint4& v) const {
+    for (uint32_t c = 0; c < size; ++c)
+      asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(peer_address(mine, c)),
+                   "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                   : "memory");
   }
 };
 
@@ -308,20 +317,29 @@ struct Bits {
 };
 
 template <uint32_t kThreads, bool kSolo>
-__device__ __forceinline__ Bits scan_free(Team<kThreads, kSolo>& team, const uint32_t* bits,
+__device__ __forceinline__ Bits load_free(const Team<kThreads, kSolo>& team, const uint32_t* bits,
                                           uint32_t n_pages) {
   const uint32_t all = (n_pages + 31) / 32, threads = team.threads();
   Bits b;
   b.quads = (all + 4 * threads - 1) / (4 * threads);
   b.first = team.id() * b.quads * 4;
   b.v = ld_quad(bits, b.first, all, n_pages);
+  return b;
+}
+
+// The free pages before them, and a vote of the team.
+template <uint32_t kThreads, bool kSolo>
+__device__ __forceinline__ bool scan_free(Team<kThreads, kSolo>& team, Bits& b,
+                                          const uint32_t* bits, uint32_t n_pages, bool vote) {
+  const uint32_t all = (n_pages + 31) / 32;
   uint32_t c = __popc(b.v.x) + __popc(b.v.y) + __popc(b.v.z) + __popc(b.v.w);
   for (uint32_t s = 1; s < b.quads; ++s) {
     const uint4 v = ld_quad(bits, b.first + 4 * s, all, n_pages);
     c += __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w);
   }
-  b.before = team.template scan<false>(c, &b.total);
-  return b;
+  uint32_t votes;
+  b.before = team.template scan<true>(c, &b.total, vote, &votes);
+  return votes;
 }
 
 // f(first word, its quad, free pages before each of the four) for a thread's
@@ -377,44 +395,45 @@ struct Rows {
   Work w;
 };
 
-// What a team of one CTA keeps of its plan on chip.
-template <uint32_t kThreads, bool kSolo>
+// What a CTA keeps on chip of its requests' plan, of the last round.
+template <uint32_t kThreads>
 struct RowPlan {
-  Plan plan[kSolo ? kThreads : 1];
-  uint32_t col[kSolo ? kThreads / kRows : 1];
-  uint32_t start[kSolo ? kThreads / kRows : kTeamSearch];
+  Plan plan[kThreads];
+  uint32_t col[kThreads / kRows];
+  uint32_t start[kThreads / kRows];
+  uint32_t units;  // of this CTA
 };
 
 // Each thread's columns into the groups (visible past the next barrier).
-// `carry`: units before.
+// `units`, `entries`: those of the requests before, and then also of these.
 template <uint32_t kThreads, bool kSolo>
 __device__ __forceinline__ void plan_rows(Team<kThreads, kSolo>& team, const Rows& p,
-                                          RowPlan<kThreads, kSolo>* s, uint32_t i, bool mine,
-                                          const Plan& pl, uint32_t* carry) {
-  uint32_t lo = pl.from < pl.end ? pl.from : 0xFFFFFFFFu, hi = pl.from < pl.end ? pl.end : 0;
+                                          RowPlan<kThreads>* s, uint32_t i, bool mine,
+                                          const Plan& pl, uint32_t* units, uint32_t* entries) {
+  const uint32_t count = pl.from < pl.end ? pl.end - pl.from : 0;
+  uint32_t lo = count ? pl.from : 0xFFFFFFFFu, hi = count ? pl.end : 0;
 #pragma unroll
   for (uint32_t o = 1; o < kRows; o <<= 1) {
     lo = min(lo, __shfl_xor_sync(kFull, lo, o));
     hi = max(hi, __shfl_xor_sync(kFull, hi, o));
   }
   lo &= ~31u;
-  const bool first = mine && i % kRows == 0;
-  uint32_t total;
-  const uint32_t x = team.template scan<false>(first && hi > lo ? (hi - lo + 31) / 32 : 0, &total);
-  if (mine) {
-    if (kSolo) {
-      s->plan[i] = pl;
-      if (first) {
-        s->start[i / kRows] = x;
-        s->col[i / kRows] = lo;
-      }
-    }
-    if (!kSolo || p.rest) {
-      st_plan(&p.w.plan[i], pl);
-      if (first) p.w.group[i / kRows] = make_uint2(*carry + x, lo);
-    }
+  const bool lead = threadIdx.x % kRows == 0, first = mine && lead;
+  const uint32_t here = first && hi > lo ? (hi - lo + 31) / 32 : 0;
+  uint32_t total, total_entries;
+  const uint32_t x = team.template scan<true>(here, &total, count, &total_entries);
+  s->plan[threadIdx.x] = pl;
+  if (lead) {
+    s->start[threadIdx.x / kRows] = x;
+    s->col[threadIdx.x / kRows] = lo;
   }
-  *carry += total;
+  if (threadIdx.x == kThreads - kRows) s->units = x + here;  // past this CTA's last
+  if (mine && p.rest) {
+    st_plan(&p.w.plan[i], pl);
+    if (first) p.w.group[i / kRows] = make_uint2(*units + x, lo);
+  }
+  *units += total;
+  *entries += total_entries;
 }
 
 struct GroupStart {
@@ -422,7 +441,7 @@ struct GroupStart {
   __device__ __forceinline__ uint32_t operator()(uint32_t g) const { return group[g].x; }
 };
 
-// Where the units of a call are found: in the workspace, or in a RowPlan.
+// Where units are found: in the workspace, or among a CTA's own.
 struct Units {
   Finder f;
   const Plan* plan;
@@ -442,34 +461,29 @@ struct Units {
 };
 
 // The units of a plan in the workspace (a barrier follows).
-__device__ __forceinline__ Units find_units(const Rows& p, uint32_t* s_start, uint32_t most) {
+__device__ __forceinline__ Units find_units(const Rows& p, uint32_t* s_start) {
   Units x;
   x.plan = p.w.plan;
   x.group = p.w.group;
   x.col = nullptr;
   x.n = p.n;
-  x.f = load_finder(s_start, most, (p.n + kRows - 1) / kRows, GroupStart{p.w.group});
+  x.f = load_finder(s_start, kSearch, (p.n + kRows - 1) / kRows, GroupStart{p.w.group});
   return x;
 }
 
-// The end of a planning team: its own units, or their number for the second
-// kernel.
+// The end of a planning team: each CTA's own units, or all units to the second
+// kernel. A team that plans in more than one round always has one.
 template <uint32_t kThreads, bool kSolo, typename F>
-__device__ __forceinline__ void own_units(Team<kThreads, kSolo>& team, const Rows& p,
-                                          RowPlan<kThreads, kSolo>* s, uint32_t units, F work) {
-  const bool own = !p.rest || units <= kOwnUnits * team.size;
-  if (team.id() == 0 && p.rest) p.w.head->units = own ? 0 : units;
+__device__ __forceinline__ void own_units(const Team<kThreads, kSolo>& team, const Rows& p,
+                                          RowPlan<kThreads>* s, uint32_t units, uint32_t entries,
+                                          F work) {
+  const bool own = !p.rest || (p.n <= team.threads() && entries <= kOwnEntries * team.size);
+  if (p.rest && team.id() == 0) p.w.head->units = own ? 0 : units;
   if (!own || !units) return;
-  team.sync();
-  Units x;
-  if (kSolo) {
-    const uint32_t groups = (p.n + kRows - 1) / kRows;
-    x = Units{Finder{s->start, groups, groups, 1}, s->plan, nullptr, s->col, p.n};
-  } else {
-    x = find_units(p, s->start, kTeamSearch);
-    __syncthreads();
-  }
-  work(x, team.id() / 32, team.threads() / 32, units);
+  __syncthreads();
+  constexpr uint32_t kGroups = kThreads / kRows;
+  work(Units{Finder{s->start, kGroups, kGroups, 1}, s->plan, nullptr, s->col, kThreads},
+       s->start[0] + threadIdx.x / 32, kThreads / 32, s->units);
 }
 
 // ---------------------------------------------------------------------- free
@@ -503,21 +517,20 @@ __device__ __forceinline__ void free_units(const Rows& p, const Units& x, uint32
       p.t.table[(uint64_t)row * p.t.columns + c] = DB_PAGE_NONE;
       if (page[j] == kNoEntry) page[j] = kBadEntry;
     }
-    uint32_t refs[kRows], times[kRows];
+    uint32_t refs[kRows], times[kRows];  // times: rows from j on that name the page, if j is the first
 #pragma unroll
-    for (uint32_t j = 0; j < kRows; ++j) {
-      times[j] = refs[j] = 0;
-      if (page[j] == kNoEntry || (j && page[j] == page[j - 1])) continue;
-      if (page[j] >= p.t.n_pages) {
+    for (int j = kRows - 1; j >= 0; --j)
+      times[j] = j + 1 < (int)kRows && page[j + 1] == page[j] ? times[j + 1] + 1 : 1;
+#pragma unroll
+    for (int j = kRows - 1; j >= 0; --j) {
+      if (page[j] == kNoEntry || (j && page[j] == page[j - 1])) {
+        times[j] = 0;
+      } else if (page[j] >= p.t.n_pages) {
+        times[j] = 0;
         bad = true;
-        continue;
+      } else {
+        refs[j] = __ldcg(&p.t.refs[page[j]]);
       }
-      uint32_t run = 1;
-#pragma unroll
-      for (uint32_t k = j + 1; k < kRows; ++k)
-        if (run == k - j && page[k] == page[j]) ++run;
-      times[j] = run;
-      refs[j] = __ldcg(&p.t.refs[page[j]]);
     }
     // References that are down to these rows' are nobody else's to drop, in
     // this call or before: a store does, and most pages have one reference.
@@ -547,27 +560,36 @@ __device__ __forceinline__ void free_units(const Rows& p, const Units& x, uint32
 template <uint32_t kThreads, bool kSolo>
 __global__ void __launch_bounds__(kThreads) page_free_kernel(const FreeParams q) {
   __shared__ TeamShared s_team;
-  __shared__ RowPlan<kThreads, kSolo> s_plan;
+  __shared__ RowPlan<kThreads> s_plan;
   const Rows& p = q.r;
   Team<kThreads, kSolo> team(&s_team);
   wait_for_prerequisites();
   dependents_may_launch();
-  const uint32_t per = team.per(p.n), at = team.rank * per + threadIdx.x;
+  const uint32_t per = team.per(p.n), at = team.rank * per + threadIdx.x, step = per * team.size;
+  const bool one = kSolo || p.n <= step;  // a thread for every request
   if (p.ctr && team.id() == 0) *p.ctr = db_counters{0, 0, 0, 0};
-  for (uint32_t i = at; threadIdx.x < per && i < p.n; i += per * team.size) {
-    const uint32_t seq = q.req[i].seq;
-    if (seq < p.t.n_seqs) claim(p.w.claim, seq, i);
+  db_page_cut r = {0, 0};
+  uint32_t len = 0;
+  for (uint32_t i = at; threadIdx.x < per && i < p.n; i += step) {
+    r = q.req[i];
+    len = 0;
+    if (r.seq < p.t.n_seqs) {
+      claim(p.w.claim, r.seq, i);
+      len = __ldcg(&p.t.length[r.seq]);
+    }
   }
   team.started();
   team.sync();
-  uint32_t units = 0, invalid = 0;
-  for (uint32_t i0 = 0; i0 < p.n; i0 += per * team.size) {
+  uint32_t units = 0, entries = 0, invalid = 0;
+  for (uint32_t i0 = 0; i0 < p.n; i0 += step) {
     const uint32_t i = i0 + at;
     const bool mine = threadIdx.x < per && i < p.n;
     Plan pl = {0, 0, 0, 0};
     if (mine) {
-      const db_page_cut r = q.req[i];
-      const uint32_t len = r.seq < p.t.n_seqs ? p.t.length[r.seq] : 0;
+      if (!one) {
+        r = q.req[i];
+        if (r.seq < p.t.n_seqs) len = __ldcg(&p.t.length[r.seq]);
+      }
       const bool ok = r.seq < p.t.n_seqs && claimed(p.w.claim, r.seq, i);
       if (ok) {
         p.w.claim[r.seq] = 0;
@@ -580,12 +602,13 @@ __global__ void __launch_bounds__(kThreads) page_free_kernel(const FreeParams q)
       invalid += !ok;
       if (p.status) p.status[i] = ok ? DB_PAGE_OK : DB_PAGE_INVALID;
     }
-    plan_rows(team, p, &s_plan, i, mine, pl, &units);
+    plan_rows(team, p, &s_plan, i, mine, pl, &units, &entries);
   }
   if (p.ctr) add_count(&p.ctr->n_invalid, invalid);
-  own_units(team, p, &s_plan, units, [&](const Units& x, uint32_t first, uint32_t stride, uint32_t n) {
-    free_units(p, x, first, stride, n);
-  });
+  own_units(team, p, &s_plan, units, entries,
+            [&](const Units& x, uint32_t first, uint32_t stride, uint32_t end) {
+              free_units(p, x, first, stride, end);
+            });
 }
 
 constexpr uint32_t kUnitThreads = 128;
@@ -597,7 +620,7 @@ __global__ void __launch_bounds__(kUnitThreads) page_free_units_kernel(const Fre
   dependents_may_launch();
   const uint32_t units = p.w.head->units, first = (blockIdx.x * kUnitThreads + threadIdx.x) / 32;
   if (blockIdx.x * (kUnitThreads / 32) >= units) return;
-  const Units x = find_units(p, s_start, kSearch);
+  const Units x = find_units(p, s_start);
   __syncthreads();
   free_units(p, x, first, gridDim.x * (kUnitThreads / 32), units);
 }
@@ -630,14 +653,15 @@ __device__ __forceinline__ void fork_units(const Rows& p, const Units& x, uint32
       if (page[j] >= p.t.n_pages) {
         bad = true;
         page[j] = kNoEntry;
-        continue;
       }
-      if (j && page[j] == page[j - 1]) continue;
-      uint32_t run = 1;
+    }
+    uint32_t times = 0;
 #pragma unroll
-      for (uint32_t k = j + 1; k < kRows; ++k)
-        if (run == k - j && page[k] == page[j]) ++run;
-      atomicAdd(&p.t.refs[page[j]], run);
+    for (int j = kRows - 1; j >= 0; --j) {
+      ++times;
+      if (j && page[j] == page[j - 1]) continue;
+      if (page[j] != kNoEntry) atomicAdd(&p.t.refs[page[j]], times);
+      times = 0;
     }
   }
   if (p.ctr) add_error(p.ctr, bad);
@@ -646,37 +670,41 @@ __device__ __forceinline__ void fork_units(const Rows& p, const Units& x, uint32
 template <uint32_t kThreads, bool kSolo>
 __global__ void __launch_bounds__(kThreads) page_fork_kernel(const ForkParams q) {
   __shared__ TeamShared s_team;
-  __shared__ RowPlan<kThreads, kSolo> s_plan;
+  __shared__ RowPlan<kThreads> s_plan;
   const Rows& p = q.r;
   Team<kThreads, kSolo> team(&s_team);
   wait_for_prerequisites();
   dependents_may_launch();
-  const uint32_t per = team.per(p.n), at = team.rank * per + threadIdx.x;
+  const uint32_t per = team.per(p.n), at = team.rank * per + threadIdx.x, step = per * team.size;
+  const bool one = kSolo || p.n <= step;  // a thread for every request
   if (p.ctr && team.id() == 0) *p.ctr = db_counters{0, 0, 0, 0};
-  for (uint32_t i = at; threadIdx.x < per && i < p.n; i += per * team.size) {
-    const uint32_t child = q.req[i].child;
-    if (child < p.t.n_seqs) claim(p.w.claim, child, i);
+  db_page_fork_req r = {0, 0, 0, 0};
+  uint32_t held = 0, of = 0;  // the child's and the parent's lengths
+  auto look = [&](uint32_t i) {
+    const uint4 v = __ldcg(reinterpret_cast<const uint4*>(&q.req[i]));
+    r = db_page_fork_req{v.x, v.y, v.z, v.w};
+    held = r.child < p.t.n_seqs ? __ldcg(&p.t.length[r.child]) : 0;
+    of = r.parent < p.t.n_seqs ? __ldcg(&p.t.length[r.parent]) : 0;
+  };
+  for (uint32_t i = at; threadIdx.x < per && i < p.n; i += step) {
+    look(i);
+    if (r.child < p.t.n_seqs) claim(p.w.claim, r.child, i);
   }
   team.started();
   team.sync();
-  const bool one = kSolo || p.n <= per * team.size;
-  uint32_t units = 0, invalid = 0;
+  uint32_t units = 0, entries = 0, invalid = 0;
   uint64_t taken = 0;
   Plan pl;
-  for (uint32_t i0 = 0; i0 < p.n; i0 += per * team.size) {
+  for (uint32_t i0 = 0; i0 < p.n; i0 += step) {
     const uint32_t i = i0 + at;
     const bool mine = threadIdx.x < per && i < p.n;
     pl = Plan{kNoMove, 0, 0, 0};
     if (mine) {
-      const db_page_fork_req r = q.req[i];
+      if (!one) look(i);
       bool ok = false;
-      if (r.child < p.t.n_seqs) {
-        const uint32_t held = __ldcg(&p.t.length[r.child]);
-        const uint32_t of = r.parent < p.t.n_seqs ? __ldcg(&p.t.length[r.parent]) : 0;
-        if (claimed(p.w.claim, r.child, i)) {
-          p.w.claim[r.child] = 0;
-          ok = r.parent < p.t.n_seqs && r.parent != r.child && held == 0 && r.tokens <= of;
-        }
+      if (r.child < p.t.n_seqs && claimed(p.w.claim, r.child, i)) {
+        p.w.claim[r.child] = 0;
+        ok = r.parent < p.t.n_seqs && r.parent != r.child && held == 0 && r.tokens <= of;
       }
       if (ok) {
         pl = Plan{r.child, 0, min(pages_of(r.tokens, p.t.page_tokens), p.t.columns), r.parent};
@@ -685,7 +713,7 @@ __global__ void __launch_bounds__(kThreads) page_fork_kernel(const ForkParams q)
       invalid += !ok;
       if (p.status) p.status[i] = ok ? DB_PAGE_OK : DB_PAGE_INVALID;
     }
-    plan_rows(team, p, &s_plan, i, mine, pl, &units);
+    plan_rows(team, p, &s_plan, i, mine, pl, &units, &entries);
   }
   if (p.ctr) {
     add_count(&p.ctr->n_invalid, invalid);
@@ -694,13 +722,18 @@ __global__ void __launch_bounds__(kThreads) page_fork_kernel(const ForkParams q)
       atomicAdd((unsigned long long*)&p.ctr->total, (unsigned long long)c);
   }
   // Every length was read before the last scan's barrier.
-  for (uint32_t i = at; threadIdx.x < per && i < p.n; i += per * team.size) {
-    const uint32_t row = one ? pl.row : p.w.plan[i].row;
-    if (row != kNoMove) p.t.length[row] = q.req[i].tokens;
+  if (one) {
+    if (threadIdx.x < per && at < p.n && pl.row != kNoMove) p.t.length[pl.row] = r.tokens;
+  } else {
+    for (uint32_t i = at; threadIdx.x < per && i < p.n; i += step) {
+      const uint32_t row = p.w.plan[i].row;
+      if (row != kNoMove) p.t.length[row] = q.req[i].tokens;
+    }
   }
-  own_units(team, p, &s_plan, units, [&](const Units& x, uint32_t first, uint32_t stride, uint32_t n) {
-    fork_units(p, x, first, stride, n);
-  });
+  own_units(team, p, &s_plan, units, entries,
+            [&](const Units& x, uint32_t first, uint32_t stride, uint32_t end) {
+              fork_units(p, x, first, stride, end);
+            });
 }
 
 __global__ void __launch_bounds__(kUnitThreads) page_fork_units_kernel(const ForkParams q) {
@@ -710,7 +743,7 @@ __global__ void __launch_bounds__(kUnitThreads) page_fork_units_kernel(const For
   dependents_may_launch();
   const uint32_t units = p.w.head->units, first = (blockIdx.x * kUnitThreads + threadIdx.x) / 32;
   if (blockIdx.x * (kUnitThreads / 32) >= units) return;
-  const Units x = find_units(p, s_start, kSearch);
+  const Units x = find_units(p, s_start);
   __syncthreads();
   fork_units(p, x, first, gridDim.x * (kUnitThreads / 32), units);
 }
@@ -736,38 +769,40 @@ struct Ask {
   uint32_t part;      // tokens in a partly filled last page that it adds to, or 0
   uint32_t last;      // that page
   uint32_t refs;      // its references
-  bool mine, ok, corrupt;
+  bool named, fits, mine, ok, corrupt;
   __device__ __forceinline__ bool shares() const { return part && refs > 1; }
 };
 
+// Its sequence and pages, before it is known whose the sequence is;
 __device__ __forceinline__ Ask ask(const ExtendParams& p, uint32_t i, bool any) {
-  Ask a = {0, 0, 0, 0, 0, 0, 0, false, false, false};
+  Ask a = {0, 0, 0, 0, 0, 0, 0, false, false, false, false, false};
   if (!any) return a;
-  const db_page_grow r = p.req[i];
-  a.seq = r.seq;
-  if (r.seq >= p.t.n_seqs) return a;
-  const uint32_t len = p.t.length[r.seq], of = __ldcg(&p.w.claim[r.seq]);
-  const uint64_t now = (uint64_t)len + r.tokens;
-  const bool fits = now <= (uint64_t)p.t.columns * p.t.page_tokens && now <= 0xFFFFFFFFull;
-  const uint32_t had = pages_of(len, p.t.page_tokens), part = len % p.t.page_tokens;
-  // its page is looked up before it is known whose sequence it is
-  uint32_t last = 0, refs = 0;
-  if (fits && r.tokens && part) {
-    last = (uint32_t)p.t.table[(uint64_t)r.seq * p.t.columns + had - 1];
-    if (last < p.t.n_pages) refs = __ldcg(&p.t.refs[last]);
-  }
-  a.mine = of == 0xFFFFFFFFu - i;
-  if (!a.mine || !fits) return a;
-  a.corrupt = last >= p.t.n_pages;
-  a.ok = !a.corrupt;
-  if (!a.ok) return a;
+  const uint2 r = __ldcg(reinterpret_cast<const uint2*>(&p.req[i]));
+  a.seq = r.x;
+  a.named = a.seq < p.t.n_seqs;
+  if (!a.named) return a;
+  const uint32_t len = __ldcg(&p.t.length[a.seq]), part = len % p.t.page_tokens;
+  const uint64_t now = (uint64_t)len + r.y;
+  a.fits = now <= (uint64_t)p.t.columns * p.t.page_tokens && now <= 0xFFFFFFFFull;
+  if (!a.fits) return a;
+  a.had = pages_of(len, p.t.page_tokens);
   a.now = (uint32_t)now;
-  a.had = had;
-  a.grow = pages_of(now, p.t.page_tokens) - had;
-  if (r.tokens) a.part = part;
-  a.last = last;
-  a.refs = refs;
+  a.grow = pages_of(now, p.t.page_tokens) - a.had;
+  if (r.y && part) {
+    a.part = part;
+    a.last = (uint32_t)__ldcg(&p.t.table[(uint64_t)a.seq * p.t.columns + a.had - 1]);
+    a.corrupt = a.last >= p.t.n_pages;
+    if (!a.corrupt) a.refs = __ldcg(&p.t.refs[a.last]);
+  }
   return a;
+}
+
+// and with that.
+__device__ __forceinline__ void settle(const ExtendParams& p, uint32_t i, Ask* a) {
+  a->mine = a->named && claimed(p.w.claim, a->seq, i);
+  a->ok = a->mine && a->fits && !a->corrupt;
+  a->corrupt &= a->mine;
+  if (!a->ok) a->grow = a->part = 0;
 }
 
 struct PlanStart {
@@ -793,12 +828,13 @@ __device__ __forceinline__ void place_pages(const ExtendParams& p, const Finder&
 
 template <uint32_t kThreads, bool kSolo>
 __global__ void __launch_bounds__(kThreads) page_extend_kernel(const ExtendParams p) {
-  constexpr uint32_t kWords = kSolo ? kSoloWords<kThreads> : kSearch;
+  constexpr uint32_t kWords = kTeamWords<kThreads>;
   __shared__ TeamShared s_team;
-  __shared__ uint32_t s_start[kSolo ? kThreads : kTeamSearch];
-  __shared__ Plan s_plan[kSolo ? kThreads : 1];
-  __shared__ __align__(16) uint32_t s_before[kWords], s_bits[kSolo ? kWords : 4];
-  __shared__ uint32_t s_used;
+  __shared__ uint32_t s_start[kThreads];
+  __shared__ Plan s_plan[kThreads];
+  __shared__ __align__(16) uint32_t s_before[kWords], s_bits[kWords];
+  __shared__ __align__(16) uint32_t s_used[4];
+  __shared__ uint32_t s_end;
   Team<kThreads, kSolo> team(&s_team);
   wait_for_prerequisites();
   dependents_may_launch();
@@ -806,61 +842,70 @@ __global__ void __launch_bounds__(kThreads) page_extend_kernel(const ExtendParam
   const uint32_t per = team.per(p.n), at = team.rank * per + threadIdx.x;
   const uint32_t step = per * team.size;
   const bool one = kSolo || p.n <= step;  // a thread for every request, which asks once
+  Bits bits = load_free(team, p.t.free, p.t.n_pages);
   if (p.ctr && id == 0) *p.ctr = db_counters{0, 0, 0, 0};
+  Ask a = ask(p, at, false);
+  bool shares = false;
   for (uint32_t i = at; threadIdx.x < per && i < p.n; i += step) {
-    const uint32_t seq = p.req[i].seq;
-    if (seq < p.t.n_seqs) claim(p.w.claim, seq, i);
+    a = ask(p, i, true);
+    if (a.named) claim(p.w.claim, a.seq, i);
+    shares |= a.shares();
   }
   team.started();
-  const Bits bits = scan_free(team, p.t.free, p.t.n_pages);  // its barrier is the claims'
-  // How many of the batch's requests hold each shared page, and the last of
-  // them; requests of a warp that hold the same one (samples of one prompt)
-  // count together.
-  Ask a;
-  bool shares = false;
-  for (uint32_t i0 = 0; i0 < p.n; i0 += step) {
-    const uint32_t i = i0 + at;
-    a = ask(p, i, threadIdx.x < per && i < p.n);
-    if (a.shares()) {
-      shares = true;
-      const uint32_t same = __match_any_sync(__activemask(), a.last);
-      if ((same & lanemask_lt()) == 0) {
-        atomicAdd(&p.w.holders[a.last], (uint32_t)__popc(same));
-        atomicMax(&p.w.latest[a.last], i + (31 - __clz(same)) - (threadIdx.x & 31));
+  // Also the barrier after the claims, and whether any request may share.
+  shares = scan_free(team, bits, p.t.free, p.t.n_pages, shares);
+  if (one && at < p.n && threadIdx.x < per) settle(p, at, &a);
+  if (shares) {
+    // How many of the batch's requests hold each shared page, and the last of
+    // them; requests of a warp that hold the same one (samples of one prompt)
+    // count together.
+    for (uint32_t i = at; threadIdx.x < per && i < p.n; i += step) {
+      if (!one) {
+        a = ask(p, i, true);
+        settle(p, i, &a);
+      }
+      if (a.shares()) {
+        const uint32_t same = __match_any_sync(__activemask(), a.last);
+        if ((same & lanemask_lt()) == 0) {
+          atomicAdd(&p.w.holders[a.last], (uint32_t)__popc(same));
+          atomicMax(&p.w.latest[a.last], i + (31 - __clz(same)) - (threadIdx.x & 31));
+        }
       }
     }
+    team.sync();
   }
-  if (kSolo) shares = __syncthreads_or(shares); else team.sync();
   uint32_t need = 0, n_moves = 0, move = kNoMove;
   for (uint32_t i0 = 0; i0 < p.n; i0 += step) {
     const uint32_t i = i0 + at;
     const bool mine = threadIdx.x < per && i < p.n;
-    if (!one) a = ask(p, i, mine);
-    bool cow = false;
-    if ((!kSolo || shares) && a.shares())
-      cow = !(__ldcg(&p.w.holders[a.last]) == a.refs && __ldcg(&p.w.latest[a.last]) == i);
-    uint32_t total, copies = 0, rank = 0, x;
-    if (!kSolo || shares)
-      x = team.template scan<true>(a.grow + cow, &total, cow, &rank, &copies);
-    else
-      x = team.template scan<false>(a.grow, &total);
-    move = cow ? n_moves + rank : kNoMove;
-    if (mine) {
-      const Plan pl = {a.seq, a.had - cow, need + x, move};
-      if (kSolo) {
-        s_plan[i] = pl;
-        s_start[i] = pl.end;
-      }
-      if (!kSolo || p.rest) st_plan(&p.w.plan[i], pl);
+    if (!one) {
+      a = ask(p, i, mine);
+      if (mine) settle(p, i, &a);
     }
+    bool cow = false;
+    uint32_t total, copies = 0, rank = 0, x;
+    if (shares) {
+      if (a.shares())
+        cow = !(__ldcg(&p.w.holders[a.last]) == a.refs && __ldcg(&p.w.latest[a.last]) == i);
+      x = team.template scan<true>(a.grow + cow, &total, cow, &copies, &rank);
+    } else {
+      x = team.template scan<false>(a.grow, &total);
+    }
+    move = cow ? n_moves + rank : kNoMove;
+    const Plan pl = {a.seq, a.had - cow, need + x, move};
+    s_plan[threadIdx.x] = pl;
+    s_start[threadIdx.x] = pl.end;
+    if (threadIdx.x == kThreads - 1) s_end = pl.end + a.grow + cow;
+    if (mine && (p.rest || !one)) st_plan(&p.w.plan[i], pl);
     need += total;
     n_moves += copies;
   }
   const bool go = need <= bits.total;
-  const bool own = !p.rest || need <= kOwnPages * team.threads();
+  // The team places few pages, each CTA those of its requests: not when it
+  // plans in more than one round, or needs more words than it keeps.
+  const bool few = !p.rest || (one && need <= kOwnPages);
   if (id == 0) {
     *p.n_moves = go ? n_moves : 0;
-    if (p.rest) p.w.head->units = go && !own ? need : 0;
     if (p.ctr) p.ctr->total = need;
   }
   // The words up to the last one used as they were, to find the pages in, and
@@ -868,19 +913,23 @@ __global__ void __launch_bounds__(kThreads) page_extend_kernel(const ExtendParam
   if (go && need && bits.before < need)
     each_quad(bits, p.t.free, p.t.n_pages, [&](uint32_t w, const uint4& v, const uint4& before) {
       if (before.x >= need) return false;
-      if (kSolo) {
-        st_quad(s_before, w, words, before);
-        st_quad(s_bits, w, words, v);
+      if (few && w < kWords) {
+        if (kSolo) {
+          *reinterpret_cast<uint4*>(&s_before[w]) = before;
+          *reinterpret_cast<uint4*>(&s_bits[w]) = v;
+        } else {
+          team.to_all(&s_before[w], before);
+          team.to_all(&s_bits[w], v);
+        }
       }
-      if (!kSolo || !own) {
+      if (p.rest) {
         st_quad(p.w.before, w, words, before);
         st_quad(p.w.bits, w, words, v);
       }
-      const uint32_t end = before.w + __popc(v.w);
       uint4 left = make_uint4(0, 0, 0, 0);
-      if (end >= need) {  // the last quad used
+      if (before.w + __popc(v.w) >= need) {  // the last quad used
         const uint32_t vs[4] = {v.x, v.y, v.z, v.w}, bs[4] = {before.x, before.y, before.z, before.w};
-        uint32_t ls[4];
+        uint32_t ls[4], used = 0;
 #pragma unroll
         for (uint32_t k = 0; k < 4; ++k) {
           ls[k] = 0;
@@ -888,11 +937,12 @@ __global__ void __launch_bounds__(kThreads) page_extend_kernel(const ExtendParam
             ls[k] = vs[k];
           } else if (bs[k] + __popc(vs[k]) >= need) {
             ls[k] = vs[k] & ~((2u << nth_bit(vs[k], need - bs[k] - 1)) - 1);
-            (kSolo ? s_used : p.w.head->used) = w + k + 1;
-            if (kSolo && !own) p.w.head->used = w + k + 1;
+            used = w + k + 1;
           }
         }
         left = make_uint4(ls[0], ls[1], ls[2], ls[3]);
+        if (kSolo) s_used[0] = used; else team.to_all(s_used, make_uint4(used, 0, 0, 0));
+        if (p.rest) p.w.head->used = used;
       }
       st_quad(p.t.free, w, words, left);
       return true;
@@ -904,6 +954,7 @@ __global__ void __launch_bounds__(kThreads) page_extend_kernel(const ExtendParam
   for (uint32_t i = at; threadIdx.x < per && i < p.n; i += step) {
     if (!one) {
       a = ask(p, i, true);
+      settle(p, i, &a);
       move = p.w.plan[i].aux;
     }
     if (move != kNoMove) {  // at least one holder of every shared page copies, and clears for all
@@ -928,18 +979,13 @@ __global__ void __launch_bounds__(kThreads) page_extend_kernel(const ExtendParam
     add_count(&p.ctr->n_overflow, refused);
     add_error(p.ctr, corrupt);
   }
-  team.sync();  // plan and words are known, and the replaced entries have been read
-  if (!go || !need || !own) return;
-  if (kSolo) {
-    const uint32_t used = s_used;
-    place_pages(p, Finder{s_start, p.n, p.n, 1}, s_plan, Finder{s_before, used, used, 1}, s_before,
-                s_bits, id, kThreads, need);
-  } else {
-    const Finder r = load_finder(s_start, kTeamSearch, p.n, PlanStart{p.w.plan});
-    const Finder f = load_finder(s_before, kWords, __ldcg(&p.w.head->used), WordStart{p.w.before});
-    __syncthreads();
-    place_pages(p, r, p.w.plan, f, p.w.before, p.w.bits, id, team.threads(), need);
-  }
+  team.sync();  // words are known, and the replaced entries have been read
+  const uint32_t used = go && need ? s_used[0] : 0;
+  const bool own = few && used <= kWords;
+  if (p.rest && id == 0) p.w.head->units = go && !own ? need : 0;
+  if (!used || !own) return;
+  place_pages(p, Finder{s_start, kThreads, kThreads, 1}, s_plan, Finder{s_before, used, used, 1},
+              s_before, s_bits, s_start[0] + threadIdx.x, kThreads, s_end);
 }
 
 constexpr uint32_t kPlaceThreads = 256;
@@ -948,10 +994,10 @@ __global__ void __launch_bounds__(kPlaceThreads) page_place_kernel(const ExtendP
   __shared__ uint32_t s_start[kSearch], s_word[kSearch];
   wait_for_prerequisites();
   dependents_may_launch();
-  const uint32_t total = p.w.head->units;
+  const uint32_t total = p.w.head->units, used = p.w.head->used;
   if (blockIdx.x * kPlaceThreads >= total) return;
   const Finder r = load_finder(s_start, kSearch, p.n, PlanStart{p.w.plan});
-  const Finder f = load_finder(s_word, kSearch, p.w.head->used, WordStart{p.w.before});
+  const Finder f = load_finder(s_word, kSearch, used, WordStart{p.w.before});
   __syncthreads();
   place_pages(p, r, p.w.plan, f, p.w.before, p.w.bits, blockIdx.x * kPlaceThreads + threadIdx.x,
               gridDim.x * kPlaceThreads, total);
@@ -1085,8 +1131,9 @@ __global__ void __launch_bounds__(kThreads) page_compact_plan_kernel(const Compa
   wait_for_prerequisites();
   dependents_may_launch();
   const uint32_t id = team.id(), n_pages = p.t.n_pages, words = (n_pages + 31) / 32;
+  Bits bits = load_free(team, p.t.free, n_pages);
   team.started();
-  const Bits bits = scan_free(team, p.t.free, n_pages);
+  scan_free(team, bits, p.t.free, n_pages, false);
   const uint32_t n_live = n_pages - bits.total;
   // M, the free pages below n_live: known to the thread that has the word.
   each_quad(bits, p.t.free, n_pages, [&](uint32_t w, const uint4& v, const uint4& before) {
@@ -1212,8 +1259,8 @@ template <typename P>
 int launch_rows(void (*small)(P), void (*solo)(P), void (*team)(P), void (*rest)(P),
                 cudaStream_t s, P& p) {
   const uint64_t units = ((uint64_t)p.r.n + kRows - 1) / kRows * (((uint64_t)p.r.t.columns + 31) / 32);
-  const uint32_t ctas = team_size(p.r.n);
-  p.r.rest = units > kRestUnits;
+  const uint32_t ctas = p.r.n <= kTeamThreads ? 1 : team_size(2 * (uint64_t)p.r.n);
+  p.r.rest = units > kRestUnits || p.r.n > ctas * kTeamThreads;
   const int e = p.r.n <= kSmallThreads ? launch_team(small, 1, kSmallThreads, s, p)
                                        : launch_team(ctas == 1 ? solo : team, ctas, kTeamThreads, s, p);
   if (e || !p.r.rest) return e;
@@ -1283,14 +1330,14 @@ extern "C" int db_page_extend(const db_page_tables* t, const db_page_grow* req, 
   p.ctr = ctr;
   const uint64_t pages = (uint64_t)n * t->columns < t->n_pages ? (uint64_t)n * t->columns : t->n_pages;
   const uint32_t words = (t->n_pages + 31) / 32;
-  p.rest = pages > kRestPages;
+  p.rest = pages > kRestPages || n > kMaxTeam * kTeamThreads || words > kTeamWords<kTeamThreads>;
   int e;
-  if (n <= kSmallThreads && words <= kSoloWords<kSmallThreads>) {
+  if (n <= kSmallThreads && words <= kTeamWords<kSmallThreads>) {
     e = launch_team(page_extend_kernel<kSmallThreads, true>, 1, kSmallThreads, s, p);
-  } else if (n <= kTeamThreads && words <= kSoloWords<kTeamThreads>) {
+  } else if (n <= kTeamThreads && words <= kTeamWords<kTeamThreads>) {
     e = launch_team(page_extend_kernel<kTeamThreads, true>, 1, kTeamThreads, s, p);
   } else {
-    uint32_t ctas = team_size(n > words / 4 ? n : words / 4);
+    uint32_t ctas = team_size((uint64_t)2 * n > words / 4 ? (uint64_t)2 * n : words / 4);
     if (ctas == 1) ctas = 2;
     e = launch_team(page_extend_kernel<kTeamThreads, false>, ctas, kTeamThreads, s, p);
   }
