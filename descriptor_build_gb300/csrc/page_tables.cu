@@ -441,33 +441,57 @@ struct GroupStart {
   __device__ __forceinline__ uint32_t operator()(uint32_t g) const { return group[g].x; }
 };
 
-// Where units are found: in the workspace, or among a CTA's own.
-struct Units {
-  Finder f;
-  const Plan* plan;
-  const uint2* group;   // in the workspace, or null:
-  const uint32_t* col;  // a RowPlan's columns
-  uint32_t n;
-  // The rows of unit u: lane j < kRows holds the j-th plan (empty if there is
-  // none); returns this lane's column.
-  __device__ __forceinline__ uint32_t load(uint32_t u, uint32_t lane, Plan* pl) const {
-    const uint32_t g = f.find(u, GroupStart{group});
-    const uint32_t i = g * kRows + lane;
-    *pl = Plan{0, 0, 0, 0};
-    if (lane < kRows && i < n) *pl = ld_plan(&plan[i]);
-    const uint2 at = group ? group[g] : make_uint2(f.s_start[g], col[g]);
-    return at.y + (u - at.x) * 32 + lane;
+// A CTA's own units, in shared memory. Starts do not decrease, so the number
+// of those at or before u is found by votes, without a search's steps.
+template <uint32_t kThreads>
+struct OwnUnits {
+  const RowPlan<kThreads>* s;
+  struct Unit {
+    const Plan* plan;
+    uint32_t base;  // its first column
+    __device__ __forceinline__ Plan row(uint32_t j) const { return ld_plan(plan + j); }
+  };
+  __device__ __forceinline__ Unit find(uint32_t u) const {
+    uint32_t g = 0;
+#pragma unroll
+    for (uint32_t k = 0; k < kThreads / kRows; k += 32)
+      g += __popc(__ballot_sync(kFull, s->start[k + (threadIdx.x & 31)] <= u));
+    --g;
+    return Unit{&s->plan[g * kRows], s->col[g] + (u - s->start[g]) * 32};
   }
 };
 
-// The units of a plan in the workspace (a barrier follows).
-__device__ __forceinline__ Units find_units(const Rows& p, uint32_t* s_start) {
-  Units x;
+// All units, in the workspace: a lane loads a row's plan and the others get
+// it from there.
+struct AllUnits {
+  Finder f;
+  const Plan* plan;
+  const uint2* group;
+  uint32_t n;
+  struct Unit {
+    Plan mine;
+    uint32_t base;
+    __device__ __forceinline__ Plan row(uint32_t j) const {
+      return Plan{__shfl_sync(kFull, mine.row, j), __shfl_sync(kFull, mine.from, j),
+                  __shfl_sync(kFull, mine.end, j), __shfl_sync(kFull, mine.aux, j)};
+    }
+  };
+  __device__ __forceinline__ Unit find(uint32_t u) const {
+    const uint32_t g = f.find(u, GroupStart{group}), lane = threadIdx.x & 31, i = g * kRows + lane;
+    Plan pl = {0, 0, 0, 0};
+    if (lane < kRows && i < n) pl = ld_plan(&plan[i]);
+    const uint2 at = group[g];
+    return Unit{pl, at.y + (u - at.x) * 32};
+  }
+};
+
+__device__ __forceinline__ AllUnits all_units(const Rows& p, uint32_t* s_start) {
+  AllUnits x;
+  x.f = load_finder(s_start, kSearch, (p.n + kRows - 1) / kRows, GroupStart{p.w.group});
   x.plan = p.w.plan;
   x.group = p.w.group;
-  x.col = nullptr;
   x.n = p.n;
-  x.f = load_finder(s_start, kSearch, (p.n + kRows - 1) / kRows, GroupStart{p.w.group});
+  __syncthreads();
   return x;
 }
 
@@ -481,9 +505,7 @@ __device__ __forceinline__ void own_units(const Team<kThreads, kSolo>& team, con
   if (p.rest && team.id() == 0) p.w.head->units = own ? 0 : units;
   if (!own || !units) return;
   __syncthreads();
-  constexpr uint32_t kGroups = kThreads / kRows;
-  work(Units{Finder{s->start, kGroups, kGroups, 1}, s->plan, nullptr, s->col, kThreads},
-       s->start[0] + threadIdx.x / 32, kThreads / 32, s->units);
+  work(OwnUnits<kThreads>{s}, s->start[0] + threadIdx.x / 32, kThreads / 32, s->units);
 }
 
 // ---------------------------------------------------------------------- free
@@ -492,29 +514,29 @@ struct FreeParams {
   const db_page_cut* req;
 };
 
-__device__ __forceinline__ void free_units(const Rows& p, const Units& x, uint32_t first,
+template <typename X>
+__device__ __forceinline__ void free_units(const Rows& p, const X& x, uint32_t first,
                                            uint32_t stride, uint32_t units) {
   const uint32_t lane = threadIdx.x & 31;
   uint32_t released = 0;
   bool bad = false;
   for (uint32_t u = first; u < units; u += stride) {
-    Plan pl;
-    const uint32_t c = x.load(u, lane, &pl);
+    const auto at = x.find(u);
+    const uint32_t c = at.base + lane;
+    int32_t* entry[kRows];
     uint32_t page[kRows];
-    bool clear[kRows];
 #pragma unroll
     for (uint32_t j = 0; j < kRows; ++j) {
-      const uint32_t row = __shfl_sync(kFull, pl.row, j), from = __shfl_sync(kFull, pl.from, j);
-      const uint32_t end = __shfl_sync(kFull, pl.end, j);
-      page[j] = kNoEntry;
-      clear[j] = c >= from && c < end;
-      if (clear[j]) page[j] = (uint32_t)p.t.table[(uint64_t)row * p.t.columns + c];
+      const Plan pl = at.row(j);
+      entry[j] = &p.t.table[(uint64_t)pl.row * p.t.columns + c];
+      if (c - pl.from >= pl.end - pl.from) entry[j] = nullptr;
     }
 #pragma unroll
+    for (uint32_t j = 0; j < kRows; ++j) page[j] = entry[j] ? (uint32_t)*entry[j] : kNoEntry;
+#pragma unroll
     for (uint32_t j = 0; j < kRows; ++j) {
-      const uint32_t row = __shfl_sync(kFull, pl.row, j);
-      if (!clear[j]) continue;
-      p.t.table[(uint64_t)row * p.t.columns + c] = DB_PAGE_NONE;
+      if (!entry[j]) continue;
+      *entry[j] = DB_PAGE_NONE;
       if (page[j] == kNoEntry) page[j] = kBadEntry;
     }
     uint32_t refs[kRows], times[kRows];  // times: rows from j on that name the page, if j is the first
@@ -528,27 +550,32 @@ __device__ __forceinline__ void free_units(const Rows& p, const Units& x, uint32
       } else if (page[j] >= p.t.n_pages) {
         times[j] = 0;
         bad = true;
-      } else {
+      } else if (times[j] == 1) {
         refs[j] = __ldcg(&p.t.refs[page[j]]);
+      } else {  // shared within the unit: likely by others too
+        refs[j] = atomicSub(&p.t.refs[page[j]], times[j]);
       }
     }
-    // References that are down to these rows' are nobody else's to drop, in
-    // this call or before: a store does, and most pages have one reference.
+    // A single reference left is nobody else's to drop, in this call or
+    // before: a store does, and most pages have one. The atomics are all under
+    // way before the first answer is looked at.
 #pragma unroll
     for (uint32_t j = 0; j < kRows; ++j) {
       if (!times[j]) continue;
-      bool last = refs[j] == times[j];
-      if (last) {
-        p.t.refs[page[j]] = 0;
-      } else if (refs[j] > times[j]) {
-        last = atomicSub(&p.t.refs[page[j]], times[j]) == times[j];
-      } else {  // more rows than references
+      if (times[j] == 1 && refs[j] > 1) {
+        refs[j] = atomicSub(&p.t.refs[page[j]], 1u);
+      } else if (refs[j] < times[j]) {  // more rows than references
         bad = true;
+        if (times[j] > 1) atomicAdd(&p.t.refs[page[j]], times[j]);
+      } else if (times[j] == 1) {
+        p.t.refs[page[j]] = 0;
       }
-      if (last) {
-        atomicOr(&p.t.free[page[j] >> 5], 1u << (page[j] & 31));
-        ++released;
-      }
+    }
+#pragma unroll
+    for (uint32_t j = 0; j < kRows; ++j) {
+      if (!times[j] || refs[j] != times[j]) continue;
+      atomicOr(&p.t.free[page[j] >> 5], 1u << (page[j] & 31));
+      ++released;
     }
   }
   if (p.ctr) {
@@ -606,7 +633,7 @@ __global__ void __launch_bounds__(kThreads) page_free_kernel(const FreeParams q)
   }
   if (p.ctr) add_count(&p.ctr->n_invalid, invalid);
   own_units(team, p, &s_plan, units, entries,
-            [&](const Units& x, uint32_t first, uint32_t stride, uint32_t end) {
+            [&](const OwnUnits<kThreads>& x, uint32_t first, uint32_t stride, uint32_t end) {
               free_units(p, x, first, stride, end);
             });
 }
@@ -620,8 +647,7 @@ __global__ void __launch_bounds__(kUnitThreads) page_free_units_kernel(const Fre
   dependents_may_launch();
   const uint32_t units = p.w.head->units, first = (blockIdx.x * kUnitThreads + threadIdx.x) / 32;
   if (blockIdx.x * (kUnitThreads / 32) >= units) return;
-  const Units x = find_units(p, s_start);
-  __syncthreads();
+  const AllUnits x = all_units(p, s_start);
   free_units(p, x, first, gridDim.x * (kUnitThreads / 32), units);
 }
 
@@ -631,25 +657,29 @@ struct ForkParams {
   const db_page_fork_req* req;
 };
 
-__device__ __forceinline__ void fork_units(const Rows& p, const Units& x, uint32_t first,
+template <typename X>
+__device__ __forceinline__ void fork_units(const Rows& p, const X& x, uint32_t first,
                                            uint32_t stride, uint32_t units) {
   const uint32_t lane = threadIdx.x & 31;
   bool bad = false;
   for (uint32_t u = first; u < units; u += stride) {
-    Plan pl;
-    const uint32_t c = x.load(u, lane, &pl);
+    const auto at = x.find(u);
+    const uint32_t c = at.base + lane;
+    const int32_t* from[kRows];
+    int32_t* to[kRows];
     uint32_t page[kRows];
 #pragma unroll
     for (uint32_t j = 0; j < kRows; ++j) {
-      const uint32_t from = __shfl_sync(kFull, pl.aux, j), end = __shfl_sync(kFull, pl.end, j);
-      page[j] = kNoEntry;
-      if (c < end) page[j] = (uint32_t)p.t.table[(uint64_t)from * p.t.columns + c];
+      const Plan pl = at.row(j);
+      from[j] = &p.t.table[(uint64_t)pl.aux * p.t.columns + c];
+      to[j] = c < pl.end ? &p.t.table[(uint64_t)pl.row * p.t.columns + c] : nullptr;
     }
 #pragma unroll
+    for (uint32_t j = 0; j < kRows; ++j) page[j] = to[j] ? (uint32_t)*from[j] : kNoEntry;
+#pragma unroll
     for (uint32_t j = 0; j < kRows; ++j) {
-      const uint32_t row = __shfl_sync(kFull, pl.row, j), end = __shfl_sync(kFull, pl.end, j);
-      if (c >= end) continue;
-      p.t.table[(uint64_t)row * p.t.columns + c] = (int32_t)page[j];
+      if (!to[j]) continue;
+      *to[j] = (int32_t)page[j];
       if (page[j] >= p.t.n_pages) {
         bad = true;
         page[j] = kNoEntry;
@@ -731,7 +761,7 @@ __global__ void __launch_bounds__(kThreads) page_fork_kernel(const ForkParams q)
     }
   }
   own_units(team, p, &s_plan, units, entries,
-            [&](const Units& x, uint32_t first, uint32_t stride, uint32_t end) {
+            [&](const OwnUnits<kThreads>& x, uint32_t first, uint32_t stride, uint32_t end) {
               fork_units(p, x, first, stride, end);
             });
 }
@@ -743,8 +773,7 @@ __global__ void __launch_bounds__(kUnitThreads) page_fork_units_kernel(const For
   dependents_may_launch();
   const uint32_t units = p.w.head->units, first = (blockIdx.x * kUnitThreads + threadIdx.x) / 32;
   if (blockIdx.x * (kUnitThreads / 32) >= units) return;
-  const Units x = find_units(p, s_start);
-  __syncthreads();
+  const AllUnits x = all_units(p, s_start);
   fork_units(p, x, first, gridDim.x * (kUnitThreads / 32), units);
 }
 
