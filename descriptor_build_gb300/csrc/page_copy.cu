@@ -8,9 +8,9 @@
 //    record, plane and segment once, and moves 8 vectors of 16 bytes a lane,
 //    all loads in flight before the first store;
 //  - page_copy_fine_kernel, for smaller ones and for addresses that are not
-//    multiples of 16: the vectors of all records and planes are numbered in
-//    one sequence, so that short runs share a warp, and each lane finds its
-//    own vectors.
+//    multiples of 16: a CTA works on one plane and segment at a time, in which
+//    as many lanes as a run has vectors (up to a warp) take a record, so that
+//    short runs share a warp and records are found without a division.
 #include "common.cuh"
 #include "pagecache.h"
 
@@ -28,15 +28,15 @@ struct CopyParams {
   db_page_pool src, dst;
   uint32_t planes, segments, page_tokens, token_bytes;
   uint64_t seg_bytes, page_bytes;
-  uint64_t slots;  // of a record in one plane; fine: vectors, a multiple of kWarpSlots or a power
-                   // of two below it; wide: chunks
-  uint32_t seg_chunks;  // wide: chunks of a segment
+  uint32_t seg_chunks;  // wide: chunks of a segment,
+  uint64_t slots;       // and of a record in one plane
+  uint32_t lanes;       // fine: lanes of a run
   db_counters* ctr;
 };
 
 // The counters, by one CTA.
 __device__ __forceinline__ void count_records(const CopyParams& p, uint32_t n) {
-  if (p.ctr && blockIdx.x == 0) {
+  if (p.ctr && blockIdx.x == 0 && blockIdx.y == 0) {
     __shared__ unsigned int s_bad;
     if (threadIdx.x == 0) s_bad = 0;
     __syncthreads();
@@ -85,85 +85,70 @@ struct Vec<1> {
   typedef uint8_t type;
 };
 
-// Where slot v of a record in a plane is: bytes [at, at + bytes) of the page.
-struct Piece {
-  uint64_t at;
-  uint32_t bytes;  // 0: none
-};
-
-template <int kVec>
-__device__ __forceinline__ Piece piece(const CopyParams& p, uint32_t tokens, uint64_t v) {
-  Piece x = {0, 0};
-  uint64_t len = p.page_bytes, run = 0;
-  if (tokens < p.page_tokens) {
-    len = (uint64_t)tokens * p.token_bytes;
-    if (!len) return x;
-    const uint64_t per = (len + kVec - 1) / kVec;
-    if (p.segments > 1) {
-      if ((v | per) >> 32) {
-        run = v / per;
-      } else {
-        run = (uint32_t)v / (uint32_t)per;
-      }
-      v -= run * per;
-      if (run >= p.segments) return x;
-    }
-  }
-  const uint64_t off = v * kVec;
-  if (off >= len) return x;
-  x.at = run * p.seg_bytes + off;
-  x.bytes = len - off < kVec ? (uint32_t)(len - off) : kVec;
-  return x;
-}
-
-template <int kVec>
+// ---------------------------------------------------------------------- fine
+// Runs of one plane and one segment: `lanes` lanes take a record's run, kUnroll
+// vectors a lane, kBatch / kUnroll records at a time.
+template <int kVec, int kUnroll>
 __global__ void __launch_bounds__(kThreads) page_copy_fine_kernel(const CopyParams p) {
   typedef typename Vec<kVec>::type V;
+  constexpr int kRecords = kBatch / kUnroll;
   wait_for_prerequisites();
   dependents_may_launch();
   const uint32_t n = min(__ldcg(p.n_moves), p.max_moves);
-  const uint32_t lane = threadIdx.x & 31;
-  const uint64_t all = (uint64_t)n * p.planes * p.slots;
-  const uint64_t stride = (uint64_t)gridDim.x * (kThreads / 32) * kWarpSlots;
-  uint64_t x0 = ((uint64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32) * kWarpSlots;
-  for (; x0 < all; x0 += stride) {
-    V v[kBatch];
-    uint64_t to[kBatch];
-    uint32_t bytes[kBatch];
+  const uint32_t lane = threadIdx.x & (p.lanes - 1), per = kThreads / p.lanes;
+  const uint64_t stride = (uint64_t)gridDim.x * per;
+  for (uint32_t y = blockIdx.y; y < p.planes * p.segments; y += gridDim.y) {
+    const uint32_t plane = y / p.segments, seg = y - plane * p.segments;
+    const char* const from = (const char*)p.src.base + plane * p.src.plane_stride + seg * p.seg_bytes;
+    char* const to = (char*)p.dst.base + plane * p.dst.plane_stride + seg * p.seg_bytes;
+    for (uint64_t r0 = (uint64_t)blockIdx.x * per + threadIdx.x / p.lanes; r0 < n; r0 += stride * kRecords) {
+      const char* src[kRecords];
+      char* dst[kRecords];
+      uint32_t len[kRecords];
 #pragma unroll
-    for (uint32_t j = 0; j < kBatch; ++j) {
-      const uint64_t x = x0 + 32 * j + lane;
-      bytes[j] = 0;
-      to[j] = 0;
-      if (x < all) {
-        const uint64_t rp = x / p.slots, r = rp / p.planes;
-        const uint64_t plane = rp - r * p.planes;
-        const uint4 m = *(reinterpret_cast<const uint4*>(p.moves) + r);
-        if (m.x < p.src.n_pages && m.y < p.dst.n_pages) {
-          const Piece c = piece<kVec>(p, m.z, x - rp * p.slots);
-          bytes[j] = c.bytes;
-          const char* from = (const char*)p.src.base + plane * p.src.plane_stride +
-                             m.x * p.src.page_stride + c.at;
-          to[j] = (uint64_t)((char*)p.dst.base + plane * p.dst.plane_stride +
-                             m.y * p.dst.page_stride + c.at);
-          if (c.bytes == kVec) {
-            v[j] = *(const V*)from;
-          } else {
-            for (uint32_t k = 0; k < c.bytes; ++k) ((char*)to[j])[k] = from[k];
+      for (int i = 0; i < kRecords; ++i) {
+        const uint64_t r = r0 + i * stride;
+        len[i] = 0;
+        src[i] = from;
+        dst[i] = to;
+        if (r < n) {
+          const uint4 m = *(reinterpret_cast<const uint4*>(p.moves) + r);
+          if (m.x < p.src.n_pages && m.y < p.dst.n_pages) {
+            src[i] = from + m.x * p.src.page_stride;
+            dst[i] = to + m.y * p.dst.page_stride;
+            len[i] = min(m.z, p.page_tokens) * p.token_bytes;
+          }
+        }
+      }
+      for (uint32_t at = lane * kVec; at < (uint32_t)p.seg_bytes; at += p.lanes * kVec * kUnroll) {
+        V v[kBatch];
+#pragma unroll
+        for (int j = 0; j < (int)kBatch; ++j) {
+          const uint32_t off = at + j % kUnroll * p.lanes * kVec;
+          if (off + kVec <= len[j / kUnroll]) v[j] = *(const V*)(src[j / kUnroll] + off);
+        }
+#pragma unroll
+        for (int j = 0; j < (int)kBatch; ++j) {
+          const uint32_t off = at + j % kUnroll * p.lanes * kVec, end = len[j / kUnroll];
+          if (off + kVec <= end) {
+            *(V*)(dst[j / kUnroll] + off) = v[j];
+          } else {  // the run's last bytes
+            uint32_t k = off;
+            if (kVec > 4)
+              for (; k + 4 <= end; k += 4)
+                *(uint32_t*)(dst[j / kUnroll] + k) = *(const uint32_t*)(src[j / kUnroll] + k);
+            for (; k < end; ++k) dst[j / kUnroll][k] = src[j / kUnroll][k];
           }
         }
       }
     }
-#pragma unroll
-    for (uint32_t j = 0; j < kBatch; ++j)
-      if (bytes[j] == kVec) *(V*)to[j] = v[j];
   }
   count_records(p, n);
 }
 
 // ---------------------------------------------------------------------- wide
 constexpr uint32_t kChunk = kWarpSlots * 16;  // bytes a warp moves at a time
-constexpr uint64_t kWideBytes = 2048;
+constexpr uint64_t kWideBytes = 8192;
 // CTAs an SM of the largest grid. How many records there are is on the device,
 // so the grid is bounded and loops; 8 CTAs are resident, and several times as
 // many even out what the loops leave at the end. 3,500 pages of 16 planes of
@@ -174,6 +159,7 @@ constexpr uint64_t kWideBytes = 2048;
 // 3 to 12 CTAs an SM, 2 or 4 stages ahead) took 570 to 607 us, and 2.8 KB
 // runs 75 us and more where these loads and stores take 44.
 constexpr uint32_t kWideCtas = 64;
+constexpr uint32_t kFineCtas = 64;
 
 __device__ __forceinline__ uint64_t div64(uint64_t a, uint32_t b) {
   return (a >> 32) ? a / b : (uint32_t)a / b;
@@ -236,19 +222,40 @@ bool pool_ok(const db_page_pool* q, const db_page_shape* f, uint64_t page_bytes)
   return true;
 }
 
+int launch_fine(void (*kernel)(CopyParams), int unroll, const CopyParams& p, cudaStream_t s) {
+  const uint64_t per = kThreads / p.lanes * (kBatch / unroll);
+  const uint64_t rows = (uint64_t)p.planes * p.segments, x = (p.max_moves + per - 1) / per;
+  // CTAs along the records and along planes and segments, in all no more than
+  // stay busy for several rounds.
+  const uint64_t most = (uint64_t)kFineCtas * num_sms();
+  const uint64_t gx = x < most ? x : most;
+  uint64_t gy = most / gx;
+  gy = gy < 1 ? 1 : gy < rows ? gy : rows;
+  if (gy > 65535) gy = 65535;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)gx, (unsigned)gy);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+  if (e != cudaSuccess) return cuda_failure(e);
+  return launch_result();
+}
+
 template <int kVec>
 int launch_copy(CopyParams& p, cudaStream_t s) {
-  const uint64_t per = (p.seg_bytes + kVec - 1) / kVec * p.segments;
-  if (per > kWarpSlots / 2) {
-    p.slots = (per + kWarpSlots - 1) / kWarpSlots * kWarpSlots;
-  } else {
-    p.slots = 1;
-    while (p.slots < per) p.slots *= 2;
-  }
-  const uint64_t warps = ((uint64_t)p.max_moves * p.planes * p.slots + kWarpSlots - 1) / kWarpSlots;
-  const uint64_t want = (warps + kThreads / 32 - 1) / (kThreads / 32), most = 16ull * num_sms();
-  return launch_dependent(page_copy_fine_kernel<kVec>, (unsigned)(want < most ? want : most), kThreads,
-                          0, s, p);
+  const uint64_t vectors = (p.seg_bytes + kVec - 1) / kVec;
+  p.lanes = 1;
+  while (p.lanes < 32 && p.lanes < vectors) p.lanes *= 2;
+  const uint64_t each = (vectors + p.lanes - 1) / p.lanes;
+  if (each <= 1) return launch_fine(page_copy_fine_kernel<kVec, 1>, 1, p, s);
+  if (each <= 2) return launch_fine(page_copy_fine_kernel<kVec, 2>, 2, p, s);
+  if (each <= 4) return launch_fine(page_copy_fine_kernel<kVec, 4>, 4, p, s);
+  return launch_fine(page_copy_fine_kernel<kVec, 8>, 8, p, s);
 }
 
 }  // namespace
