@@ -301,7 +301,7 @@ extern "C" int db_page_copy(const db_page_move* moves, uint32_t max_moves, const
   if (src->n_pages > 1) all |= src->page_stride;
   if (dst->n_pages > 1) all |= dst->page_stride;
   if (p.segments > 1) all |= p.seg_bytes;
-  if (!(all & 15) && (p.segments > 1 ? p.seg_bytes : page_bytes) >= kWideBytes) {
+  if (!(all & 15) && p.seg_bytes >= kWideBytes) {
     p.seg_chunks = (uint32_t)((p.seg_bytes + kChunk - 1) / kChunk);
     p.slots = (uint64_t)p.seg_chunks * p.segments;
     const uint64_t warps = p.max_moves * (p.planes * p.slots);

@@ -222,6 +222,65 @@ def test_page_tokens_that_pass_32_bits():
     b.free([[0, 0xE0000000 - 1], [1, 1]])
 
 
+def test_few_free_pages_far_apart():
+    """The pages taken lie in more words of free bits than a CTA keeps on chip."""
+    n_pages = 200003
+    b = Both(3, n_pages, n_pages, 4)
+    held = np.flatnonzero(np.arange(n_pages) % 1301 != 700)
+    b.o.table[0, : held.size] = held
+    b.o.length[0] = 4 * held.size
+    b.o.refs[held] = 1
+    b.load()
+    b.extend([[1, 4 * 100 + 1]])
+    b.extend([[2, 3], [1, 4]])
+    b.extend([[2, 4 * 200]])                           # more than there are
+    b.free([[1, 9], [0, 40]])
+    b.extend([[1, 70000], [2, 70000]])
+    b.compact(60000, apart=False)
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+def test_compaction_of_every_array_apart_or_in_place(shift):
+    """Each output may be the input's array or another one, 16-byte aligned or not."""
+    db = lib()
+    for mask in range(16):
+        rng = np.random.default_rng(mask)
+        b = Both(21, 9, 301, 4)
+        b.extend(np.stack([rng.permutation(21), rng.integers(1, 36, 21)], 1))
+        b.fork([[3, k, 1, 0] for k in range(21)])
+        b.free([[k, 0] for k in range(0, 21, 3)])
+
+        def other(t, k):
+            if not mask >> k & 1:
+                return t
+            off = shift if k < 3 else 4 * shift        # free bits stay on 16 bytes
+            return torch.full((t.numel() + off,), -5, dtype=torch.int32, device="cuda")[off:].view(t.shape)
+
+        t = b.t
+        out = db.PageTables(*(other(x, k) for k, x in enumerate((t.table, t.length, t.refs, t.free))), 4)
+        for cap in (7, 150):
+            moves, n = torch.zeros((cap, 4), dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+            db.page_compact(b.t, out, moves, n, b.ws)
+            _, want = b.o.compact(cap)
+            b.same(out)
+            assert moves.cpu().numpy().view(np.uint32)[: int(n)].tolist() == want
+            b.t = out
+
+
+def test_rows_without_alignment():
+    """A table, lengths and references at 4-byte addresses, a status at an odd one."""
+    db = lib()
+    b = Both(30, 7, 100, 8)
+    at = lambda t: torch.cat([t.new_zeros(1), t.reshape(-1)])[1:].view(t.shape)
+    b.t = db.PageTables(at(b.t.table), at(b.t.length), at(b.t.refs), b.t.free, 8)
+    b._status = lambda n: torch.full((n + 2,), 99, dtype=torch.uint8, device="cuda")[1:]
+    rng = np.random.default_rng(2)
+    b.extend(np.stack([rng.permutation(15), rng.integers(1, 40, 15)], 1))
+    b.fork([[k, 15 + k, int(b.o.length[k]), 0] for k in range(15)])
+    b.extend(np.stack([rng.permutation(30), np.ones(30)], 1))
+    b.free(np.stack([rng.permutation(30), rng.integers(0, 30, 30)], 1))
+
+
 def test_workspace_is_left_as_it_was():
     b = Both(70, 5, 300, 4)
     rng = np.random.default_rng(0)
