@@ -1,13 +1,17 @@
 // Page tables of a cache in the device heap: extend, fork, free, compact
 // (include/pagecache.h has the definitions).
 //
-// A call's requests are planned by one team: a single CTA, or one cluster of
-// CTAs, whose barriers are the hardware's, so no kernel here waits on memory.
-// The plan is a prefix sum over what the requests ask for, and what follows
-// is work on pieces of it, found again by a search in shared memory. The team
-// does that work itself when it is little; otherwise a second kernel does it
-// on the whole GPU, launched as a dependent of the first when the sizes of
-// the call allow for so much (how much there is, only the device knows).
+// A plan is a prefix sum over what a call's requests ask for, and what follows
+// is work on pieces of it, found again by a search. There are two ways to it,
+// and no kernel of either waits on memory:
+//
+//  - Up to 1,024 requests: a gang. Every CTA of one launch plans the whole
+//    batch for itself, in shared memory, and does its share of the pieces; the
+//    last CTA to finish writes what the others may still have been reading.
+//  - More: a team. One cluster of CTAs, whose barriers are the hardware's,
+//    plans together and does little work itself; a second kernel, launched as
+//    a dependent of the first where the sizes of the call allow for more,
+//    does it on the whole GPU (how much there is, only the device knows).
 //
 // Nothing depends on the order in which atomics land: a request's claim on
 // its sequence and the holders of a shared page are a maximum and a count,
@@ -20,8 +24,8 @@ namespace db {
 namespace {
 
 constexpr uint32_t kMaxTeam = 8;        // CTAs of the largest team
-constexpr uint32_t kTeamThreads = 1024; // threads of a CTA of a cluster
-constexpr uint32_t kSmallThreads = 256; // threads of the smallest team
+constexpr uint32_t kTeamThreads = 1024; // threads of a CTA of a team or a gang,
+constexpr uint32_t kSmallThreads = 256; // and of a gang with few requests
 constexpr uint32_t kRows = 8;           // requests of a group (see "row units")
 constexpr uint32_t kSearch = 1024;      // starts that a second kernel keeps in shared memory
 constexpr uint32_t kOwnEntries = 1024;  // entries that a team does itself, for each of its CTAs, and
@@ -34,9 +38,8 @@ constexpr uint32_t kNoMove = 0xFFFFFFFFu;
 constexpr uint32_t kNoEntry = 0xFFFFFFFEu;   // a row without an entry in the column
 constexpr uint32_t kBadEntry = 0xFFFFFFFFu;  // no page
 
-// Free words that a CTA of a team keeps in shared memory.
-template <uint32_t kThreads>
-constexpr uint32_t kTeamWords = kThreads == kSmallThreads ? 1024 : 2048;
+constexpr uint32_t kTeamWords = 2048;    // free words that a CTA of a team keeps in shared memory
+constexpr uint32_t kGangWords = 8192;    // free words that a CTA of a gang counts
 
 // One request's place in the plan.
 struct __align__(16) Plan {
@@ -47,6 +50,9 @@ struct __align__(16) Plan {
 };
 
 struct Head {
+  unsigned long long released;  // a gang's sum over its CTAs, zero between calls
+  uint32_t done;       // CTAs of a gang that are through, zero between calls
+  uint32_t bad;        // a gang's error, zero between calls
   uint32_t units;      // left for the second kernel: units, pages or moves
   uint32_t used;       // extend: free words up to the last one used
   uint32_t n_live;     // compact: live pages
@@ -285,6 +291,72 @@ __device__ __forceinline__ void add_error(db_counters* ctr, bool bad) {
     atomicOr((unsigned long long*)&ctr->err, (unsigned long long)DB_ERR_PAGE_TABLE);
 }
 
+// -------------------------------------------------------------------- the gang
+// Requests by what they name, in a CTA: open addressing with two places for
+// each thread, so that a free one is always found. Numbers are below 2^31.
+template <uint32_t kThreads>
+struct Names {
+  static constexpr uint32_t kPlaces = 2 * kThreads;
+  uint32_t key[kPlaces], least[kPlaces], count[kPlaces];
+  __device__ __forceinline__ void clear() {
+    for (uint32_t k = threadIdx.x; k < kPlaces; k += kThreads) {
+      key[k] = least[k] = 0xFFFFFFFFu;
+      count[k] = 0;
+    }
+  }
+  __device__ __forceinline__ uint32_t place(uint32_t name) {
+    uint32_t k = name * 2654435761u >> 16 & (kPlaces - 1);
+    for (uint32_t tries = 0; tries < kPlaces; ++tries) {
+      const uint32_t was = atomicCAS(&key[k], 0xFFFFFFFFu, name);
+      if (was == 0xFFFFFFFFu || was == name) break;
+      k = (k + 1) & (kPlaces - 1);
+    }
+    return k;
+  }
+};
+
+// Whether this CTA is the last of its gang to come here (a barrier of the CTA;
+// what all of them have read before is read).
+__device__ __forceinline__ bool last_of_gang(Head* head) {
+  __shared__ uint32_t s_last;
+  __syncthreads();
+  if (gridDim.x == 1) return true;
+  if (threadIdx.x == 0) {
+    __threadfence();
+    s_last = atomicAdd(&head->done, 1u) == gridDim.x - 1;
+    if (s_last) head->done = 0;
+  }
+  __syncthreads();
+  return s_last;
+}
+
+// The same, with a count and an error of every CTA summed for the last one.
+__device__ __forceinline__ bool last_of_gang(Head* head, uint32_t count, bool bad, uint64_t* total,
+                                             bool* any_bad) {
+  __shared__ uint32_t s_count, s_bad;
+  if (threadIdx.x == 0) s_count = s_bad = 0;
+  __syncthreads();
+  const uint32_t c = __reduce_add_sync(kFull, count);
+  const bool b = __any_sync(kFull, bad);
+  if ((threadIdx.x & 31) == 0) {
+    if (c) atomicAdd(&s_count, c);
+    if (b) s_bad = 1;
+  }
+  __syncthreads();
+  if (gridDim.x > 1 && threadIdx.x == 0) {
+    if (s_count) atomicAdd(&head->released, (unsigned long long)s_count);
+    if (s_bad) atomicOr(&head->bad, 1u);
+  }
+  if (!last_of_gang(head)) return false;
+  *total = s_count;
+  *any_bad = s_bad;
+  if (gridDim.x > 1 && threadIdx.x == 0) {
+    *total = atomicExch(&head->released, 0ull);
+    *any_bad = atomicExch(&head->bad, 0u);
+  }
+  return true;
+}
+
 // ---------------------------------------------------------------- free words
 // Word w of the free bits, without bits past n_pages.
 __device__ __forceinline__ uint32_t ld_word(const uint32_t* bits, uint32_t w, uint32_t n_pages) {
@@ -497,8 +569,8 @@ __device__ __forceinline__ AllUnits all_units(const Rows& p, uint32_t* s_start) 
 
 // The end of a planning team: each CTA's own units, or all units to the second
 // kernel. A team that plans in more than one round always has one.
-template <uint32_t kThreads, bool kSolo, typename F>
-__device__ __forceinline__ void own_units(const Team<kThreads, kSolo>& team, const Rows& p,
+template <uint32_t kThreads, typename F>
+__device__ __forceinline__ void own_units(const Team<kThreads, false>& team, const Rows& p,
                                           RowPlan<kThreads>* s, uint32_t units, uint32_t entries,
                                           F work) {
   const bool own = !p.rest || (p.n <= team.threads() && entries <= kOwnEntries * team.size);
@@ -516,10 +588,11 @@ struct FreeParams {
 
 template <typename X>
 __device__ __forceinline__ void free_units(const Rows& p, const X& x, uint32_t first,
-                                           uint32_t stride, uint32_t units) {
-  const uint32_t lane = threadIdx.x & 31;
+                                           uint32_t stride, uint32_t units, uint32_t* count,
+                                           bool* error) {
   uint32_t released = 0;
   bool bad = false;
+  const uint32_t lane = threadIdx.x & 31;
   for (uint32_t u = first; u < units; u += stride) {
     const auto at = x.find(u);
     const uint32_t c = at.base + lane;
@@ -578,22 +651,76 @@ __device__ __forceinline__ void free_units(const Rows& p, const X& x, uint32_t f
       ++released;
     }
   }
+  *count = released;
+  *error = bad;
+}
+
+// The same, into the counters.
+template <typename X>
+__device__ __forceinline__ void free_and_count(const Rows& p, const X& x, uint32_t first,
+                                               uint32_t stride, uint32_t units) {
+  uint32_t released;
+  bool bad;
+  free_units(p, x, first, stride, units, &released, &bad);
   if (p.ctr) {
     add_count(&p.ctr->total, released);
     add_error(p.ctr, bad);
   }
 }
 
-template <uint32_t kThreads, bool kSolo>
-__global__ void __launch_bounds__(kThreads) page_free_kernel(const FreeParams q) {
+template <uint32_t kThreads>
+__global__ void __launch_bounds__(kThreads) page_free_gang_kernel(const FreeParams q) {
   __shared__ TeamShared s_team;
   __shared__ RowPlan<kThreads> s_plan;
+  __shared__ Names<kThreads> s_names;
   const Rows& p = q.r;
-  Team<kThreads, kSolo> team(&s_team);
+  Team<kThreads, true> cta(&s_team);
+  s_names.clear();
+  __syncthreads();
+  wait_for_prerequisites();
+  dependents_may_launch();
+  const uint32_t i = threadIdx.x;
+  const bool mine = i < p.n;
+  uint2 r = make_uint2(0, 0);  // sequence, tokens kept
+  uint32_t len = 0, at = 0;
+  if (mine) r = __ldcg(reinterpret_cast<const uint2*>(&q.req[i]));
+  const bool named = mine && r.x < p.t.n_seqs;
+  if (named) {
+    len = __ldcg(&p.t.length[r.x]);
+    at = s_names.place(r.x);
+    atomicMin(&s_names.least[at], i);
+  }
+  __syncthreads();
+  const bool ok = named && s_names.least[at] == i;
+  const bool cut = ok && r.y < len;
+  Plan pl = {0, 0, 0, 0};
+  if (cut)
+    pl = Plan{r.x, pages_of(r.y, p.t.page_tokens),
+              min(pages_of(len, p.t.page_tokens), p.t.columns), 0};
+  uint32_t units = 0, entries = 0, released;
+  bool bad;
+  plan_rows(cta, p, &s_plan, i, mine, pl, &units, &entries);
+  const uint32_t invalid = __syncthreads_count(mine && !ok);
+  constexpr uint32_t kWarps = kThreads / 32;
+  free_units(p, OwnUnits<kThreads>{&s_plan}, i / 32 * gridDim.x + blockIdx.x, gridDim.x * kWarps, units,
+             &released, &bad);
+  uint64_t total;
+  if (!last_of_gang(p.w.head, released, bad, &total, &bad)) return;
+  if (cut) p.t.length[r.x] = r.y;
+  if (mine && p.status) p.status[i] = ok ? DB_PAGE_OK : DB_PAGE_INVALID;
+  if (i == 0 && p.ctr)
+    *p.ctr = db_counters{total, invalid, 0, bad ? (uint64_t)DB_ERR_PAGE_TABLE : 0};
+}
+
+__global__ void __launch_bounds__(kTeamThreads) page_free_team_kernel(const FreeParams q) {
+  __shared__ TeamShared s_team;
+  __shared__ RowPlan<kTeamThreads> s_plan;
+  const Rows& p = q.r;
+  Team<kTeamThreads, false> team(&s_team);
   wait_for_prerequisites();
   dependents_may_launch();
   const uint32_t per = team.per(p.n), at = team.rank * per + threadIdx.x, step = per * team.size;
-  const bool one = kSolo || p.n <= step;  // a thread for every request
+  const bool one = p.n <= step;  // a thread for every request
   if (p.ctr && team.id() == 0) *p.ctr = db_counters{0, 0, 0, 0};
   db_page_cut r = {0, 0};
   uint32_t len = 0;
@@ -633,8 +760,8 @@ __global__ void __launch_bounds__(kThreads) page_free_kernel(const FreeParams q)
   }
   if (p.ctr) add_count(&p.ctr->n_invalid, invalid);
   own_units(team, p, &s_plan, units, entries,
-            [&](const OwnUnits<kThreads>& x, uint32_t first, uint32_t stride, uint32_t end) {
-              free_units(p, x, first, stride, end);
+            [&](const OwnUnits<kTeamThreads>& x, uint32_t first, uint32_t stride, uint32_t end) {
+              free_and_count(p, x, first, stride, end);
             });
 }
 
@@ -648,7 +775,7 @@ __global__ void __launch_bounds__(kUnitThreads) page_free_units_kernel(const Fre
   const uint32_t units = p.w.head->units, first = (blockIdx.x * kUnitThreads + threadIdx.x) / 32;
   if (blockIdx.x * (kUnitThreads / 32) >= units) return;
   const AllUnits x = all_units(p, s_start);
-  free_units(p, x, first, gridDim.x * (kUnitThreads / 32), units);
+  free_and_count(p, x, first, gridDim.x * (kUnitThreads / 32), units);
 }
 
 // ---------------------------------------------------------------------- fork
@@ -658,7 +785,7 @@ struct ForkParams {
 };
 
 template <typename X>
-__device__ __forceinline__ void fork_units(const Rows& p, const X& x, uint32_t first,
+__device__ __forceinline__ bool fork_units(const Rows& p, const X& x, uint32_t first,
                                            uint32_t stride, uint32_t units) {
   const uint32_t lane = threadIdx.x & 31;
   bool bad = false;
@@ -694,19 +821,60 @@ __device__ __forceinline__ void fork_units(const Rows& p, const X& x, uint32_t f
       times = 0;
     }
   }
-  if (p.ctr) add_error(p.ctr, bad);
+  return bad;
 }
 
-template <uint32_t kThreads, bool kSolo>
-__global__ void __launch_bounds__(kThreads) page_fork_kernel(const ForkParams q) {
+template <uint32_t kThreads>
+__global__ void __launch_bounds__(kThreads) page_fork_gang_kernel(const ForkParams q) {
   __shared__ TeamShared s_team;
   __shared__ RowPlan<kThreads> s_plan;
+  __shared__ Names<kThreads> s_names;
   const Rows& p = q.r;
-  Team<kThreads, kSolo> team(&s_team);
+  Team<kThreads, true> cta(&s_team);
+  s_names.clear();
+  __syncthreads();
+  wait_for_prerequisites();
+  dependents_may_launch();
+  const uint32_t i = threadIdx.x;
+  const bool mine = i < p.n;
+  uint4 r = make_uint4(0, 0, 0, 0);  // parent, child, tokens
+  uint32_t held = 0, of = 0, at = 0;  // the child's and the parent's lengths
+  if (mine) r = __ldcg(reinterpret_cast<const uint4*>(&q.req[i]));
+  const bool named = mine && r.y < p.t.n_seqs;
+  if (named) {
+    held = __ldcg(&p.t.length[r.y]);
+    if (r.x < p.t.n_seqs) of = __ldcg(&p.t.length[r.x]);
+    at = s_names.place(r.y);
+    atomicMin(&s_names.least[at], i);
+  }
+  __syncthreads();
+  const bool ok = named && s_names.least[at] == i && r.x < p.t.n_seqs && r.x != r.y && held == 0 &&
+                  r.z <= of;
+  Plan pl = {0, 0, 0, 0};
+  if (ok) pl = Plan{r.y, 0, min(pages_of(r.z, p.t.page_tokens), p.t.columns), r.x};
+  uint32_t units = 0, entries = 0;
+  plan_rows(cta, p, &s_plan, i, mine, pl, &units, &entries);
+  const uint32_t invalid = __syncthreads_count(mine && !ok);
+  constexpr uint32_t kWarps = kThreads / 32;
+  bool bad = fork_units(p, OwnUnits<kThreads>{&s_plan}, i / 32 * gridDim.x + blockIdx.x,
+                        gridDim.x * kWarps, units);
+  uint64_t none;
+  if (!last_of_gang(p.w.head, 0, bad, &none, &bad)) return;
+  if (ok) p.t.length[r.y] = r.z;
+  if (mine && p.status) p.status[i] = ok ? DB_PAGE_OK : DB_PAGE_INVALID;
+  if (i == 0 && p.ctr)
+    *p.ctr = db_counters{entries, invalid, 0, bad ? (uint64_t)DB_ERR_PAGE_TABLE : 0};
+}
+
+__global__ void __launch_bounds__(kTeamThreads) page_fork_team_kernel(const ForkParams q) {
+  __shared__ TeamShared s_team;
+  __shared__ RowPlan<kTeamThreads> s_plan;
+  const Rows& p = q.r;
+  Team<kTeamThreads, false> team(&s_team);
   wait_for_prerequisites();
   dependents_may_launch();
   const uint32_t per = team.per(p.n), at = team.rank * per + threadIdx.x, step = per * team.size;
-  const bool one = kSolo || p.n <= step;  // a thread for every request
+  const bool one = p.n <= step;  // a thread for every request
   if (p.ctr && team.id() == 0) *p.ctr = db_counters{0, 0, 0, 0};
   db_page_fork_req r = {0, 0, 0, 0};
   uint32_t held = 0, of = 0;  // the child's and the parent's lengths
@@ -761,8 +929,9 @@ __global__ void __launch_bounds__(kThreads) page_fork_kernel(const ForkParams q)
     }
   }
   own_units(team, p, &s_plan, units, entries,
-            [&](const OwnUnits<kThreads>& x, uint32_t first, uint32_t stride, uint32_t end) {
-              fork_units(p, x, first, stride, end);
+            [&](const OwnUnits<kTeamThreads>& x, uint32_t first, uint32_t stride, uint32_t end) {
+              const bool bad = fork_units(p, x, first, stride, end);
+              if (p.ctr) add_error(p.ctr, bad);
             });
 }
 
@@ -774,7 +943,8 @@ __global__ void __launch_bounds__(kUnitThreads) page_fork_units_kernel(const For
   const uint32_t units = p.w.head->units, first = (blockIdx.x * kUnitThreads + threadIdx.x) / 32;
   if (blockIdx.x * (kUnitThreads / 32) >= units) return;
   const AllUnits x = all_units(p, s_start);
-  fork_units(p, x, first, gridDim.x * (kUnitThreads / 32), units);
+  const bool bad = fork_units(p, x, first, gridDim.x * (kUnitThreads / 32), units);
+  if (p.ctr) add_error(p.ctr, bad);
 }
 
 // -------------------------------------------------------------------- extend
@@ -827,8 +997,8 @@ __device__ __forceinline__ Ask ask(const ExtendParams& p, uint32_t i, bool any) 
 }
 
 // and with that.
-__device__ __forceinline__ void settle(const ExtendParams& p, uint32_t i, Ask* a) {
-  a->mine = a->named && claimed(p.w.claim, a->seq, i);
+__device__ __forceinline__ void settle(Ask* a, bool first) {
+  a->mine = a->named && first;
   a->ok = a->mine && a->fits && !a->corrupt;
   a->corrupt &= a->mine;
   if (!a->ok) a->grow = a->part = 0;
@@ -855,22 +1025,155 @@ __device__ __forceinline__ void place_pages(const ExtendParams& p, const Finder&
   }
 }
 
-template <uint32_t kThreads, bool kSolo>
-__global__ void __launch_bounds__(kThreads) page_extend_kernel(const ExtendParams p) {
-  constexpr uint32_t kWords = kTeamWords<kThreads>;
+// What is left of a quad of free words when the batch takes `need` pages;
+// *used: words up to the last one used, if that is in it.
+__device__ __forceinline__ uint4 left_of(const uint4& v, const uint4& before, uint32_t need,
+                                         uint32_t* used, uint32_t w) {
+  if (before.w + __popc(v.w) < need) return make_uint4(0, 0, 0, 0);
+  const uint32_t vs[4] = {v.x, v.y, v.z, v.w}, bs[4] = {before.x, before.y, before.z, before.w};
+  uint32_t ls[4];
+#pragma unroll
+  for (uint32_t k = 0; k < 4; ++k) {
+    ls[k] = 0;
+    if (bs[k] >= need) {
+      ls[k] = vs[k];
+    } else if (bs[k] + __popc(vs[k]) >= need) {
+      ls[k] = vs[k] & ~((2u << nth_bit(vs[k], need - bs[k] - 1)) - 1);
+      *used = w + k + 1;
+    }
+  }
+  return make_uint4(ls[0], ls[1], ls[2], ls[3]);
+}
+
+// The e-th free page, found in the free words: the thread whose share has it,
+// and then the quad of that share.
+template <uint32_t kThreads>
+__device__ __forceinline__ uint32_t nth_page(const uint32_t* bits, uint32_t n_pages,
+                                             const uint32_t* s_first, uint32_t quads, uint32_t e) {
+  uint32_t lo = 0, hi = kThreads;
+  while (hi - lo > 1) {
+    const uint32_t mid = (lo + hi) >> 1;
+    if (s_first[mid] <= e) lo = mid; else hi = mid;
+  }
+  uint32_t w = lo * quads * 4;
+  e -= s_first[lo];
+  const uint32_t all = (n_pages + 31) / 32;
+  for (uint32_t s = 0; s < quads; ++s, w += 4) {
+    const uint4 v = ld_quad(bits, w, all, n_pages);
+    const uint32_t x = __popc(v.x), y = x + __popc(v.y), z = y + __popc(v.z), end = z + __popc(v.w);
+    if (e < end) {
+      if (e < x) return 32 * w + nth_bit(v.x, e);
+      if (e < y) return 32 * (w + 1) + nth_bit(v.y, e - x);
+      if (e < z) return 32 * (w + 2) + nth_bit(v.z, e - y);
+      return 32 * (w + 3) + nth_bit(v.w, e - z);
+    }
+    e -= end;
+  }
+  return n_pages;  // not reached: e is below the free pages counted
+}
+
+template <uint32_t kThreads>
+__global__ void __launch_bounds__(kThreads) page_extend_gang_kernel(const ExtendParams p) {
+  __shared__ TeamShared s_team;
+  __shared__ Names<kThreads> s_names;
+  __shared__ Plan s_plan[kThreads];
+  __shared__ uint32_t s_first[kThreads];  // free pages before each thread's share of the words
+  Team<kThreads, true> cta(&s_team);
+  s_names.clear();
+  __syncthreads();
+  wait_for_prerequisites();
+  dependents_may_launch();
+  const uint32_t i = threadIdx.x;
+  const bool mine = i < p.n;
+  Bits bits = load_free(cta, p.t.free, p.t.n_pages);
+  Ask a = ask(p, i, mine);
+  uint32_t at = 0;
+  if (a.named) {
+    at = s_names.place(a.seq);
+    atomicMin(&s_names.least[at], i);
+  }
+  const bool shares = scan_free(cta, bits, p.t.free, p.t.n_pages, a.shares());
+  settle(&a, a.named && s_names.least[at] == i);
+  uint32_t need, n_moves = 0, rank = 0, start;
+  bool cow = false;
+  if (shares) {
+    // How many of the batch's requests hold each shared page, and the last of them.
+    __syncthreads();
+    s_names.clear();
+    __syncthreads();
+    if (a.shares()) {
+      at = s_names.place(a.last);
+      atomicAdd(&s_names.count[at], 1u);
+      atomicMin(&s_names.least[at], ~i);
+    }
+    __syncthreads();
+    if (a.shares()) cow = !(s_names.count[at] == a.refs && s_names.least[at] == ~i);
+    start = cta.template scan<true>(a.grow + cow, &need, cow, &n_moves, &rank);
+  } else {
+    start = cta.template scan<false>(a.grow, &need);
+  }
+  s_plan[i] = Plan{a.seq, a.had - cow, start, cow ? rank : kNoMove};
+  s_first[i] = bits.before;
+  const bool go = need <= bits.total;
+  const uint32_t invalid = __syncthreads_count(mine && !a.ok);
+  const bool corrupt = __syncthreads_or(a.corrupt);
+  if (go)
+    for (uint32_t e = (i / 32 * gridDim.x + blockIdx.x) * 32 + i % 32; e < need;
+         e += gridDim.x * kThreads) {
+      uint32_t lo = 0, hi = kThreads;
+      while (hi - lo > 1) {
+        const uint32_t mid = (lo + hi) >> 1;
+        if (s_plan[mid].end <= e) lo = mid; else hi = mid;
+      }
+      const Plan pl = s_plan[lo];
+      const uint32_t j = e - pl.end;
+      if (j == 0 && pl.aux != kNoMove) continue;  // replaces an entry that a CTA may yet read
+      const uint32_t page = nth_page<kThreads>(p.t.free, p.t.n_pages, s_first, bits.quads, e);
+      p.t.table[(uint64_t)pl.row * p.t.columns + pl.from + j] = (int32_t)page;
+      p.t.refs[page] = 1;
+    }
+  if (!last_of_gang(p.w.head)) return;
+  if (cow && go) {
+    const uint32_t page = nth_page<kThreads>(p.t.free, p.t.n_pages, s_first, bits.quads, start);
+    p.t.table[(uint64_t)a.seq * p.t.columns + a.had - 1] = (int32_t)page;
+    p.t.refs[page] = 1;
+    *reinterpret_cast<uint4*>(&p.moves[rank]) = make_uint4(a.last, page, a.part, 0);
+    const uint32_t same = __match_any_sync(__activemask(), a.last);
+    if ((same & lanemask_lt()) == 0) atomicSub(&p.t.refs[a.last], (uint32_t)__popc(same));
+  }
+  if (a.ok && go) p.t.length[a.seq] = a.now;
+  if (mine && p.status) p.status[i] = !a.ok ? DB_PAGE_INVALID : go ? DB_PAGE_OK : DB_PAGE_SHORT;
+  if (i == 0) {
+    *p.n_moves = go ? n_moves : 0;
+    if (p.ctr)
+      *p.ctr = db_counters{need, invalid, go ? 0 : p.n - invalid,
+                           corrupt ? (uint64_t)DB_ERR_PAGE_TABLE : 0};
+  }
+  __syncthreads();  // the pages are found
+  if (go && bits.before < need)
+    each_quad(bits, p.t.free, p.t.n_pages, [&](uint32_t w, const uint4& v, const uint4& before) {
+      if (before.x >= need) return false;
+      uint32_t used;
+      st_quad(p.t.free, w, (p.t.n_pages + 31) / 32, left_of(v, before, need, &used, w));
+      return true;
+    });
+}
+
+__global__ void __launch_bounds__(kTeamThreads) page_extend_team_kernel(const ExtendParams p) {
+  constexpr uint32_t kThreads = kTeamThreads, kWords = kTeamWords;
   __shared__ TeamShared s_team;
   __shared__ uint32_t s_start[kThreads];
   __shared__ Plan s_plan[kThreads];
   __shared__ __align__(16) uint32_t s_before[kWords], s_bits[kWords];
   __shared__ __align__(16) uint32_t s_used[4];
   __shared__ uint32_t s_end;
-  Team<kThreads, kSolo> team(&s_team);
+  Team<kThreads, false> team(&s_team);
   wait_for_prerequisites();
   dependents_may_launch();
   const uint32_t id = team.id(), words = (p.t.n_pages + 31) / 32;
   const uint32_t per = team.per(p.n), at = team.rank * per + threadIdx.x;
   const uint32_t step = per * team.size;
-  const bool one = kSolo || p.n <= step;  // a thread for every request, which asks once
+  const bool one = p.n <= step;  // a thread for every request, which asks once
   Bits bits = load_free(team, p.t.free, p.t.n_pages);
   if (p.ctr && id == 0) *p.ctr = db_counters{0, 0, 0, 0};
   Ask a = ask(p, at, false);
@@ -883,7 +1186,7 @@ __global__ void __launch_bounds__(kThreads) page_extend_kernel(const ExtendParam
   team.started();
   // Also the barrier after the claims, and whether any request may share.
   shares = scan_free(team, bits, p.t.free, p.t.n_pages, shares);
-  if (one && at < p.n && threadIdx.x < per) settle(p, at, &a);
+  if (one && at < p.n && threadIdx.x < per) settle(&a, a.named && claimed(p.w.claim, a.seq, at));
   if (shares) {
     // How many of the batch's requests hold each shared page, and the last of
     // them; requests of a warp that hold the same one (samples of one prompt)
@@ -891,7 +1194,7 @@ __global__ void __launch_bounds__(kThreads) page_extend_kernel(const ExtendParam
     for (uint32_t i = at; threadIdx.x < per && i < p.n; i += step) {
       if (!one) {
         a = ask(p, i, true);
-        settle(p, i, &a);
+        settle(&a, a.named && claimed(p.w.claim, a.seq, i));
       }
       if (a.shares()) {
         const uint32_t same = __match_any_sync(__activemask(), a.last);
@@ -909,7 +1212,7 @@ __global__ void __launch_bounds__(kThreads) page_extend_kernel(const ExtendParam
     const bool mine = threadIdx.x < per && i < p.n;
     if (!one) {
       a = ask(p, i, mine);
-      if (mine) settle(p, i, &a);
+      if (mine) settle(&a, a.named && claimed(p.w.claim, a.seq, i));
     }
     bool cow = false;
     uint32_t total, copies = 0, rank = 0, x;
@@ -943,34 +1246,17 @@ __global__ void __launch_bounds__(kThreads) page_extend_kernel(const ExtendParam
     each_quad(bits, p.t.free, p.t.n_pages, [&](uint32_t w, const uint4& v, const uint4& before) {
       if (before.x >= need) return false;
       if (few && w < kWords) {
-        if (kSolo) {
-          *reinterpret_cast<uint4*>(&s_before[w]) = before;
-          *reinterpret_cast<uint4*>(&s_bits[w]) = v;
-        } else {
-          team.to_all(&s_before[w], before);
-          team.to_all(&s_bits[w], v);
-        }
+        team.to_all(&s_before[w], before);
+        team.to_all(&s_bits[w], v);
       }
       if (p.rest) {
         st_quad(p.w.before, w, words, before);
         st_quad(p.w.bits, w, words, v);
       }
-      uint4 left = make_uint4(0, 0, 0, 0);
-      if (before.w + __popc(v.w) >= need) {  // the last quad used
-        const uint32_t vs[4] = {v.x, v.y, v.z, v.w}, bs[4] = {before.x, before.y, before.z, before.w};
-        uint32_t ls[4], used = 0;
-#pragma unroll
-        for (uint32_t k = 0; k < 4; ++k) {
-          ls[k] = 0;
-          if (bs[k] >= need) {
-            ls[k] = vs[k];
-          } else if (bs[k] + __popc(vs[k]) >= need) {
-            ls[k] = vs[k] & ~((2u << nth_bit(vs[k], need - bs[k] - 1)) - 1);
-            used = w + k + 1;
-          }
-        }
-        left = make_uint4(ls[0], ls[1], ls[2], ls[3]);
-        if (kSolo) s_used[0] = used; else team.to_all(s_used, make_uint4(used, 0, 0, 0));
+      uint32_t used = 0;
+      const uint4 left = left_of(v, before, need, &used, w);
+      if (used) {
+        team.to_all(s_used, make_uint4(used, 0, 0, 0));
         if (p.rest) p.w.head->used = used;
       }
       st_quad(p.t.free, w, words, left);
@@ -983,7 +1269,7 @@ __global__ void __launch_bounds__(kThreads) page_extend_kernel(const ExtendParam
   for (uint32_t i = at; threadIdx.x < per && i < p.n; i += step) {
     if (!one) {
       a = ask(p, i, true);
-      settle(p, i, &a);
+      settle(&a, a.named && claimed(p.w.claim, a.seq, i));
       move = p.w.plan[i].aux;
     }
     if (move != kNoMove) {  // at least one holder of every shared page copies, and clears for all
@@ -1270,6 +1556,8 @@ int nothing(db_counters* ctr, uint32_t* n_moves, cudaStream_t s) {
   return 0;
 }
 
+inline uint32_t most_of(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
 // CTAs of a team that wants `threads`.
 uint32_t team_size(uint64_t threads) {
   uint32_t c = 1;
@@ -1283,15 +1571,24 @@ unsigned whole_grid(uint64_t threads, uint32_t block, uint32_t each) {
   return (unsigned)(want < 1 ? 1 : want < most ? want : most);
 }
 
-// Free and fork: the team, and the whole GPU where there may be much to do.
+// CTAs of a gang with at most `pieces` pieces, `each` of which a CTA does at a
+// time: one where they are few, else up to `most` an SM.
+unsigned gang_size(uint64_t pieces, uint64_t few, uint32_t each, uint32_t most) {
+  if (pieces <= few) return 1;
+  const uint64_t want = (pieces + each - 1) / each, all = (uint64_t)most * num_sms();
+  return (unsigned)(want < all ? want : all);
+}
+
+// Free and fork: a gang, or a team and then the whole GPU where there may be
+// much to do.
 template <typename P>
-int launch_rows(void (*small)(P), void (*solo)(P), void (*team)(P), void (*rest)(P),
-                cudaStream_t s, P& p) {
+int launch_rows(void (*gang)(P), void (*team)(P), void (*rest)(P), cudaStream_t s, P& p) {
   const uint64_t units = ((uint64_t)p.r.n + kRows - 1) / kRows * (((uint64_t)p.r.t.columns + 31) / 32);
-  const uint32_t ctas = p.r.n <= kTeamThreads ? 1 : team_size(2 * (uint64_t)p.r.n);
+  if (p.r.n <= kSmallThreads)
+    return launch_dependent(gang, gang_size(units, kRestUnits, kSmallThreads / 32, 2), kSmallThreads, 0, s, p);
+  const uint32_t ctas = most_of(team_size(4 * (uint64_t)p.r.n), 2);
   p.r.rest = units > kRestUnits || p.r.n > ctas * kTeamThreads;
-  const int e = p.r.n <= kSmallThreads ? launch_team(small, 1, kSmallThreads, s, p)
-                                       : launch_team(ctas == 1 ? solo : team, ctas, kTeamThreads, s, p);
+  const int e = launch_team(team, ctas, kTeamThreads, s, p);
   if (e || !p.r.rest) return e;
   return launch_dependent(rest, whole_grid(units * 32, kUnitThreads, 8), kUnitThreads, 0, s, p);
 }
@@ -1320,8 +1617,7 @@ extern "C" int db_page_free(const db_page_tables* t, const db_page_cut* req, uin
   p.r.status = status;
   p.r.ctr = ctr;
   p.req = req;
-  return launch_rows(page_free_kernel<kSmallThreads, true>, page_free_kernel<kTeamThreads, true>,
-                     page_free_kernel<kTeamThreads, false>, page_free_units_kernel, s, p);
+  return launch_rows(page_free_gang_kernel<kSmallThreads>, page_free_team_kernel, page_free_units_kernel, s, p);
 }
 
 extern "C" int db_page_fork(const db_page_tables* t, const db_page_fork_req* req, uint32_t n,
@@ -1337,8 +1633,7 @@ extern "C" int db_page_fork(const db_page_tables* t, const db_page_fork_req* req
   p.r.status = status;
   p.r.ctr = ctr;
   p.req = req;
-  return launch_rows(page_fork_kernel<kSmallThreads, true>, page_fork_kernel<kTeamThreads, true>,
-                     page_fork_kernel<kTeamThreads, false>, page_fork_units_kernel, s, p);
+  return launch_rows(page_fork_gang_kernel<kSmallThreads>, page_fork_team_kernel, page_fork_units_kernel, s, p);
 }
 
 extern "C" int db_page_extend(const db_page_tables* t, const db_page_grow* req, uint32_t n,
@@ -1359,17 +1654,15 @@ extern "C" int db_page_extend(const db_page_tables* t, const db_page_grow* req, 
   p.ctr = ctr;
   const uint64_t pages = (uint64_t)n * t->columns < t->n_pages ? (uint64_t)n * t->columns : t->n_pages;
   const uint32_t words = (t->n_pages + 31) / 32;
-  p.rest = pages > kRestPages || n > kMaxTeam * kTeamThreads || words > kTeamWords<kTeamThreads>;
-  int e;
-  if (n <= kSmallThreads && words <= kTeamWords<kSmallThreads>) {
-    e = launch_team(page_extend_kernel<kSmallThreads, true>, 1, kSmallThreads, s, p);
-  } else if (n <= kTeamThreads && words <= kTeamWords<kTeamThreads>) {
-    e = launch_team(page_extend_kernel<kTeamThreads, true>, 1, kTeamThreads, s, p);
-  } else {
-    uint32_t ctas = team_size((uint64_t)2 * n > words / 4 ? (uint64_t)2 * n : words / 4);
-    if (ctas == 1) ctas = 2;
-    e = launch_team(page_extend_kernel<kTeamThreads, false>, ctas, kTeamThreads, s, p);
-  }
+  if (n <= kSmallThreads && words <= 4 * kSmallThreads && pages <= kRestPages)
+    return launch_dependent(page_extend_gang_kernel<kSmallThreads>, 1, kSmallThreads, 0, s, p);
+  if (n <= kTeamThreads && words <= kGangWords)
+    return launch_dependent(page_extend_gang_kernel<kTeamThreads>,
+                            gang_size(pages, kRestPages, kTeamThreads, 1), kTeamThreads, 0, s, p);
+  p.rest = pages > kRestPages || n > kMaxTeam * kTeamThreads || words > kTeamWords;
+  uint32_t ctas = team_size(2ull * n > words / 4 ? 2ull * n : words / 4);
+  if (ctas == 1) ctas = 2;
+  const int e = launch_team(page_extend_team_kernel, ctas, kTeamThreads, s, p);
   if (e || !p.rest) return e;
   return launch_dependent(page_place_kernel, whole_grid(pages, kPlaceThreads, 8), kPlaceThreads, 0,
                           s, p);
