@@ -169,13 +169,17 @@ def _records(t: torch.Tensor, size: int) -> int:
 # builds a Stream object for it (2.9 us a call on the GPU's host, these 0.2 us).
 _device = getattr(torch._C, "_cuda_getDevice", None)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_cuda_ready = False
 
 
 def _stream(stream) -> int:
+    global _cuda_ready
     if stream is None:
-        if _raw_stream is None or _device is None or not torch.cuda.is_initialized():
-            return torch.cuda.current_stream().cuda_stream
-        return _raw_stream(_device())
+        if _cuda_ready:
+            return _raw_stream(_device())
+        now = torch.cuda.current_stream().cuda_stream  # initialises CUDA
+        _cuda_ready = _raw_stream is not None and _device is not None
+        return now
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -501,14 +505,16 @@ def page_workspace_size(n_seqs: int, n_pages: int) -> int:
 
 
 def _requests(t: torch.Tensor, size: int) -> int:
-    n = _records(t, size)
-    if n > 0xFFFFFFFF:
-        raise ValueError("a batch has fewer than 2^32 records")
+    n, rest = divmod(t.nbytes, size)
+    if rest or n > 0xFFFFFFFF:
+        raise ValueError(f"a batch is a whole number of {size}-byte records, fewer than 2^32")
     return n
 
 
 def _status(status: torch.Tensor | None, n: int) -> int | None:
-    if status is not None and status.numel() * status.element_size() < n:
+    if status is None:
+        return None
+    if status.nbytes < n:
         raise ValueError(f"status holds fewer than {n} bytes")
     return _ptr(status)
 
@@ -523,7 +529,7 @@ def page_extend(tables: PageTables, req: torch.Tensor, moves: torch.Tensor,
         raise ValueError(f"moves holds fewer than {n} records")
     _check("db_page_extend", _lib.db_page_extend(
         tables._ref, _ptr(req), n, _ptr(moves), _ptr(n_moves), _status(status, n), _ptr(ctr),
-        _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+        _ptr(ws), ws.nbytes, _stream(stream)))
 
 
 def page_fork(tables: PageTables, req: torch.Tensor, ws: torch.Tensor,
@@ -534,7 +540,7 @@ def page_fork(tables: PageTables, req: torch.Tensor, ws: torch.Tensor,
     n = _requests(req, 16)
     _check("db_page_fork", _lib.db_page_fork(
         tables._ref, _ptr(req), n, _status(status, n), _ptr(ctr), _ptr(ws),
-        ws.numel() * ws.element_size(), _stream(stream)))
+        ws.nbytes, _stream(stream)))
 
 
 def page_free(tables: PageTables, req: torch.Tensor, ws: torch.Tensor,
@@ -545,7 +551,7 @@ def page_free(tables: PageTables, req: torch.Tensor, ws: torch.Tensor,
     n = _requests(req, 8)
     _check("db_page_free", _lib.db_page_free(
         tables._ref, _ptr(req), n, _status(status, n), _ptr(ctr), _ptr(ws),
-        ws.numel() * ws.element_size(), _stream(stream)))
+        ws.nbytes, _stream(stream)))
 
 
 def page_compact(tables: PageTables, out: PageTables, moves: torch.Tensor, n_moves: torch.Tensor,
@@ -556,7 +562,7 @@ def page_compact(tables: PageTables, out: PageTables, moves: torch.Tensor, n_mov
     move."""
     _check("db_page_compact", _lib.db_page_compact(
         tables._ref, out._ref, _ptr(moves), _requests(moves, 16), _ptr(n_moves), _ptr(ctr),
-        _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+        _ptr(ws), ws.nbytes, _stream(stream)))
 
 
 def _strides(shape, stride, item: int) -> tuple[int, int]:
