@@ -11,6 +11,9 @@
 //    multiples of 16: a CTA works on one plane and segment at a time, in which
 //    as many lanes as a run has vectors (up to a warp) take a record, so that
 //    short runs share a warp and records are found without a division.
+//
+// Both are bound by memory: a page's bytes are read once and written once.
+// Times below are of one GB300, in microseconds.
 #include "common.cuh"
 #include "pagecache.h"
 
@@ -86,6 +89,11 @@ struct Vec<1> {
 };
 
 // ---------------------------------------------------------------------- fine
+// CTAs an SM of the largest grid: with 16, 537 MB of 64-byte pages take 138 and
+// 925 MB of partial pages of 1,536 bytes 185, with 64 117 and 165 (4.6 and 5.6
+// TB/s), with 256 117 and 186.
+constexpr uint32_t kFineCtas = 64;
+
 // Runs of one plane and one segment: `lanes` lanes take a record's run, kUnroll
 // vectors a lane, kBatch / kUnroll records at a time.
 template <int kVec, int kUnroll>
@@ -148,19 +156,20 @@ __global__ void __launch_bounds__(kThreads) page_copy_fine_kernel(const CopyPara
 
 // ---------------------------------------------------------------------- wide
 constexpr uint32_t kChunk = kWarpSlots * 16;  // bytes a warp moves at a time
+// Runs from here on go to the wide kernel. The other one takes 235 for partial
+// segments of 5.6 KB and 346 for 4 KB ones, this one 246 and 351; for whole 32
+// KiB pages it is 547 against 538 above, and for six pages 5.3 against 2.6.
 constexpr uint64_t kWideBytes = 8192;
 // CTAs an SM of the largest grid. How many records there are is on the device,
 // so the grid is bounded and loops; 8 CTAs are resident, and several times as
 // many even out what the loops leave at the end. 3,500 pages of 16 planes of
-// 32 KiB (3.67 GB read and written), us: 580 with one grid of residents, 557
+// 32 KiB (3.67 GB read and written): 580 with one grid of residents, 557
 // twice, 544 four times, 538 eight times (6.8 TB/s, the rate of a plain copy),
-// 535 sixteen times; six pages alone take 0.3 us less in CTAs of 128 threads
+// 535 sixteen times; six pages alone take 0.3 less in CTAs of 128 threads
 // than of 256. The same pages through shared memory by bulk copies (4 to 16 KiB,
-// 3 to 12 CTAs an SM, 2 or 4 stages ahead) took 570 to 607 us, and 2.8 KB
-// runs 75 us and more where these loads and stores take 44.
+// 3 to 12 CTAs an SM, 2 or 4 stages ahead) took 570 to 607, and 2.8 KB
+// runs 75 and more where these loads and stores take 44.
 constexpr uint32_t kWideCtas = 64;
-constexpr uint32_t kFineCtas = 64;
-
 __device__ __forceinline__ uint64_t div64(uint64_t a, uint32_t b) {
   return (a >> 32) ? a / b : (uint32_t)a / b;
 }

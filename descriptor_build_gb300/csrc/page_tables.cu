@@ -5,10 +5,10 @@
 // is work on pieces of it, found again by a search. There are two ways to it,
 // and no kernel of either waits on memory:
 //
-//  - Up to 1,024 requests: a gang. Every CTA of one launch plans the whole
-//    batch for itself, in shared memory, and does its share of the pieces; the
-//    last CTA to finish writes what the others may still have been reading.
-//  - More: a team. One cluster of CTAs, whose barriers are the hardware's,
+//  - Few requests: a gang. Every CTA of one launch plans the whole batch for
+//    itself, in shared memory, and does its share of the pieces; the last CTA
+//    to finish writes what the others may still have been reading.
+//  - Many: a team. One cluster of CTAs, whose barriers are the hardware's,
 //    plans together and does little work itself; a second kernel, launched as
 //    a dependent of the first where the sizes of the call allow for more,
 //    does it on the whole GPU (how much there is, only the device knows).
@@ -23,23 +23,43 @@
 namespace db {
 namespace {
 
-constexpr uint32_t kMaxTeam = 8;        // CTAs of the largest team
-constexpr uint32_t kTeamThreads = 1024; // threads of a CTA of a team or a gang,
-constexpr uint32_t kSmallThreads = 256; // and of a gang with few requests
-constexpr uint32_t kRows = 8;           // requests of a group (see "row units")
-constexpr uint32_t kSearch = 1024;      // starts that a second kernel keeps in shared memory
-constexpr uint32_t kOwnEntries = 1024;  // entries that a team does itself, for each of its CTAs, and
-constexpr uint32_t kOwnPages = 4096;    // pages, when a second kernel is there: where the sizes of
-constexpr uint32_t kRestUnits = 64;     // the call allow for more than kRestUnits, kRestPages or
-constexpr uint32_t kRestPages = 16384;  // kRestMoves
-constexpr uint32_t kRestMoves = 8192;
+// Times below are of one GB300, microseconds, of the sequence of calls named.
+//
+// What bounds these kernels is latency, and past that the rate at which an SM
+// takes scattered 4-byte accesses, one line a clock: a freed entry is a load
+// and a store of its reference and an atomic on its free bit. Bandwidth is
+// far away (a freed or taken page is 24 bytes).
+constexpr uint32_t kMaxTeam = 8;          // CTAs of the largest team (a portable cluster)
+constexpr uint32_t kTeamThreads = 1024;   // threads of a CTA of a team, or of a gang that extends
+// Threads of a CTA of a gang with few requests. A step of 48 sequences takes
+// 8.2 in CTAs of 256 or of 512 threads and took 11.7 in one of 1,024, whose
+// barriers and idle warps cost more than its width saves. Up to as many
+// requests free and fork go to a gang: 1,023 of one prompt took 14.4 and 12.7
+// in a gang of 1,024 threads and 13.3 and 11.0 as a team and a second kernel.
+constexpr uint32_t kSmallThreads = 256;
+// Requests of a group (see "row units"): 4, 8, 16 or 32 of them give 61, 49,
+// 46 or 50 for dropping and forking 1,023 samples anew, 21, 23, 25 or 33 for a
+// decode step of 4,096 sequences, and 13, 14, 15 or 34 for a turnover of 256.
+constexpr uint32_t kRows = 8;
+constexpr uint32_t kSearch = 1024;        // starts that a second kernel keeps in shared memory
+// Free words that a CTA of a gang counts (262,144 pages). Each CTA reads them
+// all: an extension by 320,000 pages out of a million took 23.5 in a gang and
+// takes 15 as a team and a second kernel, one by 98,000 of 262,144 takes 9.9
+// and took 8.0 + 5.2.
+constexpr uint32_t kGangWords = 8192;
+constexpr uint32_t kTeamWords = 2048;     // free words that a CTA of a team keeps in shared memory
+// A second kernel, or a gang of more than one CTA, is launched when the sizes
+// of a call allow for more than this. It costs 1.2 on the device and 2.3 on
+// the host when there turns out to be nothing to do; without it the 98,000
+// entries of a prompt chunk took 18.6 to free in the team's SMs, with it 11.
+constexpr uint32_t kRestUnits = 64, kRestPages = 16384, kRestMoves = 8192;
+// With a second kernel there, a team still does this itself: entries for each
+// of its CTAs (an SM takes about that many a microsecond), and pages.
+constexpr uint32_t kOwnEntries = 1024, kOwnPages = 4096;
 constexpr uint32_t kSoloEntries = 32768;  // table entries that a compaction's one CTA renames itself
 constexpr uint32_t kNoMove = 0xFFFFFFFFu;
 constexpr uint32_t kNoEntry = 0xFFFFFFFEu;   // a row without an entry in the column
 constexpr uint32_t kBadEntry = 0xFFFFFFFFu;  // no page
-
-constexpr uint32_t kTeamWords = 2048;    // free words that a CTA of a team keeps in shared memory
-constexpr uint32_t kGangWords = 8192;    // free words that a CTA of a gang counts
 
 // One request's place in the plan.
 struct __align__(16) Plan {
@@ -586,6 +606,9 @@ struct FreeParams {
   const db_page_cut* req;
 };
 
+// refs[p] -= the rows of the batch that drop p; p is free when nothing is left.
+// A step of 48 sequences frees its 12 pages in 4.4 (one launch, warm), 192
+// prompt chunks of 512 pages in 9.0, 64 sequences of 5,000 pages in 11.5.
 template <typename X>
 __device__ __forceinline__ void free_units(const Rows& p, const X& x, uint32_t first,
                                            uint32_t stride, uint32_t units, uint32_t* count,
@@ -784,6 +807,9 @@ struct ForkParams {
   const db_page_fork_req* req;
 };
 
+// The child's row is the parent's, refs[p] += the children that take p. 32
+// forks of 44 pages take 4.4, 1,023 of 1,024 pages (4 MB of tables written)
+// 5.6 + 6.5 for the plan and the units.
 template <typename X>
 __device__ __forceinline__ bool fork_units(const Rows& p, const X& x, uint32_t first,
                                            uint32_t stride, uint32_t units) {
@@ -1046,7 +1072,8 @@ __device__ __forceinline__ uint4 left_of(const uint4& v, const uint4& before, ui
 }
 
 // The e-th free page, found in the free words: the thread whose share has it,
-// and then the quad of that share.
+// and then the quad of that share. (Writing the list of all pages taken first,
+// word by word, took 25 for 320,000 pages, which were then placed in 5.)
 template <uint32_t kThreads>
 __device__ __forceinline__ uint32_t nth_page(const uint32_t* bits, uint32_t n_pages,
                                              const uint32_t* s_first, uint32_t quads, uint32_t e) {
@@ -1072,6 +1099,12 @@ __device__ __forceinline__ uint32_t nth_page(const uint32_t* bits, uint32_t n_pa
   return n_pages;  // not reached: e is below the free pages counted
 }
 
+// A request needs ceil((length + tokens) / T) - ceil(length / T) pages, and one
+// for a copy when it adds to a page that others hold: all of a page's holders
+// but the last when all are in the batch, else all of them. Start of request i
+// = the needs before it; page e of the batch = the e-th free one. 5.6 for 48
+// sequences, 9.9 for 192 times 512 pages, 10.8 for 1,023 holders of one page
+// that all copy it.
 template <uint32_t kThreads>
 __global__ void __launch_bounds__(kThreads) page_extend_gang_kernel(const ExtendParams p) {
   __shared__ TeamShared s_team;
@@ -1330,6 +1363,10 @@ struct CompactParams {
   Work w;
 };
 
+// 131,072 pages, 32,000 moves, 1,024 rows of 512 entries: 9.5 for plan, moves
+// and tables together, beside 626 for the moves' 4.25 GB. Listing free and live
+// pages word by word in one CTA first took 50.
+//
 // Live pages before a word.
 struct LiveStart {
   const uint32_t* before;
