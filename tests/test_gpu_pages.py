@@ -441,11 +441,12 @@ def test_copy_offsets_past_32_bits():
     assert int(x[:, 3].abs().sum()) == 0 and int(x[:, 69997].abs().sum()) == 0
 
 
-def test_copy_to_and_from_pinned_host_memory():
+@pytest.mark.parametrize("width", [4, 256])  # short runs, and pages of 16 KiB
+def test_copy_to_and_from_pinned_host_memory(width):
     db = lib()
     rng = np.random.default_rng(1)
-    x = torch.from_numpy(pool(rng, (3, 8, 16, 4), np.int32)).cuda()
-    h = torch.zeros((3, 5, 16, 4), dtype=torch.int32).pin_memory()
+    x = torch.from_numpy(pool(rng, (3, 8, 16, width), np.int32)).cuda()
+    h = torch.zeros((3, 5, 16, width), dtype=torch.int32).pin_memory()
     db.page_copy(u32([[7, 0, po.ALL, 0], [2, 4, 5, 0]], 4), dev([2]), x, h, 2)
     torch.cuda.synchronize()
     assert torch.equal(h[:, 0], x[:, 7].cpu()) and torch.equal(h[:, 4, :5], x[:, 2, :5].cpu())
@@ -505,6 +506,71 @@ def test_a_beam_step(way):
     b.same()
     assert m.cpu()[: int(n)].tolist() == moves
     assert (x.cpu().numpy() == want).all()
+
+
+def test_a_graph_of_larger_batches():
+    """Clusters and second kernels, launched as dependents, in a captured graph."""
+    db = lib()
+    b = Both(3000, 40, 70001, 4)
+    rng = np.random.default_rng(4)
+    b.extend(np.stack([np.arange(1500), rng.integers(1, 70, 1500)], 1))
+    child = 1500 + rng.permutation(1500)
+    parent = rng.integers(0, 1500, 1500)
+    fork = np.stack([parent, child, b.o.length[parent], child], 1)
+    grow = np.stack([child, rng.integers(1, 30, 1500)], 1)
+    cut = np.stack([child, np.zeros(1500)], 1)
+    req = u32(cut, 2), u32(fork, 4), u32(grow, 2)
+    m, n = torch.zeros((1500, 4), dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        db.page_free(b.t, req[0], b.ws)
+        db.page_fork(b.t, req[1], b.ws)
+        db.page_extend(b.t, req[2], m, n, b.ws)
+    b.o.free(cut)
+    b.o.fork(fork)
+    _, _, moves = b.o.extend(grow)
+    for _ in range(3):
+        g.replay()
+        b.same()
+        assert m.cpu()[: int(n)].tolist() == moves
+
+
+def test_tables_past_32_bits():
+    """Rows whose entries lie beyond 2^32 of the table's first."""
+    db = lib()
+    columns, n_seqs, n_pages = 1 << 20, 4100, 500       # 17 GB of table
+    t = db.PageTables.empty(n_seqs, columns, n_pages, 4)
+    ws = db.workspace(db.page_workspace_size(n_seqs, n_pages))
+    o = po.Cache(3, 100, n_pages, 4)                     # the rows that are used
+    rows = np.array([0, 4097, 4099])
+
+    def same():
+        torch.cuda.synchronize()
+        for k, s in enumerate(rows):
+            assert (t.table[s, :100].cpu().numpy() == o.table[k]).all()
+            assert int(t.length[s]) == o.length[k]
+        assert (t.refs.cpu().numpy() == o.refs).all()
+        assert (t.free.cpu().numpy().view(np.uint32) == po.pack_free(o.refs)).all()
+
+    m, n = torch.zeros((250, 4), dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    db.page_extend(t, u32([[4099, 311], [0, 9]], 2), m, n, ws)
+    o.extend([[2, 311], [0, 9]])
+    same()
+    db.page_fork(t, u32([[4099, 4097, 310, 0]], 4), ws)
+    o.fork([[2, 1, 310, 0]])
+    same()
+    db.page_extend(t, u32([[4097, 1], [4099, 40]], 2), m, n, ws)
+    _, _, moves = o.extend([[1, 1], [2, 40]])
+    same()
+    assert m.cpu()[: int(n)].tolist() == moves
+    db.page_free(t, u32([[4099, 30], [0, 0]], 2), ws)
+    o.free([[2, 30], [0, 0]])
+    same()
+    db.page_compact(t, t, m, n, ws)
+    o.compact(250)
+    same()
+    assert int((t.table[1:4097, :8] != -1).sum()) == 0
 
 
 def test_compaction_beside_readers_of_the_old_tables():
