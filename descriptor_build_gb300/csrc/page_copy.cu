@@ -4,9 +4,12 @@
 // its first tokens, a run in each of `segments`. Two kernels share the rest:
 //
 //  - page_copy_wide_kernel, for pages (or segments, where there are several)
-//    of kWideBytes and more: a warp takes a chunk of 4 KiB of one run, finds
+//    of kWideBytes and more: a warp takes chunks of 4 KiB of one run, finds
 //    record, plane and segment once, and moves 8 vectors of 16 bytes a lane,
-//    all loads in flight before the first store;
+//    all loads in flight before the first store. Few runs get a warp for each
+//    chunk; where that would be more than 64 warps an SM, half as many, so that
+//    partial pages leave fewer warps without work (1,023 times 15 of 32 KiB in
+//    4 planes: 16.5, and 13.5 so; with a quarter 12, but whole pages 0.5 % more);
 //  - page_copy_fine_kernel, for smaller ones and for addresses that are not
 //    multiples of 16: a CTA works on one plane and segment at a time, in which
 //    as many lanes as a run has vectors (up to a warp) take a record, so that
@@ -21,8 +24,7 @@ namespace db {
 namespace {
 
 constexpr uint32_t kThreads = 128;
-constexpr uint32_t kBatch = 8;                   // vectors a lane has in flight
-constexpr uint32_t kWarpSlots = 32 * kBatch;     // slots a warp takes at a time
+constexpr uint32_t kBatch = 8;  // vectors a lane has in flight
 
 struct CopyParams {
   const db_page_move* moves;
@@ -31,9 +33,8 @@ struct CopyParams {
   db_page_pool src, dst;
   uint32_t planes, segments, page_tokens, token_bytes;
   uint64_t seg_bytes, page_bytes;
-  uint32_t seg_chunks;  // wide: chunks of a segment,
-  uint64_t slots;       // and of a record in one plane
-  uint32_t lanes;       // fine: lanes of a run
+  uint32_t step;   // wide: warps of a run
+  uint32_t lanes;  // fine: lanes of a run
   db_counters* ctr;
 };
 
@@ -155,7 +156,7 @@ __global__ void __launch_bounds__(kThreads) page_copy_fine_kernel(const CopyPara
 }
 
 // ---------------------------------------------------------------------- wide
-constexpr uint32_t kChunk = kWarpSlots * 16;  // bytes a warp moves at a time
+constexpr uint32_t kChunk = 32 * kBatch * 16;  // bytes a warp moves at a time
 // Runs from here on go to the wide kernel. The other one takes 235 for partial
 // segments of 5.6 KB and 346 for 4 KB ones, this one 246 and 351; for whole 32
 // KiB pages it is 547 against 538 above, and for six pages 5.3 against 2.6.
@@ -178,47 +179,35 @@ __global__ void __launch_bounds__(kThreads) page_copy_wide_kernel(const CopyPara
   wait_for_prerequisites();
   dependents_may_launch();
   const uint32_t n = min(__ldcg(p.n_moves), p.max_moves);
-  const uint32_t lane = threadIdx.x & 31;
-  const uint32_t chunks = (uint32_t)p.slots;  // of a record in one plane
-  const uint64_t all = (uint64_t)n * p.planes * chunks;
+  const uint32_t lane = threadIdx.x & 31, runs = p.planes * p.segments;
+  const uint64_t all = (uint64_t)n * runs * p.step;
   const uint64_t stride = (uint64_t)gridDim.x * (kThreads / 32);
+  const uint64_t pol = policy_evict_first();
   for (uint64_t x = (uint64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; x < all; x += stride) {
-    const uint64_t rp = div64(x, chunks), r = div64(rp, p.planes);
-    const uint32_t plane = (uint32_t)(rp - r * p.planes);
-    uint32_t k = (uint32_t)(x - rp * chunks);
+    const uint64_t run = div64(x, p.step), r = div64(run, runs);
+    const uint32_t of = (uint32_t)(run - r * runs), plane = of / p.segments, seg = of - plane * p.segments;
     const uint4 m = *(reinterpret_cast<const uint4*>(p.moves) + r);
     if (m.x >= p.src.n_pages || m.y >= p.dst.n_pages) continue;
-    uint64_t len = p.page_bytes, at = 0;
-    if (m.z < p.page_tokens) {
-      len = (uint64_t)m.z * p.token_bytes;
-      if (p.segments > 1) {
-        const uint32_t s = k / p.seg_chunks;
-        k -= s * p.seg_chunks;
-        at = s * p.seg_bytes;
+    const uint32_t len = min(m.z, p.page_tokens) * p.token_bytes;
+    const char* const from = (const char*)p.src.base + plane * p.src.plane_stride + m.x * p.src.page_stride + seg * p.seg_bytes;
+    char* const to = (char*)p.dst.base + plane * p.dst.plane_stride + m.y * p.dst.page_stride + seg * p.seg_bytes;
+    for (uint32_t off = (uint32_t)(x - run * p.step) * kChunk; off < len; off += p.step * kChunk) {
+      ulonglong2 v[kBatch];
+      if (len - off >= kChunk) {
+#pragma unroll
+        for (uint32_t j = 0; j < kBatch; ++j) v[j] = ld_page16(from + off + 16 * (32 * j + lane), pol);
+#pragma unroll
+        for (uint32_t j = 0; j < kBatch; ++j) st_stream16(to + off + 16 * (32 * j + lane), v[j].x, v[j].y, pol);
+      } else {
+        const uint32_t left = len - off, whole = left / 16;
+#pragma unroll
+        for (uint32_t j = 0; j < kBatch; ++j)
+          if (32 * j + lane < whole) v[j] = ld_page16(from + off + 16 * (32 * j + lane), pol);
+#pragma unroll
+        for (uint32_t j = 0; j < kBatch; ++j)
+          if (32 * j + lane < whole) st_stream16(to + off + 16 * (32 * j + lane), v[j].x, v[j].y, pol);
+        if (lane < left % 16) to[off + 16 * whole + lane] = from[off + 16 * whole + lane];
       }
-    }
-    const uint64_t off = (uint64_t)k * kChunk;
-    if (off >= len) continue;
-    at += off;
-    const uint32_t left = (uint32_t)min(len - off, (uint64_t)kChunk);
-    const char* from = (const char*)p.src.base + plane * p.src.plane_stride + m.x * p.src.page_stride + at;
-    char* to = (char*)p.dst.base + plane * p.dst.plane_stride + m.y * p.dst.page_stride + at;
-    const uint64_t pol = policy_evict_first();
-    ulonglong2 v[kBatch];
-    if (left == kChunk) {
-#pragma unroll
-      for (uint32_t j = 0; j < kBatch; ++j) v[j] = ld_page16(from + 16 * (32 * j + lane), pol);
-#pragma unroll
-      for (uint32_t j = 0; j < kBatch; ++j) st_stream16(to + 16 * (32 * j + lane), v[j].x, v[j].y, pol);
-    } else {
-      const uint32_t whole = left / 16;
-#pragma unroll
-      for (uint32_t j = 0; j < kBatch; ++j)
-        if (32 * j + lane < whole) v[j] = ld_page16(from + 16 * (32 * j + lane), pol);
-#pragma unroll
-      for (uint32_t j = 0; j < kBatch; ++j)
-        if (32 * j + lane < whole) st_stream16(to + 16 * (32 * j + lane), v[j].x, v[j].y, pol);
-      if (lane < left % 16) to[16 * whole + lane] = from[16 * whole + lane];
     }
   }
   count_records(p, n);
@@ -311,9 +300,10 @@ extern "C" int db_page_copy(const db_page_move* moves, uint32_t max_moves, const
   if (dst->n_pages > 1) all |= dst->page_stride;
   if (p.segments > 1) all |= p.seg_bytes;
   if (!(all & 15) && p.seg_bytes >= kWideBytes) {
-    p.seg_chunks = (uint32_t)((p.seg_bytes + kChunk - 1) / kChunk);
-    p.slots = (uint64_t)p.seg_chunks * p.segments;
-    const uint64_t warps = p.max_moves * (p.planes * p.slots);
+    const uint64_t runs = (uint64_t)max_moves * p.planes * p.segments;
+    p.step = (uint32_t)((p.seg_bytes + kChunk - 1) / kChunk);
+    if (runs * p.step > 64ull * num_sms()) p.step = (p.step + 1) / 2;
+    const uint64_t warps = runs * p.step;
     const uint64_t want = (warps + kThreads / 32 - 1) / (kThreads / 32), most = (uint64_t)kWideCtas * num_sms();
     return launch_dependent(page_copy_wide_kernel, (unsigned)(want < most ? want : most), kThreads, 0, s, p);
   }
