@@ -607,7 +607,7 @@ struct FreeParams {
 };
 
 // refs[p] -= the rows of the batch that drop p; p is free when nothing is left.
-// A step of 48 sequences frees its 12 pages in 4.4 (one launch, warm), 192
+// A step of 48 sequences frees its 12 pages in 3.7 (one launch, warm), 192
 // prompt chunks of 512 pages in 9.0, 64 sequences of 5,000 pages in 11.5.
 template <typename X>
 __device__ __forceinline__ void free_units(const Rows& p, const X& x, uint32_t first,
@@ -678,6 +678,47 @@ __device__ __forceinline__ void free_units(const Rows& p, const X& x, uint32_t f
   *error = bad;
 }
 
+// The same for a row with at most kFewEntries of them, by one thread: where no
+// request of a CTA has more (a decode step), units would be almost empty. 4,096
+// sequences with 267 pages among them: 10.0 in units, 6.9 so.
+constexpr uint32_t kFewEntries = 4;
+
+__device__ __forceinline__ void free_few(const Rows& p, const Plan& pl, uint32_t* count,
+                                         bool* error) {
+  uint32_t released = 0;
+  bool bad = false;
+  int32_t* const row = &p.t.table[(uint64_t)pl.row * p.t.columns];
+  uint32_t page[kFewEntries], refs[kFewEntries];
+#pragma unroll
+  for (uint32_t k = 0; k < kFewEntries; ++k) {
+    page[k] = pl.from + k < pl.end ? (uint32_t)row[pl.from + k] : kBadEntry;
+    if (pl.from + k < pl.end && page[k] >= p.t.n_pages) bad = true;
+  }
+#pragma unroll
+  for (uint32_t k = 0; k < kFewEntries; ++k) {
+    if (pl.from + k < pl.end) row[pl.from + k] = DB_PAGE_NONE;
+    refs[k] = page[k] < p.t.n_pages ? __ldcg(&p.t.refs[page[k]]) : 0;
+  }
+#pragma unroll
+  for (uint32_t k = 0; k < kFewEntries; ++k) {
+    if (page[k] >= p.t.n_pages) continue;
+    if (refs[k] > 1)
+      refs[k] = atomicSub(&p.t.refs[page[k]], 1u);
+    else if (refs[k] == 1)
+      p.t.refs[page[k]] = 0;
+    else
+      bad = true;
+  }
+#pragma unroll
+  for (uint32_t k = 0; k < kFewEntries; ++k) {
+    if (page[k] >= p.t.n_pages || refs[k] != 1) continue;
+    atomicOr(&p.t.free[page[k] >> 5], 1u << (page[k] & 31));
+    ++released;
+  }
+  *count = released;
+  *error = bad;
+}
+
 // The same, into the counters.
 template <typename X>
 __device__ __forceinline__ void free_and_count(const Rows& p, const X& x, uint32_t first,
@@ -725,8 +766,11 @@ __global__ void __launch_bounds__(kThreads) page_free_gang_kernel(const FreePara
   plan_rows(cta, p, &s_plan, i, mine, pl, &units, &entries);
   const uint32_t invalid = __syncthreads_count(mine && !ok);
   constexpr uint32_t kWarps = kThreads / 32;
-  free_units(p, OwnUnits<kThreads>{&s_plan}, i / 32 * gridDim.x + blockIdx.x, gridDim.x * kWarps, units,
-             &released, &bad);
+  if (gridDim.x == 1 && !__syncthreads_or(pl.end > pl.from + kFewEntries))
+    free_few(p, pl, &released, &bad);
+  else
+    free_units(p, OwnUnits<kThreads>{&s_plan}, i / 32 * gridDim.x + blockIdx.x, gridDim.x * kWarps,
+               units, &released, &bad);
   uint64_t total;
   if (!last_of_gang(p.w.head, released, bad, &total, &bad)) return;
   if (cut) p.t.length[r.x] = r.y;
@@ -758,10 +802,11 @@ __global__ void __launch_bounds__(kTeamThreads) page_free_team_kernel(const Free
   team.started();
   team.sync();
   uint32_t units = 0, entries = 0, invalid = 0;
+  Plan pl = {0, 0, 0, 0};
   for (uint32_t i0 = 0; i0 < p.n; i0 += step) {
     const uint32_t i = i0 + at;
     const bool mine = threadIdx.x < per && i < p.n;
-    Plan pl = {0, 0, 0, 0};
+    pl = Plan{0, 0, 0, 0};
     if (mine) {
       if (!one) {
         r = q.req[i];
@@ -784,7 +829,17 @@ __global__ void __launch_bounds__(kTeamThreads) page_free_team_kernel(const Free
   if (p.ctr) add_count(&p.ctr->n_invalid, invalid);
   own_units(team, p, &s_plan, units, entries,
             [&](const OwnUnits<kTeamThreads>& x, uint32_t first, uint32_t stride, uint32_t end) {
-              free_and_count(p, x, first, stride, end);
+              if (one && !__syncthreads_or(pl.end > pl.from + kFewEntries)) {
+                uint32_t released;
+                bool bad;
+                free_few(p, pl, &released, &bad);
+                if (p.ctr) {
+                  add_count(&p.ctr->total, released);
+                  add_error(p.ctr, bad);
+                }
+              } else {
+                free_and_count(p, x, first, stride, end);
+              }
             });
 }
 
@@ -1278,19 +1333,13 @@ __global__ void __launch_bounds__(kTeamThreads) page_extend_team_kernel(const Ex
   if (go && need && bits.before < need)
     each_quad(bits, p.t.free, p.t.n_pages, [&](uint32_t w, const uint4& v, const uint4& before) {
       if (before.x >= need) return false;
-      if (few && w < kWords) {
-        team.to_all(&s_before[w], before);
-        team.to_all(&s_bits[w], v);
-      }
-      if (p.rest) {
-        st_quad(p.w.before, w, words, before);
-        st_quad(p.w.bits, w, words, v);
-      }
+      st_quad(p.w.before, w, words, before);
+      st_quad(p.w.bits, w, words, v);
       uint32_t used = 0;
       const uint4 left = left_of(v, before, need, &used, w);
       if (used) {
         team.to_all(s_used, make_uint4(used, 0, 0, 0));
-        if (p.rest) p.w.head->used = used;
+        p.w.head->used = used;
       }
       st_quad(p.t.free, w, words, left);
       return true;
@@ -1332,6 +1381,11 @@ __global__ void __launch_bounds__(kTeamThreads) page_extend_team_kernel(const Ex
   const bool own = few && used <= kWords;
   if (p.rest && id == 0) p.w.head->units = go && !own ? need : 0;
   if (!used || !own) return;
+  for (uint32_t w = threadIdx.x; w < used; w += kThreads) {
+    s_before[w] = p.w.before[w];
+    s_bits[w] = p.w.bits[w];
+  }
+  __syncthreads();
   place_pages(p, Finder{s_start, kThreads, kThreads, 1}, s_plan, Finder{s_before, used, used, 1},
               s_before, s_bits, s_start[0] + threadIdx.x, kThreads, s_end);
 }
