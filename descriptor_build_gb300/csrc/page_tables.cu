@@ -208,21 +208,15 @@ struct Team {
     if (rank_w) *rank_w = base_b + __popc(__ballot_sync(kFull, w != 0) & lanemask_lt());
     return base_a + x - v;
   }
-  __device__ __forceinline__ static uint32_t peer_address(void* mine, uint32_t peer) {
+  // A word to the same place in a CTA of the cluster.
+  __device__ __forceinline__ static void to_peer(uint32_t* mine, uint32_t peer, uint32_t v) {
     uint32_t at;
     asm("mapa.shared::cluster.u32 %0, %1, %2;"
         : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(mine)), "r"(peer));
-    return at;
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
   }
-  __device__ __forceinline__ static void to_peer(uint32_t* mine, uint32_t peer, uint32_t v) {
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_address(mine, peer)), "r"(v) : "memory");
-  }
-  // A quad to the same place in every CTA.
-  __device__ __forceinline__ void to_all(uint32_t* mine, const uint4& v) const {
-    for (uint32_t c = 0; c < size; ++c)
-      asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(peer_address(mine, c)),
-                   "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                   : "memory");
+  __device__ __forceinline__ void to_all(uint32_t* mine, uint32_t v) const {
+    for (uint32_t c = 0; c < size; ++c) to_peer(mine, c, v);
   }
 };
 
@@ -1253,8 +1247,7 @@ __global__ void __launch_bounds__(kTeamThreads) page_extend_team_kernel(const Ex
   __shared__ uint32_t s_start[kThreads];
   __shared__ Plan s_plan[kThreads];
   __shared__ __align__(16) uint32_t s_before[kWords], s_bits[kWords];
-  __shared__ __align__(16) uint32_t s_used[4];
-  __shared__ uint32_t s_end;
+  __shared__ uint32_t s_used, s_end;
   Team<kThreads, false> team(&s_team);
   wait_for_prerequisites();
   dependents_may_launch();
@@ -1338,7 +1331,7 @@ __global__ void __launch_bounds__(kTeamThreads) page_extend_team_kernel(const Ex
       uint32_t used = 0;
       const uint4 left = left_of(v, before, need, &used, w);
       if (used) {
-        team.to_all(s_used, make_uint4(used, 0, 0, 0));
+        team.to_all(&s_used, used);
         p.w.head->used = used;
       }
       st_quad(p.t.free, w, words, left);
@@ -1377,7 +1370,7 @@ __global__ void __launch_bounds__(kTeamThreads) page_extend_team_kernel(const Ex
     add_error(p.ctr, corrupt);
   }
   team.sync();  // words are known, and the replaced entries have been read
-  const uint32_t used = go && need ? s_used[0] : 0;
+  const uint32_t used = go && need ? s_used : 0;
   const bool own = few && used <= kWords;
   if (p.rest && id == 0) p.w.head->units = go && !own ? need : 0;
   if (!used || !own) return;
