@@ -1215,12 +1215,13 @@ __global__ void __launch_bounds__(kThreads) page_extend_gang_kernel(const Extend
       p.t.refs[page] = 1;
     }
   if (!last_of_gang(p.w.head)) return;
+  const uint32_t copiers = __ballot_sync(kFull, cow && go);
   if (cow && go) {
     const uint32_t page = nth_page<kThreads>(p.t.free, p.t.n_pages, s_first, bits.quads, start);
     p.t.table[(uint64_t)a.seq * p.t.columns + a.had - 1] = (int32_t)page;
     p.t.refs[page] = 1;
     *reinterpret_cast<uint4*>(&p.moves[rank]) = make_uint4(a.last, page, a.part, 0);
-    const uint32_t same = __match_any_sync(__activemask(), a.last);
+    const uint32_t same = __match_any_sync(copiers, a.last);
     if ((same & lanemask_lt()) == 0) atomicSub(&p.t.refs[a.last], (uint32_t)__popc(same));
   }
   if (a.ok && go) p.t.length[a.seq] = a.now;
@@ -1271,14 +1272,18 @@ __global__ void __launch_bounds__(kTeamThreads) page_extend_team_kernel(const Ex
   if (shares) {
     // How many of the batch's requests hold each shared page, and the last of
     // them; requests of a warp that hold the same one (samples of one prompt)
-    // count together.
-    for (uint32_t i = at; threadIdx.x < per && i < p.n; i += step) {
+    // count together. (Whole warps take part in every round, so that a vote
+    // can name the lanes of each match.)
+    for (uint32_t i0 = 0; i0 < p.n; i0 += step) {
+      const uint32_t i = i0 + at;
       if (!one) {
-        a = ask(p, i, true);
-        settle(&a, a.named && claimed(p.w.claim, a.seq, i));
+        const bool mine = threadIdx.x < per && i < p.n;
+        a = ask(p, i, mine);
+        if (mine) settle(&a, a.named && claimed(p.w.claim, a.seq, i));
       }
+      const uint32_t sharers = __ballot_sync(kFull, a.shares());
       if (a.shares()) {
-        const uint32_t same = __match_any_sync(__activemask(), a.last);
+        const uint32_t same = __match_any_sync(sharers, a.last);
         if ((same & lanemask_lt()) == 0) {
           atomicAdd(&p.w.holders[a.last], (uint32_t)__popc(same));
           atomicMax(&p.w.latest[a.last], i + (31 - __clz(same)) - (threadIdx.x & 31));
@@ -1341,17 +1346,23 @@ __global__ void __launch_bounds__(kTeamThreads) page_extend_team_kernel(const Ex
   // status, and the workspace as the next call wants it.
   uint32_t invalid = 0, refused = 0;
   bool corrupt = false;
-  for (uint32_t i = at; threadIdx.x < per && i < p.n; i += step) {
+  for (uint32_t i0 = 0; i0 < p.n; i0 += step) {
+    const uint32_t i = i0 + at;
+    const bool mine = threadIdx.x < per && i < p.n;
     if (!one) {
-      a = ask(p, i, true);
-      settle(&a, a.named && claimed(p.w.claim, a.seq, i));
-      move = p.w.plan[i].aux;
+      a = ask(p, i, mine);
+      move = kNoMove;
+      if (mine) {
+        settle(&a, a.named && claimed(p.w.claim, a.seq, i));
+        move = p.w.plan[i].aux;
+      }
     }
+    const uint32_t copiers = __ballot_sync(kFull, move != kNoMove);
     if (move != kNoMove) {  // at least one holder of every shared page copies, and clears for all
       p.w.holders[a.last] = 0;
       p.w.latest[a.last] = 0;
       if (go) {
-        const uint32_t same = __match_any_sync(__activemask(), a.last);
+        const uint32_t same = __match_any_sync(copiers, a.last);
         if ((same & lanemask_lt()) == 0) atomicSub(&p.t.refs[a.last], (uint32_t)__popc(same));
         p.moves[move].src = a.last;
         *reinterpret_cast<uint2*>(&p.moves[move].tokens) = make_uint2(a.part, 0);
@@ -1359,10 +1370,10 @@ __global__ void __launch_bounds__(kTeamThreads) page_extend_team_kernel(const Ex
     }
     if (a.mine) p.w.claim[a.seq] = 0;
     if (a.ok && go) p.t.length[a.seq] = a.now;
-    invalid += !a.ok;
+    invalid += mine && !a.ok;
     refused += a.ok && !go;
     corrupt |= a.corrupt;
-    if (p.status) p.status[i] = !a.ok ? DB_PAGE_INVALID : go ? DB_PAGE_OK : DB_PAGE_SHORT;
+    if (mine && p.status) p.status[i] = !a.ok ? DB_PAGE_INVALID : go ? DB_PAGE_OK : DB_PAGE_SHORT;
   }
   if (p.ctr) {
     add_count(&p.ctr->n_invalid, invalid);
