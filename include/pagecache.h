@@ -34,10 +34,13 @@
  * In a batch, the first request that names a sequence (a fork: a child) is
  * the one that counts; later ones naming it are DB_PAGE_INVALID.
  *
- * A row that names a page outside [0, n_pages), or a page it frees that no
- * row holds, is not a state these calls leave. Such an entry is skipped
- * (nothing outside the arrays is read or written) and DB_ERR_PAGE_TABLE is
- * set in ctr->err; the cache's contents are then undefined.
+ * A row that names a page outside [0, n_pages), or a page with fewer
+ * references than rows, is not a state these calls leave. The entry of a page
+ * outside is skipped, and DB_ERR_PAGE_TABLE is set in ctr->err; a row that
+ * frees a page without references, when it looks, is reported so too, while
+ * rows of one batch that look together and then drop more references than
+ * there are go unreported. Nothing outside the arrays is read or written in
+ * either case; the cache's contents are then undefined.
  */
 #ifndef PAGECACHE_H
 #define PAGECACHE_H
