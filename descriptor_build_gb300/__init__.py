@@ -464,6 +464,38 @@ class _Shape(ctypes.Structure):  # db_page_shape
                 ("page_tokens", ctypes.c_uint32), ("token_bytes", ctypes.c_uint32)]
 
 
+def _refuse(t: torch.Tensor) -> None:
+    if not (t.is_cuda or t.is_pinned()):  # the GPU would fault in it
+        raise ValueError("a paged cache's tensors must be on the GPU or in pinned host memory")
+    raise ValueError("tensors passed to libdescbuild must be contiguous")
+
+
+def _at(t: torch.Tensor, nbytes: int) -> int:
+    """The address of a tensor of which the GPU reads or writes ``nbytes``."""
+    if not (t.is_contiguous() and (t.is_cuda or t.is_pinned())):
+        _refuse(t)
+    if t.nbytes < nbytes:
+        raise ValueError(f"tensor of {t.nbytes} bytes where {nbytes} are read or written")
+    return t.data_ptr()
+
+
+def _whole(t: torch.Tensor) -> tuple[int, int]:
+    """A tensor's address and size."""
+    if not (t.is_contiguous() and (t.is_cuda or t.is_pinned())):
+        _refuse(t)
+    return t.data_ptr(), t.nbytes
+
+
+def _batch(t: torch.Tensor, size: int) -> tuple[int, int]:
+    """The address and the number of a batch's records of ``size`` bytes."""
+    if not (t.is_contiguous() and (t.is_cuda or t.is_pinned())):
+        _refuse(t)
+    n, rest = divmod(t.nbytes, size)
+    if rest or n > 0xFFFFFFFF:
+        raise ValueError(f"a batch is a whole number of {size}-byte records, fewer than 2^32")
+    return t.data_ptr(), n
+
+
 class PageTables:
     """The state of a paged cache: int32 CUDA tensors table [n_seqs, columns],
     length [n_seqs], refs [n_pages] and free [ceil(n_pages / 32)], which the
@@ -483,8 +515,8 @@ class PageTables:
                 raise ValueError(f"{name} must be a contiguous int32 tensor of {n} elements")
         self.table, self.length, self.refs, self.free = table, length, refs, free
         self.page_tokens = int(page_tokens)
-        self._c = _Tables(table.data_ptr(), length.data_ptr(), refs.data_ptr(), free.data_ptr(),
-                          n_seqs, columns, n_pages, self.page_tokens)
+        self._c = _Tables(*(_at(t, 0) for t in (table, length, refs, free)), n_seqs, columns,
+                          n_pages, self.page_tokens)
         self._ref = ctypes.byref(self._c)
 
     @classmethod
@@ -504,32 +536,16 @@ def page_workspace_size(n_seqs: int, n_pages: int) -> int:
     return _size(_lib.db_page_workspace_size, n_seqs, n_pages)
 
 
-def _requests(t: torch.Tensor, size: int) -> int:
-    n, rest = divmod(t.nbytes, size)
-    if rest or n > 0xFFFFFFFF:
-        raise ValueError(f"a batch is a whole number of {size}-byte records, fewer than 2^32")
-    return n
-
-
-def _status(status: torch.Tensor | None, n: int) -> int | None:
-    if status is None:
-        return None
-    if status.nbytes < n:
-        raise ValueError(f"status holds fewer than {n} bytes")
-    return _ptr(status)
-
-
 def page_extend(tables: PageTables, req: torch.Tensor, moves: torch.Tensor,
                 n_moves: torch.Tensor, ws: torch.Tensor, status: torch.Tensor | None = None,
                 ctr: torch.Tensor | None = None, stream=None) -> None:
     """db_page_extend: sequences grow by tokens (req [n, 2] {seq, tokens});
     moves [>= n, 4] and n_moves [1] get the copies page_copy has to make."""
-    n = _requests(req, 8)
-    if _requests(moves, 16) < n:
-        raise ValueError(f"moves holds fewer than {n} records")
+    at, n = _batch(req, 8)
     _check("db_page_extend", _lib.db_page_extend(
-        tables._ref, _ptr(req), n, _ptr(moves), _ptr(n_moves), _status(status, n), _ptr(ctr),
-        _ptr(ws), ws.nbytes, _stream(stream)))
+        tables._ref, at, n, _at(moves, 16 * n), _at(n_moves, 0),
+        None if status is None else _at(status, n), None if ctr is None else _at(ctr, 0),
+        *_whole(ws), _stream(stream)))
 
 
 def page_fork(tables: PageTables, req: torch.Tensor, ws: torch.Tensor,
@@ -537,10 +553,10 @@ def page_fork(tables: PageTables, req: torch.Tensor, ws: torch.Tensor,
               stream=None) -> None:
     """db_page_fork: children share their parents' first tokens (req [n, 4]
     {parent, child, tokens, ignored})."""
-    n = _requests(req, 16)
+    at, n = _batch(req, 16)
     _check("db_page_fork", _lib.db_page_fork(
-        tables._ref, _ptr(req), n, _status(status, n), _ptr(ctr), _ptr(ws),
-        ws.nbytes, _stream(stream)))
+        tables._ref, at, n, None if status is None else _at(status, n),
+        None if ctr is None else _at(ctr, 0), *_whole(ws), _stream(stream)))
 
 
 def page_free(tables: PageTables, req: torch.Tensor, ws: torch.Tensor,
@@ -548,10 +564,10 @@ def page_free(tables: PageTables, req: torch.Tensor, ws: torch.Tensor,
               stream=None) -> None:
     """db_page_free: sequences cut back to their first tokens (req [n, 2]
     {seq, keep}) give their other pages back."""
-    n = _requests(req, 8)
+    at, n = _batch(req, 8)
     _check("db_page_free", _lib.db_page_free(
-        tables._ref, _ptr(req), n, _status(status, n), _ptr(ctr), _ptr(ws),
-        ws.nbytes, _stream(stream)))
+        tables._ref, at, n, None if status is None else _at(status, n),
+        None if ctr is None else _at(ctr, 0), *_whole(ws), _stream(stream)))
 
 
 def page_compact(tables: PageTables, out: PageTables, moves: torch.Tensor, n_moves: torch.Tensor,
@@ -561,8 +577,8 @@ def page_compact(tables: PageTables, out: PageTables, moves: torch.Tensor, n_mov
     same sizes); moves [cap, 4] and n_moves [1] get what page_copy has to
     move."""
     _check("db_page_compact", _lib.db_page_compact(
-        tables._ref, out._ref, _ptr(moves), _requests(moves, 16), _ptr(n_moves), _ptr(ctr),
-        _ptr(ws), ws.nbytes, _stream(stream)))
+        tables._ref, out._ref, *_batch(moves, 16), _at(n_moves, 0),
+        None if ctr is None else _at(ctr, 0), *_whole(ws), _stream(stream)))
 
 
 def _strides(shape, stride, item: int) -> tuple[int, int]:
@@ -610,10 +626,14 @@ def page_copy(moves: torch.Tensor, n_moves: torch.Tensor, src: torch.Tensor, dst
     ``token_dim`` is the axis of a page's tokens, None when it has none (then
     every move takes whole pages)."""
     shape = src.shape
+    if not (src.is_cuda or src.is_pinned()):
+        _refuse(src)
     if dst is src:
         _, form, a, _ = _copy_plan(shape, src.stride(), src.element_size(), token_dim)
         here = there = ctypes.byref(_Pool(src.data_ptr(), shape[1], *a))
     else:
+        if not (dst.is_cuda or dst.is_pinned()):
+            _refuse(dst)
         if src.dtype != dst.dtype:
             raise ValueError("source and destination pools differ in type")
         _, form, a, b = _copy_plan(shape, src.stride(), src.element_size(), token_dim, dst.shape,
@@ -621,5 +641,5 @@ def page_copy(moves: torch.Tensor, n_moves: torch.Tensor, src: torch.Tensor, dst
         here = ctypes.byref(_Pool(src.data_ptr(), shape[1], *a))
         there = ctypes.byref(_Pool(dst.data_ptr(), dst.shape[1], *b))
     _check("db_page_copy", _lib.db_page_copy(
-        _ptr(moves), _requests(moves, 16), _ptr(n_moves), here, there, form, _ptr(ctr),
-        _stream(stream)))
+        *_batch(moves, 16), _at(n_moves, 0), here, there, form,
+        None if ctr is None else _at(ctr, 0), _stream(stream)))

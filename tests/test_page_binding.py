@@ -1,0 +1,116 @@
+"""The paged cache's Python calls refuse what the GPU could not read or write, before the library is
+called. The library is a stand-in that records its calls, and tensors that stand for the GPU's are
+host tensors that say they are."""
+
+import types
+
+import pytest
+
+from test_abi import libpath  # noqa: F401  (the built library)
+
+torch = pytest.importorskip("torch")
+
+
+class OnGpu(torch.Tensor):
+    is_cuda = True
+
+
+def gpu(t):
+    return t.as_subclass(OnGpu)
+
+
+def i32(*shape):
+    return torch.zeros(shape, dtype=torch.int32)
+
+
+@pytest.fixture()
+def db(libpath, monkeypatch):  # noqa: F811
+    import descriptor_build_gb300 as db
+
+    calls = []
+    lib = types.SimpleNamespace(**{
+        f"db_page_{op}": (lambda *a, op=op: calls.append((op, a)) or 0)
+        for op in ("extend", "fork", "free", "compact", "copy")})
+    monkeypatch.setattr(db, "_lib", lib)
+    monkeypatch.setattr(db, "calls", calls, raising=False)
+    return db
+
+
+def arguments(db):
+    """Each call's tensors, all of them where they should be."""
+    g = lambda t: gpu(t)
+    cache = lambda: db.PageTables(g(i32(6, 5)), g(i32(6)), g(i32(40)), g(i32(2)), 16)
+    ws, ctr = (lambda: g(torch.zeros(4096, dtype=torch.uint8))), (lambda: g(torch.zeros(4, dtype=torch.int64)))
+    status = lambda n: g(torch.zeros(n, dtype=torch.uint8))
+    pool = lambda: g(torch.zeros(2, 40, 16, 8))
+    return {
+        "extend": dict(tables=cache(), req=g(i32(3, 2)), moves=g(i32(3, 4)), n_moves=g(i32(1)), ws=ws(),
+                       status=status(3), ctr=ctr()),
+        "fork": dict(tables=cache(), req=g(i32(3, 4)), ws=ws(), status=status(3), ctr=ctr()),
+        "free": dict(tables=cache(), req=g(i32(3, 2)), ws=ws(), status=status(3), ctr=ctr()),
+        "compact": dict(tables=cache(), out=cache(), moves=g(i32(7, 4)), n_moves=g(i32(1)), ws=ws(), ctr=ctr()),
+        "copy": dict(moves=g(i32(7, 4)), n_moves=g(i32(1)), src=pool(), dst=pool(), token_dim=2, ctr=ctr()),
+    }
+
+
+OPS = ("extend", "fork", "free", "compact", "copy")
+TENSORS = [(op, k) for op, ks in (
+    ("extend", ("req", "moves", "n_moves", "ws", "status", "ctr")), ("fork", ("req", "ws", "status", "ctr")),
+    ("free", ("req", "ws", "status", "ctr")), ("compact", ("moves", "n_moves", "ws", "ctr")),
+    ("copy", ("moves", "n_moves", "src", "dst", "ctr"))) for k in ks]
+
+
+def call(db, op, args):
+    return getattr(db, f"page_{op}")(stream=0, **args)
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_calls_reach_the_library(db, op):
+    args = arguments(db)[op]
+    call(db, op, args)
+    (name, got), = db.calls
+    assert name == op
+    for k, t in args.items():
+        if isinstance(t, torch.Tensor) and k not in ("src", "dst"):
+            assert t.data_ptr() in got
+    if op in ("extend", "fork", "free"):
+        assert got[2] == 3
+    else:
+        assert 7 in got
+
+
+@pytest.mark.parametrize("op,name", TENSORS, ids=["-".join(x) for x in TENSORS])
+def test_ordinary_host_memory_is_refused(db, op, name):
+    args = arguments(db)[op]
+    args[name] = args[name].as_subclass(torch.Tensor)
+    with pytest.raises(ValueError, match="pinned"):
+        call(db, op, args)
+    assert db.calls == []
+
+
+def test_one_pool_in_ordinary_host_memory_is_refused(db):
+    args = arguments(db)["copy"]
+    args["src"] = args["dst"] = torch.zeros(2, 40, 16, 8)
+    with pytest.raises(ValueError, match="pinned"):
+        call(db, "copy", args)
+    assert db.calls == []
+
+
+@pytest.mark.parametrize("k", range(4), ids=["table", "length", "refs", "free"])
+def test_tables_in_ordinary_host_memory_are_refused(db, k):
+    arrays = [gpu(i32(6, 5)), gpu(i32(6)), gpu(i32(40)), gpu(i32(2))]
+    db.PageTables(*arrays, 16)
+    arrays[k] = arrays[k].as_subclass(torch.Tensor)
+    with pytest.raises(ValueError, match="pinned"):
+        db.PageTables(*arrays, 16)
+
+
+@pytest.mark.parametrize("op,name", [x for x in TENSORS if x[1] not in ("src", "dst", "n_moves")],
+                         ids=["-".join(x) for x in TENSORS if x[1] not in ("src", "dst", "n_moves")])
+def test_strided_arrays_are_refused(db, op, name):
+    args = arguments(db)[op]
+    t = args[name].as_subclass(torch.Tensor)
+    args[name] = gpu(torch.cat([t, t])[::2])
+    with pytest.raises(ValueError, match="contiguous"):
+        call(db, op, args)
+    assert db.calls == []
