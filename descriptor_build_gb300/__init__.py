@@ -543,8 +543,8 @@ def page_extend(tables: PageTables, req: torch.Tensor, moves: torch.Tensor,
     moves [>= n, 4] and n_moves [1] get the copies page_copy has to make."""
     at, n = _batch(req, 8)
     _check("db_page_extend", _lib.db_page_extend(
-        tables._ref, at, n, _at(moves, 16 * n), _at(n_moves, 0),
-        None if status is None else _at(status, n), None if ctr is None else _at(ctr, 0),
+        tables._ref, at, n, _at(moves, 16 * n), _at(n_moves, 4),
+        None if status is None else _at(status, n), None if ctr is None else _at(ctr, 32),
         *_whole(ws), _stream(stream)))
 
 
@@ -556,7 +556,7 @@ def page_fork(tables: PageTables, req: torch.Tensor, ws: torch.Tensor,
     at, n = _batch(req, 16)
     _check("db_page_fork", _lib.db_page_fork(
         tables._ref, at, n, None if status is None else _at(status, n),
-        None if ctr is None else _at(ctr, 0), *_whole(ws), _stream(stream)))
+        None if ctr is None else _at(ctr, 32), *_whole(ws), _stream(stream)))
 
 
 def page_free(tables: PageTables, req: torch.Tensor, ws: torch.Tensor,
@@ -567,7 +567,7 @@ def page_free(tables: PageTables, req: torch.Tensor, ws: torch.Tensor,
     at, n = _batch(req, 8)
     _check("db_page_free", _lib.db_page_free(
         tables._ref, at, n, None if status is None else _at(status, n),
-        None if ctr is None else _at(ctr, 0), *_whole(ws), _stream(stream)))
+        None if ctr is None else _at(ctr, 32), *_whole(ws), _stream(stream)))
 
 
 def page_compact(tables: PageTables, out: PageTables, moves: torch.Tensor, n_moves: torch.Tensor,
@@ -577,8 +577,8 @@ def page_compact(tables: PageTables, out: PageTables, moves: torch.Tensor, n_mov
     same sizes); moves [cap, 4] and n_moves [1] get what page_copy has to
     move."""
     _check("db_page_compact", _lib.db_page_compact(
-        tables._ref, out._ref, *_batch(moves, 16), _at(n_moves, 0),
-        None if ctr is None else _at(ctr, 0), *_whole(ws), _stream(stream)))
+        tables._ref, out._ref, *_batch(moves, 16), _at(n_moves, 4),
+        None if ctr is None else _at(ctr, 32), *_whole(ws), _stream(stream)))
 
 
 def _strides(shape, stride, item: int) -> tuple[int, int]:
@@ -641,5 +641,5 @@ def page_copy(moves: torch.Tensor, n_moves: torch.Tensor, src: torch.Tensor, dst
         here = ctypes.byref(_Pool(src.data_ptr(), shape[1], *a))
         there = ctypes.byref(_Pool(dst.data_ptr(), dst.shape[1], *b))
     _check("db_page_copy", _lib.db_page_copy(
-        *_batch(moves, 16), _at(n_moves, 0), here, there, form,
-        None if ctr is None else _at(ctr, 0), _stream(stream)))
+        *_batch(moves, 16), _at(n_moves, 4), here, there, form,
+        None if ctr is None else _at(ctr, 32), _stream(stream)))

@@ -105,6 +105,18 @@ def test_tables_in_ordinary_host_memory_are_refused(db, k):
         db.PageTables(*arrays, 16)
 
 
+SHORT = [(op, k) for op, k in TENSORS if k in ("n_moves", "ctr", "status")] + [("extend", "moves")]
+
+
+@pytest.mark.parametrize("op,name", SHORT, ids=["-".join(x) for x in SHORT])
+def test_arrays_shorter_than_what_is_written_are_refused(db, op, name):
+    args = arguments(db)[op]
+    args[name] = args[name][:-1]
+    with pytest.raises(ValueError):
+        call(db, op, args)
+    assert db.calls == []
+
+
 @pytest.mark.parametrize("op,name", [x for x in TENSORS if x[1] not in ("src", "dst", "n_moves")],
                          ids=["-".join(x) for x in TENSORS if x[1] not in ("src", "dst", "n_moves")])
 def test_strided_arrays_are_refused(db, op, name):
