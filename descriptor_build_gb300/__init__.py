@@ -486,13 +486,24 @@ def _whole(t: torch.Tensor) -> tuple[int, int]:
     return t.data_ptr(), t.nbytes
 
 
-def _batch(t: torch.Tensor, size: int) -> tuple[int, int]:
-    """The address and the number of a batch's records of ``size`` bytes."""
+_I32, _U32 = torch.int32, torch.uint32
+
+
+def _batch(t: torch.Tensor, width: int) -> tuple[int, int]:
+    """The address and the number of a batch's records of ``width`` 32-bit
+    fields. (Another type's bytes would be read as other records.)"""
+    shape = t.shape
+    if len(shape) == 2 and shape[1] == width:
+        n = shape[0]
+    elif shape[-1:] == (width,) or (len(shape) == 1 and shape[0] % width == 0):
+        n = t.numel() // width
+    else:
+        n = -1
+    if not (0 <= n <= 0xFFFFFFFF and (t.dtype is _I32 or t.dtype is _U32)):
+        raise ValueError(f"a batch is an int32 tensor [n, {width}], n below 2^32, not "
+                         f"{t.dtype} {list(shape)}")
     if not (t.is_contiguous() and (t.is_cuda or t.is_pinned())):
         _refuse(t)
-    n, rest = divmod(t.nbytes, size)
-    if rest or n > 0xFFFFFFFF:
-        raise ValueError(f"a batch is a whole number of {size}-byte records, fewer than 2^32")
     return t.data_ptr(), n
 
 
@@ -541,11 +552,14 @@ def page_extend(tables: PageTables, req: torch.Tensor, moves: torch.Tensor,
                 ctr: torch.Tensor | None = None, stream=None) -> None:
     """db_page_extend: sequences grow by tokens (req [n, 2] {seq, tokens});
     moves [>= n, 4] and n_moves [1] get the copies page_copy has to make."""
-    at, n = _batch(req, 8)
+    at, n = _batch(req, 2)
+    to, room = _batch(moves, 4)
+    if room < n:
+        raise ValueError(f"moves holds fewer than {n} records")
+    space, nbytes = _whole(ws)
     _check("db_page_extend", _lib.db_page_extend(
-        tables._ref, at, n, _at(moves, 16 * n), _at(n_moves, 4),
-        None if status is None else _at(status, n), None if ctr is None else _at(ctr, 32),
-        *_whole(ws), _stream(stream)))
+        tables._ref, at, n, to, _at(n_moves, 4), None if status is None else _at(status, n),
+        None if ctr is None else _at(ctr, 32), space, nbytes, _stream(stream)))
 
 
 def page_fork(tables: PageTables, req: torch.Tensor, ws: torch.Tensor,
@@ -553,10 +567,11 @@ def page_fork(tables: PageTables, req: torch.Tensor, ws: torch.Tensor,
               stream=None) -> None:
     """db_page_fork: children share their parents' first tokens (req [n, 4]
     {parent, child, tokens, ignored})."""
-    at, n = _batch(req, 16)
+    at, n = _batch(req, 4)
+    space, nbytes = _whole(ws)
     _check("db_page_fork", _lib.db_page_fork(
         tables._ref, at, n, None if status is None else _at(status, n),
-        None if ctr is None else _at(ctr, 32), *_whole(ws), _stream(stream)))
+        None if ctr is None else _at(ctr, 32), space, nbytes, _stream(stream)))
 
 
 def page_free(tables: PageTables, req: torch.Tensor, ws: torch.Tensor,
@@ -564,10 +579,11 @@ def page_free(tables: PageTables, req: torch.Tensor, ws: torch.Tensor,
               stream=None) -> None:
     """db_page_free: sequences cut back to their first tokens (req [n, 2]
     {seq, keep}) give their other pages back."""
-    at, n = _batch(req, 8)
+    at, n = _batch(req, 2)
+    space, nbytes = _whole(ws)
     _check("db_page_free", _lib.db_page_free(
         tables._ref, at, n, None if status is None else _at(status, n),
-        None if ctr is None else _at(ctr, 32), *_whole(ws), _stream(stream)))
+        None if ctr is None else _at(ctr, 32), space, nbytes, _stream(stream)))
 
 
 def page_compact(tables: PageTables, out: PageTables, moves: torch.Tensor, n_moves: torch.Tensor,
@@ -576,9 +592,11 @@ def page_compact(tables: PageTables, out: PageTables, moves: torch.Tensor, n_mov
     after the moves goes to ``out`` (``tables`` itself, or other tensors of the
     same sizes); moves [cap, 4] and n_moves [1] get what page_copy has to
     move."""
+    at, cap = _batch(moves, 4)
+    space, nbytes = _whole(ws)
     _check("db_page_compact", _lib.db_page_compact(
-        tables._ref, out._ref, *_batch(moves, 16), _at(n_moves, 4),
-        None if ctr is None else _at(ctr, 32), *_whole(ws), _stream(stream)))
+        tables._ref, out._ref, at, cap, _at(n_moves, 4), None if ctr is None else _at(ctr, 32),
+        space, nbytes, _stream(stream)))
 
 
 def _strides(shape, stride, item: int) -> tuple[int, int]:
@@ -640,6 +658,7 @@ def page_copy(moves: torch.Tensor, n_moves: torch.Tensor, src: torch.Tensor, dst
                                    dst.stride())
         here = ctypes.byref(_Pool(src.data_ptr(), shape[1], *a))
         there = ctypes.byref(_Pool(dst.data_ptr(), dst.shape[1], *b))
+    at, most = _batch(moves, 4)
     _check("db_page_copy", _lib.db_page_copy(
-        *_batch(moves, 16), _at(n_moves, 4), here, there, form,
-        None if ctr is None else _at(ctr, 32), _stream(stream)))
+        at, most, _at(n_moves, 4), here, there, form, None if ctr is None else _at(ctr, 32),
+        _stream(stream)))

@@ -126,3 +126,38 @@ def test_strided_arrays_are_refused(db, op, name):
     with pytest.raises(ValueError, match="contiguous"):
         call(db, op, args)
     assert db.calls == []
+
+
+BATCHES = [(op, k) for op, k in TENSORS if k in ("req", "moves")]
+
+
+@pytest.mark.parametrize("op,name", BATCHES, ids=["-".join(x) for x in BATCHES])
+def test_batches_of_another_type_or_width_are_refused(db, op, name):
+    """An int64 [[0, 7]], what torch.tensor makes of it, would be read as the records {0, 0}, {7, 0}."""
+    n, width = arguments(db)[op][name].shape
+    for dtype in (torch.int64, torch.float32, torch.uint8, torch.int16):
+        args = arguments(db)[op]
+        args[name] = gpu(torch.zeros((n, width), dtype=dtype))
+        with pytest.raises(ValueError, match="int32"):
+            call(db, op, args)
+    for shape in ((n, 6 - width), (n, width, 1), (n * width + 1,), (n, 1), ()):
+        args = arguments(db)[op]
+        args[name] = gpu(i32(*shape))
+        with pytest.raises(ValueError, match="int32"):
+            call(db, op, args)
+    assert db.calls == []
+
+
+@pytest.mark.parametrize("op,name", BATCHES, ids=["-".join(x) for x in BATCHES])
+def test_batches_flat_unsigned_and_empty(db, op, name):
+    n, width = arguments(db)[op][name].shape
+    for t in (i32(n * width), i32(1, n, width), i32(n, width).view(torch.uint32)):
+        args = arguments(db)[op]
+        args[name] = gpu(t)
+        call(db, op, args)
+    if (op, name) != ("extend", "moves"):
+        for t in (i32(0), i32(0, width)):
+            args = arguments(db)[op]
+            args[name] = gpu(t)
+            call(db, op, args)
+            assert 0 in db.calls[-1][1]
