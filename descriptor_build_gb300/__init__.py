@@ -510,24 +510,29 @@ def _batch(t: torch.Tensor, width: int) -> tuple[int, int]:
 class PageTables:
     """The state of a paged cache: int32 CUDA tensors table [n_seqs, columns],
     length [n_seqs], refs [n_pages] and free [ceil(n_pages / 32)], which the
-    calls below update in place (their bits are the header's u32)."""
+    calls below update in place (their bits are the header's u32). n_seqs and
+    n_pages are below 2^31, and free starts on a multiple of 16 bytes."""
 
     def __init__(self, table: torch.Tensor, length: torch.Tensor, refs: torch.Tensor,
                  free: torch.Tensor, page_tokens: int):
         if table.dim() != 2:
             raise ValueError("table must be [n_seqs, columns]")
         n_seqs, columns = table.shape
-        n_pages = refs.numel()
-        if max(n_seqs, columns, n_pages, int(page_tokens)) > 0xFFFFFFFF:
-            raise ValueError("sizes of a cache are below 2^32")
+        n_pages, page_tokens = refs.numel(), int(page_tokens)
+        if not (0 < n_seqs < 1 << 31 and 0 < n_pages < 1 << 31):
+            raise ValueError("a cache has at least one sequence and one page, and below 2^31 of them")
+        if not (0 < columns < 1 << 32 and 0 < page_tokens < 1 << 32):
+            raise ValueError("columns and page_tokens are from 1 to 2^32 - 1")
         for name, t, n in (("table", table, n_seqs * columns), ("length", length, n_seqs),
                            ("refs", refs, n_pages), ("free", free, (n_pages + 31) // 32)):
             if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != n:
                 raise ValueError(f"{name} must be a contiguous int32 tensor of {n} elements")
         self.table, self.length, self.refs, self.free = table, length, refs, free
-        self.page_tokens = int(page_tokens)
+        self.page_tokens = page_tokens
         self._c = _Tables(*(_at(t, 0) for t in (table, length, refs, free)), n_seqs, columns,
                           n_pages, self.page_tokens)
+        if self._c.free % 16:
+            raise ValueError("free must start on a multiple of 16 bytes")
         self._ref = ctypes.byref(self._c)
 
     @classmethod
@@ -544,6 +549,8 @@ class PageTables:
 
 
 def page_workspace_size(n_seqs: int, n_pages: int) -> int:
+    """Bytes of the workspace of a cache of these sizes. Calls on a cache of
+    other sizes need another workspace."""
     return _size(_lib.db_page_workspace_size, n_seqs, n_pages)
 
 

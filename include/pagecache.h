@@ -16,7 +16,9 @@
  * for the next. db_page_tables and db_page_pool are HOST structs of device
  * pointers, read during the call only.
  *
- * The state of a cache of n_seqs sequences and n_pages pages:
+ * The state of a cache of n_seqs sequences and n_pages pages, both below
+ * 2^31 (no size may be 0; the free words start on a multiple of 16 bytes, the
+ * other arrays of 4):
  *   table  i32 [n_seqs][columns]: page of tokens [c*T, (c+1)*T) of the
  *          sequence, T = page_tokens; DB_PAGE_NONE past its last page
  *   length u32 [n_seqs]: tokens held; the first ceil(length/T) columns of the
@@ -102,7 +104,9 @@ typedef struct db_page_move {
   uint32_t rsvd;   /* written 0, ignored when read */
 } db_page_move;  /* 16 bytes */
 
-/* One workspace serves every call of this header on a cache of this size. */
+/* One workspace serves every call of this header on a cache of this size, and
+ * of no other: its parts lie where these two sizes put them, and one that
+ * calls on a cache of other sizes have used must be zero-filled again. */
 int db_page_workspace_size(uint32_t n_seqs, uint32_t n_pages, size_t* bytes);
 
 /* Sequences grow. Request i needs ceil((length + tokens)/T) - ceil(length/T)
@@ -111,9 +115,11 @@ int db_page_workspace_size(uint32_t n_seqs, uint32_t n_pages, size_t* bytes);
  * of whose holders are in the batch stays with the last of them, and every
  * other one gets a page of its own in its place. Pages go to the requests in
  * order (a copy's page first), the lowest free index first.
- *   moves   [n] out: the copies to make, in request order: the shared page,
- *           its replacement, and the tokens it holds for the sequence
- *   n_moves [1] out: how many
+ *   req     [n] requests (8-byte aligned)
+ *   moves   [n] out (16-byte aligned): the copies to make, in request order:
+ *           the shared page, its replacement, and the tokens it holds for the
+ *           sequence
+ *   n_moves [1] out (4-byte aligned): how many
  *   status  NULL or [n] out: DB_PAGE_INVALID when seq >= n_seqs, named
  *           before, or length + tokens > columns * T (or >= 2^32)
  *   ctr     NULL or counters: total = pages the valid requests need. With
@@ -130,7 +136,7 @@ int db_page_extend(const db_page_tables* t, const db_page_grow* req, uint32_t n,
  * Lengths are those before the call. DB_PAGE_INVALID: parent or child >=
  * n_seqs, parent == child, child named before or not empty, tokens >
  * length[parent]. ctr: total = references taken. n <= n_seqs,
- * n * columns < 2^32. */
+ * n * columns < 2^32, req 16-byte aligned. */
 int db_page_fork(const db_page_tables* t, const db_page_fork_req* req, uint32_t n,
                  uint8_t* status, db_counters* ctr, void* ws, size_t ws_bytes, void* stream);
 
@@ -138,7 +144,7 @@ int db_page_fork(const db_page_tables* t, const db_page_fork_req* req, uint32_t 
  * nothing does). Each page past ceil(keep/T) loses one reference and its
  * entry becomes DB_PAGE_NONE; a page without references is free.
  * DB_PAGE_INVALID: seq >= n_seqs or named before. ctr: total = pages that
- * became free. n <= n_seqs, n * columns < 2^32. */
+ * became free. n <= n_seqs, n * columns < 2^32, req 8-byte aligned. */
 int db_page_free(const db_page_tables* t, const db_page_cut* req, uint32_t n, uint8_t* status,
                  db_counters* ctr, void* ws, size_t ws_bytes, void* stream);
 
@@ -149,8 +155,8 @@ int db_page_free(const db_page_tables* t, const db_page_cut* req, uint32_t n, ui
  * arrays may be t's own (any of them); sizes and page_tokens must be t's.
  * The bytes are the caller's to move with db_page_copy. Sources are not
  * overwritten, so until then the cache at `t`, when kept, stays readable.
- *   moves   [cap] out: {source, destination, DB_PAGE_ALL}
- *   n_moves [1] out: how many
+ *   moves   [cap] out (16-byte aligned): {source, destination, DB_PAGE_ALL}
+ *   n_moves [1] out (4-byte aligned): how many
  *   ctr     NULL or counters: total = M, n_overflow = M - *n_moves. */
 int db_page_compact(const db_page_tables* t, const db_page_tables* out, db_page_move* moves,
                     uint32_t cap, uint32_t* n_moves, db_counters* ctr, void* ws, size_t ws_bytes,
@@ -180,8 +186,10 @@ typedef struct db_page_shape {
 /* The moves' bytes, in every plane: of each segment the first min(tokens,
  * page_tokens) slots. Slots past them keep what they hold. src and dst may be
  * the same pool, or different ones of one shape.
- *   moves   [max_moves] records, in device or pinned host memory
- *   n_moves [1] how many of them there are (more than max_moves: max_moves)
+ *   moves   [max_moves] records (16-byte aligned), in device or pinned host
+ *           memory
+ *   n_moves [1] how many of them there are (4-byte aligned; more than
+ *           max_moves: max_moves)
  * No page may be the destination of two records or of one and the source of
  * another (in one pool): its bytes are then undefined. A record naming a page
  * outside its pool is skipped; ctr (NULL or counters): total = records

@@ -161,3 +161,28 @@ def test_batches_flat_unsigned_and_empty(db, op, name):
             args[name] = gpu(t)
             call(db, op, args)
             assert 0 in db.calls[-1][1]
+
+
+@pytest.mark.parametrize("tokens", [-1, 0, -16, 1 << 32])
+def test_page_tokens_out_of_range_are_refused(db, tokens):
+    with pytest.raises(ValueError, match="page_tokens"):
+        db.PageTables(gpu(i32(6, 5)), gpu(i32(6)), gpu(i32(40)), gpu(i32(2)), tokens)
+
+
+def test_caches_of_no_or_too_many_sequences_or_pages_are_refused(db):
+    many = 1 << 31  # sizes alone: nothing is allocated
+    size = lambda *shape: torch.empty(shape, dtype=torch.int32, device="meta")
+    for table, length, refs, free in (((many, 1), many, 40, 2), ((6, 5), 6, many, many // 32),
+                                      ((0, 5), 0, 40, 2), ((6, 5), 6, 0, 0)):
+        with pytest.raises(ValueError, match="at least one sequence and one page, and below 2.31"):
+            db.PageTables(size(*table), size(length), size(refs), size(free), 16)
+    with pytest.raises(ValueError, match="columns"):
+        db.PageTables(gpu(i32(6, 0)), gpu(i32(6)), gpu(i32(40)), gpu(i32(2)), 16)
+
+
+def test_free_words_off_16_bytes_are_refused(db):
+    arrays = gpu(i32(6, 5)), gpu(i32(6)), gpu(i32(40))
+    for shift in (1, 2, 3):
+        with pytest.raises(ValueError, match="16 bytes"):
+            db.PageTables(*arrays, gpu(i32(2 + shift)[shift:]), 16)
+    db.PageTables(*arrays, gpu(i32(6)[4:]), 16)
