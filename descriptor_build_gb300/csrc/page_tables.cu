@@ -24,28 +24,41 @@ namespace db {
 namespace {
 
 // Times below are of one GB300, microseconds, of the sequence of calls named.
+// They were taken when the choice was made, unless said otherwise.
 //
-// What bounds these kernels is latency, and past that the rate at which an SM
-// takes scattered 4-byte accesses, one line a clock: a freed entry is a load
-// and a store of its reference and an atomic on its free bit. Bandwidth is
-// far away (a freed or taken page is 24 bytes).
+// What bounds these kernels is latency: a few dependent trips to memory and
+// the barriers of the plan between them. Freeing 98,304 pages in 96 CTAs (9.8)
+// keeps a scheduler issuing in 10 % of its cycles, L1 18 % and L2 4 % busy; of
+// 21 cycles between two instructions of a warp 11 are at barriers and 3 for
+// loads. The scattered lines of those pages (a load and a store of a
+// reference, an atomic on its free bit), one a clock, are 3,100 clocks of each
+// of the 96 SMs, 1.6. 320,000 pages (11.4, 256 CTAs) are alike: L1 at 29 %,
+// lines for 3.3 of the time. Only the second
+// kernel of an extension is bound by something else, by issue (63 % of cycles,
+// two searches a page). Bandwidth is far away (a freed or taken page is 24 bytes).
 constexpr uint32_t kMaxTeam = 8;          // CTAs of the largest team (a portable cluster)
 constexpr uint32_t kTeamThreads = 1024;   // threads of a CTA of a team, or of a gang that extends
-// Threads of a CTA of a gang with few requests. A step of 48 sequences takes
-// 8.2 in CTAs of 256 or of 512 threads and took 11.7 in one of 1,024, whose
-// barriers and idle warps cost more than its width saves. Up to as many
+// Threads of a CTA of a gang with few requests. A step of 48 sequences took
+// 8.2 in CTAs of 256 or of 512 threads and 11.7 in one of 1,024, whose
+// barriers and idle warps cost more than its width saves. Now it takes 7.8 in a
+// pool of 32,768 pages, 8.6 in one of 32,800, whose extensions go to CTAs of
+// 1,024 threads (a thread of the smaller ones keeps one quad of free words),
+// and 9.0 in one of 131,072. Up to as many
 // requests free and fork go to a gang: 1,023 of one prompt took 14.4 and 12.7
 // in a gang of 1,024 threads and 13.3 and 11.0 as a team and a second kernel.
 constexpr uint32_t kSmallThreads = 256;
-// Requests of a group (see "row units"): 4, 8, 16 or 32 of them give 61, 49,
-// 46 or 50 for dropping and forking 1,023 samples anew, 21, 23, 25 or 33 for a
-// decode step of 4,096 sequences, and 13, 14, 15 or 34 for a turnover of 256.
+// Requests of a group (see "row units"): 4, 8, 16 or 32 of them gave 61, 49,
+// 46 or 50 for dropping and forking 1,023 samples anew (44 now, with 8), 21,
+// 23, 25 or 33 for a decode step of 4,096 sequences (18.5 now), and 13, 14, 15
+// or 34 for a turnover of 256 (12.4 now).
 constexpr uint32_t kRows = 8;
 constexpr uint32_t kSearch = 1024;        // starts that a second kernel keeps in shared memory
 // Free words that a CTA of a gang counts (262,144 pages). Each CTA reads them
 // all: an extension by 320,000 pages out of a million took 23.5 in a gang and
 // takes 15 as a team and a second kernel, one by 98,000 of 262,144 takes 9.9
-// and took 8.0 + 5.2.
+// and took 8.0 + 5.2. For 48 sequences the limit is low: a step takes 10.2 with
+// 262,144 pages in a gang, 13.0 with 64 more as a team and a second kernel,
+// and 11.9 with a million so; where the two meet was not measured.
 constexpr uint32_t kGangWords = 8192;
 constexpr uint32_t kTeamWords = 2048;     // free words that a CTA of a team keeps in shared memory
 // A second kernel, or a gang of more than one CTA, is launched when the sizes
@@ -602,7 +615,7 @@ struct FreeParams {
 
 // refs[p] -= the rows of the batch that drop p; p is free when nothing is left.
 // A step of 48 sequences frees its 12 pages in 3.7 (one launch, warm), 192
-// prompt chunks of 512 pages in 9.0, 64 sequences of 5,000 pages in 11.5.
+// prompt chunks of 512 pages in 9.8, 64 sequences of 5,000 pages in 11.4.
 template <typename X>
 __device__ __forceinline__ void free_units(const Rows& p, const X& x, uint32_t first,
                                            uint32_t stride, uint32_t units, uint32_t* count,
@@ -674,7 +687,10 @@ __device__ __forceinline__ void free_units(const Rows& p, const X& x, uint32_t f
 
 // The same for a row with at most kFewEntries of them, by one thread: where no
 // request of a CTA has more (a decode step), units would be almost empty. 4,096
-// sequences with 267 pages among them: 10.0 in units, 6.9 so.
+// sequences with 267 pages among them: 10.0 in units, 6.9 so. A gang does it
+// so when it is one CTA, which the width of the table decides: a step of 64
+// sequences with 256 columns takes 8.1, one of 72, in units of several CTAs,
+// 9.8, of 128 11.1 and of 256 11.9.
 constexpr uint32_t kFewEntries = 4;
 
 __device__ __forceinline__ void free_few(const Rows& p, const Plan& pl, uint32_t* count,
@@ -858,7 +874,7 @@ struct ForkParams {
 
 // The child's row is the parent's, refs[p] += the children that take p. 32
 // forks of 44 pages take 4.4, 1,023 of 1,024 pages (4 MB of tables written)
-// 5.6 + 6.5 for the plan and the units.
+// 5.1 + 6.4 for the plan and the units.
 template <typename X>
 __device__ __forceinline__ bool fork_units(const Rows& p, const X& x, uint32_t first,
                                            uint32_t stride, uint32_t units) {
@@ -1151,8 +1167,8 @@ __device__ __forceinline__ uint32_t nth_page(const uint32_t* bits, uint32_t n_pa
 // A request needs ceil((length + tokens) / T) - ceil(length / T) pages, and one
 // for a copy when it adds to a page that others hold: all of a page's holders
 // but the last when all are in the batch, else all of them. Start of request i
-// = the needs before it; page e of the batch = the e-th free one. 5.6 for 48
-// sequences, 9.9 for 192 times 512 pages, 10.8 for 1,023 holders of one page
+// = the needs before it; page e of the batch = the e-th free one. 5.3 for 48
+// sequences, 10.1 for 192 times 512 pages, 10.5 for 1,023 holders of one page
 // that all copy it.
 template <uint32_t kThreads>
 __global__ void __launch_bounds__(kThreads) page_extend_gang_kernel(const ExtendParams p) {
@@ -1421,8 +1437,8 @@ struct CompactParams {
   Work w;
 };
 
-// 131,072 pages, 32,000 moves, 1,024 rows of 512 entries: 9.5 for plan, moves
-// and tables together, beside 626 for the moves' 4.25 GB. Listing free and live
+// 131,072 pages, 32,000 moves, 1,024 rows of 512 entries: 12 for plan, moves
+// and tables together, beside 628 for the moves' 4.25 GB. Listing free and live
 // pages word by word in one CTA first took 50.
 //
 // Live pages before a word.

@@ -6,8 +6,10 @@
  * A model's key/value cache lives in fixed-size pages of the device heap; the
  * ranges that db_prp_build reads or writes and that db_wqe_bucket puts to a
  * peer are such pages. The calls here keep the page tables on the device, in
- * stream order with the kernels that read them and the descriptors built
- * from them, with no host round trip.
+ * stream order with the kernels that read them, with no host round trip
+ * between them. No call makes the requests of db_prp_build or db_wqe_bucket
+ * from a row or from a list of moves: that is the caller's to do, on the
+ * device or by way of the host.
  *
  * Conventions are those of descbuild.h: device pointers owned by the caller,
  * asynchronous on `stream`, negative errno returns for bad arguments,
@@ -193,7 +195,13 @@ typedef struct db_page_shape {
  * No page may be the destination of two records or of one and the source of
  * another (in one pool): its bytes are then undefined. A record naming a page
  * outside its pool is skipped; ctr (NULL or counters): total = records
- * copied, n_invalid = records skipped. Strides must keep pages of one pool
+ * copied, n_invalid = records skipped. One CTA counts them after its share of
+ * the copying, at about a nanosecond a record: long lists of small pages
+ * copy faster without counters (a million pages of 64 bytes in 52 us, and in
+ * 853 with them). Launches are sized by max_moves: many more of them than
+ * *n_moves cost time where segments are small (6 copies of 64 planes and 8
+ * segments take 4 us in a list of 6, 27 in one of 4,096 and 516 in one of
+ * 100,000). Strides must keep pages of one pool
  * apart; they and the bases need no alignment, but 16 bytes copy fastest. A
  * page's bytes in all planes are at most 2^31, planes at most 65536. */
 int db_page_copy(const db_page_move* moves, uint32_t max_moves, const uint32_t* n_moves,
