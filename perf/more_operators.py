@@ -290,8 +290,9 @@ def plain_write(s):
         x = new.float()
         if type in LARGEST:
             top = x.abs().amax(-1)
-            scale[at] = top / LARGEST[type]
-            x = (x * (LARGEST[type] / top)[..., None]).clamp(-LARGEST[type], LARGEST[type])
+            full = torch.full_like(top, LARGEST[type])  # a tensor: by a number it would be a product with its reciprocal
+            scale[at] = top / full
+            x = (x * (full / top)[..., None]).clamp(-LARGEST[type], LARGEST[type])
             x = x.round() if type == "i8" else x
         _bytes(pool)[at] = _bytes(x.to(TYPES[type]))
     s["status"].zero_()
