@@ -19,6 +19,10 @@ Records of the paged cache (include/pagecache.h), u32 fields as int32 bits:
   grow          8 B  {seq, tokens}                     -> int32 [n, 2]
   fork         16 B  {parent, child, tokens, rsvd}     -> int32 [n, 4]
   move         16 B  {src, dst, tokens, rsvd}          -> int32 [n, 4]
+What the pages hold (include/cachedata.h) are tensors of their own types: the
+keys or values of a layer [pages, tokens, heads, width] (token_dim 1) or
+[pages, heads, tokens, width] (token_dim 2), bfloat16, float16, float8_e4m3fn
+or int8, the 8-bit ones with float32 scales of the same axes but the last.
 """
 
 from __future__ import annotations
@@ -51,6 +55,8 @@ __all__ = [
     "PageTables", "page_workspace_size", "page_extend", "page_fork", "page_free", "page_compact",
     "page_copy", "PAGE_NONE", "PAGE_ALL", "PAGE_OK", "PAGE_INVALID", "PAGE_SHORT",
     "ERR_PAGE_TABLE",
+    "cache_write", "cache_read", "cache_attention_workspace_size", "cache_attention",
+    "draft_verify", "cache_keep",
 ]
 
 PRP_OK, PRP_INVALID, PRP_OVERFLOW = 0, 1, 2
@@ -135,6 +141,18 @@ def _load():
     lib.db_page_copy.argtypes = [vp, u32, vp, vp, vp, vp, vp, vp]
     for name in ("db_page_workspace_size", "db_page_extend", "db_page_fork", "db_page_free",
                  "db_page_compact", "db_page_copy"):
+        getattr(lib, name).restype = i32
+    f32 = ctypes.c_float
+    lib.db_cache_write.argtypes = [vp, vp, vp, vp, vp, u32, vp, vp, vp]
+    lib.db_cache_read.argtypes = [vp, vp, vp, vp, vp, vp, u32, vp, vp, vp]
+    lib.db_cache_attention_workspace_size.argtypes = [u32, u32, u32, u32, u32, psz]
+    lib.db_cache_attention.argtypes = [vp, vp, vp, vp, vp, u32, u32, u32, f32, vp, u32, vp, vp, vp,
+                                       vp, sz, vp]
+    lib.db_draft_verify.argtypes = [vp, u32, u32, vp, vp, vp, u64, vp, u64, u32, u32, vp, vp, vp,
+                                    vp, vp, vp, vp]
+    lib.db_cache_keep.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    for name in ("db_cache_write", "db_cache_read", "db_cache_attention_workspace_size",
+                 "db_cache_attention", "db_draft_verify", "db_cache_keep"):
         getattr(lib, name).restype = i32
     lib.db_strerror.argtypes = [i32]
     lib.db_strerror.restype = ctypes.c_char_p
@@ -669,3 +687,248 @@ def page_copy(moves: torch.Tensor, n_moves: torch.Tensor, src: torch.Tensor, dst
     _check("db_page_copy", _lib.db_page_copy(
         at, most, _at(n_moves, 4), here, there, form, None if ctr is None else _at(ctr, 32),
         _stream(stream)))
+
+
+# ------------------------------------------------------- a paged cache's contents
+class _CacheBatch(ctypes.Structure):  # db_cache_batch
+    _fields_ = [("seq", ctypes.c_void_p), ("start", ctypes.c_void_p), ("n", ctypes.c_uint32),
+                ("rows", ctypes.c_uint32)]
+
+
+class _CacheLayer(ctypes.Structure):  # db_cache_layer
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("k_stride", ctypes.c_uint64),
+                ("v_stride", ctypes.c_uint64), ("k_scale_stride", ctypes.c_uint64),
+                ("v_scale_stride", ctypes.c_uint64), ("heads", ctypes.c_uint32),
+                ("width", ctypes.c_uint32), ("type", ctypes.c_uint32),
+                ("heads_first", ctypes.c_uint32)]
+
+
+class _CacheRows(ctypes.Structure):  # db_cache_rows
+    _fields_ = [("base", ctypes.c_void_p), ("row_stride", ctypes.c_uint64),
+                ("head_stride", ctypes.c_uint64)]
+
+
+_ROW_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_CACHE_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 3, torch.int8: 4}
+
+
+def _i32(t: torch.Tensor, n: int, what: str) -> int:
+    """The address of an int32 tensor of at least ``n`` elements."""
+    if t.dtype is not _I32 and t.dtype is not _U32:
+        raise ValueError(f"{what} must be an int32 tensor, not {t.dtype}")
+    return _at(t, 4 * n)
+
+
+def _cache_batch(seq: torch.Tensor, start: torch.Tensor, rows: int) -> tuple:
+    n = seq.numel()
+    if start.numel() != n + 1:
+        raise ValueError(f"start must have {n + 1} elements for {n} sequences")
+    b = _CacheBatch(_i32(seq, n, "seq"), _i32(start, n + 1, "start"), n, rows)
+    return ctypes.byref(b), n
+
+
+def _cache_rows(t: torch.Tensor, heads: int, width: int) -> "ctypes.pointer":
+    """Rows [rows, heads, width] outside the cache, of any strides but the last."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != width or t.stride(2) != 1:
+        raise ValueError(f"rows must be [rows, {heads}, {width}] with neighbouring values")
+    if not (t.is_cuda or t.is_pinned()):
+        _refuse(t)
+    size = t.element_size()
+    return ctypes.byref(_CacheRows(t.data_ptr(), t.stride(0) * size, t.stride(1) * size))
+
+
+@functools.lru_cache(maxsize=1024)
+def _layer_plan(shape, stride, dtype, token_dim, page_tokens, scale_shape, scale_stride):
+    """What a pool of keys or values says: (page stride and scales' page stride
+    in bytes, heads, width, type)."""
+    if len(shape) != 4 or token_dim not in (1, 2):
+        raise ValueError("a layer's pool is [pages, tokens, heads, width] (token_dim 1) or "
+                         "[pages, heads, tokens, width] (token_dim 2)")
+    if dtype not in _CACHE_TYPES:
+        raise ValueError(f"a cache holds bfloat16, float16, float8_e4m3fn or int8, not {dtype}")
+    if shape[token_dim] != page_tokens:
+        raise ValueError(f"the pool's pages hold {shape[token_dim]} tokens, the tables' {page_tokens}")
+
+    def contiguous(inner, steps):
+        want = 1
+        for size, step in zip(reversed(inner), reversed(steps)):
+            if size != 1 and step != want:
+                raise ValueError("a pool's pages must be contiguous")
+            want *= size
+
+    contiguous(shape[1:], stride[1:])
+    size = dtype.itemsize
+    scale = 0
+    if size == 1:
+        if scale_shape is None or scale_shape != shape[:3]:
+            raise ValueError(f"a cache of {dtype} needs scales {list(shape[:3])}")
+        contiguous(scale_shape[1:], scale_stride[1:])
+        scale = scale_stride[0] * 4
+    elif scale_shape is not None:
+        raise ValueError("only 8-bit caches have scales")
+    return stride[0] * size, scale, shape[3 - token_dim], shape[3], _CACHE_TYPES[dtype]
+
+
+def _cache_layer(tables: PageTables, k_pool, v_pool, k_scale, v_scale, token_dim):
+    """The layer's struct, its heads and width."""
+    said = []
+    for pool, scale in ((k_pool, k_scale), (v_pool, v_scale)):
+        if not (pool.is_cuda or pool.is_pinned()):
+            _refuse(pool)
+        if pool.shape[0] < tables._c.n_pages:
+            raise ValueError(f"a pool of {pool.shape[0]} pages where the tables have {tables._c.n_pages}")
+        if scale is not None:
+            if not (scale.is_cuda or scale.is_pinned()):
+                _refuse(scale)
+            if scale.dtype is not torch.float32:
+                raise ValueError("scales are float32")
+        said.append(_layer_plan(pool.shape, pool.stride(), pool.dtype, token_dim, tables.page_tokens,
+                                None if scale is None else scale.shape,
+                                None if scale is None else scale.stride()))
+    (k_step, ks_step, heads, width, kind), (v_step, vs_step, *rest) = said
+    if rest != [heads, width, kind]:
+        raise ValueError("the pools of keys and values differ in heads, width or type")
+    layer = _CacheLayer(k_pool.data_ptr(), v_pool.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
+                        None if v_scale is None else v_scale.data_ptr(), k_step, v_step, ks_step, vs_step,
+                        heads, width, kind, token_dim == 2)
+    return ctypes.byref(layer), heads, width
+
+
+def _row_type(*tensors: torch.Tensor) -> int:
+    dtype = tensors[0].dtype
+    if any(t.dtype is not dtype for t in tensors) or dtype not in _ROW_TYPES:
+        raise ValueError("rows are bfloat16, float16 or float32, all of one type")
+    return _ROW_TYPES[dtype]
+
+
+def _maybe(t: torch.Tensor | None, nbytes: int) -> int | None:
+    return None if t is None else _at(t, nbytes)
+
+
+def cache_write(tables: PageTables, seq: torch.Tensor, start: torch.Tensor, k: torch.Tensor,
+                v: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None,
+                token_dim: int = 1, status: torch.Tensor | None = None,
+                ctr: torch.Tensor | None = None, stream=None) -> None:
+    """db_cache_write: rows start[i] to start[i + 1] of k and v [rows, heads,
+    width] go to the slots of the last tokens of sequence seq[i], rounded to
+    the pools' type or quantised with a scale for each row."""
+    layer, heads, width = _cache_layer(tables, k_pool, v_pool, k_scale, v_scale, token_dim)
+    if k.shape[0] != v.shape[0]:
+        raise ValueError("k and v differ in rows")
+    batch, n = _cache_batch(seq, start, k.shape[0])
+    _check("db_cache_write", _lib.db_cache_write(
+        tables._ref, batch, layer, _cache_rows(k, heads, width), _cache_rows(v, heads, width),
+        _row_type(k, v), _maybe(status, n), _maybe(ctr, 32), _stream(stream)))
+
+
+def cache_read(tables: PageTables, seq: torch.Tensor, start: torch.Tensor, k: torch.Tensor,
+               v: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
+               k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None,
+               first: torch.Tensor | None = None, token_dim: int = 1,
+               status: torch.Tensor | None = None, ctr: torch.Tensor | None = None,
+               stream=None) -> None:
+    """db_cache_read: rows start[i] to start[i + 1] of k and v [rows, heads,
+    width] get the tokens of sequence seq[i] from position first[i] (0) on;
+    rows past its last token become zeros."""
+    layer, heads, width = _cache_layer(tables, k_pool, v_pool, k_scale, v_scale, token_dim)
+    if k.shape[0] != v.shape[0]:
+        raise ValueError("k and v differ in rows")
+    batch, n = _cache_batch(seq, start, k.shape[0])
+    _check("db_cache_read", _lib.db_cache_read(
+        tables._ref, batch, None if first is None else _i32(first, n, "first"), layer,
+        _cache_rows(k, heads, width), _cache_rows(v, heads, width), _row_type(k, v),
+        _maybe(status, n), _maybe(ctr, 32), _stream(stream)))
+
+
+def cache_attention_workspace_size(n: int, q_heads: int, heads: int, width: int,
+                                   max_tokens: int) -> int:
+    """Bytes of cache_attention's workspace on the current device."""
+    return _size(_lib.db_cache_attention_workspace_size, n, q_heads, heads, width, max_tokens)
+
+
+def cache_attention(tables: PageTables, seq: torch.Tensor, start: torch.Tensor, q: torch.Tensor,
+                    k_pool: torch.Tensor, v_pool: torch.Tensor, out: torch.Tensor,
+                    ws: torch.Tensor, max_tokens: int, scale: float | None = None,
+                    mask: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                    k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None,
+                    token_dim: int = 1, status: torch.Tensor | None = None,
+                    ctr: torch.Tensor | None = None, stream=None) -> None:
+    """db_cache_attention: the last tokens of sequences (rows of q and out
+    [rows, q_heads, width], at most max_tokens of a sequence) attend to all
+    tokens before them and to those of their own that mask [rows, words] of
+    bits names (None: themselves and the ones before). scale None: 1 /
+    sqrt(width). lse: float32 [rows, q_heads]."""
+    layer, heads, width = _cache_layer(tables, k_pool, v_pool, k_scale, v_scale, token_dim)
+    rows, q_heads = q.shape[0], q.shape[1]
+    if out.shape[0] != rows:
+        raise ValueError("q and out differ in rows")
+    batch, n = _cache_batch(seq, start, rows)
+    words = 0
+    if mask is not None:
+        if mask.dim() != 2 or mask.shape[0] != rows:
+            raise ValueError(f"mask must be [{rows}, words]")
+        words = mask.shape[1]
+    if lse is not None and lse.dtype is not torch.float32:
+        raise ValueError("lse is float32")
+    space, nbytes = _whole(ws)
+    _check("db_cache_attention", _lib.db_cache_attention(
+        tables._ref, batch, layer, _cache_rows(q, q_heads, width), _cache_rows(out, q_heads, width),
+        _row_type(q, out), q_heads, max_tokens, width ** -0.5 if scale is None else scale,
+        None if mask is None else _i32(mask, rows * words, "mask"), words,
+        _maybe(lse, 4 * rows * q_heads), _maybe(status, n), _maybe(ctr, 32), space, nbytes,
+        _stream(stream)))
+
+
+def draft_verify(start: torch.Tensor, parent: torch.Tensor, token: torch.Tensor, p: torch.Tensor,
+                 u: torch.Tensor, path: torch.Tensor, accepted: torch.Tensor, next: torch.Tensor,
+                 q: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                 ctr: torch.Tensor | None = None, stream=None) -> None:
+    """db_draft_verify: trees of drafted tokens (rows start[i] to start[i + 1]
+    of parent, token, u, and of the probabilities p and q [rows, vocab])
+    accepted or not; path [rows], accepted [n] and next [n] get the result."""
+    n, rows = start.numel() - 1, p.shape[0]
+    if n < 0 or p.dim() != 2 or p.stride(1) != 1:
+        raise ValueError("start must be [n + 1], p [rows, vocab] with neighbouring values")
+    if q is not None and (q.shape != p.shape or q.stride(1) != 1):
+        raise ValueError("q must be of p's shape, with neighbouring values")
+    for t in (p, q):
+        if t is not None and not (t.is_cuda or t.is_pinned()):
+            _refuse(t)
+    if u.dtype is not torch.float32:
+        raise ValueError("u is float32")
+    kind = _row_type(p) if q is None else _row_type(p, q)
+    _check("db_draft_verify", _lib.db_draft_verify(
+        _i32(start, n + 1, "start"), n, rows, _i32(parent, rows, "parent"), _i32(token, rows, "token"),
+        p.data_ptr(), p.stride(0), None if q is None else q.data_ptr(), 0 if q is None else q.stride(0),
+        kind, p.shape[1], _at(u, 4 * rows), _i32(path, rows, "path"), _i32(accepted, n, "accepted"),
+        _i32(next, n, "next"), _maybe(status, n), _maybe(ctr, 32), _stream(stream)))
+
+
+def cache_keep(tables: PageTables, seq: torch.Tensor, start: torch.Tensor, path: torch.Tensor,
+               accepted: torch.Tensor, pool: torch.Tensor, token_dim: int = 2,
+               cut: torch.Tensor | None = None, status: torch.Tensor | None = None,
+               ctr: torch.Tensor | None = None, stream=None) -> None:
+    """db_cache_keep: in every plane of ``pool`` [planes, pages, ...] (as in
+    page_copy; token_dim is the axis of a page's tokens) the tokens on the
+    accepted paths move together. cut [n, 2] gets the requests of page_free
+    that give the others' slots back."""
+    shape = pool.shape
+    if not (pool.is_cuda or pool.is_pinned()):
+        _refuse(pool)
+    if token_dim is None:
+        raise ValueError("token_dim must be one of a page's axes (2 and up)")
+    _, form, a, _ = _copy_plan(shape, pool.stride(), pool.element_size(), token_dim)
+    if shape[token_dim] != tables.page_tokens:
+        raise ValueError(f"the pool's pages hold {shape[token_dim]} tokens, the tables' {tables.page_tokens}")
+    if shape[1] < tables._c.n_pages:
+        raise ValueError(f"a pool of {shape[1]} pages where the tables have {tables._c.n_pages}")
+    rows = path.numel()
+    batch, n = _cache_batch(seq, start, rows)
+    if cut is not None and _batch(cut, 2)[1] < n:
+        raise ValueError(f"cut holds fewer than {n} records")
+    _check("db_cache_keep", _lib.db_cache_keep(
+        tables._ref, batch, _i32(path, rows, "path"), _i32(accepted, n, "accepted"),
+        ctypes.byref(_Pool(pool.data_ptr(), shape[1], *a)), form, _maybe(cut, 8 * n),
+        _maybe(status, n), _maybe(ctr, 32), _stream(stream)))

@@ -1,0 +1,8 @@
+// The attention kernels for rows of up to 256 values (cache_attention.cuh).
+#include "cache_attention.cuh"
+
+namespace db {
+int launch_attention_256(const AttnParams& p, uint32_t type, uint32_t blocks, unsigned grid, cudaStream_t s) {
+  return launch_attention<256>(p, type, blocks, grid, s);
+}
+}  // namespace db

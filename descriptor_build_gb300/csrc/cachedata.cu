@@ -1,0 +1,604 @@
+// Keys and values into a cache's pages and out of them, and tokens moved
+// within (include/cachedata.h: db_cache_write, db_cache_read, db_cache_keep).
+//
+// All three are bound by memory: a value is read once and written once. A
+// warp takes neighbouring rows (tokens) of the batch, finds its request once,
+// and handles a row's keys and values of all heads, 8 values a lane, so that
+// the 4 to 32 lanes that hold a head's row can reduce its largest magnitude.
+#include "cachedata.cuh"
+
+namespace db {
+
+int check_cache(const db_page_tables* t, const db_cache_batch* b, uint8_t* status, db_counters* ctr,
+                CacheView* v) {
+  if (!t || !b || !t->table || !t->length || !aligned(t->table, 4) || !aligned(t->length, 4))
+    return -EINVAL;
+  if (!t->n_seqs || t->n_seqs >= 1u << 31 || !t->columns || !t->n_pages || t->n_pages >= 1u << 31 ||
+      !t->page_tokens)
+    return -EINVAL;
+  if (b->n >= 1u << 31 || b->rows >= 1u << 31 || !aligned(ctr, 8)) return -EINVAL;
+  if (b->n && (!b->seq || !b->start || !aligned(b->seq, 4) || !aligned(b->start, 4))) return -EINVAL;
+  *v = CacheView{t->table, t->length, t->n_seqs, t->columns, t->n_pages, t->page_tokens,
+                 b->seq,   b->start,  b->n,      b->rows,    status,     ctr};
+  return 0;
+}
+
+int check_layer(const db_page_tables* t, const db_cache_layer* c) {
+  if (!c || !c->k || !c->v || !c->heads || !c->width || c->width % 16 || c->width > 256)
+    return -EINVAL;
+  if (c->type != DB_BF16 && c->type != DB_F16 && c->type != DB_E4M3 && c->type != DB_I8) return -EINVAL;
+  const uint64_t limit = 1ull << 31, rows = (uint64_t)c->heads * t->page_tokens;
+  if (rows >= limit || rows * c->width >= limit) return -EINVAL;
+  const uint64_t bytes = rows * c->width * item_bytes(c->type);
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || c->k_stride % 16 || c->v_stride % 16) return -EINVAL;
+  if (t->n_pages > 1 && (c->k_stride < bytes || c->v_stride < bytes)) return -EINVAL;
+  if (item_bytes(c->type) == 1) {
+    if (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) ||
+        c->k_scale_stride % 4 || c->v_scale_stride % 4)
+      return -EINVAL;
+    if (t->n_pages > 1 && (c->k_scale_stride < rows * 4 || c->v_scale_stride < rows * 4)) return -EINVAL;
+  } else if (c->k_scale || c->v_scale) {
+    return -EINVAL;
+  }
+  return 0;
+}
+
+int check_rows(const db_cache_rows* r, uint32_t rows, uint32_t heads, uint32_t width, uint32_t type,
+               bool written) {
+  if (!r || type > DB_F32) return -EINVAL;
+  if (!rows) return 0;
+  if (!r->base || !aligned(r->base, 16) || r->row_stride % 16 || r->head_stride % 16) return -EINVAL;
+  if (written && heads > 1 && r->head_stride < (uint64_t)width * item_bytes(type)) return -EINVAL;
+  return 0;
+}
+
+int zero_counters(db_counters* ctr, cudaStream_t s) {
+  if (!ctr) return 0;
+  const cudaError_t e = cudaMemsetAsync(ctr, 0, sizeof(*ctr), s);
+  return e == cudaSuccess ? 0 : cuda_failure(e);
+}
+
+namespace {
+
+constexpr uint32_t kThreads = 256, kWarps = kThreads / 32;
+constexpr int kUnroll = 4;  // heads' rows of a lane under way
+
+struct MoveParams {
+  CacheView view;
+  db_cache_layer c;
+  db_cache_rows k, v;
+  const int32_t* first;  // read: first positions or NULL
+  uint32_t chunk;        // rows of a warp
+  uint32_t lanes;        // of a head's row: a power of two, 8 values each
+  uint64_t token_step, head_step;              // bytes within a page
+  uint32_t scale_token_step, scale_head_step;  // floats
+};
+
+// Eight values of a row outside the cache.
+template <typename T>
+__device__ __forceinline__ void load8(const char* p, float* x) {
+  if (sizeof(T) == 4) {
+    const float4 a = __ldcs((const float4*)p), b = __ldcs((const float4*)p + 1);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  } else {
+    const uint4 a = __ldcs((const uint4*)p);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = unpack2<typename std::conditional<sizeof(T) == 4, __half, T>::type>(w[j]);
+      x[2 * j] = f.x;
+      x[2 * j + 1] = f.y;
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(char* p, const float* x) {
+  if (sizeof(T) == 4) {
+    ((float4*)p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    ((float4*)p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+    typedef typename std::conditional<sizeof(T) == 4, __half, T>::type H;
+    *(uint4*)p = make_uint4(pack2<H>(x[0], x[1]), pack2<H>(x[2], x[3]), pack2<H>(x[4], x[5]),
+                            pack2<H>(x[6], x[7]));
+  }
+}
+
+// The largest magnitude of the lanes that share a row, as bits: of floats
+// without their sign, larger bits are larger values, infinities above every
+// number and NaN above those.
+__device__ __forceinline__ uint32_t largest_bits(const float* x, uint32_t lanes) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(x[j]) & 0x7FFFFFFFu);
+  for (uint32_t o = lanes / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+  return m;
+}
+
+__device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+// Codes of eight values and, in `scale`, their row's scale.
+template <bool kE4m3>
+__device__ __forceinline__ uint2 quantise8(const float* x, uint32_t top, float& scale) {
+  const float largest = kE4m3 ? 448.f : 127.f;
+  if (top >= 0x7F800000u) {
+    scale = __uint_as_float(0x7FC00000u);
+    return make_uint2(0, 0);
+  }
+  const float a = __uint_as_float(top), by = __fdiv_rn(largest, a);
+  scale = __fdiv_rn(a, largest);
+  if (scale == 0.f || isinf(by)) {
+    scale = 0.f;
+    return make_uint2(0, 0);
+  }
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float* y = x + 4 * h;
+    if (kE4m3) {
+      w[h] = e4m3_pair(y[0] * by, y[1] * by) | e4m3_pair(y[2] * by, y[3] * by) << 16;
+    } else {
+      uint32_t c = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int q = max(-127, min(127, __float2int_rn(y[j] * by)));
+        c |= (uint32_t)(q & 0xFF) << (8 * j);
+      }
+      w[h] = c;
+    }
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// One warp: rows [r0, r1) of the batch. kType: what the pages hold.
+template <typename Src, int kType>
+__global__ void __launch_bounds__(kThreads) cache_write_kernel(const MoveParams p) {
+  constexpr bool kCodes = kType == DB_E4M3 || kType == DB_I8;
+  wait_for_prerequisites();
+  dependents_may_launch();
+  const CacheView& v = p.view;
+  const uint32_t lane = threadIdx.x & 31;
+  const uint64_t warp = (uint64_t)blockIdx.x * kWarps + threadIdx.x / 32;
+  report_requests(v, (uint64_t)blockIdx.x * kThreads + threadIdx.x, (uint64_t)gridDim.x * kThreads, true);
+  const uint64_t r0 = warp * p.chunk;
+  const uint32_t r1 = (uint32_t)min(r0 + p.chunk, (uint64_t)v.rows);
+  if (r0 >= r1) return;
+  const uint32_t lanes = p.lanes, at = (lane & (lanes - 1)) * 8, per = 32 / lanes;
+  const uint32_t heads = p.c.heads, units = 2 * heads;
+  const bool mine = at < p.c.width;
+  uint32_t i = find_request(v.start, v.n, (uint32_t)r0);
+  Request q = read_request(v, i, true);
+  for (uint32_t r = (uint32_t)r0; r < r1; ++r) {
+    while (i + 1 < v.n && (int32_t)r >= __ldg(v.start + i + 1)) q = read_request(v, ++i, true);
+    if (!q.ok || r < q.first || r - q.first >= q.rows) continue;
+    const uint32_t position = q.length - q.rows + (r - q.first);
+    const uint32_t column = position / v.page_tokens, slot = position - column * v.page_tokens;
+    const uint32_t page = (uint32_t)__ldg(v.table + (uint64_t)q.seq * v.columns + column);
+    if (page >= v.n_pages) {
+      if (lane == 0) report_table(v.ctr);
+      continue;
+    }
+    const uint64_t in = slot * p.token_step;
+    for (uint32_t u0 = 0; u0 < units; u0 += per * kUnroll) {
+      float x[kUnroll][8];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const uint32_t u = u0 + k * per + lane / lanes;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[k][j] = 0.f;
+        if (u < units && mine) {
+          const bool val = u >= heads;
+          const db_cache_rows& s = val ? p.v : p.k;
+          load8<Src>((const char*)s.base + r * s.row_stride + (val ? u - heads : u) * s.head_stride + at * sizeof(Src), x[k]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const uint32_t u = u0 + k * per + lane / lanes;
+        const bool val = u >= heads;
+        const uint32_t head = val ? u - heads : u;
+        char* const to = (char*)(val ? p.c.v : p.c.k) + page * (val ? p.c.v_stride : p.c.k_stride) + in + head * p.head_step;
+        if (kCodes) {
+          const uint32_t top = largest_bits(x[k], lanes);
+          float scale;
+          const uint2 w = quantise8<kType == DB_E4M3>(x[k], top, scale);
+          if (u < units && mine) {
+            *(uint2*)(to + at) = w;
+            if (at == 0) {
+              char* const s = (char*)(val ? p.c.v_scale : p.c.k_scale) + page * (val ? p.c.v_scale_stride : p.c.k_scale_stride);
+              ((float*)s)[slot * p.scale_token_step + head * p.scale_head_step] = scale;
+            }
+          }
+        } else if (u < units && mine) {
+          typedef typename std::conditional<kType == DB_F16, __half, __nv_bfloat16>::type H;
+          store8<H>(to + 2 * at, x[k]);
+        }
+      }
+    }
+  }
+}
+
+// Eight cached values.
+template <int kType>
+__device__ __forceinline__ void values8(const char* p, float scale, float* x) {
+  if (kType == DB_E4M3 || kType == DB_I8) {
+    const uint2 c = *(const uint2*)p;
+    const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (kType == DB_E4M3) {
+        const float2 a = unpack2<__half>(e4m3x2_to_f16x2(w[h])), b = unpack2<__half>(e4m3x2_to_f16x2(w[h] >> 16));
+        x[4 * h] = a.x * scale, x[4 * h + 1] = a.y * scale, x[4 * h + 2] = b.x * scale, x[4 * h + 3] = b.y * scale;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[4 * h + j] = (float)(int8_t)(w[h] >> (8 * j)) * scale;
+      }
+    }
+  } else {
+    load8<typename std::conditional<kType == DB_F16, __half, __nv_bfloat16>::type>(p, x);
+  }
+}
+
+template <typename Dst, int kType>
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const MoveParams p) {
+  constexpr bool kCodes = kType == DB_E4M3 || kType == DB_I8;
+  constexpr uint32_t kBytes = kCodes ? 1 : 2;
+  wait_for_prerequisites();
+  dependents_may_launch();
+  const CacheView& v = p.view;
+  const uint32_t lane = threadIdx.x & 31;
+  const uint64_t warp = (uint64_t)blockIdx.x * kWarps + threadIdx.x / 32;
+  report_requests(v, (uint64_t)blockIdx.x * kThreads + threadIdx.x, (uint64_t)gridDim.x * kThreads, false);
+  const uint64_t r0 = warp * p.chunk;
+  const uint32_t r1 = (uint32_t)min(r0 + p.chunk, (uint64_t)v.rows);
+  if (r0 >= r1) return;
+  const uint32_t lanes = p.lanes, at = (lane & (lanes - 1)) * 8, per = 32 / lanes;
+  const uint32_t heads = p.c.heads, units = 2 * heads;
+  const bool mine = at < p.c.width;
+  uint32_t i = find_request(v.start, v.n, (uint32_t)r0);
+  Request q = read_request(v, i, false);
+  uint32_t from = p.first && q.ok ? (uint32_t)__ldg(p.first + i) : 0;
+  for (uint32_t r = (uint32_t)r0; r < r1; ++r) {
+    while (i + 1 < v.n && (int32_t)r >= __ldg(v.start + i + 1)) {
+      q = read_request(v, ++i, false);
+      from = p.first && q.ok ? (uint32_t)__ldg(p.first + i) : 0;
+    }
+    if (!q.ok || r < q.first || r - q.first >= q.rows) continue;
+    const uint64_t position = (uint64_t)from + (r - q.first);
+    bool held = position < q.length;
+    uint32_t page = 0, slot = 0;
+    if (held) {
+      const uint32_t column = (uint32_t)position / v.page_tokens;
+      slot = (uint32_t)position - column * v.page_tokens;
+      page = (uint32_t)__ldg(v.table + (uint64_t)q.seq * v.columns + column);
+      if (page >= v.n_pages) {
+        held = false;
+        if (lane == 0) report_table(v.ctr);
+      }
+    }
+    const uint64_t in = slot * p.token_step;
+    for (uint32_t u0 = 0; u0 < units; u0 += per * kUnroll) {
+      float x[kUnroll][8];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const uint32_t u = u0 + k * per + lane / lanes;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[k][j] = 0.f;
+        if (u < units && mine && held) {
+          const bool val = u >= heads;
+          const uint32_t head = val ? u - heads : u;
+          float scale = 1.f;
+          if (kCodes) {
+            const char* const s = (const char*)(val ? p.c.v_scale : p.c.k_scale) + page * (val ? p.c.v_scale_stride : p.c.k_scale_stride);
+            scale = ((const float*)s)[slot * p.scale_token_step + head * p.scale_head_step];
+          }
+          values8<kType>((const char*)(val ? p.c.v : p.c.k) + page * (val ? p.c.v_stride : p.c.k_stride) + in + head * p.head_step + at * kBytes, scale, x[k]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const uint32_t u = u0 + k * per + lane / lanes;
+        if (u < units && mine) {
+          const bool val = u >= heads;
+          const db_cache_rows& d = val ? p.v : p.k;
+          store8<Dst>((char*)d.base + r * d.row_stride + (val ? u - heads : u) * d.head_stride + at * sizeof(Dst), x[k]);
+        }
+      }
+    }
+  }
+}
+
+MoveParams move_params(const CacheView& v, const db_cache_layer* c, const db_cache_rows* k,
+                       const db_cache_rows* vals) {
+  MoveParams p = {};
+  p.view = v;
+  p.c = *c;
+  p.k = *k;
+  p.v = *vals;
+  const uint64_t row = (uint64_t)c->width * item_bytes(c->type);
+  p.token_step = c->heads_first ? row : c->heads * row;
+  p.head_step = c->heads_first ? v.page_tokens * row : row;
+  p.scale_token_step = c->heads_first ? 1 : c->heads;
+  p.scale_head_step = c->heads_first ? v.page_tokens : 1;
+  p.lanes = 2;
+  while (p.lanes * 8 < c->width) p.lanes *= 2;
+  return p;
+}
+
+// A warp for each row up to 8 CTAs an SM (as many as are resident), then
+// neighbouring rows, whose places are neighbours too.
+int launch_move(void (*kernel)(MoveParams), MoveParams& p, cudaStream_t s) {
+  const uint64_t most = (uint64_t)8 * num_sms(), want = ((uint64_t)p.view.rows + kWarps - 1) / kWarps;
+  const uint64_t grid = want < 1 ? 1 : want < most ? want : most;
+  p.chunk = (uint32_t)((p.view.rows + grid * kWarps - 1) / (grid * kWarps));
+  if (!p.chunk) p.chunk = 1;
+  return launch_dependent(kernel, (unsigned)grid, kThreads, 0, s, p);
+}
+
+template <typename Row>
+void (*write_kernel(uint32_t type))(MoveParams) {
+  switch (type) {
+    case DB_BF16:
+      return cache_write_kernel<Row, DB_BF16>;
+    case DB_F16:
+      return cache_write_kernel<Row, DB_F16>;
+    case DB_E4M3:
+      return cache_write_kernel<Row, DB_E4M3>;
+    default:
+      return cache_write_kernel<Row, DB_I8>;
+  }
+}
+
+template <typename Row>
+void (*read_kernel(uint32_t type))(MoveParams) {
+  switch (type) {
+    case DB_BF16:
+      return cache_read_kernel<Row, DB_BF16>;
+    case DB_F16:
+      return cache_read_kernel<Row, DB_F16>;
+    case DB_E4M3:
+      return cache_read_kernel<Row, DB_E4M3>;
+    default:
+      return cache_read_kernel<Row, DB_I8>;
+  }
+}
+
+// ----------------------------------------------------------------------- keep
+constexpr uint32_t kKeepThreads = 128;
+
+struct KeepParams {
+  CacheView view;
+  const int32_t* path;
+  const int32_t* accepted;
+  db_page_pool pool;
+  uint32_t planes, segments, token_bytes;
+  uint64_t seg_bytes;
+  uint32_t vectors;  // of a token's run
+  uint32_t lanes;    // a power of two: threads of a run, which take vectors one after the other
+  db_page_cut* cut;
+};
+
+template <int kVec>
+struct Bytes;
+template <>
+struct Bytes<16> {
+  typedef uint4 type;
+};
+template <>
+struct Bytes<8> {
+  typedef uint2 type;
+};
+template <>
+struct Bytes<4> {
+  typedef uint32_t type;
+};
+template <>
+struct Bytes<2> {
+  typedef uint16_t type;
+};
+template <>
+struct Bytes<1> {
+  typedef uint8_t type;
+};
+
+// A CTA takes one request and every gridDim.y-th share of its planes and
+// segments. It lists the tokens that move (128 of the path at a time) in
+// shared memory; a thread then carries its bytes of a run through the list in
+// ascending order, 8 under way. A token goes to a place that is not above its
+// own, and places ascend, so nothing is overwritten before it has been read,
+// and no thread touches another one's bytes.
+template <int kVec>
+__global__ void __launch_bounds__(kKeepThreads) cache_keep_kernel(const KeepParams p) {
+  typedef typename Bytes<kVec>::type V;
+  __shared__ uint64_t s_src[kKeepThreads], s_dst[kKeepThreads];
+  __shared__ uint32_t s_warp[kKeepThreads / 32];
+  wait_for_prerequisites();
+  dependents_may_launch();
+  const CacheView& v = p.view;
+  const uint32_t i = blockIdx.x, tid = threadIdx.x;
+  Request q = read_request(v, i, true);
+  const uint32_t kept = q.ok ? (uint32_t)__ldg(p.accepted + i) : 0;
+  bool ok = q.ok && kept <= q.rows;
+  if (ok) {  // the path ascends below the request's rows
+    bool bad = false;
+    for (uint32_t k = tid; k < kept; k += kKeepThreads) {
+      const int32_t x = __ldg(p.path + q.first + k);
+      bad |= x < 0 || (uint32_t)x >= q.rows || (k && x <= __ldg(p.path + q.first + k - 1));
+    }
+    ok = !__syncthreads_or(bad);
+  }
+  const uint32_t base = q.length - q.rows;
+  if (tid == 0 && blockIdx.y == 0) {
+    if (v.status) v.status[i] = ok ? DB_PAGE_OK : DB_PAGE_INVALID;
+    if (p.cut) p.cut[i] = db_page_cut{q.seq, ok ? base + kept : 0xFFFFFFFFu};
+    if (v.ctr) {
+      if (ok && q.rows) atomicAdd((unsigned long long*)&v.ctr->total, (unsigned long long)q.rows);
+      if (!ok) atomicAdd((unsigned long long*)&v.ctr->n_invalid, 1ull);
+    }
+  }
+  if (!ok) return;
+  const uint32_t runs = p.planes * p.segments, per = kKeepThreads / p.lanes;
+  const uint32_t lane = tid & (p.lanes - 1);
+  for (uint32_t k0 = 0; k0 < kept; k0 += kKeepThreads) {
+    const uint32_t k = k0 + tid;
+    bool moves = false;
+    uint64_t src = 0, dst = 0;
+    if (k < kept) {
+      const uint32_t x = (uint32_t)__ldg(p.path + q.first + k);
+      if (x != k) {
+        const uint32_t a = base + x, b = base + k, ca = a / v.page_tokens, cb = b / v.page_tokens;
+        const uint32_t pa = (uint32_t)__ldg(v.table + (uint64_t)q.seq * v.columns + ca);
+        const uint32_t pb = (uint32_t)__ldg(v.table + (uint64_t)q.seq * v.columns + cb);
+        moves = pa < v.n_pages && pb < v.n_pages;
+        if (!moves) report_table(v.ctr);
+        src = pa * p.pool.page_stride + (uint64_t)(a - ca * v.page_tokens) * p.token_bytes;
+        dst = pb * p.pool.page_stride + (uint64_t)(b - cb * v.page_tokens) * p.token_bytes;
+      }
+    }
+    uint32_t place, count;
+    block_excl_scan<kKeepThreads / 32>(moves, place, count, s_warp);
+    if (moves) {
+      s_src[place] = src;
+      s_dst[place] = dst;
+    }
+    __syncthreads();
+    if (count)
+      for (uint32_t run = blockIdx.y * per + tid / p.lanes; run < runs; run += gridDim.y * per) {
+        const uint32_t plane = run / p.segments, seg = run - plane * p.segments;
+        char* const at = (char*)p.pool.base + plane * p.pool.plane_stride + seg * p.seg_bytes;
+        for (uint32_t w = lane; w < p.vectors; w += p.lanes) {
+          char* const mine = at + (uint64_t)w * kVec;
+          for (uint32_t m0 = 0; m0 < count; m0 += 8) {
+            V x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (m0 + j < count) x[j] = *(const V*)(mine + s_src[m0 + j]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (m0 + j < count) *(V*)(mine + s_dst[m0 + j]) = x[j];
+          }
+        }
+      }
+    __syncthreads();
+  }
+}
+
+template <int kVec>
+int launch_keep(KeepParams& p, cudaStream_t s) {
+  p.vectors = p.token_bytes / kVec;
+  p.lanes = 1;
+  while (p.lanes < kKeepThreads && p.lanes < p.vectors) p.lanes *= 2;
+  const uint64_t per = kKeepThreads / p.lanes, all = ((uint64_t)p.planes * p.segments + per - 1) / per;
+  // CTAs for 8 an SM, a share of at least one run for each thread
+  const uint64_t most = ((uint64_t)8 * num_sms() + p.view.n - 1) / p.view.n;
+  uint64_t y = all < most ? all : most;
+  if (y > 65535) y = 65535;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.view.n, (unsigned)y);
+  cfg.blockDim = dim3(kKeepThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, cache_keep_kernel<kVec>, p);
+  if (e != cudaSuccess) return cuda_failure(e);
+  return launch_result();
+}
+
+}  // namespace
+}  // namespace db
+
+using namespace db;
+
+extern "C" int db_cache_write(const db_page_tables* t, const db_cache_batch* b, const db_cache_layer* c,
+                              const db_cache_rows* k, const db_cache_rows* v, uint32_t type,
+                              uint8_t* status, db_counters* ctr, void* stream) {
+  CacheView view;
+  if (check_cache(t, b, status, ctr, &view) || check_layer(t, c)) return -EINVAL;
+  if (check_rows(k, b->rows, c->heads, c->width, type, false) ||
+      check_rows(v, b->rows, c->heads, c->width, type, false))
+    return -EINVAL;
+  const cudaStream_t s = (cudaStream_t)stream;
+  if (const int e = zero_counters(ctr, s)) return e;
+  if (!b->n) return 0;
+  MoveParams p = move_params(view, c, k, v);
+  switch (type) {
+    case DB_BF16:
+      return launch_move(write_kernel<__nv_bfloat16>(c->type), p, s);
+    case DB_F16:
+      return launch_move(write_kernel<__half>(c->type), p, s);
+    default:
+      return launch_move(write_kernel<float>(c->type), p, s);
+  }
+}
+
+extern "C" int db_cache_read(const db_page_tables* t, const db_cache_batch* b, const int32_t* first,
+                             const db_cache_layer* c, const db_cache_rows* k, const db_cache_rows* v,
+                             uint32_t type, uint8_t* status, db_counters* ctr, void* stream) {
+  CacheView view;
+  if (check_cache(t, b, status, ctr, &view) || check_layer(t, c) || !aligned(first, 4)) return -EINVAL;
+  if (check_rows(k, b->rows, c->heads, c->width, type, true) ||
+      check_rows(v, b->rows, c->heads, c->width, type, true))
+    return -EINVAL;
+  const cudaStream_t s = (cudaStream_t)stream;
+  if (const int e = zero_counters(ctr, s)) return e;
+  if (!b->n) return 0;
+  MoveParams p = move_params(view, c, k, v);
+  p.first = first;
+  switch (type) {
+    case DB_BF16:
+      return launch_move(read_kernel<__nv_bfloat16>(c->type), p, s);
+    case DB_F16:
+      return launch_move(read_kernel<__half>(c->type), p, s);
+    default:
+      return launch_move(read_kernel<float>(c->type), p, s);
+  }
+}
+
+extern "C" int db_cache_keep(const db_page_tables* t, const db_cache_batch* b, const int32_t* path,
+                             const int32_t* accepted, const db_page_pool* pool,
+                             const db_page_shape* shape, db_page_cut* cut, uint8_t* status,
+                             db_counters* ctr, void* stream) {
+  CacheView view;
+  if (check_cache(t, b, status, ctr, &view)) return -EINVAL;
+  if (!pool || !shape || !pool->base || !shape->planes || !shape->segments || !shape->token_bytes)
+    return -EINVAL;
+  const uint64_t limit = 1ull << 31, rows = (uint64_t)shape->segments * shape->page_tokens;
+  if (shape->page_tokens != t->page_tokens || shape->planes > 65536 || rows > limit) return -EINVAL;
+  const uint64_t page_bytes = rows * shape->token_bytes;
+  if (page_bytes > limit || page_bytes * shape->planes > limit) return -EINVAL;
+  if (pool->n_pages < t->n_pages || pool->n_pages > 0xFFFFFFFFull) return -EINVAL;
+  if (pool->n_pages > 1 && pool->page_stride < page_bytes) return -EINVAL;
+  if (shape->planes > 1 && pool->plane_stride < page_bytes) return -EINVAL;
+  if (!aligned(path, 4) || !aligned(accepted, 4) || !aligned(cut, 8)) return -EINVAL;
+  if (b->n && (!accepted || (b->rows && !path))) return -EINVAL;
+  const cudaStream_t s = (cudaStream_t)stream;
+  if (const int e = zero_counters(ctr, s)) return e;
+  if (!b->n) return 0;
+  KeepParams p = {};
+  p.view = view;
+  p.path = path;
+  p.accepted = accepted;
+  p.pool = *pool;
+  p.planes = shape->planes;
+  p.segments = shape->segments;
+  p.token_bytes = shape->token_bytes;
+  p.seg_bytes = (uint64_t)shape->page_tokens * shape->token_bytes;
+  p.cut = cut;
+  // Every run starts on a multiple of the lowest set bit of all of these.
+  uint64_t all = (uint64_t)(uintptr_t)pool->base | p.token_bytes;
+  if (p.planes > 1) all |= pool->plane_stride;
+  if (pool->n_pages > 1) all |= pool->page_stride;
+  if (!(all & 15)) return launch_keep<16>(p, s);
+  if (!(all & 7)) return launch_keep<8>(p, s);
+  if (!(all & 3)) return launch_keep<4>(p, s);
+  if (!(all & 1)) return launch_keep<2>(p, s);
+  return launch_keep<1>(p, s);
+}
