@@ -12,7 +12,7 @@ constexpr size_t kHeader = 4096;  // arrival counters, of up to 1,024 CTAs
 uint32_t padded_width(uint32_t width) { return width <= 64 ? 64 : width <= 128 ? 128 : 256; }
 
 // Blocks of 16 query rows of an item.
-uint32_t blocks_for(uint64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+uint32_t blocks_for(uint64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : kManyBlocks; }
 
 unsigned grid_of() {
   const unsigned g = kAttnCtasPerSm * (unsigned)num_sms();

@@ -20,6 +20,8 @@ constexpr uint32_t kTile = 64;             // tokens of a unit
 constexpr uint32_t kAttnThreads = 128;
 constexpr uint32_t kAttnCtasPerSm = 2;     // most CTAs an SM of the grid
 constexpr uint32_t kMaxGroup = 64;
+constexpr uint32_t kScaleSlack = 4;        // a larger exponent of scales is followed from here on
+constexpr uint32_t kManyBlocks = 8;       // blocks of 16 query rows of the tcgen05 kernel's items
 
 struct AttnParams {
   CacheView view;
@@ -137,6 +139,28 @@ __device__ __forceinline__ uint32_t owner_of(const Share& s, uint64_t x) {
 }
 
 // ------------------------------------------------------------ small operations
+__device__ __forceinline__ float exp2_of(float x);
+
+// Four values of a row from the parts that CTAs c0 to c1 left, in their order.
+template <uint32_t kRows, uint32_t kPad>
+__device__ __forceinline__ float4 join_parts(const AttnParams& p, uint32_t c0, uint32_t c1, uint32_t row, uint32_t quad,
+                                             float& m, float& l) {
+  m = -INFINITY;
+  l = 0.f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (uint32_t k = c0; k <= c1; ++k) {
+    const float* const at = p.partial + (uint64_t)(2 * k + (k == c0)) * partial_floats(kRows, kPad);
+    const float mk = __ldcg(at + kRows * kPad + row), lk = __ldcg(at + kRows * kPad + kRows + row);
+    const float4 y = __ldcg((const float4*)(at + row * kPad) + quad);
+    const float now = fmaxf(m, mk), by = now == -INFINITY ? 0.f : now;
+    const float a = exp2_of(m - by), b = exp2_of(mk - by);
+    l = l * a + lk * b;
+    v.x = v.x * a + y.x * b, v.y = v.y * a + y.y * b, v.z = v.z * a + y.z * b, v.w = v.w * a + y.w * b;
+    m = now;
+  }
+  return v;
+}
+
 __device__ __forceinline__ float exp2_of(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -253,14 +277,14 @@ struct Few {
 template <typename T, uint32_t kPad, bool kCodes, uint32_t kBlocks>
 __global__ void __launch_bounds__(kAttnThreads, kPad > 128 ? 1 : 2) attention_few_kernel(const AttnParams p) {
   typedef Few<T, kPad, kCodes, kBlocks> F;
-  typedef typename std::conditional<kCodes, __nv_bfloat16, T>::type W;  // of weights and values
+  typedef typename std::conditional<kCodes, __half, T>::type W;  // of weights and values
   constexpr uint32_t kChunks = kPad / 8;                 // 16-byte chunks of a 16-bit row
   constexpr uint32_t kRawChunks = kCodes ? kPad / 16 : kPad / 8;
   constexpr uint32_t kTokens = F::kTokens, kN = kTokens / 8, kSteps = kPad / 16;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int2 s_place[F::kRing][kTile];  // page (or -1) and byte offset in it of a tile's tokens
   __shared__ float s_max[4][16], s_sum[4][16];
-  __shared__ uint32_t s_broken, s_last;
+  __shared__ uint32_t s_broken, s_last, s_exponent[2];
   wait_for_prerequisites();
   dependents_may_launch();
   const uint32_t tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
@@ -390,6 +414,7 @@ __global__ void __launch_bounds__(kAttnThreads, kPad > 128 ? 1 : 2) attention_fe
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[d][k] = 0.f;
     float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+    uint32_t exponent = 127;  // of the values' scales so far, which the weights of codes have as a factor
 
     for (uint32_t t = t0; t < t1; ++t) {
       copies_wait<F::kStages - 2>();
@@ -404,7 +429,13 @@ __global__ void __launch_bounds__(kAttnThreads, kPad > 128 ? 1 : 2) attention_fe
         scales = all;
         // keys' scales take the call's own factor along; an infinite one
         // stands for values of both signs, whose products have no sum
-        if (tid < kTile) all[tid] = __fmaf_rn(all[tid], 0.f, all[tid]) * p.scale_log2;
+        if (tid < kTile) {
+          all[tid] = __fmaf_rn(all[tid], 0.f, all[tid]) * p.scale_log2;
+        } else {
+          const uint32_t ex = (__float_as_uint(all[tid]) >> 23) & 0xFFu;
+          const uint32_t largest = __reduce_max_sync(kFull, ex == 0xFFu ? 0u : ex);
+          if (lane == 0) s_exponent[warp & 1] = largest;
+        }
 #pragma unroll
         for (uint32_t k = 0; k < 2 * kTile * kRawChunks / kAttnThreads; ++k) {
           const uint32_t c = tid + k * kAttnThreads;  // first the keys, then the values
@@ -489,15 +520,24 @@ __global__ void __launch_bounds__(kAttnThreads, kPad > 128 ? 1 : 2) attention_fe
         m[0] = fmaxf(m[0], fmaxf(s[b][0], s[b][1]));
         m[1] = fmaxf(m[1], fmaxf(s[b][2], s[b][3]));
       }
+      // Weights are exp2(score - ref): ref is the maximum, and for codes also
+      // takes in the size of the values' scales, so that weights times scales
+      // stay in the middle of f16's range.
       float less[2];
+      uint32_t ex = 127;
+      if (kCodes) {
+        ex = min(max(max(s_exponent[0], s_exponent[1]), 31u), 227u);
+        ex = t == t0 || ex > exponent + kScaleSlack ? ex : exponent;
+      }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         m[k] = fmaxf(m[k], __shfl_xor_sync(kFull, m[k], 1));
         m[k] = fmaxf(m[k], __shfl_xor_sync(kFull, m[k], 2));
-        less[k] = m[k] == -INFINITY ? 0.f : m[k];
+        less[k] = m[k] == -INFINITY ? 0.f : m[k] + (float)((int)ex - 127);
       }
-      if (__any_sync(kFull, m[0] != top[0] || m[1] != top[1])) {
-        const float a0 = exp2_of(top[0] - less[0]), a1 = exp2_of(top[1] - less[1]);
+      if (__any_sync(kFull, m[0] != top[0] || m[1] != top[1]) || ex != exponent) {
+        const float before = (float)((int)exponent - 127);
+        const float a0 = exp2_of(top[0] + before - less[0]), a1 = exp2_of(top[1] + before - less[1]);
         sum[0] *= a0;
         sum[1] *= a1;
 #pragma unroll
@@ -509,6 +549,7 @@ __global__ void __launch_bounds__(kAttnThreads, kPad > 128 ? 1 : 2) attention_fe
         }
         top[0] = m[0];
         top[1] = m[1];
+        exponent = ex;
       }
 #pragma unroll
       for (uint32_t b = 0; b < kN; ++b)
@@ -579,6 +620,7 @@ __global__ void __launch_bounds__(kAttnThreads, kPad > 128 ? 1 : 2) attention_fe
     for (int k = 0; k < 2; ++k) {
       sum[k] += __shfl_xor_sync(kFull, sum[k], 1);
       sum[k] += __shfl_xor_sync(kFull, sum[k], 2);
+      top[k] += (float)((int)exponent - 127);  // the reference of what was summed
       if ((lane & 3) == 0) s_max[warp][lane / 4 + 8 * k] = top[k];
     }
     copies_wait<0>();
@@ -658,18 +700,8 @@ __global__ void __launch_bounds__(kAttnThreads, kPad > 128 ? 1 : 2) attention_fe
         __threadfence();
         for (uint32_t c = tid; c < rows * kQuads; c += kAttnThreads) {
           const uint32_t row = c / kQuads, quad = c % kQuads;
-          float m = -INFINITY, l = 0.f;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (uint32_t k = c0; k <= c1; ++k) {
-            const float* const part_at = p.partial + (uint64_t)(2 * k + (k == c0)) * partial_floats(F::kRows, kPad);
-            const float mk = __ldcg(part_at + F::kRows * kPad + row), lk = __ldcg(part_at + F::kRows * kPad + F::kRows + row);
-            const float4 y = __ldcg((const float4*)(part_at + row * kPad) + quad);
-            const float now = fmaxf(m, mk), by = now == -INFINITY ? 0.f : now;
-            const float a = exp2_of(m - by), b = exp2_of(mk - by);
-            l = l * a + lk * b;
-            v.x = v.x * a + y.x * b, v.y = v.y * a + y.y * b, v.z = v.z * a + y.z * b, v.w = v.w * a + y.w * b;
-            m = now;
-          }
+          float m, l;
+          const float4 v = join_parts<F::kRows, kPad>(p, c0, c1, row, quad, m, l);
           answer(row, quad, m, l, v);
         }
       }
@@ -692,21 +724,9 @@ int launch_blocks(const AttnParams& p, uint32_t blocks, unsigned grid, cudaStrea
   switch (blocks) {
     case 1:
       return launch_few<T, kPad, kCodes, 1>(p, grid, s);
-    case 2:
-      return launch_few<T, kPad, kCodes, 2>(p, grid, s);
     default:
-      return launch_few<T, kPad, kCodes, 4>(p, grid, s);
+      return launch_few<T, kPad, kCodes, 2>(p, grid, s);
   }
-}
-
-template <uint32_t kPad>
-int launch_attention(const AttnParams& p, uint32_t type, uint32_t blocks, unsigned grid, cudaStream_t s) {
-  const bool codes = item_bytes(p.c.type) == 1;
-  if (type == DB_BF16)
-    return codes ? launch_blocks<__nv_bfloat16, kPad, true>(p, blocks, grid, s)
-                 : launch_blocks<__nv_bfloat16, kPad, false>(p, blocks, grid, s);
-  return codes ? launch_blocks<__half, kPad, true>(p, blocks, grid, s)
-               : launch_blocks<__half, kPad, false>(p, blocks, grid, s);
 }
 
 }  // namespace db

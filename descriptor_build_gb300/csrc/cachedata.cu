@@ -61,7 +61,6 @@ int zero_counters(db_counters* ctr, cudaStream_t s) {
 namespace {
 
 constexpr uint32_t kThreads = 256, kWarps = kThreads / 32;
-constexpr int kUnroll = 4;  // heads' rows of a lane under way
 
 struct MoveParams {
   CacheView view;
@@ -74,16 +73,30 @@ struct MoveParams {
   uint32_t scale_token_step, scale_head_step;  // floats
 };
 
-// Eight values of a row outside the cache.
+// Eight values of a row, as they lie in memory.
 template <typename T>
-__device__ __forceinline__ void load8(const char* p, float* x) {
+struct Eight {
+  uint4 w[sizeof(T) / 2];
+};
+
+template <typename T>
+__device__ __forceinline__ Eight<T> load8(const char* p) {
+  Eight<T> e;
+#pragma unroll
+  for (uint32_t j = 0; j < sizeof(T) / 2; ++j) e.w[j] = __ldcs((const uint4*)p + j);
+  return e;
+}
+
+template <typename T>
+__device__ __forceinline__ void floats8(const Eight<T>& e, float* x) {
   if (sizeof(T) == 4) {
-    const float4 a = __ldcs((const float4*)p), b = __ldcs((const float4*)p + 1);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+#pragma unroll
+    for (uint32_t j = 0; j < sizeof(T) / 2; ++j) {
+      x[4 * j] = __uint_as_float(e.w[j].x), x[4 * j + 1] = __uint_as_float(e.w[j].y);
+      x[4 * j + 2] = __uint_as_float(e.w[j].z), x[4 * j + 3] = __uint_as_float(e.w[j].w);
+    }
   } else {
-    const uint4 a = __ldcs((const uint4*)p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+    const uint32_t w[4] = {e.w[0].x, e.w[0].y, e.w[0].z, e.w[0].w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float2 f = unpack2<typename std::conditional<sizeof(T) == 4, __half, T>::type>(w[j]);
@@ -155,10 +168,39 @@ __device__ __forceinline__ uint2 quantise8(const float* x, uint32_t top, float& 
   return make_uint2(w[0], w[1]);
 }
 
-// One warp: rows [r0, r1) of the batch. kType: what the pages hold.
+// Where a row of the batch has its token: found one row ahead of the data, so
+// that the table's answer is there when the loads before it are.
+struct Place {
+  uint32_t page, slot;
+  bool held;  // it has one
+};
+
+// The row's request is the one it is in, or a later one; `i` and `q` follow.
+// `position`: of a valid request's row.
+template <typename F>
+__device__ __forceinline__ Place find_place(const CacheView& v, uint32_t r, uint32_t& i, Request& q,
+                                            bool& mine, bool fresh, F position) {
+  while (i + 1 < v.n && (int32_t)r >= __ldg(v.start + i + 1)) q = read_request(v, ++i, fresh);
+  mine = q.ok && r >= q.first && r - q.first < q.rows;
+  Place w = {0, 0, false};
+  if (mine) {
+    const uint64_t at = position(i, q, r - q.first);
+    if (at < q.length) {
+      const uint32_t column = (uint32_t)at / v.page_tokens;
+      w.slot = (uint32_t)at - column * v.page_tokens;
+      w.page = (uint32_t)__ldg(v.table + (uint64_t)q.seq * v.columns + column);
+      w.held = true;
+    }
+  }
+  return w;
+}
+
+// One warp: rows [r0, r1) of the batch. kType: what the pages hold; kUnroll:
+// heads' rows of a lane under way.
 template <typename Src, int kType>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const MoveParams p) {
   constexpr bool kCodes = kType == DB_E4M3 || kType == DB_I8;
+  constexpr int kUnroll = sizeof(Src) == 4 ? 4 : 8;
   wait_for_prerequisites();
   dependents_may_launch();
   const CacheView& v = p.view;
@@ -171,63 +213,79 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const MoveParams 
   const uint32_t lanes = p.lanes, at = (lane & (lanes - 1)) * 8, per = 32 / lanes;
   const uint32_t heads = p.c.heads, units = 2 * heads;
   const bool mine = at < p.c.width;
+  const auto position = [&](uint32_t, const Request& q, uint32_t j) { return (uint64_t)q.length - q.rows + j; };
   uint32_t i = find_request(v.start, v.n, (uint32_t)r0);
   Request q = read_request(v, i, true);
+  bool has;
+  Place w = find_place(v, (uint32_t)r0, i, q, has, true, position);
   for (uint32_t r = (uint32_t)r0; r < r1; ++r) {
-    while (i + 1 < v.n && (int32_t)r >= __ldg(v.start + i + 1)) q = read_request(v, ++i, true);
-    if (!q.ok || r < q.first || r - q.first >= q.rows) continue;
-    const uint32_t position = q.length - q.rows + (r - q.first);
-    const uint32_t column = position / v.page_tokens, slot = position - column * v.page_tokens;
-    const uint32_t page = (uint32_t)__ldg(v.table + (uint64_t)q.seq * v.columns + column);
-    if (page >= v.n_pages) {
-      if (lane == 0) report_table(v.ctr);
-      continue;
-    }
-    const uint64_t in = slot * p.token_step;
+    Place now = w;
+    const bool go = has;
+    bool looked = false;
     for (uint32_t u0 = 0; u0 < units; u0 += per * kUnroll) {
-      float x[kUnroll][8];
+      Eight<Src> e[kUnroll];
+      if (go) {
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        const uint32_t u = u0 + k * per + lane / lanes;
+        for (int k = 0; k < kUnroll; ++k) {
+          const uint32_t u = u0 + k * per + lane / lanes;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[k][j] = 0.f;
-        if (u < units && mine) {
-          const bool val = u >= heads;
-          const db_cache_rows& s = val ? p.v : p.k;
-          load8<Src>((const char*)s.base + r * s.row_stride + (val ? u - heads : u) * s.head_stride + at * sizeof(Src), x[k]);
+          for (uint32_t j = 0; j < sizeof(Src) / 2; ++j) e[k].w[j] = make_uint4(0, 0, 0, 0);
+          if (u < units && mine) {
+            const bool val = u >= heads;
+            const db_cache_rows& s = val ? p.v : p.k;
+            e[k] = load8<Src>((const char*)s.base + r * s.row_stride + (val ? u - heads : u) * s.head_stride + at * sizeof(Src));
+          }
         }
       }
+      if (!looked) {
+        looked = true;
+        if (r + 1 < r1) w = find_place(v, r + 1, i, q, has, true, position);
+        if (go && now.held && now.page >= v.n_pages) {
+          now.held = false;
+          if (lane == 0) report_table(v.ctr);
+        }
+      }
+      if (!go) break;
+      const uint64_t in = now.slot * p.token_step;
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) {
+        if (u0 + k * per >= units) break;
         const uint32_t u = u0 + k * per + lane / lanes;
         const bool val = u >= heads;
         const uint32_t head = val ? u - heads : u;
-        char* const to = (char*)(val ? p.c.v : p.c.k) + page * (val ? p.c.v_stride : p.c.k_stride) + in + head * p.head_step;
+        char* const to = (char*)(val ? p.c.v : p.c.k) + now.page * (val ? p.c.v_stride : p.c.k_stride) + in + head * p.head_step;
+        float x[8];
+        floats8(e[k], x);
+        const bool out = u < units && mine && now.held;
         if (kCodes) {
-          const uint32_t top = largest_bits(x[k], lanes);
+          const uint32_t top = largest_bits(x, lanes);
           float scale;
-          const uint2 w = quantise8<kType == DB_E4M3>(x[k], top, scale);
-          if (u < units && mine) {
-            *(uint2*)(to + at) = w;
+          const uint2 c = quantise8<kType == DB_E4M3>(x, top, scale);
+          if (out) {
+            *(uint2*)(to + at) = c;
             if (at == 0) {
-              char* const s = (char*)(val ? p.c.v_scale : p.c.k_scale) + page * (val ? p.c.v_scale_stride : p.c.k_scale_stride);
-              ((float*)s)[slot * p.scale_token_step + head * p.scale_head_step] = scale;
+              char* const s = (char*)(val ? p.c.v_scale : p.c.k_scale) + now.page * (val ? p.c.v_scale_stride : p.c.k_scale_stride);
+              ((float*)s)[now.slot * p.scale_token_step + head * p.scale_head_step] = scale;
             }
           }
-        } else if (u < units && mine) {
+        } else if (out) {
           typedef typename std::conditional<kType == DB_F16, __half, __nv_bfloat16>::type H;
-          store8<H>(to + 2 * at, x[k]);
+          store8<H>(to + 2 * at, x);
         }
       }
     }
   }
 }
 
-// Eight cached values.
+// Eight cached values, as they lie in memory and as floats.
 template <int kType>
-__device__ __forceinline__ void values8(const char* p, float scale, float* x) {
-  if (kType == DB_E4M3 || kType == DB_I8) {
-    const uint2 c = *(const uint2*)p;
+struct Held {
+  typedef typename std::conditional<kType == DB_E4M3 || kType == DB_I8, uint2, uint4>::type type;
+};
+
+template <int kType>
+__device__ __forceinline__ void held_floats(const typename Held<kType>::type& c, float scale, float* x) {
+  if constexpr (kType == DB_E4M3 || kType == DB_I8) {
     const uint32_t w[2] = {c.x, c.y};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -240,7 +298,10 @@ __device__ __forceinline__ void values8(const char* p, float scale, float* x) {
       }
     }
   } else {
-    load8<typename std::conditional<kType == DB_F16, __half, __nv_bfloat16>::type>(p, x);
+    typedef typename std::conditional<kType == DB_F16, __half, __nv_bfloat16>::type H;
+    Eight<H> e;
+    e.w[0] = c;
+    floats8(e, x);
   }
 }
 
@@ -248,6 +309,8 @@ template <typename Dst, int kType>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const MoveParams p) {
   constexpr bool kCodes = kType == DB_E4M3 || kType == DB_I8;
   constexpr uint32_t kBytes = kCodes ? 1 : 2;
+  constexpr int kUnroll = 8;
+  typedef typename Held<kType>::type V;
   wait_for_prerequisites();
   dependents_may_launch();
   const CacheView& v = p.view;
@@ -260,53 +323,54 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const MoveParams p
   const uint32_t lanes = p.lanes, at = (lane & (lanes - 1)) * 8, per = 32 / lanes;
   const uint32_t heads = p.c.heads, units = 2 * heads;
   const bool mine = at < p.c.width;
+  const auto position = [&](uint32_t i, const Request&, uint32_t j) {
+    return (uint64_t)(p.first ? (uint32_t)__ldg(p.first + i) : 0) + j;
+  };
   uint32_t i = find_request(v.start, v.n, (uint32_t)r0);
   Request q = read_request(v, i, false);
-  uint32_t from = p.first && q.ok ? (uint32_t)__ldg(p.first + i) : 0;
+  bool has;
+  Place w = find_place(v, (uint32_t)r0, i, q, has, false, position);
   for (uint32_t r = (uint32_t)r0; r < r1; ++r) {
-    while (i + 1 < v.n && (int32_t)r >= __ldg(v.start + i + 1)) {
-      q = read_request(v, ++i, false);
-      from = p.first && q.ok ? (uint32_t)__ldg(p.first + i) : 0;
+    Place now = w;
+    const bool go = has;
+    if (now.held && now.page >= v.n_pages) {
+      now.held = false;
+      if (lane == 0) report_table(v.ctr);
     }
-    if (!q.ok || r < q.first || r - q.first >= q.rows) continue;
-    const uint64_t position = (uint64_t)from + (r - q.first);
-    bool held = position < q.length;
-    uint32_t page = 0, slot = 0;
-    if (held) {
-      const uint32_t column = (uint32_t)position / v.page_tokens;
-      slot = (uint32_t)position - column * v.page_tokens;
-      page = (uint32_t)__ldg(v.table + (uint64_t)q.seq * v.columns + column);
-      if (page >= v.n_pages) {
-        held = false;
-        if (lane == 0) report_table(v.ctr);
-      }
-    }
-    const uint64_t in = slot * p.token_step;
+    bool looked = false;
     for (uint32_t u0 = 0; u0 < units; u0 += per * kUnroll) {
-      float x[kUnroll][8];
+      V c[kUnroll];
+      float scale[kUnroll];
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) {
         const uint32_t u = u0 + k * per + lane / lanes;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[k][j] = 0.f;
-        if (u < units && mine && held) {
+        c[k] = V{};
+        scale[k] = 1.f;
+        if (go && u < units && mine && now.held) {
           const bool val = u >= heads;
           const uint32_t head = val ? u - heads : u;
-          float scale = 1.f;
+          c[k] = __ldcs((const V*)((const char*)(val ? p.c.v : p.c.k) + now.page * (val ? p.c.v_stride : p.c.k_stride) +
+                                   now.slot * p.token_step + head * p.head_step + at * kBytes));
           if (kCodes) {
-            const char* const s = (const char*)(val ? p.c.v_scale : p.c.k_scale) + page * (val ? p.c.v_scale_stride : p.c.k_scale_stride);
-            scale = ((const float*)s)[slot * p.scale_token_step + head * p.scale_head_step];
+            const char* const s = (const char*)(val ? p.c.v_scale : p.c.k_scale) + now.page * (val ? p.c.v_scale_stride : p.c.k_scale_stride);
+            scale[k] = ((const float*)s)[now.slot * p.scale_token_step + head * p.scale_head_step];
           }
-          values8<kType>((const char*)(val ? p.c.v : p.c.k) + page * (val ? p.c.v_stride : p.c.k_stride) + in + head * p.head_step + at * kBytes, scale, x[k]);
         }
       }
+      if (!looked) {
+        looked = true;
+        if (r + 1 < r1) w = find_place(v, r + 1, i, q, has, false, position);
+      }
+      if (!go) break;
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) {
         const uint32_t u = u0 + k * per + lane / lanes;
         if (u < units && mine) {
           const bool val = u >= heads;
           const db_cache_rows& d = val ? p.v : p.k;
-          store8<Dst>((char*)d.base + r * d.row_stride + (val ? u - heads : u) * d.head_stride + at * sizeof(Dst), x[k]);
+          float x[8];
+          held_floats<kType>(c[k], scale[k], x);
+          store8<Dst>((char*)d.base + r * d.row_stride + (val ? u - heads : u) * d.head_stride + at * sizeof(Dst), x);
         }
       }
     }
@@ -330,10 +394,10 @@ MoveParams move_params(const CacheView& v, const db_cache_layer* c, const db_cac
   return p;
 }
 
-// A warp for each row up to 8 CTAs an SM (as many as are resident), then
+// A warp for each row up to 24 CTAs an SM, several times what is resident, then
 // neighbouring rows, whose places are neighbours too.
 int launch_move(void (*kernel)(MoveParams), MoveParams& p, cudaStream_t s) {
-  const uint64_t most = (uint64_t)8 * num_sms(), want = ((uint64_t)p.view.rows + kWarps - 1) / kWarps;
+  const uint64_t most = (uint64_t)24 * num_sms(), want = ((uint64_t)p.view.rows + kWarps - 1) / kWarps;
   const uint64_t grid = want < 1 ? 1 : want < most ? want : most;
   p.chunk = (uint32_t)((p.view.rows + grid * kWarps - 1) / (grid * kWarps));
   if (!p.chunk) p.chunk = 1;

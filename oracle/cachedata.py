@@ -134,31 +134,33 @@ def attend(b: Batch, q, keys, vals, scale, mask=None):
             continue
         s, first, m, n = r
         places = [b.place(s, x) for x in range(n)]
+        there = np.array([p is not None for p in places], bool)
+        at = np.array([p if p is not None else (0, 0) for p in places], np.int64).reshape(n, 2)
+        k, v = keys[at[:, 0], at[:, 1]].astype(np.float64), vals[at[:, 0], at[:, 1]].astype(np.float64)
+        own = np.arange(n) - (n - m)
         for j in range(m):
-            own = np.arange(n) - (n - m)
             if mask is None:
                 sees = own <= j
             else:
-                bits = [(int(mask[first + j, o // 32]) >> (o % 32)) & 1 if o >= 0 else 1 for o in own]
-                sees = np.array(bits, bool)
-            at = [p for p, y in zip(places, sees) if y and p is not None]
+                bits = [(int(mask[first + j, o // 32]) >> (o % 32)) & 1 for o in range(m)]
+                sees = np.concatenate([np.ones(n - m, bool), np.array(bits, bool)])
+            sees = sees & there
             for x in range(q_heads):
                 where = (first + j, x)
-                if not at:
+                if not sees.any():
                     out[where], lse[where], spread[where], size[where] = 0, -np.inf, 0, 0
                     continue
-                k = np.stack([keys[p][x // group] for p in at]).astype(np.float64)
-                v = np.stack([vals[p][x // group] for p in at]).astype(np.float64)
+                kk, vv, qq = k[sees, x // group], v[sees, x // group], q[where].astype(np.float64)
                 with np.errstate(invalid="ignore", over="ignore"):
-                    sc = (k @ q[where].astype(np.float64)) * scale
-                    size[where] = np.nanmax(np.abs(k) @ np.abs(q[where].astype(np.float64))) * abs(scale)
+                    sc = (kk @ qq) * scale
+                    size[where] = np.nanmax(np.abs(kk) @ np.abs(qq)) * abs(scale)
                     top = sc.max()
                     if top == -np.inf:
                         out[where], lse[where], spread[where] = 0, -np.inf, 0
                         continue
                     w = np.exp(sc - top)
-                    out[where] = (w @ v) / w.sum()
-                    spread[where] = (w @ np.abs(v)) / w.sum()
+                    out[where] = (w @ vv) / w.sum()
+                    spread[where] = (w @ np.abs(vv)) / w.sum()
                     lse[where] = top + np.log(w.sum())
     return out, lse, spread, size
 

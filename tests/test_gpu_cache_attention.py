@@ -92,6 +92,7 @@ class Case:
         got, got_lse = out.cpu().double().numpy(), lse.cpu().double().numpy()
         assert (got[~rows] == 7).all() and (got_lse[~rows] == 7).all()  # as they were
         n, width = int(self.t.length.max()), self.q.shape[2]
+        spread, size = np.nan_to_num(spread, nan=np.inf), np.nan_to_num(size, nan=np.inf)
         e_p = 2 * (width + 8) * 2.0**-24 * size[..., None] + 2.0**-20
         coded = self.kind in ("i8", "e4m3")
         u_w = HALF["bf16"] if coded else HALF[self.qk]
@@ -156,6 +157,23 @@ def test_shapes(shape):
 def test_long_cache_is_cut_over_the_whole_gpu():
     Case("e4m3", "bf16", 1, 16, 1, 2, 64, [(30000, 1), (7, 1)], None).run()
     Case("bf16", "bf16", 1, 16, 1, 4, 128, [(9000, 6), (100, 2)], "tree").run()
+
+
+DEEP = [
+    ("bf16", "bf16", 1, 16, 4, 4, 128, [(6000, 20), (3000, 33), (90, 9)], "tree"),
+    ("i8", "f16", 2, 48, 2, 8, 112, [(9000, 20), (5000, 61)], "tree"),
+    ("e4m3", "bf16", 1, 16, 8, 8, 64, [(20000, 16)], None),
+    ("f16", "f16", 1, 7, 8, 5, 48, [(3000, 40), (2500, 9), (3, 3)], "random"),
+    ("e4m3", "f16", 1, 64, 2, 4, 256, [(12000, 30)], "tree"),
+    ("bf16", "bf16", 2, 128, 3, 8, 192, [(8000, 12), (777, 20)], "random"),
+    ("i8", "bf16", 1, 33, 16, 3, 32, [(1500, 13), (1400, 11), (1300, 12), (0, 30)], "tree"),
+]
+
+
+@pytest.mark.parametrize("shape", DEEP, ids=[f"{i}-{s[0]}-{s[1]}-{s[6]}" for i, s in enumerate(DEEP)])
+def test_many_tiles_of_many_rows(shape):
+    """Several tiles and items for each CTA, so that every ring wraps."""
+    Case(*shape, spare=1).run()
 
 
 def test_many_requests():
