@@ -134,42 +134,24 @@ __device__ __forceinline__ Share plan_share(const AttnParams& p) {
 }
 
 // The CTA that has unit x.
-__device__ __forceinline__ uint32_t owner_of(const Share& s, uint64_t x) {
+static __device__ __noinline__ uint32_t owner_of(const Share& s, uint64_t x) {
   return (uint32_t)(((x + 1) * s.ctas - 1) / s.all);
 }
 
 // ------------------------------------------------------------ small operations
-__device__ __forceinline__ float exp2_of(float x);
-
-// Four values of a row from the parts that CTAs c0 to c1 left, in their order.
-template <uint32_t kRows, uint32_t kPad>
-__device__ __forceinline__ float4 join_parts(const AttnParams& p, uint32_t c0, uint32_t c1, uint32_t row, uint32_t quad,
-                                             float& m, float& l) {
-  m = -INFINITY;
-  l = 0.f;
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (uint32_t k = c0; k <= c1; ++k) {
-    const float* const at = p.partial + (uint64_t)(2 * k + (k == c0)) * partial_floats(kRows, kPad);
-    const float mk = __ldcg(at + kRows * kPad + row), lk = __ldcg(at + kRows * kPad + kRows + row);
-    const float4 y = __ldcg((const float4*)(at + row * kPad) + quad);
-    const float now = fmaxf(m, mk), by = now == -INFINITY ? 0.f : now;
-    const float a = exp2_of(m - by), b = exp2_of(mk - by);
-    l = l * a + lk * b;
-    v.x = v.x * a + y.x * b, v.y = v.y * a + y.y * b, v.z = v.z * a + y.z * b, v.w = v.w * a + y.w * b;
-    m = now;
-  }
-  return v;
-}
-
 __device__ __forceinline__ float exp2_of(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ uint32_t smem_at(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-// 16 bytes (or zeros) into shared memory, without a register.
+// 16 bytes (or zeros) into shared memory, without a register. (The form with a
+// size in a register is several times slower to start.)
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool real) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(real ? 16 : 0) : "memory");
+  if (real)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  else
+    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t to, const void* from, bool real) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(real ? 4 : 0) : "memory");
@@ -252,6 +234,67 @@ __device__ __forceinline__ bool not_finite2<__half>(uint32_t w) {
 template <>
 __device__ __forceinline__ bool not_finite2<__nv_bfloat16>(uint32_t w) {
   return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+
+// An item that several CTAs have parts of: rows [row0, row0 + rows) of a key
+// head's queries of the request whose first row is `first`.
+struct JoinedItem {
+  uint32_t first, row0, rows, head, c0, c1;
+};
+
+// Joins the parts of CTAs c0 to c1, in their order, and writes the answer: four
+// values of four rows at a time for each of kThreads threads, so that the loads
+// of one part are under way together.
+template <typename T, uint32_t kRows, uint32_t kPad, uint32_t kThreads>
+static __device__ __noinline__ void join_item(const AttnParams& p, const JoinedItem item) {
+  constexpr uint32_t kQuads = kPad / 4, kMany = 4;
+#pragma unroll 1
+  for (uint32_t c = threadIdx.x; c < item.rows * kQuads; c += kThreads * kMany) {
+    float m[kMany], l[kMany];
+    float4 v[kMany];
+#pragma unroll
+    for (uint32_t j = 0; j < kMany; ++j) {
+      m[j] = -INFINITY;
+      l[j] = 0.f;
+      v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll 1
+    for (uint32_t k = item.c0; k <= item.c1; ++k) {
+      const float* const at = p.partial + (uint64_t)(2 * k + (k == item.c0)) * partial_floats(kRows, kPad);
+      float mk[kMany], lk[kMany];
+      float4 y[kMany];
+#pragma unroll
+      for (uint32_t j = 0; j < kMany; ++j) {
+        const uint32_t of = min(c + j * kThreads, item.rows * kQuads - 1), row = of / kQuads, quad = of % kQuads;
+        mk[j] = __ldcg(at + kRows * kPad + row);
+        lk[j] = __ldcg(at + kRows * kPad + kRows + row);
+        y[j] = quad * 4 < p.c.width ? __ldcg((const float4*)(at + row * kPad) + quad) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (uint32_t j = 0; j < kMany; ++j) {
+        const float now = fmaxf(m[j], mk[j]), by = now == -INFINITY ? 0.f : now;
+        const float a = exp2_of(m[j] - by), b = exp2_of(mk[j] - by);
+        l[j] = l[j] * a + lk[j] * b;
+        v[j].x = v[j].x * a + y[j].x * b, v[j].y = v[j].y * a + y[j].y * b;
+        v[j].z = v[j].z * a + y[j].z * b, v[j].w = v[j].w * a + y[j].w * b;
+        m[j] = now;
+      }
+    }
+#pragma unroll
+    for (uint32_t j = 0; j < kMany; ++j) {
+      const uint32_t of = c + j * kThreads;
+      if (of >= item.rows * kQuads) break;
+      const uint32_t row = item.row0 + of / kQuads, quad = of % kQuads, node = row / p.group;
+      const uint32_t qh = item.head * p.group + (row - node * p.group);
+      const float by = l[j] == 0.f ? 0.f : 1.f / l[j];
+      if (quad * 4 < p.c.width)
+        *(uint2*)((char*)p.out.base + (uint64_t)(item.first + node) * p.out.row_stride + qh * p.out.head_stride + quad * 8) =
+            make_uint2(pack2<T>(v[j].x * by, v[j].y * by), pack2<T>(v[j].z * by, v[j].w * by));
+      if (quad == 0 && p.lse)
+        p.lse[(uint64_t)(item.first + node) * (p.c.heads * p.group) + qh] =
+            l[j] == 0.f ? -INFINITY : m[j] * 0.6931471805599453f + logf(l[j]);
+    }
+  }
 }
 
 // --------------------------------------------------------- few rows: mma.sync
@@ -698,12 +741,8 @@ __global__ void __launch_bounds__(kAttnThreads, kPad > 128 ? 1 : 2) attention_fe
       __syncthreads();
       if (s_last) {
         __threadfence();
-        for (uint32_t c = tid; c < rows * kQuads; c += kAttnThreads) {
-          const uint32_t row = c / kQuads, quad = c % kQuads;
-          float m, l;
-          const float4 v = join_parts<F::kRows, kPad>(p, c0, c1, row, quad, m, l);
-          answer(row, quad, m, l, v);
-        }
+        const JoinedItem item_of = {r.first, rb * F::kRows, rows, head, c0, c1};
+        join_item<T, F::kRows, kPad, kAttnThreads>(p, item_of);
       }
     }
     at += t1 - t0;

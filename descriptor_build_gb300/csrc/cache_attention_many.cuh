@@ -3,9 +3,9 @@
 // tcgen05 products.
 //
 // A CTA has three kinds of warps that hand tiles of 64 tokens on by mbarriers:
-//   loaders (4 warps)   keys and values from their pages into a ring of tiles,
-//                       16-bit rows by asynchronous copies, 8-bit codes through
-//                       registers, where they are widened
+//   loaders (3 warps)   keys and values from their pages into a ring of tiles, by
+//                       16-byte asynchronous copies; 8-bit codes come into a
+//                       ring of their own, from which they are widened
 //   one issuing thread  S = Q K^T into TMEM (two buffers), O += P V from TMEM
 //   weights (4 warps)   a thread for each query row: S -> maxima, weights P
 //                       (over S in TMEM) and their sum
@@ -13,6 +13,12 @@
 // made, and two CTAs share an SM. A row's maximum is followed only when it has
 // risen by 2^8 (weights then are at most 2^8, which every type here holds as
 // exactly as 1), so O is hardly ever rescaled.
+//
+// A row of a page is 128 or 256 bytes, the next token's some kilobytes on. Such
+// rows of 16 tokens a page come at 6.6 TB/s (1 CTA an SM, 4 tiles ahead) by
+// 16-byte copies of 128 threads and at 3.6 by TMA boxes of 64 values x 16 tokens,
+// which a CTA starts every 150 cycles; in this kernel boxes took 225 us where the
+// copies take less than 160 (48 trees of 25, see the table of cases).
 //
 // Tiles lie as the tensor cores' 128-byte swizzle wants them: panels of 64
 // values, a row of 128 bytes for each token, 16-byte chunks exchanged by the
@@ -29,21 +35,23 @@ namespace db {
 template <uint32_t kPad, bool kCodes>
 struct Many {
   static constexpr uint32_t kRows = 128;
-  static constexpr uint32_t kThreads = 288;
-  static constexpr uint32_t kLoaders = 128, kWeights = 128;
+  // 256 threads: 128 registers each with two CTAs an SM (9 warps would leave 96)
+  static constexpr uint32_t kThreads = 256;
+  static constexpr uint32_t kWeights = 128, kLoaders = 96;
   static constexpr uint32_t kUnit = kTile * kPad * 2;  // keys or values of a tile
-  static constexpr uint32_t kUnits = kPad >= 128 ? 4 : 6;
-  static constexpr uint32_t kLag = kCodes ? 2 : 3;     // units under way before one is handed on
+  static constexpr uint32_t kUnits = kCodes ? 3 : kPad >= 128 ? 4 : 6;
   static constexpr uint32_t kQuery = kRows * kPad * 2;
-  static constexpr uint32_t kMeta = 8;                 // tiles that notes are kept of
+  static constexpr uint32_t kRaw = kTile * kPad;       // codes of a unit
+  static constexpr uint32_t kRaws = kCodes ? 3 : 0;
+  static constexpr uint32_t kMeta = kUnits / 2 + 3;    // tiles that notes are kept of
   static constexpr uint32_t kColumns = kPad <= 128 ? 256 : 512;  // of TMEM
-  static constexpr uint32_t kBytes = kUnits * kUnit + kQuery + 1024;
+  static constexpr uint32_t kBytes = kUnits * kUnit + kQuery + kRaws * kRaw + 1024;
   // no more than two CTAs an SM, which is what TMEM holds
   static constexpr uint32_t kAsk = kBytes < 80 * 1024 ? 80 * 1024 : kBytes;
 };
 
 // What the weights' warps need to know of a tile, by the loaders.
-struct alignas(16) TileNotes {  // scales are read by fours
+struct alignas(16) TileNotes {    // scales are read by fours
   int2 place[kTile];              // page (or -1) and slot of a token
   float k_scale[kTile], v_scale[kTile];
   uint32_t real[2], odd[2];       // bits of tokens: that are there; whose values are not all finite
@@ -65,29 +73,45 @@ __device__ __forceinline__ bool barrier_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok;
 }
-// Waits for a phase; gives up after a second, or when another thread has.
+// Whether it is over now (try_wait may sleep for microseconds before it says no).
+__device__ __forceinline__ bool barrier_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok;
+}
+// Waits for a phase; gives up after a second, or when another thread has. (The
+// clock is read only when a wait is long: reading it takes longer than most.)
 static __device__ __noinline__ bool barrier_wait_long(uint32_t bar, uint32_t parity, volatile uint32_t* failed) {
-  const uint64_t began = globaltimer_ns();
+  uint64_t began = 0;
   for (;;) {
-    for (int k = 0; k < 32; ++k)
+    for (int k = 0; k < 256; ++k)
       if (barrier_try(bar, parity)) return true;
     if (*failed) return false;
-    if (globaltimer_ns() - began > kWaitLimitNs) {
+    const uint64_t now = globaltimer_ns();
+    if (!began) began = now;
+    if (now - began > kWaitLimitNs) {
       *failed = 1;
       return false;
     }
   }
 }
 __device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity, volatile uint32_t* failed) {
-  if (barrier_try(bar, parity)) return true;
+  for (int k = 0; k < 8; ++k)
+    if (barrier_try(bar, parity)) return true;
   return barrier_wait_long(bar, parity, failed);
 }
 __device__ __forceinline__ void group_sync(uint32_t id, uint32_t threads) {
+  __syncwarp();
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 // The same, and whether `yes` held in all of them.
 __device__ __forceinline__ bool group_all(uint32_t id, uint32_t threads, bool yes) {
   uint32_t r;
+  __syncwarp();
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbar.red.and.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
@@ -166,31 +190,134 @@ __device__ __forceinline__ uint32_t tmem_load1(uint32_t at) {
 __device__ __forceinline__ void tmem_loaded() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Two 32-bit floats at a time.
+__device__ __forceinline__ uint64_t pair(uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float low(uint64_t x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float high(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t multiply2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t multiply_add2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float largest3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// What few tiles need is kept out of the loops' code, which is as long as the
+// instruction caches bear: a kernel of 138 KB that had all of it inline took 324
+// us for 48 trees of 25, a smaller one the time in the table of cases.
+
+// Scores of a tile that a row does not see become -infinity, in TMEM. Codes:
+// the others are multiplied by their keys' scales.
+static __device__ __noinline__ void hide_scores(uint32_t here, uint32_t sees0, uint32_t sees1, const float* k_scale) {
+#pragma unroll 1
+  for (uint32_t h = 0; h < 4; ++h) {
+    uint32_t s[16];
+    tmem_load16(here + 16 * h, s);
+    tmem_loaded();
+    const uint32_t sees = (h & 2 ? sees1 : sees0) >> (16 * (h & 1));
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      float x = __uint_as_float(s[j]);
+      if (k_scale) x *= k_scale[16 * h + j];
+      s[j] = __float_as_uint((sees >> j) & 1 ? x : -INFINITY);
+    }
+    tmem_store16(here + 16 * h, s);
+  }
+  tmem_stored();
+}
+
+// Values that are not finite, which the product is not given, added to O for
+// the rows that see them. `v`, `scale`: of the head.
+template <typename T, bool kCodes>
+static __device__ __noinline__ void add_odd(const TileNotes& m, uint32_t output, uint32_t here, uint64_t odd, uint64_t sees,
+                                            float factor, float ref, const char* v, uint64_t v_stride, uint64_t token_step,
+                                            const char* scale, uint64_t scale_stride, uint32_t scale_step, bool i8,
+                                            uint32_t width) {
+#pragma unroll 1
+  for (uint64_t left = odd; left; left &= left - 1) {
+    const uint32_t token = __ffsll((long long)left) - 1;
+    __syncwarp();
+    const float score = __uint_as_float(tmem_load1(here + token));
+    tmem_loaded();
+    const int2 place = m.place[token];
+    const char* const from = v + (uint64_t)place.x * v_stride + (uint64_t)place.y * token_step;
+    float weight = exp2_of(__fmaf_rn(score, factor, -ref));
+    if (kCodes) weight *= ((const float*)(scale + (uint64_t)place.x * scale_stride))[(uint32_t)place.y * scale_step];
+    const bool yes = (sees >> token) & 1;
+#pragma unroll 1
+    for (uint32_t c = 0; c < width; c += 16) {
+      uint32_t o[16];
+      __syncwarp();
+      tmem_load16(output + c, o);
+      tmem_loaded();
+      if (yes) {
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          float2 x;
+          if (kCodes) {
+            const uint16_t two = *(const uint16_t*)(from + c + j);
+            // I8 has no values that are not finite, its scales have
+            x = i8 ? make_float2((float)(int8_t)two, (float)(int8_t)(two >> 8)) : unpack2<__half>(e4m3x2_to_f16x2(two));
+          } else {
+            x = unpack2<T>(*(const uint32_t*)(from + 2 * (c + j)));
+          }
+          o[j] = __float_as_uint(__uint_as_float(o[j]) + weight * x.x);
+          o[j + 1] = __float_as_uint(__uint_as_float(o[j + 1]) + weight * x.y);
+        }
+      }
+      __syncwarp();
+      tmem_store16(output + c, o);
+    }
+    tmem_stored();
+  }
+}
+
+static __device__ __noinline__ uint64_t quotient(uint64_t a, uint64_t b) { return a / b; }
+
 constexpr float kSlack = 8.f;          // a maximum is followed when it has risen by this much (log2)
 
 template <typename T, uint32_t kPad, bool kCodes>
-__global__ void __launch_bounds__(288, kPad <= 128 ? 2 : 1) attention_many_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kernel(const AttnParams p) {
   typedef Many<kPad, kCodes> F;
   typedef typename std::conditional<kCodes, __half, T>::type W;  // of weights and values
   constexpr uint32_t kTypeQ = std::is_same<T, __half>::value ? 0 : 1, kTypeW = std::is_same<W, __half>::value ? 0 : 1;
   constexpr uint32_t kPanel = kTile * 128, kQueryPanel = F::kRows * 128;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ TileNotes s_notes[F::kMeta];
-  __shared__ uint64_t s_full[F::kUnits], s_empty[F::kUnits], s_scores[2], s_weights[2], s_output[2], s_query, s_drained;
+  __shared__ uint64_t s_full[F::kUnits], s_empty[F::kUnits], s_scores[2], s_weights[2], s_output[2], s_odd[F::kMeta], s_asked, s_drained;
   __shared__ uint32_t s_tmem, s_last;
+  __shared__ __align__(16) float s_ones[kCodes ? kTile : 4];  // keys' scales of scores that have theirs
   __shared__ volatile uint32_t s_failed;
   const uint32_t tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
   unsigned char* const smem = smem_raw + ((1024 - (smem_at(smem_raw) & 1023)) & 1023);
   const uint32_t ring = smem_at(smem), query = ring + F::kUnits * F::kUnit;
 
-  if (warp == 8) {
+  if (warp == 7) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_at(&s_tmem)), "n"(F::kColumns)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+  if (kCodes && tid < kTile) s_ones[tid] = 1.f;
   if (tid == 0) {
     for (uint32_t k = 0; k < F::kUnits; ++k) {
-      barrier_init(smem_at(&s_full[k]), F::kLoaders);
+      barrier_init(smem_at(&s_full[k]), 32);  // a warp's lanes
       barrier_init(smem_at(&s_empty[k]), 1);
     }
     for (int k = 0; k < 2; ++k) {
@@ -201,7 +328,8 @@ __global__ void __launch_bounds__(288, kPad <= 128 ? 2 : 1) attention_many_kerne
       // before are over when a tile's scores come)
       barrier_init(smem_at(&s_output[k]), 1);
     }
-    barrier_init(smem_at(&s_query), 1);
+    for (uint32_t k = 0; k < F::kMeta; ++k) barrier_init(smem_at(&s_odd[k]), 32);
+    barrier_init(smem_at(&s_asked), F::kWeights);  // an item's queries are there
     barrier_init(smem_at(&s_drained), 1);
     s_failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -209,7 +337,11 @@ __global__ void __launch_bounds__(288, kPad <= 128 ? 2 : 1) attention_many_kerne
   wait_for_prerequisites();
   dependents_may_launch();
   tensor_fence_before();
-  const Share share = plan_share<F::kRows, F::kThreads>(p);
+  __shared__ Share share;  // not in every thread's registers
+  {
+    const Share mine = plan_share<F::kRows, F::kThreads>(p);
+    if (tid == 0) share = mine;
+  }
   __syncthreads();
   tensor_fence_after();
   const uint32_t tmem = s_tmem, scores = tmem, output = tmem + 2 * kTile;
@@ -220,6 +352,7 @@ __global__ void __launch_bounds__(288, kPad <= 128 ? 2 : 1) attention_many_kerne
   uint64_t at = share.lo, before = share.before;
   uint32_t request = share.request;
   uint32_t items = 0, tiles = 0, units = 0;  // behind this CTA
+  uint32_t odd_phases = 0;
   bool go = true;
   while (go && at < share.hi) {
     const Request r = attention_request(p, request);
@@ -230,189 +363,261 @@ __global__ void __launch_bounds__(288, kPad <= 128 ? 2 : 1) attention_many_kerne
       continue;
     }
     const uint64_t x = at - before;
-    const uint32_t t0 = (uint32_t)(x % e.tiles);
-    const uint32_t item = (uint32_t)(x / e.tiles), head = item / e.blocks, rb = item - head * e.blocks;
+    const uint32_t item = (uint32_t)quotient(x, e.tiles), head = item / e.blocks, rb = item - head * e.blocks;
+    const uint32_t t0 = (uint32_t)(x - (uint64_t)item * e.tiles);
     const uint32_t t1 = (uint32_t)min((uint64_t)e.tiles, t0 + (share.hi - at)), n = t1 - t0;
     const uint32_t rows = min(F::kRows, r.rows * p.group - rb * F::kRows);
     const uint32_t base = r.length - r.rows;  // tokens before the request's own
 
-    if (warp >= 4 && warp < 8) {
+    if (warp >= 4 && warp < 7) {
       // ------------------------------------------------------------- loaders
-      const uint32_t me = tid - 128;
+      // A warp has every third unit to itself, and waits for no other.
+      const uint32_t me = tid - F::kWeights, mine = warp - F::kWeights / 32;
       const int32_t* const table = p.view.table + (uint64_t)r.seq * p.view.columns;
-      const char* const keys = (const char*)p.c.k + head * p.head_step;
-      const char* const values = (const char*)p.c.v + head * p.head_step;
-      const auto look = [&](uint32_t t) {  // threads 0 to 63: a token's place
-        int2 w = make_int2(-1, 0);
-        const uint32_t position = t * kTile + me;
-        if (me < kTile && t < t1 && position < r.length) {
-          const uint32_t column = position / p.view.page_tokens;
-          const uint32_t page = (uint32_t)__ldg(table + column);
-          if (page < p.view.n_pages)
-            w = make_int2((int)page, (int)(position - column * p.view.page_tokens));
-          else
-            w.y = -1;
-        }
-        return w;
-      };
-      const auto note = [&](uint32_t t, int2 w) {
-        if (t >= t1) return;
-        TileNotes& m = s_notes[(tiles + t - t0) % F::kMeta];
-        if (me < kTile) {
-          m.place[me] = w;
-          const uint32_t real = __ballot_sync(kFull, w.x >= 0);
-          if (lane == 0) {
-            m.real[me / 32] = real;
-            m.odd[me / 32] = 0;
-          }
-          if (w.y < 0) report_table(p.view.ctr);
-        }
-      };
-      constexpr uint32_t kChunks = kPad / 8, kRawChunks = kCodes ? kPad / 16 : kChunks;
-      constexpr uint32_t kStep = F::kLoaders / kRawChunks, kEach = kTile / kStep;  // tokens apart, copies a thread
-      const uint32_t chunk = me % kRawChunks, token0 = me / kRawChunks;
-      const bool mine = chunk < (kCodes ? p.c.width / 16 : p.c.width / 8);
-      uint4 raw[2][kCodes ? kEach : 1];
-      float scale[2] = {0.f, 0.f};
+      constexpr uint32_t kChunks = kPad / 8, kRawChunks = kCodes ? kPad / 16 : kChunks;  // 16-byte chunks of a row
+      constexpr uint32_t kStep = 32 / kRawChunks, kEach = kTile / kStep;  // a lane has the same chunk of every kStep-th token
+      const uint32_t chunk = lane % kRawChunks, token0 = lane / kRawChunks;
+      const bool has = chunk < (kCodes ? p.c.width / 16 : p.c.width / 8);
 
       // unit u of the item: its tile, and whether it is of keys
-      const auto unit_of = [&](uint32_t u, uint32_t& t, bool& key) {
+      const auto unit_of = [&](uint32_t u, uint32_t& t, bool& key) __attribute__((always_inline)) {
         key = u == 0 || ((u & 1) && u != 2 * n - 1);
         t = t0 + (u == 0 ? 0 : u == 2 * n - 1 ? n - 1 : key ? (u + 1) / 2 : u / 2 - 1);
       };
-      const auto issue = [&](uint32_t u, uint4* to, float& sc) {
-        uint32_t t;
-        bool key;
-        unit_of(u, t, key);
-        TileNotes& m = s_notes[(tiles + t - t0) % F::kMeta];
-        const char* const from = key ? keys : values;
-        const uint64_t step = key ? p.c.k_stride : p.c.v_stride;
-        const uint32_t slot = (units + u) % F::kUnits;
-        if (!kCodes) {
-          if (!barrier_wait(smem_at(&s_empty[slot]), ((units + u) / F::kUnits + 1) & 1, &s_failed)) return;
-        }
-#pragma unroll
-        for (uint32_t k = 0; k < kEach; ++k) {
-          const uint32_t token = token0 + k * kStep;
-          const int2 w = m.place[token];
-          const bool real = w.x >= 0 && (key || !((m.odd[token / 32] >> (token & 31)) & 1));
-          const char* const source =
-              from + (real ? (uint64_t)w.x * step + (uint64_t)w.y * p.token_step : 0) + (mine ? chunk * 16 : 0);
-          if (kCodes) {
-            to[k] = real && mine ? __ldg((const uint4*)source) : make_uint4(0, 0, 0, 0);
-          } else if (mine) {
-            copy16(ring + slot * F::kUnit + chunk / 8 * kPanel + token * 128 + ((chunk & 7) ^ (token & 7)) * 16, source, real);
-          }
-        }
-        if (!kCodes) copies_commit();
-        if (key) {
-          if (kCodes) {
-            const uint32_t token = me % kTile;
-            const bool val = me >= kTile;
-            const int2 w = m.place[token];
-            const char* const s = (const char*)(val ? p.c.v_scale : p.c.k_scale);
-            sc = w.x >= 0 ? __ldg((const float*)(s + (uint64_t)w.x * (val ? p.c.v_scale_stride : p.c.k_scale_stride)) +
-                                  w.y * p.scale_token_step + head * p.scale_head_step)
-                          : 0.f;
-          }
-          // Values of a tile that not every row sees: those that are not
-          // finite stay out of the product.
-          if ((t + 1) * kTile > base || (m.real[0] & m.real[1]) != 0xFFFFFFFFu) {
-            for (uint32_t k = 0; k < kEach; ++k) {
-              const uint32_t token = token0 + k * kStep;
-              const int2 w = m.place[token];
-              if (w.x < 0 || !mine) continue;
-              const uint4 v = __ldg((const uint4*)(values + (uint64_t)w.x * p.c.v_stride + (uint64_t)w.y * p.token_step + chunk * 16));
-              bool odd;
-              if (kCodes) {
-                const auto nan4 = [](uint32_t c) { return ((c & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; };
-                odd = e4m3 && (nan4(v.x) | nan4(v.y) | nan4(v.z) | nan4(v.w));
-              } else {
-                odd = not_finite2<W>(v.x) || not_finite2<W>(v.y) || not_finite2<W>(v.z) || not_finite2<W>(v.w);
-              }
-              if (odd) atomicOr(&m.odd[token / 32], 1u << (token & 31));
-            }
-          }
-        }
-      };
-      const auto finish = [&](uint32_t u, const uint4* got, float sc) {
-        uint32_t t;
-        bool key;
-        unit_of(u, t, key);
-        const uint32_t slot = (units + u) % F::kUnits;
-        if (u == 0) {
-          // the item's queries, when the products with the ones before are made
-          if (items && !barrier_wait(smem_at(&s_query), (items - 1) & 1, &s_failed)) return;
-          const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u, keep = p.scale_log2 == 0.f ? 0u : 0xFFFFFFFFu;
-#pragma unroll 4
-          for (uint32_t c = me; c < F::kRows * kChunks; c += F::kLoaders) {
-            const uint32_t row = c / kChunks, ch = c % kChunks, all = rb * F::kRows + row;
-            const bool real = row < rows && ch < p.c.width / 8;
-            const uint32_t nd = real ? all / p.group : 0, qh = head * p.group + (real ? all - nd * p.group : 0);
-            uint4 v = real ? __ldg((const uint4*)((const char*)p.q.base + (uint64_t)(r.first + nd) * p.q.row_stride +
-                                                  qh * p.q.head_stride + ch * 16))
-                           : make_uint4(0, 0, 0, 0);
-            v.x = (v.x ^ flip) & keep, v.y = (v.y ^ flip) & keep, v.z = (v.z ^ flip) & keep, v.w = (v.w ^ flip) & keep;
-            *(uint4*)(smem + F::kUnits * F::kUnit + ch / 8 * kQueryPanel + row * 128 + ((ch & 7) ^ (row & 7)) * 16) = v;
-          }
-        }
-        if (kCodes) {
-          if (!barrier_wait(smem_at(&s_empty[slot]), ((units + u) / F::kUnits + 1) & 1, &s_failed)) return;
-          if (mine) {
-#pragma unroll
-            for (uint32_t k = 0; k < kEach; ++k) {
-              const uint32_t token = token0 + k * kStep;
-              uint2 a, b, c, d;
-              if (key) {
-                a = widen4<T>(got[k].x, e4m3), b = widen4<T>(got[k].y, e4m3), c = widen4<T>(got[k].z, e4m3), d = widen4<T>(got[k].w, e4m3);
-              } else {
-                a = widen4<W>(got[k].x, e4m3), b = widen4<W>(got[k].y, e4m3), c = widen4<W>(got[k].z, e4m3), d = widen4<W>(got[k].w, e4m3);
-              }
-              unsigned char* const to = smem + slot * F::kUnit + chunk / 4 * kPanel + token * 128;
-              *(uint4*)(to + (((2 * chunk) & 7) ^ (token & 7)) * 16) = make_uint4(a.x, a.y, b.x, b.y);
-              *(uint4*)(to + (((2 * chunk + 1) & 7) ^ (token & 7)) * 16) = make_uint4(c.x, c.y, d.x, d.y);
-            }
-          }
-          if (key) {
-            TileNotes& m = s_notes[(tiles + t - t0) % F::kMeta];
-            if (me < kTile) {
-              // an infinite scale stands for values of both signs, whose
-              // products have no sum
-              m.k_scale[me] = __fmaf_rn(sc, 0.f, sc) * fabsf(p.scale_log2);
-            } else {
-              m.v_scale[me - kTile] = sc;
-              const uint32_t ex = (__float_as_uint(sc) >> 23) & 0xFFu;
-              const uint32_t most = __reduce_max_sync(kFull, ex == 0xFFu ? 0u : ex);
-              if (lane == 0) m.exponent[(me - kTile) / 32] = most;
-            }
-          }
-        } else if (u + F::kLag < 2 * n) {
-          copies_wait<F::kLag - 1>();
-        } else {
-          copies_wait<0>();
-        }
+      const auto slot_of = [&](uint32_t u) __attribute__((always_inline)) { return (units + u) % F::kUnits; };
+      const auto phase_of = [&](uint32_t u) __attribute__((always_inline)) { return ((units + u) / F::kUnits + 1) & 1; };
+      // What this lane has written of a unit is there for the tensor cores.
+      const auto hand_on = [&](uint32_t u) __attribute__((always_inline)) {
         writes_to_async_proxy();
-        barrier_arrive(smem_at(&s_full[slot]));
+        barrier_arrive(smem_at(&s_full[slot_of(u)]));
       };
-
-      note(t0, look(t0));
-      note(t0 + 1, look(t0 + 1));
-      int2 ahead = make_int2(-1, 0);
-      group_sync(2, F::kLoaders);
-      for (uint32_t u = 0; u < 2 * n + F::kLag; u += 2) {
-        // two units, keys of tile t0 + u / 2 + 1 among them
+      // The places of a unit's tokens: a lane looks up tokens lane and lane + 32.
+      struct Places {
+        int2 at[2];  // page and slot, or -1 and -1
+      };
+      const auto look = [&](uint32_t u) __attribute__((always_inline)) {
+        Places w;
+        uint32_t t;
+        bool key;
+        unit_of(u, t, key);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          w.at[h] = make_int2(-1, -1);
+          const uint32_t position = t * kTile + 32 * h + lane;
+          if (u < 2 * n && position < r.length) {
+            const uint32_t column = position / p.view.page_tokens;
+            w.at[h] = make_int2(__ldg(table + column), (int)(position - column * p.view.page_tokens));
+          }
+        }
+        return w;
+      };
+      const auto settle = [&](Places& w) __attribute__((always_inline)) {  // entries that are no page
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if ((uint32_t)w.at[h].x >= p.view.n_pages) {
+            if (w.at[h].y >= 0) report_table(p.view.ctr);
+            w.at[h] = make_int2(-1, -1);
+          }
+      };
+      // Notes of a tile for the weights, by the warp that has its keys.
+      const auto note = [&](uint32_t t, const Places& w) __attribute__((always_inline)) {
+        TileNotes& m = s_notes[(tiles + t - t0) % F::kMeta];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          m.place[32 * h + lane] = w.at[h];
+          const uint32_t real = __ballot_sync(kFull, w.at[h].x >= 0);
+          if (lane == 0) m.real[h] = real;
+        }
+      };
+      const auto all_seen = [&](uint32_t t, const Places& w) __attribute__((always_inline)) {
+        return __all_sync(kFull, w.at[0].x >= 0 && w.at[1].x >= 0) && (t + 1) * kTile <= base;
+      };
+      // Offsets of a lane's two tokens in the pool, of all heads and chunks.
+      const auto offset = [&](const int2& w, bool key) __attribute__((always_inline)) {
+        return (uint64_t)(uint32_t)w.x * (key ? p.c.k_stride : p.c.v_stride) + (uint64_t)(uint32_t)w.y * p.token_step;
+      };
+      // Starts the copies of a unit; a token's chunk goes to place(token, k).
+      const auto start = [&](bool key, bool whole, const Places& w, auto place) __attribute__((always_inline)) {
+        const char* const from = (const char*)(key ? p.c.k : p.c.v) + head * p.head_step + chunk * 16;
+        const uint64_t off[2] = {offset(w.at[0], key), offset(w.at[1], key)};
 #pragma unroll
         for (uint32_t h = 0; h < 2; ++h) {
-          const uint32_t v = u + h;
-          if (v >= F::kLag && v - F::kLag < 2 * n) finish(v - F::kLag, raw[h], scale[h]);
-          if (v < 2 * n) issue(v, raw[h], scale[h]);
-          if (h == 0) ahead = look(t0 + u / 2 + 2);
-          if (h == 1) note(t0 + u / 2 + 2, ahead);
-          group_sync(2, F::kLoaders);
+          const uint32_t there = __ballot_sync(kFull, w.at[h].x >= 0);
+#pragma unroll 4
+          for (uint32_t k = h * kEach / 2; k < (h + 1) * kEach / 2; ++k) {
+            const uint32_t token = token0 + k * kStep;
+            const uint64_t at = __shfl_sync(kFull, off[h], token & 31);
+            const bool real = whole || (there >> (token & 31)) & 1;
+            if (has) copy16(place(token, k), from + (real ? at : 0), real);
+          }
+        }
+        copies_commit();
+      };
+      // Values of a tile that not every row sees, when they have come: tokens
+      // with some that are not finite become zeros, and are noted for the
+      // weights. at(token, k): where this lane's chunk is.
+      const auto check = [&](uint32_t t, const Places& w, auto at) {
+        uint32_t odd[2] = {0, 0};
+#pragma unroll 2
+        for (uint32_t k = 0; k < kEach; ++k) {
+          const uint32_t token = token0 + k * kStep;
+          uint4* const mine_at = (uint4*)(smem + at(token, k));
+          bool bad = false;
+          if (has) {
+            const uint4 v = *mine_at;
+            if (kCodes) {
+              const auto nan4 = [](uint32_t c) { return ((c & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; };
+              bad = e4m3 && (nan4(v.x) | nan4(v.y) | nan4(v.z) | nan4(v.w));
+            } else {
+              bad = not_finite2<W>(v.x) || not_finite2<W>(v.y) || not_finite2<W>(v.z) || not_finite2<W>(v.w);
+            }
+          }
+          const uint32_t votes = __ballot_sync(kFull, bad) >> token0 * kRawChunks % 32;
+          if (votes & (kRawChunks == 32 ? 0xFFFFFFFFu : (1u << kRawChunks % 32) - 1)) {
+            if (has) *mine_at = make_uint4(0, 0, 0, 0);
+            odd[0] |= token < 32 ? 1u << (token & 31) : 0u;
+            odd[1] |= token < 32 ? 0u : 1u << (token & 31);
+          }
+        }
+        TileNotes& m = s_notes[(tiles + t - t0) % F::kMeta];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          odd[h] = __reduce_or_sync(kFull, odd[h]);
+          if (kCodes) {  // a scale that is not finite: the token's values are not
+            float sc = 0.f;
+            if (w.at[h].x >= 0)
+              sc = __ldg((const float*)((const char*)p.c.v_scale + (uint64_t)w.at[h].x * p.c.v_scale_stride) +
+                         (uint32_t)w.at[h].y * p.scale_token_step + head * p.scale_head_step);
+            odd[h] |= __ballot_sync(kFull, (__float_as_uint(sc) & 0x7F800000u) == 0x7F800000u);
+          }
+          if (lane == 0) m.odd[h] = odd[h];
+        }
+        barrier_arrive(smem_at(&s_odd[(tiles + t - t0) % F::kMeta]));
+      };
+
+      Places w = look(mine);
+      if constexpr (kCodes) {
+        // A lane widens the codes that it has copied itself.
+        const uint32_t raw = query + F::kQuery + mine * F::kRaw + lane * 16;
+        const unsigned char* const from = smem + (raw - ring);
+        float k_sc[2], v_sc[2];
+        bool whole = false;
+        const auto ask = [&](uint32_t u) __attribute__((always_inline)) {
+          uint32_t t;
+          bool key;
+          unit_of(u, t, key);
+          settle(w);
+          whole = all_seen(t, w);
+          start(key, whole, w, [&](uint32_t, uint32_t k) __attribute__((always_inline)) { return raw + k * 512; });
+          if (key) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              k_sc[h] = v_sc[h] = 0.f;
+              if (w.at[h].x >= 0) {
+                const uint32_t of = (uint32_t)w.at[h].y * p.scale_token_step + head * p.scale_head_step;
+                k_sc[h] = __ldg((const float*)((const char*)p.c.k_scale + (uint64_t)w.at[h].x * p.c.k_scale_stride) + of);
+                v_sc[h] = __ldg((const float*)((const char*)p.c.v_scale + (uint64_t)w.at[h].x * p.c.v_scale_stride) + of);
+              }
+            }
+          }
+        };
+        if (mine < 2 * n) ask(mine);
+        for (uint32_t u = mine; u < 2 * n; u += 3) {
+          uint32_t t;
+          bool key;
+          unit_of(u, t, key);
+          Places next = look(u + 3);
+          barrier_wait(smem_at(&s_empty[slot_of(u)]), phase_of(u), &s_failed);
+          __syncwarp();
+          if (key) {
+            note(t, w);
+            TileNotes& m = s_notes[(tiles + t - t0) % F::kMeta];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              // an infinite scale stands for values of both signs, whose
+              // products have no sum
+              m.k_scale[32 * h + lane] = __fmaf_rn(k_sc[h], 0.f, k_sc[h]) * fabsf(p.scale_log2);
+              const uint32_t ex = (__float_as_uint(v_sc[h]) >> 23) & 0xFFu;
+              m.v_scale[32 * h + lane] = !whole && ex == 0xFFu ? 0.f : v_sc[h];  // odd tokens are added by themselves
+              const uint32_t most = __reduce_max_sync(kFull, ex == 0xFFu ? 0u : ex);
+              if (lane == 0) m.exponent[h] = most;
+            }
+          }
+          copies_wait<0>();
+          if (!key && !whole) check(t, w, [&](uint32_t, uint32_t k) __attribute__((always_inline)) { return raw - ring + k * 512; });
+          unsigned char* const to = smem + slot_of(u) * F::kUnit + chunk / 4 * kPanel;
+          const auto widen_all = [&](auto as, auto four) __attribute__((always_inline)) {
+            typedef decltype(as) H;
+            constexpr bool kFour = decltype(four)::value;
+#pragma unroll 4
+            for (uint32_t k = 0; k < kEach; ++k) {
+              const uint32_t token = token0 + k * kStep;
+              const uint4 c = *(const uint4*)(from + k * 512);
+              const uint2 y[4] = {widen4<H>(c.x, kFour), widen4<H>(c.y, kFour), widen4<H>(c.z, kFour), widen4<H>(c.w, kFour)};
+              *(uint4*)(to + token * 128 + (((2 * chunk) & 7) ^ (token & 7)) * 16) = make_uint4(y[0].x, y[0].y, y[1].x, y[1].y);
+              *(uint4*)(to + token * 128 + (((2 * chunk + 1) & 7) ^ (token & 7)) * 16) = make_uint4(y[2].x, y[2].y, y[3].x, y[3].y);
+            }
+          };
+          if (has) {
+            if (e4m3) {
+              if (key)
+                widen_all(T{}, std::true_type{});
+              else
+                widen_all(W{}, std::true_type{});
+            } else {
+              if (key)
+                widen_all(T{}, std::false_type{});
+              else
+                widen_all(W{}, std::false_type{});
+            }
+          }
+          hand_on(u);
+          __syncwarp();
+          w = next;
+          if (u + 3 < 2 * n) ask(u + 3);
+        }
+      } else {
+        uint32_t waiting = 0xFFFFFFFFu;  // a unit whose copies are under way
+        for (uint32_t u = mine; u < 2 * n; u += 3) {
+          uint32_t t;
+          bool key;
+          unit_of(u, t, key);
+          settle(w);
+          const bool whole = all_seen(t, w);
+          const uint32_t bar = smem_at(&s_empty[slot_of(u)]);
+          if (!__all_sync(kFull, barrier_test(bar, phase_of(u)))) {
+            if (waiting != 0xFFFFFFFFu) {  // meanwhile what has come is handed on
+              copies_wait<0>();
+              hand_on(waiting);
+              waiting = 0xFFFFFFFFu;
+            }
+            barrier_wait(bar, phase_of(u), &s_failed);
+            __syncwarp();
+          }
+          if (key) note(t, w);
+          const uint32_t to = slot_of(u) * F::kUnit + chunk / 8 * kPanel;
+          const auto place = [&](uint32_t token, uint32_t) __attribute__((always_inline)) {
+            return to + token * 128 + ((chunk & 7) ^ (token & 7)) * 16;
+          };
+          start(key, whole, w, [&](uint32_t token, uint32_t k) __attribute__((always_inline)) { return ring + place(token, k); });
+          if (waiting != 0xFFFFFFFFu) {
+            copies_wait<1>();
+            hand_on(waiting);
+          }
+          waiting = u;
+          if (!key && !whole) {
+            copies_wait<0>();
+            check(t, w, place);
+          }
+          w = look(u + 3);
+        }
+        if (waiting != 0xFFFFFFFFu) {
+          copies_wait<0>();
+          hand_on(waiting);
         }
       }
-      go = group_all(2, F::kLoaders, !s_failed);
-    } else if (warp == 8) {
+      go = __all_sync(kFull, !s_failed);
+    } else if (warp == 7) {
       // ------------------------------------------------------------- products
       if (lane == 0) {
         const uint32_t kind_s = product_kind(kTypeQ, kTile, false), kind_o = product_kind(kTypeW, p.c.width, true);
@@ -433,10 +638,9 @@ __global__ void __launch_bounds__(288, kPad <= 128 ? 2 : 1) attention_many_kerne
           tensor_commit(smem_at(&s_scores[buffer]));
           tensor_commit(smem_at(&s_empty[slot]));
           barrier_arrive(smem_at(&s_scores[buffer]));
-          if (k == n - 1) tensor_commit(smem_at(&s_query));
           return true;
         };
-        bool ok = score(0);
+        bool ok = barrier_wait(smem_at(&s_asked), items & 1, &s_failed) && score(0);
         for (uint32_t k = 0; ok && k < n; ++k) {
           if (k + 1 < n) ok = score(k + 1);
           if (!ok) break;
@@ -472,10 +676,27 @@ __global__ void __launch_bounds__(288, kPad <= 128 ? 2 : 1) attention_many_kerne
         uint32_t zero[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) zero[j] = 0;
+#pragma unroll 1
         for (uint32_t c = 0; c < p.c.width; c += 16) tmem_store16(output + lanes + c, zero);
         tmem_stored();
       }
       bool ok = true;
+      {
+        // The row's query; the products with the one before were over when its
+        // last scores came.
+        const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u, keep = p.scale_log2 == 0.f ? 0u : 0xFFFFFFFFu;
+        const char* const from = (const char*)p.q.base + (uint64_t)(r.first + node) * p.q.row_stride +
+                                 (head * p.group + (all - node * p.group)) * p.q.head_stride;
+#pragma unroll 8
+        for (uint32_t c = 0; c < kPad / 8; ++c) {
+          if (c >= p.c.width / 8) break;
+          uint4 v = row_real ? __ldg((const uint4*)from + c) : make_uint4(0, 0, 0, 0);
+          v.x = (v.x ^ flip) & keep, v.y = (v.y ^ flip) & keep, v.z = (v.z ^ flip) & keep, v.w = (v.w ^ flip) & keep;
+          *(uint4*)(smem + F::kUnits * F::kUnit + c / 8 * kQueryPanel + row * 128 + ((c & 7) ^ (row & 7)) * 16) = v;
+        }
+        writes_to_async_proxy();
+        barrier_arrive(smem_at(&s_asked));
+      }
       for (uint32_t k = 0; k < n; ++k) {
         const uint32_t tile = tiles + k, buffer = tile & 1, t = t0 + k;
         const uint32_t here = scores + buffer * kTile + lanes;
@@ -504,37 +725,28 @@ __global__ void __launch_bounds__(288, kPad <= 128 ? 2 : 1) attention_many_kerne
             }
             sees[h] = bits & m.real[h];
           }
+          hide_scores(here, sees[0], sees[1], kCodes ? m.k_scale : nullptr);
         }
-        // The scores of half a tile; they are fetched twice, for the maximum
-        // and for the weights: 32 registers instead of 64 let two CTAs share
-        // an SM without spills.
-        const auto fetch = [&](int h, float* s) {
-          tmem_load32(here + 32 * h, (uint32_t*)s);
-          tmem_loaded();
-          if (kCodes) {
+        uint32_t w[64];
+        uint64_t x[32];
+        tmem_load32(here, w);
+        tmem_load32(here + 32, w + 32);
+        tmem_loaded();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float4 y = ((const float4*)m.k_scale)[8 * h + j];
-              s[4 * j] *= y.x, s[4 * j + 1] *= y.y, s[4 * j + 2] *= y.z, s[4 * j + 3] *= y.w;
-            }
+        for (int j = 0; j < 32; ++j) x[j] = pair(w[2 * j], w[2 * j + 1]);
+        if (kCodes) {
+          const ulonglong2* const scales = (const ulonglong2*)(masked ? s_ones : m.k_scale);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const ulonglong2 y = scales[j];
+            x[2 * j] = multiply2(x[2 * j], y.x);
+            x[2 * j + 1] = multiply2(x[2 * j + 1], y.y);
           }
-          if (masked) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (!((sees[h] >> j) & 1)) s[j] = -INFINITY;
-          }
-        };
-        float most = -INFINITY;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float s[32];
-          fetch(h, s);
-          float other = s[1];
-          most = fmaxf(most, s[0]);
-#pragma unroll
-          for (int j = 2; j < 32; j += 2) most = fmaxf(most, s[j]), other = fmaxf(other, s[j + 1]);
-          most = fmaxf(most, other);
         }
+        float most = -INFINITY, other = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) most = largest3(most, low(x[j]), high(x[j])), other = largest3(other, low(x[j + 1]), high(x[j + 1]));
+        most = fmaxf(most, other);
         if (!kCodes) most *= factor;
         const float ref_before = top + (kCodes ? (float)((int)exponent - 127) : 0.f);
         bool move = most > top + kSlack || (top == -INFINITY && most > -INFINITY);
@@ -547,7 +759,14 @@ __global__ void __launch_bounds__(288, kPad <= 128 ? 2 : 1) attention_many_kerne
           }
         }
         const float ref = top == -INFINITY ? 0.f : top + (kCodes ? (float)((int)exponent - 127) : 0.f);
-        const uint64_t odd = masked ? (uint64_t)m.odd[0] | (uint64_t)m.odd[1] << 32 : 0;
+        uint64_t odd = 0;
+        if (masked) {
+          const uint32_t at_odd = tile % F::kMeta;
+          ok = barrier_wait(smem_at(&s_odd[at_odd]), (odd_phases >> at_odd) & 1, &s_failed);
+          if (!__all_sync(kFull, ok)) break;
+          odd_phases ^= 1u << at_odd;
+          odd = (uint64_t)m.odd[0] | (uint64_t)m.odd[1] << 32;
+        }
         if (__any_sync(kFull, move && k) || odd) {
           // O belongs to this warp while no product adds to it
           if (k) {
@@ -557,73 +776,49 @@ __global__ void __launch_bounds__(288, kPad <= 128 ? 2 : 1) attention_many_kerne
           }
           const float down = move ? exp2_of(ref_before - ref) : 1.f;
           if (k) sum *= down;
-          for (uint32_t c = 0; c < p.c.width; c += 16) {
-            uint32_t o[16];
-            tmem_load16(output + lanes + c, o);
-            tmem_loaded();
-            if (k) {
+          if (k) {
+#pragma unroll 1
+            for (uint32_t c = 0; c < p.c.width; c += 16) {
+              uint32_t o[16];
+              tmem_load16(output + lanes + c, o);
+              tmem_loaded();
 #pragma unroll
               for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * down);
+              tmem_store16(output + lanes + c, o);
             }
-            // Rare: values that are not finite, which the product was not given,
-            // for the rows that see them.
-            for (uint64_t left = odd; left; left &= left - 1) {
-              const uint32_t token = __ffsll((long long)left) - 1;
-              __syncwarp();
-              const float score = __uint_as_float(tmem_load1(here + token));
-              tmem_loaded();
-              const int2 place = m.place[token];
-              const char* const from = (const char*)p.c.v + head * p.head_step + (uint64_t)place.x * p.c.v_stride +
-                                       (uint64_t)place.y * p.token_step;
-              const float weight = exp2_of(__fmaf_rn(score, kCodes ? m.k_scale[token] : factor, -ref)) *
-                                   (kCodes ? m.v_scale[token] : 1.f);
-              if ((sees[token / 32] >> (token & 31)) & 1) {
-#pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                  float2 v;
-                  if (kCodes)
-                    v = unpack2<__half>(e4m3x2_to_f16x2(*(const uint16_t*)(from + c + j)));
-                  else
-                    v = unpack2<T>(*(const uint32_t*)(from + 2 * (c + j)));
-                  o[j] = __float_as_uint(__uint_as_float(o[j]) + weight * v.x);
-                  o[j + 1] = __float_as_uint(__uint_as_float(o[j + 1]) + weight * v.y);
-                }
-              }
-            }
-            __syncwarp();
-            tmem_store16(output + lanes + c, o);
+            tmem_stored();
           }
-          tmem_stored();
+          if (odd)
+            add_odd<T, kCodes>(m, output + lanes, here, odd, (uint64_t)sees[1] << 32 | sees[0], kCodes ? 1.f : factor, ref,
+                               (const char*)p.c.v + head * p.head_step, p.c.v_stride, p.token_step,
+                               (const char*)(p.c.v_scale + (kCodes ? head * p.scale_head_step : 0)), p.c.v_scale_stride,
+                               p.scale_token_step, !e4m3, p.c.width);
         }
-        float more = 0.f;
+        uint64_t sums = pair(__float_as_uint(sum), 0), more = pair(0, 0);
+        const uint64_t by = pair(__float_as_uint(kCodes ? 1.f : factor), __float_as_uint(kCodes ? 1.f : factor));
+        const uint64_t less = pair(__float_as_uint(-ref), __float_as_uint(-ref));
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float s[32];
-          uint32_t w[16];
-          fetch(h, s);
+        for (int j = 0; j < 32; j += 2) {
+          uint64_t y[2];
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            float y[4];
-#pragma unroll
-            for (int g = 0; g < 4; ++g) y[g] = exp2_of(kCodes ? s[j + g] - ref : __fmaf_rn(s[j + g], factor, -ref));
-            sum += y[0] + y[1];
-            more += y[2] + y[3];
-            if (kCodes) {
-              const float4 z = ((const float4*)m.v_scale)[8 * h + j / 4];
-              y[0] *= z.x, y[1] *= z.y, y[2] *= z.z, y[3] *= z.w;
-              if (masked) {  // the scale of what is not seen may be NaN
-#pragma unroll
-                for (int g = 0; g < 4; ++g)
-                  if (!((sees[h] >> (j + g)) & 1)) y[g] = 0.f;
-              }
-            }
-            w[j / 2] = pack2<W>(y[0], y[1]);
-            w[j / 2 + 1] = pack2<W>(y[2], y[3]);
+          for (int g = 0; g < 2; ++g) {
+            const uint64_t z = kCodes ? add2(x[j + g], less) : multiply_add2(x[j + g], by, less);
+            y[g] = pair(__float_as_uint(exp2_of(low(z))), __float_as_uint(exp2_of(high(z))));
           }
-          __syncwarp();
-          tmem_store16(here + 16 * h, w);  // over scores that have been fetched
+          sums = add2(sums, y[0]);
+          more = add2(more, y[1]);
+          if (kCodes) {
+            const ulonglong2 z = ((const ulonglong2*)m.v_scale)[j / 2];
+            y[0] = multiply2(y[0], z.x);
+            y[1] = multiply2(y[1], z.y);
+          }
+          w[j] = pack2<W>(low(y[0]), high(y[0]));
+          w[j + 1] = pack2<W>(low(y[1]), high(y[1]));
         }
-        sum += more;
+        sums = add2(sums, more);
+        sum = low(sums) + high(sums);
+        __syncwarp();
+        tmem_store32(here, w);  // over the scores
         tmem_stored();
         tensor_fence_before();
         barrier_arrive(smem_at(&s_weights[buffer]));
@@ -644,6 +839,7 @@ __global__ void __launch_bounds__(288, kPad <= 128 ? 2 : 1) attention_many_kerne
         const uint32_t qh = query_head(row_real ? row : 0, nd);
         char* const to = (char*)p.out.base + (uint64_t)(r.first + nd) * p.out.row_stride + qh * p.out.head_stride;
         const float by = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll 2
         for (uint32_t c = 0; c < p.c.width; c += 16) {
           uint32_t o[16];
           __syncwarp();
@@ -687,19 +883,8 @@ __global__ void __launch_bounds__(288, kPad <= 128 ? 2 : 1) attention_many_kerne
           group_sync(1, F::kWeights);
           if (s_last) {
             __threadfence();
-            constexpr uint32_t kQuads = kPad / 4;
-            for (uint32_t c = tid; c < rows * kQuads; c += F::kWeights) {
-              const uint32_t row_ = c / kQuads, quad = c % kQuads;
-              if (quad * 4 >= p.c.width) continue;
-              float l, m;
-              const float4 v = join_parts<F::kRows, kPad>(p, c0, c1, row_, quad, m, l);
-              uint32_t nd_;
-              const uint32_t qh_ = query_head(row_, nd_);
-              const float by_ = l == 0.f ? 0.f : 1.f / l;
-              *(uint2*)((char*)p.out.base + (uint64_t)(r.first + nd_) * p.out.row_stride + qh_ * p.out.head_stride + quad * 8) =
-                  make_uint2(pack2<T>(v.x * by_, v.y * by_), pack2<T>(v.z * by_, v.w * by_));
-              if (quad == 0) statistics(nd_, qh_, m, l);
-            }
+            const JoinedItem item_of = {r.first, rb * F::kRows, rows, head, c0, c1};
+            join_item<T, F::kRows, kPad, F::kWeights>(p, item_of);
           }
           group_sync(1, F::kWeights);  // s_last has been read
         }
@@ -711,8 +896,8 @@ __global__ void __launch_bounds__(288, kPad <= 128 ? 2 : 1) attention_many_kerne
     units += 2 * n;
   }
   // nothing is under way when the shared memory and TMEM are given back
-  if (warp >= 4 && warp < 8) copies_wait<0>();
-  if (tid == 256) {
+  if (warp >= 4 && warp < 7) copies_wait<0>();
+  if (tid == 224) {
     tensor_commit(smem_at(&s_drained));
     const uint64_t began = globaltimer_ns();
     while (!barrier_try(smem_at(&s_drained), 0) && globaltimer_ns() - began < kWaitLimitNs) {
@@ -721,7 +906,7 @@ __global__ void __launch_bounds__(288, kPad <= 128 ? 2 : 1) attention_many_kerne
   if (!go && tid == 0 && p.view.ctr) atomicOr((unsigned int*)&p.view.ctr->err, DB_ERR_TIMEOUT);
   tensor_fence_before();
   __syncthreads();
-  if (warp == 8)
+  if (warp == 7)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(F::kColumns));
 }
 

@@ -166,6 +166,9 @@ DEEP = [
     ("f16", "f16", 1, 7, 8, 5, 48, [(3000, 40), (2500, 9), (3, 3)], "random"),
     ("e4m3", "f16", 1, 64, 2, 4, 256, [(12000, 30)], "tree"),
     ("bf16", "bf16", 2, 128, 3, 8, 192, [(8000, 12), (777, 20)], "random"),
+    ("f16", "f16", 2, 48, 2, 4, 112, [(4000, 20), (1000, 11)], "tree"),
+    ("bf16", "bf16", 1, 8, 5, 8, 80, [(2000, 9), (1999, 33)], None),
+    ("bf16", "bf16", 1, 64, 2, 8, 256, [(2500, 9), (1000, 17)], "tree"),
     ("i8", "bf16", 1, 33, 16, 3, 32, [(1500, 13), (1400, 11), (1300, 12), (0, 30)], "tree"),
 ]
 
