@@ -79,7 +79,15 @@ struct Share {
   uint32_t ctas;         // that have any
   uint32_t request;      // the one that unit lo is of
   uint64_t before;       // units of the requests before it
+  const Request* near;   // that one and the next few, in shared memory
 };
+constexpr uint32_t kNear = 8;
+
+// A request that the CTA comes to: mostly one of the few that its plan looked
+// up together, since its length is three loads one after the other.
+__device__ __forceinline__ Request near_request(const AttnParams& p, const Share& s, uint32_t i) {
+  return i - s.request < kNear ? s.near[i - s.request] : attention_request(p, i);
+}
 
 // This CTA's units. Every thread calls it.
 template <uint32_t kRows, uint32_t kThreads>
@@ -87,6 +95,7 @@ __device__ __forceinline__ Share plan_share(const AttnParams& p) {
   __shared__ uint64_t s_scan[kThreads / 32];
   __shared__ uint64_t s_before;
   __shared__ uint32_t s_request;
+  __shared__ Request s_near[kNear];
   const uint32_t tid = threadIdx.x, n = p.view.n;
   Share s;
   uint64_t units = 0, excl, all;
@@ -130,6 +139,9 @@ __device__ __forceinline__ Share plan_share(const AttnParams& p) {
   __syncthreads();
   s.request = s_request;
   s.before = s_before;
+  s.near = s_near;
+  if (tid < kNear && s.request + tid < n) s_near[tid] = attention_request(p, s.request + tid);
+  __syncthreads();
   return s;
 }
 
@@ -242,57 +254,68 @@ struct JoinedItem {
   uint32_t first, row0, rows, head, c0, c1;
 };
 
-// Joins the parts of CTAs c0 to c1, in their order, and writes the answer: four
-// values of four rows at a time for each of kThreads threads, so that the loads
-// of one part are under way together.
+// Joins the parts of CTAs c0 to c1, in their order, and writes the answer. A
+// thread for each row finds the rows' maxima and sums, which go to `row_notes`
+// (16 bytes a row of shared memory); then kMany times four values a thread are
+// summed at a time, so that their loads are under way together. `group` is a
+// named barrier of the kThreads threads.
 template <typename T, uint32_t kRows, uint32_t kPad, uint32_t kThreads>
-static __device__ __noinline__ void join_item(const AttnParams& p, const JoinedItem item) {
-  constexpr uint32_t kQuads = kPad / 4, kMany = 4;
+static __device__ __noinline__ void join_item(const AttnParams& p, const JoinedItem item, float4* row_notes, uint32_t barrier) {
+  constexpr uint32_t kQuads = kPad / 4, kMany = 8, kPart = kRows * (kPad + 2);
+  const float* const parts = p.partial + (uint64_t)2 * item.c0 * kPart;  // the first is its CTA's second
+  const auto part_at = [&](uint32_t k) { return parts + (k == item.c0 ? kPart : (uint64_t)2 * (k - item.c0) * kPart); };
+  if (threadIdx.x < item.rows) {
+    const uint32_t row = threadIdx.x;
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+    for (uint32_t k = item.c0; k <= item.c1; ++k) {
+      const float mk = __ldcg(part_at(k) + kRows * kPad + row), lk = __ldcg(part_at(k) + kRows * kPad + kRows + row);
+      const float now = fmaxf(m, mk), by = now == -INFINITY ? 0.f : now;
+      l = l * exp2_of(m - by) + lk * exp2_of(mk - by);
+      m = now;
+    }
+    const uint32_t all = item.row0 + row, node = all / p.group, qh = item.head * p.group + (all - node * p.group);
+    const uint64_t to = (uint64_t)(item.first + node) * p.out.row_stride + qh * p.out.head_stride;
+    row_notes[row] = make_float4(m == -INFINITY ? 0.f : m, l == 0.f ? 0.f : 1.f / l, __uint_as_float((uint32_t)to),
+                                 __uint_as_float((uint32_t)(to >> 32)));
+    if (p.lse)
+      p.lse[(uint64_t)(item.first + node) * (p.c.heads * p.group) + qh] =
+          l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+  }
+  __syncwarp();
+  asm volatile("bar.sync %0, %1;" ::"r"(barrier), "n"(kThreads) : "memory");
+  const uint32_t all = item.rows * kQuads;
 #pragma unroll 1
-  for (uint32_t c = threadIdx.x; c < item.rows * kQuads; c += kThreads * kMany) {
-    float m[kMany], l[kMany];
+  for (uint32_t c = threadIdx.x; c < all; c += kThreads * kMany) {
     float4 v[kMany];
 #pragma unroll
-    for (uint32_t j = 0; j < kMany; ++j) {
-      m[j] = -INFINITY;
-      l[j] = 0.f;
-      v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+    for (uint32_t j = 0; j < kMany; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
     for (uint32_t k = item.c0; k <= item.c1; ++k) {
-      const float* const at = p.partial + (uint64_t)(2 * k + (k == item.c0)) * partial_floats(kRows, kPad);
-      float mk[kMany], lk[kMany];
+      const float* const at = part_at(k);
+      float m[kMany];
       float4 y[kMany];
 #pragma unroll
       for (uint32_t j = 0; j < kMany; ++j) {
-        const uint32_t of = min(c + j * kThreads, item.rows * kQuads - 1), row = of / kQuads, quad = of % kQuads;
-        mk[j] = __ldcg(at + kRows * kPad + row);
-        lk[j] = __ldcg(at + kRows * kPad + kRows + row);
-        y[j] = quad * 4 < p.c.width ? __ldcg((const float4*)(at + row * kPad) + quad) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const uint32_t of = min(c + j * kThreads, all - 1), row = of / kQuads, quad = min(of % kQuads, p.c.width / 4 - 1);
+        m[j] = __ldcg(at + kRows * kPad + row);
+        y[j] = __ldcg((const float4*)(at + row * kPad) + quad);
       }
 #pragma unroll
       for (uint32_t j = 0; j < kMany; ++j) {
-        const float now = fmaxf(m[j], mk[j]), by = now == -INFINITY ? 0.f : now;
-        const float a = exp2_of(m[j] - by), b = exp2_of(mk[j] - by);
-        l[j] = l[j] * a + lk[j] * b;
-        v[j].x = v[j].x * a + y[j].x * b, v[j].y = v[j].y * a + y[j].y * b;
-        v[j].z = v[j].z * a + y[j].z * b, v[j].w = v[j].w * a + y[j].w * b;
-        m[j] = now;
+        const float b = exp2_of(m[j] - row_notes[min(c + j * kThreads, all - 1) / kQuads].x);
+        v[j].x += y[j].x * b, v[j].y += y[j].y * b, v[j].z += y[j].z * b, v[j].w += y[j].w * b;
       }
     }
 #pragma unroll
     for (uint32_t j = 0; j < kMany; ++j) {
       const uint32_t of = c + j * kThreads;
-      if (of >= item.rows * kQuads) break;
-      const uint32_t row = item.row0 + of / kQuads, quad = of % kQuads, node = row / p.group;
-      const uint32_t qh = item.head * p.group + (row - node * p.group);
-      const float by = l[j] == 0.f ? 0.f : 1.f / l[j];
-      if (quad * 4 < p.c.width)
-        *(uint2*)((char*)p.out.base + (uint64_t)(item.first + node) * p.out.row_stride + qh * p.out.head_stride + quad * 8) =
-            make_uint2(pack2<T>(v[j].x * by, v[j].y * by), pack2<T>(v[j].z * by, v[j].w * by));
-      if (quad == 0 && p.lse)
-        p.lse[(uint64_t)(item.first + node) * (p.c.heads * p.group) + qh] =
-            l[j] == 0.f ? -INFINITY : m[j] * 0.6931471805599453f + logf(l[j]);
+      if (of < all && of % kQuads * 4 < p.c.width) {
+        const float4 n = row_notes[of / kQuads];
+        const uint64_t to = (uint64_t)__float_as_uint(n.w) << 32 | __float_as_uint(n.z);
+        *(uint2*)((char*)p.out.base + to + of % kQuads * 8) =
+            make_uint2(pack2<T>(v[j].x * n.y, v[j].y * n.y), pack2<T>(v[j].z * n.y, v[j].w * n.y));
+      }
     }
   }
 }
@@ -341,7 +364,7 @@ __global__ void __launch_bounds__(kAttnThreads, kPad > 128 ? 1 : 2) attention_fe
   uint32_t i = share.request;
   if (tid == 0) s_broken = 0;
   while (at < share.hi) {
-    const Request r = attention_request(p, i);
+    const Request r = near_request(p, share, i);
     const Extent e = extent_of<F::kRows>(p, r);
     if (at - before >= e.units) {
       before += e.units;
@@ -742,7 +765,7 @@ __global__ void __launch_bounds__(kAttnThreads, kPad > 128 ? 1 : 2) attention_fe
       if (s_last) {
         __threadfence();
         const JoinedItem item_of = {r.first, rb * F::kRows, rows, head, c0, c1};
-        join_item<T, F::kRows, kPad, kAttnThreads>(p, item_of);
+        join_item<T, F::kRows, kPad, kAttnThreads>(p, item_of, (float4*)smem, 0);
       }
     }
     at += t1 - t0;

@@ -3,7 +3,7 @@
 // tcgen05 products.
 //
 // A CTA has three kinds of warps that hand tiles of 64 tokens on by mbarriers:
-//   loaders (3 warps)   keys and values from their pages into a ring of tiles, by
+//   loaders (2 or 3)    keys and values from their pages into a ring of tiles, by
 //                       16-byte asynchronous copies; 8-bit codes come into a
 //                       ring of their own, from which they are widened
 //   one issuing thread  S = Q K^T into TMEM (two buffers), O += P V from TMEM
@@ -37,9 +37,14 @@ struct Many {
   static constexpr uint32_t kRows = 128;
   // 256 threads: 128 registers each with two CTAs an SM (9 warps would leave 96)
   static constexpr uint32_t kThreads = 256;
-  static constexpr uint32_t kWeights = 128, kLoaders = 96;
+  static constexpr uint32_t kWeights = 128;
+  // Loaders that have units in turn. As they divide the ring, a place of it is
+  // always the same warp's, which so sees every phase of its barrier (a wait by
+  // parity is true too early when another phase lies between).
+  static constexpr uint32_t kLoaderWarps = kCodes ? 3 : 2;
   static constexpr uint32_t kUnit = kTile * kPad * 2;  // keys or values of a tile
   static constexpr uint32_t kUnits = kCodes ? 3 : kPad >= 128 ? 4 : 6;
+  static_assert(kUnits % kLoaderWarps == 0, "see kLoaderWarps");
   static constexpr uint32_t kQuery = kRows * kPad * 2;
   static constexpr uint32_t kRaw = kTile * kPad;       // codes of a unit
   static constexpr uint32_t kRaws = kCodes ? 3 : 0;
@@ -355,7 +360,7 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
   uint32_t odd_phases = 0;
   bool go = true;
   while (go && at < share.hi) {
-    const Request r = attention_request(p, request);
+    const Request r = near_request(p, share, request);
     const Extent e = extent_of<F::kRows>(p, r);
     if (at - before >= e.units) {
       before += e.units;
@@ -369,10 +374,10 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
     const uint32_t rows = min(F::kRows, r.rows * p.group - rb * F::kRows);
     const uint32_t base = r.length - r.rows;  // tokens before the request's own
 
-    if (warp >= 4 && warp < 7) {
+    if (warp >= 4 && warp < 4 + F::kLoaderWarps) {
       // ------------------------------------------------------------- loaders
-      // A warp has every third unit to itself, and waits for no other.
-      const uint32_t me = tid - F::kWeights, mine = warp - F::kWeights / 32;
+      // A warp has every second or third unit to itself, and waits for no other.
+      const uint32_t mine = warp - F::kWeights / 32, own = (mine + F::kLoaderWarps - units % F::kLoaderWarps) % F::kLoaderWarps;
       const int32_t* const table = p.view.table + (uint64_t)r.seq * p.view.columns;
       constexpr uint32_t kChunks = kPad / 8, kRawChunks = kCodes ? kPad / 16 : kChunks;  // 16-byte chunks of a row
       constexpr uint32_t kStep = 32 / kRawChunks, kEach = kTile / kStep;  // a lane has the same chunk of every kStep-th token
@@ -443,12 +448,24 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
 #pragma unroll
         for (uint32_t h = 0; h < 2; ++h) {
           const uint32_t there = __ballot_sync(kFull, w.at[h].x >= 0);
-#pragma unroll 4
-          for (uint32_t k = h * kEach / 2; k < (h + 1) * kEach / 2; ++k) {
-            const uint32_t token = token0 + k * kStep;
-            const uint64_t at = __shfl_sync(kFull, off[h], token & 31);
-            const bool real = whole || (there >> (token & 31)) & 1;
-            if (has) copy16(place(token, k), from + (real ? at : 0), real);
+          constexpr uint32_t kBatch = kEach / 2 < 8 ? kEach / 2 : 8;  // addresses first, then their copies
+#pragma unroll 1
+          for (uint32_t k0 = h * kEach / 2; k0 < (h + 1) * kEach / 2; k0 += kBatch) {
+            uint64_t at[kBatch];
+#pragma unroll
+            for (uint32_t k = 0; k < kBatch; ++k) at[k] = __shfl_sync(kFull, off[h], (token0 + (k0 + k) * kStep) & 31);
+            if (!has) continue;
+            if (whole) {
+#pragma unroll
+              for (uint32_t k = 0; k < kBatch; ++k) copy16(place(token0 + (k0 + k) * kStep, k0 + k), from + at[k], true);
+            } else {
+#pragma unroll
+              for (uint32_t k = 0; k < kBatch; ++k) {
+                const uint32_t token = token0 + (k0 + k) * kStep;
+                const bool real = (there >> (token & 31)) & 1;
+                copy16(place(token, k0 + k), from + (real ? at[k] : 0), real);
+              }
+            }
           }
         }
         copies_commit();
@@ -458,25 +475,27 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
       // weights. at(token, k): where this lane's chunk is.
       const auto check = [&](uint32_t t, const Places& w, auto at) {
         uint32_t odd[2] = {0, 0};
-#pragma unroll 2
-        for (uint32_t k = 0; k < kEach; ++k) {
-          const uint32_t token = token0 + k * kStep;
-          uint4* const mine_at = (uint4*)(smem + at(token, k));
-          bool bad = false;
-          if (has) {
-            const uint4 v = *mine_at;
-            if (kCodes) {
-              const auto nan4 = [](uint32_t c) { return ((c & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; };
-              bad = e4m3 && (nan4(v.x) | nan4(v.y) | nan4(v.z) | nan4(v.w));
-            } else {
-              bad = not_finite2<W>(v.x) || not_finite2<W>(v.y) || not_finite2<W>(v.z) || not_finite2<W>(v.w);
-            }
+        const auto bad_at = [&](uint32_t k) __attribute__((always_inline)) {
+          const uint4 v = *(const uint4*)(smem + at(token0 + k * kStep, k));
+          if (kCodes) {
+            const auto nan4 = [](uint32_t c) { return ((c & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; };
+            return e4m3 && (nan4(v.x) | nan4(v.y) | nan4(v.z) | nan4(v.w));
           }
-          const uint32_t votes = __ballot_sync(kFull, bad) >> token0 * kRawChunks % 32;
-          if (votes & (kRawChunks == 32 ? 0xFFFFFFFFu : (1u << kRawChunks % 32) - 1)) {
-            if (has) *mine_at = make_uint4(0, 0, 0, 0);
-            odd[0] |= token < 32 ? 1u << (token & 31) : 0u;
-            odd[1] |= token < 32 ? 0u : 1u << (token & 31);
+          return not_finite2<W>(v.x) || not_finite2<W>(v.y) || not_finite2<W>(v.z) || not_finite2<W>(v.w);
+        };
+        bool any = false;
+#pragma unroll 8
+        for (uint32_t k = 0; k < kEach; ++k) any |= has && bad_at(k);
+        if (__any_sync(kFull, any)) {
+#pragma unroll 1
+          for (uint32_t k = 0; k < kEach; ++k) {
+            const uint32_t token = token0 + k * kStep;
+            const uint32_t votes = __ballot_sync(kFull, has && bad_at(k)) >> token0 * kRawChunks % 32;
+            if (votes & (kRawChunks == 32 ? 0xFFFFFFFFu : (1u << kRawChunks % 32) - 1)) {
+              if (has) *(uint4*)(smem + at(token, k)) = make_uint4(0, 0, 0, 0);
+              odd[0] |= token < 32 ? 1u << (token & 31) : 0u;
+              odd[1] |= token < 32 ? 0u : 1u << (token & 31);
+            }
           }
         }
         TileNotes& m = s_notes[(tiles + t - t0) % F::kMeta];
@@ -495,7 +514,7 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
         barrier_arrive(smem_at(&s_odd[(tiles + t - t0) % F::kMeta]));
       };
 
-      Places w = look(mine);
+      Places w = look(own);  // its first unit of the item
       if constexpr (kCodes) {
         // A lane widens the codes that it has copied itself.
         const uint32_t raw = query + F::kQuery + mine * F::kRaw + lane * 16;
@@ -521,12 +540,12 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
             }
           }
         };
-        if (mine < 2 * n) ask(mine);
-        for (uint32_t u = mine; u < 2 * n; u += 3) {
+        if (own < 2 * n) ask(own);
+        for (uint32_t u = own; u < 2 * n; u += F::kLoaderWarps) {
           uint32_t t;
           bool key;
           unit_of(u, t, key);
-          Places next = look(u + 3);
+          Places next = look(u + F::kLoaderWarps);
           barrier_wait(smem_at(&s_empty[slot_of(u)]), phase_of(u), &s_failed);
           __syncwarp();
           if (key) {
@@ -549,13 +568,19 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
           const auto widen_all = [&](auto as, auto four) __attribute__((always_inline)) {
             typedef decltype(as) H;
             constexpr bool kFour = decltype(four)::value;
-#pragma unroll 4
-            for (uint32_t k = 0; k < kEach; ++k) {
-              const uint32_t token = token0 + k * kStep;
-              const uint4 c = *(const uint4*)(from + k * 512);
-              const uint2 y[4] = {widen4<H>(c.x, kFour), widen4<H>(c.y, kFour), widen4<H>(c.z, kFour), widen4<H>(c.w, kFour)};
-              *(uint4*)(to + token * 128 + (((2 * chunk) & 7) ^ (token & 7)) * 16) = make_uint4(y[0].x, y[0].y, y[1].x, y[1].y);
-              *(uint4*)(to + token * 128 + (((2 * chunk + 1) & 7) ^ (token & 7)) * 16) = make_uint4(y[2].x, y[2].y, y[3].x, y[3].y);
+            constexpr uint32_t kBatch = kEach < 8 ? kEach : 8;
+#pragma unroll 1
+            for (uint32_t k0 = 0; k0 < kEach; k0 += kBatch) {
+              uint4 c[kBatch];
+#pragma unroll
+              for (uint32_t k = 0; k < kBatch; ++k) c[k] = *(const uint4*)(from + (k0 + k) * 512);
+#pragma unroll
+              for (uint32_t k = 0; k < kBatch; ++k) {
+                const uint32_t token = token0 + (k0 + k) * kStep;
+                const uint2 y[4] = {widen4<H>(c[k].x, kFour), widen4<H>(c[k].y, kFour), widen4<H>(c[k].z, kFour), widen4<H>(c[k].w, kFour)};
+                *(uint4*)(to + token * 128 + (((2 * chunk) & 7) ^ (token & 7)) * 16) = make_uint4(y[0].x, y[0].y, y[1].x, y[1].y);
+                *(uint4*)(to + token * 128 + (((2 * chunk + 1) & 7) ^ (token & 7)) * 16) = make_uint4(y[2].x, y[2].y, y[3].x, y[3].y);
+              }
             }
           };
           if (has) {
@@ -574,14 +599,15 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
           hand_on(u);
           __syncwarp();
           w = next;
-          if (u + 3 < 2 * n) ask(u + 3);
+          if (u + F::kLoaderWarps < 2 * n) ask(u + F::kLoaderWarps);
         }
       } else {
         uint32_t waiting = 0xFFFFFFFFu;  // a unit whose copies are under way
-        for (uint32_t u = mine; u < 2 * n; u += 3) {
+        for (uint32_t u = own; u < 2 * n; u += F::kLoaderWarps) {
           uint32_t t;
           bool key;
           unit_of(u, t, key);
+          const Places next = look(u + F::kLoaderWarps);
           settle(w);
           const bool whole = all_seen(t, w);
           const uint32_t bar = smem_at(&s_empty[slot_of(u)]);
@@ -609,7 +635,7 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
             copies_wait<0>();
             check(t, w, place);
           }
-          w = look(u + 3);
+          w = next;
         }
         if (waiting != 0xFFFFFFFFu) {
           copies_wait<0>();
@@ -660,13 +686,35 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
         go = ok;
       }
       go = __shfl_sync(kFull, go, 0);
-    } else {
+    } else if (warp < 4) {
       // -------------------------------------------------------------- weights
       const uint32_t row = tid, lanes = (warp * 32) << 16;
       const bool row_real = row < rows;
       const uint32_t all = rb * F::kRows + (row_real ? row : 0), node = all / p.group;
       const uint32_t* const mask = p.mask ? p.mask + (uint64_t)(r.first + node) * p.mask_words : nullptr;
       const float factor = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
+      {
+        // The row's query; the products with the one before were over when its
+        // last scores came.
+        constexpr uint32_t kFetch = kPad == 64 ? 8 : 16;
+        const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u, keep = p.scale_log2 == 0.f ? 0u : 0xFFFFFFFFu;
+        const char* const from = (const char*)p.q.base + (uint64_t)(r.first + node) * p.q.row_stride +
+                                 (head * p.group + (all - node * p.group)) * p.q.head_stride;
+#pragma unroll 1
+        for (uint32_t c0 = 0; c0 < p.c.width / 8; c0 += kFetch) {
+          uint4 v[kFetch];
+#pragma unroll
+          for (uint32_t c = 0; c < kFetch; ++c)
+            v[c] = row_real && c0 + c < p.c.width / 8 ? __ldg((const uint4*)from + c0 + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (uint32_t c = 0; c < kFetch; ++c) {
+            v[c].x = (v[c].x ^ flip) & keep, v[c].y = (v[c].y ^ flip) & keep, v[c].z = (v[c].z ^ flip) & keep, v[c].w = (v[c].w ^ flip) & keep;
+            *(uint4*)(smem + F::kUnits * F::kUnit + (c0 + c) / 8 * kQueryPanel + row * 128 + ((c & 7) ^ (row & 7)) * 16) = v[c];
+          }
+        }
+        writes_to_async_proxy();
+        barrier_arrive(smem_at(&s_asked));
+      }
       // Weights are exp2(score - ref). ref is a score that was the largest, and
       // for codes also takes in the size of the values' scales, which P has as
       // a factor, so that P stays in the middle of f16's range.
@@ -681,22 +729,6 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
         tmem_stored();
       }
       bool ok = true;
-      {
-        // The row's query; the products with the one before were over when its
-        // last scores came.
-        const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u, keep = p.scale_log2 == 0.f ? 0u : 0xFFFFFFFFu;
-        const char* const from = (const char*)p.q.base + (uint64_t)(r.first + node) * p.q.row_stride +
-                                 (head * p.group + (all - node * p.group)) * p.q.head_stride;
-#pragma unroll 8
-        for (uint32_t c = 0; c < kPad / 8; ++c) {
-          if (c >= p.c.width / 8) break;
-          uint4 v = row_real ? __ldg((const uint4*)from + c) : make_uint4(0, 0, 0, 0);
-          v.x = (v.x ^ flip) & keep, v.y = (v.y ^ flip) & keep, v.z = (v.z ^ flip) & keep, v.w = (v.w ^ flip) & keep;
-          *(uint4*)(smem + F::kUnits * F::kUnit + c / 8 * kQueryPanel + row * 128 + ((c & 7) ^ (row & 7)) * 16) = v;
-        }
-        writes_to_async_proxy();
-        barrier_arrive(smem_at(&s_asked));
-      }
       for (uint32_t k = 0; k < n; ++k) {
         const uint32_t tile = tiles + k, buffer = tile & 1, t = t0 + k;
         const uint32_t here = scores + buffer * kTile + lanes;
@@ -884,7 +916,8 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
           if (s_last) {
             __threadfence();
             const JoinedItem item_of = {r.first, rb * F::kRows, rows, head, c0, c1};
-            join_item<T, F::kRows, kPad, F::kWeights>(p, item_of);
+            // the queries' place is free: all products with them are made
+            join_item<T, F::kRows, kPad, F::kWeights>(p, item_of, (float4*)(smem + F::kUnits * F::kUnit), 1);
           }
           group_sync(1, F::kWeights);  // s_last has been read
         }
