@@ -118,15 +118,23 @@ __device__ __forceinline__ void store8(char* p, const float* x) {
   }
 }
 
-// The largest magnitude of the lanes that share a row, as bits: of floats
-// without their sign, larger bits are larger values, infinities above every
-// number and NaN above those.
-__device__ __forceinline__ uint32_t largest_bits(const float* x, uint32_t lanes) {
+// The largest magnitude of the lanes that share a row, as a float's bits: of
+// values without their sign, larger bits are larger values, infinities above
+// every number and NaN above those. 16-bit values are compared in pairs.
+template <typename T>
+__device__ __forceinline__ uint32_t largest_bits(const Eight<T>& e, uint32_t lanes) {
   uint32_t m = 0;
+  if (sizeof(T) == 4) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(x[j]) & 0x7FFFFFFFu);
-  for (uint32_t o = lanes / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
-  return m;
+    for (uint32_t j = 0; j < sizeof(T) / 2; ++j)
+      m = max(max(max(m, e.w[j].x & 0x7FFFFFFFu), max(e.w[j].y & 0x7FFFFFFFu, e.w[j].z & 0x7FFFFFFFu)), e.w[j].w & 0x7FFFFFFFu);
+    for (uint32_t o = lanes / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+    return m;
+  }
+  m = __vmaxu2(__vmaxu2(e.w[0].x & 0x7FFF7FFFu, e.w[0].y & 0x7FFF7FFFu), __vmaxu2(e.w[0].z & 0x7FFF7FFFu, e.w[0].w & 0x7FFF7FFFu));
+  for (uint32_t o = lanes / 2; o; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(kFull, m, o));
+  m = max(m & 0xFFFFu, m >> 16);
+  return __float_as_uint(unpack2<typename std::conditional<sizeof(T) == 4, __half, T>::type>(m).x);
 }
 
 __device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
@@ -135,20 +143,25 @@ __device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
   return r;
 }
 
-// Codes of eight values and, in `scale`, their row's scale.
+// A row's scale and what its values are multiplied by (0: codes are 0).
 template <bool kE4m3>
-__device__ __forceinline__ uint2 quantise8(const float* x, uint32_t top, float& scale) {
-  const float largest = kE4m3 ? 448.f : 127.f;
-  if (top >= 0x7F800000u) {
-    scale = __uint_as_float(0x7FC00000u);
-    return make_uint2(0, 0);
-  }
-  const float a = __uint_as_float(top), by = __fdiv_rn(largest, a);
+__device__ __forceinline__ void scale_of(uint32_t top, float& scale, float& by) {
+  const float largest = kE4m3 ? 448.f : 127.f, a = __uint_as_float(top);
+  by = __fdiv_rn(largest, a);
   scale = __fdiv_rn(a, largest);
-  if (scale == 0.f || isinf(by)) {
-    scale = 0.f;
-    return make_uint2(0, 0);
+  if (top >= 0x7F800000u) {
+    by = 0.f;
+    scale = __uint_as_float(0x7FC00000u);
+  } else if (scale == 0.f || isinf(by)) {
+    by = scale = 0.f;
   }
+}
+
+// Codes of eight values. I8: adding 1.5 * 2^23 leaves the nearest whole number,
+// ties to even, in a float's low bits; products are at most 127 and its last
+// place, so nothing has to be cut.
+template <bool kE4m3>
+__device__ __forceinline__ uint2 codes8(const float* x, float by) {
   uint32_t w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -156,16 +169,13 @@ __device__ __forceinline__ uint2 quantise8(const float* x, uint32_t top, float& 
     if (kE4m3) {
       w[h] = e4m3_pair(y[0] * by, y[1] * by) | e4m3_pair(y[2] * by, y[3] * by) << 16;
     } else {
-      uint32_t c = 0;
+      uint32_t c[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int q = max(-127, min(127, __float2int_rn(y[j] * by)));
-        c |= (uint32_t)(q & 0xFF) << (8 * j);
-      }
-      w[h] = c;
+      for (int j = 0; j < 4; ++j) c[j] = __float_as_uint(__fadd_rn(__fmul_rn(y[j], by), 12582912.f));
+      w[h] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
     }
   }
-  return make_uint2(w[0], w[1]);
+  return by > 0.f ? make_uint2(w[0], w[1]) : make_uint2(0, 0);
 }
 
 // Where a row of the batch has its token: found one row ahead of the data, so
@@ -198,7 +208,7 @@ __device__ __forceinline__ Place find_place(const CacheView& v, uint32_t r, uint
 // One warp: rows [r0, r1) of the batch. kType: what the pages hold; kUnroll:
 // heads' rows of a lane under way.
 template <typename Src, int kType>
-__global__ void __launch_bounds__(kThreads) cache_write_kernel(const MoveParams p) {
+__global__ void __launch_bounds__(kThreads, 3) cache_write_kernel(const MoveParams p) {
   constexpr bool kCodes = kType == DB_E4M3 || kType == DB_I8;
   constexpr int kUnroll = sizeof(Src) == 4 ? 4 : 8;
   wait_for_prerequisites();
@@ -210,9 +220,16 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const MoveParams 
   const uint64_t r0 = warp * p.chunk;
   const uint32_t r1 = (uint32_t)min(r0 + p.chunk, (uint64_t)v.rows);
   if (r0 >= r1) return;
-  const uint32_t lanes = p.lanes, at = (lane & (lanes - 1)) * 8, per = 32 / lanes;
-  const uint32_t heads = p.c.heads, units = 2 * heads;
+  // kHalf heads' keys and as many values at a time: a lane has eight values of
+  // head h0 + j * per + lane / lanes
+  constexpr int kHalf = kUnroll / 2;
+  const uint32_t lanes = p.lanes, at = (lane & (lanes - 1)) * 8, per = 32 / lanes, first_head = lane / lanes;
+  const uint32_t heads = p.c.heads;
   const bool mine = at < p.c.width;
+  const uint64_t k_next = per * p.k.head_stride, v_next = per * p.v.head_stride, next = per * p.head_step;
+  const char* const k_from = (const char*)p.k.base + first_head * p.k.head_stride + at * sizeof(Src);
+  const char* const v_from = (const char*)p.v.base + first_head * p.v.head_stride + at * sizeof(Src);
+  const uint64_t in_page = first_head * p.head_step + at * (kCodes ? 1 : 2);
   const auto position = [&](uint32_t, const Request& q, uint32_t j) { return (uint64_t)q.length - q.rows + j; };
   uint32_t i = find_request(v.start, v.n, (uint32_t)r0);
   Request q = read_request(v, i, true);
@@ -221,24 +238,24 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const MoveParams 
   for (uint32_t r = (uint32_t)r0; r < r1; ++r) {
     Place now = w;
     const bool go = has;
-    bool looked = false;
-    for (uint32_t u0 = 0; u0 < units; u0 += per * kUnroll) {
+    for (uint32_t h0 = 0; h0 < heads; h0 += per * kHalf) {
       Eight<Src> e[kUnroll];
       if (go) {
+        const char* const kf = k_from + r * p.k.row_stride + h0 * p.k.head_stride;
+        const char* const vf = v_from + r * p.v.row_stride + h0 * p.v.head_stride;
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-          const uint32_t u = u0 + k * per + lane / lanes;
+        for (int j = 0; j < kHalf; ++j) {
+          if (h0 + j * per >= heads) break;
+          const bool real = mine && h0 + j * per + first_head < heads;
 #pragma unroll
-          for (uint32_t j = 0; j < sizeof(Src) / 2; ++j) e[k].w[j] = make_uint4(0, 0, 0, 0);
-          if (u < units && mine) {
-            const bool val = u >= heads;
-            const db_cache_rows& s = val ? p.v : p.k;
-            e[k] = load8<Src>((const char*)s.base + r * s.row_stride + (val ? u - heads : u) * s.head_stride + at * sizeof(Src));
+          for (uint32_t z = 0; z < sizeof(Src) / 2; ++z) e[j].w[z] = e[j + kHalf].w[z] = make_uint4(0, 0, 0, 0);
+          if (real) {
+            e[j] = load8<Src>(kf + j * k_next);
+            e[j + kHalf] = load8<Src>(vf + j * v_next);
           }
         }
       }
-      if (!looked) {
-        looked = true;
+      if (h0 == 0) {
         if (r + 1 < r1) w = find_place(v, r + 1, i, q, has, true, position);
         if (go && now.held && now.page >= v.n_pages) {
           now.held = false;
@@ -246,31 +263,59 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const MoveParams 
         }
       }
       if (!go) break;
-      const uint64_t in = now.slot * p.token_step;
+      const uint64_t off = now.slot * p.token_step + h0 * p.head_step + in_page;
+      char* const kt = (char*)p.c.k + now.page * p.c.k_stride + off;
+      char* const vt = (char*)p.c.v + now.page * p.c.v_stride + off;
+      float by[kUnroll];
+      if (kCodes) {
+        // A row's largest magnitude is in all of its lanes: lane j of them
+        // divides for the j-th of the lane group's rows (few lanes: for each).
+        const uint32_t of = lane & (lanes - 1);
+        float my_scale = 0.f, my_by = 0.f;
+        if (lanes >= kUnroll) {
+          uint32_t top = 0;
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        if (u0 + k * per >= units) break;
-        const uint32_t u = u0 + k * per + lane / lanes;
-        const bool val = u >= heads;
-        const uint32_t head = val ? u - heads : u;
-        char* const to = (char*)(val ? p.c.v : p.c.k) + now.page * (val ? p.c.v_stride : p.c.k_stride) + in + head * p.head_step;
-        float x[8];
-        floats8(e[k], x);
-        const bool out = u < units && mine && now.held;
-        if (kCodes) {
-          const uint32_t top = largest_bits(x, lanes);
-          float scale;
-          const uint2 c = quantise8<kType == DB_E4M3>(x, top, scale);
-          if (out) {
-            *(uint2*)(to + at) = c;
-            if (at == 0) {
-              char* const s = (char*)(val ? p.c.v_scale : p.c.k_scale) + now.page * (val ? p.c.v_scale_stride : p.c.k_scale_stride);
-              ((float*)s)[now.slot * p.scale_token_step + head * p.scale_head_step] = scale;
+          for (int j = 0; j < kUnroll; ++j) {
+            if (h0 + (j >= kHalf ? j - kHalf : j) * per >= heads) continue;
+            const uint32_t t = largest_bits(e[j], lanes);
+            if (of == j) top = t;
+          }
+          scale_of<kType == DB_E4M3>(top, my_scale, my_by);
+#pragma unroll
+          for (int j = 0; j < kUnroll; ++j) by[j] = __shfl_sync(kFull, my_by, (lane & ~(lanes - 1)) | j);
+          const bool val = of >= kHalf;
+          const uint32_t head = h0 + (val ? of - kHalf : of) * per + first_head;
+          if (of < kUnroll && head < heads && now.held) {
+            char* const to = (char*)(val ? p.c.v_scale : p.c.k_scale) + now.page * (val ? p.c.v_scale_stride : p.c.k_scale_stride);
+            ((float*)to)[now.slot * p.scale_token_step + head * p.scale_head_step] = my_scale;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < kUnroll; ++j) {
+            if (h0 + (j >= kHalf ? j - kHalf : j) * per >= heads) continue;
+            scale_of<kType == DB_E4M3>(largest_bits(e[j], lanes), my_scale, by[j]);
+            const bool val = j >= kHalf;
+            const uint32_t head = h0 + (val ? j - kHalf : j) * per + first_head;
+            if (of == 0 && head < heads && now.held) {
+              char* const to = (char*)(val ? p.c.v_scale : p.c.k_scale) + now.page * (val ? p.c.v_scale_stride : p.c.k_scale_stride);
+              ((float*)to)[now.slot * p.scale_token_step + head * p.scale_head_step] = my_scale;
             }
           }
-        } else if (out) {
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j) {
+        const int jj = j >= kHalf ? j - kHalf : j;
+        if (h0 + jj * per >= heads) continue;
+        char* const to = (j >= kHalf ? vt : kt) + jj * next;
+        float x[8];
+        floats8(e[j], x);
+        if (kCodes) {
+          const uint2 c = codes8<kType == DB_E4M3>(x, by[j]);
+          if (mine && now.held && h0 + jj * per + first_head < heads) *(uint2*)to = c;
+        } else if (mine && now.held && h0 + jj * per + first_head < heads) {
           typedef typename std::conditional<kType == DB_F16, __half, __nv_bfloat16>::type H;
-          store8<H>(to + 2 * at, x);
+          store8<H>(to, x);
         }
       }
     }
@@ -293,8 +338,11 @@ __device__ __forceinline__ void held_floats(const typename Held<kType>::type& c,
         const float2 a = unpack2<__half>(e4m3x2_to_f16x2(w[h])), b = unpack2<__half>(e4m3x2_to_f16x2(w[h] >> 16));
         x[4 * h] = a.x * scale, x[4 * h + 1] = a.y * scale, x[4 * h + 2] = b.x * scale, x[4 * h + 3] = b.y * scale;
       } else {
+        // a code and 128 as the low bits of 2^23
+        const uint32_t u = w[h] ^ 0x80808080u;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[4 * h + j] = (float)(int8_t)(w[h] >> (8 * j)) * scale;
+        for (int j = 0; j < 4; ++j)
+          x[4 * h + j] = __fmul_rn(__fsub_rn(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7540 + j)), 8388736.f), scale);
       }
     }
   } else {
@@ -306,7 +354,7 @@ __device__ __forceinline__ void held_floats(const typename Held<kType>::type& c,
 }
 
 template <typename Dst, int kType>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(const MoveParams p) {
+__global__ void __launch_bounds__(kThreads, 4) cache_read_kernel(const MoveParams p) {
   constexpr bool kCodes = kType == DB_E4M3 || kType == DB_I8;
   constexpr uint32_t kBytes = kCodes ? 1 : 2;
   constexpr int kUnroll = 8;
@@ -320,9 +368,14 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const MoveParams p
   const uint64_t r0 = warp * p.chunk;
   const uint32_t r1 = (uint32_t)min(r0 + p.chunk, (uint64_t)v.rows);
   if (r0 >= r1) return;
-  const uint32_t lanes = p.lanes, at = (lane & (lanes - 1)) * 8, per = 32 / lanes;
-  const uint32_t heads = p.c.heads, units = 2 * heads;
+  constexpr int kHalf = kUnroll / 2;
+  const uint32_t lanes = p.lanes, at = (lane & (lanes - 1)) * 8, per = 32 / lanes, first_head = lane / lanes;
+  const uint32_t heads = p.c.heads;
   const bool mine = at < p.c.width;
+  const uint64_t k_next = per * p.k.head_stride, v_next = per * p.v.head_stride, next = per * p.head_step;
+  char* const k_to = (char*)p.k.base + first_head * p.k.head_stride + at * sizeof(Dst);
+  char* const v_to = (char*)p.v.base + first_head * p.v.head_stride + at * sizeof(Dst);
+  const uint64_t in_page = first_head * p.head_step + at * kBytes;
   const auto position = [&](uint32_t i, const Request&, uint32_t j) {
     return (uint64_t)(p.first ? (uint32_t)__ldg(p.first + i) : 0) + j;
   };
@@ -337,40 +390,40 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const MoveParams p
       now.held = false;
       if (lane == 0) report_table(v.ctr);
     }
-    bool looked = false;
-    for (uint32_t u0 = 0; u0 < units; u0 += per * kUnroll) {
+    for (uint32_t h0 = 0; h0 < heads; h0 += per * kHalf) {
       V c[kUnroll];
       float scale[kUnroll];
+      const uint64_t off = now.slot * p.token_step + h0 * p.head_step + in_page;
+      const char* const kf = (const char*)p.c.k + now.page * p.c.k_stride + off;
+      const char* const vf = (const char*)p.c.v + now.page * p.c.v_stride + off;
+      const uint32_t of = now.slot * p.scale_token_step + (h0 + first_head) * p.scale_head_step;
+      const float* const ks = (const float*)((const char*)p.c.k_scale + now.page * p.c.k_scale_stride) + (kCodes ? of : 0);
+      const float* const vs = (const float*)((const char*)p.c.v_scale + now.page * p.c.v_scale_stride) + (kCodes ? of : 0);
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        const uint32_t u = u0 + k * per + lane / lanes;
-        c[k] = V{};
-        scale[k] = 1.f;
-        if (go && u < units && mine && now.held) {
-          const bool val = u >= heads;
-          const uint32_t head = val ? u - heads : u;
-          c[k] = __ldcs((const V*)((const char*)(val ? p.c.v : p.c.k) + now.page * (val ? p.c.v_stride : p.c.k_stride) +
-                                   now.slot * p.token_step + head * p.head_step + at * kBytes));
+      for (int j = 0; j < kHalf; ++j) {
+        if (h0 + j * per >= heads) break;
+        c[j] = c[j + kHalf] = V{};
+        scale[j] = scale[j + kHalf] = 0.f;
+        if (go && mine && now.held && h0 + j * per + first_head < heads) {
+          c[j] = __ldcs((const V*)(kf + j * next));
+          c[j + kHalf] = __ldcs((const V*)(vf + j * next));
           if (kCodes) {
-            const char* const s = (const char*)(val ? p.c.v_scale : p.c.k_scale) + now.page * (val ? p.c.v_scale_stride : p.c.k_scale_stride);
-            scale[k] = ((const float*)s)[now.slot * p.scale_token_step + head * p.scale_head_step];
+            scale[j] = ks[j * per * p.scale_head_step];
+            scale[j + kHalf] = vs[j * per * p.scale_head_step];
           }
         }
       }
-      if (!looked) {
-        looked = true;
-        if (r + 1 < r1) w = find_place(v, r + 1, i, q, has, false, position);
-      }
+      if (h0 == 0 && r + 1 < r1) w = find_place(v, r + 1, i, q, has, false, position);
       if (!go) break;
+      char* const kt = k_to + r * p.k.row_stride + h0 * p.k.head_stride;
+      char* const vt = v_to + r * p.v.row_stride + h0 * p.v.head_stride;
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        const uint32_t u = u0 + k * per + lane / lanes;
-        if (u < units && mine) {
-          const bool val = u >= heads;
-          const db_cache_rows& d = val ? p.v : p.k;
+      for (int j = 0; j < kUnroll; ++j) {
+        const int jj = j >= kHalf ? j - kHalf : j;
+        if (mine && h0 + jj * per + first_head < heads) {
           float x[8];
-          held_floats<kType>(c[k], scale[k], x);
-          store8<Dst>((char*)d.base + r * d.row_stride + (val ? u - heads : u) * d.head_stride + at * sizeof(Dst), x);
+          held_floats<kType>(c[j], scale[j], x);
+          store8<Dst>(j >= kHalf ? vt + jj * v_next : kt + jj * k_next, x);
         }
       }
     }

@@ -17,9 +17,15 @@
 namespace db {
 namespace {
 
-constexpr uint32_t kThreads = 512, kWarps = kThreads / 32;
+constexpr uint32_t kThreads = 256, kWarps = kThreads / 32;
 constexpr uint32_t kMaxNodes = 1024;
 constexpr uint32_t kMaxCluster = 8;
+// A request gets twice as many CTAs while each still has kMinTokens tokens and
+// all together are at most kCtas an SM: a walk's rows follow one another, so a
+// row should be short for each. 256 trees over 50,001 tokens: 117 us with at
+// most 4 CTAs an SM, 76 with 8, 75 with 16; 48 chains over 32,000: 9.0 us with
+// 4,096 tokens at least, 8.3 with 2,048.
+constexpr uint32_t kMinTokens = 2048, kCtas = 16;
 constexpr int kUnroll = 8;
 
 struct VerifyParams {
@@ -104,19 +110,29 @@ __device__ __forceinline__ void sum_row(const VerifyParams& a, Shared& s, uint32
   const T* const q = kDraft ? (const T*)a.q + row * a.q_stride : nullptr;
   const uint32_t t0 = min((uint64_t)g * a.range, (uint64_t)a.vocab), t1 = min(t0 + a.range, a.vocab);
   uint64_t sum = 0;
-  for (uint32_t t = t0 + lane; t < t1; t += 32 * kUnroll) {
-    float x[kUnroll], y[kUnroll];
+  const auto go_through = [&](auto weigh, bool with_q) __attribute__((always_inline)) {
+    for (uint32_t t = t0 + lane; t < t1; t += 32 * kUnroll) {
+      float x[kUnroll], y[kUnroll];
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      const bool in = t + 32 * k < t1;
-      x[k] = in ? to_float(p[t + 32 * k]) : 0.f;
-      y[k] = kDraft && level && in ? to_float(q[t + 32 * k]) : 0.f;
+      for (int k = 0; k < kUnroll; ++k) {
+        const bool in = t + 32 * k < t1;
+        x[k] = in ? to_float(p[t + 32 * k]) : 0.f;
+        y[k] = with_q && in ? to_float(q[t + 32 * k]) : 0.f;
+      }
+      Parts parts;
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) parts.add(weigh(probability(x[k]), probability(y[k])));
+      sum += parts.sum();
     }
-    Parts parts;
-#pragma unroll
-    for (int k = 0; k < kUnroll; ++k)
-      parts.add(weight<kDraft>(probability(x[k]), probability(y[k]), s, level));
-    sum += parts.sum();
+  };
+  // the first refusals without a loop over them for each token
+  if (!kDraft || level == 0) {
+    go_through([](float x, float) { return x; }, false);
+  } else if (level == 1) {
+    const float a0 = s.by[0];
+    go_through([&](float x, float y) { return fmaxf(__fmaf_rn(x, a0, -y), 0.f); }, true);
+  } else {
+    go_through([&](float x, float y) { return weight<kDraft>(x, y, s, level); }, true);
   }
   sum = warp_sum64(sum);
   if (!kDraft)
@@ -337,10 +353,8 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
 template <typename T>
 int launch_verify(VerifyParams& p, cudaStream_t s) {
   p.cluster = 1;
-  // as many CTAs for a request as keep all of them on the GPU at once, with
-  // two thousand tokens each at least
-  while (p.cluster < kMaxCluster && (uint64_t)p.n * p.cluster * 2 <= 2ull * num_sms() &&
-         p.vocab / (p.cluster * 2) >= 2048)
+  while (p.cluster < kMaxCluster && p.n * (uint64_t)p.cluster * 2 <= kCtas * (uint64_t)num_sms() &&
+         p.vocab / (p.cluster * 2) >= kMinTokens)
     p.cluster *= 2;
   const uint32_t warps = p.cluster * kWarps;
   p.range = (p.vocab + warps - 1) / warps;
