@@ -11,8 +11,8 @@ constexpr size_t kHeader = 4096;  // arrival counters, of up to 1,024 CTAs
 
 uint32_t padded_width(uint32_t width) { return width <= 64 ? 64 : width <= 128 ? 128 : 256; }
 
-// Blocks of 16 query rows of an item.
-uint32_t blocks_for(uint64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : kManyBlocks; }
+// Blocks of 8 query rows of an item.
+uint32_t blocks_for(uint64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : kManyBlocks; }
 
 unsigned grid_of() {
   const unsigned g = kAttnCtasPerSm * (unsigned)num_sms();
@@ -25,7 +25,7 @@ bool shape_ok(uint32_t n, uint32_t q_heads, uint32_t heads, uint32_t width, uint
 }
 
 size_t workspace_bytes(uint32_t group, uint32_t width, uint32_t max_tokens) {
-  const uint32_t rows = 16 * blocks_for((uint64_t)max_tokens * group);
+  const uint32_t rows = 8 * blocks_for((uint64_t)max_tokens * group);
   const size_t floats = (size_t)2 * grid_of() * partial_floats(rows, padded_width(width));
   return (kHeader + floats * 4 + 255) / 256 * 256;
 }

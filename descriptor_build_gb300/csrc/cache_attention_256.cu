@@ -1,5 +1,5 @@
-// The attention kernels for rows of up to 256 values (cache_attention.cuh, cache_attention_many.cuh).
-#include "cache_attention_many.cuh"
+// The attention kernels for rows of up to 256 values (cache_attention_few.cuh, cache_attention_many.cuh).
+#include "cache_attention_launch.cuh"
 
 namespace db {
 int launch_attention_256(const AttnParams& p, uint32_t type, uint32_t blocks, unsigned grid, cudaStream_t s) {

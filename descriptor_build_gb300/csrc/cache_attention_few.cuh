@@ -1,0 +1,573 @@
+// Attention over a paged cache for up to 16 query rows of a key head
+// (cache_attention.cuh: the mathematics and the way work is cut): single
+// tokens, mostly, of which memory is the bound.
+//
+// A CTA's four warps work for themselves: of every tile of 64 tokens each has
+// 16, which it fetches from their pages by 16-byte asynchronous copies into a
+// ring of its own, several tiles ahead, and no barrier is passed until the item
+// is done and their results are joined. Products are turned so that few rows
+// do not leave the matrix instructions empty: S^T = K Q^T with 16 tokens by 8
+// rows, O^T += V^T P^T with 16 values by 8 rows (mma.sync; at 16 rows a tile of
+// tcgen05 would be an eighth full, and its hand-overs take longer than the
+// loads). The weights turn over between the two by movmatrix.
+//
+// 8-bit codes go from the ring straight into the matrix instructions'
+// registers, in an order of the values that makes a thread's codes neighbours:
+// keys as they lie, values with those of two tokens interleaved bytewise. They
+// are multiplied as f16, exactly; queries are f16 too, each row times the power
+// of two that takes its largest value to 2^14, so that what a bf16 query loses
+// is 2^-38 of that.
+#pragma once
+
+#include <type_traits>
+
+#include "cache_attention.cuh"
+
+namespace db {
+
+template <uint32_t kPad, bool kCodes, uint32_t kN>
+struct Few {
+  static constexpr uint32_t kRows = 8 * kN;
+  static constexpr uint32_t kTokens = 16;                                  // of a warp in a tile
+  static constexpr uint32_t kRaw = kTokens * kPad * (kCodes ? 1 : 2);      // keys or values
+  static constexpr uint32_t kStage = 2 * kRaw + (kCodes ? 2 * kTokens * 4 : 0);
+  static constexpr uint32_t kStages = kCodes ? (kPad == 64 ? 8 : kPad == 128 ? 6 : 4) : (kPad == 64 ? 6 : 3);
+  static constexpr uint32_t kBytes = 4 * kStages * kStage;
+  static_assert(kStages * kStage >= kRows * kPad * 4, "the join of the warps reuses the rings");
+};
+
+constexpr float kFewSlack = 8.f;  // a maximum is followed when it has risen by this much (log2)
+
+// Transposes an 8 x 8 matrix of 16-bit values, a row in four lanes.
+__device__ __forceinline__ uint32_t turned(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+template <typename T, uint32_t kPad, bool kCodes, uint32_t kN>
+__global__ void __launch_bounds__(kAttnThreads, kPad > 128 ? 1 : 2) attention_few_kernel(const AttnParams p) {
+  typedef Few<kPad, kCodes, kN> F;
+  typedef typename std::conditional<kCodes, __half, T>::type H;  // what is multiplied
+  constexpr uint32_t kChunks = kCodes ? kPad / 16 : kPad / 8;    // 16-byte chunks of a row
+  constexpr uint32_t kStep = 32 / kChunks, kEach = F::kTokens / kStep;  // tokens between a lane's chunks, and how many
+  constexpr uint32_t kSteps = kPad / 16;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ float s_ref[4][F::kRows], s_sum[4][F::kRows];
+  __shared__ uint32_t s_there[4][F::kStages];  // the tokens that are there, of each warp's stages
+  __shared__ uint32_t s_last;
+  wait_for_prerequisites();
+  dependents_may_launch();
+  const uint32_t tid = threadIdx.x, warp = tid / 32, lane = tid & 31, g = lane / 4, c = lane & 3;
+  unsigned char* const ring = smem + warp * F::kStages * F::kStage;
+  const uint32_t steps = p.c.width / 16;
+  const bool e4m3 = p.c.type == DB_E4M3, one_stride = p.c.k_stride == p.c.v_stride;
+  // the values whose sums this lane has: value_of(d) and kOther on
+  const auto value_of = [g](uint32_t d) __attribute__((always_inline)) {
+    return !kCodes ? 16 * d + g : kPad == 64 ? 8 * g + 2 * d : 128 * (d / 8) + 16 * g + 2 * (d % 8);
+  };
+  constexpr uint32_t kOther = kCodes ? 1 : 8;
+  // a lane copies the same chunk of every kStep-th token
+  const uint32_t chunk = lane % kChunks, token0 = lane / kChunks;
+  const bool has = chunk < (kCodes ? p.c.width / 16 : p.c.width / 8);
+  // Place of a chunk in a stage's keys or values: the lanes of one access differ in banks, in eight
+  // tokens' same chunk (16 bits), two tokens' four keys and four tokens' two values (codes).
+  const auto place = [](uint32_t token, uint32_t ch) __attribute__((always_inline)) {
+    const uint32_t turn = !kCodes ? token & 7 : kPad == 64 ? token >> 1 & 3 : (token & 1) << 2 ^ (token >> 1 & 3) << 1;
+    return (token * kChunks + (ch ^ turn)) * 16;
+  };
+
+  const Share share = plan_share<F::kRows, kAttnThreads>(p);
+  uint64_t at = share.lo, before = share.before;
+  uint32_t i = share.request;
+  while (at < share.hi) {
+    const Request r = near_request(p, share, i);
+    const Extent e = extent_of<F::kRows>(p, r);
+    if (at - before >= e.units) {
+      before += e.units;
+      ++i;
+      continue;
+    }
+    const uint64_t x = at - before;
+    const uint32_t item = (uint32_t)quotient(x, e.tiles), head = item / e.blocks, rb = item - head * e.blocks;
+    const uint32_t t0 = (uint32_t)(x - (uint64_t)item * e.tiles);
+    const uint32_t t1 = (uint32_t)min((uint64_t)e.tiles, t0 + (share.hi - at));
+    const uint32_t rows = min(F::kRows, r.rows * p.group - rb * F::kRows);
+    const uint32_t base = r.length - r.rows;  // tokens before the request's own
+
+    // Lanes 0 to 15 look up a token each, of the next tile to be fetched.
+    const int32_t* const table = p.view.table + (uint64_t)r.seq * p.view.columns;
+    uint32_t position = t0 * kTile + warp * F::kTokens + (lane & 15);
+    uint32_t column = position / p.view.page_tokens, in_page = position - column * p.view.page_tokens;
+    const uint32_t columns_on = kTile / p.view.page_tokens, tokens_on = kTile - columns_on * p.view.page_tokens;
+    int2 w;  // page and slot, or -1 and -1
+    const auto look = [&]() __attribute__((always_inline)) {
+      w = make_int2(-1, -1);
+      if (position < r.length) w = make_int2(__ldg(table + column), (int)in_page);
+      position += kTile;
+      column += columns_on;
+      in_page += tokens_on;
+      if (in_page >= p.view.page_tokens) in_page -= p.view.page_tokens, ++column;
+    };
+    const char* const keys = (const char*)p.c.k + head * p.head_step + chunk * 16;
+    const char* const values = (const char*)p.c.v + head * p.head_step + chunk * 16;
+    const auto fetch = [&](uint32_t slot, bool any) __attribute__((always_inline)) {
+      uint32_t there = 0;
+      if (any) {
+        if ((uint32_t)w.x >= p.view.n_pages) {
+          if (w.y >= 0 && lane < 16) report_table(p.view.ctr);
+          w = make_int2(-1, -1);
+        }
+        there = __ballot_sync(kFull, w.x >= 0) & 0xFFFFu;
+        if (lane == 0) s_there[warp][slot] = there;
+        const uint64_t page = (uint32_t)max(w.x, 0), in = (uint64_t)(uint32_t)max(w.y, 0) * p.token_step;
+        const uint64_t off = page * p.c.k_stride + in, off_v = one_stride ? off : page * p.c.v_stride + in;
+        const uint32_t to = smem_at(ring + slot * F::kStage);
+        uint64_t from_k[kEach], from_v[kEach];
+#pragma unroll
+        for (uint32_t k = 0; k < kEach; ++k) from_v[k] = from_k[k] = __shfl_sync(kFull, off, token0 + k * kStep);
+        if (!one_stride) {
+#pragma unroll
+          for (uint32_t k = 0; k < kEach; ++k) from_v[k] = __shfl_sync(kFull, off_v, token0 + k * kStep);
+        }
+        if (there == 0xFFFFu && (!kCodes || __all_sync(kFull, has))) {
+          if (has) {
+#pragma unroll
+            for (uint32_t k = 0; k < kEach; ++k) {
+              const uint32_t at_chunk = to + place(token0 + k * kStep, chunk);
+              copy16(at_chunk, keys + from_k[k], true);
+              copy16(at_chunk + F::kRaw, values + from_v[k], true);
+            }
+          }
+        } else {
+#pragma unroll
+          for (uint32_t k = 0; k < kEach; ++k) {
+            const uint32_t token = token0 + k * kStep, at_chunk = to + place(token, chunk);
+            const bool real = has && (there >> token & 1);
+            copy16(at_chunk, keys + (real ? from_k[k] : 0), real);
+            copy16(at_chunk + F::kRaw, values + (real ? from_v[k] : 0), real);
+          }
+        }
+        if (kCodes) {  // lanes 0 to 15 the keys' scales, the others the values'
+          const uint32_t of = (uint32_t)__shfl_sync(kFull, max(w.y, 0), lane & 15) * p.scale_token_step + head * p.scale_head_step;
+          const uint64_t pg = (uint64_t)__shfl_sync(kFull, (uint32_t)page, lane & 15);
+          const char* const scales = lane < 16 ? (const char*)p.c.k_scale + pg * p.c.k_scale_stride : (const char*)p.c.v_scale + pg * p.c.v_scale_stride;
+          const bool real = there >> (lane & 15) & 1;
+          copy4(to + 2 * F::kRaw + lane * 4, real ? (const float*)scales + of : (const float*)p.c.k_scale, real);
+        }
+      }
+      copies_commit();
+    };
+
+    __syncthreads();  // the item before is done with the rings
+    look();
+#pragma unroll 1
+    for (uint32_t k = 0; k + 1 < F::kStages; ++k) {
+      fetch(k, t0 + k < t1);
+      look();
+    }
+
+    // Queries as the second operand: this lane's are of row g of each block.
+    uint32_t q[kSteps][2 * kN];
+    float factor[kN][2];  // of scores of rows 2c and 2c + 1
+    uint32_t node[kN][2];
+#pragma unroll
+    for (uint32_t n = 0; n < kN; ++n) {
+      const uint32_t row = n * 8 + g, all = rb * F::kRows + (row < rows ? row : 0), nd = all / p.group;
+      const char* const from = (const char*)p.q.base + (uint64_t)(r.first + nd) * p.q.row_stride +
+                               (head * p.group + (all - nd * p.group)) * p.q.head_stride;
+      if constexpr (kCodes) {
+        uint32_t top = 0;
+#pragma unroll
+        for (uint32_t st = 0; st < kSteps; ++st) {  // values 64 (st / 4) + 16 c + 4 (st % 4) and three more
+          const uint32_t d = 64 * (st / 4) + 16 * c + 4 * (st % 4);
+          uint2 v = make_uint2(0, 0);
+          if (row < rows && d < p.c.width) v = __ldg((const uint2*)(from + d * 2));
+          q[st][2 * n] = v.x;
+          q[st][2 * n + 1] = v.y;
+          const float2 a = unpack2<T>(v.x & 0x7FFF7FFFu), b = unpack2<T>(v.y & 0x7FFF7FFFu);
+          top = max(max(max(top, __float_as_uint(a.x)), max(__float_as_uint(a.y), __float_as_uint(b.x))), __float_as_uint(b.y));
+        }
+        top = max(top, __shfl_xor_sync(kFull, top, 1));
+        top = max(top, __shfl_xor_sync(kFull, top, 2));
+        const int exponent = top == 0 || top >= 0x7F800000u ? 14 : max((int)(top >> 23) - 127, 14 - 126);
+        const float up = __uint_as_float((uint32_t)(14 - exponent + 127) << 23);
+#pragma unroll
+        for (uint32_t st = 0; st < kSteps; ++st)
+#pragma unroll
+          for (uint32_t h = 0; h < 2; ++h) {
+            const float2 a = unpack2<T>(q[st][2 * n + h]);
+            q[st][2 * n + h] = pack2<__half>(a.x * up, a.y * up);
+          }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int ex = __shfl_sync(kFull, exponent, (2 * c + h) * 4);
+          factor[n][h] = p.scale_log2 * __uint_as_float((uint32_t)(max(ex - 14, -126) + 127) << 23);
+        }
+      } else {
+#pragma unroll
+        for (uint32_t st = 0; st < kSteps; ++st)
+#pragma unroll
+          for (uint32_t h = 0; h < 2; ++h)
+            q[st][2 * n + h] = row < rows && st < steps ? __ldg((const uint32_t*)(from + (st * 16 + 2 * c + 8 * h) * 2)) : 0u;
+        factor[n][0] = factor[n][1] = p.scale_log2;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t of = rb * F::kRows + n * 8 + 2 * c + h;
+        node[n][h] = n * 8 + 2 * c + h < rows ? of / p.group : 0;
+      }
+    }
+
+    float o[kSteps][kN][4];
+    float top[kN][2], sum[kN][2];
+    uint32_t exponent = 127;  // codes: of the values' scales so far
+#pragma unroll
+    for (uint32_t d = 0; d < kSteps; ++d)
+#pragma unroll
+      for (uint32_t n = 0; n < kN; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[d][n][k] = 0.f;
+#pragma unroll
+    for (uint32_t n = 0; n < kN; ++n) top[n][0] = top[n][1] = -INFINITY, sum[n][0] = sum[n][1] = 0.f;
+
+    uint32_t slot = 0;
+    for (uint32_t t = t0; t < t1; ++t) {
+      copies_wait<F::kStages - 2>();
+      __syncwarp();  // the stage is here for all lanes, and the one before is done with
+      const uint32_t there = s_there[warp][slot];
+      fetch(slot == 0 ? F::kStages - 1 : slot - 1, t + F::kStages - 1 < t1);
+      look();
+      unsigned char* const kt = ring + slot * F::kStage;
+      unsigned char* const vt = kt + F::kRaw;
+      const float* const scales = (const float*)(kt + 2 * F::kRaw);
+      slot = slot + 1 == F::kStages ? 0 : slot + 1;
+
+      // scores of tokens g and g + 8, rows 2c and 2c + 1 of each block
+      float s[kN][4];
+#pragma unroll
+      for (uint32_t n = 0; n < kN; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[n][k] = 0.f;
+      if constexpr (kCodes) {
+#pragma unroll
+        for (uint32_t j = 0; j < kPad / 64; ++j) {
+          const uint4 lo = *(const uint4*)(kt + place(g, 4 * j + c)), hi = *(const uint4*)(kt + place(g + 8, 4 * j + c));
+          const uint32_t a[4] = {lo.x, lo.y, lo.z, lo.w}, b[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const uint2 u = widen4<H>(a[m], e4m3), v = widen4<H>(b[m], e4m3);
+            const uint32_t f[4] = {u.x, v.x, u.y, v.y};
+#pragma unroll
+            for (uint32_t n = 0; n < kN; ++n) multiply<H>(s[n], f, q[4 * j + m][2 * n], q[4 * j + m][2 * n + 1]);
+          }
+        }
+        const float k0 = scales[g], k1 = scales[g + 8];
+        // (an infinite scale stands for values of both signs, whose products have no sum)
+        const float f0 = __fmaf_rn(k0, 0.f, k0), f1 = __fmaf_rn(k1, 0.f, k1);
+#pragma unroll
+        for (uint32_t n = 0; n < kN; ++n)
+          s[n][0] *= f0, s[n][1] *= f0, s[n][2] *= f1, s[n][3] *= f1;
+      } else {
+#pragma unroll
+        for (uint32_t st = 0; st < kSteps; ++st) {
+          if (st >= steps) break;
+          uint32_t f[4];
+          load_matrices(f, smem_at(kt) + place((lane & 7) + (lane >> 3 & 1) * 8, 2 * st + (lane >> 4)));
+#pragma unroll
+          for (uint32_t n = 0; n < kN; ++n) multiply<H>(s[n], f, q[st][2 * n], q[st][2 * n + 1]);
+        }
+      }
+#pragma unroll
+      for (uint32_t n = 0; n < kN; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[n][k] *= factor[n][k & 1];
+      // what is not seen: only the last tiles, or those of broken tables, have any
+      const uint32_t first = t * kTile + warp * F::kTokens;  // position of the stage's first token
+      const bool masked = first + F::kTokens > base || there != 0xFFFFu;
+      uint32_t sees = 0xFFFFFFFFu;
+      if (masked) {
+        sees = 0;
+#pragma unroll
+        for (uint32_t n = 0; n < kN; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t token = g + (k >> 1) * 8, nd = node[n][k & 1];
+            bool yes = there >> token & 1;
+            if (yes && first + token >= base) {
+              const uint32_t own = first + token - base;
+              yes = p.mask ? __ldg(p.mask + (uint64_t)(r.first + nd) * p.mask_words + own / 32) >> (own & 31) & 1 : own <= nd;
+            }
+            if (yes)
+              sees |= 1u << (n * 4 + k);
+            else
+              s[n][k] = -INFINITY;
+          }
+      }
+      // Weights are exp2(score - ref). ref is a score that was a row's largest,
+      // followed when one is 2^8 above it; for codes it also takes in the size
+      // of the values' scales, so that weights times scales stay in the middle
+      // of f16's range.
+      float most[kN][2];
+      bool rises = false;
+#pragma unroll
+      for (uint32_t n = 0; n < kN; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          most[n][h] = fmaxf(s[n][h], s[n][2 + h]);
+          rises |= most[n][h] > top[n][h] + kFewSlack || (top[n][h] == -INFINITY && most[n][h] > -INFINITY);
+        }
+      float v0 = 1.f, v1 = 1.f;
+      uint32_t scale_ex = 0;
+      if (kCodes) {
+        v0 = scales[16 + g], v1 = scales[24 + g];
+        const uint32_t e0 = (__float_as_uint(v0) >> 23) & 0xFFu, e1 = (__float_as_uint(v1) >> 23) & 0xFFu;
+        scale_ex = max(e0 == 0xFFu ? 0u : e0, e1 == 0xFFu ? 0u : e1);
+        rises |= t == t0 || min(max(scale_ex, 31u), 227u) > exponent + kScaleSlack;
+      }
+      if (__any_sync(kFull, rises)) {
+        const uint32_t ex_before = exponent;
+        if (kCodes) {
+          const uint32_t now = min(max(__reduce_max_sync(kFull, scale_ex), 31u), 227u);
+          if (t == t0 || now > exponent + kScaleSlack) exponent = now;
+        }
+#pragma unroll
+        for (uint32_t n = 0; n < kN; ++n)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float m = most[n][h];
+            m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
+            m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
+            m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
+            const float was = top[n][h] + (float)((int)ex_before - 127);
+            if (m > top[n][h] + kFewSlack || top[n][h] == -INFINITY) top[n][h] = m;
+            const float ref = top[n][h] == -INFINITY ? 0.f : top[n][h] + (float)((int)exponent - 127);
+            const float down = exp2_of(was - ref);
+            sum[n][h] *= down;
+#pragma unroll
+            for (uint32_t d = 0; d < kSteps; ++d) {
+              o[d][n][h] *= down;
+              o[d][n][2 + h] *= down;
+            }
+          }
+      }
+      const float shift = (float)((int)exponent - 127);
+#pragma unroll
+      for (uint32_t n = 0; n < kN; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float ref = top[n][k & 1] == -INFINITY ? 0.f : top[n][k & 1] + shift;
+          s[n][k] = exp2_of(s[n][k] - ref);
+          sum[n][k & 1] += s[n][k];
+        }
+      if (kCodes) {
+#pragma unroll
+        for (uint32_t n = 0; n < kN; ++n)
+          s[n][0] *= v0, s[n][1] *= v0, s[n][2] *= v1, s[n][3] *= v1;
+      }
+      // Values that not every row sees and that are not finite: rare, by hand.
+      if (masked) {
+        bool bad = false;
+#pragma unroll 2
+        for (uint32_t k = 0; k < kEach; ++k) {
+          const uint4 v = *(const uint4*)(vt + place(token0 + k * kStep, chunk));
+          bool here;
+          if (kCodes) {
+            const auto nan4 = [](uint32_t a) { return ((a & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; };
+            here = e4m3 && (nan4(v.x) | nan4(v.y) | nan4(v.z) | nan4(v.w));
+          } else {
+            here = not_finite2<H>(v.x) || not_finite2<H>(v.y) || not_finite2<H>(v.z) || not_finite2<H>(v.w);
+          }
+          bad |= has && here;
+        }
+        const auto odd_scale = [](float a) { return (__float_as_uint(a) & 0x7F800000u) == 0x7F800000u; };
+        if (kCodes) bad |= odd_scale(v0) || odd_scale(v1);
+        if (__any_sync(kFull, bad)) {
+#pragma unroll 1
+          for (uint32_t token = 0; token < F::kTokens; ++token) {
+            // the weights of rows 2c and 2c + 1 with the token, by the lane that has them
+            const uint32_t from = (token & 7) * 4 + c;
+            float weight[kN][2];
+            bool yes[kN][2];
+            const uint32_t bits = __shfl_sync(kFull, sees, from);
+#pragma unroll
+            for (uint32_t n = 0; n < kN; ++n)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float a = __shfl_sync(kFull, s[n][h], from), b = __shfl_sync(kFull, s[n][2 + h], from);
+                weight[n][h] = token < 8 ? a : b;
+                yes[n][h] = bits >> (n * 4 + (token < 8 ? 0 : 2) + h) & 1;
+              }
+#pragma unroll
+            for (uint32_t d = 0; d < kSteps; ++d)
+#pragma unroll
+              for (uint32_t half = 0; half < 2; ++half) {
+                float v;
+                if (kCodes) {
+                  const uint32_t of = value_of(d) + half;
+                  const unsigned char code = vt[place(token, of / 16) + of % 16];
+                  v = e4m3 ? unpack2<__half>(e4m3x2_to_f16x2(code)).x : (float)(int8_t)code;
+                } else {
+                  const uint32_t of = value_of(d) + 8 * half;
+                  v = d < steps ? to_float(*(const H*)(vt + place(token, of / 8) + of % 8 * 2)) : 0.f;
+                }
+#pragma unroll
+                for (uint32_t n = 0; n < kN; ++n)
+#pragma unroll
+                  for (int h = 0; h < 2; ++h)
+                    if (yes[n][h]) o[d][n][2 * half + h] += weight[n][h] * v;
+              }
+          }
+          continue;
+        }
+        if (kCodes) {  // an unseen token's scale may be anything finite: its weights are 0
+#pragma unroll
+          for (uint32_t n = 0; n < kN; ++n)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (!(sees >> (n * 4 + k) & 1)) s[n][k] = 0.f;
+        }
+      }
+      uint32_t b[kN][2];
+#pragma unroll
+      for (uint32_t n = 0; n < kN; ++n) {
+        b[n][0] = turned(pack2<H>(s[n][0], s[n][1]));
+        b[n][1] = turned(pack2<H>(s[n][2], s[n][3]));
+      }
+      if constexpr (kCodes) {
+        // words of this lane's values of tokens 2c, 2c + 1, 2c + 8, 2c + 9
+#pragma unroll
+        for (uint32_t j = 0; j < (kPad == 64 ? 1 : kPad / 128); ++j) {
+          constexpr uint32_t kWords = kPad == 64 ? 2 : 4;
+          uint32_t u[4][kWords];
+#pragma unroll
+          for (uint32_t k = 0; k < 4; ++k) {
+            const uint32_t token = 2 * c + (k & 1) + (k >> 1) * 8;
+            if constexpr (kPad == 64) {
+              const uint2 y = *(const uint2*)(vt + place(token, g / 2) + (g & 1) * 8);
+              u[k][0] = y.x, u[k][1] = y.y;
+            } else {
+              const uint4 y = *(const uint4*)(vt + place(token, 8 * j + g));
+              u[k][0] = y.x, u[k][1] = y.y, u[k][kWords - 2] = y.z, u[k][kWords - 1] = y.w;
+            }
+          }
+#pragma unroll
+          for (uint32_t m = 0; m < kWords; ++m)
+#pragma unroll
+            for (uint32_t half = 0; half < 2; ++half) {
+              const uint2 lo = widen4<H>(__byte_perm(u[0][m], u[1][m], half ? 0x7362 : 0x5140), e4m3);
+              const uint2 hi = widen4<H>(__byte_perm(u[2][m], u[3][m], half ? 0x7362 : 0x5140), e4m3);
+              const uint32_t f[4] = {lo.x, lo.y, hi.x, hi.y};
+              const uint32_t d = j * 8 + 2 * m + half;
+#pragma unroll
+              for (uint32_t n = 0; n < kN; ++n) multiply<H>(o[d][n], f, b[n][0], b[n][1]);
+            }
+        }
+      } else {
+#pragma unroll
+        for (uint32_t d = 0; d < kSteps; ++d) {
+          if (d >= steps) break;
+          uint32_t f[4];
+          load_matrices_t(f, smem_at(vt) + place((lane & 7) + (lane >> 4) * 8, 2 * d + (lane >> 3 & 1)));
+#pragma unroll
+          for (uint32_t n = 0; n < kN; ++n) multiply<H>(o[d][n], f, b[n][0], b[n][1]);
+        }
+      }
+    }
+
+    // The warps' results joined, through shared memory.
+#pragma unroll
+    for (uint32_t n = 0; n < kN; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float l = sum[n][h];
+        l += __shfl_xor_sync(kFull, l, 4);
+        l += __shfl_xor_sync(kFull, l, 8);
+        l += __shfl_xor_sync(kFull, l, 16);
+        sum[n][h] = l;
+        top[n][h] += (float)((int)exponent - 127);  // the reference of what was summed
+        if (g == 0) s_ref[warp][n * 8 + 2 * c + h] = top[n][h];
+      }
+    copies_wait<0>();
+    __syncthreads();
+#pragma unroll
+    for (uint32_t n = 0; n < kN; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t row = n * 8 + 2 * c + h;
+        float m = s_ref[0][row];
+#pragma unroll
+        for (int k = 1; k < 4; ++k) m = fmaxf(m, s_ref[k][row]);
+        const float a = exp2_of(top[n][h] - (m == -INFINITY ? 0.f : m));
+        if (g == 0) s_sum[warp][row] = sum[n][h] * a;
+        float* const to = (float*)smem + (warp * F::kRows + row) * kPad;
+#pragma unroll
+        for (uint32_t d = 0; d < kSteps; ++d) {
+          to[value_of(d)] = o[d][n][h] * a;
+          to[value_of(d) + kOther] = o[d][n][2 + h] * a;
+        }
+      }
+    __syncthreads();
+    const bool whole = t0 == 0 && t1 == e.tiles;
+    float* const mine = p.partial + (uint64_t)(2 * blockIdx.x + (t0 == 0)) * partial_floats(F::kRows, kPad);
+    constexpr uint32_t kQuads = kPad / 4;
+#pragma unroll 1
+    for (uint32_t of = tid; of < rows * kQuads; of += kAttnThreads) {
+      const uint32_t row = of / kQuads, quad = of % kQuads;
+      float m = -INFINITY, l = 0.f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (uint32_t k = 0; k < 4; ++k) {
+        m = fmaxf(m, s_ref[k][row]);
+        l += s_sum[k][row];
+        const float4 y = *((const float4*)((const float*)smem + (k * F::kRows + row) * kPad) + quad);
+        v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+      }
+      if (whole) {
+        const uint32_t all = rb * F::kRows + row, nd = all / p.group, qh = head * p.group + (all - nd * p.group);
+        const float by = l == 0.f ? 0.f : 1.f / l;
+        if (quad * 4 < p.c.width)
+          *(uint2*)((char*)p.out.base + (uint64_t)(r.first + nd) * p.out.row_stride + qh * p.out.head_stride + quad * 8) =
+              make_uint2(pack2<T>(v.x * by, v.y * by), pack2<T>(v.z * by, v.w * by));
+        if (quad == 0 && p.lse)
+          p.lse[(uint64_t)(r.first + nd) * (p.c.heads * p.group) + qh] =
+              l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+      } else {
+        __stcg((float4*)(mine + row * kPad) + quad, v);
+        if (quad == 0) {
+          __stcg(mine + F::kRows * kPad + row, m);
+          __stcg(mine + F::kRows * kPad + F::kRows + row, l);
+        }
+      }
+    }
+    if (!whole) {
+      __threadfence();
+      __syncthreads();
+      const uint64_t first = at - t0;
+      const uint32_t c0 = owner_of(share, first), c1 = owner_of(share, first + e.tiles - 1);
+      if (tid == 0) {
+        const unsigned int seen = atomicAdd(p.arrived + c0, 1u);
+        s_last = seen == c1 - c0;
+        if (s_last) p.arrived[c0] = 0;
+      }
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        const JoinedItem item_of = {r.first, rb * F::kRows, rows, head, c0, c1};
+        join_item<T, F::kRows, kPad, kAttnThreads>(p, item_of, (float4*)smem, 0);
+      }
+    }
+    at += t1 - t0;
+  }
+}
+
+template <typename T, uint32_t kPad, bool kCodes, uint32_t kN>
+int launch_few(const AttnParams& p, unsigned grid, cudaStream_t s) {
+  typedef Few<kPad, kCodes, kN> F;
+  const cudaError_t e = cudaFuncSetAttribute(attention_few_kernel<T, kPad, kCodes, kN>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, F::kBytes);
+  if (e != cudaSuccess) return cuda_failure(e);
+  return launch_dependent(attention_few_kernel<T, kPad, kCodes, kN>, grid, kAttnThreads, F::kBytes, s, p);
+}
+
+}  // namespace db

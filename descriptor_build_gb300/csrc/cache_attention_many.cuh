@@ -294,8 +294,6 @@ static __device__ __noinline__ void add_odd(const TileNotes& m, uint32_t output,
   }
 }
 
-static __device__ __noinline__ uint64_t quotient(uint64_t a, uint64_t b) { return a / b; }
-
 constexpr float kSlack = 8.f;          // a maximum is followed when it has risen by this much (log2)
 
 template <typename T, uint32_t kPad, bool kCodes>
@@ -950,21 +948,6 @@ int launch_many(const AttnParams& p, unsigned grid, cudaStream_t s) {
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, F::kAsk);
   if (e != cudaSuccess) return cuda_failure(e);
   return launch_dependent(attention_many_kernel<T, kPad, kCodes>, grid, F::kThreads, F::kAsk, s, p);
-}
-
-template <uint32_t kPad>
-int launch_attention(const AttnParams& p, uint32_t type, uint32_t blocks, unsigned grid, cudaStream_t s) {
-  const bool codes = item_bytes(p.c.type) == 1;
-  if (blocks == kManyBlocks) {
-    if (type == DB_BF16)
-      return codes ? launch_many<__nv_bfloat16, kPad, true>(p, grid, s) : launch_many<__nv_bfloat16, kPad, false>(p, grid, s);
-    return codes ? launch_many<__half, kPad, true>(p, grid, s) : launch_many<__half, kPad, false>(p, grid, s);
-  }
-  if (type == DB_BF16)
-    return codes ? launch_blocks<__nv_bfloat16, kPad, true>(p, blocks, grid, s)
-                 : launch_blocks<__nv_bfloat16, kPad, false>(p, blocks, grid, s);
-  return codes ? launch_blocks<__half, kPad, true>(p, blocks, grid, s)
-               : launch_blocks<__half, kPad, false>(p, blocks, grid, s);
 }
 
 }  // namespace db
