@@ -250,18 +250,25 @@ __global__ void __launch_bounds__(kAttnThreads, kPad > 128 ? 1 : 2) attention_fe
 #pragma unroll
         for (int k = 0; k < 4; ++k) s[n][k] = 0.f;
       if constexpr (kCodes) {
+        const auto scores = [&](auto is_float) __attribute__((always_inline)) {
+          constexpr bool kFloat = decltype(is_float)::value;
 #pragma unroll
-        for (uint32_t j = 0; j < kPad / 64; ++j) {
-          const uint4 lo = *(const uint4*)(kt + place(g, 4 * j + c)), hi = *(const uint4*)(kt + place(g + 8, 4 * j + c));
-          const uint32_t a[4] = {lo.x, lo.y, lo.z, lo.w}, b[4] = {hi.x, hi.y, hi.z, hi.w};
+          for (uint32_t j = 0; j < kPad / 64; ++j) {
+            const uint4 lo = *(const uint4*)(kt + place(g, 4 * j + c)), hi = *(const uint4*)(kt + place(g + 8, 4 * j + c));
+            const uint32_t a[4] = {lo.x, lo.y, lo.z, lo.w}, b[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const uint2 u = widen4<H>(a[m], e4m3), v = widen4<H>(b[m], e4m3);
-            const uint32_t f[4] = {u.x, v.x, u.y, v.y};
+            for (int m = 0; m < 4; ++m) {
+              const uint2 u = widen4<H>(a[m], kFloat), v = widen4<H>(b[m], kFloat);
+              const uint32_t f[4] = {u.x, v.x, u.y, v.y};
 #pragma unroll
-            for (uint32_t n = 0; n < kN; ++n) multiply<H>(s[n], f, q[4 * j + m][2 * n], q[4 * j + m][2 * n + 1]);
+              for (uint32_t n = 0; n < kN; ++n) multiply<H>(s[n], f, q[4 * j + m][2 * n], q[4 * j + m][2 * n + 1]);
+            }
           }
-        }
+        };
+        if (e4m3)
+          scores(std::true_type());
+        else
+          scores(std::false_type());
         const float k0 = scales[g], k1 = scales[g + 8];
         // (an infinite scale stands for values of both signs, whose products have no sum)
         const float f0 = __fmaf_rn(k0, 0.f, k0), f1 = __fmaf_rn(k1, 0.f, k1);
@@ -435,34 +442,41 @@ __global__ void __launch_bounds__(kAttnThreads, kPad > 128 ? 1 : 2) attention_fe
         b[n][1] = turned(pack2<H>(s[n][2], s[n][3]));
       }
       if constexpr (kCodes) {
-        // words of this lane's values of tokens 2c, 2c + 1, 2c + 8, 2c + 9
+        const auto outputs = [&](auto is_float) __attribute__((always_inline)) {
+          constexpr bool kFloat = decltype(is_float)::value;
+          // words of this lane's values of tokens 2c, 2c + 1, 2c + 8, 2c + 9
 #pragma unroll
-        for (uint32_t j = 0; j < (kPad == 64 ? 1 : kPad / 128); ++j) {
-          constexpr uint32_t kWords = kPad == 64 ? 2 : 4;
-          uint32_t u[4][kWords];
+          for (uint32_t j = 0; j < (kPad == 64 ? 1 : kPad / 128); ++j) {
+            constexpr uint32_t kWords = kPad == 64 ? 2 : 4;
+            uint32_t u[4][kWords];
 #pragma unroll
-          for (uint32_t k = 0; k < 4; ++k) {
-            const uint32_t token = 2 * c + (k & 1) + (k >> 1) * 8;
-            if constexpr (kPad == 64) {
-              const uint2 y = *(const uint2*)(vt + place(token, g / 2) + (g & 1) * 8);
-              u[k][0] = y.x, u[k][1] = y.y;
-            } else {
-              const uint4 y = *(const uint4*)(vt + place(token, 8 * j + g));
-              u[k][0] = y.x, u[k][1] = y.y, u[k][kWords - 2] = y.z, u[k][kWords - 1] = y.w;
+            for (uint32_t k = 0; k < 4; ++k) {
+              const uint32_t token = 2 * c + (k & 1) + (k >> 1) * 8;
+              if constexpr (kPad == 64) {
+                const uint2 y = *(const uint2*)(vt + place(token, g / 2) + (g & 1) * 8);
+                u[k][0] = y.x, u[k][1] = y.y;
+              } else {
+                const uint4 y = *(const uint4*)(vt + place(token, 8 * j + g));
+                u[k][0] = y.x, u[k][1] = y.y, u[k][kWords - 2] = y.z, u[k][kWords - 1] = y.w;
+              }
             }
+#pragma unroll
+            for (uint32_t m = 0; m < kWords; ++m)
+#pragma unroll
+              for (uint32_t half = 0; half < 2; ++half) {
+                const uint2 lo = widen4<H>(__byte_perm(u[0][m], u[1][m], half ? 0x7362 : 0x5140), kFloat);
+                const uint2 hi = widen4<H>(__byte_perm(u[2][m], u[3][m], half ? 0x7362 : 0x5140), kFloat);
+                const uint32_t f[4] = {lo.x, lo.y, hi.x, hi.y};
+                const uint32_t d = j * 8 + 2 * m + half;
+#pragma unroll
+                for (uint32_t n = 0; n < kN; ++n) multiply<H>(o[d][n], f, b[n][0], b[n][1]);
+              }
           }
-#pragma unroll
-          for (uint32_t m = 0; m < kWords; ++m)
-#pragma unroll
-            for (uint32_t half = 0; half < 2; ++half) {
-              const uint2 lo = widen4<H>(__byte_perm(u[0][m], u[1][m], half ? 0x7362 : 0x5140), e4m3);
-              const uint2 hi = widen4<H>(__byte_perm(u[2][m], u[3][m], half ? 0x7362 : 0x5140), e4m3);
-              const uint32_t f[4] = {lo.x, lo.y, hi.x, hi.y};
-              const uint32_t d = j * 8 + 2 * m + half;
-#pragma unroll
-              for (uint32_t n = 0; n < kN; ++n) multiply<H>(o[d][n], f, b[n][0], b[n][1]);
-            }
-        }
+        };
+        if (e4m3)
+          outputs(std::true_type());
+        else
+          outputs(std::false_type());
       } else {
 #pragma unroll
         for (uint32_t d = 0; d < kSteps; ++d) {
