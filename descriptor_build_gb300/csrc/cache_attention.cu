@@ -2,22 +2,19 @@
 // (cache_attention.cuh).
 #include <cmath>
 
+#include <algorithm>
+
 #include "cache_attention.cuh"
 
 namespace db {
 namespace {
 
-constexpr size_t kHeader = 4096;  // arrival counters, of up to 1,024 CTAs
+constexpr size_t kHeader = 4 * kMaxAttnCtas;  // arrival counters
 
 uint32_t padded_width(uint32_t width) { return width <= 64 ? 64 : width <= 128 ? 128 : 256; }
 
 // Blocks of 8 query rows of an item.
 uint32_t blocks_for(uint64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : kManyBlocks; }
-
-unsigned grid_of() {
-  const unsigned g = kAttnCtasPerSm * (unsigned)num_sms();
-  return g < kHeader / 4 ? g : (unsigned)(kHeader / 4);
-}
 
 bool shape_ok(uint32_t n, uint32_t q_heads, uint32_t heads, uint32_t width, uint32_t max_tokens) {
   if (n > 65536 || !heads || !q_heads || q_heads % heads || q_heads / heads > kMaxGroup) return false;
@@ -25,8 +22,9 @@ bool shape_ok(uint32_t n, uint32_t q_heads, uint32_t heads, uint32_t width, uint
 }
 
 size_t workspace_bytes(uint32_t group, uint32_t width, uint32_t max_tokens) {
-  const uint32_t rows = 8 * blocks_for((uint64_t)max_tokens * group);
-  const size_t floats = (size_t)2 * grid_of() * partial_floats(rows, padded_width(width));
+  const uint32_t blocks = blocks_for((uint64_t)max_tokens * group), pad = padded_width(width);
+  const uint32_t ctas = std::max(attn_ctas_per_sm(pad, false, blocks), attn_ctas_per_sm(pad, true, blocks));
+  const size_t floats = (size_t)2 * attn_grid(ctas) * partial_floats(8 * blocks, pad);
   return (kHeader + floats * 4 + 255) / 256 * 256;
 }
 
@@ -85,10 +83,10 @@ extern "C" int db_cache_attention(const db_page_tables* t, const db_cache_batch*
   const uint32_t blocks = blocks_for((uint64_t)max_tokens * p.group);
   switch (padded_width(c->width)) {
     case 64:
-      return launch_attention_64(p, type, blocks, grid_of(), s);
+      return launch_attention_64(p, type, blocks, s);
     case 128:
-      return launch_attention_128(p, type, blocks, grid_of(), s);
+      return launch_attention_128(p, type, blocks, s);
     default:
-      return launch_attention_256(p, type, blocks, grid_of(), s);
+      return launch_attention_256(p, type, blocks, s);
   }
 }

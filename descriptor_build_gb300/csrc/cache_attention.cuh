@@ -18,7 +18,6 @@ namespace db {
 
 constexpr uint32_t kTile = 64;             // tokens of a unit
 constexpr uint32_t kAttnThreads = 128;
-constexpr uint32_t kAttnCtasPerSm = 2;     // most CTAs an SM of the grid
 constexpr uint32_t kMaxGroup = 64;
 constexpr uint32_t kScaleSlack = 4;        // a larger exponent of scales is followed from here on
 constexpr uint32_t kManyBlocks = 16;      // blocks of 8 query rows of the tcgen05 kernel's items
@@ -40,9 +39,21 @@ struct AttnParams {
 };
 
 // Host: one instance of the kernels for a padded width.
-int launch_attention_64(const AttnParams& p, uint32_t type, uint32_t blocks, unsigned grid, cudaStream_t s);
-int launch_attention_128(const AttnParams& p, uint32_t type, uint32_t blocks, unsigned grid, cudaStream_t s);
-int launch_attention_256(const AttnParams& p, uint32_t type, uint32_t blocks, unsigned grid, cudaStream_t s);
+// CTAs of an SM of a kernel for so many blocks of 8 query rows: as many as
+// registers and shared memory hold.
+constexpr uint32_t attn_ctas_per_sm(uint32_t pad, bool codes, uint32_t blocks) {
+  if (blocks > 2) return 2;
+  return pad == 64 ? 4 : pad == 128 ? (codes || blocks == 1 ? 3 : 2) : codes ? 2 : 1;
+}
+constexpr unsigned kMaxAttnCtas = 1024;
+inline unsigned attn_grid(uint32_t ctas_per_sm) {
+  const unsigned g = ctas_per_sm * (unsigned)num_sms();
+  return g < kMaxAttnCtas ? g : kMaxAttnCtas;
+}
+
+int launch_attention_64(const AttnParams& p, uint32_t type, uint32_t blocks, cudaStream_t s);
+int launch_attention_128(const AttnParams& p, uint32_t type, uint32_t blocks, cudaStream_t s);
+int launch_attention_256(const AttnParams& p, uint32_t type, uint32_t blocks, cudaStream_t s);
 
 // Floats of a partial result of `rows` query rows: the weighted values, then
 // maxima and sums.

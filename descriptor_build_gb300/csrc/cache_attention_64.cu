@@ -2,7 +2,7 @@
 #include "cache_attention_launch.cuh"
 
 namespace db {
-int launch_attention_64(const AttnParams& p, uint32_t type, uint32_t blocks, unsigned grid, cudaStream_t s) {
-  return launch_attention<64>(p, type, blocks, grid, s);
+int launch_attention_64(const AttnParams& p, uint32_t type, uint32_t blocks, cudaStream_t s) {
+  return launch_attention<64>(p, type, blocks, s);
 }
 }  // namespace db

@@ -31,7 +31,8 @@ struct Few {
   static constexpr uint32_t kTokens = 16;                                  // of a warp in a tile
   static constexpr uint32_t kRaw = kTokens * kPad * (kCodes ? 1 : 2);      // keys or values
   static constexpr uint32_t kStage = 2 * kRaw + (kCodes ? 2 * kTokens * 4 : 0);
-  static constexpr uint32_t kStages = kCodes ? (kPad == 64 ? 8 : kPad == 128 ? 6 : 4) : (kPad == 64 ? 6 : 3);
+  static constexpr uint32_t kCtas = attn_ctas_per_sm(kPad, kCodes, kN);
+  static constexpr uint32_t kStages = kCodes ? (kPad == 64 ? 5 : kPad == 128 ? 4 : 3) : kPad == 128 && kN == 1 ? 2 : 3;
   static constexpr uint32_t kBytes = 4 * kStages * kStage;
   static_assert(kStages * kStage >= kRows * kPad * 4, "the join of the warps reuses the rings");
 };
@@ -46,7 +47,7 @@ __device__ __forceinline__ uint32_t turned(uint32_t x) {
 }
 
 template <typename T, uint32_t kPad, bool kCodes, uint32_t kN>
-__global__ void __launch_bounds__(kAttnThreads, kPad > 128 ? 1 : 2) attention_few_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN>::kCtas)) attention_few_kernel(const AttnParams p) {
   typedef Few<kPad, kCodes, kN> F;
   typedef typename std::conditional<kCodes, __half, T>::type H;  // what is multiplied
   constexpr uint32_t kChunks = kCodes ? kPad / 16 : kPad / 8;    // 16-byte chunks of a row
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(kAttnThreads, kPad > 128 ? 1 : 2) attention_fe
 #pragma unroll
           for (uint32_t k = 0; k < kEach; ++k) from_v[k] = __shfl_sync(kFull, off_v, token0 + k * kStep);
         }
-        if (there == 0xFFFFu && (!kCodes || __all_sync(kFull, has))) {
+        if (there == 0xFFFFu) {
           if (has) {
 #pragma unroll
             for (uint32_t k = 0; k < kEach; ++k) {
@@ -143,9 +144,9 @@ __global__ void __launch_bounds__(kAttnThreads, kPad > 128 ? 1 : 2) attention_fe
 #pragma unroll
           for (uint32_t k = 0; k < kEach; ++k) {
             const uint32_t token = token0 + k * kStep, at_chunk = to + place(token, chunk);
-            const bool real = has && (there >> token & 1);
-            copy16(at_chunk, keys + (real ? from_k[k] : 0), real);
-            copy16(at_chunk + F::kRaw, values + (real ? from_v[k] : 0), real);
+            if (!has) continue;
+            copy16(at_chunk, keys + from_k[k], there >> token & 1);
+            copy16(at_chunk + F::kRaw, values + from_v[k], there >> token & 1);
           }
         }
         if (kCodes) {  // lanes 0 to 15 the keys' scales, the others the values'
@@ -160,6 +161,12 @@ __global__ void __launch_bounds__(kAttnThreads, kPad > 128 ? 1 : 2) attention_fe
     };
 
     __syncthreads();  // the item before is done with the rings
+    if (kCodes && !has) {  // keys behind the width's end are zeros, as queries are there
+#pragma unroll 1
+      for (uint32_t k = 0; k < F::kStages; ++k)
+        for (uint32_t j = 0; j < kEach; ++j)
+          *(uint4*)(ring + k * F::kStage + place(token0 + j * kStep, chunk)) = make_uint4(0, 0, 0, 0);
+    }
     look();
 #pragma unroll 1
     for (uint32_t k = 0; k + 1 < F::kStages; ++k) {
@@ -576,12 +583,12 @@ __global__ void __launch_bounds__(kAttnThreads, kPad > 128 ? 1 : 2) attention_fe
 }
 
 template <typename T, uint32_t kPad, bool kCodes, uint32_t kN>
-int launch_few(const AttnParams& p, unsigned grid, cudaStream_t s) {
+int launch_few(const AttnParams& p, cudaStream_t s) {
   typedef Few<kPad, kCodes, kN> F;
   const cudaError_t e = cudaFuncSetAttribute(attention_few_kernel<T, kPad, kCodes, kN>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, F::kBytes);
   if (e != cudaSuccess) return cuda_failure(e);
-  return launch_dependent(attention_few_kernel<T, kPad, kCodes, kN>, grid, kAttnThreads, F::kBytes, s, p);
+  return launch_dependent(attention_few_kernel<T, kPad, kCodes, kN>, attn_grid(F::kCtas), kAttnThreads, F::kBytes, s, p);
 }
 
 }  // namespace db

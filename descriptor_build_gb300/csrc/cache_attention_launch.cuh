@@ -7,25 +7,25 @@
 namespace db {
 
 template <typename T, uint32_t kPad, bool kCodes>
-int launch_blocks(const AttnParams& p, uint32_t blocks, unsigned grid, cudaStream_t s) {
+int launch_blocks(const AttnParams& p, uint32_t blocks, cudaStream_t s) {
   switch (blocks) {
     case 1:
-      return launch_few<T, kPad, kCodes, 1>(p, grid, s);
+      return launch_few<T, kPad, kCodes, 1>(p, s);
     case 2:
-      return launch_few<T, kPad, kCodes, 2>(p, grid, s);
+      return launch_few<T, kPad, kCodes, 2>(p, s);
     default:
-      return launch_many<T, kPad, kCodes>(p, grid, s);
+      return launch_many<T, kPad, kCodes>(p, s);
   }
 }
 
 template <uint32_t kPad>
-int launch_attention(const AttnParams& p, uint32_t type, uint32_t blocks, unsigned grid, cudaStream_t s) {
+int launch_attention(const AttnParams& p, uint32_t type, uint32_t blocks, cudaStream_t s) {
   const bool codes = item_bytes(p.c.type) == 1;
   if (type == DB_BF16)
-    return codes ? launch_blocks<__nv_bfloat16, kPad, true>(p, blocks, grid, s)
-                 : launch_blocks<__nv_bfloat16, kPad, false>(p, blocks, grid, s);
-  return codes ? launch_blocks<__half, kPad, true>(p, blocks, grid, s)
-               : launch_blocks<__half, kPad, false>(p, blocks, grid, s);
+    return codes ? launch_blocks<__nv_bfloat16, kPad, true>(p, blocks, s)
+                 : launch_blocks<__nv_bfloat16, kPad, false>(p, blocks, s);
+  return codes ? launch_blocks<__half, kPad, true>(p, blocks, s)
+               : launch_blocks<__half, kPad, false>(p, blocks, s);
 }
 
 }  // namespace db

@@ -942,12 +942,12 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
 }
 
 template <typename T, uint32_t kPad, bool kCodes>
-int launch_many(const AttnParams& p, unsigned grid, cudaStream_t s) {
+int launch_many(const AttnParams& p, cudaStream_t s) {
   typedef Many<kPad, kCodes> F;
   const cudaError_t e = cudaFuncSetAttribute(attention_many_kernel<T, kPad, kCodes>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, F::kAsk);
   if (e != cudaSuccess) return cuda_failure(e);
-  return launch_dependent(attention_many_kernel<T, kPad, kCodes>, grid, F::kThreads, F::kAsk, s, p);
+  return launch_dependent(attention_many_kernel<T, kPad, kCodes>, attn_grid(attn_ctas_per_sm(kPad, kCodes, kManyBlocks)), F::kThreads, F::kAsk, s, p);
 }
 
 }  // namespace db
