@@ -174,7 +174,7 @@ __device__ __forceinline__ uint32_t smem_at(const void* p) { return (uint32_t)__
 // size in a register is several times slower to start.)
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool real) {
   if (real)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::64B [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
   else
     asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
 }

@@ -46,6 +46,88 @@ __device__ __forceinline__ uint32_t turned(uint32_t x) {
   return r;
 }
 
+// The parts of an item whose rows are few, joined by a whole CTA: long
+// sequences leave it tens of parts, so the warps share them out (one after
+// another they took 20 us of 110 for 23 parts) and are summed in their order.
+template <typename T, uint32_t kRows, uint32_t kPad>
+static __device__ __noinline__ void join_few(const AttnParams& p, const JoinedItem item, float* const room) {
+  constexpr uint32_t kPart = kRows * (kPad + 2), kQuads = kPad / 4, kSlices = kAttnThreads / kRows, kMany = 8;
+  __shared__ float s_top[kSlices][kRows], s_sum[kSlices][kRows];
+  __shared__ float4 s_note[kRows];
+  const uint32_t tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
+  const float* const parts = p.partial + (uint64_t)2 * item.c0 * kPart;  // the first is its CTA's second
+  const auto part_at = [&](uint32_t k) { return parts + (k == item.c0 ? kPart : (uint64_t)2 * (k - item.c0) * kPart); };
+  {
+    const uint32_t row = tid % kRows, slice = tid / kRows;
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 2
+    for (uint32_t k = item.c0 + slice; k <= item.c1; k += kSlices) {
+      const float mk = __ldcg(part_at(k) + kRows * kPad + row), lk = __ldcg(part_at(k) + kRows * kPad + kRows + row);
+      const float now = fmaxf(m, mk), by = now == -INFINITY ? 0.f : now;
+      l = l * exp2_of(m - by) + lk * exp2_of(mk - by);
+      m = now;
+    }
+    s_top[slice][row] = m;
+    s_sum[slice][row] = l;
+  }
+  __syncthreads();
+  if (tid < item.rows) {
+    const uint32_t row = tid;
+    float m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (uint32_t k = 0; k < kSlices; ++k) m = fmaxf(m, s_top[k][row]);
+    const float by = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (uint32_t k = 0; k < kSlices; ++k) l += s_sum[k][row] * exp2_of(s_top[k][row] - by);
+    const uint32_t all = item.row0 + row, node = all / p.group, qh = item.head * p.group + (all - node * p.group);
+    const uint64_t to = (uint64_t)(item.first + node) * p.out.row_stride + qh * p.out.head_stride;
+    s_note[row] = make_float4(by, l == 0.f ? 0.f : 1.f / l, __uint_as_float((uint32_t)to),
+                              __uint_as_float((uint32_t)(to >> 32)));
+    if (p.lse)
+      p.lse[(uint64_t)(item.first + node) * (p.c.heads * p.group) + qh] =
+          l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+  }
+  __syncthreads();
+  const uint32_t all = item.rows * kQuads;
+  float4* const sums = (float4*)room;  // [4][rows * kQuads]
+#pragma unroll 1
+  for (uint32_t c = lane; c < all; c += 32 * kMany) {
+    float4 v[kMany];
+#pragma unroll
+    for (uint32_t j = 0; j < kMany; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (uint32_t k = item.c0 + warp; k <= item.c1; k += 4) {
+      const float* const at = part_at(k);
+      float m[kMany];
+      float4 y[kMany];
+#pragma unroll
+      for (uint32_t j = 0; j < kMany; ++j) {
+        const uint32_t of = min(c + j * 32, all - 1), row = of / kQuads, quad = min(of % kQuads, p.c.width / 4 - 1);
+        m[j] = __ldcg(at + kRows * kPad + row);
+        y[j] = __ldcg((const float4*)(at + row * kPad) + quad);
+      }
+#pragma unroll
+      for (uint32_t j = 0; j < kMany; ++j) {
+        const float b = exp2_of(m[j] - s_note[min(c + j * 32, all - 1) / kQuads].x);
+        v[j].x += y[j].x * b, v[j].y += y[j].y * b, v[j].z += y[j].z * b, v[j].w += y[j].w * b;
+      }
+    }
+#pragma unroll
+    for (uint32_t j = 0; j < kMany; ++j)
+      if (c + j * 32 < all) sums[warp * all + c + j * 32] = v[j];
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (uint32_t of = tid; of < all; of += kAttnThreads) {
+    const float4 a = sums[of], b = sums[all + of], c = sums[2 * all + of], d = sums[3 * all + of], n = s_note[of / kQuads];
+    const uint64_t to = (uint64_t)__float_as_uint(n.w) << 32 | __float_as_uint(n.z);
+    if (of % kQuads * 4 < p.c.width)
+      *(uint2*)((char*)p.out.base + to + of % kQuads * 8) =
+          make_uint2(pack2<T>((a.x + b.x + c.x + d.x) * n.y, (a.y + b.y + c.y + d.y) * n.y),
+                     pack2<T>((a.z + b.z + c.z + d.z) * n.y, (a.w + b.w + c.w + d.w) * n.y));
+  }
+}
+
 template <typename T, uint32_t kPad, bool kCodes, uint32_t kN>
 __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN>::kCtas)) attention_few_kernel(const AttnParams p) {
   typedef Few<kPad, kCodes, kN> F;
@@ -575,7 +657,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN>::kCtas)) 
       if (s_last) {
         __threadfence();
         const JoinedItem item_of = {r.first, rb * F::kRows, rows, head, c0, c1};
-        join_item<T, F::kRows, kPad, kAttnThreads>(p, item_of, (float4*)smem, 0);
+        join_few<T, F::kRows, kPad>(p, item_of, (float*)smem);
       }
     }
     at += t1 - t0;
