@@ -31,6 +31,7 @@ import ctypes
 import functools
 import math
 import os
+import struct
 
 import numpy as np
 import torch
@@ -690,24 +691,12 @@ def page_copy(moves: torch.Tensor, n_moves: torch.Tensor, src: torch.Tensor, dst
 
 
 # ------------------------------------------------------- a paged cache's contents
-class _CacheBatch(ctypes.Structure):  # db_cache_batch
-    _fields_ = [("seq", ctypes.c_void_p), ("start", ctypes.c_void_p), ("n", ctypes.c_uint32),
-                ("rows", ctypes.c_uint32)]
-
-
-class _CacheLayer(ctypes.Structure):  # db_cache_layer
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
-                ("v_scale", ctypes.c_void_p), ("k_stride", ctypes.c_uint64),
-                ("v_stride", ctypes.c_uint64), ("k_scale_stride", ctypes.c_uint64),
-                ("v_scale_stride", ctypes.c_uint64), ("heads", ctypes.c_uint32),
-                ("width", ctypes.c_uint32), ("type", ctypes.c_uint32),
-                ("heads_first", ctypes.c_uint32)]
-
-
-class _CacheRows(ctypes.Structure):  # db_cache_rows
-    _fields_ = [("base", ctypes.c_void_p), ("row_stride", ctypes.c_uint64),
-                ("head_stride", ctypes.c_uint64)]
-
+# The C structs as bytes, which a call reads before it returns (making a
+# ctypes.Structure takes four times as long).
+_pack_batch = struct.Struct("=2Q2I").pack  # db_cache_batch: seq, start, n, rows
+_pack_layer = struct.Struct("=4Q").pack  # db_cache_layer: k, v, k_scale, v_scale, and after them
+_pack_layer_plan = struct.Struct("=4Q4I").pack  # their strides, heads, width, type, heads_first
+_pack_rows = struct.Struct("=3Q").pack  # db_cache_rows: base, row_stride, head_stride
 
 _ROW_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _CACHE_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 3, torch.int8: 4}
@@ -720,26 +709,27 @@ def _i32(t: torch.Tensor, n: int, what: str) -> int:
     return _at(t, 4 * n)
 
 
-def _cache_batch(seq: torch.Tensor, start: torch.Tensor, rows: int) -> tuple:
+def _cache_batch(seq: torch.Tensor, start: torch.Tensor, rows: int) -> tuple[bytes, int]:
     n = seq.numel()
     if start.numel() != n + 1:
         raise ValueError(f"start must have {n + 1} elements for {n} sequences")
-    b = _CacheBatch(_i32(seq, n, "seq"), _i32(start, n + 1, "start"), n, rows)
-    return ctypes.byref(b), n
+    return _pack_batch(_i32(seq, n, "seq"), _i32(start, n + 1, "start"), n, rows), n
 
 
-def _cache_rows(t: torch.Tensor, heads: int, width: int) -> "ctypes.pointer":
+def _cache_rows(t: torch.Tensor, heads: int, width: int) -> bytes:
     """Rows [rows, heads, width] outside the cache, of any strides but the last."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != width or t.stride(2) != 1:
-        raise ValueError(f"rows must be [rows, {heads}, {width}] with neighbouring values")
+    if t.shape[1:] != (heads, width):
+        raise ValueError(f"rows must be [rows, {heads}, {width}]")
+    row, head, one = t.stride()
+    if one != 1:
+        raise ValueError("the values of a row must be neighbours")
     if not (t.is_cuda or t.is_pinned()):
         _refuse(t)
     size = t.element_size()
-    return ctypes.byref(_CacheRows(t.data_ptr(), t.stride(0) * size, t.stride(1) * size))
+    return _pack_rows(t.data_ptr(), row * size, head * size)
 
 
-@functools.lru_cache(maxsize=1024)
-def _layer_plan(shape, stride, dtype, token_dim, page_tokens, scale_shape, scale_stride):
+def _pool_plan(shape, stride, dtype, token_dim, page_tokens, scale_shape, scale_stride):
     """What a pool of keys or values says: (page stride and scales' page stride
     in bytes, heads, width, type)."""
     if len(shape) != 4 or token_dim not in (1, 2):
@@ -770,36 +760,54 @@ def _layer_plan(shape, stride, dtype, token_dim, page_tokens, scale_shape, scale
     return stride[0] * size, scale, shape[3 - token_dim], shape[3], _CACHE_TYPES[dtype]
 
 
+@functools.lru_cache(maxsize=1024)
+def _layer_plan(token_dim, page_tokens, k, k_scale, v, v_scale) -> tuple[bytes, int, int]:
+    """The rest of a layer's struct, its heads and width, from what the tensors
+    look like (shape, stride and a pool's type)."""
+    k_step, ks_step, *of_k = _pool_plan(*k, token_dim, page_tokens, *k_scale)
+    v_step, vs_step, *of_v = _pool_plan(*v, token_dim, page_tokens, *v_scale)
+    if of_k != of_v:
+        raise ValueError("the pools of keys and values differ in heads, width or type")
+    heads, width, kind = of_k
+    return (_pack_layer_plan(k_step, v_step, ks_step, vs_step, heads, width, kind, token_dim == 2),
+            heads, width)
+
+
+_NO_SCALE = (None, None)
+
+
 def _cache_layer(tables: PageTables, k_pool, v_pool, k_scale, v_scale, token_dim):
     """The layer's struct, its heads and width."""
-    said = []
-    for pool, scale in ((k_pool, k_scale), (v_pool, v_scale)):
-        if not (pool.is_cuda or pool.is_pinned()):
-            _refuse(pool)
-        if pool.shape[0] < tables._c.n_pages:
-            raise ValueError(f"a pool of {pool.shape[0]} pages where the tables have {tables._c.n_pages}")
+    k_shape, v_shape, pages = k_pool.shape, v_pool.shape, tables._c.n_pages
+    if not (k_pool.is_cuda or k_pool.is_pinned()):
+        _refuse(k_pool)
+    if not (v_pool.is_cuda or v_pool.is_pinned()):
+        _refuse(v_pool)
+    like_k = like_v = _NO_SCALE
+    at_k = at_v = 0
+    for scale in (k_scale, v_scale):
         if scale is not None:
             if not (scale.is_cuda or scale.is_pinned()):
                 _refuse(scale)
             if scale.dtype is not torch.float32:
                 raise ValueError("scales are float32")
-        said.append(_layer_plan(pool.shape, pool.stride(), pool.dtype, token_dim, tables.page_tokens,
-                                None if scale is None else scale.shape,
-                                None if scale is None else scale.stride()))
-    (k_step, ks_step, heads, width, kind), (v_step, vs_step, *rest) = said
-    if rest != [heads, width, kind]:
-        raise ValueError("the pools of keys and values differ in heads, width or type")
-    layer = _CacheLayer(k_pool.data_ptr(), v_pool.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
-                        None if v_scale is None else v_scale.data_ptr(), k_step, v_step, ks_step, vs_step,
-                        heads, width, kind, token_dim == 2)
-    return ctypes.byref(layer), heads, width
+    if k_scale is not None:
+        like_k, at_k = (k_scale.shape, k_scale.stride()), k_scale.data_ptr()
+    if v_scale is not None:
+        like_v, at_v = (v_scale.shape, v_scale.stride()), v_scale.data_ptr()
+    rest, heads, width = _layer_plan(token_dim, tables.page_tokens, (k_shape, k_pool.stride(), k_pool.dtype), like_k,
+                                     (v_shape, v_pool.stride(), v_pool.dtype), like_v)
+    if k_shape[0] < pages or v_shape[0] < pages:
+        raise ValueError(f"a pool of {min(k_shape[0], v_shape[0])} pages where the tables have {pages}")
+    return _pack_layer(k_pool.data_ptr(), v_pool.data_ptr(), at_k, at_v) + rest, heads, width
 
 
 def _row_type(*tensors: torch.Tensor) -> int:
     dtype = tensors[0].dtype
-    if any(t.dtype is not dtype for t in tensors) or dtype not in _ROW_TYPES:
+    kind = _ROW_TYPES.get(dtype)
+    if kind is None or tensors[-1].dtype is not dtype:
         raise ValueError("rows are bfloat16, float16 or float32, all of one type")
-    return _ROW_TYPES[dtype]
+    return kind
 
 
 def _maybe(t: torch.Tensor | None, nbytes: int) -> int | None:
@@ -861,7 +869,7 @@ def cache_attention(tables: PageTables, seq: torch.Tensor, start: torch.Tensor, 
     bits names (None: themselves and the ones before). scale None: 1 /
     sqrt(width). lse: float32 [rows, q_heads]."""
     layer, heads, width = _cache_layer(tables, k_pool, v_pool, k_scale, v_scale, token_dim)
-    rows, q_heads = q.shape[0], q.shape[1]
+    rows, q_heads, _ = q.shape
     if out.shape[0] != rows:
         raise ValueError("q and out differ in rows")
     batch, n = _cache_batch(seq, start, rows)
