@@ -13,8 +13,13 @@ constexpr size_t kHeader = 4 * kMaxAttnCtas;  // arrival counters
 
 uint32_t padded_width(uint32_t width) { return width <= 64 ? 64 : width <= 128 ? 128 : 256; }
 
-// Blocks of 8 query rows of an item.
-uint32_t blocks_for(uint64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : kManyBlocks; }
+// Blocks of 8 query rows of an item. Up to 16 rows memory is the bound of the
+// kernel for few; with 32, warps that share a ring two by two are faster for
+// codes (64 sequences of 20,000 tokens, 2 key heads: 288 us, the kernel for many
+// 350) and slower for 16-bit values (334, 270).
+uint32_t blocks_for(uint64_t rows, bool codes) {
+  return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 && codes ? 4 : kManyBlocks;
+}
 
 bool shape_ok(uint32_t n, uint32_t q_heads, uint32_t heads, uint32_t width, uint32_t max_tokens) {
   if (n > 65536 || !heads || !q_heads || q_heads % heads || q_heads / heads > kMaxGroup) return false;
@@ -22,9 +27,12 @@ bool shape_ok(uint32_t n, uint32_t q_heads, uint32_t heads, uint32_t width, uint
 }
 
 size_t workspace_bytes(uint32_t group, uint32_t width, uint32_t max_tokens) {
-  const uint32_t blocks = blocks_for((uint64_t)max_tokens * group), pad = padded_width(width);
-  const uint32_t ctas = std::max(attn_ctas_per_sm(pad, false, blocks), attn_ctas_per_sm(pad, true, blocks));
-  const size_t floats = (size_t)2 * attn_grid(ctas) * partial_floats(8 * blocks, pad);
+  const uint32_t pad = padded_width(width);
+  size_t floats = 0;  // the larger need of 16-bit values and codes
+  for (const bool codes : {false, true}) {
+    const uint32_t blocks = blocks_for((uint64_t)max_tokens * group, codes);
+    floats = std::max(floats, (size_t)2 * attn_grid(attn_ctas_per_sm(pad, codes, blocks)) * partial_floats(8 * blocks, pad));
+  }
   return (kHeader + floats * 4 + 255) / 256 * 256;
 }
 
@@ -80,7 +88,7 @@ extern "C" int db_cache_attention(const db_page_tables* t, const db_cache_batch*
   p.scale_head_step = c->heads_first ? t->page_tokens : 1;
   p.arrived = (unsigned int*)ws;
   p.partial = (float*)((char*)ws + kHeader);
-  const uint32_t blocks = blocks_for((uint64_t)max_tokens * p.group);
+  const uint32_t blocks = blocks_for((uint64_t)max_tokens * p.group, item_bytes(c->type) == 1);
   switch (padded_width(c->width)) {
     case 64:
       return launch_attention_64(p, type, blocks, s);

@@ -42,7 +42,7 @@ struct AttnParams {
 // CTAs of an SM of a kernel for so many blocks of 8 query rows: as many as
 // registers and shared memory hold.
 constexpr uint32_t attn_ctas_per_sm(uint32_t pad, bool codes, uint32_t blocks) {
-  if (blocks > 2) return 2;
+  if (blocks == kManyBlocks) return 2;
   return pad == 64 ? 4 : pad == 128 ? (codes || blocks == 1 ? 3 : 2) : codes ? 2 : 1;
 }
 constexpr unsigned kMaxAttnCtas = 1024;

@@ -1,9 +1,9 @@
-// Attention over a paged cache for up to 16 query rows of a key head
-// (cache_attention.cuh: the mathematics and the way work is cut): single
+// Attention over a paged cache for up to 16 query rows of a key head, with codes
+// 32 (cache_attention.cuh: the mathematics and the way work is cut): single
 // tokens, mostly, of which memory is the bound.
 //
-// A CTA's four warps work for themselves: of every tile of 64 tokens each has
-// 16, which it fetches from their pages by 16-byte asynchronous copies into a
+// A CTA's four warps work for themselves (with 17 to 32 rows two by two, 16 rows
+// each): of every tile of 64 tokens each has 16, which it fetches from their pages by 16-byte asynchronous copies into a
 // ring of its own, several tiles ahead, and no barrier is passed until the item
 // is done and their results are joined. Products are turned so that few rows
 // do not leave the matrix instructions empty: S^T = K Q^T with 16 tokens by 8
@@ -25,16 +25,20 @@
 
 namespace db {
 
-template <uint32_t kPad, bool kCodes, uint32_t kN>
+constexpr uint32_t kJoined = 256;  // quads of values that are joined at a time
+
+template <uint32_t kPad, bool kCodes, uint32_t kN, uint32_t kShare>
 struct Few {
-  static constexpr uint32_t kRows = 8 * kN;
-  static constexpr uint32_t kTokens = 16;                                  // of a warp in a tile
+  static constexpr uint32_t kRows = 8 * kN * kShare;
+  static constexpr uint32_t kGroups = 4 / kShare;                          // of kShare warps with a ring
+  static constexpr uint32_t kTokens = 16;                                  // of a stage
   static constexpr uint32_t kRaw = kTokens * kPad * (kCodes ? 1 : 2);      // keys or values
   static constexpr uint32_t kStage = 2 * kRaw + (kCodes ? 2 * kTokens * 4 : 0);
-  static constexpr uint32_t kCtas = attn_ctas_per_sm(kPad, kCodes, kN);
-  static constexpr uint32_t kStages = kCodes ? (kPad == 64 ? 5 : kPad == 128 ? 4 : 3) : kPad == 128 && kN == 1 ? 2 : 3;
-  static constexpr uint32_t kBytes = 4 * kStages * kStage;
-  static_assert(kStages * kStage >= kRows * kPad * 4, "the join of the warps reuses the rings");
+  static constexpr uint32_t kCtas = attn_ctas_per_sm(kPad, kCodes, kN * kShare);
+  static constexpr uint32_t kStages =
+      kShare * (kCodes ? (kPad == 64 ? 5 : kPad == 128 ? 4 : 3) : kPad == 128 && kN == 1 ? 2 : 3);
+  static constexpr uint32_t kBytes = kGroups * kStages * kStage;
+  static_assert(kBytes >= kGroups * kRows * kPad * 4 && kBytes >= 4 * kJoined * 16, "joins reuse the rings");
 };
 
 constexpr float kFewSlack = 8.f;  // a maximum is followed when it has risen by this much (log2)
@@ -51,7 +55,7 @@ __device__ __forceinline__ uint32_t turned(uint32_t x) {
 // another they took 20 us of 110 for 23 parts) and are summed in their order.
 template <typename T, uint32_t kRows, uint32_t kPad>
 static __device__ __noinline__ void join_few(const AttnParams& p, const JoinedItem item, float* const room) {
-  constexpr uint32_t kPart = kRows * (kPad + 2), kQuads = kPad / 4, kSlices = kAttnThreads / kRows, kMany = 8;
+  constexpr uint32_t kPart = kRows * (kPad + 2), kQuads = kPad / 4, kSlices = kAttnThreads / kRows, kMany = kJoined / 32;
   __shared__ float s_top[kSlices][kRows], s_sum[kSlices][kRows];
   __shared__ float4 s_note[kRows];
   const uint32_t tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
@@ -89,9 +93,9 @@ static __device__ __noinline__ void join_few(const AttnParams& p, const JoinedIt
   }
   __syncthreads();
   const uint32_t all = item.rows * kQuads;
-  float4* const sums = (float4*)room;  // [4][rows * kQuads]
+  float4* const sums = (float4*)room;  // [4][32 * kMany]
 #pragma unroll 1
-  for (uint32_t c = lane; c < all; c += 32 * kMany) {
+  for (uint32_t c = 0; c < all; c += 32 * kMany) {
     float4 v[kMany];
 #pragma unroll
     for (uint32_t j = 0; j < kMany; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -102,47 +106,53 @@ static __device__ __noinline__ void join_few(const AttnParams& p, const JoinedIt
       float4 y[kMany];
 #pragma unroll
       for (uint32_t j = 0; j < kMany; ++j) {
-        const uint32_t of = min(c + j * 32, all - 1), row = of / kQuads, quad = min(of % kQuads, p.c.width / 4 - 1);
+        const uint32_t of = min(c + lane + j * 32, all - 1), row = of / kQuads, quad = min(of % kQuads, p.c.width / 4 - 1);
         m[j] = __ldcg(at + kRows * kPad + row);
         y[j] = __ldcg((const float4*)(at + row * kPad) + quad);
       }
 #pragma unroll
       for (uint32_t j = 0; j < kMany; ++j) {
-        const float b = exp2_of(m[j] - s_note[min(c + j * 32, all - 1) / kQuads].x);
+        const float b = exp2_of(m[j] - s_note[min(c + lane + j * 32, all - 1) / kQuads].x);
         v[j].x += y[j].x * b, v[j].y += y[j].y * b, v[j].z += y[j].z * b, v[j].w += y[j].w * b;
       }
     }
 #pragma unroll
-    for (uint32_t j = 0; j < kMany; ++j)
-      if (c + j * 32 < all) sums[warp * all + c + j * 32] = v[j];
-  }
-  __syncthreads();
-#pragma unroll 1
-  for (uint32_t of = tid; of < all; of += kAttnThreads) {
-    const float4 a = sums[of], b = sums[all + of], c = sums[2 * all + of], d = sums[3 * all + of], n = s_note[of / kQuads];
-    const uint64_t to = (uint64_t)__float_as_uint(n.w) << 32 | __float_as_uint(n.z);
-    if (of % kQuads * 4 < p.c.width)
-      *(uint2*)((char*)p.out.base + to + of % kQuads * 8) =
-          make_uint2(pack2<T>((a.x + b.x + c.x + d.x) * n.y, (a.y + b.y + c.y + d.y) * n.y),
-                     pack2<T>((a.z + b.z + c.z + d.z) * n.y, (a.w + b.w + c.w + d.w) * n.y));
+    for (uint32_t j = 0; j < kMany; ++j) sums[warp * 32 * kMany + lane + j * 32] = v[j];
+    __syncthreads();
+#pragma unroll
+    for (uint32_t at = tid; at < 32 * kMany; at += kAttnThreads) {
+      const uint32_t of = c + at;
+      if (of < all && of % kQuads * 4 < p.c.width) {
+        const float4 w0 = sums[at], w1 = sums[32 * kMany + at], w2 = sums[64 * kMany + at], w3 = sums[96 * kMany + at];
+        const float4 n = s_note[of / kQuads];
+        const uint64_t to = (uint64_t)__float_as_uint(n.w) << 32 | __float_as_uint(n.z);
+        *(uint2*)((char*)p.out.base + to + of % kQuads * 8) =
+            make_uint2(pack2<T>((w0.x + w1.x + w2.x + w3.x) * n.y, (w0.y + w1.y + w2.y + w3.y) * n.y),
+                       pack2<T>((w0.z + w1.z + w2.z + w3.z) * n.y, (w0.w + w1.w + w2.w + w3.w) * n.y));
+      }
+    }
+    __syncthreads();
   }
 }
 
-template <typename T, uint32_t kPad, bool kCodes, uint32_t kN>
-__global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN>::kCtas)) attention_few_kernel(const AttnParams p) {
-  typedef Few<kPad, kCodes, kN> F;
+template <typename T, uint32_t kPad, bool kCodes, uint32_t kN, uint32_t kShare>
+__global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::kCtas)) attention_few_kernel(const AttnParams p) {
+  typedef Few<kPad, kCodes, kN, kShare> F;
   typedef typename std::conditional<kCodes, __half, T>::type H;  // what is multiplied
   constexpr uint32_t kChunks = kCodes ? kPad / 16 : kPad / 8;    // 16-byte chunks of a row
   constexpr uint32_t kStep = 32 / kChunks, kEach = F::kTokens / kStep;  // tokens between a lane's chunks, and how many
   constexpr uint32_t kSteps = kPad / 16;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ float s_ref[4][F::kRows], s_sum[4][F::kRows];
+  constexpr uint32_t kCopies = (kEach + kShare - 1) / kShare;    // of a lane in a stage
+  constexpr uint32_t kStride = F::kTokens * F::kGroups;          // tokens from one stage to the next
+  __shared__ float s_ref[F::kGroups][F::kRows], s_sum[F::kGroups][F::kRows];
   __shared__ uint32_t s_there[4][F::kStages];  // the tokens that are there, of each warp's stages
   __shared__ uint32_t s_last;
   wait_for_prerequisites();
   dependents_may_launch();
   const uint32_t tid = threadIdx.x, warp = tid / 32, lane = tid & 31, g = lane / 4, c = lane & 3;
-  unsigned char* const ring = smem + warp * F::kStages * F::kStage;
+  const uint32_t team = warp / kShare, member = warp % kShare, row0 = member * 8 * kN;  // its rows of the item
+  unsigned char* const ring = smem + team * F::kStages * F::kStage;
   const uint32_t steps = p.c.width / 16;
   const bool e4m3 = p.c.type == DB_E4M3, one_stride = p.c.k_stride == p.c.v_stride;
   // the values whose sums this lane has: value_of(d) and kOther on
@@ -178,16 +188,18 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN>::kCtas)) 
     const uint32_t rows = min(F::kRows, r.rows * p.group - rb * F::kRows);
     const uint32_t base = r.length - r.rows;  // tokens before the request's own
 
-    // Lanes 0 to 15 look up a token each, of the next tile to be fetched.
+    const uint32_t stages = (t1 - t0) * kShare;
+
+    // Lanes 0 to 15 look up a token each, of the next stage to be fetched.
     const int32_t* const table = p.view.table + (uint64_t)r.seq * p.view.columns;
-    uint32_t position = t0 * kTile + warp * F::kTokens + (lane & 15);
+    uint32_t position = t0 * kTile + team * F::kTokens + (lane & 15);
     uint32_t column = position / p.view.page_tokens, in_page = position - column * p.view.page_tokens;
-    const uint32_t columns_on = kTile / p.view.page_tokens, tokens_on = kTile - columns_on * p.view.page_tokens;
+    const uint32_t columns_on = kStride / p.view.page_tokens, tokens_on = kStride - columns_on * p.view.page_tokens;
     int2 w;  // page and slot, or -1 and -1
     const auto look = [&]() __attribute__((always_inline)) {
       w = make_int2(-1, -1);
       if (position < r.length) w = make_int2(__ldg(table + column), (int)in_page);
-      position += kTile;
+      position += kStride;
       column += columns_on;
       in_page += tokens_on;
       if (in_page >= p.view.page_tokens) in_page -= p.view.page_tokens, ++column;
@@ -206,32 +218,34 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN>::kCtas)) 
         const uint64_t page = (uint32_t)max(w.x, 0), in = (uint64_t)(uint32_t)max(w.y, 0) * p.token_step;
         const uint64_t off = page * p.c.k_stride + in, off_v = one_stride ? off : page * p.c.v_stride + in;
         const uint32_t to = smem_at(ring + slot * F::kStage);
-        uint64_t from_k[kEach], from_v[kEach];
+        const uint32_t token1 = token0 + member * kCopies * kStep;  // this warp's share of the copies
+        const bool mine = has && token1 < F::kTokens;
+        uint64_t from_k[kCopies], from_v[kCopies];
 #pragma unroll
-        for (uint32_t k = 0; k < kEach; ++k) from_v[k] = from_k[k] = __shfl_sync(kFull, off, token0 + k * kStep);
+        for (uint32_t k = 0; k < kCopies; ++k) from_v[k] = from_k[k] = __shfl_sync(kFull, off, token1 + k * kStep);
         if (!one_stride) {
 #pragma unroll
-          for (uint32_t k = 0; k < kEach; ++k) from_v[k] = __shfl_sync(kFull, off_v, token0 + k * kStep);
+          for (uint32_t k = 0; k < kCopies; ++k) from_v[k] = __shfl_sync(kFull, off_v, token1 + k * kStep);
         }
         if (there == 0xFFFFu) {
-          if (has) {
+          if (mine) {
 #pragma unroll
-            for (uint32_t k = 0; k < kEach; ++k) {
-              const uint32_t at_chunk = to + place(token0 + k * kStep, chunk);
+            for (uint32_t k = 0; k < kCopies; ++k) {
+              const uint32_t at_chunk = to + place(token1 + k * kStep, chunk);
               copy16(at_chunk, keys + from_k[k], true);
               copy16(at_chunk + F::kRaw, values + from_v[k], true);
             }
           }
         } else {
 #pragma unroll
-          for (uint32_t k = 0; k < kEach; ++k) {
-            const uint32_t token = token0 + k * kStep, at_chunk = to + place(token, chunk);
-            if (!has) continue;
+          for (uint32_t k = 0; k < kCopies; ++k) {
+            const uint32_t token = token1 + k * kStep, at_chunk = to + place(token, chunk);
+            if (!mine) continue;
             copy16(at_chunk, keys + from_k[k], there >> token & 1);
             copy16(at_chunk + F::kRaw, values + from_v[k], there >> token & 1);
           }
         }
-        if (kCodes) {  // lanes 0 to 15 the keys' scales, the others the values'
+        if (kCodes && member == 0) {  // lanes 0 to 15 the keys' scales, the others the values'
           const uint32_t of = (uint32_t)__shfl_sync(kFull, max(w.y, 0), lane & 15) * p.scale_token_step + head * p.scale_head_step;
           const uint64_t pg = (uint64_t)__shfl_sync(kFull, (uint32_t)page, lane & 15);
           const char* const scales = lane < 16 ? (const char*)p.c.k_scale + pg * p.c.k_scale_stride : (const char*)p.c.v_scale + pg * p.c.v_scale_stride;
@@ -252,7 +266,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN>::kCtas)) 
     look();
 #pragma unroll 1
     for (uint32_t k = 0; k + 1 < F::kStages; ++k) {
-      fetch(k, t0 + k < t1);
+      fetch(k, k < stages);
       look();
     }
 
@@ -262,7 +276,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN>::kCtas)) 
     uint32_t node[kN][2];
 #pragma unroll
     for (uint32_t n = 0; n < kN; ++n) {
-      const uint32_t row = n * 8 + g, all = rb * F::kRows + (row < rows ? row : 0), nd = all / p.group;
+      const uint32_t row = row0 + n * 8 + g, all = rb * F::kRows + (row < rows ? row : 0), nd = all / p.group;
       const char* const from = (const char*)p.q.base + (uint64_t)(r.first + nd) * p.q.row_stride +
                                (head * p.group + (all - nd * p.group)) * p.q.head_stride;
       if constexpr (kCodes) {
@@ -303,8 +317,8 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN>::kCtas)) 
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t of = rb * F::kRows + n * 8 + 2 * c + h;
-        node[n][h] = n * 8 + 2 * c + h < rows ? of / p.group : 0;
+        const uint32_t row = row0 + n * 8 + 2 * c + h;
+        node[n][h] = row < rows ? (rb * F::kRows + row) / p.group : 0;
       }
     }
 
@@ -321,11 +335,16 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN>::kCtas)) 
     for (uint32_t n = 0; n < kN; ++n) top[n][0] = top[n][1] = -INFINITY, sum[n][0] = sum[n][1] = 0.f;
 
     uint32_t slot = 0;
-    for (uint32_t t = t0; t < t1; ++t) {
+    uint32_t first = t0 * kTile + team * F::kTokens;  // position of the stage's first token
+    for (uint32_t t = 0; t < stages; ++t, first += kStride) {
       copies_wait<F::kStages - 2>();
-      __syncwarp();  // the stage is here for all lanes, and the one before is done with
+      if (kShare > 1)
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * kShare) : "memory");
+      else
+        __syncwarp();
+      // the stage is here for all, and the one before is done with
       const uint32_t there = s_there[warp][slot];
-      fetch(slot == 0 ? F::kStages - 1 : slot - 1, t + F::kStages - 1 < t1);
+      fetch(slot == 0 ? F::kStages - 1 : slot - 1, t + F::kStages - 1 < stages);
       look();
       unsigned char* const kt = ring + slot * F::kStage;
       unsigned char* const vt = kt + F::kRaw;
@@ -379,7 +398,6 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN>::kCtas)) 
 #pragma unroll
         for (int k = 0; k < 4; ++k) s[n][k] *= factor[n][k & 1];
       // what is not seen: only the last tiles, or those of broken tables, have any
-      const uint32_t first = t * kTile + warp * F::kTokens;  // position of the stage's first token
       const bool masked = first + F::kTokens > base || there != 0xFFFFu;
       uint32_t sees = 0xFFFFFFFFu;
       if (masked) {
@@ -419,13 +437,13 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN>::kCtas)) 
         v0 = scales[16 + g], v1 = scales[24 + g];
         const uint32_t e0 = (__float_as_uint(v0) >> 23) & 0xFFu, e1 = (__float_as_uint(v1) >> 23) & 0xFFu;
         scale_ex = max(e0 == 0xFFu ? 0u : e0, e1 == 0xFFu ? 0u : e1);
-        rises |= t == t0 || min(max(scale_ex, 31u), 227u) > exponent + kScaleSlack;
+        rises |= t == 0 || min(max(scale_ex, 31u), 227u) > exponent + kScaleSlack;
       }
       if (__any_sync(kFull, rises)) {
         const uint32_t ex_before = exponent;
         if (kCodes) {
           const uint32_t now = min(max(__reduce_max_sync(kFull, scale_ex), 31u), 227u);
-          if (t == t0 || now > exponent + kScaleSlack) exponent = now;
+          if (t == 0 || now > exponent + kScaleSlack) exponent = now;
         }
 #pragma unroll
         for (uint32_t n = 0; n < kN; ++n)
@@ -589,7 +607,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN>::kCtas)) 
         l += __shfl_xor_sync(kFull, l, 16);
         sum[n][h] = l;
         top[n][h] += (float)((int)exponent - 127);  // the reference of what was summed
-        if (g == 0) s_ref[warp][n * 8 + 2 * c + h] = top[n][h];
+        if (g == 0) s_ref[team][row0 + n * 8 + 2 * c + h] = top[n][h];
       }
     copies_wait<0>();
     __syncthreads();
@@ -597,13 +615,13 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN>::kCtas)) 
     for (uint32_t n = 0; n < kN; ++n)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t row = n * 8 + 2 * c + h;
+        const uint32_t row = row0 + n * 8 + 2 * c + h;
         float m = s_ref[0][row];
 #pragma unroll
-        for (int k = 1; k < 4; ++k) m = fmaxf(m, s_ref[k][row]);
+        for (uint32_t k = 1; k < F::kGroups; ++k) m = fmaxf(m, s_ref[k][row]);
         const float a = exp2_of(top[n][h] - (m == -INFINITY ? 0.f : m));
-        if (g == 0) s_sum[warp][row] = sum[n][h] * a;
-        float* const to = (float*)smem + (warp * F::kRows + row) * kPad;
+        if (g == 0) s_sum[team][row] = sum[n][h] * a;
+        float* const to = (float*)smem + (team * F::kRows + row) * kPad;
 #pragma unroll
         for (uint32_t d = 0; d < kSteps; ++d) {
           to[value_of(d)] = o[d][n][h] * a;
@@ -620,7 +638,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN>::kCtas)) 
       float m = -INFINITY, l = 0.f;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (uint32_t k = 0; k < 4; ++k) {
+      for (uint32_t k = 0; k < F::kGroups; ++k) {
         m = fmaxf(m, s_ref[k][row]);
         l += s_sum[k][row];
         const float4 y = *((const float4*)((const float*)smem + (k * F::kRows + row) * kPad) + quad);
@@ -664,13 +682,13 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN>::kCtas)) 
   }
 }
 
-template <typename T, uint32_t kPad, bool kCodes, uint32_t kN>
+template <typename T, uint32_t kPad, bool kCodes, uint32_t kN, uint32_t kShare>
 int launch_few(const AttnParams& p, cudaStream_t s) {
-  typedef Few<kPad, kCodes, kN> F;
-  const cudaError_t e = cudaFuncSetAttribute(attention_few_kernel<T, kPad, kCodes, kN>,
+  typedef Few<kPad, kCodes, kN, kShare> F;
+  const cudaError_t e = cudaFuncSetAttribute(attention_few_kernel<T, kPad, kCodes, kN, kShare>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, F::kBytes);
   if (e != cudaSuccess) return cuda_failure(e);
-  return launch_dependent(attention_few_kernel<T, kPad, kCodes, kN>, attn_grid(F::kCtas), kAttnThreads, F::kBytes, s, p);
+  return launch_dependent(attention_few_kernel<T, kPad, kCodes, kN, kShare>, attn_grid(F::kCtas), kAttnThreads, F::kBytes, s, p);
 }
 
 }  // namespace db

@@ -10,9 +10,11 @@ template <typename T, uint32_t kPad, bool kCodes>
 int launch_blocks(const AttnParams& p, uint32_t blocks, cudaStream_t s) {
   switch (blocks) {
     case 1:
-      return launch_few<T, kPad, kCodes, 1>(p, s);
+      return launch_few<T, kPad, kCodes, 1, 1>(p, s);
     case 2:
-      return launch_few<T, kPad, kCodes, 2>(p, s);
+      return launch_few<T, kPad, kCodes, 2, 1>(p, s);
+    case 4:
+      if constexpr (kCodes) return launch_few<T, kPad, kCodes, 2, 2>(p, s);
     default:
       return launch_many<T, kPad, kCodes>(p, s);
   }
