@@ -17,7 +17,8 @@ uint32_t padded_width(uint32_t width) { return width <= 64 ? 64 : width <= 128 ?
 // kernel for few; with 32, warps that share a ring two by two are faster for
 // codes (64 sequences of 20,000 tokens, 2 key heads: 288 us, the kernel for many
 // 350) and slower for 16-bit values (334, 270).
-uint32_t blocks_for(uint64_t rows, bool codes) {
+uint32_t blocks_for(uint64_t rows, uint32_t pad, bool codes) {
+  if (rows > 128 && pad <= 128) return 2 * kManyBlocks;
   return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 && codes ? 4 : kManyBlocks;
 }
 
@@ -30,7 +31,7 @@ size_t workspace_bytes(uint32_t group, uint32_t width, uint32_t max_tokens) {
   const uint32_t pad = padded_width(width);
   size_t floats = 0;  // the larger need of 16-bit values and codes
   for (const bool codes : {false, true}) {
-    const uint32_t blocks = blocks_for((uint64_t)max_tokens * group, codes);
+    const uint32_t blocks = blocks_for((uint64_t)max_tokens * group, pad, codes);
     floats = std::max(floats, (size_t)2 * attn_grid(attn_ctas_per_sm(pad, codes, blocks)) * partial_floats(8 * blocks, pad));
   }
   return (kHeader + floats * 4 + 255) / 256 * 256;
@@ -88,7 +89,7 @@ extern "C" int db_cache_attention(const db_page_tables* t, const db_cache_batch*
   p.scale_head_step = c->heads_first ? t->page_tokens : 1;
   p.arrived = (unsigned int*)ws;
   p.partial = (float*)((char*)ws + kHeader);
-  const uint32_t blocks = blocks_for((uint64_t)max_tokens * p.group, item_bytes(c->type) == 1);
+  const uint32_t blocks = blocks_for((uint64_t)max_tokens * p.group, padded_width(c->width), item_bytes(c->type) == 1);
   switch (padded_width(c->width)) {
     case 64:
       return launch_attention_64(p, type, blocks, s);

@@ -20,7 +20,7 @@ constexpr uint32_t kTile = 64;             // tokens of a unit
 constexpr uint32_t kAttnThreads = 128;
 constexpr uint32_t kMaxGroup = 64;
 constexpr uint32_t kScaleSlack = 4;        // a larger exponent of scales is followed from here on
-constexpr uint32_t kManyBlocks = 16;      // blocks of 8 query rows of the tcgen05 kernel's items
+constexpr uint32_t kManyBlocks = 16;      // blocks of 8 query rows of the tcgen05 kernel's items, or twice as many
 
 struct AttnParams {
   CacheView view;
@@ -42,7 +42,7 @@ struct AttnParams {
 // CTAs of an SM of a kernel for so many blocks of 8 query rows: as many as
 // registers and shared memory hold.
 constexpr uint32_t attn_ctas_per_sm(uint32_t pad, bool codes, uint32_t blocks) {
-  if (blocks == kManyBlocks) return 2;
+  if (blocks >= kManyBlocks) return pad <= 128 && blocks == kManyBlocks ? 2 : 1;
   return pad == 64 ? 4 : pad == 128 ? (codes || blocks == 1 ? 3 : 2) : codes ? 2 : 1;
 }
 constexpr unsigned kMaxAttnCtas = 1024;

@@ -32,27 +32,31 @@
 
 namespace db {
 
-template <uint32_t kPad, bool kCodes>
+template <uint32_t kPad, bool kCodes, uint32_t kTiles>
 struct Many {
-  static constexpr uint32_t kRows = 128;
-  // 256 threads: 128 registers each with two CTAs an SM (9 warps would leave 96)
-  static constexpr uint32_t kThreads = 256;
-  static constexpr uint32_t kWeights = 128;
+  static constexpr uint32_t kRows = 128 * kTiles;
+  static constexpr uint32_t kWeights = 128 * kTiles;
   // Loaders that have units in turn. As they divide the ring, a place of it is
   // always the same warp's, which so sees every phase of its barrier (a wait by
   // parity is true too early when another phase lies between).
-  static constexpr uint32_t kLoaderWarps = kCodes ? 3 : 2;
+  static constexpr uint32_t kLoaderWarps = kCodes ? 3 * kTiles : 2 * kTiles;
+  // With 128 rows 256 threads: 128 registers each with two CTAs an SM (9 warps
+  // would leave 96).
+  static constexpr uint32_t kWarps = kTiles == 1 ? 8 : kWeights / 32 + kLoaderWarps + 1;
+  static constexpr uint32_t kThreads = 32 * kWarps;
   static constexpr uint32_t kUnit = kTile * kPad * 2;  // keys or values of a tile
-  static constexpr uint32_t kUnits = kCodes ? 3 : kPad >= 128 ? 4 : 6;
+  static constexpr uint32_t kUnits = kCodes ? 3 * kTiles : kTiles == 2 ? 8 : kPad >= 128 ? 4 : 6;
   static_assert(kUnits % kLoaderWarps == 0, "see kLoaderWarps");
   static constexpr uint32_t kQuery = kRows * kPad * 2;
   static constexpr uint32_t kRaw = kTile * kPad;       // codes of a unit
-  static constexpr uint32_t kRaws = kCodes ? 3 : 0;
+  static constexpr uint32_t kRaws = kCodes ? kLoaderWarps : 0;
   static constexpr uint32_t kMeta = kUnits / 2 + 3;    // tiles that notes are kept of
-  static constexpr uint32_t kColumns = kPad <= 128 ? 256 : 512;  // of TMEM
+  static constexpr uint32_t kColumns = kPad * kTiles <= 128 ? 256 : 512;  // of TMEM
+  static constexpr uint32_t kCtas = kPad <= 128 && kTiles == 1 ? 2 : 1;   // of an SM
   static constexpr uint32_t kBytes = kUnits * kUnit + kQuery + kRaws * kRaw + 1024;
-  // no more than two CTAs an SM, which is what TMEM holds
-  static constexpr uint32_t kAsk = kBytes < 80 * 1024 ? 80 * 1024 : kBytes;
+  // no more CTAs an SM than TMEM holds
+  static constexpr uint32_t kLeast = (kCtas == 2 ? 80 : 120) * 1024;
+  static constexpr uint32_t kAsk = kBytes < kLeast ? kLeast : kBytes;
 };
 
 // What the weights' warps need to know of a tile, by the loaders.
@@ -296,15 +300,16 @@ static __device__ __noinline__ void add_odd(const TileNotes& m, uint32_t output,
 
 constexpr float kSlack = 8.f;          // a maximum is followed when it has risen by this much (log2)
 
-template <typename T, uint32_t kPad, bool kCodes>
-__global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kernel(const AttnParams p) {
-  typedef Many<kPad, kCodes> F;
-  typedef typename std::conditional<kCodes, __half, T>::type W;  // of weights and values
-  constexpr uint32_t kTypeQ = std::is_same<T, __half>::value ? 0 : 1, kTypeW = std::is_same<W, __half>::value ? 0 : 1;
-  constexpr uint32_t kPanel = kTile * 128, kQueryPanel = F::kRows * 128;
+template <typename T, uint32_t kPad, bool kCodes, uint32_t kTiles>
+__global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<kPad, kCodes, kTiles>::kCtas))
+    attention_many_kernel(const AttnParams p) {
+  typedef Many<kPad, kCodes, kTiles> F;
+  typedef typename std::conditional<kCodes, __half, T>::type W;  // what is multiplied
+  constexpr uint32_t kTypeW = std::is_same<W, __half>::value ? 0 : 1, kIssuer = F::kWarps - 1;
+  constexpr uint32_t kPanel = kTile * 128, kQueryPanel = 128 * 128, kQueryTile = 128 * kPad * 2;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ TileNotes s_notes[F::kMeta];
-  __shared__ uint64_t s_full[F::kUnits], s_empty[F::kUnits], s_scores[2], s_weights[2], s_output[2], s_odd[F::kMeta], s_asked, s_drained;
+  __shared__ uint64_t s_full[F::kUnits], s_empty[F::kUnits], s_scores[kTiles][2], s_weights[kTiles][2], s_output[kTiles][2], s_odd[F::kMeta], s_asked, s_drained;
   __shared__ uint32_t s_tmem, s_last;
   __shared__ __align__(16) float s_ones[kCodes ? kTile : 4];  // keys' scales of scores that have theirs
   __shared__ volatile uint32_t s_failed;
@@ -312,7 +317,7 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
   unsigned char* const smem = smem_raw + ((1024 - (smem_at(smem_raw) & 1023)) & 1023);
   const uint32_t ring = smem_at(smem), query = ring + F::kUnits * F::kUnit;
 
-  if (warp == 7) {
+  if (warp == kIssuer) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_at(&s_tmem)), "n"(F::kColumns)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -323,13 +328,13 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
       barrier_init(smem_at(&s_full[k]), 32);  // a warp's lanes
       barrier_init(smem_at(&s_empty[k]), 1);
     }
-    for (int k = 0; k < 2; ++k) {
-      barrier_init(smem_at(&s_scores[k]), 2);  // the products, and the notes that came with the keys
-      barrier_init(smem_at(&s_weights[k]), F::kWeights);
+    for (uint32_t k = 0; k < 2 * kTiles; ++k) {
+      barrier_init(smem_at(&s_scores[k / 2][k & 1]), 2);  // the products, and the notes that came with the keys
+      barrier_init(smem_at(&s_weights[k / 2][k & 1]), 128);
       // one for even and one for odd tiles: a wait by parity must not be two
       // phases behind, and not every product is waited for (those of two tiles
       // before are over when a tile's scores come)
-      barrier_init(smem_at(&s_output[k]), 1);
+      barrier_init(smem_at(&s_output[k / 2][k & 1]), 1);
     }
     for (uint32_t k = 0; k < F::kMeta; ++k) barrier_init(smem_at(&s_odd[k]), 32);
     barrier_init(smem_at(&s_asked), F::kWeights);  // an item's queries are there
@@ -347,7 +352,7 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
   }
   __syncthreads();
   tensor_fence_after();
-  const uint32_t tmem = s_tmem, scores = tmem, output = tmem + 2 * kTile;
+  const uint32_t tmem = s_tmem, scores = tmem, output = tmem + 2 * kTiles * kTile;  // of the first 128 rows
   const uint32_t steps = p.c.width / 16;
   const bool e4m3 = p.c.type == DB_E4M3;
 
@@ -372,7 +377,7 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
     const uint32_t rows = min(F::kRows, r.rows * p.group - rb * F::kRows);
     const uint32_t base = r.length - r.rows;  // tokens before the request's own
 
-    if (warp >= 4 && warp < 4 + F::kLoaderWarps) {
+    if (warp >= F::kWeights / 32 && warp < F::kWeights / 32 + F::kLoaderWarps) {
       // ------------------------------------------------------------- loaders
       // A warp has every second or third unit to itself, and waits for no other.
       const uint32_t mine = warp - F::kWeights / 32, own = (mine + F::kLoaderWarps - units % F::kLoaderWarps) % F::kLoaderWarps;
@@ -563,8 +568,7 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
           copies_wait<0>();
           if (!key && !whole) check(t, w, [&](uint32_t, uint32_t k) __attribute__((always_inline)) { return raw - ring + k * 512; });
           unsigned char* const to = smem + slot_of(u) * F::kUnit + chunk / 4 * kPanel;
-          const auto widen_all = [&](auto as, auto four) __attribute__((always_inline)) {
-            typedef decltype(as) H;
+          const auto widen_all = [&](auto four) __attribute__((always_inline)) {
             constexpr bool kFour = decltype(four)::value;
             constexpr uint32_t kBatch = kEach < 8 ? kEach : 8;
 #pragma unroll 1
@@ -575,24 +579,17 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
 #pragma unroll
               for (uint32_t k = 0; k < kBatch; ++k) {
                 const uint32_t token = token0 + (k0 + k) * kStep;
-                const uint2 y[4] = {widen4<H>(c[k].x, kFour), widen4<H>(c[k].y, kFour), widen4<H>(c[k].z, kFour), widen4<H>(c[k].w, kFour)};
+                const uint2 y[4] = {widen4<W>(c[k].x, kFour), widen4<W>(c[k].y, kFour), widen4<W>(c[k].z, kFour), widen4<W>(c[k].w, kFour)};
                 *(uint4*)(to + token * 128 + (((2 * chunk) & 7) ^ (token & 7)) * 16) = make_uint4(y[0].x, y[0].y, y[1].x, y[1].y);
                 *(uint4*)(to + token * 128 + (((2 * chunk + 1) & 7) ^ (token & 7)) * 16) = make_uint4(y[2].x, y[2].y, y[3].x, y[3].y);
               }
             }
           };
           if (has) {
-            if (e4m3) {
-              if (key)
-                widen_all(T{}, std::true_type{});
-              else
-                widen_all(W{}, std::true_type{});
-            } else {
-              if (key)
-                widen_all(T{}, std::false_type{});
-              else
-                widen_all(W{}, std::false_type{});
-            }
+            if (e4m3)
+              widen_all(std::true_type{});
+            else
+              widen_all(std::false_type{});
           }
           hand_on(u);
           __syncwarp();
@@ -641,10 +638,10 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
         }
       }
       go = __all_sync(kFull, !s_failed);
-    } else if (warp == 7) {
+    } else if (warp == kIssuer) {
       // ------------------------------------------------------------- products
       if (lane == 0) {
-        const uint32_t kind_s = product_kind(kTypeQ, kTile, false), kind_o = product_kind(kTypeW, p.c.width, true);
+        const uint32_t kind_s = product_kind(kTypeW, kTile, false), kind_o = product_kind(kTypeW, p.c.width, true);
         const auto unit_at = [&](uint32_t u, uint32_t& slot) {  // waits until a unit is there
           slot = (units + u) % F::kUnits;
           return barrier_wait(smem_at(&s_full[slot]), ((units + u) / F::kUnits) & 1, &s_failed);
@@ -654,14 +651,17 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
           if (!unit_at(k ? 2 * k - 1 : 0, slot)) return false;
           tensor_fence_after();
           const uint32_t buffer = (tiles + k) & 1;
-          for (uint32_t st = 0; st < steps; ++st) {
-            const uint32_t off = (st & 3) * 32;
-            tensor_multiply(scores + buffer * kTile, tile_descriptor(query + (st / 4) * kQueryPanel + off, 16),
-                            tile_descriptor(ring + slot * F::kUnit + (st / 4) * kPanel + off, 16), kind_s, st > 0);
+#pragma unroll 1
+          for (uint32_t i = 0; i < kTiles; ++i) {
+            for (uint32_t st = 0; st < steps; ++st) {
+              const uint32_t off = (st & 3) * 32;
+              tensor_multiply(scores + (2 * i + buffer) * kTile, tile_descriptor(query + i * kQueryTile + (st / 4) * kQueryPanel + off, 16),
+                              tile_descriptor(ring + slot * F::kUnit + (st / 4) * kPanel + off, 16), kind_s, st > 0);
+            }
+            tensor_commit(smem_at(&s_scores[i][buffer]));
+            barrier_arrive(smem_at(&s_scores[i][buffer]));
           }
-          tensor_commit(smem_at(&s_scores[buffer]));
           tensor_commit(smem_at(&s_empty[slot]));
-          barrier_arrive(smem_at(&s_scores[buffer]));
           return true;
         };
         bool ok = barrier_wait(smem_at(&s_asked), items & 1, &s_failed) && score(0);
@@ -670,44 +670,84 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
           if (!ok) break;
           const uint32_t buffer = (tiles + k) & 1;
           uint32_t slot;
-          ok = unit_at(k + 1 < n ? 2 * k + 2 : 2 * n - 1, slot) &&
-               barrier_wait(smem_at(&s_weights[buffer]), ((tiles + k) >> 1) & 1, &s_failed);
-          if (!ok) break;
-          tensor_fence_after();
+          ok = unit_at(k + 1 < n ? 2 * k + 2 : 2 * n - 1, slot);
+#pragma unroll 1
+          for (uint32_t i = 0; ok && i < kTiles; ++i) {
+            ok = barrier_wait(smem_at(&s_weights[i][buffer]), ((tiles + k) >> 1) & 1, &s_failed);
+            if (!ok) break;
+            tensor_fence_after();
 #pragma unroll
-          for (uint32_t st = 0; st < kTile / 16; ++st)
-            tensor_multiply_t(output, scores + buffer * kTile + st * 8,
-                              tile_descriptor(ring + slot * F::kUnit + st * 2048, kPanel), kind_o, true);
+            for (uint32_t st = 0; st < kTile / 16; ++st)
+              tensor_multiply_t(output + i * kPad, scores + (2 * i + buffer) * kTile + st * 8,
+                                tile_descriptor(ring + slot * F::kUnit + st * 2048, kPanel), kind_o, true);
+            tensor_commit(smem_at(&s_output[i][buffer]));
+          }
+          if (!ok) break;
           tensor_commit(smem_at(&s_empty[slot]));
-          tensor_commit(smem_at(&s_output[buffer]));
         }
         go = ok;
       }
       go = __shfl_sync(kFull, go, 0);
-    } else if (warp < 4) {
+    } else if (warp < F::kWeights / 32) {
       // -------------------------------------------------------------- weights
-      const uint32_t row = tid, lanes = (warp * 32) << 16;
+      const uint32_t row = tid, lanes = (warp & 3) << 21, half = warp / 4;  // of 128 rows
+      const uint32_t sums_at = output + half * kPad + lanes;
       const bool row_real = row < rows;
       const uint32_t all = rb * F::kRows + (row_real ? row : 0), node = all / p.group;
       const uint32_t* const mask = p.mask ? p.mask + (uint64_t)(r.first + node) * p.mask_words : nullptr;
-      const float factor = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
+      float factor = kCodes || p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);  // of the row's scores
       {
         // The row's query; the products with the one before were over when its
-        // last scores came.
+        // last scores came. For codes a bf16 one becomes f16, times the power of
+        // two that takes its largest value to 2^14.
         constexpr uint32_t kFetch = kPad == 64 ? 8 : 16;
+        constexpr bool kTurns = kCodes && !std::is_same<T, __half>::value;
         const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u, keep = p.scale_log2 == 0.f ? 0u : 0xFFFFFFFFu;
         const char* const from = (const char*)p.q.base + (uint64_t)(r.first + node) * p.q.row_stride +
                                  (head * p.group + (all - node * p.group)) * p.q.head_stride;
+        uint32_t largest = 0;
 #pragma unroll 1
-        for (uint32_t c0 = 0; c0 < p.c.width / 8; c0 += kFetch) {
-          uint4 v[kFetch];
+        for (uint32_t pass = kTurns && kPad > 128 ? 0 : 1; pass < 2; ++pass) {
+#pragma unroll 1
+          for (uint32_t c0 = 0; c0 < p.c.width / 8; c0 += kFetch) {
+            uint4 v[kFetch];
 #pragma unroll
-          for (uint32_t c = 0; c < kFetch; ++c)
-            v[c] = row_real && c0 + c < p.c.width / 8 ? __ldg((const uint4*)from + c0 + c) : make_uint4(0, 0, 0, 0);
+            for (uint32_t c = 0; c < kFetch; ++c) {
+              v[c] = row_real && c0 + c < p.c.width / 8 ? __ldg((const uint4*)from + c0 + c) : make_uint4(0, 0, 0, 0);
+              v[c].x = (v[c].x ^ flip) & keep, v[c].y = (v[c].y ^ flip) & keep, v[c].z = (v[c].z ^ flip) & keep, v[c].w = (v[c].w ^ flip) & keep;
+            }
+            float up = 1.f;
+            if constexpr (kTurns) {
+              if (kPad <= 128 || pass == 0) {
 #pragma unroll
-          for (uint32_t c = 0; c < kFetch; ++c) {
-            v[c].x = (v[c].x ^ flip) & keep, v[c].y = (v[c].y ^ flip) & keep, v[c].z = (v[c].z ^ flip) & keep, v[c].w = (v[c].w ^ flip) & keep;
-            *(uint4*)(smem + F::kUnits * F::kUnit + (c0 + c) / 8 * kQueryPanel + row * 128 + ((c & 7) ^ (row & 7)) * 16) = v[c];
+                for (uint32_t c = 0; c < kFetch; ++c) {
+                  const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {  // bits of magnitudes, those of infinities and NaN left out
+                    const uint32_t lo = w[k] & 0x7FFFu, hi = w[k] >> 16 & 0x7FFFu;
+                    largest = max(largest, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+                  }
+                }
+              }
+              const int exponent = largest == 0 ? 14 : max((int)(largest >> 7) - 127, 14 - 126);
+              up = __uint_as_float((uint32_t)(14 - exponent + 127) << 23);
+              factor = __uint_as_float((uint32_t)(max(exponent - 14, -126) + 127) << 23);
+            }
+            if (pass == 0) continue;
+#pragma unroll
+            for (uint32_t c = 0; c < kFetch; ++c) {
+              if constexpr (kTurns) {
+                uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const float2 a = unpack2<T>(w[k]);
+                  w[k] = pack2<W>(a.x * up, a.y * up);
+                }
+                v[c] = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+              *(uint4*)(smem + F::kUnits * F::kUnit + half * kQueryTile + (c0 + c) / 8 * kQueryPanel + (row & 127) * 128 +
+                        ((c & 7) ^ (row & 7)) * 16) = v[c];
+            }
           }
         }
         writes_to_async_proxy();
@@ -723,14 +763,14 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
 #pragma unroll
         for (int j = 0; j < 16; ++j) zero[j] = 0;
 #pragma unroll 1
-        for (uint32_t c = 0; c < p.c.width; c += 16) tmem_store16(output + lanes + c, zero);
+        for (uint32_t c = 0; c < p.c.width; c += 16) tmem_store16(sums_at + c, zero);
         tmem_stored();
       }
       bool ok = true;
       for (uint32_t k = 0; k < n; ++k) {
         const uint32_t tile = tiles + k, buffer = tile & 1, t = t0 + k;
-        const uint32_t here = scores + buffer * kTile + lanes;
-        ok = barrier_wait(smem_at(&s_scores[buffer]), (tile >> 1) & 1, &s_failed);
+        const uint32_t here = scores + (2 * half + buffer) * kTile + lanes;
+        ok = barrier_wait(smem_at(&s_scores[half][buffer]), (tile >> 1) & 1, &s_failed);
         if (!__all_sync(kFull, ok)) break;
         tensor_fence_after();
         const TileNotes& m = s_notes[tile % F::kMeta];
@@ -777,7 +817,7 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
 #pragma unroll
         for (int j = 0; j < 32; j += 2) most = largest3(most, low(x[j]), high(x[j])), other = largest3(other, low(x[j + 1]), high(x[j + 1]));
         most = fmaxf(most, other);
-        if (!kCodes) most *= factor;
+        most *= factor;
         const float ref_before = top + (kCodes ? (float)((int)exponent - 127) : 0.f);
         bool move = most > top + kSlack || (top == -INFINITY && most > -INFINITY);
         if (move) top = most;
@@ -800,7 +840,7 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
         if (__any_sync(kFull, move && k) || odd) {
           // O belongs to this warp while no product adds to it
           if (k) {
-            ok = barrier_wait(smem_at(&s_output[buffer ^ 1]), ((tile - 1) >> 1) & 1, &s_failed);
+            ok = barrier_wait(smem_at(&s_output[half][buffer ^ 1]), ((tile - 1) >> 1) & 1, &s_failed);
             if (!__all_sync(kFull, ok)) break;
             tensor_fence_after();
           }
@@ -810,29 +850,29 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
 #pragma unroll 1
             for (uint32_t c = 0; c < p.c.width; c += 16) {
               uint32_t o[16];
-              tmem_load16(output + lanes + c, o);
+              tmem_load16(sums_at + c, o);
               tmem_loaded();
 #pragma unroll
               for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * down);
-              tmem_store16(output + lanes + c, o);
+              tmem_store16(sums_at + c, o);
             }
             tmem_stored();
           }
           if (odd)
-            add_odd<T, kCodes>(m, output + lanes, here, odd, (uint64_t)sees[1] << 32 | sees[0], kCodes ? 1.f : factor, ref,
+            add_odd<T, kCodes>(m, sums_at, here, odd, (uint64_t)sees[1] << 32 | sees[0], factor, ref,
                                (const char*)p.c.v + head * p.head_step, p.c.v_stride, p.token_step,
                                (const char*)(p.c.v_scale + (kCodes ? head * p.scale_head_step : 0)), p.c.v_scale_stride,
                                p.scale_token_step, !e4m3, p.c.width);
         }
         uint64_t sums = pair(__float_as_uint(sum), 0), more = pair(0, 0);
-        const uint64_t by = pair(__float_as_uint(kCodes ? 1.f : factor), __float_as_uint(kCodes ? 1.f : factor));
+        const uint64_t by = pair(__float_as_uint(factor), __float_as_uint(factor));
         const uint64_t less = pair(__float_as_uint(-ref), __float_as_uint(-ref));
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
           uint64_t y[2];
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            const uint64_t z = kCodes ? add2(x[j + g], less) : multiply_add2(x[j + g], by, less);
+            const uint64_t z = multiply_add2(x[j + g], by, less);
             y[g] = pair(__float_as_uint(exp2_of(low(z))), __float_as_uint(exp2_of(high(z))));
           }
           sums = add2(sums, y[0]);
@@ -851,9 +891,9 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
         tmem_store32(here, w);  // over the scores
         tmem_stored();
         tensor_fence_before();
-        barrier_arrive(smem_at(&s_weights[buffer]));
+        barrier_arrive(smem_at(&s_weights[half][buffer]));
       }
-      if (ok) ok = barrier_wait(smem_at(&s_output[(tiles + n - 1) & 1]), ((tiles + n - 1) >> 1) & 1, &s_failed);
+      if (ok) ok = barrier_wait(smem_at(&s_output[half][(tiles + n - 1) & 1]), ((tiles + n - 1) >> 1) & 1, &s_failed);
       go = group_all(1, F::kWeights, ok);
       if (go) {
         tensor_fence_after();
@@ -873,7 +913,7 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
         for (uint32_t c = 0; c < p.c.width; c += 16) {
           uint32_t o[16];
           __syncwarp();
-          tmem_load16(output + lanes + c, o);
+          tmem_load16(sums_at + c, o);
           tmem_loaded();
           if (!row_real) continue;
           const float* const f = (const float*)o;
@@ -927,8 +967,8 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
     units += 2 * n;
   }
   // nothing is under way when the shared memory and TMEM are given back
-  if (warp >= 4 && warp < 7) copies_wait<0>();
-  if (tid == 224) {
+  if (warp >= F::kWeights / 32 && warp < kIssuer) copies_wait<0>();
+  if (tid == 32 * kIssuer) {
     tensor_commit(smem_at(&s_drained));
     const uint64_t began = globaltimer_ns();
     while (!barrier_try(smem_at(&s_drained), 0) && globaltimer_ns() - began < kWaitLimitNs) {
@@ -937,17 +977,17 @@ __global__ void __launch_bounds__(256, kPad <= 128 ? 2 : 1) attention_many_kerne
   if (!go && tid == 0 && p.view.ctr) atomicOr((unsigned int*)&p.view.ctr->err, DB_ERR_TIMEOUT);
   tensor_fence_before();
   __syncthreads();
-  if (warp == 7)
+  if (warp == kIssuer)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(F::kColumns));
 }
 
-template <typename T, uint32_t kPad, bool kCodes>
+template <typename T, uint32_t kPad, bool kCodes, uint32_t kTiles>
 int launch_many(const AttnParams& p, cudaStream_t s) {
-  typedef Many<kPad, kCodes> F;
-  const cudaError_t e = cudaFuncSetAttribute(attention_many_kernel<T, kPad, kCodes>,
+  typedef Many<kPad, kCodes, kTiles> F;
+  const cudaError_t e = cudaFuncSetAttribute(attention_many_kernel<T, kPad, kCodes, kTiles>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, F::kAsk);
   if (e != cudaSuccess) return cuda_failure(e);
-  return launch_dependent(attention_many_kernel<T, kPad, kCodes>, attn_grid(attn_ctas_per_sm(kPad, kCodes, kManyBlocks)), F::kThreads, F::kAsk, s, p);
+  return launch_dependent(attention_many_kernel<T, kPad, kCodes, kTiles>, attn_grid(attn_ctas_per_sm(kPad, kCodes, F::kRows / 8)), F::kThreads, F::kAsk, s, p);
 }
 
 }  // namespace db
