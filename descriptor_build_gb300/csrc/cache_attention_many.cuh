@@ -42,7 +42,7 @@ struct Many {
   static constexpr uint32_t kLoaderWarps = kCodes ? 3 * kTiles : 2 * kTiles;
   // With 128 rows 256 threads: 128 registers each with two CTAs an SM (9 warps
   // would leave 96).
-  static constexpr uint32_t kWarps = kTiles == 1 ? 8 : kWeights / 32 + kLoaderWarps + 1;
+  static constexpr uint32_t kWarps = kTiles == 1 ? 8 : kWeights / 32 + kLoaderWarps + kTiles;
   static constexpr uint32_t kThreads = 32 * kWarps;
   static constexpr uint32_t kUnit = kTile * kPad * 2;  // keys or values of a tile
   static constexpr uint32_t kUnits = kCodes ? 3 * kTiles : kTiles == 2 ? 8 : kPad >= 128 ? 4 : 6;
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
     attention_many_kernel(const AttnParams p) {
   typedef Many<kPad, kCodes, kTiles> F;
   typedef typename std::conditional<kCodes, __half, T>::type W;  // what is multiplied
-  constexpr uint32_t kTypeW = std::is_same<W, __half>::value ? 0 : 1, kIssuer = F::kWarps - 1;
+  constexpr uint32_t kTypeW = std::is_same<W, __half>::value ? 0 : 1, kIssuer = F::kWarps - kTiles;  // the first warp with an issuing thread
   constexpr uint32_t kPanel = kTile * 128, kQueryPanel = 128 * 128, kQueryTile = 128 * kPad * 2;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ TileNotes s_notes[F::kMeta];
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
   unsigned char* const smem = smem_raw + ((1024 - (smem_at(smem_raw) & 1023)) & 1023);
   const uint32_t ring = smem_at(smem), query = ring + F::kUnits * F::kUnit;
 
-  if (warp == kIssuer) {
+  if (warp == F::kWarps - 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_at(&s_tmem)), "n"(F::kColumns)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
   if (tid == 0) {
     for (uint32_t k = 0; k < F::kUnits; ++k) {
       barrier_init(smem_at(&s_full[k]), 32);  // a warp's lanes
-      barrier_init(smem_at(&s_empty[k]), 1);
+      barrier_init(smem_at(&s_empty[k]), kTiles);
     }
     for (uint32_t k = 0; k < 2 * kTiles; ++k) {
       barrier_init(smem_at(&s_scores[k / 2][k & 1]), 2);  // the products, and the notes that came with the keys
@@ -338,9 +338,20 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
     }
     for (uint32_t k = 0; k < F::kMeta; ++k) barrier_init(smem_at(&s_odd[k]), 32);
     barrier_init(smem_at(&s_asked), F::kWeights);  // an item's queries are there
-    barrier_init(smem_at(&s_drained), 1);
+    barrier_init(smem_at(&s_drained), kTiles);
     s_failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  // Keys behind the width's end are zeros, which nothing writes over, so that
+  // the number of products is known to the code.
+  if (p.c.width < kPad) {
+    constexpr uint32_t kChunks = kPad / 8;
+    for (uint32_t i = tid; i < F::kUnits * kTile * kChunks; i += F::kThreads) {
+      const uint32_t chunk = i % kChunks, token = i / kChunks % kTile, unit = i / (kChunks * kTile);
+      if (chunk * 8 >= p.c.width)
+        *(uint4*)(smem + unit * F::kUnit + chunk / 8 * kPanel + token * 128 + ((chunk & 7) ^ (token & 7)) * 16) = make_uint4(0, 0, 0, 0);
+    }
+    writes_to_async_proxy();
   }
   wait_for_prerequisites();
   dependents_may_launch();
@@ -353,7 +364,6 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
   __syncthreads();
   tensor_fence_after();
   const uint32_t tmem = s_tmem, scores = tmem, output = tmem + 2 * kTiles * kTile;  // of the first 128 rows
-  const uint32_t steps = p.c.width / 16;
   const bool e4m3 = p.c.type == DB_E4M3;
 
   // All kinds of warps go through the same items and tiles.
@@ -638,11 +648,17 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
         }
       }
       go = __all_sync(kFull, !s_failed);
-    } else if (warp == kIssuer) {
+    } else if (warp >= kIssuer) {
       // ------------------------------------------------------------- products
       if (lane == 0) {
         const uint32_t kind_s = product_kind(kTypeW, kTile, false), kind_o = product_kind(kTypeW, p.c.width, true);
-        const auto unit_at = [&](uint32_t u, uint32_t& slot) {  // waits until a unit is there
+        // A thread makes all products of 128 rows, and is short of time.
+        const uint32_t i = warp - kIssuer;
+        const uint64_t queries = tile_descriptor(query + i * kQueryTile, 16), keys = tile_descriptor(ring, 16), values = tile_descriptor(ring, kPanel);
+        const auto moved = [](uint64_t d, uint32_t bytes) __attribute__((always_inline)) {
+          return d & 0xFFFFFFFF00000000ull | (uint32_t)((uint32_t)d + bytes / 16);
+        };
+        const auto unit_at = [&](uint32_t u, uint32_t& slot) __attribute__((always_inline)) {  // waits until a unit is there
           slot = (units + u) % F::kUnits;
           return barrier_wait(smem_at(&s_full[slot]), ((units + u) / F::kUnits) & 1, &s_failed);
         };
@@ -650,18 +666,14 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
           uint32_t slot;
           if (!unit_at(k ? 2 * k - 1 : 0, slot)) return false;
           tensor_fence_after();
-          const uint32_t buffer = (tiles + k) & 1;
-#pragma unroll 1
-          for (uint32_t i = 0; i < kTiles; ++i) {
-            for (uint32_t st = 0; st < steps; ++st) {
-              const uint32_t off = (st & 3) * 32;
-              tensor_multiply(scores + (2 * i + buffer) * kTile, tile_descriptor(query + i * kQueryTile + (st / 4) * kQueryPanel + off, 16),
-                              tile_descriptor(ring + slot * F::kUnit + (st / 4) * kPanel + off, 16), kind_s, st > 0);
-            }
-            tensor_commit(smem_at(&s_scores[i][buffer]));
-            barrier_arrive(smem_at(&s_scores[i][buffer]));
-          }
+          const uint32_t buffer = (tiles + k) & 1, to = scores + (2 * i + buffer) * kTile;
+          const uint64_t key = moved(keys, slot * F::kUnit);
+#pragma unroll
+          for (uint32_t st = 0; st < kPad / 16; ++st)
+            tensor_multiply(to, moved(queries, st / 4 * kQueryPanel + st % 4 * 32), moved(key, st / 4 * kPanel + st % 4 * 32), kind_s, st > 0);
+          tensor_commit(smem_at(&s_scores[i][buffer]));
           tensor_commit(smem_at(&s_empty[slot]));
+          barrier_arrive(smem_at(&s_scores[i][buffer]));
           return true;
         };
         bool ok = barrier_wait(smem_at(&s_asked), items & 1, &s_failed) && score(0);
@@ -670,19 +682,15 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
           if (!ok) break;
           const uint32_t buffer = (tiles + k) & 1;
           uint32_t slot;
-          ok = unit_at(k + 1 < n ? 2 * k + 2 : 2 * n - 1, slot);
-#pragma unroll 1
-          for (uint32_t i = 0; ok && i < kTiles; ++i) {
-            ok = barrier_wait(smem_at(&s_weights[i][buffer]), ((tiles + k) >> 1) & 1, &s_failed);
-            if (!ok) break;
-            tensor_fence_after();
-#pragma unroll
-            for (uint32_t st = 0; st < kTile / 16; ++st)
-              tensor_multiply_t(output + i * kPad, scores + (2 * i + buffer) * kTile + st * 8,
-                                tile_descriptor(ring + slot * F::kUnit + st * 2048, kPanel), kind_o, true);
-            tensor_commit(smem_at(&s_output[i][buffer]));
-          }
+          ok = unit_at(k + 1 < n ? 2 * k + 2 : 2 * n - 1, slot) &&
+               barrier_wait(smem_at(&s_weights[i][buffer]), ((tiles + k) >> 1) & 1, &s_failed);
           if (!ok) break;
+          tensor_fence_after();
+          const uint64_t value = moved(values, slot * F::kUnit);
+#pragma unroll
+          for (uint32_t st = 0; st < kTile / 16; ++st)
+            tensor_multiply_t(output + i * kPad, scores + (2 * i + buffer) * kTile + st * 8, moved(value, st * 2048), kind_o, true);
+          tensor_commit(smem_at(&s_output[i][buffer]));
           tensor_commit(smem_at(&s_empty[slot]));
         }
         go = ok;
@@ -968,7 +976,7 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
   }
   // nothing is under way when the shared memory and TMEM are given back
   if (warp >= F::kWeights / 32 && warp < kIssuer) copies_wait<0>();
-  if (tid == 32 * kIssuer) {
+  if (warp >= kIssuer && lane == 0) {
     tensor_commit(smem_at(&s_drained));
     const uint64_t began = globaltimer_ns();
     while (!barrier_try(smem_at(&s_drained), 0) && globaltimer_ns() - began < kWaitLimitNs) {
@@ -977,7 +985,7 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
   if (!go && tid == 0 && p.view.ctr) atomicOr((unsigned int*)&p.view.ctr->err, DB_ERR_TIMEOUT);
   tensor_fence_before();
   __syncthreads();
-  if (warp == kIssuer)
+  if (warp == F::kWarps - 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(F::kColumns));
 }
 
