@@ -267,70 +267,4 @@ struct JoinedItem {
   uint32_t first, row0, rows, head, c0, c1;
 };
 
-// Joins the parts of CTAs c0 to c1, in their order, and writes the answer. A
-// thread for each row finds the rows' maxima and sums, which go to `row_notes`
-// (16 bytes a row of shared memory); then kMany times four values a thread are
-// summed at a time, so that their loads are under way together. `group` is a
-// named barrier of the kThreads threads.
-template <typename T, uint32_t kRows, uint32_t kPad, uint32_t kThreads>
-static __device__ __noinline__ void join_item(const AttnParams& p, const JoinedItem item, float4* row_notes, uint32_t barrier) {
-  constexpr uint32_t kQuads = kPad / 4, kMany = 8, kPart = kRows * (kPad + 2);
-  const float* const parts = p.partial + (uint64_t)2 * item.c0 * kPart;  // the first is its CTA's second
-  const auto part_at = [&](uint32_t k) { return parts + (k == item.c0 ? kPart : (uint64_t)2 * (k - item.c0) * kPart); };
-  if (threadIdx.x < item.rows) {
-    const uint32_t row = threadIdx.x;
-    float m = -INFINITY, l = 0.f;
-#pragma unroll 4
-    for (uint32_t k = item.c0; k <= item.c1; ++k) {
-      const float mk = __ldcg(part_at(k) + kRows * kPad + row), lk = __ldcg(part_at(k) + kRows * kPad + kRows + row);
-      const float now = fmaxf(m, mk), by = now == -INFINITY ? 0.f : now;
-      l = l * exp2_of(m - by) + lk * exp2_of(mk - by);
-      m = now;
-    }
-    const uint32_t all = item.row0 + row, node = all / p.group, qh = item.head * p.group + (all - node * p.group);
-    const uint64_t to = (uint64_t)(item.first + node) * p.out.row_stride + qh * p.out.head_stride;
-    row_notes[row] = make_float4(m == -INFINITY ? 0.f : m, l == 0.f ? 0.f : 1.f / l, __uint_as_float((uint32_t)to),
-                                 __uint_as_float((uint32_t)(to >> 32)));
-    if (p.lse)
-      p.lse[(uint64_t)(item.first + node) * (p.c.heads * p.group) + qh] =
-          l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
-  }
-  __syncwarp();
-  asm volatile("bar.sync %0, %1;" ::"r"(barrier), "n"(kThreads) : "memory");
-  const uint32_t all = item.rows * kQuads;
-#pragma unroll 1
-  for (uint32_t c = threadIdx.x; c < all; c += kThreads * kMany) {
-    float4 v[kMany];
-#pragma unroll
-    for (uint32_t j = 0; j < kMany; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-    for (uint32_t k = item.c0; k <= item.c1; ++k) {
-      const float* const at = part_at(k);
-      float m[kMany];
-      float4 y[kMany];
-#pragma unroll
-      for (uint32_t j = 0; j < kMany; ++j) {
-        const uint32_t of = min(c + j * kThreads, all - 1), row = of / kQuads, quad = min(of % kQuads, p.c.width / 4 - 1);
-        m[j] = __ldcg(at + kRows * kPad + row);
-        y[j] = __ldcg((const float4*)(at + row * kPad) + quad);
-      }
-#pragma unroll
-      for (uint32_t j = 0; j < kMany; ++j) {
-        const float b = exp2_of(m[j] - row_notes[min(c + j * kThreads, all - 1) / kQuads].x);
-        v[j].x += y[j].x * b, v[j].y += y[j].y * b, v[j].z += y[j].z * b, v[j].w += y[j].w * b;
-      }
-    }
-#pragma unroll
-    for (uint32_t j = 0; j < kMany; ++j) {
-      const uint32_t of = c + j * kThreads;
-      if (of < all && of % kQuads * 4 < p.c.width) {
-        const float4 n = row_notes[of / kQuads];
-        const uint64_t to = (uint64_t)__float_as_uint(n.w) << 32 | __float_as_uint(n.z);
-        *(uint2*)((char*)p.out.base + to + of % kQuads * 8) =
-            make_uint2(pack2<T>(v[j].x * n.y, v[j].y * n.y), pack2<T>(v[j].z * n.y, v[j].w * n.y));
-      }
-    }
-  }
-}
-
 }  // namespace db

@@ -298,6 +298,75 @@ static __device__ __noinline__ void add_odd(const TileNotes& m, uint32_t output,
   }
 }
 
+// The parts of an item, joined by kThreads threads (the named barrier is
+// theirs). A part lies by fours of values, of all rows: a warp's rows are
+// neighbours when it stores its sums, a row to a thread, and when it reads them
+// here. A thread joins 32 values of a row (16 where rows are few), two parts' loads under way together.
+template <typename T, uint32_t kRows, uint32_t kPad, uint32_t kThreads>
+static __device__ __noinline__ void join_item(const AttnParams& p, const JoinedItem item, float4* row_notes, uint32_t barrier) {
+  constexpr uint32_t kMany = 8, kPart = kRows * (kPad + 2);
+  const float* const parts = p.partial + (uint64_t)2 * item.c0 * kPart;  // the first is its CTA's second
+  const auto part_at = [&](uint32_t k) { return parts + (k == item.c0 ? kPart : (uint64_t)2 * (k - item.c0) * kPart); };
+  if (threadIdx.x < item.rows) {
+    const uint32_t row = threadIdx.x;
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+    for (uint32_t k = item.c0; k <= item.c1; ++k) {
+      const float mk = __ldcg(part_at(k) + kRows * kPad + row), lk = __ldcg(part_at(k) + kRows * kPad + kRows + row);
+      const float now = fmaxf(m, mk), by = now == -INFINITY ? 0.f : now;
+      l = l * exp2_of(m - by) + lk * exp2_of(mk - by);
+      m = now;
+    }
+    const uint32_t all = item.row0 + row, node = all / p.group, qh = item.head * p.group + (all - node * p.group);
+    const uint64_t to = (uint64_t)(item.first + node) * p.out.row_stride + qh * p.out.head_stride;
+    row_notes[row] = make_float4(m == -INFINITY ? 0.f : m, l == 0.f ? 0.f : 1.f / l, __uint_as_float((uint32_t)to),
+                                 __uint_as_float((uint32_t)(to >> 32)));
+    if (p.lse)
+      p.lse[(uint64_t)(item.first + node) * (p.c.heads * p.group) + qh] =
+          l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+  }
+  __syncwarp();
+  asm volatile("bar.sync %0, %1;" ::"r"(barrier), "n"(kThreads) : "memory");
+  const uint32_t bits = item.rows > 32 ? 32 - __clz(item.rows - 1) : 5;  // 2^bits rows side by side
+  const uint32_t each = (p.c.width / 32) << bits >= kThreads ? kMany : 4;  // by fours, of a thread
+#pragma unroll 1
+  for (uint32_t c = threadIdx.x; c < (p.c.width / 4 + each - 1) / each << bits; c += kThreads) {
+    const uint32_t row = c & ((1u << bits) - 1), quad0 = (c >> bits) * each;
+    if (row >= item.rows) continue;
+    const uint32_t quads = min(each, p.c.width / 4 - quad0);
+    const float4 n = row_notes[row];
+    float4 v[kMany];
+#pragma unroll
+    for (uint32_t j = 0; j < kMany; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (uint32_t k = item.c0; k <= item.c1; k += 2) {
+      const bool two = k < item.c1;
+      const float* const a = part_at(k);
+      const float* const b = part_at(two ? k + 1 : k);
+      const float ma = __ldcg(a + kRows * kPad + row), mb = __ldcg(b + kRows * kPad + row);
+      float4 x[kMany], y[kMany];
+#pragma unroll
+      for (uint32_t j = 0; j < kMany; ++j) {
+        x[j] = __ldcg((const float4*)a + (quad0 + min(j, quads - 1)) * kRows + row);
+        y[j] = __ldcg((const float4*)b + (quad0 + min(j, quads - 1)) * kRows + row);
+      }
+      const float fa = exp2_of(ma - n.x), fb = two ? exp2_of(mb - n.x) : 0.f;
+#pragma unroll
+      for (uint32_t j = 0; j < kMany; ++j) {
+        v[j].x += x[j].x * fa, v[j].y += x[j].y * fa, v[j].z += x[j].z * fa, v[j].w += x[j].w * fa;
+        if (two) v[j].x += y[j].x * fb, v[j].y += y[j].y * fb, v[j].z += y[j].z * fb, v[j].w += y[j].w * fb;
+      }
+    }
+    char* const to = (char*)p.out.base + ((uint64_t)__float_as_uint(n.w) << 32 | __float_as_uint(n.z)) + quad0 * 8;
+#pragma unroll
+    for (uint32_t j = 0; j < kMany; j += 2)  // (width is a multiple of 16 values)
+      if (j < quads)
+        *(uint4*)(to + j * 8) =
+            make_uint4(pack2<T>(v[j].x * n.y, v[j].y * n.y), pack2<T>(v[j].z * n.y, v[j].w * n.y),
+                       pack2<T>(v[j + 1].x * n.y, v[j + 1].y * n.y), pack2<T>(v[j + 1].z * n.y, v[j + 1].w * n.y));
+  }
+}
+
 constexpr float kSlack = 8.f;          // a maximum is followed when it has risen by this much (log2)
 
 template <typename T, uint32_t kPad, bool kCodes, uint32_t kTiles>
@@ -934,7 +1003,7 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
           } else {
 #pragma unroll
             for (int j = 0; j < 16; j += 4)
-              __stcg((float4*)(mine + row * kPad + c + j), make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]));
+              __stcg((float4*)mine + (c + j) / 4 * F::kRows + row, make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]));
           }
         }
         const auto statistics = [&](uint32_t nd_, uint32_t qh_, float m_, float l_) {
