@@ -12,6 +12,8 @@
 // of the tokens: results do not depend on which one that is, and no CTA waits.
 #pragma once
 
+#include <type_traits>
+
 #include "cachedata.cuh"
 
 namespace db {
@@ -19,7 +21,17 @@ namespace db {
 constexpr uint32_t kTile = 64;             // tokens of a unit
 constexpr uint32_t kAttnThreads = 128;
 constexpr uint32_t kMaxGroup = 64;
-constexpr uint32_t kScaleSlack = 4;        // a larger exponent of scales is followed from here on
+// A row's maximum, and for codes the exponent of the values' largest scale, are
+// followed when they have risen by more than this (log2).
+constexpr float kSlack = 6.f;
+constexpr uint32_t kScaleSlack = 2;
+// Weights times scales are below 2^(kLift + 6 + 3): f16 ones start high, so that
+// those of 2^-20 are normal numbers still (without it the answers' error for
+// long caches was 1.5 times that of their rounding, 1.4 with it).
+template <typename W, bool kCodes>
+__host__ __device__ constexpr int attn_lift() {
+  return !std::is_same<W, __half>::value ? 0 : kCodes ? 6 : 8;
+}
 constexpr uint32_t kManyBlocks = 16;      // blocks of 8 query rows of the tcgen05 kernel's items, or twice as many
 
 struct AttnParams {

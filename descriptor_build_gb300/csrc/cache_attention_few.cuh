@@ -41,8 +41,6 @@ struct Few {
   static_assert(kBytes >= kGroups * kRows * kPad * 4 && kBytes >= 4 * kJoined * 16, "joins reuse the rings");
 };
 
-constexpr float kFewSlack = 8.f;  // a maximum is followed when it has risen by this much (log2)
-
 // Transposes an 8 x 8 matrix of 16-bit values, a row in four lanes.
 __device__ __forceinline__ uint32_t turned(uint32_t x) {
   uint32_t r;
@@ -160,6 +158,9 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
     return !kCodes ? 16 * d + g : kPad == 64 ? 8 * g + 2 * d : 128 * (d / 8) + 16 * g + 2 * (d % 8);
   };
   constexpr uint32_t kOther = kCodes ? 1 : 8;
+  const auto shift_of = [](uint32_t exponent) __attribute__((always_inline)) {
+    return (float)((int)exponent - 127 - attn_lift<H, kCodes>());
+  };
   // a lane copies the same chunk of every kStep-th token
   const uint32_t chunk = lane % kChunks, token0 = lane / kChunks;
   const bool has = chunk < (kCodes ? p.c.width / 16 : p.c.width / 8);
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
           }
       }
       // Weights are exp2(score - ref). ref is a score that was a row's largest,
-      // followed when one is 2^8 above it; for codes it also takes in the size
+      // followed when one is 2^kSlack above it; for codes it also takes in the size
       // of the values' scales, so that weights times scales stay in the middle
       // of f16's range.
       float most[kN][2];
@@ -429,7 +430,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           most[n][h] = fmaxf(s[n][h], s[n][2 + h]);
-          rises |= most[n][h] > top[n][h] + kFewSlack || (top[n][h] == -INFINITY && most[n][h] > -INFINITY);
+          rises |= most[n][h] > top[n][h] + kSlack || (top[n][h] == -INFINITY && most[n][h] > -INFINITY);
         }
       float v0 = 1.f, v1 = 1.f;
       uint32_t scale_ex = 0;
@@ -453,9 +454,9 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
             m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
             m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
             m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
-            const float was = top[n][h] + (float)((int)ex_before - 127);
-            if (m > top[n][h] + kFewSlack || top[n][h] == -INFINITY) top[n][h] = m;
-            const float ref = top[n][h] == -INFINITY ? 0.f : top[n][h] + (float)((int)exponent - 127);
+            const float was = top[n][h] + shift_of(ex_before);
+            if (m > top[n][h] + kSlack || top[n][h] == -INFINITY) top[n][h] = m;
+            const float ref = top[n][h] == -INFINITY ? 0.f : top[n][h] + shift_of(exponent);
             const float down = exp2_of(was - ref);
             sum[n][h] *= down;
 #pragma unroll
@@ -465,7 +466,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
             }
           }
       }
-      const float shift = (float)((int)exponent - 127);
+      const float shift = shift_of(exponent);
 #pragma unroll
       for (uint32_t n = 0; n < kN; ++n)
 #pragma unroll
@@ -606,7 +607,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
         l += __shfl_xor_sync(kFull, l, 8);
         l += __shfl_xor_sync(kFull, l, 16);
         sum[n][h] = l;
-        top[n][h] += (float)((int)exponent - 127);  // the reference of what was summed
+        top[n][h] += shift_of(exponent);  // the reference of what was summed
         if (g == 0) s_ref[team][row0 + n * 8 + 2 * c + h] = top[n][h];
       }
     copies_wait<0>();

@@ -367,8 +367,6 @@ static __device__ __noinline__ void join_item(const AttnParams& p, const JoinedI
   }
 }
 
-constexpr float kSlack = 8.f;          // a maximum is followed when it has risen by this much (log2)
-
 template <typename T, uint32_t kPad, bool kCodes, uint32_t kTiles>
 __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<kPad, kCodes, kTiles>::kCtas))
     attention_many_kernel(const AttnParams p) {
@@ -895,7 +893,7 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
         for (int j = 0; j < 32; j += 2) most = largest3(most, low(x[j]), high(x[j])), other = largest3(other, low(x[j + 1]), high(x[j + 1]));
         most = fmaxf(most, other);
         most *= factor;
-        const float ref_before = top + (kCodes ? (float)((int)exponent - 127) : 0.f);
+        const float ref_before = top + (float)((kCodes ? (int)exponent - 127 : 0) - attn_lift<W, kCodes>());
         bool move = most > top + kSlack || (top == -INFINITY && most > -INFINITY);
         if (move) top = most;
         if (kCodes) {
@@ -905,7 +903,7 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
             move = true;
           }
         }
-        const float ref = top == -INFINITY ? 0.f : top + (kCodes ? (float)((int)exponent - 127) : 0.f);
+        const float ref = top == -INFINITY ? 0.f : top + (float)((kCodes ? (int)exponent - 127 : 0) - attn_lift<W, kCodes>());
         uint64_t odd = 0;
         if (masked) {
           const uint32_t at_odd = tile % F::kMeta;
@@ -974,7 +972,7 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
       go = group_all(1, F::kWeights, ok);
       if (go) {
         tensor_fence_after();
-        const float ref = top == -INFINITY ? -INFINITY : top + (kCodes ? (float)((int)exponent - 127) : 0.f);
+        const float ref = top == -INFINITY ? -INFINITY : top + (float)((kCodes ? (int)exponent - 127 : 0) - attn_lift<W, kCodes>());
         const bool whole = t0 == 0 && t1 == e.tiles;
         const auto query_head = [&](uint32_t row_, uint32_t& nd) {
           const uint32_t a = rb * F::kRows + row_;
