@@ -63,7 +63,7 @@ extern "C" int db_cache_attention(const db_page_tables* t, const db_cache_batch*
   if (check_rows(q, b->rows, q_heads, c->width, type, false) ||
       check_rows(out, b->rows, q_heads, c->width, type, true))
     return -EINVAL;
-  if (!std::isfinite(scale)) return -EINVAL;
+  if (!std::isfinite(scale * 1.4426950408889634f)) return -EINVAL;
   if (!aligned(mask, 4) || !aligned(lse, 4) || (mask && (!mask_words || max_tokens > 32ull * mask_words)))
     return -EINVAL;
   if (!ws || !aligned(ws, 256)) return -EINVAL;
