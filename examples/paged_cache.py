@@ -1,7 +1,8 @@
 """A paged cache in the device heap, from prompts to descriptors.
 
 Sequences of a small model are admitted, forked into beams, extended token by
-token and cut back, all on the device; the pool is compacted; then one
+token and cut back, all on the device; the winners take steps with trees of
+drafted tokens, of which the verified ones stay; the pool is compacted; then one
 sequence is written to an NVMe drive (PRP lists for its pages) and another is
 put to a peer (work-queue entries for its pages). Run on a GPU:
 
@@ -58,17 +59,51 @@ class Cache:
         db.page_compact(self.tables, self.tables, self.moves, self.n_moves, self.ws)
         db.page_copy(self.moves, self.n_moves, self.pool, self.pool)
 
-    def write(self, seq, first, values):
-        """The model's part: keys and values [planes, tokens, heads, width] of tokens from `first` on."""
-        at = torch.arange(first, first + values.shape[1], device=self.device)
-        page = self.tables.table[seq, at // TOKENS].long()
-        self.heap[page, :, at % TOKENS] = values.transpose(0, 1)
+    def _batch(self, seqs, counts):
+        start = [0]
+        for n in counts:
+            start.append(start[-1] + n)
+        return self._req(seqs), self._req(start)
+
+    def write(self, seqs, counts, values):
+        """Keys and values [planes, rows, heads, width] of the sequences' last tokens, `counts` of each."""
+        seq, start = self._batch(seqs, counts)
+        for x in range(LAYERS):
+            db.cache_write(self.tables, seq, start, values[2 * x], values[2 * x + 1], self.pool[2 * x], self.pool[2 * x + 1])
 
     def read(self, seq):
-        """What the model's attention reads: [planes, length, heads, width]."""
+        """What a sequence holds: [planes, length, heads, width]."""
         n = int(self.tables.length[seq])
-        at = torch.arange(n, device=self.device)
-        return self.heap[self.tables.table[seq, at // TOKENS].long(), :, at % TOKENS].transpose(0, 1)
+        values = torch.empty((PLANES, n, HEADS, WIDTH), dtype=self.heap.dtype, device=self.device)
+        seq, start = self._batch([seq], [n])
+        for x in range(LAYERS):
+            db.cache_read(self.tables, seq, start, values[2 * x], values[2 * x + 1], self.pool[2 * x], self.pool[2 * x + 1])
+        return values
+
+    def speculate(self, seqs, parent, model):
+        """One step of each sequence with a tree of drafted tokens (`parent`, the root first): room, keys and values,
+        attention, verification, and the others' slots given back. The model says what the tokens are and how likely;
+        returns the nodes that stay [sequences, nodes] (-1 behind the last) and the tokens that follow them."""
+        m, n = len(parent), len(seqs)
+        self.extend([[s, m] for s in seqs])
+        seq, start = self._batch(seqs, [m] * n)
+        sees = [1 << j for j in range(m)]
+        for j in range(1, m):
+            sees[j] |= sees[parent[j]]
+        mask = self._req([[w] for w in sees * n])
+        values, out = model["values"], torch.empty_like(model["queries"][0])
+        ws = db.workspace(db.cache_attention_workspace_size(n, out.shape[1], HEADS, WIDTH, m), self.device)
+        for x in range(LAYERS):
+            k, v = self.pool[2 * x], self.pool[2 * x + 1]
+            db.cache_write(self.tables, seq, start, values[2 * x], values[2 * x + 1], k, v)
+            db.cache_attention(self.tables, seq, start, model["queries"][x], k, v, out, ws, m, mask=mask)
+        path, accepted, following = (torch.empty(k, dtype=torch.int32, device=self.device) for k in (n * m, n, n))
+        db.draft_verify(start, self._req(parent * n), model["tokens"], model["target"], model["random"], path, accepted, following,
+                        q=model["drafter"])
+        cut = torch.empty((n, 2), dtype=torch.int32, device=self.device)
+        db.cache_keep(self.tables, seq, start, path, accepted, self.pool, token_dim=2, cut=cut)
+        db.page_free(self.tables, cut, self.ws)
+        return path.view(n, m), following
 
     def ranges(self, seq):
         """The heap ranges {offset, bytes} of a sequence's pages, neighbours merged."""
@@ -89,11 +124,11 @@ def main():
 
     def grow(rows):
         c.extend(rows)
-        for seq, n in rows:
-            v = values(n)
-            have = kept.get(seq)
-            c.write(seq, 0 if have is None else have.shape[1], v)
-            kept[seq] = v if have is None else torch.cat([have, v], 1)
+        seqs, counts = zip(*rows)
+        new = values(sum(counts))
+        c.write(seqs, counts, new)
+        for seq, v in zip(seqs, new.split(counts, 1)):
+            kept[seq] = v if seq not in kept else torch.cat([kept[seq], v], 1)
 
     # eight prompts, each decoded by four beams for twenty steps
     grow([[s, 37 + 29 * s] for s in range(8)])
@@ -114,6 +149,20 @@ def main():
     for s in over:
         del kept[s]
     kept[8] = kept[8][:, :-2]
+    # the winners draft trees of six tokens; a path of each stays
+    parent, winners, vocab, stayed = [0, 0, 0, 1, 1, 3], sorted(kept), 100, 0
+    rows = len(winners) * len(parent)
+    for _ in range(3):
+        likely = torch.randn((2, rows, vocab), device="cuda").mul(2).softmax(-1)
+        model = dict(values=values(rows), queries=torch.randn((LAYERS, rows, 2 * HEADS, WIDTH), device="cuda").bfloat16(),
+                     tokens=torch.randint(vocab, (rows,), dtype=torch.int32, device="cuda"), target=likely[0], drafter=likely[1],
+                     random=torch.rand(rows, device="cuda"))
+        path, _ = c.speculate(winners, parent, model)
+        for s, way, v in zip(winners, path.tolist(), model["values"].split(len(parent), 1)):
+            way = [j for j in way if j >= 0]
+            stayed += len(way)
+            kept[s] = torch.cat([kept[s], v[:, way]], 1)
+    print(f"{len(winners)} sequences kept {stayed} tokens in 3 steps")
     before = {s: c.ranges(s).shape[0] for s in kept}
     used = int((c.tables.refs > 0).sum())
     c.compact()

@@ -131,13 +131,21 @@ int db_cache_read(const db_page_tables* t, const db_cache_batch* b, const int32_
  * lse -infinity. What a row does not see does not reach it, whatever the
  * slots hold (infinities and NaN included).
  * `type` is that of q and out, DB_BF16 or DB_F16; 16-bit caches are of the
- * same type. Statistics and sums are held in 32 bits; weights are rounded to
- * `type` for the product with 16-bit values and to bf16 for that with codes.
+ * same type. Statistics and sums are held in 32 bits. Weights are rounded to
+ * `type` for the product with 16-bit values; with codes weights times scales
+ * are rounded to f16, and bf16 queries are taken as f16 times a power of two
+ * that is each row's own (off by 2^-38 of the row's largest value at most).
+ * Sums of weights times values have to stay within 32 bits' range: values up
+ * to 2^100 do, and those of codes above 2^-90 keep their precision.
  *   max_tokens  no request has more rows (one that has is DB_PAGE_INVALID);
  *               with a mask at most 32 * mask_words
  *   ws          of db_cache_attention_workspace_size bytes for these heads,
  *               width and max_tokens (or larger ones of the same heads and
- *               width); the size is that of the current device
+ *               width); the size is that of the current device. Zeros at
+ *               first, and left ready for the next call; calls that may run at
+ *               the same time (on two streams, in two graphs) need one each.
+ *               After DB_ERR_TIMEOUT in ctr (a kernel gave up waiting, and out
+ *               is not valid) it has to be zeros again.
  * q may be out. n <= 65536, q_heads a multiple of heads and at most 64 of
  * them to a key head. */
 int db_cache_attention_workspace_size(uint32_t n, uint32_t q_heads, uint32_t heads, uint32_t width,
