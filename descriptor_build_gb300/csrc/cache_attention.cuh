@@ -21,16 +21,17 @@ namespace db {
 constexpr uint32_t kTile = 64;             // tokens of a unit
 constexpr uint32_t kAttnThreads = 128;
 constexpr uint32_t kMaxGroup = 64;
-// A row's maximum, and for codes the exponent of the values' largest scale, are
-// followed when they have risen by more than this (log2).
-constexpr float kSlack = 6.f;
+// A row's maximum is followed when it has risen by more than a slack (log2), for
+// codes also the exponent of the values' largest scale. Weights times scales
+// are then below 2^(lift + slack + 3), or 2^(lift + slack) without scales. f16
+// ones (below 2^16) start that much above 1, so that small ones are normal numbers
+// still: the kernel for few rows follows sooner and starts higher, for which the
+// error of long answers in f16 is 1.4 times their rounding's (1.5 with the
+// other's).
 constexpr uint32_t kScaleSlack = 2;
-// Weights times scales are below 2^(kLift + 6 + 3): f16 ones start high, so that
-// those of 2^-20 are normal numbers still (without it the answers' error for
-// long caches was 1.5 times that of their rounding, 1.4 with it).
 template <typename W, bool kCodes>
-__host__ __device__ constexpr int attn_lift() {
-  return !std::is_same<W, __half>::value ? 0 : kCodes ? 6 : 8;
+__host__ __device__ constexpr int attn_lift(int slack) {
+  return !std::is_same<W, __half>::value ? 0 : (kCodes ? 12 : 14) - slack;
 }
 constexpr uint32_t kManyBlocks = 16;      // blocks of 8 query rows of the tcgen05 kernel's items, or twice as many
 

@@ -41,6 +41,8 @@ struct Few {
   static_assert(kBytes >= kGroups * kRows * kPad * 4 && kBytes >= 4 * kJoined * 16, "joins reuse the rings");
 };
 
+constexpr int kFewSlack = 6;
+
 // Transposes an 8 x 8 matrix of 16-bit values, a row in four lanes.
 __device__ __forceinline__ uint32_t turned(uint32_t x) {
   uint32_t r;
@@ -159,7 +161,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
   };
   constexpr uint32_t kOther = kCodes ? 1 : 8;
   const auto shift_of = [](uint32_t exponent) __attribute__((always_inline)) {
-    return (float)((int)exponent - 127 - attn_lift<H, kCodes>());
+    return (float)((int)exponent - 127 - attn_lift<H, kCodes>(kFewSlack));
   };
   // a lane copies the same chunk of every kStep-th token
   const uint32_t chunk = lane % kChunks, token0 = lane / kChunks;
@@ -420,7 +422,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
           }
       }
       // Weights are exp2(score - ref). ref is a score that was a row's largest,
-      // followed when one is 2^kSlack above it; for codes it also takes in the size
+      // followed when one is 2^kFewSlack above it; for codes it also takes in the size
       // of the values' scales, so that weights times scales stay in the middle
       // of f16's range.
       float most[kN][2];
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           most[n][h] = fmaxf(s[n][h], s[n][2 + h]);
-          rises |= most[n][h] > top[n][h] + kSlack || (top[n][h] == -INFINITY && most[n][h] > -INFINITY);
+          rises |= most[n][h] > top[n][h] + (float)kFewSlack || (top[n][h] == -INFINITY && most[n][h] > -INFINITY);
         }
       float v0 = 1.f, v1 = 1.f;
       uint32_t scale_ex = 0;
@@ -455,7 +457,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
             m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
             m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
             const float was = top[n][h] + shift_of(ex_before);
-            if (m > top[n][h] + kSlack || top[n][h] == -INFINITY) top[n][h] = m;
+            if (m > top[n][h] + (float)kFewSlack || top[n][h] == -INFINITY) top[n][h] = m;
             const float ref = top[n][h] == -INFINITY ? 0.f : top[n][h] + shift_of(exponent);
             const float down = exp2_of(was - ref);
             sum[n][h] *= down;

@@ -11,8 +11,8 @@
 //                       (over S in TMEM) and their sum
 // so that the product of one tile runs while weights of the one before are
 // made, and two CTAs share an SM. A row's maximum is followed only when it has
-// risen by 2^8 (weights then are at most 2^8, which every type here holds as
-// exactly as 1), so O is hardly ever rescaled.
+// risen by 2^kSlack (weights of 2^kSlack are held as exactly as 1), so O is
+// hardly ever rescaled.
 //
 // A row of a page is 128 or 256 bytes, the next token's some kilobytes on. Such
 // rows of 16 tokens a page come at 6.6 TB/s (1 CTA an SM, 4 tiles ahead) by
@@ -367,6 +367,9 @@ static __device__ __noinline__ void join_item(const AttnParams& p, const JoinedI
   }
 }
 
+// Sums are rescaled seldom (16 wide trees: 297 us with a slack of 6, 279 with 8, 274 with 10).
+constexpr int kSlack = 10;
+
 template <typename T, uint32_t kPad, bool kCodes, uint32_t kTiles>
 __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<kPad, kCodes, kTiles>::kCtas))
     attention_many_kernel(const AttnParams p) {
@@ -647,7 +650,7 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
           unsigned char* const to = smem + slot_of(u) * F::kUnit + chunk / 4 * kPanel;
           const auto widen_all = [&](auto four) __attribute__((always_inline)) {
             constexpr bool kFour = decltype(four)::value;
-            constexpr uint32_t kBatch = kEach < 8 ? kEach : 8;
+            constexpr uint32_t kBatch = kEach < 4 ? kEach : 4;
 #pragma unroll 1
             for (uint32_t k0 = 0; k0 < kEach; k0 += kBatch) {
               uint4 c[kBatch];
@@ -872,29 +875,50 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
           }
           hide_scores(here, sees[0], sees[1], kCodes ? m.k_scale : nullptr);
         }
-        uint32_t w[64];
-        uint64_t x[32];
-        tmem_load32(here, w);
-        tmem_load32(here + 32, w + 32);
-        tmem_loaded();
+        // 16-bit values: both passes over the scores read them from TMEM, by halves,
+        // in a loop whose code is short enough for the instruction caches (48 trees
+        // 185 us with all of it unrolled, 156 so). Codes' scores are kept between
+        // the passes, times their scales (16 wide trees 297 us, 313 by halves).
+        const ulonglong2* const scales = (const ulonglong2*)(masked ? s_ones : m.k_scale);
+        const auto half_of = [&](uint32_t h, uint64_t (&x)[16]) __attribute__((always_inline)) {
+          uint32_t w[32];
+          __syncwarp();
+          tmem_load32(here + 32 * h, w);
+          tmem_loaded();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] = pair(w[2 * j], w[2 * j + 1]);
-        if (kCodes) {
-          const ulonglong2* const scales = (const ulonglong2*)(masked ? s_ones : m.k_scale);
+          for (int j = 0; j < 16; ++j) x[j] = pair(w[2 * j], w[2 * j + 1]);
+        };
+        uint64_t kept[kCodes ? 32 : 1];  // codes' scores, times their scales
+        float most = -INFINITY, other = -INFINITY;
+        const auto largest_of = [&](const uint64_t* x) __attribute__((always_inline)) {
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) most = largest3(most, low(x[j]), high(x[j])), other = largest3(other, low(x[j + 1]), high(x[j + 1]));
+        };
+        if constexpr (kCodes) {
+          uint32_t w[64];
+          tmem_load32(here, w);
+          tmem_load32(here + 32, w + 32);
+          tmem_loaded();
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const ulonglong2 y = scales[j];
-            x[2 * j] = multiply2(x[2 * j], y.x);
-            x[2 * j + 1] = multiply2(x[2 * j + 1], y.y);
+            kept[2 * j] = multiply2(pair(w[4 * j], w[4 * j + 1]), y.x);
+            kept[2 * j + 1] = multiply2(pair(w[4 * j + 2], w[4 * j + 3]), y.y);
+          }
+          largest_of(kept);
+          largest_of(kept + 16);
+        } else {
+#pragma unroll 1
+          for (uint32_t h = 0; h < 2; ++h) {
+            uint64_t x[16];
+            half_of(h, x);
+            largest_of(x);
           }
         }
-        float most = -INFINITY, other = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < 32; j += 2) most = largest3(most, low(x[j]), high(x[j])), other = largest3(other, low(x[j + 1]), high(x[j + 1]));
         most = fmaxf(most, other);
         most *= factor;
-        const float ref_before = top + (float)((kCodes ? (int)exponent - 127 : 0) - attn_lift<W, kCodes>());
-        bool move = most > top + kSlack || (top == -INFINITY && most > -INFINITY);
+        const float ref_before = top + (float)((kCodes ? (int)exponent - 127 : 0) - attn_lift<W, kCodes>(kSlack));
+        bool move = most > top + (float)kSlack || (top == -INFINITY && most > -INFINITY);
         if (move) top = most;
         if (kCodes) {
           const uint32_t ex = min(max(max(m.exponent[0], m.exponent[1]), 31u), 227u);
@@ -903,7 +927,7 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
             move = true;
           }
         }
-        const float ref = top == -INFINITY ? 0.f : top + (float)((kCodes ? (int)exponent - 127 : 0) - attn_lift<W, kCodes>());
+        const float ref = top == -INFINITY ? 0.f : top + (float)((kCodes ? (int)exponent - 127 : 0) - attn_lift<W, kCodes>(kSlack));
         uint64_t odd = 0;
         if (masked) {
           const uint32_t at_odd = tile % F::kMeta;
@@ -942,28 +966,42 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
         uint64_t sums = pair(__float_as_uint(sum), 0), more = pair(0, 0);
         const uint64_t by = pair(__float_as_uint(factor), __float_as_uint(factor));
         const uint64_t less = pair(__float_as_uint(-ref), __float_as_uint(-ref));
+        const auto weigh = [&](const uint64_t* x, uint32_t h) __attribute__((always_inline)) {
+          uint32_t w[16];
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          uint64_t y[2];
+          for (int j = 0; j < 16; j += 2) {
+            uint64_t y[2];
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const uint64_t z = multiply_add2(x[j + g], by, less);
-            y[g] = pair(__float_as_uint(exp2_of(low(z))), __float_as_uint(exp2_of(high(z))));
+            for (int g = 0; g < 2; ++g) {
+              const uint64_t z = multiply_add2(x[j + g], by, less);
+              y[g] = pair(__float_as_uint(exp2_of(low(z))), __float_as_uint(exp2_of(high(z))));
+            }
+            sums = add2(sums, y[0]);
+            more = add2(more, y[1]);
+            if (kCodes) {
+              const ulonglong2 z = ((const ulonglong2*)m.v_scale)[8 * h + j / 2];
+              y[0] = multiply2(y[0], z.x);
+              y[1] = multiply2(y[1], z.y);
+            }
+            w[j] = pack2<W>(low(y[0]), high(y[0]));
+            w[j + 1] = pack2<W>(low(y[1]), high(y[1]));
           }
-          sums = add2(sums, y[0]);
-          more = add2(more, y[1]);
-          if (kCodes) {
-            const ulonglong2 z = ((const ulonglong2*)m.v_scale)[j / 2];
-            y[0] = multiply2(y[0], z.x);
-            y[1] = multiply2(y[1], z.y);
+          __syncwarp();
+          tmem_store16(here + 16 * h, w);  // over the scores that have been read
+        };
+        if constexpr (kCodes) {
+          weigh(kept, 0);
+          weigh(kept + 16, 1);
+        } else {
+#pragma unroll 1
+          for (uint32_t h = 0; h < 2; ++h) {
+            uint64_t x[16];
+            half_of(h, x);
+            weigh(x, h);
           }
-          w[j] = pack2<W>(low(y[0]), high(y[0]));
-          w[j + 1] = pack2<W>(low(y[1]), high(y[1]));
         }
         sums = add2(sums, more);
         sum = low(sums) + high(sums);
-        __syncwarp();
-        tmem_store32(here, w);  // over the scores
         tmem_stored();
         tensor_fence_before();
         barrier_arrive(smem_at(&s_weights[half][buffer]));
@@ -972,7 +1010,7 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
       go = group_all(1, F::kWeights, ok);
       if (go) {
         tensor_fence_after();
-        const float ref = top == -INFINITY ? -INFINITY : top + (float)((kCodes ? (int)exponent - 127 : 0) - attn_lift<W, kCodes>());
+        const float ref = top == -INFINITY ? -INFINITY : top + (float)((kCodes ? (int)exponent - 127 : 0) - attn_lift<W, kCodes>(kSlack));
         const bool whole = t0 == 0 && t1 == e.tiles;
         const auto query_head = [&](uint32_t row_, uint32_t& nd) {
           const uint32_t a = rb * F::kRows + row_;
