@@ -566,12 +566,14 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
           }
           return not_finite2<W>(v.x) || not_finite2<W>(v.y) || not_finite2<W>(v.z) || not_finite2<W>(v.w);
         };
+        // (tokens before the request's own are seen by all rows, missing ones are zeros)
+        const uint32_t k1 = t * kTile < base ? (base - t * kTile) / kStep : 0;
         bool any = false;
-#pragma unroll 8
-        for (uint32_t k = 0; k < kEach; ++k) any |= has && bad_at(k);
+#pragma unroll 4
+        for (uint32_t k = k1; k < kEach; ++k) any |= has && bad_at(k);
         if (__any_sync(kFull, any)) {
 #pragma unroll 1
-          for (uint32_t k = 0; k < kEach; ++k) {
+          for (uint32_t k = k1; k < kEach; ++k) {
             const uint32_t token = token0 + k * kStep;
             const uint32_t votes = __ballot_sync(kFull, has && bad_at(k)) >> token0 * kRawChunks % 32;
             if (votes & (kRawChunks == 32 ? 0xFFFFFFFFu : (1u << kRawChunks % 32) - 1)) {
