@@ -87,6 +87,7 @@ extern "C" int db_cache_attention(const db_page_tables* t, const db_cache_batch*
   p.head_step = c->heads_first ? t->page_tokens * row : row;
   p.scale_token_step = c->heads_first ? 1 : c->heads;
   p.scale_head_step = c->heads_first ? t->page_tokens : 1;
+  p.narrow = std::max(c->k_stride, c->v_stride) <= ((1ull << 36) - 16) / t->n_pages;
   p.arrived = (unsigned int*)ws;
   p.partial = (float*)((char*)ws + kHeader);
   const uint32_t blocks = blocks_for((uint64_t)max_tokens * p.group, padded_width(c->width), item_bytes(c->type) == 1);

@@ -49,6 +49,7 @@ struct AttnParams {
   uint32_t scale_token_step, scale_head_step;
   float* partial;          // [2 * grid][rows of an item][width + 2 rounded]
   unsigned int* arrived;   // [grid], zero between calls
+  uint32_t narrow;         // offsets in the pools, by 16 bytes, fit 32 bits
 };
 
 // Host: one instance of the kernels for a padded width.

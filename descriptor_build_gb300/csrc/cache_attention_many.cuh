@@ -527,6 +527,26 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
       // Starts the copies of a unit; a token's chunk goes to place(token, k).
       const auto start = [&](bool key, bool whole, const Places& w, auto place) __attribute__((always_inline)) {
         const char* const from = (const char*)(key ? p.c.k : p.c.v) + head * p.head_step + chunk * 16;
+        if (whole && p.narrow) {  // half the shuffles
+          const uint32_t page_step = (uint32_t)((key ? p.c.k_stride : p.c.v_stride) / 16), step = (uint32_t)p.token_step / 16;
+#pragma unroll
+          for (uint32_t h = 0; h < 2; ++h) {
+            const uint32_t off = (uint32_t)w.at[h].x * page_step + (uint32_t)w.at[h].y * step;
+            constexpr uint32_t kBatch = kEach / 2 < 8 ? kEach / 2 : 8;
+#pragma unroll 1
+            for (uint32_t k0 = h * kEach / 2; k0 < (h + 1) * kEach / 2; k0 += kBatch) {
+              uint32_t at[kBatch];
+#pragma unroll
+              for (uint32_t k = 0; k < kBatch; ++k) at[k] = __shfl_sync(kFull, off, (token0 + (k0 + k) * kStep) & 31);
+              if (!has) continue;
+#pragma unroll
+              for (uint32_t k = 0; k < kBatch; ++k)
+                copy16(place(token0 + (k0 + k) * kStep, k0 + k), from + (uint64_t)at[k] * 16, true);
+            }
+          }
+          copies_commit();
+          return;
+        }
         const uint64_t off[2] = {offset(w.at[0], key), offset(w.at[1], key)};
 #pragma unroll
         for (uint32_t h = 0; h < 2; ++h) {
@@ -538,16 +558,11 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
 #pragma unroll
             for (uint32_t k = 0; k < kBatch; ++k) at[k] = __shfl_sync(kFull, off[h], (token0 + (k0 + k) * kStep) & 31);
             if (!has) continue;
-            if (whole) {
 #pragma unroll
-              for (uint32_t k = 0; k < kBatch; ++k) copy16(place(token0 + (k0 + k) * kStep, k0 + k), from + at[k], true);
-            } else {
-#pragma unroll
-              for (uint32_t k = 0; k < kBatch; ++k) {
-                const uint32_t token = token0 + (k0 + k) * kStep;
-                const bool real = (there >> (token & 31)) & 1;
-                copy16(place(token, k0 + k), from + (real ? at[k] : 0), real);
-              }
+            for (uint32_t k = 0; k < kBatch; ++k) {
+              const uint32_t token = token0 + (k0 + k) * kStep;
+              const bool real = (there >> (token & 31)) & 1;
+              copy16(place(token, k0 + k), from + (real ? at[k] : 0), real);
             }
           }
         }
