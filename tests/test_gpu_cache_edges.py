@@ -184,6 +184,28 @@ def test_pools_larger_than_4_gib(kind):
     assert (numbers(at(67)) * sc(68) - want[68]).max() <= 2.0**-20 and (numbers(at(68)) * sc(69) - want[69]).max() <= 2.0**-20
 
 
+@pytest.mark.parametrize("rows", ["8", "96"])
+def test_pools_larger_than_64_gib(rows):
+    """Pages 3 GiB apart, so that offsets by 16 bytes pass 32 bits."""
+    need_gpu()
+    db = lib()
+    nodes, group = ROWS[rows]
+    c = Case("e4m3", "bf16", 1, 16, 1, group, 64, [(200, nodes), (150, nodes)], "tree")
+    gap = 3 << 30
+    assert c.t.n_pages * gap > 1 << 36
+    if torch.cuda.mem_get_info()[0] < c.t.n_pages * gap + (8 << 30):
+        pytest.skip("not enough memory")
+    b, want = c.oracle()
+    dev = c.device()
+    store = torch.empty(c.t.n_pages * gap, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    for k, name in enumerate(("k", "v")):  # values one MiB behind the keys
+        dev[name] = torch.as_strided(store, dev[name].shape, (gap,) + dev[name].stride()[1:], k << 20).copy_(dev[name])
+    out, lse = torch.full_like(c.q, 7.0).cuda(), torch.full(c.q.shape[:2], 7.0, device="cuda")
+    c.call(db, c.t.device(), c.workspace(db), dev, out, lse)
+    finish()
+    c.check(out, lse, b, want)
+
+
 def test_many_requests_of_all_kinds():
     rng = np.random.default_rng(12)
     for group, most in ((4, 2), (4, 8), (8, 30)):
