@@ -894,10 +894,10 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
           }
           hide_scores(here, sees[0], sees[1], kCodes ? m.k_scale : nullptr);
         }
-        // 16-bit values: both passes over the scores read them from TMEM, by halves,
-        // in a loop whose code is short enough for the instruction caches (48 trees
-        // 185 us with all of it unrolled, 156 so). Codes' scores are kept between
-        // the passes, times their scales (16 wide trees 297 us, 313 by halves).
+        // Both passes over the scores read them from TMEM, by halves, in loops whose
+        // code is short enough for the instruction caches (48 trees 185 us with all
+        // of it unrolled, 156 so). Codes' scores go back times their keys' scales in
+        // between (16 wide trees 249 us with them held in registers, 236 so).
         const ulonglong2* const scales = (const ulonglong2*)(masked ? s_ones : m.k_scale);
         const auto half_of = [&](uint32_t h, uint64_t (&x)[16]) __attribute__((always_inline)) {
           uint32_t w[32];
@@ -907,33 +907,28 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
 #pragma unroll
           for (int j = 0; j < 16; ++j) x[j] = pair(w[2 * j], w[2 * j + 1]);
         };
-        uint64_t kept[kCodes ? 32 : 1];  // codes' scores, times their scales
         float most = -INFINITY, other = -INFINITY;
-        const auto largest_of = [&](const uint64_t* x) __attribute__((always_inline)) {
+#pragma unroll 1
+        for (uint32_t h = 0; h < 2; ++h) {
+          uint64_t x[16];
+          half_of(h, x);
+          if constexpr (kCodes) {
+            uint32_t w[32];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const ulonglong2 y = scales[8 * h + j];
+              x[2 * j] = multiply2(x[2 * j], y.x);
+              x[2 * j + 1] = multiply2(x[2 * j + 1], y.y);
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) w[2 * j] = __float_as_uint(low(x[j])), w[2 * j + 1] = __float_as_uint(high(x[j]));
+            __syncwarp();
+            tmem_store32(here + 32 * h, w);
+          }
 #pragma unroll
           for (int j = 0; j < 16; j += 2) most = largest3(most, low(x[j]), high(x[j])), other = largest3(other, low(x[j + 1]), high(x[j + 1]));
-        };
-        if constexpr (kCodes) {
-          uint32_t w[64];
-          tmem_load32(here, w);
-          tmem_load32(here + 32, w + 32);
-          tmem_loaded();
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const ulonglong2 y = scales[j];
-            kept[2 * j] = multiply2(pair(w[4 * j], w[4 * j + 1]), y.x);
-            kept[2 * j + 1] = multiply2(pair(w[4 * j + 2], w[4 * j + 3]), y.y);
-          }
-          largest_of(kept);
-          largest_of(kept + 16);
-        } else {
-#pragma unroll 1
-          for (uint32_t h = 0; h < 2; ++h) {
-            uint64_t x[16];
-            half_of(h, x);
-            largest_of(x);
-          }
         }
+        if (kCodes) tmem_stored();
         most = fmaxf(most, other);
         most *= factor;
         const float ref_before = top + (float)((kCodes ? (int)exponent - 127 : 0) - attn_lift<W, kCodes>(kSlack));
@@ -985,8 +980,11 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
         uint64_t sums = pair(__float_as_uint(sum), 0), more = pair(0, 0);
         const uint64_t by = pair(__float_as_uint(factor), __float_as_uint(factor));
         const uint64_t less = pair(__float_as_uint(-ref), __float_as_uint(-ref));
-        const auto weigh = [&](const uint64_t* x, uint32_t h) __attribute__((always_inline)) {
+#pragma unroll 1
+        for (uint32_t h = 0; h < 2; ++h) {
+          uint64_t x[16];
           uint32_t w[16];
+          half_of(h, x);
 #pragma unroll
           for (int j = 0; j < 16; j += 2) {
             uint64_t y[2];
@@ -1007,17 +1005,6 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
           }
           __syncwarp();
           tmem_store16(here + 16 * h, w);  // over the scores that have been read
-        };
-        if constexpr (kCodes) {
-          weigh(kept, 0);
-          weigh(kept + 16, 1);
-        } else {
-#pragma unroll 1
-          for (uint32_t h = 0; h < 2; ++h) {
-            uint64_t x[16];
-            half_of(h, x);
-            weigh(x, h);
-          }
         }
         sums = add2(sums, more);
         sum = low(sums) + high(sums);
