@@ -118,23 +118,49 @@ __device__ __forceinline__ void store8(char* p, const float* x) {
   }
 }
 
-// The largest magnitude of the lanes that share a row, as a float's bits: of
-// values without their sign, larger bits are larger values, infinities above
-// every number and NaN above those. 16-bit values are compared in pairs.
+// The largest magnitude of a lane's values as a float's bits (two 16-bit ones
+// side by side for 16-bit values): of values without their sign, larger bits are
+// larger values, infinities above every number and NaN above those.
 template <typename T>
-__device__ __forceinline__ uint32_t largest_bits(const Eight<T>& e, uint32_t lanes) {
+__device__ __forceinline__ uint32_t largest_bits(const Eight<T>& e) {
   uint32_t m = 0;
   if (sizeof(T) == 4) {
 #pragma unroll
     for (uint32_t j = 0; j < sizeof(T) / 2; ++j)
       m = max(max(max(m, e.w[j].x & 0x7FFFFFFFu), max(e.w[j].y & 0x7FFFFFFFu, e.w[j].z & 0x7FFFFFFFu)), e.w[j].w & 0x7FFFFFFFu);
-    for (uint32_t o = lanes / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
     return m;
   }
-  m = __vmaxu2(__vmaxu2(e.w[0].x & 0x7FFF7FFFu, e.w[0].y & 0x7FFF7FFFu), __vmaxu2(e.w[0].z & 0x7FFF7FFFu, e.w[0].w & 0x7FFF7FFFu));
-  for (uint32_t o = lanes / 2; o; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(kFull, m, o));
+  return __vmaxu2(__vmaxu2(e.w[0].x & 0x7FFF7FFFu, e.w[0].y & 0x7FFF7FFFu), __vmaxu2(e.w[0].z & 0x7FFF7FFFu, e.w[0].w & 0x7FFF7FFFu));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t larger_bits(uint32_t a, uint32_t b) {
+  return sizeof(T) == 4 ? max(a, b) : __vmaxu2(a, b);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t one_of(uint32_t m) {
+  if (sizeof(T) == 4) return m;
   m = max(m & 0xFFFFu, m >> 16);
   return __float_as_uint(unpack2<typename std::conditional<sizeof(T) == 4, __half, T>::type>(m).x);
+}
+
+// The largest of kMany rows' values over the `lanes` lanes that share them: a
+// lane ends with that of row (lane % lanes) / (lanes / kMany). Lanes hand half of
+// their rows on at each step, so that 8 rows of 16 lanes take 8 shuffles, not 32.
+template <typename T, int kMany>
+__device__ __forceinline__ uint32_t largest_of_rows(uint32_t (&m)[kMany], uint32_t lanes) {
+  uint32_t bit = lanes / 2;
+#pragma unroll
+  for (int n = kMany / 2; n; n /= 2) {
+    const bool upper = threadIdx.x & bit;
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+      const uint32_t sent = upper ? m[j] : m[j + n], kept = upper ? m[j + n] : m[j];
+      m[j] = larger_bits<T>(kept, __shfl_xor_sync(kFull, sent, bit));
+    }
+    bit /= 2;
+  }
+  for (; bit; bit /= 2) m[0] = larger_bits<T>(m[0], __shfl_xor_sync(kFull, m[0], bit));
+  return one_of<T>(m[0]);
 }
 
 __device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
@@ -245,10 +271,10 @@ __global__ void __launch_bounds__(kThreads, 3) cache_write_kernel(const MovePara
         const char* const vf = v_from + r * p.v.row_stride + h0 * p.v.head_stride;
 #pragma unroll
         for (int j = 0; j < kHalf; ++j) {
-          if (h0 + j * per >= heads) break;
-          const bool real = mine && h0 + j * per + first_head < heads;
 #pragma unroll
           for (uint32_t z = 0; z < sizeof(Src) / 2; ++z) e[j].w[z] = e[j + kHalf].w[z] = make_uint4(0, 0, 0, 0);
+          if (h0 + j * per >= heads) continue;
+          const bool real = mine && h0 + j * per + first_head < heads;
           if (real) {
             e[j] = load8<Src>(kf + j * k_next);
             e[j + kHalf] = load8<Src>(vf + j * v_next);
@@ -268,24 +294,20 @@ __global__ void __launch_bounds__(kThreads, 3) cache_write_kernel(const MovePara
       char* const vt = (char*)p.c.v + now.page * p.c.v_stride + off;
       float by[kUnroll];
       if (kCodes) {
-        // A row's largest magnitude is in all of its lanes: lane j of them
-        // divides for the j-th of the lane group's rows (few lanes: for each).
+        // A lane divides for one of the lane group's rows (few lanes: for each).
         const uint32_t of = lane & (lanes - 1);
         float my_scale = 0.f, my_by = 0.f;
         if (lanes >= kUnroll) {
-          uint32_t top = 0;
+          uint32_t top[kUnroll];
 #pragma unroll
-          for (int j = 0; j < kUnroll; ++j) {
-            if (h0 + (j >= kHalf ? j - kHalf : j) * per >= heads) continue;
-            const uint32_t t = largest_bits(e[j], lanes);
-            if (of == j) top = t;
-          }
-          scale_of<kType == DB_E4M3>(top, my_scale, my_by);
+          for (int j = 0; j < kUnroll; ++j) top[j] = largest_bits(e[j]);
+          scale_of<kType == DB_E4M3>(largest_of_rows<Src, kUnroll>(top, lanes), my_scale, my_by);
+          const uint32_t every = lanes / kUnroll, row = of / every;
 #pragma unroll
-          for (int j = 0; j < kUnroll; ++j) by[j] = __shfl_sync(kFull, my_by, (lane & ~(lanes - 1)) | j);
-          const bool val = of >= kHalf;
-          const uint32_t head = h0 + (val ? of - kHalf : of) * per + first_head;
-          if (of < kUnroll && head < heads && now.held) {
+          for (int j = 0; j < kUnroll; ++j) by[j] = __shfl_sync(kFull, my_by, (lane & ~(lanes - 1)) | j * every);
+          const bool val = row >= kHalf;
+          const uint32_t head = h0 + (val ? row - kHalf : row) * per + first_head;
+          if (row * every == of && head < heads && now.held) {
             char* const to = (char*)(val ? p.c.v_scale : p.c.k_scale) + now.page * (val ? p.c.v_scale_stride : p.c.k_scale_stride);
             ((float*)to)[now.slot * p.scale_token_step + head * p.scale_head_step] = my_scale;
           }
@@ -293,7 +315,8 @@ __global__ void __launch_bounds__(kThreads, 3) cache_write_kernel(const MovePara
 #pragma unroll
           for (int j = 0; j < kUnroll; ++j) {
             if (h0 + (j >= kHalf ? j - kHalf : j) * per >= heads) continue;
-            scale_of<kType == DB_E4M3>(largest_bits(e[j], lanes), my_scale, by[j]);
+            uint32_t top[1] = {largest_bits(e[j])};
+            scale_of<kType == DB_E4M3>(largest_of_rows<Src, 1>(top, lanes), my_scale, by[j]);
             const bool val = j >= kHalf;
             const uint32_t head = h0 + (val ? j - kHalf : j) * per + first_head;
             if (of == 0 && head < heads && now.held) {
