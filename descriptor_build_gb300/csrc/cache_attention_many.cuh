@@ -3,22 +3,31 @@
 // tcgen05 products.
 //
 // A CTA has three kinds of warps that hand tiles of 64 tokens on by mbarriers:
-//   loaders (2 or 3)    keys and values from their pages into a ring of tiles, by
+//   loaders (2 to 6)    keys and values from their pages into a ring of tiles, by
 //                       16-byte asynchronous copies; 8-bit codes come into a
 //                       ring of their own, from which they are widened
 //   one issuing thread  S = Q K^T into TMEM (two buffers), O += P V from TMEM
 //   weights (4 warps)   a thread for each query row: S -> maxima, weights P
 //                       (over S in TMEM) and their sum
 // so that the product of one tile runs while weights of the one before are
-// made, and two CTAs share an SM. A row's maximum is followed only when it has
+// made, and two CTAs share an SM. Items of more than 128 rows have a CTA of two
+// such tiles of rows, each with its issuing thread and weights' warps, which
+// share what is loaded and widened (wide trees of 488 rows 396 us with CTAs of
+// 128 rows, 374 with two tiles and one issuing thread, 312 with two). A row's maximum is followed only when it has
 // risen by 2^kSlack (weights of 2^kSlack are held as exactly as 1), so O is
 // hardly ever rescaled.
 //
 // A row of a page is 128 or 256 bytes, the next token's some kilobytes on. Such
 // rows of 16 tokens a page come at 6.6 TB/s (1 CTA an SM, 4 tiles ahead) by
 // 16-byte copies of 128 threads and at 3.6 by TMA boxes of 64 values x 16 tokens,
-// which a CTA starts every 150 cycles; in this kernel boxes took 225 us where the
-// copies take less than 160 (48 trees of 25, see the table of cases).
+// which a CTA starts every 150 cycles; in this kernel boxes took 225 us where
+// the copies are done in less than 143 (48 trees of 25 nodes over 3,000 tokens).
+//
+// 48 trees of 25 nodes over 3,000 tokens (100 rows, bf16): 143 us, 4.5 TB/s: the
+// loaders' and issuing thread's instructions, and at each item's ends latency (a
+// third of the time before they were cut). 16 trees of 61 over 8,192 (488 rows,
+// I8): 235 us, 0.46 PFLOP/s: the weights' warps, of which a scheduler has two,
+// and instructions not yet fetched.
 //
 // Tiles lie as the tensor cores' 128-byte swizzle wants them: panels of 64
 // values, a row of 128 bytes for each token, 16-byte chunks exchanged by the
@@ -230,7 +239,7 @@ __device__ __forceinline__ float largest3(float a, float b, float c) {
 
 // What few tiles need is kept out of the loops' code, which is as long as the
 // instruction caches bear: a kernel of 138 KB that had all of it inline took 324
-// us for 48 trees of 25, a smaller one the time in the table of cases.
+// us for 48 trees of 25, a smaller one 270 then.
 
 // Scores of a tile that a row does not see become -infinity, in TMEM. Codes:
 // the others are multiplied by their keys' scales.
@@ -669,7 +678,7 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
           unsigned char* const to = smem + slot_of(u) * F::kUnit + chunk / 4 * kPanel;
           const auto widen_all = [&](auto four) __attribute__((always_inline)) {
             constexpr bool kFour = decltype(four)::value;
-            constexpr uint32_t kBatch = kEach < 4 ? kEach : 4;
+            constexpr uint32_t kBatch = kEach < 4 ? kEach : 4;  // (wide trees: 2 268 us, 4 236, 8 284)
 #pragma unroll 1
             for (uint32_t k0 = 0; k0 < kEach; k0 += kBatch) {
               uint4 c[kBatch];
