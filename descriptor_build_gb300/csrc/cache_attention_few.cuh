@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
   constexpr uint32_t kSteps = kPad / 16;
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr uint32_t kCopies = (kEach + kShare - 1) / kShare;    // of a lane in a stage
-  constexpr uint32_t kStride = F::kTokens * F::kGroups;          // tokens from one stage to the next
+  constexpr uint32_t kStride = F::kTokens * F::kGroups;
   __shared__ float s_ref[F::kGroups][F::kRows], s_sum[F::kGroups][F::kRows];
   __shared__ uint32_t s_there[4][F::kStages];  // the tokens that are there, of each warp's stages
   __shared__ uint32_t s_last;
@@ -190,24 +190,31 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
       continue;
     }
     const uint64_t x = at - before;
-    const uint32_t item = (uint32_t)quotient(x, e.tiles), head = item / e.blocks, rb = item - head * e.blocks;
-    const uint32_t t0 = (uint32_t)(x - (uint64_t)item * e.tiles);
+    const uint32_t item0 = (uint32_t)quotient(x, e.tiles);
+    const uint32_t t0 = (uint32_t)(x - (uint64_t)item0 * e.tiles);
     const uint32_t t1 = (uint32_t)min((uint64_t)e.tiles, t0 + (share.hi - at));
+    // Where as many whole items as teams follow one another in a request, each
+    // team takes one: what an item waits for beside its loads is then waited for
+    // once for all of them (1,024 sequences of 200 tokens, 8 key heads by 4: 198
+    // us one by one, 170 so; with half of the teams idle it took longer).
+    const bool alone = t0 == 0 && e.blocks * p.c.heads - item0 >= F::kGroups && share.hi - at >= (uint64_t)F::kGroups * e.tiles;
+    const uint32_t item = item0 + (alone ? team : 0), head = item / e.blocks, rb = item - head * e.blocks;
     const uint32_t rows = min(F::kRows, r.rows * p.group - rb * F::kRows);
     const uint32_t base = r.length - r.rows;  // tokens before the request's own
 
-    const uint32_t stages = (t1 - t0) * kShare;
+    const uint32_t stride = alone ? F::kTokens : kStride;  // tokens from one stage to the next
+    const uint32_t stages = alone ? (r.length + F::kTokens - 1) / F::kTokens : (t1 - t0) * kShare;
 
     // Lanes 0 to 15 look up a token each, of the next stage to be fetched.
     const int32_t* const table = p.view.table + (uint64_t)r.seq * p.view.columns;
-    uint32_t position = t0 * kTile + team * F::kTokens + (lane & 15);
+    uint32_t position = t0 * kTile + (alone ? 0 : team * F::kTokens) + (lane & 15);
     uint32_t column = position / p.view.page_tokens, in_page = position - column * p.view.page_tokens;
-    const uint32_t columns_on = kStride / p.view.page_tokens, tokens_on = kStride - columns_on * p.view.page_tokens;
+    const uint32_t columns_on = stride / p.view.page_tokens, tokens_on = stride - columns_on * p.view.page_tokens;
     int2 w;  // page and slot, or -1 and -1
     const auto look = [&]() __attribute__((always_inline)) {
       w = make_int2(-1, -1);
       if (position < r.length) w = make_int2(__ldg(table + column), (int)in_page);
-      position += kStride;
+      position += stride;
       column += columns_on;
       in_page += tokens_on;
       if (in_page >= p.view.page_tokens) in_page -= p.view.page_tokens, ++column;
@@ -343,8 +350,8 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
     for (uint32_t n = 0; n < kN; ++n) top[n][0] = top[n][1] = -INFINITY, sum[n][0] = sum[n][1] = 0.f;
 
     uint32_t slot = 0;
-    uint32_t first = t0 * kTile + team * F::kTokens;  // position of the stage's first token
-    for (uint32_t t = 0; t < stages; ++t, first += kStride) {
+    uint32_t first = t0 * kTile + (alone ? 0 : team * F::kTokens);  // position of the stage's first token
+    for (uint32_t t = 0; t < stages; ++t, first += stride) {
       copies_wait<F::kStages - 2>();
       if (kShare > 1)
         asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * kShare) : "memory");
@@ -624,9 +631,11 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t row = row0 + n * 8 + 2 * c + h;
-        float m = s_ref[0][row];
+        float m = top[n][h];
+        if (!alone) {
 #pragma unroll
-        for (uint32_t k = 1; k < F::kGroups; ++k) m = fmaxf(m, s_ref[k][row]);
+          for (uint32_t k = 0; k < F::kGroups; ++k) m = fmaxf(m, s_ref[k][row]);
+        }
         const float a = exp2_of(top[n][h] - (m == -INFINITY ? 0.f : m));
         if (g == 0) s_sum[team][row] = sum[n][h] * a;
         float* const to = (float*)smem + (team * F::kRows + row) * kPad;
@@ -637,35 +646,41 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
         }
       }
     __syncthreads();
-    const bool whole = t0 == 0 && t1 == e.tiles;
+    const bool whole = alone || (t0 == 0 && t1 == e.tiles);
     float* const mine = p.partial + (uint64_t)(2 * blockIdx.x + (t0 == 0)) * partial_floats(F::kRows, kPad);
     constexpr uint32_t kQuads = kPad / 4;
 #pragma unroll 1
-    for (uint32_t of = tid; of < rows * kQuads; of += kAttnThreads) {
-      const uint32_t row = of / kQuads, quad = of % kQuads;
-      float m = -INFINITY, l = 0.f;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (uint32_t k0 = 0; k0 < (alone ? F::kGroups : 1); ++k0) {
+      const uint32_t of_head = (item0 + k0) / e.blocks, of_rb = item0 + k0 - of_head * e.blocks;
+      const uint32_t of_rows = min(F::kRows, r.rows * p.group - of_rb * F::kRows);
+#pragma unroll 1
+      for (uint32_t of = tid; of < of_rows * kQuads; of += kAttnThreads) {
+        const uint32_t row = of / kQuads, quad = of % kQuads;
+        float m = -INFINITY, l = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (uint32_t k = 0; k < F::kGroups; ++k) {
-        m = fmaxf(m, s_ref[k][row]);
-        l += s_sum[k][row];
-        const float4 y = *((const float4*)((const float*)smem + (k * F::kRows + row) * kPad) + quad);
-        v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
-      }
-      if (whole) {
-        const uint32_t all = rb * F::kRows + row, nd = all / p.group, qh = head * p.group + (all - nd * p.group);
-        const float by = l == 0.f ? 0.f : 1.f / l;
-        if (quad * 4 < p.c.width)
-          *(uint2*)((char*)p.out.base + (uint64_t)(r.first + nd) * p.out.row_stride + qh * p.out.head_stride + quad * 8) =
-              make_uint2(pack2<T>(v.x * by, v.y * by), pack2<T>(v.z * by, v.w * by));
-        if (quad == 0 && p.lse)
-          p.lse[(uint64_t)(r.first + nd) * (p.c.heads * p.group) + qh] =
-              l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
-      } else {
-        __stcg((float4*)(mine + row * kPad) + quad, v);
-        if (quad == 0) {
-          __stcg(mine + F::kRows * kPad + row, m);
-          __stcg(mine + F::kRows * kPad + F::kRows + row, l);
+        for (uint32_t k = 0; k < F::kGroups; ++k) {
+          if (alone && k != k0) continue;
+          m = fmaxf(m, s_ref[k][row]);
+          l += s_sum[k][row];
+          const float4 y = *((const float4*)((const float*)smem + (k * F::kRows + row) * kPad) + quad);
+          v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+        }
+        if (whole) {
+          const uint32_t all = of_rb * F::kRows + row, nd = all / p.group, qh = of_head * p.group + (all - nd * p.group);
+          const float by = l == 0.f ? 0.f : 1.f / l;
+          if (quad * 4 < p.c.width)
+            *(uint2*)((char*)p.out.base + (uint64_t)(r.first + nd) * p.out.row_stride + qh * p.out.head_stride + quad * 8) =
+                make_uint2(pack2<T>(v.x * by, v.y * by), pack2<T>(v.z * by, v.w * by));
+          if (quad == 0 && p.lse)
+            p.lse[(uint64_t)(r.first + nd) * (p.c.heads * p.group) + qh] =
+                l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+        } else {
+          __stcg((float4*)(mine + row * kPad) + quad, v);
+          if (quad == 0) {
+            __stcg(mine + F::kRows * kPad + row, m);
+            __stcg(mine + F::kRows * kPad + F::kRows + row, l);
+          }
         }
       }
     }
@@ -686,7 +701,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
         join_few<T, F::kRows, kPad>(p, item_of, (float*)smem);
       }
     }
-    at += t1 - t0;
+    at += alone ? (uint64_t)F::kGroups * e.tiles : t1 - t0;
   }
 }
 

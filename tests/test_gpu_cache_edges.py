@@ -212,3 +212,13 @@ def test_many_requests_of_all_kinds():
         seqs = [(int(rng.integers(0, 90)), int(rng.integers(0, most + 1))) for _ in range(300)]
         seqs[7] = (5, most)
         Case("e4m3", "bf16", 1, 16, 1, group, 64, seqs, "tree", spare=3).run()
+
+
+@pytest.mark.parametrize("kind,q,group,nodes", [("bf16", "bf16", 4, 1), ("e4m3", "bf16", 4, 4), ("i8", "f16", 4, 8), ("f16", "f16", 1, 3)])
+def test_many_short_sequences_of_many_heads(kind, q, group, nodes):
+    """Whole items that follow one another in a request are worked on side by side; those that a share of the work
+    begins or ends in are not."""
+    rng = np.random.default_rng(nodes)
+    seqs = [(int(rng.choice([0, 1, 20, 63, 64, 130, 200])), int(rng.integers(1, nodes + 1))) for _ in range(260)]
+    seqs[40], seqs[41] = (3000, nodes), (0, 0)
+    Case(kind, q, 1, 16, 8 if group > 1 else 5, group, 64, seqs, "tree" if nodes > 1 else None).run()
