@@ -304,11 +304,14 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
           q[st][2 * n] = v.x;
           q[st][2 * n + 1] = v.y;
           const float2 a = unpack2<T>(v.x & 0x7FFF7FFFu), b = unpack2<T>(v.y & 0x7FFF7FFFu);
-          top = max(max(max(top, __float_as_uint(a.x)), max(__float_as_uint(a.y), __float_as_uint(b.x))), __float_as_uint(b.y));
+          const float y[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)  // (infinities and NaN left out)
+            if (__float_as_uint(y[k]) < 0x7F800000u) top = max(top, __float_as_uint(y[k]));
         }
         top = max(top, __shfl_xor_sync(kFull, top, 1));
         top = max(top, __shfl_xor_sync(kFull, top, 2));
-        const int exponent = top == 0 || top >= 0x7F800000u ? 14 : max((int)(top >> 23) - 127, 14 - 126);
+        const int exponent = top == 0 ? 14 : max((int)(top >> 23) - 127, 14 - 126);
         const float up = __uint_as_float((uint32_t)(14 - exponent + 127) << 23);
 #pragma unroll
         for (uint32_t st = 0; st < kSteps; ++st)

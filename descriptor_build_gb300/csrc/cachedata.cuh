@@ -38,7 +38,7 @@ __device__ __forceinline__ Request read_request(const CacheView& v, uint32_t i, 
   r.ok = r.seq < v.n_seqs && a >= 0 && a <= b && (uint32_t)b <= v.rows;
   r.rows = r.ok ? (uint32_t)(b - a) : 0;
   r.length = r.ok ? __ldg(v.length + r.seq) : 0;
-  if (r.length > (uint64_t)v.columns * v.page_tokens || (fresh && r.rows > r.length)) {
+  if (r.length >= 1u << 31 || r.length > (uint64_t)v.columns * v.page_tokens || (fresh && r.rows > r.length)) {
     r.ok = false;
     r.rows = 0;
   }

@@ -28,7 +28,7 @@
  * as db_page_extend has made room for them. A request is DB_PAGE_INVALID, and
  * does nothing, when
  *   - its seq is not below n_seqs, its sequence has more tokens than a row of
- *     the table has places for,
+ *     the table has places for, or 2^31,
  *   - start[i] > start[i+1] or start[i+1] > rows, or
  *   - (new tokens) it has more rows than the sequence tokens.
  * No sequence may be named twice where a call writes to the cache: what two

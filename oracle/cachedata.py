@@ -68,7 +68,7 @@ class Batch:
             s, a, b = int(seq[i]), int(start[i]), int(start[i + 1])
             ok = 0 <= s < self.table.shape[0] and 0 <= a <= b <= rows
             n = int(self.length[s]) & 0xFFFFFFFF if ok else 0
-            ok = ok and n <= self.table.shape[1] * T and not (fresh and b - a > n)
+            ok = ok and n < 1 << 31 and n <= self.table.shape[1] * T and not (fresh and b - a > n)
             ok = ok and (max_tokens is None or b - a <= max_tokens)
             self.status.append(OK if ok else INVALID)
             self.requests.append((s, a, b - a, n) if ok else None)

@@ -87,6 +87,41 @@ def test_infinite_queries(rows):
 
 
 @pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("width", [64, 128, 256])
+def test_an_infinite_query_and_a_large_one(rows, width):
+    """All scores of a row are minus infinity, by one infinite value of its query; another one, which f16 would not
+    hold, does not make them anything else."""
+    nodes, group = ROWS[rows]
+    c = Case("e4m3", "bf16", 1, 16, 1, group, width, [(90, nodes)], None)
+    c.pools[0][..., 5] = -1.0
+    c.q[1, 0, 5], c.q[1, 0, 9] = float("inf"), 1e5
+    out, lse = c.run()
+    assert (out[1, 0] == 0).all() and lse[1, 0] == -float("inf")
+
+
+def test_lengths_of_2_31_are_refused():
+    """A sequence's length as it may not be, with a table that would have room for it (pages of 2^23 tokens)."""
+    need_gpu()
+    db = lib()
+    pool = torch.zeros((2, 1 << 23, 1, 16), dtype=torch.int8, device="cuda")
+    scale = torch.zeros((2, 1 << 23, 1), device="cuda")
+    t = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    refs, free = torch.ones(2, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    tabs = db.PageTables(torch.zeros((1, 512), dtype=torch.int32, device="cuda"), t(-(1 << 31)), refs, free, 1 << 23)
+    layer = dict(k_pool=pool, v_pool=pool.clone(), k_scale=scale, v_scale=scale.clone())
+    q = torch.zeros((1, 1, 16), dtype=torch.bfloat16, device="cuda")
+    out, status = torch.full_like(q, 7), torch.zeros(1, dtype=torch.uint8, device="cuda")
+    ws = db.workspace(db.cache_attention_workspace_size(1, 1, 1, 16, 1))
+    for call in (lambda: db.cache_attention(tabs, t(0), t(0, 1), q, out=out, ws=ws, max_tokens=1, status=status, **layer),
+                 lambda: db.cache_write(tabs, t(0), t(0, 1), q, q, status=status, **layer),
+                 lambda: db.cache_read(tabs, t(0), t(0, 1), out, out.clone(), status=status, **layer)):
+        status.zero_()
+        call()
+        finish()
+        assert status.item() == 1 and (out == 7).all()
+
+
+@pytest.mark.parametrize("rows", ROWS)
 @pytest.mark.parametrize("kind,q,width", [("bf16", "bf16", 128), ("e4m3", "bf16", 112)])
 def test_every_end_of_a_tile(kind, q, width, rows):
     nodes, group = ROWS[rows]

@@ -53,6 +53,8 @@ def moves(m):
     b = tables(m, [0, 2, 1], [0, 4, 4, 4], 4, True, length=(3, 9))
     assert b.status == [1, 1, 1] and b.counters() == [0, 3, 0, 0]
     assert tables(m, [0], [0, 3], 3, True, max_tokens=2).status == [1]
+    b = m.Batch(np.zeros((1, 1 << 10), np.int64), [-(1 << 31)], 4, 1 << 22, [0], [0, 1], 1, True)
+    assert b.status == [1]  # 2^31 tokens, of 2^32 places
     assert tables(m, [0, 0, 0], [2, 1, 3, 4], 3, False).status == [1, 0, 1]
     # page 9 of 4 is none: its token reads as zeros, and the counters say so
     b = m.Batch([[9]], [2], 4, 4, [0], [0, 2], 2, False)
@@ -130,7 +132,7 @@ def test_hand_worked(case):
 MISTAKES = [
     ("(up == down) & (hi % 2 == 0)", "(up == down)"), ("np.float32(full / top), np.float32(top / full)", "np.float32(top / full), np.float32(full / top)"),
     ("not np.isfinite(row).all()", "np.isnan(row).all()"), ("scale == 0 or np.isinf(by)", "scale == 0"),
-    ("fresh and b - a > n", "fresh and b - a > n + 1"), ("n <= self.table.shape[1] * T", "n <= self.table.shape[1] * T + 1"),
+    ("fresh and b - a > n", "fresh and b - a > n + 1"), ("n <= self.table.shape[1] * T", "n <= self.table.shape[1] * T + 1"), ("n < 1 << 31 and", ""),
     ("b.place(s, n - m + j)", "b.place(s, j)"), ("if position < n else None", "if position <= n else None"),
     ("sees = own <= j", "sees = own < j"), ("group = q_heads // keys.shape[2]", "group = 1"), ("(kk @ qq) * scale", "(kk @ qq)  * scale * 2"),
     ("out[where] = (w @ vv) / w.sum()", "out[where] = w @ vv"), ("top + np.log(w.sum())", "np.log(w.sum())"),
