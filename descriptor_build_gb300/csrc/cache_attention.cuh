@@ -114,6 +114,11 @@ __device__ __forceinline__ Request near_request(const AttnParams& p, const Share
   return i - s.request < kNear ? s.near[i - s.request] : attention_request(p, i);
 }
 
+// (most are of 32 bits, which take a tenth of the instructions)
+static __device__ __noinline__ uint64_t quotient(uint64_t a, uint64_t b) {
+  return (a | b) >> 32 ? a / b : (uint32_t)a / (uint32_t)b;
+}
+
 // This CTA's units. Every thread calls it.
 template <uint32_t kRows, uint32_t kThreads>
 __device__ __forceinline__ Share plan_share(const AttnParams& p) {
@@ -126,8 +131,9 @@ __device__ __forceinline__ Share plan_share(const AttnParams& p) {
   uint64_t units = 0, excl, all;
   uint32_t bad = 0;
   uint64_t rows = 0;
+  Request r = {};
   for (uint32_t i = tid; i < n; i += kThreads) {
-    const Request r = attention_request(p, i);
+    r = attention_request(p, i);
     units += extent_of<kRows>(p, r).units;
     rows += r.rows;
     bad += !r.ok;
@@ -144,8 +150,8 @@ __device__ __forceinline__ Share plan_share(const AttnParams& p) {
   s.request = 0;
   s.before = 0;
   if (blockIdx.x >= s.ctas) return s;
-  s.lo = all * blockIdx.x / s.ctas;
-  s.hi = all * (blockIdx.x + 1) / s.ctas;
+  s.lo = quotient(all * blockIdx.x, s.ctas);
+  s.hi = quotient(all * (blockIdx.x + 1), s.ctas);
   uint64_t base = 0;
   for (uint32_t i0 = 0;; i0 += kThreads) {
     const uint32_t i = i0 + tid;
@@ -165,16 +171,18 @@ __device__ __forceinline__ Share plan_share(const AttnParams& p) {
   s.request = s_request;
   s.before = s_before;
   s.near = s_near;
-  if (tid < kNear && s.request + tid < n) s_near[tid] = attention_request(p, s.request + tid);
+  if (n <= kThreads) {  // a thread has read each
+    if (tid - s.request < kNear && tid < n) s_near[tid - s.request] = r;
+  } else if (tid < kNear && s.request + tid < n) {
+    s_near[tid] = attention_request(p, s.request + tid);
+  }
   __syncthreads();
   return s;
 }
 
-static __device__ __noinline__ uint64_t quotient(uint64_t a, uint64_t b) { return a / b; }
-
 // The CTA that has unit x.
 static __device__ __noinline__ uint32_t owner_of(const Share& s, uint64_t x) {
-  return (uint32_t)(((x + 1) * s.ctas - 1) / s.all);
+  return (uint32_t)quotient((x + 1) * s.ctas - 1, s.all);
 }
 
 // ------------------------------------------------------------ small operations
