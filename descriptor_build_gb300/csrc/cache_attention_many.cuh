@@ -48,13 +48,13 @@ struct Many {
   // Loaders that have units in turn. As they divide the ring, a place of it is
   // always the same warp's, which so sees every phase of its barrier (a wait by
   // parity is true too early when another phase lies between).
-  static constexpr uint32_t kLoaderWarps = kCodes ? 3 * kTiles : 2 * kTiles;
+  static constexpr uint32_t kLoaderWarps = kCodes ? 3 * kTiles : kPad == 128 && kTiles == 1 ? 3 : 2 * kTiles;
   // With 128 rows 256 threads: 128 registers each with two CTAs an SM (9 warps
   // would leave 96).
   static constexpr uint32_t kWarps = kTiles == 1 ? 8 : kWeights / 32 + kLoaderWarps + kTiles;
   static constexpr uint32_t kThreads = 32 * kWarps;
   static constexpr uint32_t kUnit = kTile * kPad * 2;  // keys or values of a tile
-  static constexpr uint32_t kUnits = kCodes ? 3 * kTiles : kTiles == 2 ? 8 : kPad >= 128 ? 4 : 6;
+  static constexpr uint32_t kUnits = kCodes ? 3 * kTiles : kTiles == 2 ? 8 : kPad == 128 ? 3 : kPad > 128 ? 4 : 6;
   static_assert(kUnits % kLoaderWarps == 0, "see kLoaderWarps");
   static constexpr uint32_t kQuery = kRows * kPad * 2;
   static constexpr uint32_t kRaw = kTile * kPad;       // codes of a unit
