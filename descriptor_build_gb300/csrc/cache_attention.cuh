@@ -57,7 +57,7 @@ struct AttnParams {
 // registers and shared memory hold.
 constexpr uint32_t attn_ctas_per_sm(uint32_t pad, bool codes, uint32_t blocks) {
   if (blocks >= kManyBlocks) return pad <= 128 && blocks == kManyBlocks ? 2 : 1;
-  return pad == 64 ? 4 : pad == 128 ? (codes || blocks == 1 ? 3 : 2) : codes ? 2 : 1;
+  return pad == 64 ? 4 : pad == 128 ? (codes || blocks == 1 ? 3 : 2) : codes || blocks == 2 ? 2 : 1;
 }
 constexpr unsigned kMaxAttnCtas = 1024;
 inline unsigned attn_grid(uint32_t ctas_per_sm) {

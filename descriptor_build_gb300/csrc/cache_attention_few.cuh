@@ -41,7 +41,7 @@ struct Few {
   static constexpr uint32_t kStage = 2 * kRaw + (kCodes ? 2 * kTokens * 4 : 0);
   static constexpr uint32_t kCtas = attn_ctas_per_sm(kPad, kCodes, kN * kShare);
   static constexpr uint32_t kStages =
-      kShare * (kCodes ? (kPad == 64 ? 5 : kPad == 128 ? 4 : 3) : kPad == 128 && kN == 1 ? 2 : 3);
+      kPad == 256 && !kCodes ? 3 : kShare * (kCodes ? (kPad == 64 ? 5 : kPad == 128 ? 4 : 3) : kPad == 128 && kN == 1 ? 2 : 3);
   static constexpr uint32_t kBytes = kGroups * kStages * kStage;
   static_assert(kBytes >= kGroups * kRows * kPad * 4 && kBytes >= 4 * kJoined * 16, "joins reuse the rings");
 };

@@ -12,7 +12,13 @@ int launch_blocks(const AttnParams& p, uint32_t blocks, cudaStream_t s) {
     case 1:
       return launch_few<T, kPad, kCodes, 1, 1>(p, s);
     case 2:
-      return launch_few<T, kPad, kCodes, 2, 1>(p, s);
+      // 16 rows of 256 16-bit values are more than a warp's registers hold: two
+      // warps share them, and two CTAs an SM (113 sequences of 4,223 tokens, 8 key
+      // heads: 701 us, 928 with a warp for all; codes 688, 652).
+      if constexpr (kPad == 256 && !kCodes)
+        return launch_few<T, kPad, kCodes, 1, 2>(p, s);
+      else
+        return launch_few<T, kPad, kCodes, 2, 1>(p, s);
     case 4:
       if constexpr (kCodes) return launch_few<T, kPad, kCodes, 2, 2>(p, s);
     case kManyBlocks:
