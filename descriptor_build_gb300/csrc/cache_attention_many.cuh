@@ -3,7 +3,7 @@
 // tcgen05 products.
 //
 // A CTA has three kinds of warps that hand tiles of 64 tokens on by mbarriers:
-//   loaders (2 to 6)    keys and values from their pages into a ring of tiles, by
+//   loaders (3 or 6)    keys and values from their pages into a ring of tiles, by
 //                       16-byte asynchronous copies; 8-bit codes come into a
 //                       ring of their own, from which they are widened
 //   one issuing thread  S = Q K^T into TMEM (two buffers), O += P V from TMEM
@@ -21,9 +21,9 @@
 // rows of 16 tokens a page come at 6.6 TB/s (1 CTA an SM, 4 tiles ahead) by
 // 16-byte copies of 128 threads and at 3.6 by TMA boxes of 64 values x 16 tokens,
 // which a CTA starts every 150 cycles; in this kernel boxes took 225 us where
-// the copies are done in less than 143 (48 trees of 25 nodes over 3,000 tokens).
+// the copies are done in less than 141 (48 trees of 25 nodes over 3,000 tokens).
 //
-// 48 trees of 25 nodes over 3,000 tokens (100 rows, bf16): 143 us, 4.5 TB/s: the
+// 48 trees of 25 nodes over 3,000 tokens (100 rows, bf16): 141 us, 4.6 TB/s: the
 // loaders' and issuing thread's instructions, and at each item's ends latency (a
 // third of the time before they were cut). 16 trees of 61 over 8,192 (488 rows,
 // I8): 235 us, 0.46 PFLOP/s: the weights' warps, of which a scheduler has two,
@@ -47,20 +47,21 @@ struct Many {
   static constexpr uint32_t kWeights = 128 * kTiles;
   // Loaders that have units in turn. As they divide the ring, a place of it is
   // always the same warp's, which so sees every phase of its barrier (a wait by
-  // parity is true too early when another phase lies between).
-  static constexpr uint32_t kLoaderWarps = kCodes ? 3 * kTiles : kPad == 128 && kTiles == 1 ? 3 : 2 * kTiles;
-  // With 128 rows 256 threads: 128 registers each with two CTAs an SM (9 warps
-  // would leave 96).
-  static constexpr uint32_t kWarps = kTiles == 1 ? 8 : kWeights / 32 + kLoaderWarps + kTiles;
+  // parity is true too early when another phase lies between). (48 trees, 16 bits:
+  // 144 us with two and a ring of four, 141 with three and a ring of three; four
+  // would leave 96 registers a thread, 145.)
+  static constexpr uint32_t kLoaderWarps = 3 * kTiles;
+  static constexpr uint32_t kWarps = kWeights / 32 + kLoaderWarps + kTiles;
   static constexpr uint32_t kThreads = 32 * kWarps;
   static constexpr uint32_t kUnit = kTile * kPad * 2;  // keys or values of a tile
-  static constexpr uint32_t kUnits = kCodes ? 3 * kTiles : kTiles == 2 ? 8 : kPad == 128 ? 3 : kPad > 128 ? 4 : 6;
+  static constexpr uint32_t kUnits = !kCodes && kPad == 64 ? 6 : 3 * kTiles;
   static_assert(kUnits % kLoaderWarps == 0, "see kLoaderWarps");
   static constexpr uint32_t kQuery = kRows * kPad * 2;
   static constexpr uint32_t kRaw = kTile * kPad;       // codes of a unit
   static constexpr uint32_t kRaws = kCodes ? kLoaderWarps : 0;
   static constexpr uint32_t kMeta = kUnits / 2 + 3;    // tiles that notes are kept of
-  static constexpr uint32_t kColumns = kPad * kTiles <= 128 ? 256 : 512;  // of TMEM
+  static constexpr uint32_t kColumns = kPad <= 128 && kTiles == 1 ? 256 : 512;  // of TMEM
+  static_assert(kTiles * (2 * kTile + kPad) <= kColumns, "scores of two tiles of tokens, and sums");
   static constexpr uint32_t kCtas = kPad <= 128 && kTiles == 1 ? 2 : 1;   // of an SM
   static constexpr uint32_t kBytes = kUnits * kUnit + kQuery + kRaws * kRaw + 1024;
   // no more CTAs an SM than TMEM holds
