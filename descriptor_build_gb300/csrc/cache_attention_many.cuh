@@ -64,8 +64,10 @@ struct Many {
   static_assert(kTiles * (2 * kTile + kPad) <= kColumns, "scores of two tiles of tokens, and sums");
   static constexpr uint32_t kCtas = kPad <= 128 && kTiles == 1 ? 2 : 1;   // of an SM
   static constexpr uint32_t kBytes = kUnits * kUnit + kQuery + kRaws * kRaw + 1024;
-  // no more CTAs an SM than TMEM holds
-  static constexpr uint32_t kLeast = (kCtas == 2 ? 80 : 120) * 1024;
+  // Shared memory for no more CTAs an SM than TMEM holds, of this launch and of
+  // the next, which may have begun: one that got TMEM before a CTA that it waits
+  // for would wait for ever.
+  static constexpr uint32_t kLeast = (kCtas == 2 ? 80 : 200) * 1024;
   static constexpr uint32_t kAsk = kBytes < kLeast ? kLeast : kBytes;
 };
 
