@@ -13,9 +13,10 @@
 // made, and two CTAs share an SM. Items of more than 128 rows have a CTA of two
 // such tiles of rows, each with its issuing thread and weights' warps, which
 // share what is loaded and widened (wide trees of 488 rows 396 us with CTAs of
-// 128 rows, 374 with two tiles and one issuing thread, 312 with two). A row's maximum is followed only when it has
-// risen by 2^kSlack (weights of 2^kSlack are held as exactly as 1), so O is
-// hardly ever rescaled.
+// 128 rows, 374 with two tiles and one issuing thread, 312 with two).
+//
+// A row's maximum is followed only when it has risen by 2^kSlack (weights of
+// 2^kSlack are held as exactly as 1), so O is hardly ever rescaled.
 //
 // A row of a page is 128 or 256 bytes, the next token's some kilobytes on. Such
 // rows of 16 tokens a page come at 6.6 TB/s (1 CTA an SM, 4 tiles ahead) by
