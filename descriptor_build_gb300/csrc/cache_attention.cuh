@@ -21,17 +21,16 @@ namespace db {
 constexpr uint32_t kTile = 64;             // tokens of a unit
 constexpr uint32_t kAttnThreads = 128;
 constexpr uint32_t kMaxGroup = 64;
-// A row's maximum is followed when it has risen by more than a slack (log2), for
-// codes also the exponent of the values' largest scale. Weights times scales
-// are then below 2^(lift + slack + 3), or 2^(lift + slack) without scales. f16
-// ones (below 2^16) start that much above 1, so that small ones are normal numbers
-// still: the kernel for few rows follows sooner and starts higher, for which the
-// error of long answers in f16 is 1.4 times their rounding's (1.5 with the
-// other's).
-constexpr uint32_t kScaleSlack = 2;
-template <typename W, bool kCodes>
+// A row's reference is the largest score, for codes the largest score times its
+// values' scale (as a power of two), of the tokens that the row sees, and is followed
+// when one is more than 2^slack above it. f16 weights times scales are then below
+// 2^(lift + slack + 1), those without scales below 2^(lift + slack). They start as far
+// above 1 as f16 (below 2^16) allows, so that small ones are normal numbers still: the
+// kernel for few rows follows sooner and starts higher, for which the error of long
+// answers in f16 is 1.4 times their rounding's (1.5 with the other's).
+template <typename W>
 __host__ __device__ constexpr int attn_lift(int slack) {
-  return !std::is_same<W, __half>::value ? 0 : (kCodes ? 12 : 14) - slack;
+  return std::is_same<W, __half>::value ? 14 - slack : 0;
 }
 constexpr uint32_t kManyBlocks = 16;      // blocks of 8 query rows of the tcgen05 kernel's items, or twice as many
 
@@ -191,6 +190,21 @@ __device__ __forceinline__ float exp2_of(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// l times 2^d, d <= 0, also where 2^d alone is below the range of the numbers.
+__device__ __forceinline__ float times_exp2(float l, float d) {
+  const float h = exp2_of(0.5f * d);
+  return l * h * h;
+}
+// The exponent of a scale. What a row sums has the size of its references' inverse, and
+// 2^31 weights that start at 2^lift must not leave the range: scales below 2^-80 (zeros)
+// are taken as that, those from 2^101 on as 2^100. One that is not finite makes the row's
+// answer so whatever its reference.
+constexpr uint32_t kLeastExponent = 127 - 80, kMostExponent = 127 + 100;
+__device__ __forceinline__ uint32_t scale_exponent(float scale) {
+  const uint32_t e = __float_as_uint(scale) >> 23 & 0xFFu;
+  return e == 0xFFu ? kLeastExponent : min(max(e, kLeastExponent), kMostExponent);
+}
+__device__ __forceinline__ float scale_size(float scale) { return (float)((int)scale_exponent(scale) - 127); }
 __device__ __forceinline__ uint32_t smem_at(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 // 16 bytes (or zeros) into shared memory, without a register. (The form with a
 // size in a register is several times slower to start.)

@@ -73,7 +73,7 @@ static __device__ __noinline__ void join_few(const AttnParams& p, const JoinedIt
     for (uint32_t k = item.c0 + slice; k <= item.c1; k += kSlices) {
       const float mk = __ldcg(part_at(k) + kRows * kPad + row), lk = __ldcg(part_at(k) + kRows * kPad + kRows + row);
       const float now = fmaxf(m, mk), by = now == -INFINITY ? 0.f : now;
-      l = l * exp2_of(m - by) + lk * exp2_of(mk - by);
+      l = times_exp2(l, m - by) + times_exp2(lk, mk - by);
       m = now;
     }
     s_top[slice][row] = m;
@@ -87,7 +87,7 @@ static __device__ __noinline__ void join_few(const AttnParams& p, const JoinedIt
     for (uint32_t k = 0; k < kSlices; ++k) m = fmaxf(m, s_top[k][row]);
     const float by = m == -INFINITY ? 0.f : m;
 #pragma unroll
-    for (uint32_t k = 0; k < kSlices; ++k) l += s_sum[k][row] * exp2_of(s_top[k][row] - by);
+    for (uint32_t k = 0; k < kSlices; ++k) l += times_exp2(s_sum[k][row], s_top[k][row] - by);
     const uint32_t all = item.row0 + row, node = all / p.group, qh = item.head * p.group + (all - node * p.group);
     const uint64_t to = (uint64_t)(item.first + node) * p.out.row_stride + qh * p.out.head_stride;
     s_note[row] = make_float4(by, l == 0.f ? 0.f : 1.f / l, __uint_as_float((uint32_t)to),
@@ -165,9 +165,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
     return !kCodes ? 16 * d + g : kPad == 64 ? 8 * g + 2 * d : 128 * (d / 8) + 16 * g + 2 * (d % 8);
   };
   constexpr uint32_t kOther = kCodes ? 1 : 8;
-  const auto shift_of = [](uint32_t exponent) __attribute__((always_inline)) {
-    return (float)((int)exponent - 127 - attn_lift<H, kCodes>(kFewSlack));
-  };
+  constexpr float kLift = (float)attn_lift<H>(kFewSlack);
   // a lane copies the same chunk of every kStep-th token
   const uint32_t chunk = lane % kChunks, token0 = lane / kChunks;
   const bool has = chunk < (kCodes ? p.c.width / 16 : p.c.width / 8);
@@ -342,7 +340,6 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
 
     float o[kSteps][kN][4];
     float top[kN][2], sum[kN][2];
-    uint32_t exponent = 127;  // codes: of the values' scales so far
 #pragma unroll
     for (uint32_t d = 0; d < kSteps; ++d)
 #pragma unroll
@@ -436,33 +433,27 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
               s[n][k] = -INFINITY;
           }
       }
-      // Weights are exp2(score - ref). ref is a score that was a row's largest,
-      // followed when one is 2^kFewSlack above it; for codes it also takes in the size
-      // of the values' scales, so that weights times scales stay in the middle
-      // of f16's range.
+      // Weights are exp2(score - ref). ref is kLift below what was a row's largest score,
+      // followed when one is 2^kFewSlack above it; with codes the largest score times
+      // its values' scale, of the tokens that the row sees, so that weights times scales
+      // stay in the middle of f16's range. (Of all tokens of a tile, or without the
+      // scores, one large scale would take the others' products out of that range,
+      // though no row sees it or it hardly counts.)
+      float v0 = 1.f, v1 = 1.f, e0 = 0.f, e1 = 0.f;
+      if (kCodes) {
+        v0 = scales[16 + g], v1 = scales[24 + g];
+        e0 = scale_size(v0), e1 = scale_size(v1);
+      }
       float most[kN][2];
       bool rises = false;
 #pragma unroll
       for (uint32_t n = 0; n < kN; ++n)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          most[n][h] = fmaxf(s[n][h], s[n][2 + h]);
+          most[n][h] = kCodes ? fmaxf(s[n][h] + e0, s[n][2 + h] + e1) : fmaxf(s[n][h], s[n][2 + h]);
           rises |= most[n][h] > top[n][h] + (float)kFewSlack || (top[n][h] == -INFINITY && most[n][h] > -INFINITY);
         }
-      float v0 = 1.f, v1 = 1.f;
-      uint32_t scale_ex = 0;
-      if (kCodes) {
-        v0 = scales[16 + g], v1 = scales[24 + g];
-        const uint32_t e0 = (__float_as_uint(v0) >> 23) & 0xFFu, e1 = (__float_as_uint(v1) >> 23) & 0xFFu;
-        scale_ex = max(e0 == 0xFFu ? 0u : e0, e1 == 0xFFu ? 0u : e1);
-        rises |= t == 0 || min(max(scale_ex, 31u), 227u) > exponent + kScaleSlack;
-      }
       if (__any_sync(kFull, rises)) {
-        const uint32_t ex_before = exponent;
-        if (kCodes) {
-          const uint32_t now = min(max(__reduce_max_sync(kFull, scale_ex), 31u), 227u);
-          if (t == 0 || now > exponent + kScaleSlack) exponent = now;
-        }
 #pragma unroll
         for (uint32_t n = 0; n < kN; ++n)
 #pragma unroll
@@ -471,11 +462,10 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
             m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
             m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
             m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
-            const float was = top[n][h] + shift_of(ex_before);
-            if (m > top[n][h] + (float)kFewSlack || top[n][h] == -INFINITY) top[n][h] = m;
-            const float ref = top[n][h] == -INFINITY ? 0.f : top[n][h] + shift_of(exponent);
-            const float down = exp2_of(was - ref);
-            sum[n][h] *= down;
+            const float was = top[n][h];
+            if (m > was + (float)kFewSlack || was == -INFINITY) top[n][h] = m;
+            const float fall = was - (top[n][h] == -INFINITY ? 0.f : top[n][h]), down = exp2_of(fall);
+            sum[n][h] = times_exp2(sum[n][h], fall);
 #pragma unroll
             for (uint32_t d = 0; d < kSteps; ++d) {
               o[d][n][h] *= down;
@@ -483,12 +473,11 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
             }
           }
       }
-      const float shift = shift_of(exponent);
 #pragma unroll
       for (uint32_t n = 0; n < kN; ++n)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float ref = top[n][k & 1] == -INFINITY ? 0.f : top[n][k & 1] + shift;
+          const float ref = top[n][k & 1] == -INFINITY ? 0.f : top[n][k & 1] - kLift;
           s[n][k] = exp2_of(s[n][k] - ref);
           sum[n][k & 1] += s[n][k];
         }
@@ -624,7 +613,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
         l += __shfl_xor_sync(kFull, l, 8);
         l += __shfl_xor_sync(kFull, l, 16);
         sum[n][h] = l;
-        top[n][h] += shift_of(exponent);  // the reference of what was summed
+        top[n][h] -= kLift;  // the reference of what was summed
         if (g == 0) s_ref[team][row0 + n * 8 + 2 * c + h] = top[n][h];
       }
     copies_wait<0>();
@@ -639,8 +628,8 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
 #pragma unroll
           for (uint32_t k = 0; k < F::kGroups; ++k) m = fmaxf(m, s_ref[k][row]);
         }
-        const float a = exp2_of(top[n][h] - (m == -INFINITY ? 0.f : m));
-        if (g == 0) s_sum[team][row] = sum[n][h] * a;
+        const float fall = top[n][h] - (m == -INFINITY ? 0.f : m), a = exp2_of(fall);
+        if (g == 0) s_sum[team][row] = times_exp2(sum[n][h], fall);
         float* const to = (float*)smem + (team * F::kRows + row) * kPad;
 #pragma unroll
         for (uint32_t d = 0; d < kSteps; ++d) {

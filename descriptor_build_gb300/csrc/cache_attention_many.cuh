@@ -27,7 +27,7 @@
 // 48 trees of 25 nodes over 3,000 tokens (100 rows, bf16): 141 us, 4.6 TB/s: the
 // loaders' and issuing thread's instructions, and at each item's ends latency (a
 // third of the time before they were cut). 16 trees of 61 over 8,192 (488 rows,
-// I8): 235 us, 0.46 PFLOP/s: the weights' warps, of which a scheduler has two,
+// I8): 241 us, 0.45 PFLOP/s: the weights' warps, of which a scheduler has two,
 // and instructions not yet fetched.
 //
 // Tiles lie as the tensor cores' 128-byte swizzle wants them: panels of 64
@@ -77,7 +77,7 @@ struct alignas(16) TileNotes {    // scales are read by fours
   int2 place[kTile];              // page (or -1) and slot of a token
   float k_scale[kTile], v_scale[kTile];
   uint32_t real[2], odd[2];       // bits of tokens: that are there; whose values are not all finite
-  uint32_t exponent[2];           // of the largest scale of values
+  uint32_t exponent[2];           // of the largest scale of values (scale_exponent)
 };
 
 __device__ __forceinline__ void barrier_init(uint32_t bar, uint32_t count) {
@@ -265,6 +265,23 @@ static __device__ __noinline__ void hide_scores(uint32_t here, uint32_t sees0, u
   tmem_stored();
 }
 
+// The largest score times its values' scale of a row: codes' reference (log2). (Of an
+// item's first tile, and hardly another. As a function that is called it took 20 us more
+// of 16 wide trees.)
+__device__ __forceinline__ float largest_product(uint32_t here, float factor, const float* v_scale) {
+  float most = -INFINITY;
+#pragma unroll 1
+  for (uint32_t h = 0; h < 4; ++h) {
+    uint32_t s[16];
+    __syncwarp();
+    tmem_load16(here + 16 * h, s);
+    tmem_loaded();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) most = fmaxf(most, __fmaf_rn(__uint_as_float(s[j]), factor, scale_size(v_scale[16 * h + j])));
+  }
+  return most;
+}
+
 // Values that are not finite, which the product is not given, added to O for
 // the rows that see them. `v`, `scale`: of the head.
 template <typename T, bool kCodes>
@@ -327,7 +344,7 @@ static __device__ __noinline__ void join_item(const AttnParams& p, const JoinedI
     for (uint32_t k = item.c0; k <= item.c1; ++k) {
       const float mk = __ldcg(part_at(k) + kRows * kPad + row), lk = __ldcg(part_at(k) + kRows * kPad + kRows + row);
       const float now = fmaxf(m, mk), by = now == -INFINITY ? 0.f : now;
-      l = l * exp2_of(m - by) + lk * exp2_of(mk - by);
+      l = times_exp2(l, m - by) + times_exp2(lk, mk - by);
       m = now;
     }
     const uint32_t all = item.row0 + row, node = all / p.group, qh = item.head * p.group + (all - node * p.group);
@@ -671,9 +688,9 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
               // an infinite scale stands for values of both signs, whose
               // products have no sum
               m.k_scale[32 * h + lane] = __fmaf_rn(k_sc[h], 0.f, k_sc[h]) * fabsf(p.scale_log2);
-              const uint32_t ex = (__float_as_uint(v_sc[h]) >> 23) & 0xFFu;
-              m.v_scale[32 * h + lane] = !whole && ex == 0xFFu ? 0.f : v_sc[h];  // odd tokens are added by themselves
-              const uint32_t most = __reduce_max_sync(kFull, ex == 0xFFu ? 0u : ex);
+              const bool finite = (__float_as_uint(v_sc[h]) & 0x7F800000u) != 0x7F800000u;
+              m.v_scale[32 * h + lane] = !whole && !finite ? 0.f : v_sc[h];  // odd tokens are added by themselves
+              const uint32_t most = __reduce_max_sync(kFull, scale_exponent(v_sc[h]));
               if (lane == 0) m.exponent[h] = most;
             }
           }
@@ -863,11 +880,11 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
         writes_to_async_proxy();
         barrier_arrive(smem_at(&s_asked));
       }
-      // Weights are exp2(score - ref). ref is a score that was the largest, and
-      // for codes also takes in the size of the values' scales, which P has as
-      // a factor, so that P stays in the middle of f16's range.
+      // Weights are exp2(score - ref). ref is kLift below what was the largest score, for
+      // codes the largest score times its values' scale of the tokens that the row sees:
+      // P has the scales as a factor, and so stays in the middle of f16's range.
+      constexpr float kLift = (float)attn_lift<W>(kSlack);
       float top = -INFINITY, sum = 0.f;
-      uint32_t exponent = 0;
       {
         uint32_t zero[16];
 #pragma unroll
@@ -944,17 +961,14 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
         if (kCodes) tmem_stored();
         most = fmaxf(most, other);
         most *= factor;
-        const float ref_before = top + (float)((kCodes ? (int)exponent - 127 : 0) - attn_lift<W, kCodes>(kSlack));
-        bool move = most > top + (float)kSlack || (top == -INFINITY && most > -INFINITY);
-        if (move) top = most;
-        if (kCodes) {
-          const uint32_t ex = min(max(max(m.exponent[0], m.exponent[1]), 31u), 227u);
-          if (exponent == 0 || ex > exponent + kScaleSlack) {
-            exponent = ex;
-            move = true;
-          }
-        }
-        const float ref = top == -INFINITY ? 0.f : top + (float)((kCodes ? (int)exponent - 127 : 0) - attn_lift<W, kCodes>(kSlack));
+        // With codes no product is larger than the largest score times the tile's largest
+        // scale, hidden tokens' among them; only where that would move the reference is
+        // the row's own largest looked for, so what is hidden has no part in it. (16 wide
+        // trees 241 us; 253 with all scores times their scales in the loop above.)
+        const auto rises = [&](float x) __attribute__((always_inline)) {
+          return x > top + (float)kSlack || (top == -INFINITY && x > -INFINITY);
+        };
+        bool move = rises(kCodes ? most + (float)((int)max(m.exponent[0], m.exponent[1]) - 127) : most);
         uint64_t odd = 0;
         if (masked) {
           const uint32_t at_odd = tile % F::kMeta;
@@ -963,16 +977,20 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
           odd_phases ^= 1u << at_odd;
           odd = (uint64_t)m.odd[0] | (uint64_t)m.odd[1] << 32;
         }
-        if (__any_sync(kFull, move && k) || odd) {
+        if (__any_sync(kFull, move) || odd) {
+          if (kCodes) {
+            most = largest_product(here, factor, m.v_scale);
+            move = rises(most);
+          }
+          const float fall = move ? top - most : 0.f;
+          if (move) top = most;
           // O belongs to this warp while no product adds to it
-          if (k) {
+          if (k && (odd || __any_sync(kFull, move))) {
             ok = barrier_wait(smem_at(&s_output[half][buffer ^ 1]), ((tile - 1) >> 1) & 1, &s_failed);
             if (!__all_sync(kFull, ok)) break;
             tensor_fence_after();
-          }
-          const float down = move ? exp2_of(ref_before - ref) : 1.f;
-          if (k) sum *= down;
-          if (k) {
+            const float down = exp2_of(fall);
+            sum = times_exp2(sum, fall);
 #pragma unroll 1
             for (uint32_t c = 0; c < p.c.width; c += 16) {
               uint32_t o[16];
@@ -985,11 +1003,12 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
             tmem_stored();
           }
           if (odd)
-            add_odd<T, kCodes>(m, sums_at, here, odd, (uint64_t)sees[1] << 32 | sees[0], factor, ref,
+            add_odd<T, kCodes>(m, sums_at, here, odd, (uint64_t)sees[1] << 32 | sees[0], factor, top == -INFINITY ? 0.f : top - kLift,
                                (const char*)p.c.v + head * p.head_step, p.c.v_stride, p.token_step,
                                (const char*)(p.c.v_scale + (kCodes ? head * p.scale_head_step : 0)), p.c.v_scale_stride,
                                p.scale_token_step, !e4m3, p.c.width);
         }
+        const float ref = top == -INFINITY ? 0.f : top - kLift;
         uint64_t sums = pair(__float_as_uint(sum), 0), more = pair(0, 0);
         const uint64_t by = pair(__float_as_uint(factor), __float_as_uint(factor));
         const uint64_t less = pair(__float_as_uint(-ref), __float_as_uint(-ref));
@@ -1029,7 +1048,7 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
       go = group_all(1, F::kWeights, ok);
       if (go) {
         tensor_fence_after();
-        const float ref = top == -INFINITY ? -INFINITY : top + (float)((kCodes ? (int)exponent - 127 : 0) - attn_lift<W, kCodes>(kSlack));
+        const float ref = top - kLift;
         const bool whole = t0 == 0 && t1 == e.tiles;
         const auto query_head = [&](uint32_t row_, uint32_t& nd) {
           const uint32_t a = rb * F::kRows + row_;
