@@ -285,6 +285,13 @@ __device__ __forceinline__ uint2 widen4<__nv_bfloat16>(uint32_t w, bool e4m3) {
   return r;
 }
 
+// Four sums of weights times values as answers; `by`: 1 over the sum of weights, or 0 for a
+// row that has none. Its answers are 0, also where values are not finite (0 times them is NaN).
+template <typename T>
+__device__ __forceinline__ uint2 four_answers(const float4& v, float by) {
+  return by == 0.f ? make_uint2(0, 0) : make_uint2(pack2<T>(v.x * by, v.y * by), pack2<T>(v.z * by, v.w * by));
+}
+
 // Whether one of two 16-bit values is an infinity or NaN.
 template <typename T>
 __device__ __forceinline__ bool not_finite2(uint32_t w);

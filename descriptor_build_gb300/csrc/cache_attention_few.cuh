@@ -131,9 +131,8 @@ static __device__ __noinline__ void join_few(const AttnParams& p, const JoinedIt
         const float4 w0 = sums[at], w1 = sums[32 * kMany + at], w2 = sums[64 * kMany + at], w3 = sums[96 * kMany + at];
         const float4 n = s_note[of / kQuads];
         const uint64_t to = (uint64_t)__float_as_uint(n.w) << 32 | __float_as_uint(n.z);
-        *(uint2*)((char*)p.out.base + to + of % kQuads * 8) =
-            make_uint2(pack2<T>((w0.x + w1.x + w2.x + w3.x) * n.y, (w0.y + w1.y + w2.y + w3.y) * n.y),
-                       pack2<T>((w0.z + w1.z + w2.z + w3.z) * n.y, (w0.w + w1.w + w2.w + w3.w) * n.y));
+        *(uint2*)((char*)p.out.base + to + of % kQuads * 8) = four_answers<T>(
+            make_float4(w0.x + w1.x + w2.x + w3.x, w0.y + w1.y + w2.y + w3.y, w0.z + w1.z + w2.z + w3.z, w0.w + w1.w + w2.w + w3.w), n.y);
       }
     }
     __syncthreads();
@@ -663,7 +662,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
           const float by = l == 0.f ? 0.f : 1.f / l;
           if (quad * 4 < p.c.width)
             *(uint2*)((char*)p.out.base + (uint64_t)(r.first + nd) * p.out.row_stride + qh * p.out.head_stride + quad * 8) =
-                make_uint2(pack2<T>(v.x * by, v.y * by), pack2<T>(v.z * by, v.w * by));
+                four_answers<T>(v, by);
           if (quad == 0 && p.lse)
             p.lse[(uint64_t)(r.first + nd) * (p.c.heads * p.group) + qh] =
                 l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);

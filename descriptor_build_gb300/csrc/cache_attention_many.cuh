@@ -390,10 +390,10 @@ static __device__ __noinline__ void join_item(const AttnParams& p, const JoinedI
     char* const to = (char*)p.out.base + ((uint64_t)__float_as_uint(n.w) << 32 | __float_as_uint(n.z)) + quad0 * 8;
 #pragma unroll
     for (uint32_t j = 0; j < kMany; j += 2)  // (width is a multiple of 16 values)
-      if (j < quads)
-        *(uint4*)(to + j * 8) =
-            make_uint4(pack2<T>(v[j].x * n.y, v[j].y * n.y), pack2<T>(v[j].z * n.y, v[j].w * n.y),
-                       pack2<T>(v[j + 1].x * n.y, v[j + 1].y * n.y), pack2<T>(v[j + 1].z * n.y, v[j + 1].w * n.y));
+      if (j < quads) {
+        const uint2 a = four_answers<T>(v[j], n.y), b = four_answers<T>(v[j + 1], n.y);
+        *(uint4*)(to + j * 8) = make_uint4(a.x, a.y, b.x, b.y);
+      }
   }
 }
 
@@ -1070,10 +1070,11 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
           const float* const f = (const float*)o;
           if (whole) {
 #pragma unroll
-            for (int j = 0; j < 16; j += 8)
-              *(uint4*)(to + (c + j) * 2) =
-                  make_uint4(pack2<T>(f[j] * by, f[j + 1] * by), pack2<T>(f[j + 2] * by, f[j + 3] * by),
-                             pack2<T>(f[j + 4] * by, f[j + 5] * by), pack2<T>(f[j + 6] * by, f[j + 7] * by));
+            for (int j = 0; j < 16; j += 8) {
+              const uint2 a = four_answers<T>(make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]), by);
+              const uint2 b = four_answers<T>(make_float4(f[j + 4], f[j + 5], f[j + 6], f[j + 7]), by);
+              *(uint4*)(to + (c + j) * 2) = make_uint4(a.x, a.y, b.x, b.y);
+            }
           } else {
 #pragma unroll
             for (int j = 0; j < 16; j += 4)
