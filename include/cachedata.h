@@ -31,6 +31,10 @@
  *     the table has places for, or 2^31,
  *   - start[i] > start[i+1] or start[i+1] > rows, or
  *   - (new tokens) it has more rows than the sequence tokens.
+ * Every other request is done by itself, whatever is wrong beside it; where
+ * start does not ascend and valid requests share rows, each reads them, and
+ * what several write is any one's (write and read take longer then: they look
+ * for a row's request by its place among the starts first).
  * No sequence may be named twice where a call writes to the cache: what two
  * requests both write is then either's (nothing else is touched).
  *
