@@ -65,9 +65,8 @@ struct Many {
   static_assert(kTiles * (2 * kTile + kPad) <= kColumns, "scores of two tiles of tokens, and sums");
   static constexpr uint32_t kCtas = kPad <= 128 && kTiles == 1 ? 2 : 1;   // of an SM
   static constexpr uint32_t kBytes = kUnits * kUnit + kQuery + kRaws * kRaw + 1024;
-  // Shared memory for no more CTAs an SM than TMEM holds, of this launch and of
-  // the next, which may have begun: one that got TMEM before a CTA that it waits
-  // for would wait for ever.
+  // Shared memory for no more CTAs an SM than TMEM holds: another would wait for TMEM
+  // until one of them is done, while a different SM has room.
   static constexpr uint32_t kLeast = (kCtas == 2 ? 80 : 200) * 1024;
   static constexpr uint32_t kAsk = kBytes < kLeast ? kLeast : kBytes;
 };
@@ -417,11 +416,6 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
   unsigned char* const smem = smem_raw + ((1024 - (smem_at(smem_raw) & 1023)) & 1023);
   const uint32_t ring = smem_at(smem), query = ring + F::kUnits * F::kUnit;
 
-  if (warp == F::kWarps - 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_at(&s_tmem)), "n"(F::kColumns)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-  }
   if (kCodes && tid < kTile) s_ones[tid] = 1.f;
   if (tid == 0) {
     for (uint32_t k = 0; k < F::kUnits; ++k) {
@@ -455,6 +449,13 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
   }
   wait_for_prerequisites();
   dependents_may_launch();
+  // TMEM only now: a CTA that had it while it waits would keep it from the CTAs, of any
+  // library, of the kernels that it waits for.
+  if (warp == F::kWarps - 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_at(&s_tmem)), "n"(F::kColumns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
   tensor_fence_before();
   __shared__ Share share;  // not in every thread's registers
   {
