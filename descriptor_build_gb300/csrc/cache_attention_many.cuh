@@ -1127,11 +1127,16 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
     while (!barrier_try(smem_at(&s_drained), 0) && globaltimer_ns() - began < kWaitLimitNs) {
     }
   }
-  if (!go && tid == 0 && p.view.ctr) atomicOr((unsigned int*)&p.view.ctr->err, DB_ERR_TIMEOUT);
   tensor_fence_before();
   __syncthreads();
   if (warp == F::kWarps - 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(F::kColumns));
+  if (s_failed) {  // (CTA 0 wrote the status when it began, the length of a wait's limit ago)
+    if (tid == 0 && p.view.ctr) atomicOr((unsigned int*)&p.view.ctr->err, DB_ERR_TIMEOUT);
+    if (p.view.status)
+#pragma unroll 1
+      for (uint32_t i = tid; i < p.view.n; i += F::kThreads) p.view.status[i] = DB_PAGE_INVALID;
+  }
 }
 
 template <typename T, uint32_t kPad, bool kCodes, uint32_t kTiles>

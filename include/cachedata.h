@@ -150,8 +150,9 @@ int db_cache_read(const db_page_tables* t, const db_cache_batch* b, const int32_
  *               width); the size is that of the current device. Zeros at
  *               first, and left ready for the next call; calls that may run at
  *               the same time (on two streams, in two graphs) need one each.
- *               After DB_ERR_TIMEOUT in ctr (a kernel gave up waiting, and out
- *               is not valid) it has to be zeros again.
+ *               After DB_ERR_TIMEOUT in ctr (a kernel gave up waiting, out is not
+ *               valid, and status is DB_PAGE_INVALID for all requests) it has to
+ *               be zeros again.
  * q may be out. n <= 65536, q_heads a multiple of heads and at most 64 of
  * them to a key head. */
 int db_cache_attention_workspace_size(uint32_t n, uint32_t q_heads, uint32_t heads, uint32_t width,

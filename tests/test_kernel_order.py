@@ -38,3 +38,15 @@ def test_what_is_taken_is_given_back(call):
             for kernel in kernels(f.read()):
                 if "tcgen05.alloc" in kernel:
                     assert kernel.count(call) == 1, path
+
+
+def test_a_wait_that_runs_out_is_told_in_the_status_too():
+    """A kernel of attention that gives up waiting says so in the counters, and that no request is a valid one."""
+    told = 0
+    for path in SOURCES:
+        with open(path) as f:
+            for kernel in kernels(f.read()):
+                if "DB_ERR_TIMEOUT" in kernel and "attention_" in kernel:
+                    told += 1
+                    assert "status[i] = DB_PAGE_INVALID" in kernel[kernel.index("DB_ERR_TIMEOUT"):], path
+    assert told
