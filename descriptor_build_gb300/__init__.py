@@ -895,7 +895,9 @@ def draft_verify(start: torch.Tensor, parent: torch.Tensor, token: torch.Tensor,
                  ctr: torch.Tensor | None = None, stream=None) -> None:
     """db_draft_verify: trees of drafted tokens (rows start[i] to start[i + 1]
     of parent, token, u, and of the probabilities p and q [rows, vocab])
-    accepted or not; path [rows], accepted [n] and next [n] get the result."""
+    accepted or not; path [rows], accepted [n] and next [n] get the result. Of
+    a tree that is refused none is accepted, not the root either: cache_keep
+    and page_free then take its sequence's step back."""
     n, rows = start.numel() - 1, p.shape[0]
     if n < 0 or p.dim() != 2 or p.stride(1) != 1:
         raise ValueError("start must be [n + 1], p [rows, vocab] with neighbouring values")

@@ -190,7 +190,10 @@ int db_cache_attention(const db_page_tables* t, const db_cache_batch* b, const d
  * computed in 32 bits, the test of a child in 64.
  * DB_PAGE_INVALID: no rows or more than 1024, start as in a batch, a node's
  * parent not below it or its token outside. Then accepted = 0, next = -1, and
- * the rows' path -1 (unless start is what is wrong). next is -1 as well where
+ * the rows' path -1 (unless start is what is wrong). A step goes on with that:
+ * db_cache_keep keeps none of the request's tokens and cuts to base, so that
+ * db_page_free leaves the sequence as it was before the step's db_page_extend,
+ * the root not in it; the step can be taken again. next is -1 as well where
  * all of p_j is 0. vocab <= 2^19. */
 int db_draft_verify(const int32_t* start, uint32_t n, uint32_t rows, const int32_t* parent,
                     const int32_t* token, const void* p, uint64_t p_stride, const void* q,
