@@ -867,7 +867,8 @@ def cache_attention(tables: PageTables, seq: torch.Tensor, start: torch.Tensor, 
     [rows, q_heads, width], at most max_tokens of a sequence) attend to all
     tokens before them and to those of their own that mask [rows, words] of
     bits names (None: themselves and the ones before). scale None: 1 /
-    sqrt(width). lse: float32 [rows, q_heads]."""
+    sqrt(width). lse: float32 [rows, q_heads]. max_tokens chooses the kernel
+    for the whole call, so single tokens go faster in one of their own."""
     layer, heads, width = _cache_layer(tables, k_pool, v_pool, k_scale, v_scale, token_dim)
     rows, q_heads, _ = q.shape
     if out.shape[0] != rows:

@@ -144,7 +144,9 @@ int db_cache_read(const db_page_tables* t, const db_cache_batch* b, const int32_
  * Sums of weights times values have to stay within 32 bits' range: values up
  * to 2^100 do, and those of codes above 2^-90 keep their precision.
  *   max_tokens  no request has more rows (one that has is DB_PAGE_INVALID);
- *               with a mask at most 32 * mask_words
+ *               with a mask at most 32 * mask_words. It chooses the kernel for
+ *               all requests of the call: single tokens go faster in a call of
+ *               their own than beside requests of many
  *   ws          of db_cache_attention_workspace_size bytes for these heads,
  *               width and max_tokens (or larger ones of the same heads and
  *               width); the size is that of the current device. Zeros at
