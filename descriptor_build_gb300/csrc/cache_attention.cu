@@ -17,11 +17,11 @@ uint32_t padded_width(uint32_t width) { return width <= 64 ? 64 : width <= 128 ?
 // kernel for few; with 32, warps that share a ring two by two are faster for
 // codes (64 sequences of 20,000 tokens, 2 key heads: 288 us, the kernel for many
 // 350) and slower for 16-bit values (334, 270).
+// Above 128 rows two tiles of 128 share a CTA's loads (wide trees of 488 rows
+// 396 us one by one, 312 so) where TMEM holds the sums of both.
 // The rows are those of max_tokens, for all requests of a call: 100 single tokens of 8
 // query heads to a key head over 3,000 E4M3 tokens take 41 us with max_tokens 1, 124 with
 // 61 (bf16 58 and 89).
-// Above 128 rows two tiles of 128 share a CTA's loads (wide trees of 488 rows
-// 396 us one by one, 312 so) where TMEM holds the sums of both.
 uint32_t blocks_for(uint64_t rows, uint32_t pad, bool codes) {
   if (rows > 128 && pad <= 128) return 2 * kManyBlocks;
   return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 && codes ? 4 : kManyBlocks;

@@ -51,7 +51,6 @@ struct AttnParams {
   uint32_t narrow;         // offsets in the pools, by 16 bytes, fit 32 bits
 };
 
-// Host: one instance of the kernels for a padded width.
 // CTAs of an SM of a kernel for so many blocks of 8 query rows: as many as
 // registers and shared memory hold.
 constexpr uint32_t attn_ctas_per_sm(uint32_t pad, bool codes, uint32_t blocks) {
@@ -64,6 +63,7 @@ inline unsigned attn_grid(uint32_t ctas_per_sm) {
   return g < kMaxAttnCtas ? g : kMaxAttnCtas;
 }
 
+// Host: one instance of the kernels for a padded width.
 int launch_attention_64(const AttnParams& p, uint32_t type, uint32_t blocks, cudaStream_t s);
 int launch_attention_128(const AttnParams& p, uint32_t type, uint32_t blocks, cudaStream_t s);
 int launch_attention_256(const AttnParams& p, uint32_t type, uint32_t blocks, cudaStream_t s);
@@ -251,35 +251,14 @@ __device__ __forceinline__ void multiply<__half>(float (&c)[4], const uint32_t (
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Four 8-bit codes as four 16-bit values, exactly. I8 to bf16: a code's low
-// seven bits c fit bf16's seven, 128 + c, from which 128 or, for a negative
-// code, 256 goes. I8 to f16: 1024 + (code + 128), less 1152.
-template <typename T>
-__device__ __forceinline__ uint2 widen4(uint32_t w, bool e4m3);
-template <>
-__device__ __forceinline__ uint2 widen4<__half>(uint32_t w, bool e4m3) {
+// Four 8-bit codes as four f16, exactly. I8: 1024 + (code + 128), less 1152.
+__device__ __forceinline__ uint2 widen4(uint32_t w, bool e4m3) {
   if (e4m3) return make_uint2(e4m3x2_to_f16x2(w), e4m3x2_to_f16x2(w >> 16));
   uint2 r;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const uint32_t a = (__byte_perm(w, 0, h ? 0x4342 : 0x4140) ^ 0x00800080u) | 0x64006400u;
     const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&a), __half2half2(__ushort_as_half(0x6480)));
-    (h ? r.y : r.x) = *reinterpret_cast<const uint32_t*>(&v);
-  }
-  return r;
-}
-template <>
-__device__ __forceinline__ uint2 widen4<__nv_bfloat16>(uint32_t w, bool e4m3) {
-  uint2 r;
-  if (e4m3) {
-    const float2 a = unpack2<__half>(e4m3x2_to_f16x2(w)), b = unpack2<__half>(e4m3x2_to_f16x2(w >> 16));
-    return make_uint2(pack2<__nv_bfloat16>(a.x, a.y), pack2<__nv_bfloat16>(b.x, b.y));
-  }
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t a = __byte_perm(w, 0, h ? 0x4342 : 0x4140);
-    const uint32_t x = (a & 0x007F007Fu) | 0x43004300u, y = (a & 0x00800080u) | 0x43004300u;
-    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
     (h ? r.y : r.x) = *reinterpret_cast<const uint32_t*>(&v);
   }
   return r;

@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
             const uint32_t a[4] = {lo.x, lo.y, lo.z, lo.w}, b[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-              const uint2 u = widen4<H>(a[m], kFloat), v = widen4<H>(b[m], kFloat);
+              const uint2 u = widen4(a[m], kFloat), v = widen4(b[m], kFloat);
               const uint32_t f[4] = {u.x, v.x, u.y, v.y};
 #pragma unroll
               for (uint32_t n = 0; n < kN; ++n) multiply<H>(s[n], f, q[4 * j + m][2 * n], q[4 * j + m][2 * n + 1]);
@@ -577,8 +577,8 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
             for (uint32_t m = 0; m < kWords; ++m)
 #pragma unroll
               for (uint32_t half = 0; half < 2; ++half) {
-                const uint2 lo = widen4<H>(__byte_perm(u[0][m], u[1][m], half ? 0x7362 : 0x5140), kFloat);
-                const uint2 hi = widen4<H>(__byte_perm(u[2][m], u[3][m], half ? 0x7362 : 0x5140), kFloat);
+                const uint2 lo = widen4(__byte_perm(u[0][m], u[1][m], half ? 0x7362 : 0x5140), kFloat);
+                const uint2 hi = widen4(__byte_perm(u[2][m], u[3][m], half ? 0x7362 : 0x5140), kFloat);
                 const uint32_t f[4] = {lo.x, lo.y, hi.x, hi.y};
                 const uint32_t d = j * 8 + 2 * m + half;
 #pragma unroll

@@ -21,6 +21,7 @@ int launch_blocks(const AttnParams& p, uint32_t blocks, cudaStream_t s) {
         return launch_few<T, kPad, kCodes, 2, 1>(p, s);
     case 4:
       if constexpr (kCodes) return launch_few<T, kPad, kCodes, 2, 2>(p, s);
+      return -EINVAL;
     case kManyBlocks:
       return launch_many<T, kPad, kCodes, 1>(p, s);
     default:

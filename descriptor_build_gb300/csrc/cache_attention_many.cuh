@@ -490,7 +490,7 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
 
     if (warp >= F::kWeights / 32 && warp < F::kWeights / 32 + F::kLoaderWarps) {
       // ------------------------------------------------------------- loaders
-      // A warp has every second or third unit to itself, and waits for no other.
+      // A warp has every third unit to itself (every sixth with two tiles of rows), and waits for no other.
       const uint32_t mine = warp - F::kWeights / 32, own = (mine + F::kLoaderWarps - units % F::kLoaderWarps) % F::kLoaderWarps;
       const int32_t* const table = p.view.table + (uint64_t)r.seq * p.view.columns;
       constexpr uint32_t kChunks = kPad / 8, kRawChunks = kCodes ? kPad / 16 : kChunks;  // 16-byte chunks of a row
@@ -709,7 +709,7 @@ __global__ void __launch_bounds__((Many<kPad, kCodes, kTiles>::kThreads), (Many<
 #pragma unroll
               for (uint32_t k = 0; k < kBatch; ++k) {
                 const uint32_t token = token0 + (k0 + k) * kStep;
-                const uint2 y[4] = {widen4<W>(c[k].x, kFour), widen4<W>(c[k].y, kFour), widen4<W>(c[k].z, kFour), widen4<W>(c[k].w, kFour)};
+                const uint2 y[4] = {widen4(c[k].x, kFour), widen4(c[k].y, kFour), widen4(c[k].z, kFour), widen4(c[k].w, kFour)};
                 *(uint4*)(to + token * 128 + (((2 * chunk) & 7) ^ (token & 7)) * 16) = make_uint4(y[0].x, y[0].y, y[1].x, y[1].y);
                 *(uint4*)(to + token * 128 + (((2 * chunk + 1) & 7) ^ (token & 7)) * 16) = make_uint4(y[2].x, y[2].y, y[3].x, y[3].y);
               }
