@@ -25,7 +25,7 @@ def test_kept_bytes_behind_4_gib(width):
     t.table = np.where(t.table >= 0, pages - 1 - 3 * t.table, -1).astype(np.int32)
     t.n_pages = pages
     used = np.unique(t.table[t.table >= 0])
-    assert used.min() * gap > 1 << 32
+    assert int(used.min()) * gap > 1 << 32
     at = torch.from_numpy(used.astype(np.int64)).cuda()
     pool[:, at] = torch.from_numpy(rng.integers(-128, 128, (planes, len(used), T, heads, width)).astype(np.int8)).cuda()
     before = pool[:, at].cpu().numpy()
