@@ -15,8 +15,9 @@ uint32_t padded_width(uint32_t width) { return width <= 64 ? 64 : width <= 128 ?
 
 // Blocks of 8 query rows of an item. Up to 16 rows memory is the bound of the
 // kernel for few; with 32, warps that share a ring two by two are faster for
-// codes (64 sequences of 20,000 tokens, 2 key heads: 288 us, the kernel for many
-// 350) and slower for 16-bit values (334, 270).
+// most codes (64 sequences of 20,000 tokens, 2 key heads: int8 380 us, the kernel for
+// many 412, E4M3 290 and 255; 48 of 3,000, 8 key heads, E4M3 148 and 161) and slower for
+// 16-bit values (334, 270).
 // Above 128 rows two tiles of 128 share a CTA's loads (wide trees of 488 rows
 // 396 us one by one, 312 so) where TMEM holds the sums of both.
 // The rows are those of max_tokens, for all requests of a call: 100 single tokens of 8

@@ -19,7 +19,8 @@
 // is 2^-38 of that.
 //
 // 64 sequences of 80,003 tokens, E4M3, 2 key heads of 128 values by 8 query heads:
-// 404 us, 6.6 TB/s of 2.67 GB (the copy rate is 6.8); bf16 caches come at 6.4 to 6.8.
+// 406 to 419 us, 6.4 to 6.6 TB/s of 2.67 GB (the copy rate is 6.8); bf16 caches of 64
+// sequences of 20,000 tokens come at 6.6 to 6.9.
 // With two CTAs an SM the codes took 494 us; with the type of codes tested at each
 // product, which kept them from overlapping, 712.
 #pragma once

@@ -14,7 +14,7 @@ int launch_blocks(const AttnParams& p, uint32_t blocks, cudaStream_t s) {
     case 2:
       // 16 rows of 256 16-bit values are more than a warp's registers hold: two
       // warps share them, and two CTAs an SM (113 sequences of 4,223 tokens, 8 key
-      // heads: 701 us, 928 with a warp for all; codes 688, 652).
+      // heads: 687 us, 928 with a warp for all; int8 697 and 661, E4M3 475 and 544).
       if constexpr (kPad == 256 && !kCodes)
         return launch_few<T, kPad, kCodes, 1, 2>(p, s);
       else

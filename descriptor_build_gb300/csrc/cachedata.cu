@@ -5,10 +5,10 @@
 // warp takes neighbouring rows (tokens) of the batch, finds its request once,
 // and handles a row's keys and values of all heads, 8 values a lane, so that
 // the 4 to 32 lanes that hold a head's row can reduce its largest magnitude.
-// 192,000 tokens of 8 heads of 128 from bf16 to E4M3: 198 us, 6.0 TB/s (issue: 67 %
-// of the schedulers' cycles); 384,000 tokens of 5 heads of 112 from I8 to f16: 253
-// us, 4.7 TB/s of what is asked for, 5.6 of DRAM (rows of 112 bytes share their
-// sectors; 14 of 16 lanes and 5 of 6 heads' places are in use).
+// 192,000 tokens of 8 heads of 128 from bf16 to E4M3: 197 us, 6.0 TB/s (issue: 67 %
+// of the schedulers' cycles), to bf16 235, 6.6; 384,000 tokens of 5 heads of 112 from I8
+// to f16: 256 us, 4.6 TB/s of what is asked for, 5.6 of DRAM (rows of 112 bytes share
+// their sectors; 14 of 16 lanes and 5 of 6 heads' places are in use).
 #include "cachedata.cuh"
 
 namespace db {
