@@ -195,10 +195,10 @@ __device__ __forceinline__ float times_exp2(float l, float d) {
   const float h = exp2_of(0.5f * d);
   return l * h * h;
 }
-// The exponent of a scale. What a row sums has the size of its references' inverse, and
-// 2^31 weights that start at 2^lift must not leave the range: scales below 2^-80 (zeros)
-// are taken as that, those from 2^101 on as 2^100. One that is not finite makes the row's
-// answer so whatever its reference.
+// The exponent of a scale, for references. A row's weights are the larger the smaller its
+// values' scales are, and 2^31 of them must not leave the numbers' range, nor those beside
+// large scales fall out of it: scales below 2^-80 (zeros too) are taken as that, those from
+// 2^101 on as 2^100. One that is not finite makes the answer so whatever the reference.
 constexpr uint32_t kLeastExponent = 127 - 80, kMostExponent = 127 + 100;
 __device__ __forceinline__ uint32_t scale_exponent(float scale) {
   const uint32_t e = __float_as_uint(scale) >> 23 & 0xFFu;
