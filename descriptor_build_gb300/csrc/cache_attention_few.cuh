@@ -166,6 +166,13 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
   };
   constexpr uint32_t kOther = kCodes ? 1 : 8;
   constexpr float kLift = (float)attn_lift<H>(kFewSlack);
+  // Weights are rounded to the type that is multiplied. Where that is as coarse as the
+  // answers' type, which made their error 1.4 times that of rounding them, more where
+  // few weights count, what the rounding left is multiplied too, if that costs little:
+  // bf16 values of 128 198 -> 200 us (64 sequences of 20,000, 2 key heads by 8), of 256
+  // 237 -> 257 (32); f16 answers from E4M3 codes of 128 120 -> 124, 158 -> 177 with 16
+  // rows, 291 -> 328 with 32.
+  constexpr uint32_t kParts = std::is_same<H, T>::value && (kCodes ? F::kRows == 8 : kPad <= 128) ? 2 : 1;
   // a lane copies the same chunk of every kStep-th token
   const uint32_t chunk = lane % kChunks, token0 = lane / kChunks;
   const bool has = chunk < (kCodes ? p.c.width / 16 : p.c.width / 8);
@@ -549,12 +556,20 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
               if (!(sees >> (n * 4 + k) & 1)) s[n][k] = 0.f;
         }
       }
-      uint32_t b[kN][2];
+      uint32_t b[kParts][kN][2];
 #pragma unroll
-      for (uint32_t n = 0; n < kN; ++n) {
-        b[n][0] = turned(pack2<H>(s[n][0], s[n][1]));
-        b[n][1] = turned(pack2<H>(s[n][2], s[n][3]));
-      }
+      for (uint32_t n = 0; n < kN; ++n)
+#pragma unroll
+        for (uint32_t h = 0; h < 2; ++h) {
+          const float x = s[n][2 * h], y = s[n][2 * h + 1];
+          const uint32_t w = pack2<H>(x, y);
+          b[0][n][h] = turned(w);
+          if constexpr (kParts == 2) {  // what the rounding left (of infinities and NaN nothing)
+            const float2 r = unpack2<H>(w);
+            const float u = x - r.x, v = y - r.y;
+            b[1][n][h] = turned(pack2<H>(fabsf(u) < 64.f ? u : 0.f, fabsf(v) < 64.f ? v : 0.f));
+          }
+        }
       if constexpr (kCodes) {
         const auto outputs = [&](auto is_float) __attribute__((always_inline)) {
           constexpr bool kFloat = decltype(is_float)::value;
@@ -583,7 +598,9 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
                 const uint32_t f[4] = {lo.x, lo.y, hi.x, hi.y};
                 const uint32_t d = j * 8 + 2 * m + half;
 #pragma unroll
-                for (uint32_t n = 0; n < kN; ++n) multiply<H>(o[d][n], f, b[n][0], b[n][1]);
+                for (uint32_t n = 0; n < kN; ++n)
+#pragma unroll
+                  for (uint32_t k = 0; k < kParts; ++k) multiply<H>(o[d][n], f, b[k][n][0], b[k][n][1]);
               }
           }
         };
@@ -598,7 +615,9 @@ __global__ void __launch_bounds__(kAttnThreads, (Few<kPad, kCodes, kN, kShare>::
           uint32_t f[4];
           load_matrices_t(f, smem_at(vt) + place((lane & 7) + (lane >> 4) * 8, 2 * d + (lane >> 3 & 1)));
 #pragma unroll
-          for (uint32_t n = 0; n < kN; ++n) multiply<H>(o[d][n], f, b[n][0], b[n][1]);
+          for (uint32_t n = 0; n < kN; ++n)
+#pragma unroll
+            for (uint32_t k = 0; k < kParts; ++k) multiply<H>(o[d][n], f, b[k][n][0], b[k][n][1]);
         }
       }
     }

@@ -136,12 +136,12 @@ int db_cache_read(const db_page_tables* t, const db_cache_batch* b, const int32_
  * slots hold (infinities and NaN included).
  * `type` is that of q and out, DB_BF16 or DB_F16; 16-bit caches are of the
  * same type. Statistics and sums are held in 32 bits. Weights are rounded to
- * `type` for the product with 16-bit values; with codes weights times scales
- * are rounded to f16, each off by 2^-11 of itself or by 2^-29 of the largest
- * among the tokens that the row sees, whichever is more (where scales below
- * 2^-80, 0 too, count as that), and bf16 queries are taken as f16 times a power
- * of two that is each row's own (off by 2^-38 of the row's largest value at
- * most).
+ * `type`, or held finer, for the product with 16-bit values; with codes
+ * weights times scales are rounded to f16 or held finer, each off by 2^-11 of
+ * itself or by 2^-29 of the largest among the tokens that the row sees,
+ * whichever is more (where scales below 2^-80, 0 too, count as that), and bf16
+ * queries are taken as f16 times a power of two that is each row's own (off by
+ * 2^-38 of the row's largest value at most).
  * Sums of weights times values have to stay within 32 bits' range: values up
  * to 2^100 do, and those of codes above 2^-90 keep their precision.
  *   max_tokens  no request has more rows (one that has is DB_PAGE_INVALID);
